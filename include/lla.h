@@ -136,9 +136,10 @@ size_t lla_forward_host_buffer_size(int dtype, int path, int B, int H, int n, in
 
 /*
  * lla_sync_status -- synchronise `stream`, then report and clear the library's device error
- * word: set when a bounded wait inside a kernel gave up (LLA_ERR_DEVICE_TIMEOUT), or when the
+ * word: set when a bounded wait inside a kernel gave up (LLA_ERR_DEVICE_TIMEOUT), when the
  * tensor kernel found its dynamic shared memory not 1024-byte aligned and did no work
- * (LLA_ERR_CUDA).
+ * (LLA_ERR_CUDA), or when a paged call found a length, slot or page id on the device that its
+ * tensors do not hold (LLA_ERR_INVALID_ARG).
  */
 int lla_sync_status(void* stream);
 
@@ -336,6 +337,102 @@ int lla_backward_host(int dtype, int path, const void* q, const void* k, const v
 
 /* Bytes of device buffer lla_backward_host needs for these arguments (0 for invalid ones). */
 size_t lla_backward_host_buffer_size(int dtype, int path, int B, int H, int n, int d, int chunk_slices);
+
+/*
+ * Paged caches: the keys and values of many sequences of different lengths in pages of page_size
+ * positions, [num_pages, Hkv, page_size, d] in dtype, page_size a power of two in 8 .. 256.  Position
+ * x of sequence s lies in page block_table[s][x / page_size] at row x % page_size; its slot is
+ * page * page_size + row.  Token rows of a step ([T, heads, d]) are packed sequence after sequence:
+ * sequence s has rows cu_q[s] .. cu_q[s+1]-1, and rows from cu_q[S] on are padding.  A step is
+ * lla_paged_plan, then per layer lla_paged_append and lla_paged_parallax.  Every length lives on the
+ * device and no call synchronises, so a step can be captured into a CUDA graph and replayed with other
+ * lengths.
+ *
+ * lla_paged_plan -- block tables and slot maps from request lengths, on the GPU.
+ *
+ * S sequences in [1, 8192]; T is the number of token rows the step's tensors have.  Sequence s has
+ * ctx_lens[s] positions cached and brings new_lens[s] tokens (negative values count as 0).  It needs
+ * ceil((ctx+new)/page_size) - ceil(ctx/page_size) fresh pages; they are taken from the end of the free
+ * list free_pages[0 .. *free_count-1] (a stack), sequences in order.  A sequence is granted all of its
+ * tokens or none: it is refused when ctx + new exceeds table_width * page_size, when its rows do not
+ * lie within T, or when it needs pages and the free list does not hold its pages and those of the
+ * sequences before it; a refused sequence keeps its length and its table row, and its rows' slots are -1.
+ *
+ * ctx_lens, new_lens  [S] int32.
+ * block_table  [S, table_width] int32, updated: the ceil(ctx/page_size) entries held are read, entries
+ *              for fresh pages are written, others are left alone.
+ * free_pages   [free_capacity] int32, read.  free_count [1] int32 (values above free_capacity count as it).
+ * kv_lens      [S] int32, written: ctx + new if granted, else ctx.
+ * cu_q         [S+1] int32, written: running sum of new_lens, cut at T.
+ * slots        [T] int64, written: each token row's slot; -1 for padding, refused sequences and held
+ *              table entries below 0.
+ * positions    NULL or [T] int32, written: each row's position in its sequence (padding: 0).
+ * granted      [S] int32, written: 1 or 0.
+ * free_left    [1] int32, written: the free list's new length.
+ * kv_lens may be ctx_lens and free_left may be free_count (a decode loop in place); no other two
+ * arrays may overlap.  Asynchronous on `stream`, one launch, no scratch.
+ */
+int lla_paged_plan(const int* ctx_lens, const int* new_lens, int S, int page_size, int* block_table, int table_width,
+                   const int* free_pages, int free_capacity, const int* free_count, int T, int* kv_lens, int* cu_q,
+                   long long* slots, int* positions, int* granted, int* free_left, void* stream);
+
+/*
+ * lla_paged_append -- write a step's new keys and values into the paged caches.
+ *
+ * k_new, v_new  [T, Hkv, d] in dtype; token t starts k_stride (v_stride) elements after token t-1
+ *               (>= Hkv*d, a multiple of 16 bytes), so slices of a fused projection can be passed.
+ * slots         [T] int64: the slot of each token; rows with a negative slot are skipped.  A slot beyond
+ *               num_pages * page_size is skipped and reported by lla_sync_status.  Two rows must not
+ *               have the same slot.
+ * k_cache, v_cache  [num_pages, Hkv, page_size, d] in dtype, pages page_stride elements apart
+ *               (>= Hkv*page_size*d, a multiple of 16 bytes).
+ * Pointers 16-byte aligned; d in {16, 32, 64, 128}.  Asynchronous on `stream`, one launch, no scratch.
+ */
+int lla_paged_append(int dtype, const void* k_new, const void* v_new, const long long* slots, void* k_cache,
+                     void* v_cache, int T, int Hkv, int d, int page_size, int num_pages, long long k_stride,
+                     long long v_stride, long long page_stride, void* stream);
+
+/*
+ * lla_paged_parallax -- Parallax-form attention (lla_parallax_forward's formula) of a step's token
+ * rows over their sequences' paged caches: a decode step, a chunk of a prompt or whole prompts, in one
+ * ragged batch.  For the row of token i of sequence s (n = cu_q[s+1]-cu_q[s] tokens, L = kv_lens[s]
+ * cached positions, the step's own tokens among them) and query head h, over the keys j < L, and with
+ * causal != 0 also j <= L - n + i, of key head h / (Hq / Hkv):
+ *
+ *     p_j = softmax_j(tau q.k_j),  t_j = probe.k_j,  c = sum_j p_j t_j,
+ *     out = sum_j p_j (1 - (t_j - c)) v_j         (a row that sees no key: zeros).
+ *
+ * With causal = 0 every row sees all L keys (cross attention to cached states of another length).
+ * A probe of zeros gives softmax attention.
+ *
+ * dtype      of q, probe, out and the caches.  The probe is taken in dtype (lla_parallax_forward
+ *            takes fp32), as a serving projection gives it.
+ * path       LLA_PATH_AUTO: bf16 with d in {64, 128} takes the tensor cores, all else LLA_PATH_FP32
+ *            (CUDA cores, every product in fp32).
+ * q, probe   [T, Hq, d], token strides q_stride / probe_stride elements (>= Hq*d, multiples of 16 bytes).
+ * out        [T, Hq, d] contiguous; rows behind the last sequence are not written.
+ * block_table [S, table_width], cu_q [S+1], kv_lens [S] int32.  max_new: the most tokens of a sequence
+ *            (T serves; a small value lets a decode step take the decode kernel).
+ * Hq a multiple of Hkv; d in {16, 32, 64, 128}; S <= 2^20; T*Hq <= 2^30.
+ * Lengths or page ids on the device that lie outside the tensors (cu_q beyond T or falling, more than
+ * max_new tokens, kv_lens beyond the table, a page id outside [0, num_pages)) are never followed: the
+ * access is cut or reads zeros, and lla_sync_status reports LLA_ERR_INVALID_ARG.  What pages hold behind a
+ * sequence's length never reaches a result; values at positions that are part of it should be finite (a
+ * NaN or infinity at one position can reach rows of the same step that do not see it).
+ * workspace  NULL (stream-ordered pool) or lla_paged_parallax_workspace_size(...) bytes, 256-byte aligned,
+ *            used by no other call at the same time; its contents need not be kept or cleared.
+ * Results do not depend on the run: the order of every sum is fixed by the lengths.
+ * Asynchronous on `stream`; errors as for lla_forward_ex.  The paged calls record no profiling events.
+ */
+int lla_paged_parallax(int dtype, int path, const void* q, const void* probe, const void* k_cache, const void* v_cache,
+                       const int* block_table, const int* cu_q, const int* kv_lens, void* out, int T, int S, int Hq,
+                       int Hkv, int d, int page_size, int num_pages, int table_width, int max_new, long long q_stride,
+                       long long probe_stride, long long page_stride, float tau, int causal, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/* Bytes of scratch lla_paged_parallax needs for these sizes (0 for invalid ones). */
+size_t lla_paged_parallax_workspace_size(int dtype, int path, int T, int S, int Hq, int Hkv, int d, int page_size,
+                                         int table_width, int max_new);
 
 /* Message for the calling thread's most recent failure ("" if none). Owned by the library. */
 const char* lla_last_error(void);

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from collections import namedtuple
 
 __all__ = [
     "LLAError", "load_library", "library_path", "forward", "forward_host", "lla_forward", "lla_forward_ex",
@@ -20,6 +21,8 @@ __all__ = [
     "lla_profile_enable", "lla_profile_read", "lla_forward_noalloc", "lla_parallax_forward", "parallax_forward",
     "lla_decode", "lla_decode_ex", "lla_decode_max_n", "decode", "lla_backward", "lla_backward_workspace_size", "backward",
     "lla_backward_host", "lla_backward_host_buffer_size", "backward_host",
+    "lla_paged_plan", "lla_paged_append", "lla_paged_parallax", "lla_paged_parallax_workspace_size",
+    "PagedPlan", "paged_plan", "paged_append", "paged_parallax",
     "LLA_OK", "LLA_ERR_INVALID_ARG", "LLA_ERR_UNSUPPORTED", "LLA_ERR_CUDA", "LLA_ERR_DEVICE_TIMEOUT",
     "LLA_DTYPE_BF16", "LLA_DTYPE_FP32", "LLA_PATH_AUTO", "LLA_PATH_TENSOR", "LLA_PATH_FP32",
     "LLA_DECODE_AUTO", "LLA_DECODE_MOMENT", "LLA_DECODE_STREAM", "LLA_DECODE_CLUSTER",
@@ -35,6 +38,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
 
 _c_int, _c_float, _c_size, _vp = ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p
+_c_ll = ctypes.c_longlong
 
 # name -> (restype, argtypes); mirrors include/lla.h
 _SIGNATURES = {
@@ -65,6 +69,14 @@ _SIGNATURES = {
     "lla_backward_host": (_c_int, [_c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int,
                                    _c_int, _c_int, _c_float, _c_float, _c_int, _c_float, _c_int, _vp, _c_size, _vp]),
     "lla_backward_host_buffer_size": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_int]),
+    "lla_paged_plan": (_c_int, [_vp, _vp, _c_int, _c_int, _vp, _c_int, _vp, _c_int, _vp, _c_int, _vp, _vp, _vp, _vp,
+                                _vp, _vp, _vp]),
+    "lla_paged_append": (_c_int, [_c_int, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _c_ll, _c_ll,
+                                  _c_ll, _vp]),
+    "lla_paged_parallax": (_c_int, [_c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int,
+                                    _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_ll, _c_ll, _c_ll, _c_float,
+                                    _c_int, _vp, _c_size, _vp]),
+    "lla_paged_parallax_workspace_size": (_c_size, [_c_int] * 10),
     "lla_profile_enable": (_c_int, [_c_int]),
     "lla_profile_read": (_c_int, [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_float)]),
     "lla_version": (_c_int, []),
@@ -458,3 +470,201 @@ def forward_host(q, k, v, tau, lam, cg_max_iters, cg_tol=0.0, *, path=LLA_PATH_A
     if return_iters:
         return out, rho, denom, iters
     return out, rho, denom
+
+
+def lla_paged_plan(ctx_ptr, new_ptr, S, page_size, table_ptr, table_width, free_ptr, free_capacity, free_count_ptr, T,
+                   kv_ptr, cu_ptr, slots_ptr, positions_ptr, granted_ptr, free_left_ptr, stream_ptr):
+    """Raw page-planning entry point on device pointers (ints); raises LLAError on failure."""
+    _check(load_library().lla_paged_plan(ctx_ptr, new_ptr, S, page_size, table_ptr, table_width, free_ptr, free_capacity,
+                                         free_count_ptr, T, kv_ptr, cu_ptr, slots_ptr, positions_ptr, granted_ptr,
+                                         free_left_ptr, stream_ptr))
+
+
+def lla_paged_append(dtype, k_ptr, v_ptr, slots_ptr, k_cache_ptr, v_cache_ptr, T, Hkv, d, page_size, num_pages, k_stride,
+                     v_stride, page_stride, stream_ptr):
+    """Raw cache-append entry point on device pointers (ints); raises LLAError on failure."""
+    _check(load_library().lla_paged_append(dtype, k_ptr, v_ptr, slots_ptr, k_cache_ptr, v_cache_ptr, T, Hkv, d, page_size,
+                                           num_pages, k_stride, v_stride, page_stride, stream_ptr))
+
+
+def lla_paged_parallax(dtype, path, q_ptr, probe_ptr, k_cache_ptr, v_cache_ptr, table_ptr, cu_ptr, kv_ptr, out_ptr, T, S,
+                       Hq, Hkv, d, page_size, num_pages, table_width, max_new, q_stride, probe_stride, page_stride, tau,
+                       causal, ws_ptr, ws_bytes, stream_ptr):
+    """Raw paged Parallax entry point on device pointers (ints); raises LLAError on failure."""
+    _check(load_library().lla_paged_parallax(dtype, path, q_ptr, probe_ptr, k_cache_ptr, v_cache_ptr, table_ptr, cu_ptr,
+                                             kv_ptr, out_ptr, T, S, Hq, Hkv, d, page_size, num_pages, table_width, max_new,
+                                             q_stride, probe_stride, page_stride, tau, causal, ws_ptr, ws_bytes,
+                                             stream_ptr))
+
+
+def lla_paged_parallax_workspace_size(dtype, path, T, S, Hq, Hkv, d, page_size, table_width, max_new):
+    return load_library().lla_paged_parallax_workspace_size(dtype, path, T, S, Hq, Hkv, d, page_size, table_width, max_new)
+
+
+PagedPlan = namedtuple("PagedPlan", "kv_lens cu_q slots positions granted free_left")
+
+
+class _on_stream:
+    """Makes `device` current and, where a stream is given, that stream: what a call allocates or copies
+    inside belongs to the stream that its kernels run on.  Yields the stream's pointer."""
+
+    def __init__(self, device, stream):
+        import torch
+        self._device, self._stream = torch.cuda.device(device), stream
+
+    def __enter__(self):
+        import torch
+        self._device.__enter__()
+        self._inner = None
+        if self._stream is not None:
+            self._inner = torch.cuda.stream(self._stream)
+            self._inner.__enter__()
+        return _stream_ptr(None)
+
+    def __exit__(self, *exc):
+        if self._inner is not None:
+            self._inner.__exit__(*exc)
+        self._device.__exit__(*exc)
+
+
+def _bad(message):
+    return LLAError(LLA_ERR_INVALID_ARG, message)
+
+
+def _check_ints(device, dtype, **tensors):
+    """Contiguous integer tensors of one dtype on one device; shapes as (tensor, shape) pairs."""
+    for name, (t, shape) in tensors.items():
+        if t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+            raise _bad(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                       f"{t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _check_caches(k_cache, v_cache):
+    """(num_pages, Hkv, page_size, d, page stride) of two caches laid out alike."""
+    if not (k_cache.is_cuda and v_cache.is_cuda):
+        raise _bad("the caches must be CUDA tensors (there is no CPU path)")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or \
+            k_cache.device != v_cache.device:
+        raise _bad(f"caches [num_pages, Hkv, page_size, d] of one dtype and device expected, got {tuple(k_cache.shape)} "
+                   f"{k_cache.dtype}, {tuple(v_cache.shape)} {v_cache.dtype}")
+    import torch
+    if k_cache.dtype not in (torch.bfloat16, torch.float32):
+        raise _bad("the caches must be bf16 or fp32")
+    P, Hkv, Z, d = k_cache.shape
+    for c in (k_cache, v_cache):
+        if c.numel() and not c[0].is_contiguous():
+            raise _bad("each page of a cache must be contiguous (a cache is written in place, so it is not copied)")
+    strides = {c.stride(0) if P > 1 else Hkv * Z * d for c in (k_cache, v_cache)}
+    if len(strides) != 1:
+        raise _bad("the caches must have one page stride")
+    return P, Hkv, Z, d, strides.pop()
+
+
+def _token_rows(t, name, like, heads, d):
+    """[T, heads, d] rows as the kernels take them: heads packed, any 16-byte token stride; else a copy."""
+    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, d) or t.dtype != like.dtype or t.device != like.device:
+        raise _bad(f"{name} must be [T, {heads}, {d}] {like.dtype} on {like.device}, got {tuple(t.shape)} {t.dtype} on "
+                   f"{t.device}")
+    step = 16 // t.element_size()
+    packed = (t.shape[2] == 1 or t.stride(2) == 1) and (heads == 1 or t.stride(1) == d)
+    if packed and t.data_ptr() % 16 == 0 and (t.shape[0] <= 1 or (t.stride(0) >= heads * d and t.stride(0) % step == 0)):
+        return t, (t.stride(0) if t.shape[0] > 1 else heads * d)
+    t = t.contiguous() if t.data_ptr() % 16 == 0 and not t.is_contiguous() else t.clone(memory_format=_contiguous())
+    return t, heads * d
+
+
+def _contiguous():
+    import torch
+    return torch.contiguous_format
+
+
+def paged_plan(ctx_lens, new_lens, block_table, free_pages, free_count, page_size, num_rows, *, kv_lens=None, cu_q=None,
+               slots=None, positions=None, granted=None, free_left=None, stream=None):
+    """Pages and slots for a step's new tokens, from the requests' lengths, on the GPU (include/lla.h,
+    lla_paged_plan).
+
+    ctx_lens, new_lens [S]; block_table [S, W], updated in place; free_pages [F] with free_count [1], a
+    stack of free page ids; num_rows: token rows of the step's tensors.  All int32 CUDA tensors.
+    Returns PagedPlan(kv_lens [S], cu_q [S+1], slots [num_rows] int64, positions [num_rows], granted [S],
+    free_left [1]).  kv_lens=ctx_lens and free_left=free_count update a decode loop's state in place.
+    Asynchronous on the current (or given) stream.
+    """
+    import torch
+    if not ctx_lens.is_cuda:
+        raise _bad("paged_plan takes CUDA tensors (there is no CPU path)")
+    dev, T, i32 = ctx_lens.device, int(num_rows), torch.int32
+    S = ctx_lens.numel()
+    if block_table.dim() != 2 or T < 1:
+        raise _bad("block_table must be [S, W] and num_rows >= 1")
+    _check_ints(dev, i32, ctx_lens=(ctx_lens, (S,)), new_lens=(new_lens, (S,)),
+                block_table=(block_table, (S, block_table.shape[1])), free_pages=(free_pages, (free_pages.numel(),)),
+                free_count=(free_count, (1,)))
+    with _on_stream(dev, stream) as sp:
+        new = lambda t, shape, dt=i32: torch.empty(shape, dtype=dt, device=dev) if t is None else t  # noqa: E731
+        kv_lens, cu_q, granted = new(kv_lens, (S,)), new(cu_q, (S + 1,)), new(granted, (S,))
+        slots, positions, free_left = new(slots, (T,), torch.int64), new(positions, (T,)), new(free_left, (1,))
+        _check_ints(dev, i32, kv_lens=(kv_lens, (S,)), cu_q=(cu_q, (S + 1,)), positions=(positions, (T,)),
+                    granted=(granted, (S,)), free_left=(free_left, (1,)))
+        _check_ints(dev, torch.int64, slots=(slots, (T,)))
+        lla_paged_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), S, int(page_size), block_table.data_ptr(),
+                       block_table.shape[1], free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(), T,
+                       kv_lens.data_ptr(), cu_q.data_ptr(), slots.data_ptr(), positions.data_ptr(), granted.data_ptr(),
+                       free_left.data_ptr(), sp)
+    return PagedPlan(kv_lens, cu_q, slots, positions, granted, free_left)
+
+
+def paged_append(k_new, v_new, slots, k_cache, v_cache, *, stream=None):
+    """Write k_new, v_new [T, Hkv, d] into the paged caches [num_pages, Hkv, page_size, d] at slots [T]
+    (int64, a plan's; rows with a negative slot are skipped).  In place, asynchronous on the current (or
+    given) stream.  Rows may be slices of a fused projection (any 16-byte token stride)."""
+    import torch
+    P, Hkv, Z, d, page_stride = _check_caches(k_cache, v_cache)
+    if k_new.shape != v_new.shape:
+        raise _bad("k_new and v_new must have one shape")
+    T = k_new.shape[0] if k_new.dim() == 3 else 0
+    dtype = LLA_DTYPE_BF16 if k_cache.dtype == torch.bfloat16 else LLA_DTYPE_FP32
+    with _on_stream(k_cache.device, stream) as sp:
+        k_new, ks = _token_rows(k_new, "k_new", k_cache, Hkv, d)
+        v_new, vs = _token_rows(v_new, "v_new", k_cache, Hkv, d)
+        _check_ints(k_cache.device, torch.int64, slots=(slots, (T,)))
+        lla_paged_append(dtype, k_new.data_ptr(), v_new.data_ptr(), slots.data_ptr(), k_cache.data_ptr(),
+                         v_cache.data_ptr(), T, Hkv, d, Z, P, ks, vs, page_stride, sp)
+
+
+def paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, max_new, *, causal=True,
+                   path=LLA_PATH_AUTO, out=None, workspace=None, stream=None):
+    """Parallax-form attention of a step's token rows q, probe [T, Hq, d] over paged caches
+    [num_pages, Hkv, page_size, d] (include/lla.h, lla_paged_parallax).
+
+    block_table [S, W], cu_q [S+1], kv_lens [S]: int32 CUDA tensors (paged_plan's); max_new: the most
+    tokens of one sequence in this step.  causal=False: every row sees all of its sequence's keys.
+    Returns out [T, Hq, d]; rows behind the last sequence are left as they were.  Asynchronous on the
+    current (or given) stream.
+    """
+    import torch
+    P, Hkv, Z, d, page_stride = _check_caches(k_cache, v_cache)
+    dev = k_cache.device
+    if q.dim() != 3:
+        raise _bad(f"q must be [T, Hq, d], got {tuple(q.shape)}")
+    T, Hq = q.shape[:2]
+    if probe.shape != q.shape:
+        raise _bad(f"probe must have q's shape {tuple(q.shape)}, got {tuple(probe.shape)}")
+    if block_table.dim() != 2:
+        raise _bad("block_table must be [S, W]")
+    S, W = block_table.shape
+    _check_ints(dev, torch.int32, block_table=(block_table, (S, W)), cu_q=(cu_q, (S + 1,)), kv_lens=(kv_lens, (S,)))
+    dtype = LLA_DTYPE_BF16 if k_cache.dtype == torch.bfloat16 else LLA_DTYPE_FP32
+    with _on_stream(dev, stream) as sp:
+        q, qs = _token_rows(q, "q", k_cache, Hq, d)
+        probe, rs = _token_rows(probe, "probe", k_cache, Hq, d)
+        if out is None:
+            out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
+        elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
+            raise _bad(f"out must be a contiguous {q.dtype} tensor of shape {tuple(q.shape)} on {dev}")
+        ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                                                workspace.numel() * workspace.element_size())
+        lla_paged_parallax(dtype, int(path), q.data_ptr(), probe.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                           block_table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(), out.data_ptr(), T, S, Hq, Hkv, d,
+                           Z, P, W, int(max_new), qs, rs, page_stride, float(tau), 1 if causal else 0, ws_ptr, ws_bytes,
+                           sp)
+    return out

@@ -679,6 +679,9 @@ int lla_sync_status(void* stream) {
     if (word & lla::kDevErrSmemAlign)
         return fail(LLA_ERR_CUDA, "tensor kernel: dynamic shared memory not 1024-byte aligned, no work done (error word 0x%x)",
                     word);
+    if (word & lla::kDevErrPagedArg)
+        return fail(LLA_ERR_INVALID_ARG,
+                    "a paged call met a length, slot or page id that its tensors do not hold (error word 0x%x)", word);
     if (word & lla::kDevErrMbarTimeout)
         return fail(LLA_ERR_DEVICE_TIMEOUT, "a bounded device-side wait gave up (error word 0x%x)", word);
     return LLA_OK;

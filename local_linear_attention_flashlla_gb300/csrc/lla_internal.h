@@ -29,8 +29,9 @@ struct Problem {
 };
 
 // Device error word: bit flags set by kernels that gave up (a bounded wait ran out, or the
-// tensor kernel found its dynamic shared memory misaligned and did no work).
-enum DeviceError : unsigned { kDevErrMbarTimeout = 1u, kDevErrSmemAlign = 2u };
+// tensor kernel found its dynamic shared memory misaligned and did no work), or that met a length,
+// slot or page id on the device that the tensors of a paged call do not hold.
+enum DeviceError : unsigned { kDevErrMbarTimeout = 1u, kDevErrSmemAlign = 2u, kDevErrPagedArg = 4u };
 
 // Decode step: one new query per (b, h) against a key/value cache of n rows (row stride n_cap).
 struct DecodeProblem {

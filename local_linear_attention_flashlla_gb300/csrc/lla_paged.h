@@ -1,0 +1,332 @@
+// Shared by the paged-cache translation units: the problem description, the division of ragged
+// (sequence, key head, row tile) work among a fixed number of CTAs, and the partial results of tiles
+// that several CTAs share.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace lla {
+
+// lla_paged_parallax arguments after validation (include/lla.h describes them).
+struct PagedProblem {
+    const void* q;            // [T, Hq, d], token stride q_stride
+    const void* probe;        // [T, Hq, d], token stride r_stride
+    const void* k;            // [num_pages, Hkv, page, d], page stride page_stride
+    const void* v;
+    const int* table;         // [S, width]
+    const int* cu_q;          // [S + 1]
+    const int* kv_lens;       // [S]
+    void* out;                // [T, Hq, d] contiguous
+    int T, S, Hq, Hkv, G, d, page_shift, num_pages, width, max_new;
+    long long q_stride, r_stride, page_stride;   // elements
+    float tau;
+    int causal, dtype;
+    unsigned* err;            // device error word
+    void* ws;                 // partial results (paged_workspace_bytes)
+};
+
+// A row tile of a (sequence, key head): rows [tile R, (tile + 1) R) of its nq * G query rows, where
+// row r is token r / G and query head h G + r % G.  A tile's work is its key blocks; a unit is one of
+// them.  All units of a call, in the order (sequence, key head, tile, block), are dealt to the CTAs in
+// contiguous ranges of equal length, whatever the lengths of the sequences: a tile that a range border
+// cuts is finished by merging its parts (paged_merge).
+struct PartHeader {
+    int parts;      // 0: this CTA starts no tile that others finish; else CTAs that share it
+    int row0;       // first row (in the flat row space of its sequence: token * G + head in group)
+    int rows;       // rows of the tile
+    int token0;     // row of q / out that holds token 0 of the sequence
+    int head;       // key head
+    int pad[3];
+};
+
+constexpr int kPagedMaxCtas = 1024;
+
+// Partials: per CTA two slots (0: the tile whose earlier blocks another CTA has, 1: the tile whose
+// later blocks another CTA has); a slot holds rows x { m, omega, A, s0 } and rows x 2 x d sums.
+inline size_t paged_part_floats(int rows, int d) { return (size_t)rows * (4 + 2 * (size_t)d); }
+inline size_t paged_workspace_bytes(int ctas, int rows, int d) {
+    return (size_t)kPagedMaxCtas * sizeof(PartHeader) + (size_t)ctas * 2 * paged_part_floats(rows, d) * sizeof(float);
+}
+
+// How a path divides the work: rows of a tile, keys of a block, CTAs, least units worth a CTA.
+struct PagedSplit {
+    int rows, keys, ctas, min_units;
+};
+
+PagedSplit paged_simt_split(const PagedProblem& p, int sms);
+cudaError_t launch_paged_simt(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream);
+cudaError_t launch_paged_merge(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream);
+
+#ifdef __CUDACC__
+namespace paged {
+
+// What a kernel needs of the problem, by value.
+struct Work {
+    const int* table;
+    const int* cu_q;
+    const int* kv_lens;
+    int T, S, Hkv, G, width, page_shift, num_pages, max_new, causal;
+    int rows, keys, ctas, min_units;
+    PartHeader* hdr;
+    float* part;
+    unsigned* err;
+};
+
+inline Work make_work(const PagedProblem& p, const PagedSplit& sp) {
+    Work w;
+    w.table = p.table; w.cu_q = p.cu_q; w.kv_lens = p.kv_lens;
+    w.T = p.T; w.S = p.S; w.Hkv = p.Hkv; w.G = p.G; w.width = p.width; w.page_shift = p.page_shift;
+    w.num_pages = p.num_pages; w.max_new = p.max_new; w.causal = p.causal;
+    w.rows = sp.rows; w.keys = sp.keys; w.ctas = sp.ctas; w.min_units = sp.min_units;
+    w.hdr = static_cast<PartHeader*>(p.ws);
+    w.part = reinterpret_cast<float*>(static_cast<char*>(p.ws) + (size_t)kPagedMaxCtas * sizeof(PartHeader));
+    w.err = p.err;
+    return w;
+}
+
+// A sequence as the kernels see it: lengths outside what the tensors hold are cut to it and reported
+// through the device error word, so that no later index can leave them.
+struct Seq {
+    int token0, nq, L;
+};
+
+__device__ __forceinline__ Seq load_seq(const Work& w, int s) {
+    const int c0 = w.cu_q[s], c1 = w.cu_q[s + 1], kv = w.kv_lens[s];
+    Seq q;
+    q.token0 = min(max(c0, 0), w.T);
+    const int end = min(max(c1, q.token0), w.T);
+    q.nq = min(end - q.token0, w.max_new);
+    q.L = min(max(kv, 0), w.width << w.page_shift);
+    if (q.token0 != c0 || q.token0 + q.nq != c1 || q.L != kv) atomicOr(w.err, (unsigned)kDevErrPagedArg);
+    return q;
+}
+
+// sum_{i < n} floor((a i + b) / m), by the Euclid-like exchange of slope and modulus.
+__device__ inline unsigned long long floor_sum(unsigned long long n, unsigned long long m, unsigned long long a,
+                                               unsigned long long b) {
+    unsigned long long ans = 0;
+    while (n > 0) {
+        if (a >= m) {
+            ans += (n - 1) * n / 2 * (a / m);
+            a %= m;
+        }
+        if (b >= m) {
+            ans += n * (b / m);
+            b %= m;
+        }
+        const unsigned long long y = a * n + b;
+        if (y < m) break;
+        n = y / m;
+        b = y % m;
+        const unsigned long long t = m;
+        m = a;
+        a = t;
+    }
+    return ans;
+}
+
+__device__ __forceinline__ int tiles_of(const Work& w, const Seq& q) { return (q.nq * w.G + w.rows - 1) / w.rows; }
+
+// Keys that the rows of tile i see, at most (the last row's); 0 if none.
+__device__ __forceinline__ int tile_keys(const Work& w, const Seq& q, int i) {
+    if (!w.causal) return q.L;
+    const int last = (min((i + 1) * w.rows, q.nq * w.G) - 1) / w.G;
+    return min(max(q.L - q.nq + last + 1, 0), q.L);
+}
+
+// Units charged for tile i (>= 1: a tile without keys still has its rows to write).  A causal sequence
+// with fewer keys than tokens is charged as if it had as many.
+__device__ __forceinline__ int tile_units(const Work& w, const Seq& q, int i) {
+    if (!w.causal) return max(1, (q.L + w.keys - 1) / w.keys);
+    const int last = (min((i + 1) * w.rows, q.nq * w.G) - 1) / w.G;
+    return (max(q.L - q.nq, 0) + last) / w.keys + 1;
+}
+
+// Units of the first n tiles of one key head (n <= tiles).
+__device__ inline long long units_before(const Work& w, const Seq& q, int n) {
+    if (n == 0) return 0;
+    if (!w.causal) return (long long)n * tile_units(w, q, 0);
+    const int tiles = tiles_of(w, q);
+    long long u = 0;
+    int full = n;
+    if (n == tiles) {
+        u = tile_units(w, q, n - 1);
+        --full;
+    }
+    if (full > 0) {
+        const unsigned long long c0 = (unsigned long long)max(q.L - q.nq, 0);
+        u += full + (long long)floor_sum(full, (unsigned long long)w.keys * w.G, w.rows, c0 * w.G + w.rows - 1);
+    }
+    return u;
+}
+
+__device__ __forceinline__ long long seq_units(const Work& w, const Seq& q) {
+    return q.nq > 0 ? units_before(w, q, tiles_of(w, q)) * w.Hkv : 0;
+}
+
+// A position in the order of units.
+struct Walk {
+    long long u, end;     // next unit of this CTA, end of its range
+    long long total;
+    int active;           // CTAs that have work
+    int s, h, i, j;       // sequence, key head, tile, block
+    Seq q;
+};
+
+__device__ __forceinline__ long long block_sum(long long v, long long* red) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (blockDim.x + 31) >> 5;
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    long long t = 0;
+    for (int i = 0; i < nw; ++i) t += red[i];
+    __syncthreads();
+    return t;
+}
+
+// Range of this CTA (blockIdx.x) and the tile it begins in.  Every thread of the block calls it; the
+// shared scratch is 40 long longs.  active = 0: no units at all.  blockDim.x is a multiple of 32.
+__device__ inline Walk begin_walk(const Work& w, long long* sh) {
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
+    long long mine = 0;
+    for (int s = tid; s < w.S; s += nt) mine += seq_units(w, load_seq(w, s));
+    Walk k;
+    k.total = block_sum(mine, sh);
+    k.s = k.h = k.i = k.j = 0;
+    k.q.token0 = k.q.nq = k.q.L = 0;
+    k.u = k.end = 0;
+    const long long most = (k.total + w.min_units - 1) / w.min_units;
+    k.active = (int)(most < w.ctas ? most : w.ctas);
+    if ((int)blockIdx.x >= k.active) return k;
+    k.u = k.total * blockIdx.x / k.active;
+    k.end = k.total * (blockIdx.x + 1) / k.active;
+    long long before = 0;
+    int* at = reinterpret_cast<int*>(sh + 36);
+    for (int s0 = 0; s0 < w.S; s0 += nt) {
+        const int s = s0 + tid;
+        const long long mineu = s < w.S ? seq_units(w, load_seq(w, s)) : 0;
+        long long inc = mineu;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += t;
+        }
+        if (lane == 31) sh[warp] = inc;
+        if (tid == 0) *at = -1;
+        __syncthreads();
+        long long pre = before, all = before;
+        for (int i = 0; i < nw; ++i) {
+            if (i < warp) pre += sh[i];
+            all += sh[i];
+        }
+        pre += inc - mineu;
+        if (mineu > 0 && k.u >= pre && k.u < pre + mineu) {
+            *at = s;
+            sh[35] = pre;
+        }
+        __syncthreads();
+        const int found = *at;
+        const long long fpre = sh[35];
+        __syncthreads();
+        if (found >= 0) {
+            k.s = found;
+            k.q = load_seq(w, found);
+            const int tiles = tiles_of(w, k.q);
+            long long rem = k.u - fpre;
+            const long long per = units_before(w, k.q, tiles);
+            k.h = (int)(rem / per);
+            rem -= k.h * per;
+            int lo = 0, hi = tiles - 1;       // the last tile with units_before <= rem
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (units_before(w, k.q, mid) <= rem) lo = mid;
+                else hi = mid - 1;
+            }
+            k.i = lo;
+            k.j = (int)(rem - units_before(w, k.q, lo));
+            break;
+        }
+        before = all;
+    }
+    return k;
+}
+
+// The CTA's next piece of work: blocks [j0, j1) of a tile.
+struct Piece {
+    int s, h, i;
+    Seq q;
+    int row0, rows;       // flat rows of the tile
+    int keys;             // keys that the tile's last row sees
+    int j0, j1;           // blocks that hold any of them
+    int slot;             // -1: the whole tile is this CTA's; 0, 1: partial slot
+    int parts;            // slot 1: CTAs that share the tile
+};
+
+__device__ __forceinline__ bool next_piece(const Work& w, Walk& k, Piece& p) {
+    if (k.u >= k.end) return false;
+    const int units = tile_units(w, k.q, k.i);
+    const long long left = k.end - k.u;
+    const int take = (int)(left < units - k.j ? left : units - k.j);
+    p.s = k.s; p.h = k.h; p.i = k.i; p.q = k.q;
+    p.row0 = k.i * w.rows;
+    p.rows = min(w.rows, k.q.nq * w.G - p.row0);
+    p.keys = tile_keys(w, k.q, k.i);
+    const int nb = (p.keys + w.keys - 1) / w.keys;
+    p.j0 = min(k.j, nb);
+    p.j1 = min(k.j + take, nb);
+    const bool first = k.j == 0, last = k.j + take == units;
+    p.slot = first && last ? -1 : first ? 1 : 0;
+    p.parts = 0;
+    if (p.slot == 1) {
+        const long long tile_end = k.u + units;      // first unit behind the tile (k.j is 0)
+        const long long c = (tile_end * k.active - 1) / k.total;
+        p.parts = (int)(c - blockIdx.x) + 1;
+    }
+    k.u += take;
+    k.j += take;
+    if (k.j == units) {
+        k.j = 0;
+        if (++k.i == tiles_of(w, k.q)) {
+            k.i = 0;
+            if (++k.h == w.Hkv) {
+                k.h = 0;
+                if (k.u < k.end) {
+                    do {
+                        if (++k.s >= w.S) {           // lengths that changed during the call
+                            k.end = k.u;
+                            break;
+                        }
+                        k.q = load_seq(w, k.s);
+                    } while (k.q.nq == 0);
+                }
+            }
+        }
+    }
+    return true;
+}
+
+__device__ __forceinline__ float* part_stats(const Work& w, int cta, int slot, int d) {
+    return w.part + ((size_t)cta * 2 + slot) * ((size_t)w.rows * (4 + 2 * d));
+}
+__device__ __forceinline__ float* part_sums(const Work& w, int cta, int slot, int d) {
+    return part_stats(w, cta, slot, d) + (size_t)w.rows * 4;
+}
+
+// This CTA's header: written once by every CTA, with the tile that it starts and others finish (its
+// last piece) or none.
+__device__ __forceinline__ void write_header(const Work& w, const Piece& p, bool shared) {
+    PartHeader h;
+    h.parts = shared ? p.parts : 0;
+    h.row0 = p.row0;
+    h.rows = p.rows;
+    h.token0 = p.q.token0;
+    h.head = p.h;
+    h.pad[0] = h.pad[1] = h.pad[2] = 0;
+    w.hdr[blockIdx.x] = h;
+}
+
+}  // namespace paged
+#endif
+
+}  // namespace lla

@@ -1,0 +1,364 @@
+// Parallax attention over a paged cache on CUDA cores (every product in fp32; any head dim, bf16 or
+// fp32), and the merge of row tiles that several CTAs share (all paths).
+//
+// Per query row, over its keys in blocks, one pass (base-2 logits l = tau log2(e) q.k, t = probe.k):
+//   m <- max(m, max l),  p = 2^(l - m),  w += p,  A += p (t - s0),  O1 += p v,  O2 += p (t - s0) v,
+//   out = ((1 + A/w) O1 - O2) / w.
+// The centre s0 is the softmax mean of t over the row's first block: the formula holds for any value,
+// and one near the mean keeps O2 from holding a large multiple of O1 that the end would cancel.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+
+#include "../../include/lla.h"
+#include "lla_internal.h"
+#include "lla_paged.h"
+
+namespace lla {
+namespace paged {
+namespace {
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void put(float* p, float x) { *p = x; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// 16 bytes of T as floats.
+template <typename T>
+__device__ __forceinline__ void load16(const T* g, float* dst) {
+    const uint4 raw = *reinterpret_cast<const uint4*>(g);
+    const T* e = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+    for (int i = 0; i < (int)(16 / sizeof(T)); ++i) dst[i] = to_f(e[i]);
+}
+
+constexpr int kThreads = 256;
+
+// R rows of a tile, TX threads to a row (they lie in one warp), BN keys of a block.
+template <int D, int R>
+struct Shape {
+    static constexpr int TX = kThreads / R;
+    static constexpr int BN = R == 32 ? 32 : 64;
+    static constexpr int KPT = BN / TX;                 // keys of a thread
+    static constexpr int CPT = (D + TX - 1) / TX;       // output columns of a thread
+    static constexpr int KS = D + 4;                    // row stride of K: float4 reads of TX rows do not collide
+    static constexpr size_t smem = sizeof(float) * (2 * R * D + BN * KS + BN * D + 2 * R * BN);
+};
+
+struct SimtArgs {
+    Work w;
+    const void* q;
+    const void* probe;
+    const void* k;
+    const void* v;
+    void* out;
+    int Hq;
+    long long q_stride, r_stride, page_stride;
+    float scale;     // tau log2(e)
+};
+
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
+    using Sh = Shape<D, R>;
+    constexpr int TX = Sh::TX, BN = Sh::BN, KPT = Sh::KPT, CPT = Sh::CPT, KS = Sh::KS, VE = 16 / sizeof(T);
+    extern __shared__ __align__(16) float sm[];
+    __shared__ long long scratch[40];
+    float* Qs = sm;
+    float* Rs = Qs + R * D;
+    float* Ks = Rs + R * D;
+    float* Vs = Ks + BN * KS;
+    float* P1 = Vs + BN * D;
+    float* P2 = P1 + R * BN;
+    const Work& w = a.w;
+    const int tid = threadIdx.x, row = tid / TX, tx = tid % TX;
+    const T* gq = static_cast<const T*>(a.q);
+    const T* gr = static_cast<const T*>(a.probe);
+    const T* gk = static_cast<const T*>(a.k);
+    const T* gv = static_cast<const T*>(a.v);
+
+    Walk wk = begin_walk(w, scratch);
+    Piece p;
+    p.parts = 0; p.row0 = p.rows = p.h = 0; p.q.token0 = 0;
+    bool shared = false;
+    while (next_piece(w, wk, p)) {
+        shared = p.slot == 1;
+        for (int e = tid; e < R * (D / VE); e += kThreads) {
+            const int r = e / (D / VE), c = (e % (D / VE)) * VE;
+            float* dq = Qs + r * D + c;
+            float* dr = Rs + r * D + c;
+            if (r < p.rows) {
+                const int fr = p.row0 + r, token = p.q.token0 + fr / w.G, head = p.h * w.G + fr % w.G;
+                load16(gq + token * a.q_stride + (long long)head * D + c, dq);
+                load16(gr + token * a.r_stride + (long long)head * D + c, dr);
+            } else {
+#pragma unroll
+                for (int i = 0; i < VE; ++i) dq[i] = dr[i] = 0.f;
+            }
+        }
+        int limit = 0;                                   // keys this row sees
+        if (row < p.rows)
+            limit = w.causal ? min(max(p.q.L - p.q.nq + (p.row0 + row) / w.G + 1, 0), p.q.L) : p.q.L;
+        float m = -INFINITY, om = 0.f, A = 0.f, s0 = 0.f;
+        float o1[CPT], o2[CPT];
+#pragma unroll
+        for (int i = 0; i < CPT; ++i) o1[i] = o2[i] = 0.f;
+
+        for (int j = p.j0; j < p.j1; ++j) {
+            const int key0 = j * BN;
+            for (int e = tid; e < BN * (D / VE); e += kThreads) {
+                const int kk = e / (D / VE), c = (e % (D / VE)) * VE, key = key0 + kk;
+                float* dk = Ks + kk * KS + c;
+                float* dv = Vs + kk * D + c;
+                int page = -1;
+                if (key < p.keys) {
+                    page = w.table[(size_t)p.s * w.width + (key >> w.page_shift)];
+                    if (page < 0 || page >= w.num_pages) {
+                        page = -1;
+                        atomicOr(w.err, (unsigned)kDevErrPagedArg);
+                    }
+                }
+                if (page >= 0) {
+                    const long long off = page * a.page_stride +
+                        (((long long)p.h << w.page_shift) + (key & ((1 << w.page_shift) - 1))) * D + c;
+                    load16(gk + off, dk);
+                    load16(gv + off, dv);
+                } else {                                 // keys that no row sees: zeros, whatever the page holds
+#pragma unroll
+                    for (int i = 0; i < VE; ++i) dk[i] = dv[i] = 0.f;
+                }
+            }
+            __syncthreads();
+            float s[KPT], t[KPT];
+#pragma unroll
+            for (int u = 0; u < KPT; ++u) s[u] = t[u] = 0.f;
+#pragma unroll 4
+            for (int c = 0; c < D; c += 4) {
+                const float4 q4 = *reinterpret_cast<const float4*>(Qs + row * D + c);
+                const float4 r4 = *reinterpret_cast<const float4*>(Rs + row * D + c);
+#pragma unroll
+                for (int u = 0; u < KPT; ++u) {
+                    const float4 k4 = *reinterpret_cast<const float4*>(Ks + (tx + TX * u) * KS + c);
+                    s[u] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[u]))));
+                    t[u] = fmaf(r4.x, k4.x, fmaf(r4.y, k4.y, fmaf(r4.z, k4.z, fmaf(r4.w, k4.w, t[u]))));
+                }
+            }
+            float bm = -INFINITY;
+#pragma unroll
+            for (int u = 0; u < KPT; ++u) {
+                s[u] = key0 + tx + TX * u < limit ? s[u] * a.scale : -INFINITY;
+                bm = fmaxf(bm, s[u]);
+            }
+#pragma unroll
+            for (int o = TX / 2; o; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
+            const float mn = fmaxf(m, bm);
+            const float base = mn == -INFINITY ? 0.f : mn;
+            const float corr = exp2f(m - base);          // m = -inf: 0
+            float ps = 0.f, pt = 0.f;
+#pragma unroll
+            for (int u = 0; u < KPT; ++u) {
+                s[u] = exp2f(s[u] - base);
+                ps += s[u];
+                pt = fmaf(s[u], t[u], pt);
+            }
+#pragma unroll
+            for (int o = TX / 2; o; o >>= 1) {
+                ps += __shfl_xor_sync(0xffffffffu, ps, o);
+                pt += __shfl_xor_sync(0xffffffffu, pt, o);
+            }
+            if (om == 0.f && ps > 0.f) s0 = pt / ps;     // the row's first block with keys
+            m = mn;
+            om = om * corr + ps;
+            A = A * corr + (pt - s0 * ps);
+#pragma unroll
+            for (int u = 0; u < KPT; ++u) {
+                P1[row * BN + tx + TX * u] = s[u];
+                P2[row * BN + tx + TX * u] = s[u] * (t[u] - s0);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < CPT; ++i) {
+                o1[i] *= corr;
+                o2[i] *= corr;
+            }
+#pragma unroll 4
+            for (int kk = 0; kk < BN; ++kk) {
+                const float a1 = P1[row * BN + kk], a2 = P2[row * BN + kk];
+#pragma unroll
+                for (int i = 0; i < CPT; ++i) {
+                    const int c = tx + TX * i;
+                    if (D % TX == 0 || c < D) {
+                        const float x = Vs[kk * D + c];
+                        o1[i] = fmaf(a1, x, o1[i]);
+                        o2[i] = fmaf(a2, x, o2[i]);
+                    }
+                }
+            }
+            __syncthreads();
+        }
+
+        if (row < p.rows) {
+            if (p.slot < 0) {
+                const int fr = p.row0 + row, token = p.q.token0 + fr / w.G, head = p.h * w.G + fr % w.G;
+                T* o = static_cast<T*>(a.out) + ((long long)token * a.Hq + head) * D;
+                const float inv = om != 0.f ? 1.f / om : 0.f, c1 = 1.f + A * inv;
+#pragma unroll
+                for (int i = 0; i < CPT; ++i)
+                    if (D % TX == 0 || tx + TX * i < D) put(o + tx + TX * i, (c1 * o1[i] - o2[i]) * inv);
+            } else {
+                if (tx == 0)
+                    *reinterpret_cast<float4*>(part_stats(w, blockIdx.x, p.slot, D) + row * 4) = make_float4(m, om, A, s0);
+                float* o = part_sums(w, blockIdx.x, p.slot, D) + (size_t)row * 2 * D;
+#pragma unroll
+                for (int i = 0; i < CPT; ++i)
+                    if (D % TX == 0 || tx + TX * i < D) {
+                        o[tx + TX * i] = o1[i];
+                        o[D + tx + TX * i] = o2[i];
+                    }
+            }
+        }
+        __syncthreads();
+    }
+    if (tid == 0) write_header(w, p, shared);
+}
+
+// Joins the parts of the tile that CTA blockIdx.x starts and others finish: part 0 is its slot 1, part
+// i > 0 slot 0 of CTA blockIdx.x + i.  With the common maximum and one centre,
+//   out = sum_i f_i ((1 + A/w - (s0_i - s0)) O1_i - O2_i) / w,   f_i = 2^(m_i - m).
+// The order of the sum is that of the keys: results do not depend on which CTA was first.  With many
+// parts and few rows (a long cache and one query) several warps share a row's parts.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) paged_merge_kernel(Work w, T* __restrict__ out, int Hq) {
+    constexpr int VE = D >= 32 ? D / 32 : 1;
+    __shared__ float red[8][D];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    cudaGridDependencySynchronize();
+    const PartHeader h = w.hdr[blockIdx.x];
+    if (h.parts == 0) return;
+    const int share = h.parts >= 24 ? 8 : h.parts >= 8 ? 4 : h.parts >= 4 ? 2 : 1;   // warps on a row
+    const int rpi = 8 / share, mine = warp / share, sub = warp % share;
+    for (int r0 = blockIdx.y * rpi; r0 < h.rows; r0 += gridDim.y * rpi) {
+        const int r = r0 + mine;
+        float acc[VE];
+#pragma unroll
+        for (int i = 0; i < VE; ++i) acc[i] = 0.f;
+        if (r < h.rows) {
+            float m = -INFINITY;
+            for (int i = lane; i < h.parts; i += 32)
+                m = fmaxf(m, part_stats(w, blockIdx.x + i, i == 0, D)[r * 4]);
+            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float base = m == -INFINITY ? 0.f : m;
+            const float s0 = part_stats(w, blockIdx.x, 1, D)[r * 4 + 3];
+            float om = 0.f, A = 0.f;
+            for (int i = lane; i < h.parts; i += 32) {
+                const float4 st = *reinterpret_cast<const float4*>(part_stats(w, blockIdx.x + i, i == 0, D) + r * 4);
+                const float f = exp2f(st.x - base);
+                om = fmaf(f, st.y, om);
+                A = fmaf(f, fmaf(st.w - s0, st.y, st.z), A);
+            }
+            for (int o = 16; o; o >>= 1) {
+                om += __shfl_xor_sync(0xffffffffu, om, o);
+                A += __shfl_xor_sync(0xffffffffu, A, o);
+            }
+            if (om != 0.f) {                             // 0: no key in any part; NaN stays NaN
+                const float inv = 1.f / om, c1 = 1.f + A * inv;
+#pragma unroll 4
+                for (int i = sub; i < h.parts; i += share) {
+                    const float4 st = *reinterpret_cast<const float4*>(part_stats(w, blockIdx.x + i, i == 0, D) + r * 4);
+                    const float f = exp2f(st.x - base) * inv, f1 = f * (c1 - (st.w - s0));
+                    const float* o = part_sums(w, blockIdx.x + i, i == 0, D) + (size_t)r * 2 * D;
+                    if (f != 0.f && (D >= 32 || lane < D)) {
+#pragma unroll
+                        for (int e = 0; e < VE; ++e)
+                            acc[e] = fmaf(f1, o[lane * VE + e], fmaf(-f, o[D + lane * VE + e], acc[e]));
+                    }
+                }
+            }
+        }
+        if (share > 1) {
+            __syncthreads();
+            if (D >= 32 || lane < D)
+#pragma unroll
+                for (int e = 0; e < VE; ++e) red[warp][lane * VE + e] = acc[e];
+            __syncthreads();
+            if (sub == 0 && (D >= 32 || lane < D))
+                for (int i = 1; i < share; ++i)
+#pragma unroll
+                    for (int e = 0; e < VE; ++e) acc[e] += red[warp + i][lane * VE + e];
+        }
+        if (r < h.rows && sub == 0 && (D >= 32 || lane < D)) {
+            const int fr = h.row0 + r;
+            T* o = out + ((long long)(h.token0 + fr / w.G) * Hq + h.head * w.G + fr % w.G) * D + lane * VE;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) put(o + e, acc[e]);
+        }
+    }
+}
+
+template <typename T, int D, int R>
+cudaError_t launch_one(const SimtArgs& a, cudaStream_t stream) {
+    constexpr size_t smem = Shape<D, R>::smem;
+    auto* kern = paged_simt_kernel<T, D, R>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kern<<<a.w.ctas, kThreads, smem, stream>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_typed(const SimtArgs& a, int d, cudaStream_t stream) {
+    const bool few = a.w.rows == 8;
+    switch (d) {
+        case 16: return few ? launch_one<T, 16, 8>(a, stream) : launch_one<T, 16, 32>(a, stream);
+        case 32: return few ? launch_one<T, 32, 8>(a, stream) : launch_one<T, 32, 32>(a, stream);
+        case 64: return few ? launch_one<T, 64, 8>(a, stream) : launch_one<T, 64, 32>(a, stream);
+        default: return few ? launch_one<T, 128, 8>(a, stream) : launch_one<T, 128, 32>(a, stream);
+    }
+}
+
+template <typename T, int D>
+cudaError_t merge_one(const Work& w, void* out, int Hq, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(w.ctas, (w.rows + 7) / 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D>, w, static_cast<T*>(out), Hq);
+}
+
+template <typename T>
+cudaError_t merge_typed(const Work& w, void* out, int Hq, int d, cudaStream_t stream) {
+    switch (d) {
+        case 16: return merge_one<T, 16>(w, out, Hq, stream);
+        case 32: return merge_one<T, 32>(w, out, Hq, stream);
+        case 64: return merge_one<T, 64>(w, out, Hq, stream);
+        default: return merge_one<T, 128>(w, out, Hq, stream);
+    }
+}
+
+}  // namespace
+}  // namespace paged
+
+PagedSplit paged_simt_split(const PagedProblem& p, int sms) {
+    // rows: 8 where no sequence has more than eight query rows to a key head (a decode step), else 32
+    const bool few = (long long)p.max_new * p.G <= 8;
+    return PagedSplit{few ? 8 : 32, few ? 64 : 32, 2 * sms, few ? 2 : 4};
+}
+
+cudaError_t launch_paged_simt(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream) {
+    paged::SimtArgs a{paged::make_work(p, sp), p.q, p.probe, p.k, p.v, p.out, p.Hq, p.q_stride, p.r_stride,
+                      p.page_stride, p.tau * 1.4426950408889634f};
+    return p.dtype == LLA_DTYPE_BF16 ? paged::launch_typed<__nv_bfloat16>(a, p.d, stream)
+                                     : paged::launch_typed<float>(a, p.d, stream);
+}
+
+cudaError_t launch_paged_merge(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream) {
+    const paged::Work w = paged::make_work(p, sp);
+    return p.dtype == LLA_DTYPE_BF16 ? paged::merge_typed<__nv_bfloat16>(w, p.out, p.Hq, p.d, stream)
+                                     : paged::merge_typed<float>(w, p.out, p.Hq, p.d, stream);
+}
+
+}  // namespace lla
