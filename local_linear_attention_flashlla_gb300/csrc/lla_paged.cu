@@ -265,7 +265,7 @@ int check_paged_sizes(int dtype, int path, int T, int S, int Hq, int Hkv, int d,
 }
 
 PagedSplit split_of(const PagedProblem& p, int rpath, int sms) {
-    (void)rpath;
+    if (rpath == LLA_PATH_TENSOR && paged_decode_fits(p)) return paged_decode_split(p, sms);
     return paged_simt_split(p, sms);
 }
 
@@ -410,13 +410,15 @@ int lla_paged_parallax(int dtype, int path, const void* q, const void* probe, co
     cudaError_t e = cudaSuccess;
     if (!workspace && (e = cudaMallocAsync(&p.ws, need, stream)) != cudaSuccess)
         return cuda_failf(e, "cudaMallocAsync(workspace)");
-    e = lla::launch_paged_simt(p, sp, stream);
+    const char* why = nullptr;
+    if (rpath == LLA_PATH_TENSOR && lla::paged_decode_fits(p)) e = lla::launch_paged_decode(p, sp, stream, &why);
+    else e = lla::launch_paged_simt(p, sp, stream);
     if (e == cudaSuccess) e = lla::launch_paged_merge(p, sp, stream);
     if (!workspace) {
         const cudaError_t e2 = cudaFreeAsync(p.ws, stream);
         if (e == cudaSuccess && e2 != cudaSuccess) return cuda_failf(e2, "cudaFreeAsync(workspace)");
     }
-    if (e != cudaSuccess) return cuda_failf(e, "paged attention launch");
+    if (e != cudaSuccess) return cuda_failf(e, why ? why : "paged attention launch");
     return LLA_OK;
 }
 

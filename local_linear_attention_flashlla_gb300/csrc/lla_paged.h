@@ -55,6 +55,10 @@ struct PagedSplit {
     int rows, keys, ctas, min_units;
 };
 
+// bf16, d in {64, 128}, at most 16 query rows to a key head (max_new * G): lla_paged_decode.cu.
+bool paged_decode_fits(const PagedProblem& p);
+PagedSplit paged_decode_split(const PagedProblem& p, int sms);
+cudaError_t launch_paged_decode(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream, const char** why);
 PagedSplit paged_simt_split(const PagedProblem& p, int sms);
 cudaError_t launch_paged_simt(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream);
 cudaError_t launch_paged_merge(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream);

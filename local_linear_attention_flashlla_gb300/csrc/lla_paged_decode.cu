@@ -1,0 +1,435 @@
+// Parallax attention over a paged bf16 cache for few query rows to a key head (a decode step, a few
+// drafted tokens): reading the cache bounds it, 2 d bytes of K and of V for 8 d flops per row.
+//
+// The query rows and their probes are stacked in one 16-row operand of mma.m16n8k16 (rows 0-7 the
+// queries, 8-15 the probes of the same rows), so one product gives the logits and t = probe.k, and the
+// accumulator layout puts both of a (row, key) pair in one thread.  The weights p and p (t - s0) are
+// then, without any exchange, the two row halves of the second product's operand, whose accumulators
+// hold O1 = sum p v and O2 = sum p (t - s0) v.  A 128-row tcgen05 tile would carry 8 to 16 useful
+// rows; here the tensor pipe has a third of the time that the bytes take.
+//
+// A CTA has four computing warps, each with a quarter of every 64-key block and a running maximum of
+// its own, and one warp that feeds the blocks through a TMA ring (a box per page); two CTAs to an SM
+// keep 192 KB of the cache in flight.  The four warps' sums are joined once per tile.
+#include <math.h>
+
+#include "../../include/lla.h"
+#include "lla_internal.h"
+#include "lla_paged.h"
+#include "paged_tc.cuh"
+
+namespace lla {
+namespace paged {
+namespace {
+
+constexpr int kKeys = 64;                      // keys of a block
+constexpr int kWarps = 4;                      // computing warps
+constexpr int kThreads = (kWarps + 1) * 32;
+
+template <int D>
+struct DecShape {
+    static constexpr int kStages = D == 128 ? 3 : 6;
+    static constexpr int kTile = kKeys * D * 2;            // bytes of a K (or V) block: [D / 64][64 rows][128 B]
+    static constexpr int kScratch = 8192;                  // joining the warps' sums
+    static constexpr size_t smem = (size_t)kStages * 2 * kTile + kScratch + 1024;   // 1024: alignment of the ring
+};
+
+struct DecArgs {
+    Work w;
+    const __nv_bfloat16* q;
+    const __nv_bfloat16* probe;
+    __nv_bfloat16* out;
+    int Hq;
+    long long q_stride, r_stride;
+    float scale;                               // tau log2(e)
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Byte offset of 16-byte piece c of row r in a block ([D / 64][64 rows][128 B], 128-byte swizzle).
+__device__ __forceinline__ uint32_t piece_off(int r, int c) {
+    return (uint32_t)((c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+}
+
+// The feeding warp: one block after another of this CTA's pieces, a box to a lane.
+template <int D>
+__device__ void feed(const Work& w, Walk wk, const CUtensorMap* mk, const CUtensorMap* mv, uint32_t ring, uint64_t* full,
+                     uint64_t* empty, volatile int* err) {
+    constexpr int kStages = DecShape<D>::kStages, kTile = DecShape<D>::kTile;
+    const int lane = threadIdx.x & 31;
+    const int box = min(1 << w.page_shift, kBoxRows);        // rows of a box
+    const int boxes = kKeys / box;                           // <= 8
+    int stage = 0, phase = 0, issued = 0;
+    bool ok = true;
+    Piece p;
+    while (ok && next_piece(w, wk, p)) {
+        const int* row = w.table + (size_t)p.s * w.width;
+        for (int j = p.j0; j < p.j1; ++j) {
+            const int key = j * kKeys + lane * box;          // first key of this lane's box
+            const bool mine = lane < boxes && key < p.keys;
+            const int page = mine ? checked_page(w, row, key) : 0;
+            const int count = __popc(__ballot_sync(0xffffffffu, mine));
+            ok = __all_sync(0xffffffffu, tc::mbar_wait(&empty[stage], phase ^ 1, err));
+            if (!ok) break;
+            if (lane == 0) tc::mbar_arrive_expect_tx(&full[stage], (uint32_t)(count * box * D * 4));
+            __syncwarp();
+            if (mine) {
+                const uint32_t dst = ring + (uint32_t)(stage * 2 * kTile + lane * box * 128);
+                const int y = key & ((1 << w.page_shift) - 1);
+#pragma unroll
+                for (int x = 0; x < D / 64; ++x) {
+                    tma_load_4d(dst + x * (kKeys * 128), mk, &full[stage], x * 64, y, p.h, page);
+                    tma_load_4d(dst + kTile + x * (kKeys * 128), mv, &full[stage], x * 64, y, p.h, page);
+                }
+            }
+            __syncwarp();
+            ++issued;
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+    }
+    if (!ok || *err)
+        for (int t = max(issued - kStages, 0); t < issued; ++t) drain(&full[t % kStages], (t / kStages) & 1);
+}
+
+// MT sets of eight query rows.
+template <int D, int MT>
+__global__ void __launch_bounds__(kThreads, 2)
+    paged_decode_kernel(DecArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    using Sh = DecShape<D>;
+    constexpr int kStages = Sh::kStages, kTile = Sh::kTile;
+    constexpr int KS = D / 16;                 // k steps of the first product
+    constexpr int NT = D / 8;                  // column tiles of the second
+    constexpr int R = 8 * MT;
+    constexpr int SW = Sh::kScratch / (kWarps * R * 2 * 4);   // columns joined at a time
+    extern __shared__ unsigned char raw[];
+    __shared__ long long scratch[40];
+    __shared__ uint64_t full[kStages], empty[kStages];
+    __shared__ int err;
+    __shared__ float4 stats[kWarps][R];
+    unsigned char* base = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
+    const uint32_t ring = tc::smem_u32(base);
+    float* join = reinterpret_cast<float*>(base + (size_t)kStages * 2 * kTile);
+    // MT > 1: the first operand, by lane; the space serves the join after the last block of a piece
+    uint32_t* qs = reinterpret_cast<uint32_t*>(join);
+    static_assert(MT == 1 || MT * KS * 4 * 32 * 4 <= Sh::kScratch, "operand space");
+    const Work& w = a.w;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&empty[i], kWarps);
+        }
+        err = 0;
+        tc::mbar_fence_init();
+    }
+    Walk wk = begin_walk(w, scratch);
+    __syncthreads();
+
+    if (warp == kWarps) {
+        feed<D>(w, wk, &mk, &mv, ring, full, empty, &err);
+    } else {
+        const int g = lane >> 2, c2 = (lane & 3) * 2;
+        int stage = 0, phase = 0;
+        bool shared = false, ok = true;
+        Piece p;
+        p.parts = 0; p.row0 = p.rows = p.h = 0; p.q.token0 = 0;
+        // a warp whose wait gave up (ok false) computes nothing more, but passes every barrier of the join
+        while (next_piece(w, wk, p)) {
+            shared = p.slot == 1;
+            // first operand, rows g: queries in registers 0 and 2, probes in 1 and 3
+            uint32_t qf[MT == 1 ? KS : 1][4];
+            int limit[MT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                const int r = mt * 8 + g, fr = p.row0 + r;
+                const bool in = r < p.rows;
+                limit[mt] = 0;
+                const __nv_bfloat16* gq = a.q;
+                const __nv_bfloat16* gr = a.probe;
+                if (in) {
+                    limit[mt] = w.causal ? min(max(p.q.L - p.q.nq + fr / w.G + 1, 0), p.q.L) : p.q.L;
+                    const long long token = p.q.token0 + fr / w.G;
+                    const int head = p.h * w.G + fr % w.G;
+                    gq += token * a.q_stride + (long long)head * D + c2;
+                    gr += token * a.r_stride + (long long)head * D + c2;
+                }
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    if (MT > 1 && k % kWarps != warp) continue;      // MT > 1: a quarter of the steps each
+                    uint32_t f[4] = {0u, 0u, 0u, 0u};
+                    if (in) {
+                        f[0] = *reinterpret_cast<const uint32_t*>(gq + k * 16);
+                        f[1] = *reinterpret_cast<const uint32_t*>(gr + k * 16);
+                        f[2] = *reinterpret_cast<const uint32_t*>(gq + k * 16 + 8);
+                        f[3] = *reinterpret_cast<const uint32_t*>(gr + k * 16 + 8);
+                    }
+                    if (MT == 1) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) qf[k % (MT == 1 ? KS : 1)][i] = f[i];
+                    } else {
+                        *reinterpret_cast<uint4*>(&qs[((mt * KS + k) * 32 + lane) * 4]) = make_uint4(f[0], f[1], f[2], f[3]);
+                    }
+                }
+            }
+            if (MT > 1) tc::named_bar_sync(1, kWarps * 32);
+            float m[MT], om[MT], A[MT], s0[MT];
+            float o[MT][NT][4];                // per column pair: O1, O1, O2, O2
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                m[mt] = -INFINITY;
+                om[mt] = A[mt] = s0[mt] = 0.f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
+            }
+            bool first = true;
+            for (int j = p.j0; ok && j < p.j1; ++j) {
+                ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[stage], phase, &err));
+                if (!ok) break;
+                const int key0 = j * kKeys + warp * 16;
+                if (key0 < p.keys) {
+                    const uint32_t kt = ring + stage * 2 * kTile, vt = kt + kTile;
+                    const int row0 = warp * 16;
+                    if (key0 + 16 > p.keys) {
+                        // keys behind the last: their value rows hold a page's rest or an earlier block, and
+                        // a zero weight does not remove a NaN, so the rows are cleared
+                        for (int e = lane; e < 16 * (D / 8); e += 32) {
+                            const int r = e / (D / 8), c = e % (D / 8);
+                            if (key0 + r >= p.keys)
+                                *reinterpret_cast<uint4*>(base + (vt - ring) + piece_off(row0 + r, c)) = make_uint4(0, 0, 0, 0);
+                        }
+                        tc::fence_proxy_async_smem();        // the ring's next copy is the async proxy's
+                        __syncwarp();
+                    }
+                    float s[MT][2][4];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.f;
+                    {
+                        const int r = row0 + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+#pragma unroll
+                        for (int k = 0; k < KS; ++k) {
+                            uint32_t b[4];
+                            ldsm4(kt + piece_off(r, k * 2 + half), b);
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+                                uint32_t f[4];
+                                if (MT == 1) {
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) f[i] = qf[k % (MT == 1 ? KS : 1)][i];
+                                } else {
+                                    const uint4 x = *reinterpret_cast<const uint4*>(&qs[((mt * KS + k) * 32 + lane) * 4]);
+                                    f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+                                }
+                                mma16816(s[mt][0], f, b[0], b[1]);
+                                mma16816(s[mt][1], f, b[2], b[3]);
+                            }
+                        }
+                    }
+                    uint32_t pf[MT][4];
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        float l[4], t[4];
+#pragma unroll
+                        for (int n = 0; n < 2; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const bool in = key0 + n * 8 + c2 + e < limit[mt];
+                                l[n * 2 + e] = in ? s[mt][n][e] * a.scale : -INFINITY;
+                                t[n * 2 + e] = in ? s[mt][n][2 + e] : 0.f;
+                            }
+                        float bm = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
+                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
+                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
+                        // the reference point of the exponents follows the maximum only when that has grown by
+                        // more than 8 (weights to 2^8): most blocks then rescale nothing
+                        if (__any_sync(0xffffffffu, bm > m[mt] + 8.f)) {
+                            const float mn = fmaxf(m[mt], bm);
+                            const float f = mn == -INFINITY ? 1.f : tc::ex2(m[mt] - mn);
+                            m[mt] = mn;
+                            om[mt] *= f;
+                            A[mt] *= f;
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                o[mt][n][0] *= f;
+                                o[mt][n][1] *= f;
+                                o[mt][n][2] *= f;
+                                o[mt][n][3] *= f;
+                            }
+                        }
+                        const float mb = m[mt] == -INFINITY ? 0.f : m[mt];
+                        float ps = 0.f, pt = 0.f;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            l[e] = tc::ex2(l[e] - mb);
+                            ps += l[e];
+                            pt = fmaf(l[e], t[e], pt);
+                        }
+                        if (first) {           // centre: the softmax mean of t over the first keys
+                            float x = ps, y = pt;
+                            x += __shfl_xor_sync(0xffffffffu, x, 1);
+                            y += __shfl_xor_sync(0xffffffffu, y, 1);
+                            x += __shfl_xor_sync(0xffffffffu, x, 2);
+                            y += __shfl_xor_sync(0xffffffffu, y, 2);
+                            s0[mt] = x > 0.f ? y / x : 0.f;
+                        }
+                        om[mt] += ps;
+                        A[mt] += pt - s0[mt] * ps;
+                        // the value product takes the weights in bf16 (half a step is 2^-8 of each): its sums are fp32
+                        pf[mt][0] = pack_bf16(l[0], l[1]);
+                        pf[mt][1] = pack_bf16(l[0] * (t[0] - s0[mt]), l[1] * (t[1] - s0[mt]));
+                        pf[mt][2] = pack_bf16(l[2], l[3]);
+                        pf[mt][3] = pack_bf16(l[2] * (t[2] - s0[mt]), l[3] * (t[3] - s0[mt]));
+                    }
+                    first = false;
+                    {
+                        const int r = row0 + (lane & 15), half = lane >> 4;
+#pragma unroll
+                        for (int n = 0; n < NT / 2; ++n) {
+                            uint32_t b[4];
+                            ldsm4t(vt + piece_off(r, n * 2 + half), b);
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) {
+                                mma16816(o[mt][n * 2], pf[mt], b[0], b[1]);
+                                mma16816(o[mt][n * 2 + 1], pf[mt], b[2], b[3]);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(&empty[stage]);
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
+
+            // join the four warps: common maximum, centre of warp 0 (it has the piece's first keys)
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                for (int x = 1; x <= 2; x <<= 1) {
+                    om[mt] += __shfl_xor_sync(0xffffffffu, om[mt], x);
+                    A[mt] += __shfl_xor_sync(0xffffffffu, A[mt], x);
+                }
+                if ((lane & 3) == 0) stats[warp][mt * 8 + g] = make_float4(m[mt], om[mt], A[mt], s0[mt]);
+            }
+            tc::named_bar_sync(1, kWarps * 32);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                float mm = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < kWarps; ++x) mm = fmaxf(mm, stats[x][mt * 8 + g].x);
+                const float f = m[mt] == -INFINITY ? (om[mt] == 0.f ? 0.f : om[mt]) : tc::ex2(m[mt] - mm);
+                const float ds = s0[mt] - stats[0][mt * 8 + g].w;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    o[mt][n][2] = f * fmaf(ds, o[mt][n][0], o[mt][n][2]);
+                    o[mt][n][3] = f * fmaf(ds, o[mt][n][1], o[mt][n][3]);
+                    o[mt][n][0] *= f;
+                    o[mt][n][1] *= f;
+                }
+            }
+#pragma unroll
+            for (int sl = 0; sl < D / SW; ++sl) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int n = 0; n < SW / 8; ++n) {
+                        float* d1 = join + ((size_t)(warp * R + mt * 8 + g) * 2) * SW + n * 8 + c2;
+                        *reinterpret_cast<float2*>(d1) = make_float2(o[mt][sl * (SW / 8) + n][0], o[mt][sl * (SW / 8) + n][1]);
+                        *reinterpret_cast<float2*>(d1 + SW) = make_float2(o[mt][sl * (SW / 8) + n][2], o[mt][sl * (SW / 8) + n][3]);
+                    }
+                tc::named_bar_sync(1, kWarps * 32);
+                for (int e = tid; e < R * SW; e += kWarps * 32) {
+                    const int r = e / SW, c = e % SW;
+                    if (r < p.rows) {
+                        float x1 = 0.f, x2 = 0.f, mm = -INFINITY, ow = 0.f, aw = 0.f;
+                        const float sref = stats[0][r].w;
+#pragma unroll
+                        for (int x = 0; x < kWarps; ++x) {
+                            x1 += join[((size_t)(x * R + r) * 2) * SW + c];
+                            x2 += join[((size_t)(x * R + r) * 2 + 1) * SW + c];
+                            mm = fmaxf(mm, stats[x][r].x);
+                        }
+                        const float mb = mm == -INFINITY ? 0.f : mm;
+#pragma unroll
+                        for (int x = 0; x < kWarps; ++x) {
+                            const float4 st = stats[x][r];
+                            const float f = tc::ex2(st.x - mb);
+                            ow = fmaf(f, st.y, ow);
+                            aw = fmaf(f, fmaf(st.w - sref, st.y, st.z), aw);
+                        }
+                        if (p.slot < 0) {
+                            const int fr = p.row0 + r;
+                            const float inv = ow != 0.f ? 1.f / ow : 0.f;
+                            a.out[((long long)(p.q.token0 + fr / w.G) * a.Hq + p.h * w.G + fr % w.G) * D + sl * SW + c] =
+                                __float2bfloat16_rn(((1.f + aw * inv) * x1 - x2) * inv);
+                        } else {
+                            float* ps = part_sums(w, blockIdx.x, p.slot, D) + (size_t)r * 2 * D + sl * SW + c;
+                            ps[0] = x1;
+                            ps[D] = x2;
+                            if (sl == 0 && c == 0)
+                                *reinterpret_cast<float4*>(part_stats(w, blockIdx.x, p.slot, D) + r * 4) = make_float4(mm, ow, aw, sref);
+                        }
+                    }
+                }
+                tc::named_bar_sync(1, kWarps * 32);
+            }
+        }
+        if (tid == 0) write_header(w, p, shared);
+    }
+    __syncthreads();
+    if (tid == 0 && err) atomicOr(w.err, (unsigned)kDevErrMbarTimeout);
+}
+
+template <int D, int MT>
+cudaError_t launch_dec(const DecArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
+    constexpr size_t smem = DecShape<D>::smem;
+    auto* kern = paged_decode_kernel<D, MT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kern<<<a.w.ctas, kThreads, smem, stream>>>(a, mk, mv);
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace paged
+
+bool paged_decode_fits(const PagedProblem& p) { return (long long)p.max_new * p.G <= 16; }
+
+PagedSplit paged_decode_split(const PagedProblem& p, int sms) {
+    return PagedSplit{(long long)p.max_new * p.G <= 8 ? 8 : 16, paged::kKeys, 2 * sms, 2};
+}
+
+cudaError_t launch_paged_decode(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream, const char** why) {
+    CUtensorMap mk, mv;
+    if (!paged::make_cache_map(&mk, p.k, p) || !paged::make_cache_map(&mv, p.v, p)) {
+        *why = "tensor map of a paged cache";
+        return cudaErrorInvalidValue;
+    }
+    paged::DecArgs a{paged::make_work(p, sp), static_cast<const __nv_bfloat16*>(p.q), static_cast<const __nv_bfloat16*>(p.probe),
+                     static_cast<__nv_bfloat16*>(p.out), p.Hq, p.q_stride, p.r_stride, p.tau * 1.4426950408889634f};
+    if (p.d == 128)
+        return sp.rows == 8 ? paged::launch_dec<128, 1>(a, mk, mv, stream) : paged::launch_dec<128, 2>(a, mk, mv, stream);
+    return sp.rows == 8 ? paged::launch_dec<64, 1>(a, mk, mv, stream) : paged::launch_dec<64, 2>(a, mk, mv, stream);
+}
+
+}  // namespace lla
