@@ -10,6 +10,7 @@ raises ``LLAError``.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from collections import namedtuple
 
@@ -509,22 +510,22 @@ class _on_stream:
     inside belongs to the stream that its kernels run on.  Yields the stream's pointer."""
 
     def __init__(self, device, stream):
-        import torch
-        self._device, self._stream = torch.cuda.device(device), stream
+        self._device, self._stream, self._open = device, stream, ()
 
     def __enter__(self):
         import torch
-        self._device.__enter__()
-        self._inner = None
+        cuda = torch.cuda
+        if self._device.index != cuda.current_device():
+            self._open += (cuda.device(self._device),)
+            self._open[-1].__enter__()
         if self._stream is not None:
-            self._inner = torch.cuda.stream(self._stream)
-            self._inner.__enter__()
-        return _stream_ptr(None)
+            self._open += (cuda.stream(self._stream),)
+            self._open[-1].__enter__()
+        return cuda.current_stream().cuda_stream
 
     def __exit__(self, *exc):
-        if self._inner is not None:
-            self._inner.__exit__(*exc)
-        self._device.__exit__(*exc)
+        for c in reversed(self._open):
+            c.__exit__(*exc)
 
 
 def _bad(message):
@@ -576,6 +577,12 @@ def _token_rows(t, name, like, heads, d):
 def _contiguous():
     import torch
     return torch.contiguous_format
+
+
+@functools.lru_cache(maxsize=256)
+def _paged_workspace_bytes(device_index, dtype, path, Hq, Hkv, d, page_size, max_new):
+    """Scratch of a paged attention call: a function of these sizes alone (0: the call will be refused)."""
+    return lla_paged_parallax_workspace_size(dtype, path, 1, 1, Hq, Hkv, d, page_size, 1, max_new)
 
 
 def paged_plan(ctx_lens, new_lens, block_table, free_pages, free_count, page_size, num_rows, *, kv_lens=None, cu_q=None,
@@ -639,7 +646,8 @@ def paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, 
     block_table [S, W], cu_q [S+1], kv_lens [S]: int32 CUDA tensors (paged_plan's); max_new: the most
     tokens of one sequence in this step.  causal=False: every row sees all of its sequence's keys.
     Returns out [T, Hq, d]; rows behind the last sequence are left as they were.  Asynchronous on the
-    current (or given) stream.
+    current (or given) stream.  workspace: None (taken from torch's allocator), or a uint8 CUDA tensor of
+    lla_paged_parallax_workspace_size(...) bytes.
     """
     import torch
     P, Hkv, Z, d, page_stride = _check_caches(k_cache, v_cache)
@@ -661,8 +669,10 @@ def paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, 
             out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
         elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
             raise _bad(f"out must be a contiguous {q.dtype} tensor of shape {tuple(q.shape)} on {dev}")
-        ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(),
-                                                                workspace.numel() * workspace.element_size())
+        if workspace is None:
+            workspace = torch.empty(_paged_workspace_bytes(dev.index, dtype, int(path), Hq, Hkv, d, Z, int(max_new)),
+                                    dtype=torch.uint8, device=dev)
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         lla_paged_parallax(dtype, int(path), q.data_ptr(), probe.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                            block_table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(), out.data_ptr(), T, S, Hq, Hkv, d,
                            Z, P, W, int(max_new), qs, rs, page_stride, float(tau), 1 if causal else 0, ws_ptr, ws_bytes,

@@ -59,6 +59,9 @@ struct PagedSplit {
 bool paged_decode_fits(const PagedProblem& p);
 PagedSplit paged_decode_split(const PagedProblem& p, int sms);
 cudaError_t launch_paged_decode(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream, const char** why);
+// bf16, d in {64, 128}, any number of rows: lla_paged_tc.cu.
+PagedSplit paged_tc_split(const PagedProblem& p, int sms);
+cudaError_t launch_paged_tc(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream, const char** why);
 PagedSplit paged_simt_split(const PagedProblem& p, int sms);
 cudaError_t launch_paged_simt(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream);
 cudaError_t launch_paged_merge(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream);
