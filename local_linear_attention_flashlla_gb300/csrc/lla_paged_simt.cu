@@ -318,7 +318,7 @@ cudaError_t launch_typed(const SimtArgs& a, int d, cudaStream_t stream) {
 template <typename T, int D>
 cudaError_t merge_one(const Work& w, void* out, int Hq, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(w.ctas, (w.rows + 7) / 8);
+    cfg.gridDim = dim3(w.ctas, w.rows < 16 ? w.rows : 16);
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];

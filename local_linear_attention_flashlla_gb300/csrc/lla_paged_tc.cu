@@ -6,11 +6,12 @@
 // 512 TMEM columns, so S and T have one buffer each, and P and P' (bf16) overwrite the halves of S and T
 // that they came from.  The products are issued as
 //     S(j+1)  O2(j)  T(j+1)  O1(j+1)  S(j+2)  O2(j+1) ...
-// : the softmax of S(j+1) runs under O2(j) and T(j+1), the weighting of T(j+1) under O1(j+1) and S(j+2),
-// so each side has two products' time for its half and the tensor pipe is not waited for.
+// : the softmax of S(j+1) runs under O2(j) and T(j+1), the weighting of T(j+1) under O1(j+1) and S(j+2).
 //
-// Eight warps hold the rows, a thread half of a row's columns (the halves' maxima meet in shared
-// memory); one warp feeds K and V through TMA rings (a box per page), one issues the products.
+// Two groups of four warps hold the rows, a thread a row, and take the blocks in turn, so that one
+// group's weighting runs beside the other's softmax: a row's maximum needs no exchange, and each
+// scheduler has a warp that waits for exponentials and one that does not need them.  Two more warps
+// feed K and V through TMA rings (a box per page) and issue the products.
 #include <math.h>
 
 #include "../../include/lla.h"
@@ -50,12 +51,12 @@ template <int D>
 struct TcBars {
     uint64_t kfull[TcShape<D>::kStages], kempty[TcShape<D>::kStages];
     uint64_t vfull[TcShape<D>::kStages], vempty[TcShape<D>::kStages];
-    uint64_t qfull, sfull, tfull, p1, p2, done, fin;
+    uint64_t sfull[2], tfull[2], p1[2], p2[2];  // by block parity
+    uint64_t qfull, done, fin;
     uint32_t tmem;
     int err;
-    float mx[2][2][kRows];                     // block parity, column half: row maxima
-    float2 ex[2][kRows];                       // column half: first block's sums of p and p t
-    float2 tot[2][kRows];                      // column half: omega and A of a tile
+    float m[kRows], s0[kRows];                 // the groups' common reference point and centre of a row
+    float2 tot[2][kRows];                      // group: omega and A of a tile
 };
 
 __device__ __forceinline__ uint32_t piece_off(int r, int c) {
@@ -132,7 +133,10 @@ __device__ __forceinline__ void gemm_ts(uint32_t d, uint32_t p, uint32_t v_addr,
         umma_ts_c<true>(d, p + (ks >> 2) * 64 + (ks & 3) * 8, b0 + (uint64_t)((ks * 2048) >> 4), ID);
 }
 
-// The issuing thread.
+// The issuing warp.  All lanes run the loop and one elected lane issues: with everything that the products'
+// descriptors are made of uniform across the warp the descriptors stay in uniform registers, which
+// tcgen05.mma takes (issued from a branch of lane 0 each product's eight instructions took 570 to 830
+// cycles to issue, more than the 512 it takes to run).
 template <int D>
 __device__ void issue(const Work& w, Walk wk, uint32_t tm, uint32_t qa, uint32_t ra, uint32_t kring, uint32_t vring,
                       TcBars<D>& b) {
@@ -142,44 +146,56 @@ __device__ void issue(const Work& w, Walk wk, uint32_t tm, uint32_t qa, uint32_t
     bool ok = true;
     Piece p;
     while (ok && next_piece(w, wk, p)) {
-        const int nb = p.j1 - p.j0;
+        const int nb = __shfl_sync(0xffffffffu, p.j1 - p.j0, 0);
         if (nb == 0) continue;
-        ok = mbar_wait(&b.qfull, pieces & 1, &b.err) && mbar_wait(&b.kfull[n % NS], (n / NS) & 1, &b.err);
+        ok = __all_sync(0xffffffffu, mbar_wait(&b.qfull, pieces & 1, &b.err) &&
+                                         mbar_wait(&b.kfull[n % NS], (n / NS) & 1, &b.err));
         if (!ok) break;
         tc_fence_after();
-        gemm_ss<D>(tS, qa, kring + (n % NS) * kTile);
-        umma_commit(&b.sfull);
-        gemm_ss<D>(tT, ra, kring + (n % NS) * kTile);
-        umma_commit(&b.tfull);
-        umma_commit(&b.kempty[n % NS]);
+        if (elect_one()) {
+            gemm_ss<D>(tS, qa, kring + (n % NS) * kTile);
+            umma_commit(&b.sfull[n & 1]);
+            gemm_ss<D>(tT, ra, kring + (n % NS) * kTile);
+            umma_commit(&b.tfull[n & 1]);
+            umma_commit(&b.kempty[n % NS]);
+        }
+        __syncwarp();
         for (int j = 0; j < nb; ++j, ++n) {
             const int st = n % NS, sk = (n + 1) % NS;
-            ok = mbar_wait(&b.vfull[st], (n / NS) & 1, &b.err) && mbar_wait(&b.p1, n & 1, &b.err);
+            const bool more = j + 1 < nb;
+            ok = __all_sync(0xffffffffu, mbar_wait(&b.vfull[st], (n / NS) & 1, &b.err) &&
+                                             (!more || mbar_wait(&b.kfull[sk], ((n + 1) / NS) & 1, &b.err)) &&
+                                             mbar_wait(&b.p1[n & 1], (n >> 1) & 1, &b.err));
             if (!ok) break;
             tc_fence_after();
-            gemm_ts<D>(tO1, tS, vring + st * kTile, j > 0);
-            if (j + 1 < nb) {
-                ok = mbar_wait(&b.kfull[sk], ((n + 1) / NS) & 1, &b.err);
-                if (!ok) break;
-                gemm_ss<D>(tS, qa, kring + sk * kTile);
-                umma_commit(&b.sfull);
+            if (elect_one()) {
+                gemm_ts<D>(tO1, tS, vring + st * kTile, j > 0);
+                if (more) {
+                    gemm_ss<D>(tS, qa, kring + sk * kTile);
+                    umma_commit(&b.sfull[(n + 1) & 1]);
+                }
             }
-            ok = mbar_wait(&b.p2, n & 1, &b.err);
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, mbar_wait(&b.p2[n & 1], (n >> 1) & 1, &b.err));
             if (!ok) break;
             tc_fence_after();
-            gemm_ts<D>(tO2, tT, vring + st * kTile, j > 0);
-            umma_commit(&b.vempty[st]);
-            if (j + 1 < nb) {
-                gemm_ss<D>(tT, ra, kring + sk * kTile);
-                umma_commit(&b.tfull);
-                umma_commit(&b.kempty[sk]);
+            if (elect_one()) {
+                gemm_ts<D>(tO2, tT, vring + st * kTile, j > 0);
+                umma_commit(&b.vempty[st]);
+                if (more) {
+                    gemm_ss<D>(tT, ra, kring + sk * kTile);
+                    umma_commit(&b.tfull[(n + 1) & 1]);
+                    umma_commit(&b.kempty[sk]);
+                } else {
+                    umma_commit(&b.done);
+                }
             }
+            __syncwarp();
         }
-        if (!ok) break;
-        umma_commit(&b.done);
         ++pieces;
     }
-    umma_commit(&b.fin);
+    __syncwarp();
+    if (elect_one()) umma_commit(&b.fin);
     drain(&b.fin, 0);                          // no product runs when TMEM is given back
 }
 
@@ -222,10 +238,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&b.vempty[i], 1);
         }
         mbar_init(&b.qfull, kSoft / 32);
-        mbar_init(&b.p1, kSoft / 32);
-        mbar_init(&b.p2, kSoft / 32);
-        mbar_init(&b.sfull, 1);
-        mbar_init(&b.tfull, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&b.p1[i], kSoft / 64);
+            mbar_init(&b.p2[i], kSoft / 64);
+            mbar_init(&b.sfull[i], 1);
+            mbar_init(&b.tfull[i], 1);
+        }
         mbar_init(&b.done, 1);
         mbar_init(&b.fin, 1);
         b.err = 0;
@@ -244,12 +262,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kSoft / 32) {
         feed_kv<D>(w, wk, &mk, &mv, kring, vring, b);
     } else if (warp == kSoft / 32 + 1) {
-        if (lane == 0) issue<D>(w, wk, tm, smem_u32(qs), smem_u32(rs), kring, vring, b);
+        issue<D>(w, wk, __shfl_sync(0xffffffffu, tm, 0), __shfl_sync(0xffffffffu, smem_u32(qs), 0),
+                 __shfl_sync(0xffffffffu, smem_u32(rs), 0), __shfl_sync(0xffffffffu, kring, 0),
+                 __shfl_sync(0xffffffffu, vring, 0), b);
     } else {
-        const int half = warp >> 2, r = (warp & 3) * 32 + lane;      // column half, row
+        const int half = warp >> 2, r = (warp & 3) * 32 + lane;      // group, row
         const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t tS = lanes + half * 64, tT = lanes + 128 + half * 64;
-        const uint32_t tO1 = lanes + 256 + half * HD, tO2 = tO1 + D;   // this half's output columns
+        const uint32_t tS = lanes, tT = lanes + 128, tO = lanes + 256;
+        const uint32_t tO1 = tO + half * HD, tO2 = tO1 + D;   // the output columns this group writes
         int n = 0, pieces = 0;
         bool shared = false;
         Piece p;
@@ -283,153 +303,214 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b.qfull);
             }
+            bool centred = false;
             for (int j = 0; j < nb; ++j, ++n) {
-                const int key0 = (p.j0 + j) * kKeys, col0 = key0 + half * 64;
+                if ((n & 1) != half) continue;
+                const int key0 = (p.j0 + j) * kKeys, ph = (n >> 1) & 1;
                 const bool masked = !__all_sync(0xffffffffu, limit >= key0 + kKeys);
-                mbar_wait(&b.sfull, n & 1, &b.err);
+                const bool tail = p.keys < key0 + kKeys;
+                // ---------------------------------------------------------------- S: the weights p
+                float mo = -INFINITY;              // the reference point before this block
+                if (j > 0) {
+                    mbar_wait(&b.p1[half ^ 1], ((n - 1) >> 1) & 1, &b.err);
+                    mo = b.m[r];
+                }
+                mbar_wait(&b.sfull[half], ph, &b.err);
                 tc_fence_after();
-                float s[64];
-                {
-                    float (&lo)[32] = *reinterpret_cast<float (*)[32]>(&s[0]);
-                    float (&hi)[32] = *reinterpret_cast<float (*)[32]>(&s[32]);
-                    tmem_ld32(tS, lo);
-                    tmem_ld32(tS + 32, hi);
-                    tmem_ld_wait();
-                }
-                if (masked) {
+                float mn = mo;
+                if (j == 0 || masked) {            // the maximum first; keys that the row does not see out of the way
+                    float bm = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < kKeys; c += 32) {
+                        float x[32];
+                        tmem_ld32(tS + c, x);
+                        tmem_ld_wait();
+                        const int in = limit - key0 - c;
 #pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (col0 + i >= limit) s[i] = -INFINITY;
-                }
-                float bm0 = s[0], bm1 = s[1];
+                        for (int i = 0; i < 32; ++i) {
+                            if (i >= in) x[i] = -INFINITY;
+                            bm = fmaxf(bm, x[i]);
+                        }
+                        if (masked) {
+                            uint32_t y[16], z[16];
 #pragma unroll
-                for (int i = 2; i < 64; i += 2) {
-                    bm0 = fmaxf(bm0, s[i]);
-                    bm1 = fmaxf(bm1, s[i + 1]);
-                }
-                b.mx[n & 1][half][r] = fmaxf(bm0, bm1);
-                named_bar_sync(1, kSoft);
-                const float bm = a.scale * fmaxf(b.mx[n & 1][0][r], b.mx[n & 1][1][r]);
-                // the exponents' reference follows the maximum only when that has grown by more than 8 (weights
-                // to 2^8): most blocks rescale nothing.  Both halves of a row decide alike.
-                float f = 1.f;
-                const bool grow = __any_sync(0xffffffffu, bm > m + 8.f);
-                if (grow) {
-                    const float mn = fmaxf(m, bm);
-                    f = mn == -INFINITY ? 1.f : ex2(m - mn);
-                    m = mn;
-                    om *= f;
-                    A *= f;
-                    if (j > 0) {               // O1 of the blocks before (complete: S of this one came after it)
-#pragma unroll
-                        for (int c = 0; c < HD; c += 32) scale32(tO1 + c, f);
+                            for (int i = 0; i < 16; ++i) {
+                                y[i] = __float_as_uint(x[i]);
+                                z[i] = __float_as_uint(x[16 + i]);
+                            }
+                            tmem_st16(tS + c, y);
+                            tmem_st16(tS + c + 16, z);
+                        }
                     }
+                    tmem_st_wait();
+                    bm *= a.scale;
+                    if (__any_sync(0xffffffffu, bm > mo + 8.f)) mn = fmaxf(mo, bm);
                 }
-                if (p.keys < key0 + kKeys) {
+                if (tail) {
                     // value rows behind the last key hold a page's rest or an earlier block; a zero weight does
                     // not remove a NaN, so they are cleared before the products read them
                     const int st = n % NS;
                     mbar_wait(&b.vfull[st], (n / NS) & 1, &b.err);
-                    for (int e = tid; e < kKeys * (D / 8); e += kSoft) {
+                    for (int e = tid & 127; e < kKeys * (D / 8); e += 128) {
                         const int rr = e / (D / 8), c = e % (D / 8);
                         if (key0 + rr >= p.keys)
                             *reinterpret_cast<uint4*>(vs + (size_t)st * kTile + piece_off(rr, c)) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                 }
-                const float mb = m == -INFINITY ? 0.f : m;
-                const uint64_t sc2 = f2_pack(a.scale, a.scale), nm2 = f2_pack(-mb, -mb);
-                uint64_t sum2 = f2_pack(0.f, 0.f);
-                uint32_t pk[32];
+                uint32_t pk[64];
+                float ps;
+                // One pass with the reference point of the blocks before: it follows the maximum only when that
+                // has grown by more than 8 (weights to 2^8), and then the pass is repeated (S is still there).
+                for (;;) {
+                    const float mb = mn == -INFINITY ? 0.f : mn;
+                    const uint64_t sc2 = f2_pack(a.scale, a.scale), nm2 = f2_pack(-mb, -mb);
+                    uint64_t sum2 = f2_pack(0.f, 0.f);
+                    float b0 = -INFINITY, b1 = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    float x, y;
-                    f2_unpack(f2_fma(f2_pack(s[2 * i], s[2 * i + 1]), sc2, nm2), x, y);
-                    x = ex2(x);
-                    y = ex2(y);
-                    s[2 * i] = x;
-                    s[2 * i + 1] = y;
-                    sum2 = f2_add(sum2, f2_pack(x, y));
-                    // the value product takes the weights in bf16 (half a step is 2^-8 of each); its sums are fp32
-                    pk[i] = pack_bf16(x, y);
+                    for (int c = 0; c < kKeys; c += 32) {
+                        float x[32];
+                        tmem_ld32(tS + c, x);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            b0 = fmaxf(b0, x[2 * i]);
+                            b1 = fmaxf(b1, x[2 * i + 1]);
+                            float u, v;
+                            f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), sc2, nm2), u, v);
+                            u = ex2(u);
+                            v = ex2(v);
+                            sum2 = f2_add(sum2, f2_pack(u, v));
+                            // the value products take the weights in bf16 (half a step is 2^-8 of each), the same
+                            // rounded weight in both; their sums and the normaliser are fp32
+                            pk[c / 2 + i] = pack_bf16(u, v);
+                        }
+                    }
+                    float u;
+                    f2_unpack(sum2, ps, u);
+                    ps += u;
+                    const float bm = a.scale * fmaxf(b0, b1);
+                    if (!__any_sync(0xffffffffu, bm > mn + 8.f)) break;
+                    mn = fmaxf(mn, bm);
                 }
+                float f = 1.f;                     // from the reference before to this block's
+                const bool grow = __any_sync(0xffffffffu, mn > mo);
+                if (grow) {
+                    f = mn == -INFINITY ? 1.f : ex2(mo - mn);
+                    if (j > 0) {                   // O1 of the blocks before (complete: S of this one came after it)
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) scale32(tO + c, f);
+                    }
+                }
+                if (grow || j == 0) b.m[r] = mn;
                 tmem_st16(tS, *reinterpret_cast<uint32_t (*)[16]>(&pk[0]));
                 tmem_st16(tS + 16, *reinterpret_cast<uint32_t (*)[16]>(&pk[16]));
+                tmem_st16(tS + 64, *reinterpret_cast<uint32_t (*)[16]>(&pk[32]));
+                tmem_st16(tS + 80, *reinterpret_cast<uint32_t (*)[16]>(&pk[48]));
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&b.p1);
-                float ps, ps1;
-                f2_unpack(sum2, ps, ps1);
-                ps += ps1;
-                om += ps;
+                if (lane == 0) mbar_arrive(&b.p1[half]);
+                // this group's sums to the new reference (m: the reference of its last block)
+                const float fs = mn == -INFINITY || m == -INFINITY ? 1.f : ex2(m - mn);
+                om = om * fs + ps;
+                A *= fs;
+                m = mn;
 
-                mbar_wait(&b.tfull, n & 1, &b.err);
+                // ------------------------------------------------------------- T: the weights p (t - s0)
+                if (j > 0 && !centred) {
+                    mbar_wait(&b.p2[half ^ 1], ((n - 1) >> 1) & 1, &b.err);
+                    s0 = b.s0[r];
+                }
+                mbar_wait(&b.tfull[half], ph, &b.err);
                 tc_fence_after();
-                if (j == 0) {                  // centre: the softmax mean of t over the first block
-                    float pt = 0.f;
+                if (j == 0) {                  // centre: the softmax mean of t over the first keys
+                    float x = 0.f, y = 0.f, t[32];
+                    tmem_ld32(tT, t);
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int c = 0; c < 64; c += 32) {
-                        float t[32];
-                        tmem_ld32(tT + c, t);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!masked || col0 + c + i < limit) pt = fmaf(s[c + i], t[i], pt);
+                    for (int i = 0; i < 32; ++i) {
+                        const float q = __uint_as_float(i & 1 ? pk[i / 2] & 0xffff0000u : pk[i / 2] << 16);
+                        if (key0 + i < limit) {
+                            x += q;
+                            y = fmaf(q, t[i], y);
+                        }
                     }
-                    b.ex[half][r] = make_float2(ps, pt);
-                    named_bar_sync(1, kSoft);
-                    const float2 e0 = b.ex[0][r], e1 = b.ex[1][r];
-                    s0 = e0.x + e1.x > 0.f ? (e0.y + e1.y) / (e0.x + e1.x) : 0.f;
+                    s0 = x > 0.f ? y / x : t[0];
+                    b.s0[r] = s0;
                 } else if (grow) {             // O2 of the blocks before (complete: T of this one came after it)
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) scale32(tO + D + c, f);
+                }
+                centred = true;
+                if (tail) {                    // t of keys behind the last may be anything, a NaN too
+#pragma unroll 1
+                    for (int c = 0; c < kKeys; c += 32) {
+                        float x[32];
+                        tmem_ld32(tT + c, x);
+                        tmem_ld_wait();
+                        const int in = p.keys - key0 - c;
+                        uint32_t y[16], z[16];
 #pragma unroll
-                    for (int c = 0; c < HD; c += 32) scale32(tO2 + c, f);
+                        for (int i = 0; i < 16; ++i) {
+                            y[i] = __float_as_uint(i < in ? x[i] : s0);
+                            z[i] = __float_as_uint(16 + i < in ? x[16 + i] : s0);
+                        }
+                        tmem_st16(tT + c, y);
+                        tmem_st16(tT + c + 16, z);
+                    }
+                    tmem_st_wait();
                 }
                 const uint64_t ns2 = f2_pack(-s0, -s0);
-                sum2 = f2_pack(0.f, 0.f);
+                uint64_t sum2 = f2_pack(0.f, 0.f);
 #pragma unroll
-                for (int c = 0; c < 64; c += 32) {
+                for (int c = 0; c < kKeys; c += 32) {
                     float t[32];
                     tmem_ld32(tT + c, t);
                     tmem_ld_wait();
-                    if (masked) {              // behind the limit t may be anything, a NaN too
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (col0 + c + i >= limit) t[i] = s0;
-                    }
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        const uint64_t x2 = f2_mul(f2_pack(s[c + 2 * i], s[c + 2 * i + 1]),
+                        const uint32_t q = pk[c / 2 + i];
+                        const uint64_t x2 = f2_mul(f2_pack(__uint_as_float(q << 16), __uint_as_float(q & 0xffff0000u)),
                                                    f2_add(f2_pack(t[2 * i], t[2 * i + 1]), ns2));
                         sum2 = f2_add(sum2, x2);
-                        float x, y;
-                        f2_unpack(x2, x, y);
-                        pk[i] = pack_bf16(x, y);
-                    }
-                    if (c == 0) {              // into the first half's columns once both halves are read
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) pk[16 + i] = pk[i];
+                        float u, v;
+                        f2_unpack(x2, u, v);
+                        pk[c / 2 + i] = pack_bf16(u, v);
                     }
                 }
-                tmem_st16(tT, *reinterpret_cast<uint32_t (*)[16]>(&pk[16]));
-                tmem_st16(tT + 16, *reinterpret_cast<uint32_t (*)[16]>(&pk[0]));
+                tmem_st16(tT, *reinterpret_cast<uint32_t (*)[16]>(&pk[0]));
+                tmem_st16(tT + 16, *reinterpret_cast<uint32_t (*)[16]>(&pk[16]));
+                tmem_st16(tT + 64, *reinterpret_cast<uint32_t (*)[16]>(&pk[32]));
+                tmem_st16(tT + 80, *reinterpret_cast<uint32_t (*)[16]>(&pk[48]));
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&b.p2);
+                if (lane == 0) mbar_arrive(&b.p2[half]);
                 float x, y;
                 f2_unpack(sum2, x, y);
                 A += x + y;
             }
 
             if (nb > 0) {
+                mbar_wait(&b.done, pieces & 1, &b.err);
+                tc_fence_after();
+                ++pieces;
+                // the last reference and the centre: written before the arrivals that `done` came after
+                const int last = (n - 1) & 1;
+                if (last != half) {
+                    mbar_wait(&b.p1[last], ((n - 1) >> 1) & 1, &b.err);
+                    mbar_wait(&b.p2[last], ((n - 1) >> 1) & 1, &b.err);
+                    const float mn = b.m[r], fs = m == -INFINITY ? 0.f : ex2(m - mn);
+                    om *= fs;
+                    A *= fs;
+                    m = mn;
+                    s0 = b.s0[r];
+                }
                 b.tot[half][r] = make_float2(om, A);
                 named_bar_sync(1, kSoft);
                 om = b.tot[0][r].x + b.tot[1][r].x;
                 A = b.tot[0][r].y + b.tot[1][r].y;
-                mbar_wait(&b.done, pieces & 1, &b.err);
-                tc_fence_after();
-                ++pieces;
             }
             const float inv = om != 0.f ? 1.f / om : 0.f, c1 = (1.f + A * inv) * inv;
 #pragma unroll
