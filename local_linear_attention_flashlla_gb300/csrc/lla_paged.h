@@ -76,6 +76,8 @@ struct Work {
     const int* kv_lens;
     int T, S, Hkv, G, width, page_shift, num_pages, max_new, causal;
     int rows, keys, ctas, min_units;
+    int keys_shift, both_shift;       // log2 of keys and of min(rows, keys)
+    unsigned g_mul, g_shift;          // division by G (over_g)
     PartHeader* hdr;
     float* part;
     unsigned* err;
@@ -87,10 +89,26 @@ inline Work make_work(const PagedProblem& p, const PagedSplit& sp) {
     w.T = p.T; w.S = p.S; w.Hkv = p.Hkv; w.G = p.G; w.width = p.width; w.page_shift = p.page_shift;
     w.num_pages = p.num_pages; w.max_new = p.max_new; w.causal = p.causal;
     w.rows = sp.rows; w.keys = sp.keys; w.ctas = sp.ctas; w.min_units = sp.min_units;
+    auto log2i = [](int x) { int s = 0; while ((1 << s) < x) ++s; return s; };
+    w.keys_shift = log2i(sp.keys);
+    w.both_shift = log2i(sp.rows < sp.keys ? sp.rows : sp.keys);
+    w.g_shift = (unsigned)log2i(p.G);
+    w.g_mul = (unsigned)((((1ull << 32) * ((1ull << w.g_shift) - (unsigned)p.G)) / (unsigned)p.G) + 1);
     w.hdr = static_cast<PartHeader*>(p.ws);
     w.part = reinterpret_cast<float*>(static_cast<char*>(p.ws) + (size_t)kPagedMaxCtas * sizeof(PartHeader));
     w.err = p.err;
     return w;
+}
+
+// x / G for 0 <= x < 2^31, by multiplication with the rounded-up reciprocal.
+__device__ __forceinline__ int over_g(const Work& w, int x) {
+    return (int)((__umulhi(w.g_mul, (unsigned)x) + (unsigned)x) >> w.g_shift);
+}
+
+// a / b for 0 <= a, 0 < b; a 32-bit division where both fit (they nearly always do).
+__device__ __forceinline__ long long div_units(long long a, long long b) {
+    if (((unsigned long long)(a | b) >> 32) == 0) return (unsigned)a / (unsigned)b;
+    return a / b;
 }
 
 // A sequence as the kernels see it: lengths outside what the tensors hold are cut to it and reported
@@ -110,28 +128,19 @@ __device__ __forceinline__ Seq load_seq(const Work& w, int s) {
     return q;
 }
 
-// sum_{i < n} floor((a i + b) / m), by the Euclid-like exchange of slope and modulus.
-__device__ inline unsigned long long floor_sum(unsigned long long n, unsigned long long m, unsigned long long a,
-                                               unsigned long long b) {
-    unsigned long long ans = 0;
-    while (n > 0) {
-        if (a >= m) {
-            ans += (n - 1) * n / 2 * (a / m);
-            a %= m;
-        }
-        if (b >= m) {
-            ans += n * (b / m);
-            b %= m;
-        }
-        const unsigned long long y = a * n + b;
-        if (y < m) break;
-        n = y / m;
-        b = y % m;
-        const unsigned long long t = m;
-        m = a;
-        a = t;
-    }
-    return ans;
+// sum_{x < X} floor(x / m) = m q (q - 1) / 2 + q r, X = q m + r.
+__device__ inline long long quotient_sum(unsigned X, unsigned m) {
+    const unsigned q = X / m, r = X - q * m;
+    return (long long)((unsigned long long)q * (q - 1) / 2 * m + (unsigned long long)q * r);
+}
+// sum_{i < n} floor((a i + b) / m), a 1 or 2: the difference of two quotient sums; for a = 2 with
+// floor((2 i + b) / (2 m)) = floor((i + floor(b / 2)) / m) and, for odd m, floor(x / m) = floor(x / (2 m)) +
+// floor((x + m) / (2 m)).
+__device__ inline long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
+    if (a == 1) return quotient_sum(b + n, m) - quotient_sum(b, m);
+    if ((m & 1) == 0) return quotient_sum((b >> 1) + n, m >> 1) - quotient_sum(b >> 1, m >> 1);
+    const unsigned c = b + m;
+    return quotient_sum((b >> 1) + n, m) - quotient_sum(b >> 1, m) + quotient_sum((c >> 1) + n, m) - quotient_sum(c >> 1, m);
 }
 
 __device__ __forceinline__ int tiles_of(const Work& w, const Seq& q) { return (q.nq * w.G + w.rows - 1) / w.rows; }
@@ -139,16 +148,16 @@ __device__ __forceinline__ int tiles_of(const Work& w, const Seq& q) { return (q
 // Keys that the rows of tile i see, at most (the last row's); 0 if none.
 __device__ __forceinline__ int tile_keys(const Work& w, const Seq& q, int i) {
     if (!w.causal) return q.L;
-    const int last = (min((i + 1) * w.rows, q.nq * w.G) - 1) / w.G;
+    const int last = over_g(w, min((i + 1) * w.rows, q.nq * w.G) - 1);
     return min(max(q.L - q.nq + last + 1, 0), q.L);
 }
 
 // Units charged for tile i (>= 1: a tile without keys still has its rows to write).  A causal sequence
 // with fewer keys than tokens is charged as if it had as many.
 __device__ __forceinline__ int tile_units(const Work& w, const Seq& q, int i) {
-    if (!w.causal) return max(1, (q.L + w.keys - 1) / w.keys);
-    const int last = (min((i + 1) * w.rows, q.nq * w.G) - 1) / w.G;
-    return (max(q.L - q.nq, 0) + last) / w.keys + 1;
+    if (!w.causal) return max(1, (q.L + w.keys - 1) >> w.keys_shift);
+    const int last = over_g(w, min((i + 1) * w.rows, q.nq * w.G) - 1);
+    return ((max(q.L - q.nq, 0) + last) >> w.keys_shift) + 1;
 }
 
 // Units of the first n tiles of one key head (n <= tiles).
@@ -163,8 +172,10 @@ __device__ inline long long units_before(const Work& w, const Seq& q, int n) {
         --full;
     }
     if (full > 0) {
-        const unsigned long long c0 = (unsigned long long)max(q.L - q.nq, 0);
-        u += full + (long long)floor_sum(full, (unsigned long long)w.keys * w.G, w.rows, c0 * w.G + w.rows - 1);
+        // tile i: floor((c0 G + rows (i + 1) - 1) / (keys G)) + 1 units; rows and keys are powers of two, so
+        // their common factor leaves the quotient as it is
+        const unsigned c0 = (unsigned)max(q.L - q.nq, 0) * w.G + w.rows - 1;
+        u += full + floor_sum(full, (w.keys >> w.both_shift) * w.G, w.rows >> w.both_shift, c0 >> w.both_shift);
     }
     return u;
 }
@@ -175,6 +186,7 @@ __device__ __forceinline__ long long seq_units(const Work& w, const Seq& q) {
 
 // A position in the order of units.
 struct Walk {
+    int cta;              // whose range it is (a CTA, or a pair of them)
     long long u, end;     // next unit of this CTA, end of its range
     long long total;
     int active;           // CTAs that have work
@@ -193,22 +205,23 @@ __device__ __forceinline__ long long block_sum(long long v, long long* red) {
     return t;
 }
 
-// Range of this CTA (blockIdx.x) and the tile it begins in.  Every thread of the block calls it; the
+// Range of CTA `cta` and the tile it begins in.  Every thread of the block calls it; the
 // shared scratch is 40 long longs.  active = 0: no units at all.  blockDim.x is a multiple of 32.
-__device__ inline Walk begin_walk(const Work& w, long long* sh) {
+__device__ inline Walk begin_walk(const Work& w, int cta, long long* sh) {
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
     long long mine = 0;
     for (int s = tid; s < w.S; s += nt) mine += seq_units(w, load_seq(w, s));
     Walk k;
+    k.cta = cta;
     k.total = block_sum(mine, sh);
     k.s = k.h = k.i = k.j = 0;
     k.q.token0 = k.q.nq = k.q.L = 0;
     k.u = k.end = 0;
-    const long long most = (k.total + w.min_units - 1) / w.min_units;
+    const long long most = div_units(k.total + w.min_units - 1, w.min_units);
     k.active = (int)(most < w.ctas ? most : w.ctas);
-    if ((int)blockIdx.x >= k.active) return k;
-    k.u = k.total * blockIdx.x / k.active;
-    k.end = k.total * (blockIdx.x + 1) / k.active;
+    if (cta >= k.active) return k;
+    k.u = div_units(k.total * cta, k.active);
+    k.end = div_units(k.total * (cta + 1), k.active);
     long long before = 0;
     int* at = reinterpret_cast<int*>(sh + 36);
     for (int s0 = 0; s0 < w.S; s0 += nt) {
@@ -242,13 +255,14 @@ __device__ inline Walk begin_walk(const Work& w, long long* sh) {
             const int tiles = tiles_of(w, k.q);
             long long rem = k.u - fpre;
             const long long per = units_before(w, k.q, tiles);
-            k.h = (int)(rem / per);
+            k.h = (int)div_units(rem, per);
             rem -= k.h * per;
-            int lo = 0, hi = tiles - 1;       // the last tile with units_before <= rem
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (units_before(w, k.q, mid) <= rem) lo = mid;
-                else hi = mid - 1;
+            int lo = 0;                       // the last tile with units_before <= rem: 32 probes at a time
+            for (int range = tiles; range > 1;) {
+                const int step = (range + 31) >> 5, at = lo + lane * step;
+                const bool yes = lane * step < range && units_before(w, k.q, at) <= rem;
+                lo += (__popc(__ballot_sync(0xffffffffu, yes)) - 1) * step;
+                range = min(step, tiles - lo);
             }
             k.i = lo;
             k.j = (int)(rem - units_before(w, k.q, lo));
@@ -279,7 +293,7 @@ __device__ __forceinline__ bool next_piece(const Work& w, Walk& k, Piece& p) {
     p.row0 = k.i * w.rows;
     p.rows = min(w.rows, k.q.nq * w.G - p.row0);
     p.keys = tile_keys(w, k.q, k.i);
-    const int nb = (p.keys + w.keys - 1) / w.keys;
+    const int nb = (p.keys + w.keys - 1) >> w.keys_shift;
     p.j0 = min(k.j, nb);
     p.j1 = min(k.j + take, nb);
     const bool first = k.j == 0, last = k.j + take == units;
@@ -287,8 +301,8 @@ __device__ __forceinline__ bool next_piece(const Work& w, Walk& k, Piece& p) {
     p.parts = 0;
     if (p.slot == 1) {
         const long long tile_end = k.u + units;      // first unit behind the tile (k.j is 0)
-        const long long c = (tile_end * k.active - 1) / k.total;
-        p.parts = (int)(c - blockIdx.x) + 1;
+        const long long c = div_units(tile_end * k.active - 1, k.total);
+        p.parts = (int)(c - k.cta) + 1;
     }
     k.u += take;
     k.j += take;
@@ -313,16 +327,22 @@ __device__ __forceinline__ bool next_piece(const Work& w, Walk& k, Piece& p) {
     return true;
 }
 
-__device__ __forceinline__ float* part_stats(const Work& w, int cta, int slot, int d) {
-    return w.part + ((size_t)cta * 2 + slot) * ((size_t)w.rows * (4 + 2 * d));
+// A slot's parts: { m, omega, A, s0 } of each row, then the sums as float4 [2][d / 4][rows] (O1, then O2):
+// the threads of a warp have a row each where it matters, and consecutive rows are consecutive in memory.
+__device__ __forceinline__ float4* part_stats(const Work& w, int cta, int slot, int d) {
+    return reinterpret_cast<float4*>(w.part) + ((size_t)cta * 2 + slot) * ((size_t)w.rows * (1 + d / 2));
 }
-__device__ __forceinline__ float* part_sums(const Work& w, int cta, int slot, int d) {
-    return part_stats(w, cta, slot, d) + (size_t)w.rows * 4;
+__device__ __forceinline__ float4* part_sums(const Work& w, int cta, int slot, int d) {
+    return part_stats(w, cta, slot, d) + w.rows;
+}
+// Element of the sums (half 0: O1, 1: O2) of a row's column.
+__device__ __forceinline__ float* part_element(float4* sums, int rows, int d, int half, int row, int col) {
+    return reinterpret_cast<float*>(sums + (size_t)(half * (d / 4) + col / 4) * rows + row) + col % 4;
 }
 
 // This CTA's header: written once by every CTA, with the tile that it starts and others finish (its
 // last piece) or none.
-__device__ __forceinline__ void write_header(const Work& w, const Piece& p, bool shared) {
+__device__ __forceinline__ void write_header(const Work& w, int cta, const Piece& p, bool shared) {
     PartHeader h;
     h.parts = shared ? p.parts : 0;
     h.row0 = p.row0;
@@ -330,7 +350,7 @@ __device__ __forceinline__ void write_header(const Work& w, const Piece& p, bool
     h.token0 = p.q.token0;
     h.head = p.h;
     h.pad[0] = h.pad[1] = h.pad[2] = 0;
-    w.hdr[blockIdx.x] = h;
+    w.hdr[cta] = h;
 }
 
 }  // namespace paged

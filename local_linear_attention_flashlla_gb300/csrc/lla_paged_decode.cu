@@ -139,7 +139,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         err = 0;
         tc::mbar_fence_init();
     }
-    Walk wk = begin_walk(w, scratch);
+    Walk wk = begin_walk(w, blockIdx.x, scratch);
+    cudaTriggerProgrammaticLaunchCompletion();   // the merge waits for this grid's end all the same
     __syncthreads();
 
     if (warp == kWarps) {
@@ -164,9 +165,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const __nv_bfloat16* gq = a.q;
                 const __nv_bfloat16* gr = a.probe;
                 if (in) {
-                    limit[mt] = w.causal ? min(max(p.q.L - p.q.nq + fr / w.G + 1, 0), p.q.L) : p.q.L;
-                    const long long token = p.q.token0 + fr / w.G;
-                    const int head = p.h * w.G + fr % w.G;
+                    limit[mt] = w.causal ? min(max(p.q.L - p.q.nq + over_g(w, fr) + 1, 0), p.q.L) : p.q.L;
+                    const long long token = p.q.token0 + over_g(w, fr);
+                    const int head = p.h * w.G + (fr - over_g(w, fr) * w.G);
                     gq += token * a.q_stride + (long long)head * D + c2;
                     gr += token * a.r_stride + (long long)head * D + c2;
                 }
@@ -380,21 +381,20 @@ __global__ void __launch_bounds__(kThreads, 2)
                         if (p.slot < 0) {
                             const int fr = p.row0 + r;
                             const float inv = ow != 0.f ? 1.f / ow : 0.f;
-                            a.out[((long long)(p.q.token0 + fr / w.G) * a.Hq + p.h * w.G + fr % w.G) * D + sl * SW + c] =
+                            a.out[((long long)(p.q.token0 + over_g(w, fr)) * a.Hq + p.h * w.G + (fr - over_g(w, fr) * w.G)) * D + sl * SW + c] =
                                 __float2bfloat16_rn(((1.f + aw * inv) * x1 - x2) * inv);
                         } else {
-                            float* ps = part_sums(w, blockIdx.x, p.slot, D) + (size_t)r * 2 * D + sl * SW + c;
-                            ps[0] = x1;
-                            ps[D] = x2;
-                            if (sl == 0 && c == 0)
-                                *reinterpret_cast<float4*>(part_stats(w, blockIdx.x, p.slot, D) + r * 4) = make_float4(mm, ow, aw, sref);
+                            float4* ps = part_sums(w, blockIdx.x, p.slot, D);
+                            *part_element(ps, R, D, 0, r, sl * SW + c) = x1;
+                            *part_element(ps, R, D, 1, r, sl * SW + c) = x2;
+                            if (sl == 0 && c == 0) part_stats(w, blockIdx.x, p.slot, D)[r] = make_float4(mm, ow, aw, sref);
                         }
                     }
                 }
                 tc::named_bar_sync(1, kWarps * 32);
             }
         }
-        if (tid == 0) write_header(w, p, shared);
+        if (tid == 0) write_header(w, blockIdx.x, p, shared);
     }
     __syncthreads();
     if (tid == 0 && err) atomicOr(w.err, (unsigned)kDevErrMbarTimeout);

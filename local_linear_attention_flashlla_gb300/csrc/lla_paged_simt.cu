@@ -76,7 +76,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
     const T* gk = static_cast<const T*>(a.k);
     const T* gv = static_cast<const T*>(a.v);
 
-    Walk wk = begin_walk(w, scratch);
+    Walk wk = begin_walk(w, blockIdx.x, scratch);
+    cudaTriggerProgrammaticLaunchCompletion();   // the merge waits for this grid's end all the same
     Piece p;
     p.parts = 0; p.row0 = p.rows = p.h = 0; p.q.token0 = 0;
     bool shared = false;
@@ -87,7 +88,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
             float* dq = Qs + r * D + c;
             float* dr = Rs + r * D + c;
             if (r < p.rows) {
-                const int fr = p.row0 + r, token = p.q.token0 + fr / w.G, head = p.h * w.G + fr % w.G;
+                const int fr = p.row0 + r, token = p.q.token0 + over_g(w, fr), head = p.h * w.G + (fr - over_g(w, fr) * w.G);
                 load16(gq + token * a.q_stride + (long long)head * D + c, dq);
                 load16(gr + token * a.r_stride + (long long)head * D + c, dr);
             } else {
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
         }
         int limit = 0;                                   // keys this row sees
         if (row < p.rows)
-            limit = w.causal ? min(max(p.q.L - p.q.nq + (p.row0 + row) / w.G + 1, 0), p.q.L) : p.q.L;
+            limit = w.causal ? min(max(p.q.L - p.q.nq + over_g(w, p.row0 + row) + 1, 0), p.q.L) : p.q.L;
         float m = -INFINITY, om = 0.f, A = 0.f, s0 = 0.f;
         float o1[CPT], o2[CPT];
 #pragma unroll
@@ -198,99 +199,119 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
 
         if (row < p.rows) {
             if (p.slot < 0) {
-                const int fr = p.row0 + row, token = p.q.token0 + fr / w.G, head = p.h * w.G + fr % w.G;
+                const int fr = p.row0 + row, token = p.q.token0 + over_g(w, fr), head = p.h * w.G + (fr - over_g(w, fr) * w.G);
                 T* o = static_cast<T*>(a.out) + ((long long)token * a.Hq + head) * D;
                 const float inv = om != 0.f ? 1.f / om : 0.f, c1 = 1.f + A * inv;
 #pragma unroll
                 for (int i = 0; i < CPT; ++i)
                     if (D % TX == 0 || tx + TX * i < D) put(o + tx + TX * i, (c1 * o1[i] - o2[i]) * inv);
             } else {
-                if (tx == 0)
-                    *reinterpret_cast<float4*>(part_stats(w, blockIdx.x, p.slot, D) + row * 4) = make_float4(m, om, A, s0);
-                float* o = part_sums(w, blockIdx.x, p.slot, D) + (size_t)row * 2 * D;
+                if (tx == 0) part_stats(w, blockIdx.x, p.slot, D)[row] = make_float4(m, om, A, s0);
+                float4* ps = part_sums(w, blockIdx.x, p.slot, D);
 #pragma unroll
                 for (int i = 0; i < CPT; ++i)
                     if (D % TX == 0 || tx + TX * i < D) {
-                        o[tx + TX * i] = o1[i];
-                        o[D + tx + TX * i] = o2[i];
+                        *part_element(ps, R, D, 0, row, tx + TX * i) = o1[i];
+                        *part_element(ps, R, D, 1, row, tx + TX * i) = o2[i];
                     }
             }
         }
         __syncthreads();
     }
-    if (tid == 0) write_header(w, p, shared);
+    if (tid == 0) write_header(w, blockIdx.x, p, shared);
 }
 
 // Joins the parts of the tile that CTA blockIdx.x starts and others finish: part 0 is its slot 1, part
 // i > 0 slot 0 of CTA blockIdx.x + i.  With the common maximum and one centre,
 //   out = sum_i f_i ((1 + A/w - (s0_i - s0)) O1_i - O2_i) / w,   f_i = 2^(m_i - m).
-// The order of the sum is that of the keys: results do not depend on which CTA was first.  With many
-// parts and few rows (a long cache and one query) several warps share a row's parts.
-template <typename T, int D>
+// The order of the sum is fixed by the parts: results do not depend on which CTA was first.  Each block
+// turns the parts' statistics into two factors per (part, row) in shared memory, after which every load of
+// the sums is independent of the others; a thread has four columns of a row, and where rows are few,
+// kLanes threads share them and take the parts in turn.  Reading the parts from L2 bounds it.
+constexpr int kFactors = 4096;                 // (part, row) factors held at a time
+
+template <typename T, int D, int R>
 __global__ void __launch_bounds__(256) paged_merge_kernel(Work w, T* __restrict__ out, int Hq) {
-    constexpr int VE = D >= 32 ? D / 32 : 1;
-    __shared__ float red[8][D];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kItems = R * D / 4 >= 1024 ? 256 : R * D / 4 >= 256 ? 64 : 32;   // (row, four columns) of a block
+    constexpr int kLanes = 256 / kItems;
+    constexpr int kPer = 256 / R;              // threads on a row's statistics
+    constexpr int kChunk = kFactors / R;       // parts at a time
+    static_assert(kPer <= 32 && kPer >= 1, "a row's threads lie in one warp");
+    __shared__ float2 fac[kFactors];
+    __shared__ float4 red[kLanes > 1 ? 256 : 1];
+    const int tid = threadIdx.x;
     cudaGridDependencySynchronize();
     const PartHeader h = w.hdr[blockIdx.x];
     if (h.parts == 0) return;
-    const int share = h.parts >= 24 ? 8 : h.parts >= 8 ? 4 : h.parts >= 4 ? 2 : 1;   // warps on a row
-    const int rpi = 8 / share, mine = warp / share, sub = warp % share;
-    for (int r0 = blockIdx.y * rpi; r0 < h.rows; r0 += gridDim.y * rpi) {
-        const int r = r0 + mine;
-        float acc[VE];
+    const int row = tid / kPer, sub = tid % kPer;
+    float m = -INFINITY, om = 0.f, A = 0.f;
+    const float s0 = part_stats(w, blockIdx.x, 1, D)[row].w;     // rows behind h.rows: never used
+    const bool live = row < h.rows;
+    if (live)
+        for (int i = sub; i < h.parts; i += kPer) m = fmaxf(m, part_stats(w, blockIdx.x + i, i == 0, D)[row].x);
 #pragma unroll
-        for (int i = 0; i < VE; ++i) acc[i] = 0.f;
+    for (int o = kPer / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float base = m == -INFINITY ? 0.f : m;
+    if (live)
+        for (int i = sub; i < h.parts; i += kPer) {
+            const float4 st = part_stats(w, blockIdx.x + i, i == 0, D)[row];
+            const float f = exp2f(st.x - base);
+            om = fmaf(f, st.y, om);
+            A = fmaf(f, fmaf(st.w - s0, st.y, st.z), A);
+        }
+#pragma unroll
+    for (int o = kPer / 2; o; o >>= 1) {
+        om += __shfl_xor_sync(0xffffffffu, om, o);
+        A += __shfl_xor_sync(0xffffffffu, A, o);
+    }
+    const float inv = om != 0.f ? 1.f / om : 0.f, c1 = 1.f + A * inv;   // om 0: no key in any part; NaN stays NaN
+
+    const int item = blockIdx.y * kItems + tid % kItems, lane = tid / kItems;
+    const int r = item % R;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < h.parts; i0 += kChunk) {
+        const int n = min(kChunk, h.parts - i0);
+        if (live)
+            for (int i = sub; i < n; i += kPer) {
+                const float4 st = part_stats(w, blockIdx.x + i0 + i, i0 + i == 0, D)[row];
+                const float f = exp2f(st.x - base) * inv;
+                fac[i * R + row] = make_float2(f * (c1 - (st.w - s0)), f);
+            }
+        __syncthreads();
         if (r < h.rows) {
-            float m = -INFINITY;
-            for (int i = lane; i < h.parts; i += 32)
-                m = fmaxf(m, part_stats(w, blockIdx.x + i, i == 0, D)[r * 4]);
-            for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-            const float base = m == -INFINITY ? 0.f : m;
-            const float s0 = part_stats(w, blockIdx.x, 1, D)[r * 4 + 3];
-            float om = 0.f, A = 0.f;
-            for (int i = lane; i < h.parts; i += 32) {
-                const float4 st = *reinterpret_cast<const float4*>(part_stats(w, blockIdx.x + i, i == 0, D) + r * 4);
-                const float f = exp2f(st.x - base);
-                om = fmaf(f, st.y, om);
-                A = fmaf(f, fmaf(st.w - s0, st.y, st.z), A);
-            }
-            for (int o = 16; o; o >>= 1) {
-                om += __shfl_xor_sync(0xffffffffu, om, o);
-                A += __shfl_xor_sync(0xffffffffu, A, o);
-            }
-            if (om != 0.f) {                             // 0: no key in any part; NaN stays NaN
-                const float inv = 1.f / om, c1 = 1.f + A * inv;
 #pragma unroll 4
-                for (int i = sub; i < h.parts; i += share) {
-                    const float4 st = *reinterpret_cast<const float4*>(part_stats(w, blockIdx.x + i, i == 0, D) + r * 4);
-                    const float f = exp2f(st.x - base) * inv, f1 = f * (c1 - (st.w - s0));
-                    const float* o = part_sums(w, blockIdx.x + i, i == 0, D) + (size_t)r * 2 * D;
-                    if (f != 0.f && (D >= 32 || lane < D)) {
-#pragma unroll
-                        for (int e = 0; e < VE; ++e)
-                            acc[e] = fmaf(f1, o[lane * VE + e], fmaf(-f, o[D + lane * VE + e], acc[e]));
-                    }
-                }
+            for (int i = lane; i < n; i += kLanes) {
+                const float2 f = fac[i * R + r];
+                const float4* o = part_sums(w, blockIdx.x + i0 + i, i0 + i == 0, D) + item;
+                const float4 x = o[0], y = o[R * D / 4];
+                acc.x = fmaf(f.x, x.x, fmaf(-f.y, y.x, acc.x));
+                acc.y = fmaf(f.x, x.y, fmaf(-f.y, y.y, acc.y));
+                acc.z = fmaf(f.x, x.z, fmaf(-f.y, y.z, acc.z));
+                acc.w = fmaf(f.x, x.w, fmaf(-f.y, y.w, acc.w));
             }
         }
-        if (share > 1) {
-            __syncthreads();
-            if (D >= 32 || lane < D)
+        __syncthreads();
+    }
+    if (kLanes > 1) {
+        red[tid] = acc;
+        __syncthreads();
+        if (lane == 0)
 #pragma unroll
-                for (int e = 0; e < VE; ++e) red[warp][lane * VE + e] = acc[e];
-            __syncthreads();
-            if (sub == 0 && (D >= 32 || lane < D))
-                for (int i = 1; i < share; ++i)
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) acc[e] += red[warp + i][lane * VE + e];
-        }
-        if (r < h.rows && sub == 0 && (D >= 32 || lane < D)) {
-            const int fr = h.row0 + r;
-            T* o = out + ((long long)(h.token0 + fr / w.G) * Hq + h.head * w.G + fr % w.G) * D + lane * VE;
-#pragma unroll
-            for (int e = 0; e < VE; ++e) put(o + e, acc[e]);
-        }
+            for (int i = 1; i < kLanes; ++i) {
+                const float4 x = red[i * kItems + tid];
+                acc.x += x.x;
+                acc.y += x.y;
+                acc.z += x.z;
+                acc.w += x.w;
+            }
+    }
+    if (lane == 0 && r < h.rows) {
+        const int fr = h.row0 + r;
+        T* o = out + ((long long)(h.token0 + over_g(w, fr)) * Hq + h.head * w.G + (fr - over_g(w, fr) * w.G)) * D + item / R * 4;
+        put(o, acc.x);
+        put(o + 1, acc.y);
+        put(o + 2, acc.z);
+        put(o + 3, acc.w);
     }
 }
 
@@ -315,10 +336,12 @@ cudaError_t launch_typed(const SimtArgs& a, int d, cudaStream_t stream) {
     }
 }
 
-template <typename T, int D>
+template <typename T, int D, int R>
 cudaError_t merge_one(const Work& w, void* out, int Hq, cudaStream_t stream) {
+    constexpr int kItems = R * D / 4 >= 1024 ? 256 : R * D / 4 >= 256 ? 64 : 32;
+    static_assert(R * D / 4 % kItems == 0, "whole blocks");
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(w.ctas, w.rows < 16 ? w.rows : 16);
+    cfg.gridDim = dim3(w.ctas, R * D / 4 / kItems);
     cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
@@ -326,16 +349,27 @@ cudaError_t merge_one(const Work& w, void* out, int Hq, cudaStream_t stream) {
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D>, w, static_cast<T*>(out), Hq);
+    return cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D, R>, w, static_cast<T*>(out), Hq);
+}
+
+template <typename T, int D>
+cudaError_t merge_rows(const Work& w, void* out, int Hq, cudaStream_t stream) {
+    switch (w.rows) {
+        case 8: return merge_one<T, D, 8>(w, out, Hq, stream);
+        case 16: return merge_one<T, D, 16>(w, out, Hq, stream);
+        case 32: return merge_one<T, D, 32>(w, out, Hq, stream);
+        case 128: return merge_one<T, D, 128>(w, out, Hq, stream);
+    }
+    return cudaErrorInvalidValue;
 }
 
 template <typename T>
 cudaError_t merge_typed(const Work& w, void* out, int Hq, int d, cudaStream_t stream) {
     switch (d) {
-        case 16: return merge_one<T, 16>(w, out, Hq, stream);
-        case 32: return merge_one<T, 32>(w, out, Hq, stream);
-        case 64: return merge_one<T, 64>(w, out, Hq, stream);
-        default: return merge_one<T, 128>(w, out, Hq, stream);
+        case 16: return merge_rows<T, 16>(w, out, Hq, stream);
+        case 32: return merge_rows<T, 32>(w, out, Hq, stream);
+        case 64: return merge_rows<T, 64>(w, out, Hq, stream);
+        default: return merge_rows<T, 128>(w, out, Hq, stream);
     }
 }
 

@@ -8,10 +8,11 @@
 //     S(j+1)  O2(j)  T(j+1)  O1(j+1)  S(j+2)  O2(j+1) ...
 // : the softmax of S(j+1) runs under O2(j) and T(j+1), the weighting of T(j+1) under O1(j+1) and S(j+2).
 //
-// Two groups of four warps hold the rows, a thread a row, and take the blocks in turn, so that one
-// group's weighting runs beside the other's softmax: a row's maximum needs no exchange, and each
-// scheduler has a warp that waits for exponentials and one that does not need them.  Two more warps
-// feed K and V through TMA rings (a box per page) and issue the products.
+// Eight warps hold the rows, a thread half of a row's columns.  The exponents are taken against the
+// reference point of the blocks before while the maximum is taken beside them, and only the vote of a
+// row's two warps on whether it grew stands between: the softmax of a block is one pass.  One warp feeds K
+// and V through TMA rings (a box per page), one issues the products.  The next tile's queries are loaded
+// while the last block of a tile is weighted, and its first products run under the epilogue.
 #include <math.h>
 
 #include "../../include/lla.h"
@@ -51,12 +52,11 @@ template <int D>
 struct TcBars {
     uint64_t kfull[TcShape<D>::kStages], kempty[TcShape<D>::kStages];
     uint64_t vfull[TcShape<D>::kStages], vempty[TcShape<D>::kStages];
-    uint64_t sfull[2], tfull[2], p1[2], p2[2];  // by block parity
-    uint64_t qfull, done, fin;
+    uint64_t qfull, sfull, tfull, p1, p2, done, fin;
     uint32_t tmem;
     int err;
-    float m[kRows], s0[kRows];                 // the groups' common reference point and centre of a row
-    float2 tot[2][kRows];                      // group: omega and A of a tile
+    float mx[2][kRows], s0[kRows];             // by column half: row maxima; centres
+    float2 tot[2][kRows];                      // by column half: omega and A of a tile
 };
 
 __device__ __forceinline__ uint32_t piece_off(int r, int c) {
@@ -154,9 +154,9 @@ __device__ void issue(const Work& w, Walk wk, uint32_t tm, uint32_t qa, uint32_t
         tc_fence_after();
         if (elect_one()) {
             gemm_ss<D>(tS, qa, kring + (n % NS) * kTile);
-            umma_commit(&b.sfull[n & 1]);
+            umma_commit(&b.sfull);
             gemm_ss<D>(tT, ra, kring + (n % NS) * kTile);
-            umma_commit(&b.tfull[n & 1]);
+            umma_commit(&b.tfull);
             umma_commit(&b.kempty[n % NS]);
         }
         __syncwarp();
@@ -165,18 +165,18 @@ __device__ void issue(const Work& w, Walk wk, uint32_t tm, uint32_t qa, uint32_t
             const bool more = j + 1 < nb;
             ok = __all_sync(0xffffffffu, mbar_wait(&b.vfull[st], (n / NS) & 1, &b.err) &&
                                              (!more || mbar_wait(&b.kfull[sk], ((n + 1) / NS) & 1, &b.err)) &&
-                                             mbar_wait(&b.p1[n & 1], (n >> 1) & 1, &b.err));
+                                             mbar_wait(&b.p1, n & 1, &b.err));
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
                 gemm_ts<D>(tO1, tS, vring + st * kTile, j > 0);
                 if (more) {
                     gemm_ss<D>(tS, qa, kring + sk * kTile);
-                    umma_commit(&b.sfull[(n + 1) & 1]);
+                    umma_commit(&b.sfull);
                 }
             }
             __syncwarp();
-            ok = __all_sync(0xffffffffu, mbar_wait(&b.p2[n & 1], (n >> 1) & 1, &b.err));
+            ok = __all_sync(0xffffffffu, mbar_wait(&b.p2, n & 1, &b.err));
             if (!ok) break;
             tc_fence_after();
             if (elect_one()) {
@@ -184,7 +184,7 @@ __device__ void issue(const Work& w, Walk wk, uint32_t tm, uint32_t qa, uint32_t
                 umma_commit(&b.vempty[st]);
                 if (more) {
                     gemm_ss<D>(tT, ra, kring + sk * kTile);
-                    umma_commit(&b.tfull[(n + 1) & 1]);
+                    umma_commit(&b.tfull);
                     umma_commit(&b.kempty[sk]);
                 } else {
                     umma_commit(&b.done);
@@ -197,6 +197,11 @@ __device__ void issue(const Work& w, Walk wk, uint32_t tm, uint32_t qa, uint32_t
     __syncwarp();
     if (elect_one()) umma_commit(&b.fin);
     drain(&b.fin, 0);                          // no product runs when TMEM is given back
+}
+
+// 16 bytes to shared memory without a register stop; zeros where `in` is false (src is then not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 
 // 32 columns of this thread's row x f.
@@ -214,6 +219,66 @@ __device__ __forceinline__ void scale32(uint32_t t, float f) {
     tmem_st16(t + 16, z);
 }
 
+// 64 columns of this thread's row.
+__device__ __forceinline__ void load64(uint32_t t, float (&x)[64]) {
+    tmem_ld32(t, *reinterpret_cast<float (*)[32]>(&x[0]));
+    tmem_ld32(t + 32, *reinterpret_cast<float (*)[32]>(&x[32]));
+    tmem_ld_wait();
+}
+__device__ __forceinline__ void store32(uint32_t t, const uint32_t (&x)[32]) {
+    tmem_st16(t, *reinterpret_cast<const uint32_t (*)[16]>(&x[0]));
+    tmem_st16(t + 16, *reinterpret_cast<const uint32_t (*)[16]>(&x[16]));
+    tmem_st_wait();
+}
+
+// Or of x over the two warps of a row set (64 threads).
+__device__ __forceinline__ bool pair_or(int id, bool x) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 64, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"(id), "r"((uint32_t)x) : "memory");
+    return r != 0;
+}
+
+// x <- 2^(scale x - ref) as bf16 pairs; their fp32 sum, and the maximum of x.
+__device__ __forceinline__ void weigh(const float (&x)[64], float scale, float ref, uint32_t (&pk)[32], float& sum, float& top) {
+    const uint64_t sc2 = f2_pack(scale, scale), nr2 = f2_pack(-ref, -ref);
+    uint64_t sum2 = f2_pack(0.f, 0.f);
+    float t0 = x[0], t1 = x[1];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        t0 = fmaxf(t0, x[2 * i]);
+        t1 = fmaxf(t1, x[2 * i + 1]);
+        float u, v;
+        f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), sc2, nr2), u, v);
+        u = ex2(u);
+        v = ex2(v);
+        sum2 = f2_add(sum2, f2_pack(u, v));
+        // the value products take the weights in bf16 (half a step is 2^-8 of each), the same rounded weight in
+        // both; their sums and the normaliser are fp32
+        pk[i] = pack_bf16(u, v);
+    }
+    float v;
+    f2_unpack(sum2, sum, v);
+    sum += v;
+    top = fmaxf(t0, t1);
+}
+
+// The tile's queries and probes into shared memory (not waited for); rows behind its last are zeros.
+template <int D>
+__device__ __forceinline__ void load_rows(const TcArgs& a, const Piece& p, uint32_t qa, uint32_t ra) {
+    const Work& w = a.w;
+    const int tid = threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < kRows * (D / 8) / kSoft; ++i) {
+        const int e = i * kSoft + tid, rr = e / (D / 8), c = e % (D / 8);
+        const bool in = rr < p.rows;
+        const int f = in ? p.row0 + rr : 0, tk = over_g(w, f);
+        const long long token = p.q.token0 + tk, hc = (long long)(p.h * w.G + f - tk * w.G) * D + c * 8;
+        copy16(qa + piece_off(rr, c), a.q + token * a.q_stride + hc, in);
+        copy16(ra + piece_off(rr, c), a.probe + token * a.r_stride + hc, in);
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
@@ -223,10 +288,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ long long scratch[40];
     __shared__ TcBars<D> b;
     unsigned char* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    unsigned char* qs = base;
-    unsigned char* rs = base + kTile;
+    const uint32_t qa = smem_u32(base), ra = qa + kTile;
     unsigned char* vs = base + (size_t)(2 + NS) * kTile;
-    const uint32_t kring = smem_u32(base) + 2 * kTile, vring = kring + NS * kTile;
+    const uint32_t kring = qa + 2 * kTile, vring = kring + NS * kTile;
     const Work& w = a.w;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -238,12 +302,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&b.vempty[i], 1);
         }
         mbar_init(&b.qfull, kSoft / 32);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&b.p1[i], kSoft / 64);
-            mbar_init(&b.p2[i], kSoft / 64);
-            mbar_init(&b.sfull[i], 1);
-            mbar_init(&b.tfull[i], 1);
-        }
+        mbar_init(&b.p1, kSoft / 32);
+        mbar_init(&b.p2, kSoft / 32);
+        mbar_init(&b.sfull, 1);
+        mbar_init(&b.tfull, 1);
         mbar_init(&b.done, 1);
         mbar_init(&b.fin, 1);
         b.err = 0;
@@ -253,7 +315,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&b.tmem, 512);
         tmem_relinquish();
     }
-    Walk wk = begin_walk(w, scratch);
+    Walk wk = begin_walk(w, blockIdx.x, scratch);
+    cudaTriggerProgrammaticLaunchCompletion();   // the merge waits for this grid's end all the same
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -262,256 +325,180 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kSoft / 32) {
         feed_kv<D>(w, wk, &mk, &mv, kring, vring, b);
     } else if (warp == kSoft / 32 + 1) {
-        issue<D>(w, wk, __shfl_sync(0xffffffffu, tm, 0), __shfl_sync(0xffffffffu, smem_u32(qs), 0),
-                 __shfl_sync(0xffffffffu, smem_u32(rs), 0), __shfl_sync(0xffffffffu, kring, 0),
+        issue<D>(w, wk, __shfl_sync(0xffffffffu, tm, 0), __shfl_sync(0xffffffffu, qa, 0),
+                 __shfl_sync(0xffffffffu, ra, 0), __shfl_sync(0xffffffffu, kring, 0),
                  __shfl_sync(0xffffffffu, vring, 0), b);
     } else {
-        const int half = warp >> 2, r = (warp & 3) * 32 + lane;      // group, row
+        const int half = warp >> 2, r = (warp & 3) * 32 + lane;      // column half, row
+        const int pair = 1 + (warp & 3);                             // barrier of the row's two warps
         const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t tS = lanes, tT = lanes + 128, tO = lanes + 256;
-        const uint32_t tO1 = tO + half * HD, tO2 = tO1 + D;   // the output columns this group writes
+        const uint32_t tS = lanes + half * 64, tT = lanes + 128 + half * 64;
+        const uint32_t tO1 = lanes + 256 + half * HD, tO2 = tO1 + D;   // this half's output columns
         int n = 0, pieces = 0;
-        bool shared = false;
-        Piece p;
+        bool shared = false, loaded = false;
+        Piece p, next;
         p.parts = 0; p.row0 = p.rows = p.h = 0; p.q.token0 = 0;
+        bool have = next_piece(w, wk, next);
         // after a wait that gave up, the others give up at once (they see the flag) and every barrier is still
         // passed: the CTA ends, with results that the error word disowns
-        while (next_piece(w, wk, p)) {
+        while (have) {
+            p = next;
             shared = p.slot == 1;
             const int nb = p.j1 - p.j0;
-            const int fr = p.row0 + r;
-            const long long token = p.q.token0 + fr / w.G;
-            const int head = p.h * w.G + fr % w.G;
-            float m = -INFINITY, om = 0.f, A = 0.f, s0 = 0.f;
-            // rows behind the tile's last compute on zeros and are not written
-            int limit = p.keys;
-            if (r < p.rows && w.causal) limit = min(max(p.q.L - p.q.nq + fr / w.G + 1, 0), p.q.L);
-            if (nb > 0) {
-                for (int e = tid; e < kRows * (D / 8); e += kSoft) {
-                    const int rr = e / (D / 8), c = e % (D / 8), f2 = p.row0 + rr;
-                    uint4 x = make_uint4(0, 0, 0, 0), y = x;
-                    if (rr < p.rows) {
-                        const long long tk = p.q.token0 + f2 / w.G;
-                        const long long hc = (long long)(p.h * w.G + f2 % w.G) * D + c * 8;
-                        x = *reinterpret_cast<const uint4*>(a.q + tk * a.q_stride + hc);
-                        y = *reinterpret_cast<const uint4*>(a.probe + tk * a.r_stride + hc);
-                    }
-                    *reinterpret_cast<uint4*>(qs + piece_off(rr, c)) = x;
-                    *reinterpret_cast<uint4*>(rs + piece_off(rr, c)) = y;
-                }
+            if (nb > 0 && !loaded) {
+                load_rows<D>(a, p, qa, ra);
+                asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b.qfull);
             }
-            bool centred = false;
+            loaded = false;
+            have = next_piece(w, wk, next);
+            const int fr = min(p.row0 + r, p.row0 + p.rows - 1), tk = over_g(w, fr);
+            float m = -INFINITY, om = 0.f, A = 0.f, s0 = 0.f;
+            // rows behind the tile's last compute on zeros and are not written
+            int limit = p.keys;
+            if (r < p.rows && w.causal) limit = min(max(p.q.L - p.q.nq + tk + 1, 0), p.q.L);
             for (int j = 0; j < nb; ++j, ++n) {
-                if ((n & 1) != half) continue;
-                const int key0 = (p.j0 + j) * kKeys, ph = (n >> 1) & 1;
-                const bool masked = !__all_sync(0xffffffffu, limit >= key0 + kKeys);
+                const int key0 = (p.j0 + j) * kKeys, in = limit - key0 - half * 64;   // columns of this thread it sees
+                const bool masked = !__all_sync(0xffffffffu, in >= 64);
                 const bool tail = p.keys < key0 + kKeys;
                 // ---------------------------------------------------------------- S: the weights p
-                float mo = -INFINITY;              // the reference point before this block
-                if (j > 0) {
-                    mbar_wait(&b.p1[half ^ 1], ((n - 1) >> 1) & 1, &b.err);
-                    mo = b.m[r];
-                }
-                mbar_wait(&b.sfull[half], ph, &b.err);
+                mbar_wait(&b.sfull, n & 1, &b.err);
                 tc_fence_after();
-                float mn = mo;
-                if (j == 0 || masked) {            // the maximum first; keys that the row does not see out of the way
-                    float bm = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < kKeys; c += 32) {
-                        float x[32];
-                        tmem_ld32(tS + c, x);
-                        tmem_ld_wait();
-                        const int in = limit - key0 - c;
+                uint32_t pk[32];
+                float ps, top, f = 1.f;
+                bool grow = j == 0;
+                {
+                    float x[64];
+                    load64(tS, x);
+                    if (masked) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
+                        for (int i = 0; i < 64; ++i)
                             if (i >= in) x[i] = -INFINITY;
-                            bm = fmaxf(bm, x[i]);
-                        }
-                        if (masked) {
-                            uint32_t y[16], z[16];
+                    }
+                    if (j == 0) {
+                        top = x[0];
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                y[i] = __float_as_uint(x[i]);
-                                z[i] = __float_as_uint(x[16 + i]);
+                        for (int i = 1; i < 64; ++i) top = fmaxf(top, x[i]);
+                    } else {
+                        weigh(x, a.scale, m == -INFINITY ? 0.f : m, pk, ps, top);
+                        // the reference follows the maximum only when that has grown by more than 8 (weights to 2^8)
+                        grow = pair_or(pair, top * a.scale > m + 8.f);
+                    }
+                    if (grow) {
+                        b.mx[half][r] = top;
+                        named_bar_sync(pair, 64);
+                        const float mn = fmaxf(m, a.scale * fmaxf(top, b.mx[half ^ 1][r]));
+                        f = mn == -INFINITY || j == 0 ? 1.f : ex2(m - mn);
+                        m = mn;
+                        om *= f;
+                        A *= f;
+                        if (j > 0) {           // S is still there
+                            load64(tS, x);
+                            if (masked) {
+#pragma unroll
+                                for (int i = 0; i < 64; ++i)
+                                    if (i >= in) x[i] = -INFINITY;
                             }
-                            tmem_st16(tS + c, y);
-                            tmem_st16(tS + c + 16, z);
+                        }
+                        weigh(x, a.scale, m == -INFINITY ? 0.f : m, pk, ps, top);
+                        if (j > 0) {           // O1 of the blocks before (complete: S of this one came after it)
+#pragma unroll 1
+                            for (int c = 0; c < HD; c += 32) scale32(tO1 + c, f);
                         }
                     }
-                    tmem_st_wait();
-                    bm *= a.scale;
-                    if (__any_sync(0xffffffffu, bm > mo + 8.f)) mn = fmaxf(mo, bm);
                 }
                 if (tail) {
                     // value rows behind the last key hold a page's rest or an earlier block; a zero weight does
                     // not remove a NaN, so they are cleared before the products read them
                     const int st = n % NS;
                     mbar_wait(&b.vfull[st], (n / NS) & 1, &b.err);
-                    for (int e = tid & 127; e < kKeys * (D / 8); e += 128) {
+                    for (int e = tid; e < kKeys * (D / 8); e += kSoft) {
                         const int rr = e / (D / 8), c = e % (D / 8);
                         if (key0 + rr >= p.keys)
                             *reinterpret_cast<uint4*>(vs + (size_t)st * kTile + piece_off(rr, c)) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                 }
-                uint32_t pk[64];
-                float ps;
-                // One pass with the reference point of the blocks before: it follows the maximum only when that
-                // has grown by more than 8 (weights to 2^8), and then the pass is repeated (S is still there).
-                for (;;) {
-                    const float mb = mn == -INFINITY ? 0.f : mn;
-                    const uint64_t sc2 = f2_pack(a.scale, a.scale), nm2 = f2_pack(-mb, -mb);
-                    uint64_t sum2 = f2_pack(0.f, 0.f);
-                    float b0 = -INFINITY, b1 = -INFINITY;
-#pragma unroll
-                    for (int c = 0; c < kKeys; c += 32) {
-                        float x[32];
-                        tmem_ld32(tS + c, x);
-                        tmem_ld_wait();
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            b0 = fmaxf(b0, x[2 * i]);
-                            b1 = fmaxf(b1, x[2 * i + 1]);
-                            float u, v;
-                            f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), sc2, nm2), u, v);
-                            u = ex2(u);
-                            v = ex2(v);
-                            sum2 = f2_add(sum2, f2_pack(u, v));
-                            // the value products take the weights in bf16 (half a step is 2^-8 of each), the same
-                            // rounded weight in both; their sums and the normaliser are fp32
-                            pk[c / 2 + i] = pack_bf16(u, v);
-                        }
-                    }
-                    float u;
-                    f2_unpack(sum2, ps, u);
-                    ps += u;
-                    const float bm = a.scale * fmaxf(b0, b1);
-                    if (!__any_sync(0xffffffffu, bm > mn + 8.f)) break;
-                    mn = fmaxf(mn, bm);
-                }
-                float f = 1.f;                     // from the reference before to this block's
-                const bool grow = __any_sync(0xffffffffu, mn > mo);
-                if (grow) {
-                    f = mn == -INFINITY ? 1.f : ex2(mo - mn);
-                    if (j > 0) {                   // O1 of the blocks before (complete: S of this one came after it)
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 32) scale32(tO + c, f);
-                    }
-                }
-                if (grow || j == 0) b.m[r] = mn;
-                tmem_st16(tS, *reinterpret_cast<uint32_t (*)[16]>(&pk[0]));
-                tmem_st16(tS + 16, *reinterpret_cast<uint32_t (*)[16]>(&pk[16]));
-                tmem_st16(tS + 64, *reinterpret_cast<uint32_t (*)[16]>(&pk[32]));
-                tmem_st16(tS + 80, *reinterpret_cast<uint32_t (*)[16]>(&pk[48]));
-                tmem_st_wait();
+                store32(tS, pk);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&b.p1[half]);
-                // this group's sums to the new reference (m: the reference of its last block)
-                const float fs = mn == -INFINITY || m == -INFINITY ? 1.f : ex2(m - mn);
-                om = om * fs + ps;
-                A *= fs;
-                m = mn;
+                if (lane == 0) mbar_arrive(&b.p1);
+                om += ps;
 
                 // ------------------------------------------------------------- T: the weights p (t - s0)
-                if (j > 0 && !centred) {
-                    mbar_wait(&b.p2[half ^ 1], ((n - 1) >> 1) & 1, &b.err);
+                mbar_wait(&b.tfull, n & 1, &b.err);
+                tc_fence_after();
+                if (j + 1 == nb && have && next.j1 > next.j0) {   // Q and R have been read: the next tile's
+                    load_rows<D>(a, next, qa, ra);
+                    loaded = true;
+                }
+                if (j > 0 && grow) {           // O2 of the blocks before (complete: T of this one came after it)
+#pragma unroll 1
+                    for (int c = 0; c < HD; c += 32) scale32(tO2 + c, f);
+                }
+                float t[64];
+                load64(tT, t);
+                if (j == 0) {                  // centre: the softmax mean of t over the first keys
+                    if (half == 0) {
+                        float x = 0.f, y = 0.f;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float q = __uint_as_float(i & 1 ? pk[i / 2] & 0xffff0000u : pk[i / 2] << 16);
+                            if (i < in) {
+                                x += q;
+                                y = fmaf(q, t[i], y);
+                            }
+                        }
+                        b.s0[r] = x > 0.f ? y / x : t[0];
+                    }
+                    named_bar_sync(pair, 64);
                     s0 = b.s0[r];
                 }
-                mbar_wait(&b.tfull[half], ph, &b.err);
-                tc_fence_after();
-                if (j == 0) {                  // centre: the softmax mean of t over the first keys
-                    float x = 0.f, y = 0.f, t[32];
-                    tmem_ld32(tT, t);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const float q = __uint_as_float(i & 1 ? pk[i / 2] & 0xffff0000u : pk[i / 2] << 16);
-                        if (key0 + i < limit) {
-                            x += q;
-                            y = fmaf(q, t[i], y);
-                        }
-                    }
-                    s0 = x > 0.f ? y / x : t[0];
-                    b.s0[r] = s0;
-                } else if (grow) {             // O2 of the blocks before (complete: T of this one came after it)
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) scale32(tO + D + c, f);
-                }
-                centred = true;
                 if (tail) {                    // t of keys behind the last may be anything, a NaN too
-#pragma unroll 1
-                    for (int c = 0; c < kKeys; c += 32) {
-                        float x[32];
-                        tmem_ld32(tT + c, x);
-                        tmem_ld_wait();
-                        const int in = p.keys - key0 - c;
-                        uint32_t y[16], z[16];
+                    const int left = p.keys - key0 - half * 64;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            y[i] = __float_as_uint(i < in ? x[i] : s0);
-                            z[i] = __float_as_uint(16 + i < in ? x[16 + i] : s0);
-                        }
-                        tmem_st16(tT + c, y);
-                        tmem_st16(tT + c + 16, z);
-                    }
-                    tmem_st_wait();
+                    for (int i = 0; i < 64; ++i)
+                        if (i >= left) t[i] = s0;
                 }
                 const uint64_t ns2 = f2_pack(-s0, -s0);
                 uint64_t sum2 = f2_pack(0.f, 0.f);
 #pragma unroll
-                for (int c = 0; c < kKeys; c += 32) {
-                    float t[32];
-                    tmem_ld32(tT + c, t);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const uint32_t q = pk[c / 2 + i];
-                        const uint64_t x2 = f2_mul(f2_pack(__uint_as_float(q << 16), __uint_as_float(q & 0xffff0000u)),
-                                                   f2_add(f2_pack(t[2 * i], t[2 * i + 1]), ns2));
-                        sum2 = f2_add(sum2, x2);
-                        float u, v;
-                        f2_unpack(x2, u, v);
-                        pk[c / 2 + i] = pack_bf16(u, v);
-                    }
+                for (int i = 0; i < 32; ++i) {
+                    const uint64_t x2 = f2_mul(f2_pack(__uint_as_float(pk[i] << 16), __uint_as_float(pk[i] & 0xffff0000u)),
+                                               f2_add(f2_pack(t[2 * i], t[2 * i + 1]), ns2));
+                    sum2 = f2_add(sum2, x2);
+                    float u, v;
+                    f2_unpack(x2, u, v);
+                    pk[i] = pack_bf16(u, v);
                 }
-                tmem_st16(tT, *reinterpret_cast<uint32_t (*)[16]>(&pk[0]));
-                tmem_st16(tT + 16, *reinterpret_cast<uint32_t (*)[16]>(&pk[16]));
-                tmem_st16(tT + 64, *reinterpret_cast<uint32_t (*)[16]>(&pk[32]));
-                tmem_st16(tT + 80, *reinterpret_cast<uint32_t (*)[16]>(&pk[48]));
-                tmem_st_wait();
+                store32(tT, pk);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&b.p2[half]);
+                if (lane == 0) mbar_arrive(&b.p2);
                 float x, y;
                 f2_unpack(sum2, x, y);
                 A += x + y;
             }
 
             if (nb > 0) {
+                if (loaded) {
+                    asm volatile("cp.async.wait_all;" ::: "memory");
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&b.qfull);
+                }
+                b.tot[half][r] = make_float2(om, A);
+                named_bar_sync(pair, 64);
+                om = b.tot[0][r].x + b.tot[1][r].x;
+                A = b.tot[0][r].y + b.tot[1][r].y;
                 mbar_wait(&b.done, pieces & 1, &b.err);
                 tc_fence_after();
                 ++pieces;
-                // the last reference and the centre: written before the arrivals that `done` came after
-                const int last = (n - 1) & 1;
-                if (last != half) {
-                    mbar_wait(&b.p1[last], ((n - 1) >> 1) & 1, &b.err);
-                    mbar_wait(&b.p2[last], ((n - 1) >> 1) & 1, &b.err);
-                    const float mn = b.m[r], fs = m == -INFINITY ? 0.f : ex2(m - mn);
-                    om *= fs;
-                    A *= fs;
-                    m = mn;
-                    s0 = b.s0[r];
-                }
-                b.tot[half][r] = make_float2(om, A);
-                named_bar_sync(1, kSoft);
-                om = b.tot[0][r].x + b.tot[1][r].x;
-                A = b.tot[0][r].y + b.tot[1][r].y;
             }
+            const long long token = p.q.token0 + tk;
+            const int head = p.h * w.G + fr - tk * w.G;
             const float inv = om != 0.f ? 1.f / om : 0.f, c1 = (1.f + A * inv) * inv;
 #pragma unroll
             for (int c = 0; c < HD; c += 32) {
@@ -539,22 +526,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                             o[i] = make_uint4(y[0], y[1], y[2], y[3]);
                         }
                     } else {
-                        float4* d1 = reinterpret_cast<float4*>(part_sums(w, blockIdx.x, p.slot, D) + (size_t)r * 2 * D + col);
-                        float4* d2 = d1 + D / 4;
+                        float4* d1 = part_sums(w, blockIdx.x, p.slot, D) + (size_t)(col / 4) * kRows + r;
+                        float4* d2 = d1 + (size_t)(D / 4) * kRows;
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            d1[i] = make_float4(o1[4 * i], o1[4 * i + 1], o1[4 * i + 2], o1[4 * i + 3]);
-                            d2[i] = make_float4(o2[4 * i], o2[4 * i + 1], o2[4 * i + 2], o2[4 * i + 3]);
+                            d1[i * kRows] = make_float4(o1[4 * i], o1[4 * i + 1], o1[4 * i + 2], o1[4 * i + 3]);
+                            d2[i * kRows] = make_float4(o2[4 * i], o2[4 * i + 1], o2[4 * i + 2], o2[4 * i + 3]);
                         }
                     }
                 }
             }
             if (r < p.rows && half == 0 && p.slot >= 0)
-                *reinterpret_cast<float4*>(part_stats(w, blockIdx.x, p.slot, D) + r * 4) = make_float4(m, om, A, s0);
-            tc_fence_before();                 // O is read: the next tile's products may write it
-            named_bar_sync(1, kSoft);          // and tot is free
+                part_stats(w, blockIdx.x, p.slot, D)[r] = make_float4(m, om, A, s0);
+            tc_fence_before();                 // O is read: the next tile's products may write it (after p1)
         }
-        if (tid == 0) write_header(w, p, shared);
+        if (tid == 0) write_header(w, blockIdx.x, p, shared);
     }
     tc_fence_before();
     __syncthreads();
