@@ -507,21 +507,18 @@ PagedPlan = namedtuple("PagedPlan", "kv_lens cu_q slots positions granted free_l
 
 class _on_stream:
     """Makes `device` current and, where a stream is given, that stream: what a call allocates or copies
-    inside belongs to the stream that its kernels run on.  Yields the stream's pointer."""
+    inside belongs to the stream that its kernels run on."""
 
     def __init__(self, device, stream):
         self._device, self._stream, self._open = device, stream, ()
 
     def __enter__(self):
         import torch
-        cuda = torch.cuda
-        if self._device.index != cuda.current_device():
-            self._open += (cuda.device(self._device),)
-            self._open[-1].__enter__()
+        self._open = (torch.cuda.device(self._device),)
+        self._open[0].__enter__()
         if self._stream is not None:
-            self._open += (cuda.stream(self._stream),)
-            self._open[-1].__enter__()
-        return cuda.current_stream().cuda_stream
+            self._open += (torch.cuda.stream(self._stream),)
+            self._open[1].__enter__()
 
     def __exit__(self, *exc):
         for c in reversed(self._open):
@@ -532,51 +529,55 @@ def _bad(message):
     return LLAError(LLA_ERR_INVALID_ARG, message)
 
 
-def _check_ints(device, dtype, **tensors):
-    """Contiguous integer tensors of one dtype on one device; shapes as (tensor, shape) pairs."""
-    for name, (t, shape) in tensors.items():
-        if t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-            raise _bad(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
-                       f"{t.dtype} {tuple(t.shape)} on {t.device}")
+def _ints(name, t, shape, dtype, device):
+    """t's pointer, if it is a contiguous tensor of this shape, dtype and device."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise _bad(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}, got {t.dtype} "
+                   f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
 
 
 def _check_caches(k_cache, v_cache):
-    """(num_pages, Hkv, page_size, d, page stride) of two caches laid out alike."""
-    if not (k_cache.is_cuda and v_cache.is_cuda):
-        raise _bad("the caches must be CUDA tensors (there is no CPU path)")
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype or \
-            k_cache.device != v_cache.device:
-        raise _bad(f"caches [num_pages, Hkv, page_size, d] of one dtype and device expected, got {tuple(k_cache.shape)} "
-                   f"{k_cache.dtype}, {tuple(v_cache.shape)} {v_cache.dtype}")
+    """(num_pages, Hkv, page_size, d, page stride, lla dtype) of two caches laid out alike."""
     import torch
-    if k_cache.dtype not in (torch.bfloat16, torch.float32):
+    dt = k_cache.dtype
+    if not k_cache.is_cuda or v_cache.device != k_cache.device:
+        raise _bad("the caches must be CUDA tensors of one device (there is no CPU path)")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or v_cache.dtype is not dt:
+        raise _bad(f"caches [num_pages, Hkv, page_size, d] of one dtype expected, got {tuple(k_cache.shape)} "
+                   f"{dt}, {tuple(v_cache.shape)} {v_cache.dtype}")
+    if dt is torch.bfloat16:
+        dtype = LLA_DTYPE_BF16
+    elif dt is torch.float32:
+        dtype = LLA_DTYPE_FP32
+    else:
         raise _bad("the caches must be bf16 or fp32")
     P, Hkv, Z, d = k_cache.shape
-    for c in (k_cache, v_cache):
-        if c.numel() and not c[0].is_contiguous():
-            raise _bad("each page of a cache must be contiguous (a cache is written in place, so it is not copied)")
-    strides = {c.stride(0) if P > 1 else Hkv * Z * d for c in (k_cache, v_cache)}
-    if len(strides) != 1:
-        raise _bad("the caches must have one page stride")
-    return P, Hkv, Z, d, strides.pop()
+    strides, inner = k_cache.stride(), (Z * d, d, 1)
+    if strides[1:] != inner or v_cache.stride() != strides:
+        for c in (k_cache, v_cache):
+            if c.numel() and not c[0].is_contiguous():
+                raise _bad("each page of a cache must be contiguous (a cache is written in place, so it is not copied)")
+        if P > 1 and v_cache.stride(0) != strides[0]:
+            raise _bad("the caches must have one page stride")
+    return P, Hkv, Z, d, (strides[0] if P > 1 else Hkv * Z * d), dtype
 
 
 def _token_rows(t, name, like, heads, d):
     """[T, heads, d] rows as the kernels take them: heads packed, any 16-byte token stride; else a copy."""
-    if t.dim() != 3 or tuple(t.shape[1:]) != (heads, d) or t.dtype != like.dtype or t.device != like.device:
+    if t.dim() != 3 or t.shape[1:] != (heads, d) or t.dtype is not like.dtype or t.device != like.device:
         raise _bad(f"{name} must be [T, {heads}, {d}] {like.dtype} on {like.device}, got {tuple(t.shape)} {t.dtype} on "
                    f"{t.device}")
-    step = 16 // t.element_size()
-    packed = (t.shape[2] == 1 or t.stride(2) == 1) and (heads == 1 or t.stride(1) == d)
-    if packed and t.data_ptr() % 16 == 0 and (t.shape[0] <= 1 or (t.stride(0) >= heads * d and t.stride(0) % step == 0)):
-        return t, (t.stride(0) if t.shape[0] > 1 else heads * d)
-    t = t.contiguous() if t.data_ptr() % 16 == 0 and not t.is_contiguous() else t.clone(memory_format=_contiguous())
-    return t, heads * d
-
-
-def _contiguous():
+    rows, most = t.shape[0], heads * d
+    token, head, element = t.stride()
+    if element == 1 and (head == d or heads == 1) and t.data_ptr() % 16 == 0:
+        if rows <= 1:
+            return t, most
+        if token >= most and token * t.element_size() % 16 == 0:
+            return t, token
     import torch
-    return torch.contiguous_format
+    t = t.contiguous() if t.data_ptr() % 16 == 0 and not t.is_contiguous() else t.clone(memory_format=torch.contiguous_format)
+    return t, most
 
 
 @functools.lru_cache(maxsize=256)
@@ -599,24 +600,35 @@ def paged_plan(ctx_lens, new_lens, block_table, free_pages, free_count, page_siz
     import torch
     if not ctx_lens.is_cuda:
         raise _bad("paged_plan takes CUDA tensors (there is no CPU path)")
-    dev, T, i32 = ctx_lens.device, int(num_rows), torch.int32
-    S = ctx_lens.numel()
+    dev, T, i32, i64 = ctx_lens.device, int(num_rows), torch.int32, torch.int64
+    if stream is not None or dev.index != torch.cuda.current_device():
+        with _on_stream(dev, stream):
+            return paged_plan(ctx_lens, new_lens, block_table, free_pages, free_count, page_size, T, kv_lens=kv_lens,
+                              cu_q=cu_q, slots=slots, positions=positions, granted=granted, free_left=free_left)
     if block_table.dim() != 2 or T < 1:
         raise _bad("block_table must be [S, W] and num_rows >= 1")
-    _check_ints(dev, i32, ctx_lens=(ctx_lens, (S,)), new_lens=(new_lens, (S,)),
-                block_table=(block_table, (S, block_table.shape[1])), free_pages=(free_pages, (free_pages.numel(),)),
-                free_count=(free_count, (1,)))
-    with _on_stream(dev, stream) as sp:
-        new = lambda t, shape, dt=i32: torch.empty(shape, dtype=dt, device=dev) if t is None else t  # noqa: E731
-        kv_lens, cu_q, granted = new(kv_lens, (S,)), new(cu_q, (S + 1,)), new(granted, (S,))
-        slots, positions, free_left = new(slots, (T,), torch.int64), new(positions, (T,)), new(free_left, (1,))
-        _check_ints(dev, i32, kv_lens=(kv_lens, (S,)), cu_q=(cu_q, (S + 1,)), positions=(positions, (T,)),
-                    granted=(granted, (S,)), free_left=(free_left, (1,)))
-        _check_ints(dev, torch.int64, slots=(slots, (T,)))
-        lla_paged_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), S, int(page_size), block_table.data_ptr(),
-                       block_table.shape[1], free_pages.data_ptr(), free_pages.numel(), free_count.data_ptr(), T,
-                       kv_lens.data_ptr(), cu_q.data_ptr(), slots.data_ptr(), positions.data_ptr(), granted.data_ptr(),
-                       free_left.data_ptr(), sp)
+    S, W, F = ctx_lens.numel(), block_table.shape[1], free_pages.numel()
+    ctx_ptr, new_ptr = _ints("ctx_lens", ctx_lens, (S,), i32, dev), _ints("new_lens", new_lens, (S,), i32, dev)
+    table_ptr = _ints("block_table", block_table, (S, W), i32, dev)
+    free_ptr, count_ptr = _ints("free_pages", free_pages, (F,), i32, dev), _ints("free_count", free_count, (1,), i32, dev)
+    empty = torch.empty
+    if kv_lens is None:
+        kv_lens = empty(S, dtype=i32, device=dev)
+    if cu_q is None:
+        cu_q = empty(S + 1, dtype=i32, device=dev)
+    if slots is None:
+        slots = empty(T, dtype=i64, device=dev)
+    if positions is None:
+        positions = empty(T, dtype=i32, device=dev)
+    if granted is None:
+        granted = empty(S, dtype=i32, device=dev)
+    if free_left is None:
+        free_left = empty(1, dtype=i32, device=dev)
+    lla_paged_plan(ctx_ptr, new_ptr, S, int(page_size), table_ptr, W, free_ptr, F, count_ptr, T,
+                   _ints("kv_lens", kv_lens, (S,), i32, dev), _ints("cu_q", cu_q, (S + 1,), i32, dev),
+                   _ints("slots", slots, (T,), i64, dev), _ints("positions", positions, (T,), i32, dev),
+                   _ints("granted", granted, (S,), i32, dev), _ints("free_left", free_left, (1,), i32, dev),
+                   torch._C._cuda_getCurrentRawStream(dev.index))
     return PagedPlan(kv_lens, cu_q, slots, positions, granted, free_left)
 
 
@@ -625,17 +637,19 @@ def paged_append(k_new, v_new, slots, k_cache, v_cache, *, stream=None):
     (int64, a plan's; rows with a negative slot are skipped).  In place, asynchronous on the current (or
     given) stream.  Rows may be slices of a fused projection (any 16-byte token stride)."""
     import torch
-    P, Hkv, Z, d, page_stride = _check_caches(k_cache, v_cache)
+    P, Hkv, Z, d, page_stride, dtype = _check_caches(k_cache, v_cache)
+    dev = k_cache.device
+    if stream is not None or dev.index != torch.cuda.current_device():
+        with _on_stream(dev, stream):
+            return paged_append(k_new, v_new, slots, k_cache, v_cache)
     if k_new.shape != v_new.shape:
         raise _bad("k_new and v_new must have one shape")
-    T = k_new.shape[0] if k_new.dim() == 3 else 0
-    dtype = LLA_DTYPE_BF16 if k_cache.dtype == torch.bfloat16 else LLA_DTYPE_FP32
-    with _on_stream(k_cache.device, stream) as sp:
-        k_new, ks = _token_rows(k_new, "k_new", k_cache, Hkv, d)
-        v_new, vs = _token_rows(v_new, "v_new", k_cache, Hkv, d)
-        _check_ints(k_cache.device, torch.int64, slots=(slots, (T,)))
-        lla_paged_append(dtype, k_new.data_ptr(), v_new.data_ptr(), slots.data_ptr(), k_cache.data_ptr(),
-                         v_cache.data_ptr(), T, Hkv, d, Z, P, ks, vs, page_stride, sp)
+    k_new, ks = _token_rows(k_new, "k_new", k_cache, Hkv, d)
+    v_new, vs = _token_rows(v_new, "v_new", k_cache, Hkv, d)
+    T = k_new.shape[0]
+    lla_paged_append(dtype, k_new.data_ptr(), v_new.data_ptr(), _ints("slots", slots, (T,), torch.int64, dev),
+                     k_cache.data_ptr(), v_cache.data_ptr(), T, Hkv, d, Z, P, ks, vs, page_stride,
+                     torch._C._cuda_getCurrentRawStream(dev.index))
 
 
 def paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, max_new, *, causal=True,
@@ -650,31 +664,38 @@ def paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, 
     lla_paged_parallax_workspace_size(...) bytes.
     """
     import torch
-    P, Hkv, Z, d, page_stride = _check_caches(k_cache, v_cache)
+    P, Hkv, Z, d, page_stride, dtype = _check_caches(k_cache, v_cache)
     dev = k_cache.device
+    if stream is not None or dev.index != torch.cuda.current_device():
+        with _on_stream(dev, stream):
+            return paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, max_new, causal=causal,
+                                  path=path, out=out, workspace=workspace)
     if q.dim() != 3:
         raise _bad(f"q must be [T, Hq, d], got {tuple(q.shape)}")
-    T, Hq = q.shape[:2]
     if probe.shape != q.shape:
         raise _bad(f"probe must have q's shape {tuple(q.shape)}, got {tuple(probe.shape)}")
     if block_table.dim() != 2:
         raise _bad("block_table must be [S, W]")
+    T, Hq, _ = q.shape
     S, W = block_table.shape
-    _check_ints(dev, torch.int32, block_table=(block_table, (S, W)), cu_q=(cu_q, (S + 1,)), kv_lens=(kv_lens, (S,)))
-    dtype = LLA_DTYPE_BF16 if k_cache.dtype == torch.bfloat16 else LLA_DTYPE_FP32
-    with _on_stream(dev, stream) as sp:
-        q, qs = _token_rows(q, "q", k_cache, Hq, d)
-        probe, rs = _token_rows(probe, "probe", k_cache, Hq, d)
-        if out is None:
-            out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
-        elif out.shape != q.shape or out.dtype != q.dtype or out.device != dev or not out.is_contiguous():
-            raise _bad(f"out must be a contiguous {q.dtype} tensor of shape {tuple(q.shape)} on {dev}")
-        if workspace is None:
-            workspace = torch.empty(_paged_workspace_bytes(dev.index, dtype, int(path), Hq, Hkv, d, Z, int(max_new)),
-                                    dtype=torch.uint8, device=dev)
-        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        lla_paged_parallax(dtype, int(path), q.data_ptr(), probe.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                           block_table.data_ptr(), cu_q.data_ptr(), kv_lens.data_ptr(), out.data_ptr(), T, S, Hq, Hkv, d,
-                           Z, P, W, int(max_new), qs, rs, page_stride, float(tau), 1 if causal else 0, ws_ptr, ws_bytes,
-                           sp)
+    i32, path, max_new = torch.int32, int(path), int(max_new)
+    table_ptr = _ints("block_table", block_table, (S, W), i32, dev)
+    cu_ptr, kv_ptr = _ints("cu_q", cu_q, (S + 1,), i32, dev), _ints("kv_lens", kv_lens, (S,), i32, dev)
+    q, qs = _token_rows(q, "q", k_cache, Hq, d)
+    probe, rs = _token_rows(probe, "probe", k_cache, Hq, d)
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
+    elif out.shape != q.shape or out.dtype is not q.dtype or out.device != dev or not out.is_contiguous():
+        raise _bad(f"out must be a contiguous {q.dtype} tensor of shape {tuple(q.shape)} on {dev}")
+    if workspace is None:
+        workspace = torch.empty(_paged_workspace_bytes(dev.index, dtype, path, Hq, Hkv, d, Z, max_new),
+                                dtype=torch.uint8, device=dev)
+        ws_bytes = workspace.numel()
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise _bad(f"workspace must be a contiguous tensor on {dev}")
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    lla_paged_parallax(dtype, path, q.data_ptr(), probe.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table_ptr,
+                       cu_ptr, kv_ptr, out.data_ptr(), T, S, Hq, Hkv, d, Z, P, W, max_new, qs, rs, page_stride, float(tau),
+                       1 if causal else 0, workspace.data_ptr(), ws_bytes, torch._C._cuda_getCurrentRawStream(dev.index))
     return out
