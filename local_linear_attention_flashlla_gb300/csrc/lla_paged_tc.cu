@@ -160,22 +160,27 @@ __device__ void issue(const Work& w, Walk wk, uint32_t tm, uint32_t qa, uint32_t
             umma_commit(&b.kempty[n % NS]);
         }
         __syncwarp();
-        for (int j = 0; j < nb; ++j, ++n) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&b.vfull[n % NS], (n / NS) & 1, &b.err));
+        for (int j = 0; ok && j < nb; ++j, ++n) {
             const int st = n % NS, sk = (n + 1) % NS;
             const bool more = j + 1 < nb;
-            ok = __all_sync(0xffffffffu, mbar_wait(&b.vfull[st], (n / NS) & 1, &b.err) &&
-                                             (!more || mbar_wait(&b.kfull[sk], ((n + 1) / NS) & 1, &b.err)) &&
-                                             mbar_wait(&b.p1, n & 1, &b.err));
+            ok = __all_sync(0xffffffffu, mbar_wait(&b.p1, n & 1, &b.err));
             if (!ok) break;
             tc_fence_after();
-            if (elect_one()) {
-                gemm_ts<D>(tO1, tS, vring + st * kTile, j > 0);
-                if (more) {
+            if (elect_one()) gemm_ts<D>(tO1, tS, vring + st * kTile, j > 0);
+            __syncwarp();
+            if (more) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&b.kfull[sk], ((n + 1) / NS) & 1, &b.err));
+                if (!ok) break;
+                if (elect_one()) {
                     gemm_ss<D>(tS, qa, kring + sk * kTile);
                     umma_commit(&b.sfull);
                 }
+                __syncwarp();
+                // the next block's V, off the path from its P to its first product
+                ok = __all_sync(0xffffffffu, mbar_wait(&b.vfull[sk], ((n + 1) / NS) & 1, &b.err));
+                if (!ok) break;
             }
-            __syncwarp();
             ok = __all_sync(0xffffffffu, mbar_wait(&b.p2, n & 1, &b.err));
             if (!ok) break;
             tc_fence_after();
@@ -442,16 +447,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load64(tT, t);
                 if (j == 0) {                  // centre: the softmax mean of t over the first keys
                     if (half == 0) {
-                        float x = 0.f, y = 0.f;
+                        float x[2] = {0.f, 0.f}, y[2] = {0.f, 0.f};
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
+                        for (int i = 0; i < 16; ++i) {
                             const float q = __uint_as_float(i & 1 ? pk[i / 2] & 0xffff0000u : pk[i / 2] << 16);
                             if (i < in) {
-                                x += q;
-                                y = fmaf(q, t[i], y);
+                                x[i & 1] += q;
+                                y[i & 1] = fmaf(q, t[i], y[i & 1]);
                             }
                         }
-                        b.s0[r] = x > 0.f ? y / x : t[0];
+                        x[0] += x[1];
+                        b.s0[r] = x[0] > 0.f ? (y[0] + y[1]) / x[0] : t[0];
                     }
                     named_bar_sync(pair, 64);
                     s0 = b.s0[r];
