@@ -3,7 +3,7 @@
 //
 // Per block of 128 keys four products of 128 x 128 x d: S = Q K^T, T = R K^T, O1 += P V and O2 += P' V
 // with P = 2^(l - m) and P' = P (T - s0) (the formulas of lla_paged_simt.cu).  S, T, O1 and O2 fill the
-// 512 TMEM columns, so S and T have one buffer each, and P and P' (bf16) overwrite the halves of S and T
+// 512 TMEM columns (d = 128), so S and T have one buffer each, and P and P' (bf16) overwrite the halves of S and T
 // that they came from.  The products are issued as
 //     S(j+1)  O2(j)  T(j+1)  O1(j+1)  S(j+2)  O2(j+1) ...
 // : the softmax of S(j+1) runs under O2(j) and T(j+1), the weighting of T(j+1) under O1(j+1) and S(j+2).
@@ -27,15 +27,18 @@ namespace {
 using namespace tc;
 
 constexpr int kRows = 128;
-constexpr int kKeys = 128;
 constexpr int kSoft = 256;                     // threads that hold rows
-constexpr int kThreads = kSoft + 64;
+constexpr int kThreads = kSoft + 128;          // 168 registers each at launch: 384 x 168 = 256 x 216 + 128 x 72
 
 template <int D>
 struct TcShape {
+    static constexpr int kKeys = 128;                      // of a block
     static constexpr int kStages = D == 128 ? 2 : 4;       // of K and of V
-    static constexpr int kTile = kKeys * D * 2;            // bytes of a K or V block, and of Q or R: [D / 64][128 rows][128 B]
-    static constexpr size_t smem = (size_t)(2 + 2 * kStages) * kTile + 1024;
+    static constexpr int kCols = kKeys / 2;                // columns of S (and T) that a thread holds
+    static constexpr int kTmem = 512;                      // columns: S, T, O1, O2 (a power of two)
+    static constexpr int kRowTile = kRows * D * 2;         // bytes of Q or R: [D / 64][128 rows][128 B]
+    static constexpr int kTile = kKeys * D * 2;            // bytes of a K or V block: [D / 64][kKeys rows][128 B]
+    static constexpr size_t smem = (size_t)2 * kRowTile + (size_t)2 * kStages * kTile + 1024;
 };
 
 struct TcArgs {
@@ -59,15 +62,16 @@ struct TcBars {
     float2 tot[2][kRows];                      // by column half: omega and A of a tile
 };
 
-__device__ __forceinline__ uint32_t piece_off(int r, int c) {
-    return (uint32_t)((c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+// Byte offset of 16-byte piece c of row r in a tile of `rows` rows ([D / 64][rows][128 B], 128-byte swizzle).
+__device__ __forceinline__ uint32_t piece_off(int rows, int r, int c) {
+    return (uint32_t)((c >> 3) * (rows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
 }
 
 // One box to a lane; K and V of a block go to rings of their own (K is given back a product earlier).
 template <int D>
 __device__ void feed_kv(const Work& w, Walk wk, const CUtensorMap* mk, const CUtensorMap* mv, uint32_t kring,
                         uint32_t vring, TcBars<D>& b) {
-    constexpr int NS = TcShape<D>::kStages, kTile = TcShape<D>::kTile;
+    constexpr int NS = TcShape<D>::kStages, kTile = TcShape<D>::kTile, kKeys = TcShape<D>::kKeys;
     const int lane = threadIdx.x & 31;
     const int box = min(1 << w.page_shift, kBoxRows), boxes = kKeys / box;     // <= 16
     int n = 0;                                 // blocks issued
@@ -108,29 +112,32 @@ __device__ void feed_kv(const Work& w, Walk wk, const CUtensorMap* mk, const CUt
         }
 }
 
-// D[tmem] = A B^T, 128 x 128 x D, both operands K-major in shared memory.
+// D[tmem] = A B^T, 128 x kKeys x D, both operands K-major in shared memory.
 template <int D>
 __device__ __forceinline__ void gemm_ss(uint32_t d, uint32_t a_addr, uint32_t b_addr) {
+    constexpr int kKeys = TcShape<D>::kKeys;
     constexpr uint32_t ID = idesc_bf16(kRows, kKeys, false, false);
     const uint64_t a0 = sdesc_sw128(a_addr, 16, 1024), b0 = sdesc_sw128(b_addr, 16, 1024);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-        const uint64_t off = (uint64_t)(((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4);
-        if (ks == 0) umma_ss_c<false>(d, a0 + off, b0 + off, ID);
-        else umma_ss_c<true>(d, a0 + off, b0 + off, ID);
+        const uint64_t ao = (uint64_t)(((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4);
+        const uint64_t bo = (uint64_t)(((ks >> 2) * (kKeys * 128) + (ks & 3) * 32) >> 4);
+        if (ks == 0) umma_ss_c<false>(d, a0 + ao, b0 + bo, ID);
+        else umma_ss_c<true>(d, a0 + ao, b0 + bo, ID);
     }
 }
-// D[tmem] (+)= P V, 128 x D x 128: P bf16 pairs in TMEM (keys 0-63 at column 0, 64-127 at column 64), V
-// [128 keys x D] read MN-major.
+// D[tmem] (+)= P V, 128 x D x kKeys: P bf16 pairs in TMEM (each half of the keys in the first columns of the half
+// its S or T was in), V [kKeys x D] read MN-major.
 template <int D>
 __device__ __forceinline__ void gemm_ts(uint32_t d, uint32_t p, uint32_t v_addr, bool acc) {
+    constexpr int kKeys = TcShape<D>::kKeys, kHalf = kKeys / 32;      // k steps of a half
     constexpr uint32_t ID = idesc_bf16(kRows, D, false, true);
     const uint64_t b0 = sdesc_sw128(v_addr, kKeys * 128, 1024);
     if (acc) umma_ts_c<true>(d, p, b0, ID);
     else umma_ts_c<false>(d, p, b0, ID);
 #pragma unroll
     for (int ks = 1; ks < kKeys / 16; ++ks)
-        umma_ts_c<true>(d, p + (ks >> 2) * 64 + (ks & 3) * 8, b0 + (uint64_t)((ks * 2048) >> 4), ID);
+        umma_ts_c<true>(d, p + (ks / kHalf) * (kKeys / 2) + (ks % kHalf) * 8, b0 + (uint64_t)((ks * 2048) >> 4), ID);
 }
 
 // The issuing warp.  All lanes run the loop and one elected lane issues: with everything that the products'
@@ -140,8 +147,8 @@ __device__ __forceinline__ void gemm_ts(uint32_t d, uint32_t p, uint32_t v_addr,
 template <int D>
 __device__ void issue(const Work& w, Walk wk, uint32_t tm, uint32_t qa, uint32_t ra, uint32_t kring, uint32_t vring,
                       TcBars<D>& b) {
-    constexpr int NS = TcShape<D>::kStages, kTile = TcShape<D>::kTile;
-    const uint32_t tS = tm, tT = tm + 128, tO1 = tm + 256, tO2 = tm + 256 + D;
+    constexpr int NS = TcShape<D>::kStages, kTile = TcShape<D>::kTile, kKeys = TcShape<D>::kKeys;
+    const uint32_t tS = tm, tT = tm + kKeys, tO1 = tm + 2 * kKeys, tO2 = tO1 + D;
     int n = 0, pieces = 0;
     bool ok = true;
     Piece p;
@@ -224,15 +231,16 @@ __device__ __forceinline__ void scale32(uint32_t t, float f) {
     tmem_st16(t + 16, z);
 }
 
-// 64 columns of this thread's row.
-__device__ __forceinline__ void load64(uint32_t t, float (&x)[64]) {
-    tmem_ld32(t, *reinterpret_cast<float (*)[32]>(&x[0]));
-    tmem_ld32(t + 32, *reinterpret_cast<float (*)[32]>(&x[32]));
-    tmem_ld_wait();
+// This thread's N columns of a row; the caller waits.
+template <int N>
+__device__ __forceinline__ void load_cols(uint32_t t, float (&x)[N]) {
+#pragma unroll
+    for (int c = 0; c < N; c += 32) tmem_ld32(t + c, *reinterpret_cast<float (*)[32]>(&x[c]));
 }
-__device__ __forceinline__ void store32(uint32_t t, const uint32_t (&x)[32]) {
-    tmem_st16(t, *reinterpret_cast<const uint32_t (*)[16]>(&x[0]));
-    tmem_st16(t + 16, *reinterpret_cast<const uint32_t (*)[16]>(&x[16]));
+template <int N>
+__device__ __forceinline__ void store_cols(uint32_t t, const uint32_t (&x)[N]) {
+#pragma unroll
+    for (int c = 0; c < N; c += 16) tmem_st16(t + c, *reinterpret_cast<const uint32_t (*)[16]>(&x[c]));
     tmem_st_wait();
 }
 
@@ -244,28 +252,43 @@ __device__ __forceinline__ bool pair_or(int id, bool x) {
     return r != 0;
 }
 
-// x <- 2^(scale x - ref) as bf16 pairs; their fp32 sum, and the maximum of x.
-__device__ __forceinline__ void weigh(const float (&x)[64], float scale, float ref, uint32_t (&pk)[32], float& sum, float& top) {
+// x <- p = 2^(scale x - ref), and p as bf16 pairs; the fp32 sum, and whether any p reached 2.
+// The exponents' reference lies kHead above the maximum that set it, so a weight reaches 2 when a logit has
+// grown kHead + 1 = 8 past that maximum, and that is a bit of its bf16 exponent: the maximum itself is taken only
+// when the reference moves.  (Weights near 2^-kHead lose nothing: every sum is floating.)
+constexpr float kHead = 7.f;
+template <int N>
+__device__ __forceinline__ void weigh(float (&x)[N], float scale, float ref, uint32_t (&pk)[N / 2], float& sum, bool& over) {
     const uint64_t sc2 = f2_pack(scale, scale), nr2 = f2_pack(-ref, -ref);
-    uint64_t sum2 = f2_pack(0.f, 0.f);
-    float t0 = x[0], t1 = x[1];
+    uint64_t s0 = f2_pack(0.f, 0.f), s1 = s0;
+    uint32_t bits = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        t0 = fmaxf(t0, x[2 * i]);
-        t1 = fmaxf(t1, x[2 * i + 1]);
+    for (int i = 0; i < N / 2; ++i) {
         float u, v;
         f2_unpack(f2_fma(f2_pack(x[2 * i], x[2 * i + 1]), sc2, nr2), u, v);
-        u = ex2(u);
-        v = ex2(v);
-        sum2 = f2_add(sum2, f2_pack(u, v));
-        // the value products take the weights in bf16 (half a step is 2^-8 of each), the same rounded weight in
-        // both; their sums and the normaliser are fp32
+        x[2 * i] = u = ex2(u);
+        x[2 * i + 1] = v = ex2(v);
+        if (i & 1) s1 = f2_add(s1, f2_pack(u, v));
+        else s0 = f2_add(s0, f2_pack(u, v));
+        // the value products take the weights in bf16 (half a step is 2^-8 of each); their sums and the normaliser
+        // are fp32
         pk[i] = pack_bf16(u, v);
+        bits |= pk[i];
     }
     float v;
-    f2_unpack(sum2, sum, v);
+    f2_unpack(f2_add(s0, s1), sum, v);
     sum += v;
-    top = fmaxf(t0, t1);
+    over = (bits & 0x40004000u) != 0;
+}
+template <int N>
+__device__ __forceinline__ float top_of(const float (&x)[N]) {
+    float a = x[0], b = x[1];
+#pragma unroll
+    for (int i = 2; i < N; i += 2) {
+        a = fmaxf(a, x[i]);
+        b = fmaxf(b, x[i + 1]);
+    }
+    return fmaxf(a, b);
 }
 
 // The tile's queries and probes into shared memory (not waited for); rows behind its last are zeros.
@@ -279,8 +302,8 @@ __device__ __forceinline__ void load_rows(const TcArgs& a, const Piece& p, uint3
         const bool in = rr < p.rows;
         const int f = in ? p.row0 + rr : 0, tk = over_g(w, f);
         const long long token = p.q.token0 + tk, hc = (long long)(p.h * w.G + f - tk * w.G) * D + c * 8;
-        copy16(qa + piece_off(rr, c), a.q + token * a.q_stride + hc, in);
-        copy16(ra + piece_off(rr, c), a.probe + token * a.r_stride + hc, in);
+        copy16(qa + piece_off(kRows, rr, c), a.q + token * a.q_stride + hc, in);
+        copy16(ra + piece_off(kRows, rr, c), a.probe + token * a.r_stride + hc, in);
     }
 }
 
@@ -288,14 +311,14 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
     using Sh = TcShape<D>;
-    constexpr int NS = Sh::kStages, kTile = Sh::kTile, HD = D / 2;
+    constexpr int NS = Sh::kStages, kTile = Sh::kTile, kKeys = Sh::kKeys, kCols = Sh::kCols, HD = D / 2;
     extern __shared__ unsigned char raw[];
     __shared__ long long scratch[40];
     __shared__ TcBars<D> b;
     unsigned char* base = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-    const uint32_t qa = smem_u32(base), ra = qa + kTile;
-    unsigned char* vs = base + (size_t)(2 + NS) * kTile;
-    const uint32_t kring = qa + 2 * kTile, vring = kring + NS * kTile;
+    const uint32_t qa = smem_u32(base), ra = qa + Sh::kRowTile;
+    unsigned char* vs = base + 2 * Sh::kRowTile + (size_t)NS * kTile;
+    const uint32_t kring = qa + 2 * Sh::kRowTile, vring = kring + NS * kTile;
     const Work& w = a.w;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -317,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_fence_init();
     }
     if (warp == kSoft / 32) {
-        tmem_alloc(&b.tmem, 512);
+        tmem_alloc(&b.tmem, Sh::kTmem);
         tmem_relinquish();
     }
     Walk wk = begin_walk(w, blockIdx.x, scratch);
@@ -327,18 +350,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     const uint32_t tm = b.tmem;
 
-    if (warp == kSoft / 32) {
-        feed_kv<D>(w, wk, &mk, &mv, kring, vring, b);
-    } else if (warp == kSoft / 32 + 1) {
+    if (warp >= kSoft / 32) {
+        setmaxnreg_dec72();
+        if (warp == kSoft / 32) feed_kv<D>(w, wk, &mk, &mv, kring, vring, b);
+        if (warp == kSoft / 32 + 1)
         issue<D>(w, wk, __shfl_sync(0xffffffffu, tm, 0), __shfl_sync(0xffffffffu, qa, 0),
                  __shfl_sync(0xffffffffu, ra, 0), __shfl_sync(0xffffffffu, kring, 0),
                  __shfl_sync(0xffffffffu, vring, 0), b);
     } else {
+        setmaxnreg_inc216();
         const int half = warp >> 2, r = (warp & 3) * 32 + lane;      // column half, row
         const int pair = 1 + (warp & 3);                             // barrier of the row's two warps
         const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t tS = lanes + half * 64, tT = lanes + 128 + half * 64;
-        const uint32_t tO1 = lanes + 256 + half * HD, tO2 = tO1 + D;   // this half's output columns
+        const uint32_t tS = lanes + half * kCols, tT = tS + kKeys;
+        const uint32_t tO1 = lanes + 2 * kKeys + half * HD, tO2 = tO1 + D;   // this half's output columns
         int n = 0, pieces = 0;
         bool shared = false, loaded = false;
         Piece p, next;
@@ -365,53 +390,43 @@ __global__ void __launch_bounds__(kThreads, 1)
             int limit = p.keys;
             if (r < p.rows && w.causal) limit = min(max(p.q.L - p.q.nq + tk + 1, 0), p.q.L);
             for (int j = 0; j < nb; ++j, ++n) {
-                const int key0 = (p.j0 + j) * kKeys, in = limit - key0 - half * 64;   // columns of this thread it sees
-                const bool masked = !__all_sync(0xffffffffu, in >= 64);
+                const int key0 = (p.j0 + j) * kKeys, in = limit - key0 - half * kCols;   // columns of this thread it sees
+                const bool masked = !__all_sync(0xffffffffu, in >= kCols);
                 const bool tail = p.keys < key0 + kKeys;
                 // ---------------------------------------------------------------- S: the weights p
                 mbar_wait(&b.sfull, n & 1, &b.err);
                 tc_fence_after();
-                uint32_t pk[32];
-                float ps, top, f = 1.f;
-                bool grow = j == 0;
-                {
-                    float x[64];
-                    load64(tS, x);
+                uint32_t pk[kCols / 2];
+                float x[kCols], ps, f = 1.f;
+                bool grow = j == 0, over;
+                auto scores = [&] {
+                    load_cols(tS, x);
+                    tmem_ld_wait();
                     if (masked) {
 #pragma unroll
-                        for (int i = 0; i < 64; ++i)
+                        for (int i = 0; i < kCols; ++i)
                             if (i >= in) x[i] = -INFINITY;
                     }
-                    if (j == 0) {
-                        top = x[0];
-#pragma unroll
-                        for (int i = 1; i < 64; ++i) top = fmaxf(top, x[i]);
-                    } else {
-                        weigh(x, a.scale, m == -INFINITY ? 0.f : m, pk, ps, top);
-                        // the reference follows the maximum only when that has grown by more than 8 (weights to 2^8)
-                        grow = pair_or(pair, top * a.scale > m + 8.f);
-                    }
-                    if (grow) {
-                        b.mx[half][r] = top;
-                        named_bar_sync(pair, 64);
-                        const float mn = fmaxf(m, a.scale * fmaxf(top, b.mx[half ^ 1][r]));
-                        f = mn == -INFINITY || j == 0 ? 1.f : ex2(m - mn);
-                        m = mn;
-                        om *= f;
-                        A *= f;
-                        if (j > 0) {           // S is still there
-                            load64(tS, x);
-                            if (masked) {
-#pragma unroll
-                                for (int i = 0; i < 64; ++i)
-                                    if (i >= in) x[i] = -INFINITY;
-                            }
-                        }
-                        weigh(x, a.scale, m == -INFINITY ? 0.f : m, pk, ps, top);
-                        if (j > 0) {           // O1 of the blocks before (complete: S of this one came after it)
+                };
+                scores();
+                if (j > 0) {
+                    weigh(x, a.scale, m == -INFINITY ? 0.f : m, pk, ps, over);
+                    grow = pair_or(pair, over);
+                    if (grow) scores();        // S is still there
+                }
+                if (grow) {
+                    const float top = top_of(x);
+                    b.mx[half][r] = top;
+                    named_bar_sync(pair, 64);
+                    const float mn = fmaxf(m, fmaf(a.scale, fmaxf(top, b.mx[half ^ 1][r]), kHead));
+                    f = mn == -INFINITY || j == 0 ? 1.f : ex2(m - mn);
+                    m = mn;
+                    om *= f;
+                    A *= f;
+                    weigh(x, a.scale, m == -INFINITY ? 0.f : m, pk, ps, over);
+                    if (j > 0) {               // O1 of the blocks before (complete: S of this one came after it)
 #pragma unroll 1
-                            for (int c = 0; c < HD; c += 32) scale32(tO1 + c, f);
-                        }
+                        for (int c = 0; c < HD; c += 32) scale32(tO1 + c, f);
                     }
                 }
                 if (tail) {
@@ -422,11 +437,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = tid; e < kKeys * (D / 8); e += kSoft) {
                         const int rr = e / (D / 8), c = e % (D / 8);
                         if (key0 + rr >= p.keys)
-                            *reinterpret_cast<uint4*>(vs + (size_t)st * kTile + piece_off(rr, c)) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4*>(vs + (size_t)st * kTile + piece_off(kKeys, rr, c)) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                 }
-                store32(tS, pk);
+                store_cols(tS, pk);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b.p1);
@@ -443,49 +458,53 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int c = 0; c < HD; c += 32) scale32(tO2 + c, f);
                 }
-                float t[64];
-                load64(tT, t);
                 if (j == 0) {                  // centre: the softmax mean of t over the first keys
                     if (half == 0) {
-                        float x[2] = {0.f, 0.f}, y[2] = {0.f, 0.f};
+                        float t[16], y[2] = {0.f, 0.f}, z[2] = {0.f, 0.f};
+                        tmem_ld16(tT, t);
+                        tmem_ld_wait();
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float q = __uint_as_float(i & 1 ? pk[i / 2] & 0xffff0000u : pk[i / 2] << 16);
+                        for (int i = 0; i < 16; ++i)
                             if (i < in) {
-                                x[i & 1] += q;
-                                y[i & 1] = fmaf(q, t[i], y[i & 1]);
+                                z[i & 1] += x[i];
+                                y[i & 1] = fmaf(x[i], t[i], y[i & 1]);
                             }
-                        }
-                        x[0] += x[1];
-                        b.s0[r] = x[0] > 0.f ? (y[0] + y[1]) / x[0] : t[0];
+                        z[0] += z[1];
+                        b.s0[r] = z[0] > 0.f ? (y[0] + y[1]) / z[0] : t[0];
                     }
                     named_bar_sync(pair, 64);
                     s0 = b.s0[r];
                 }
-                if (tail) {                    // t of keys behind the last may be anything, a NaN too
-                    const int left = p.keys - key0 - half * 64;
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        if (i >= left) t[i] = s0;
-                }
                 const uint64_t ns2 = f2_pack(-s0, -s0);
                 uint64_t sum2 = f2_pack(0.f, 0.f);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const uint64_t x2 = f2_mul(f2_pack(__uint_as_float(pk[i] << 16), __uint_as_float(pk[i] & 0xffff0000u)),
-                                               f2_add(f2_pack(t[2 * i], t[2 * i + 1]), ns2));
-                    sum2 = f2_add(sum2, x2);
-                    float u, v;
-                    f2_unpack(x2, u, v);
-                    pk[i] = pack_bf16(u, v);
+                for (int c = 0; c < kCols; c += 32) {
+                    float t[32];
+                    tmem_ld32(tT + c, t);
+                    tmem_ld_wait();
+                    if (tail) {                // t of keys behind the last may be anything, a NaN too
+                        const int left = p.keys - key0 - half * kCols - c;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (i >= left) t[i] = s0;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint64_t x2 = f2_mul(f2_pack(x[c + 2 * i], x[c + 2 * i + 1]),
+                                                   f2_add(f2_pack(t[2 * i], t[2 * i + 1]), ns2));
+                        sum2 = f2_add(sum2, x2);
+                        float u, v;
+                        f2_unpack(x2, u, v);
+                        pk[c / 2 + i] = pack_bf16(u, v);
+                    }
                 }
-                store32(tT, pk);
+                store_cols(tT, pk);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b.p2);
-                float x, y;
-                f2_unpack(sum2, x, y);
-                A += x + y;
+                float y, z;
+                f2_unpack(sum2, y, z);
+                A += y + z;
             }
 
             if (nb > 0) {
@@ -553,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     if (warp == kSoft / 32) {
         __syncwarp();
-        tmem_dealloc(tm, 512);
+        tmem_dealloc(tm, Sh::kTmem);
     }
     if (tid == 0 && b.err) atomicOr(w.err, (unsigned)kDevErrMbarTimeout);
 }
@@ -572,7 +591,7 @@ cudaError_t launch_tc(const TcArgs& a, const CUtensorMap& mk, const CUtensorMap&
 
 PagedSplit paged_tc_split(const PagedProblem& p, int sms) {
     (void)p;
-    return PagedSplit{paged::kRows, paged::kKeys, sms, 2};
+    return PagedSplit{paged::kRows, paged::TcShape<128>::kKeys, sms, 2};
 }
 
 cudaError_t launch_paged_tc(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream, const char** why) {
