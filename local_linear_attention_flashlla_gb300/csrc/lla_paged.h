@@ -69,6 +69,23 @@ cudaError_t launch_paged_merge(const PagedProblem& p, const PagedSplit& sp, cuda
 #ifdef __CUDACC__
 namespace paged {
 
+// Launches with programmatic stream serialisation: the grid may be set up while the kernel before it still
+// runs, and waits for that kernel's end in cudaGridDependencySynchronize before it reads anything.
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // What a kernel needs of the problem, by value.
 struct Work {
     const int* table;
@@ -194,82 +211,86 @@ struct Walk {
     Seq q;
 };
 
-__device__ __forceinline__ long long block_sum(long long v, long long* red) {
+// Inclusive sum of v over the block's threads in thread order; *all: the block's total.  sh: 32 long longs.
+__device__ __forceinline__ long long block_scan(long long v, long long* sh, long long* all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (blockDim.x + 31) >> 5;
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (lane == 0) red[warp] = v;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long t = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += t;
+    }
+    if (lane == 31) sh[warp] = v;
     __syncthreads();
-    long long t = 0;
-    for (int i = 0; i < nw; ++i) t += red[i];
+    long long sum = 0;
+    for (int i = 0; i < nw; ++i) {
+        if (i == warp) v += sum;
+        sum += sh[i];
+    }
+    *all = sum;
     __syncthreads();
-    return t;
+    return v;
 }
 
-// Range of CTA `cta` and the tile it begins in.  Every thread of the block calls it; the
-// shared scratch is 40 long longs.  active = 0: no units at all.  blockDim.x is a multiple of 32.
+// Range of CTA `cta` and the tile it begins in.  Every thread of the block calls it; the shared scratch is
+// 40 long longs.  active = 0: no units at all.  blockDim.x is a multiple of 32.  A thread sums a run of
+// consecutive sequences, so that one scan finds the total and, with it, whose sequence the range begins in.
 __device__ inline Walk begin_walk(const Work& w, int cta, long long* sh) {
-    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5, nw = nt >> 5;
-    long long mine = 0;
-    for (int s = tid; s < w.S; s += nt) mine += seq_units(w, load_seq(w, s));
+    const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31;
+    const int per = (w.S + nt - 1) / nt, s0 = min(tid * per, w.S), s1 = min(s0 + per, w.S);
     Walk k;
     k.cta = cta;
-    k.total = block_sum(mine, sh);
     k.s = k.h = k.i = k.j = 0;
     k.q.token0 = k.q.nq = k.q.L = 0;
     k.u = k.end = 0;
+    long long mine = 0;
+    for (int s = s0; s < s1; ++s) {
+        k.q = load_seq(w, s);
+        mine += seq_units(w, k.q);
+    }
+    long long pre = block_scan(mine, sh, &k.total) - mine;
     const long long most = div_units(k.total + w.min_units - 1, w.min_units);
     k.active = (int)(most < w.ctas ? most : w.ctas);
     if (cta >= k.active) return k;
     k.u = div_units(k.total * cta, k.active);
     k.end = div_units(k.total * (cta + 1), k.active);
-    long long before = 0;
-    int* at = reinterpret_cast<int*>(sh + 36);
-    for (int s0 = 0; s0 < w.S; s0 += nt) {
-        const int s = s0 + tid;
-        const long long mineu = s < w.S ? seq_units(w, load_seq(w, s)) : 0;
-        long long inc = mineu;
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long t = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += t;
-        }
-        if (lane == 31) sh[warp] = inc;
-        if (tid == 0) *at = -1;
-        __syncthreads();
-        long long pre = before, all = before;
-        for (int i = 0; i < nw; ++i) {
-            if (i < warp) pre += sh[i];
-            all += sh[i];
-        }
-        pre += inc - mineu;
-        if (mineu > 0 && k.u >= pre && k.u < pre + mineu) {
-            *at = s;
-            sh[35] = pre;
-        }
-        __syncthreads();
-        const int found = *at;
-        const long long fpre = sh[35];
-        __syncthreads();
-        if (found >= 0) {
-            k.s = found;
-            k.q = load_seq(w, found);
-            const int tiles = tiles_of(w, k.q);
-            long long rem = k.u - fpre;
-            const long long per = units_before(w, k.q, tiles);
-            k.h = (int)div_units(rem, per);
-            rem -= k.h * per;
-            int lo = 0;                       // the last tile with units_before <= rem: 32 probes at a time
-            for (int range = tiles; range > 1;) {
-                const int step = (range + 31) >> 5, at = lo + lane * step;
-                const bool yes = lane * step < range && units_before(w, k.q, at) <= rem;
-                lo += (__popc(__ballot_sync(0xffffffffu, yes)) - 1) * step;
-                range = min(step, tiles - lo);
+    int* at = reinterpret_cast<int*>(sh + 32);     // sequence, token0, nq, L
+    if (k.u >= pre && k.u < pre + mine) {
+        int s = s0;
+        if (per > 1) {
+            for (; s + 1 < s1; ++s) {
+                const long long u = seq_units(w, load_seq(w, s));
+                if (k.u < pre + u) break;
+                pre += u;
             }
-            k.i = lo;
-            k.j = (int)(rem - units_before(w, k.q, lo));
-            break;
+            k.q = load_seq(w, s);
         }
-        before = all;
+        sh[36] = pre;
+        at[0] = s;
+        at[1] = k.q.token0;
+        at[2] = k.q.nq;
+        at[3] = k.q.L;
     }
+    __syncthreads();
+    k.s = at[0];
+    k.q.token0 = at[1];
+    k.q.nq = at[2];
+    k.q.L = at[3];
+    long long rem = k.u - sh[36];
+    const int tiles = tiles_of(w, k.q);
+    const long long unit = units_before(w, k.q, tiles);
+    k.h = (int)div_units(rem, unit);
+    rem -= k.h * unit;
+    if (tiles > 1) {
+        int lo = 0;                                // the last tile with units_before <= rem: 32 probes at a time
+        for (int range = tiles; range > 1;) {
+            const int step = (range + 31) >> 5, probe = lo + lane * step;
+            const bool yes = lane * step < range && units_before(w, k.q, probe) <= rem;
+            lo += (__popc(__ballot_sync(0xffffffffu, yes)) - 1) * step;
+            range = min(step, tiles - lo);
+        }
+        k.i = lo;
+        rem -= units_before(w, k.q, lo);
+    }
+    k.j = (int)rem;
     return k;
 }
 

@@ -139,6 +139,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         err = 0;
         tc::mbar_fence_init();
     }
+    cudaGridDependencySynchronize();           // the lengths may be the previous kernel's
     Walk wk = begin_walk(w, blockIdx.x, scratch);
     cudaTriggerProgrammaticLaunchCompletion();   // the merge waits for this grid's end all the same
     __syncthreads();
@@ -406,8 +407,7 @@ cudaError_t launch_dec(const DecArgs& a, const CUtensorMap& mk, const CUtensorMa
     auto* kern = paged_decode_kernel<D, MT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<a.w.ctas, kThreads, smem, stream>>>(a, mk, mv);
-    return cudaGetLastError();
+    return launch_after(kern, dim3(a.w.ctas), kThreads, smem, stream, a, mk, mv);
 }
 
 }  // namespace

@@ -23,6 +23,13 @@ __device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float
 __device__ __forceinline__ void put(float* p, float x) { *p = x; }
 __device__ __forceinline__ void put(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+// Four values side by side (16- or 8-byte aligned).
+__device__ __forceinline__ void put4(float* p, float4 x) { *reinterpret_cast<float4*>(p) = x; }
+__device__ __forceinline__ void put4(__nv_bfloat16* p, float4 x) {
+    __nv_bfloat162 y[2] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w)};
+    *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(y);
+}
+
 // 16 bytes of T as floats.
 template <typename T>
 __device__ __forceinline__ void load16(const T* g, float* dst) {
@@ -76,6 +83,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
     const T* gk = static_cast<const T*>(a.k);
     const T* gv = static_cast<const T*>(a.v);
 
+    cudaGridDependencySynchronize();           // the lengths may be the previous kernel's
     Walk wk = begin_walk(w, blockIdx.x, scratch);
     cudaTriggerProgrammaticLaunchCompletion();   // the merge waits for this grid's end all the same
     Piece p;
@@ -224,70 +232,82 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
 // Joins the parts of the tile that CTA blockIdx.x starts and others finish: part 0 is its slot 1, part
 // i > 0 slot 0 of CTA blockIdx.x + i.  With the common maximum and one centre,
 //   out = sum_i f_i ((1 + A/w - (s0_i - s0)) O1_i - O2_i) / w,   f_i = 2^(m_i - m).
-// The order of the sum is fixed by the parts: results do not depend on which CTA was first.  Each block
-// turns the parts' statistics into two factors per (part, row) in shared memory, after which every load of
-// the sums is independent of the others; a thread has four columns of a row, and where rows are few,
-// kLanes threads share them and take the parts in turn.  Reading the parts from L2 bounds it.
-constexpr int kFactors = 4096;                 // (part, row) factors held at a time
+// The order of the sum is fixed by the parts: results do not depend on which CTA was first.  A block has
+// eight rows and kC groups of four columns: a warp turns a row's statistics into two factors per part in
+// shared memory, after which the loads of the sums are independent of one another.  Eight rows side by side
+// are a full line of a part, and the four columns of four neighbouring threads a full sector of the output.
+// Where parts are many and rows few, kLanes threads share a (row, columns) and take the parts in turn.
+constexpr int kMergeRows = 8;
+constexpr int kChunk = 128;                    // parts whose factors are held at a time
+
+template <int D, int R>
+struct MergeShape {
+    static constexpr int kC = R <= 16 ? 4 : D / 4;                     // groups of four columns of a block
+    static constexpr int kItems = kMergeRows * kC, kLanes = 256 / kItems;
+    static constexpr int kBlocks = R / kMergeRows * (D / 4 / kC);      // of a tile
+};
 
 template <typename T, int D, int R>
 __global__ void __launch_bounds__(256) paged_merge_kernel(Work w, T* __restrict__ out, int Hq) {
-    constexpr int kItems = R * D / 4 >= 1024 ? 256 : R * D / 4 >= 256 ? 64 : 32;   // (row, four columns) of a block
-    constexpr int kLanes = 256 / kItems;
-    constexpr int kPer = 256 / R;              // threads on a row's statistics
-    constexpr int kChunk = kFactors / R;       // parts at a time
-    static_assert(kPer <= 32 && kPer >= 1, "a row's threads lie in one warp");
-    __shared__ float2 fac[kFactors];
+    using Sh = MergeShape<D, R>;
+    constexpr int kItems = Sh::kItems, kLanes = Sh::kLanes;
+    __shared__ float2 fac[kChunk][kMergeRows];
     __shared__ float4 red[kLanes > 1 ? 256 : 1];
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, warp = tid >> 5, ln = tid & 31;
     cudaGridDependencySynchronize();
     const PartHeader h = w.hdr[blockIdx.x];
-    if (h.parts == 0) return;
-    const int row = tid / kPer, sub = tid % kPer;
-    float m = -INFINITY, om = 0.f, A = 0.f;
-    const float s0 = part_stats(w, blockIdx.x, 1, D)[row].w;     // rows behind h.rows: never used
+    const int row0 = blockIdx.y % (R / kMergeRows) * kMergeRows, c0 = blockIdx.y / (R / kMergeRows) * Sh::kC;
+    if (h.parts == 0 || row0 >= h.rows) return;
+
+    // this warp's row: statistics of its parts (a lane's first in a register)
+    const int row = row0 + warp;
     const bool live = row < h.rows;
+    auto stats = [&](int i) { return part_stats(w, blockIdx.x + i, i == 0, D)[row]; };
+    float4 first = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+    if (live && ln < h.parts) first = stats(ln);
+    float m = first.x;
     if (live)
-        for (int i = sub; i < h.parts; i += kPer) m = fmaxf(m, part_stats(w, blockIdx.x + i, i == 0, D)[row].x);
+        for (int i = ln + 32; i < h.parts; i += 32) m = fmaxf(m, stats(i).x);
 #pragma unroll
-    for (int o = kPer / 2; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float base = m == -INFINITY ? 0.f : m;
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float base = m == -INFINITY ? 0.f : m, s0 = __shfl_sync(0xffffffffu, first.w, 0);
+    float f = exp2f(first.x - base), om = f * first.y, A = f * fmaf(first.w - s0, first.y, first.z);
     if (live)
-        for (int i = sub; i < h.parts; i += kPer) {
-            const float4 st = part_stats(w, blockIdx.x + i, i == 0, D)[row];
-            const float f = exp2f(st.x - base);
+        for (int i = ln + 32; i < h.parts; i += 32) {
+            const float4 st = stats(i);
+            f = exp2f(st.x - base);
             om = fmaf(f, st.y, om);
             A = fmaf(f, fmaf(st.w - s0, st.y, st.z), A);
         }
 #pragma unroll
-    for (int o = kPer / 2; o; o >>= 1) {
+    for (int o = 16; o; o >>= 1) {
         om += __shfl_xor_sync(0xffffffffu, om, o);
         A += __shfl_xor_sync(0xffffffffu, A, o);
     }
     const float inv = om != 0.f ? 1.f / om : 0.f, c1 = 1.f + A * inv;   // om 0: no key in any part; NaN stays NaN
 
-    const int item = blockIdx.y * kItems + tid % kItems, lane = tid / kItems;
-    const int r = item % R;
+    const int r = tid % kMergeRows, c4 = c0 + tid / kMergeRows % Sh::kC, lane = tid / kItems;
+    const bool mine = row0 + r < h.rows;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = 0; i0 < h.parts; i0 += kChunk) {
         const int n = min(kChunk, h.parts - i0);
         if (live)
-            for (int i = sub; i < n; i += kPer) {
-                const float4 st = part_stats(w, blockIdx.x + i0 + i, i0 + i == 0, D)[row];
-                const float f = exp2f(st.x - base) * inv;
-                fac[i * R + row] = make_float2(f * (c1 - (st.w - s0)), f);
+            for (int i = ln; i < n; i += 32) {
+                const float4 st = i0 + i < 32 ? first : stats(i0 + i);
+                const float g = exp2f(st.x - base) * inv;
+                fac[i][warp] = make_float2(g * (c1 - (st.w - s0)), g);
             }
         __syncthreads();
-        if (r < h.rows) {
+        if (mine) {
 #pragma unroll 4
             for (int i = lane; i < n; i += kLanes) {
-                const float2 f = fac[i * R + r];
-                const float4* o = part_sums(w, blockIdx.x + i0 + i, i0 + i == 0, D) + item;
-                const float4 x = o[0], y = o[R * D / 4];
-                acc.x = fmaf(f.x, x.x, fmaf(-f.y, y.x, acc.x));
-                acc.y = fmaf(f.x, x.y, fmaf(-f.y, y.y, acc.y));
-                acc.z = fmaf(f.x, x.z, fmaf(-f.y, y.z, acc.z));
-                acc.w = fmaf(f.x, x.w, fmaf(-f.y, y.w, acc.w));
+                const float2 g = fac[i][r];
+                const float4* o = part_sums(w, blockIdx.x + i0 + i, i0 + i == 0, D) + (size_t)c4 * R + row0 + r;
+                const float4 x = o[0], y = o[(size_t)(D / 4) * R];
+                acc.x = fmaf(g.x, x.x, fmaf(-g.y, y.x, acc.x));
+                acc.y = fmaf(g.x, x.y, fmaf(-g.y, y.y, acc.y));
+                acc.z = fmaf(g.x, x.z, fmaf(-g.y, y.z, acc.z));
+                acc.w = fmaf(g.x, x.w, fmaf(-g.y, y.w, acc.w));
             }
         }
         __syncthreads();
@@ -305,13 +325,9 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(Work w, T* __restrict_
                 acc.w += x.w;
             }
     }
-    if (lane == 0 && r < h.rows) {
-        const int fr = h.row0 + r;
-        T* o = out + ((long long)(h.token0 + over_g(w, fr)) * Hq + h.head * w.G + (fr - over_g(w, fr) * w.G)) * D + item / R * 4;
-        put(o, acc.x);
-        put(o + 1, acc.y);
-        put(o + 2, acc.z);
-        put(o + 3, acc.w);
+    if (lane == 0 && mine) {
+        const int fr = h.row0 + row0 + r, tk = over_g(w, fr);
+        put4(out + ((long long)(h.token0 + tk) * Hq + h.head * w.G + fr - tk * w.G) * D + c4 * 4, acc);
     }
 }
 
@@ -321,8 +337,7 @@ cudaError_t launch_one(const SimtArgs& a, cudaStream_t stream) {
     auto* kern = paged_simt_kernel<T, D, R>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kern<<<a.w.ctas, kThreads, smem, stream>>>(a);
-    return cudaGetLastError();
+    return launch_after(kern, dim3(a.w.ctas), kThreads, smem, stream, a);
 }
 
 template <typename T>
@@ -338,18 +353,8 @@ cudaError_t launch_typed(const SimtArgs& a, int d, cudaStream_t stream) {
 
 template <typename T, int D, int R>
 cudaError_t merge_one(const Work& w, void* out, int Hq, cudaStream_t stream) {
-    constexpr int kItems = R * D / 4 >= 1024 ? 256 : R * D / 4 >= 256 ? 64 : 32;
-    static_assert(R * D / 4 % kItems == 0, "whole blocks");
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(w.ctas, R * D / 4 / kItems);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, paged_merge_kernel<T, D, R>, w, static_cast<T*>(out), Hq);
+    return launch_after(paged_merge_kernel<T, D, R>, dim3(w.ctas, MergeShape<D, R>::kBlocks), 256, 0, stream, w,
+                        static_cast<T*>(out), Hq);
 }
 
 template <typename T, int D>

@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(&b.tmem, Sh::kTmem);
         tmem_relinquish();
     }
+    cudaGridDependencySynchronize();           // the lengths may be the previous kernel's
     Walk wk = begin_walk(w, blockIdx.x, scratch);
     cudaTriggerProgrammaticLaunchCompletion();   // the merge waits for this grid's end all the same
     tc_fence_before();
@@ -582,8 +583,7 @@ cudaError_t launch_tc(const TcArgs& a, const CUtensorMap& mk, const CUtensorMap&
     constexpr size_t smem = TcShape<D>::smem;
     cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    paged_tc_kernel<D><<<a.w.ctas, kThreads, smem, stream>>>(a, mk, mv);
-    return cudaGetLastError();
+    return launch_after(paged_tc_kernel<D>, dim3(a.w.ctas), kThreads, smem, stream, a, mk, mv);
 }
 
 }  // namespace
