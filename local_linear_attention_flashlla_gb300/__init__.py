@@ -611,24 +611,23 @@ def paged_plan(ctx_lens, new_lens, block_table, free_pages, free_count, page_siz
     ctx_ptr, new_ptr = _ints("ctx_lens", ctx_lens, (S,), i32, dev), _ints("new_lens", new_lens, (S,), i32, dev)
     table_ptr = _ints("block_table", block_table, (S, W), i32, dev)
     free_ptr, count_ptr = _ints("free_pages", free_pages, (F,), i32, dev), _ints("free_count", free_count, (1,), i32, dev)
-    empty = torch.empty
-    if kv_lens is None:
-        kv_lens = empty(S, dtype=i32, device=dev)
-    if cu_q is None:
-        cu_q = empty(S + 1, dtype=i32, device=dev)
+    given = (kv_lens, cu_q, granted, free_left, positions)
+    kv_lens, cu_q, granted, free_left, positions = (
+        torch.empty(n, dtype=i32, device=dev) if t is None else t for t, n in zip(given, (S, S + 1, S, 1, T)))
+    if any(t is not None for t in given):
+        for name, t, n in (("kv_lens", kv_lens, S), ("cu_q", cu_q, S + 1), ("granted", granted, S),
+                           ("free_left", free_left, 1), ("positions", positions, T)):
+            _ints(name, t, (n,), i32, dev)
     if slots is None:
-        slots = empty(T, dtype=i64, device=dev)
-    if positions is None:
-        positions = empty(T, dtype=i32, device=dev)
-    if granted is None:
-        granted = empty(S, dtype=i32, device=dev)
-    if free_left is None:
-        free_left = empty(1, dtype=i32, device=dev)
-    lla_paged_plan(ctx_ptr, new_ptr, S, int(page_size), table_ptr, W, free_ptr, F, count_ptr, T,
-                   _ints("kv_lens", kv_lens, (S,), i32, dev), _ints("cu_q", cu_q, (S + 1,), i32, dev),
-                   _ints("slots", slots, (T,), i64, dev), _ints("positions", positions, (T,), i32, dev),
-                   _ints("granted", granted, (S,), i32, dev), _ints("free_left", free_left, (1,), i32, dev),
-                   torch._C._cuda_getCurrentRawStream(dev.index))
+        slots = torch.empty(T, dtype=i64, device=dev)
+    else:
+        _ints("slots", slots, (T,), i64, dev)
+    status = load_library().lla_paged_plan(
+        ctx_ptr, new_ptr, S, int(page_size), table_ptr, W, free_ptr, F, count_ptr, T, kv_lens.data_ptr(), cu_q.data_ptr(),
+        slots.data_ptr(), positions.data_ptr(), granted.data_ptr(), free_left.data_ptr(),
+        torch._C._cuda_getCurrentRawStream(dev.index))
+    if status != LLA_OK:
+        _check(status)
     return PagedPlan(kv_lens, cu_q, slots, positions, granted, free_left)
 
 
@@ -647,9 +646,11 @@ def paged_append(k_new, v_new, slots, k_cache, v_cache, *, stream=None):
     k_new, ks = _token_rows(k_new, "k_new", k_cache, Hkv, d)
     v_new, vs = _token_rows(v_new, "v_new", k_cache, Hkv, d)
     T = k_new.shape[0]
-    lla_paged_append(dtype, k_new.data_ptr(), v_new.data_ptr(), _ints("slots", slots, (T,), torch.int64, dev),
-                     k_cache.data_ptr(), v_cache.data_ptr(), T, Hkv, d, Z, P, ks, vs, page_stride,
-                     torch._C._cuda_getCurrentRawStream(dev.index))
+    status = load_library().lla_paged_append(
+        dtype, k_new.data_ptr(), v_new.data_ptr(), _ints("slots", slots, (T,), torch.int64, dev), k_cache.data_ptr(),
+        v_cache.data_ptr(), T, Hkv, d, Z, P, ks, vs, page_stride, torch._C._cuda_getCurrentRawStream(dev.index))
+    if status != LLA_OK:
+        _check(status)
 
 
 def paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, max_new, *, causal=True,
@@ -695,7 +696,10 @@ def paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, 
         raise _bad(f"workspace must be a contiguous tensor on {dev}")
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
-    lla_paged_parallax(dtype, path, q.data_ptr(), probe.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table_ptr,
-                       cu_ptr, kv_ptr, out.data_ptr(), T, S, Hq, Hkv, d, Z, P, W, max_new, qs, rs, page_stride, float(tau),
-                       1 if causal else 0, workspace.data_ptr(), ws_bytes, torch._C._cuda_getCurrentRawStream(dev.index))
+    status = load_library().lla_paged_parallax(
+        dtype, path, q.data_ptr(), probe.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table_ptr, cu_ptr, kv_ptr,
+        out.data_ptr(), T, S, Hq, Hkv, d, Z, P, W, max_new, qs, rs, page_stride, float(tau), 1 if causal else 0,
+        workspace.data_ptr(), ws_bytes, torch._C._cuda_getCurrentRawStream(dev.index))
+    if status != LLA_OK:
+        _check(status)
     return out

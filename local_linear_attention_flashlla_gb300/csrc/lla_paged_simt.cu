@@ -30,15 +30,6 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, float4 x) {
     *reinterpret_cast<uint2*>(p) = *reinterpret_cast<uint2*>(y);
 }
 
-// 16 bytes of T as floats.
-template <typename T>
-__device__ __forceinline__ void load16(const T* g, float* dst) {
-    const uint4 raw = *reinterpret_cast<const uint4*>(g);
-    const T* e = reinterpret_cast<const T*>(&raw);
-#pragma unroll
-    for (int i = 0; i < (int)(16 / sizeof(T)); ++i) dst[i] = to_f(e[i]);
-}
-
 constexpr int kThreads = 256;
 
 // R rows of a tile, TX threads to a row (they lie in one warp), BN keys of a block.
@@ -47,9 +38,11 @@ struct Shape {
     static constexpr int TX = kThreads / R;
     static constexpr int BN = R == 32 ? 32 : 64;
     static constexpr int KPT = BN / TX;                 // keys of a thread
-    static constexpr int CPT = (D + TX - 1) / TX;       // output columns of a thread
-    static constexpr int KS = D + 4;                    // row stride of K: float4 reads of TX rows do not collide
-    static constexpr size_t smem = sizeof(float) * (2 * R * D + BN * KS + BN * D + 2 * R * BN);
+    static constexpr int CPT = (D + TX - 1) / TX;       // output columns of a thread,
+    static constexpr int VW = CPT < 4 ? CPT : 4;        // this many side by side
+    static constexpr int KS = D + 4;                    // row strides of K and of the weights: the float4 reads of
+    static constexpr int PS = BN + 4;                   // a warp's rows do not collide
+    static constexpr size_t smem = sizeof(float) * (2 * R * D + BN * KS + BN * D + 2 * R * PS);
 };
 
 struct SimtArgs {
@@ -67,7 +60,9 @@ struct SimtArgs {
 template <typename T, int D, int R>
 __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
     using Sh = Shape<D, R>;
-    constexpr int TX = Sh::TX, BN = Sh::BN, KPT = Sh::KPT, CPT = Sh::CPT, KS = Sh::KS, VE = 16 / sizeof(T);
+    constexpr int TX = Sh::TX, BN = Sh::BN, KPT = Sh::KPT, CPT = Sh::CPT, VW = Sh::VW, KS = Sh::KS, PS = Sh::PS;
+    constexpr int VE = 16 / sizeof(T);                  // elements of a 16-byte piece
+    constexpr int PPT = (BN * D / VE + kThreads - 1) / kThreads;   // pieces of K (and of V) that a thread loads
     extern __shared__ __align__(16) float sm[];
     __shared__ long long scratch[40];
     float* Qs = sm;
@@ -75,7 +70,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
     float* Ks = Rs + R * D;
     float* Vs = Ks + BN * KS;
     float* P1 = Vs + BN * D;
-    float* P2 = P1 + R * BN;
+    float* P2 = P1 + R * PS;
     const Work& w = a.w;
     const int tid = threadIdx.x, row = tid / TX, tx = tid % TX;
     const T* gq = static_cast<const T*>(a.q);
@@ -89,24 +84,51 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
     Piece p;
     p.parts = 0; p.row0 = p.rows = p.h = 0; p.q.token0 = 0;
     bool shared = false;
-    while (next_piece(w, wk, p)) {
-        shared = p.slot == 1;
-        for (int e = tid; e < R * (D / VE); e += kThreads) {
-            const int r = e / (D / VE), c = (e % (D / VE)) * VE;
-            float* dq = Qs + r * D + c;
-            float* dr = Rs + r * D + c;
-            if (r < p.rows) {
-                const int fr = p.row0 + r, token = p.q.token0 + over_g(w, fr), head = p.h * w.G + (fr - over_g(w, fr) * w.G);
-                load16(gq + token * a.q_stride + (long long)head * D + c, dq);
-                load16(gr + token * a.r_stride + (long long)head * D + c, dr);
-            } else {
+    // a block of K and V on its way: loaded into registers while the block before is computed
+    uint4 kraw[PPT], vraw[PPT];
+    auto fetch = [&](int j) {
 #pragma unroll
-                for (int i = 0; i < VE; ++i) dq[i] = dr[i] = 0.f;
+        for (int i = 0; i < PPT; ++i) {
+            const int e = tid + i * kThreads, kk = e / (D / VE), c = (e % (D / VE)) * VE, key = j * BN + kk;
+            kraw[i] = vraw[i] = make_uint4(0, 0, 0, 0);  // keys that no row sees: zeros, whatever the page holds
+            if (e < BN * (D / VE) && key < p.keys) {
+                const int page = w.table[(size_t)p.s * w.width + (key >> w.page_shift)];
+                if (page < 0 || page >= w.num_pages) {
+                    atomicOr(w.err, (unsigned)kDevErrPagedArg);
+                } else {
+                    const long long off = page * a.page_stride +
+                        (((long long)p.h << w.page_shift) + (key & ((1 << w.page_shift) - 1))) * D + c;
+                    kraw[i] = *reinterpret_cast<const uint4*>(gk + off);
+                    vraw[i] = *reinterpret_cast<const uint4*>(gv + off);
+                }
             }
         }
+    };
+    auto unpack = [&](const uint4& raw, float* dst) {
+        const T* e = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+        for (int i = 0; i < VE; i += 4)
+            *reinterpret_cast<float4*>(dst + i) = make_float4(to_f(e[i]), to_f(e[i + 1]), to_f(e[i + 2]), to_f(e[i + 3]));
+    };
+
+    while (next_piece(w, wk, p)) {
+        shared = p.slot == 1;
+        if (p.j0 < p.j1) fetch(p.j0);
+        for (int e = tid; e < R * (D / VE); e += kThreads) {
+            const int r = e / (D / VE), c = (e % (D / VE)) * VE;
+            uint4 x = make_uint4(0, 0, 0, 0), y = x;
+            if (r < p.rows) {
+                const int fr = p.row0 + r, tk = over_g(w, fr);
+                const long long token = p.q.token0 + tk, hc = (long long)(p.h * w.G + fr - tk * w.G) * D + c;
+                x = *reinterpret_cast<const uint4*>(gq + token * a.q_stride + hc);
+                y = *reinterpret_cast<const uint4*>(gr + token * a.r_stride + hc);
+            }
+            unpack(x, Qs + r * D + c);
+            unpack(y, Rs + r * D + c);
+        }
         int limit = 0;                                   // keys this row sees
-        if (row < p.rows)
-            limit = w.causal ? min(max(p.q.L - p.q.nq + over_g(w, p.row0 + row) + 1, 0), p.q.L) : p.q.L;
+        if (row < p.rows) limit = w.causal ? min(max(p.q.L - p.q.nq + over_g(w, p.row0 + row) + 1, 0), p.q.L) : p.q.L;
+        const bool busy = __any_sync(0xffffffffu, row < p.rows);   // a warp without rows only helps to load
         float m = -INFINITY, om = 0.f, A = 0.f, s0 = 0.f;
         float o1[CPT], o2[CPT];
 #pragma unroll
@@ -114,92 +136,97 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
 
         for (int j = p.j0; j < p.j1; ++j) {
             const int key0 = j * BN;
-            for (int e = tid; e < BN * (D / VE); e += kThreads) {
-                const int kk = e / (D / VE), c = (e % (D / VE)) * VE, key = key0 + kk;
-                float* dk = Ks + kk * KS + c;
-                float* dv = Vs + kk * D + c;
-                int page = -1;
-                if (key < p.keys) {
-                    page = w.table[(size_t)p.s * w.width + (key >> w.page_shift)];
-                    if (page < 0 || page >= w.num_pages) {
-                        page = -1;
-                        atomicOr(w.err, (unsigned)kDevErrPagedArg);
-                    }
-                }
-                if (page >= 0) {
-                    const long long off = page * a.page_stride +
-                        (((long long)p.h << w.page_shift) + (key & ((1 << w.page_shift) - 1))) * D + c;
-                    load16(gk + off, dk);
-                    load16(gv + off, dv);
-                } else {                                 // keys that no row sees: zeros, whatever the page holds
 #pragma unroll
-                    for (int i = 0; i < VE; ++i) dk[i] = dv[i] = 0.f;
+            for (int i = 0; i < PPT; ++i) {
+                const int e = tid + i * kThreads, kk = e / (D / VE), c = (e % (D / VE)) * VE;
+                if (e < BN * (D / VE)) {
+                    unpack(kraw[i], Ks + kk * KS + c);
+                    unpack(vraw[i], Vs + kk * D + c);
                 }
             }
             __syncthreads();
-            float s[KPT], t[KPT];
+            if (j + 1 < p.j1) fetch(j + 1);
+            if (busy) {
+                float s[KPT], t[KPT];
 #pragma unroll
-            for (int u = 0; u < KPT; ++u) s[u] = t[u] = 0.f;
+                for (int u = 0; u < KPT; ++u) s[u] = t[u] = 0.f;
 #pragma unroll 4
-            for (int c = 0; c < D; c += 4) {
-                const float4 q4 = *reinterpret_cast<const float4*>(Qs + row * D + c);
-                const float4 r4 = *reinterpret_cast<const float4*>(Rs + row * D + c);
+                for (int c = 0; c < D; c += 4) {
+                    const float4 q4 = *reinterpret_cast<const float4*>(Qs + row * D + c);
+                    const float4 r4 = *reinterpret_cast<const float4*>(Rs + row * D + c);
+#pragma unroll
+                    for (int u = 0; u < KPT; ++u) {
+                        const float4 k4 = *reinterpret_cast<const float4*>(Ks + (tx + TX * u) * KS + c);
+                        s[u] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[u]))));
+                        t[u] = fmaf(r4.x, k4.x, fmaf(r4.y, k4.y, fmaf(r4.z, k4.z, fmaf(r4.w, k4.w, t[u]))));
+                    }
+                }
+                float bm = -INFINITY;
 #pragma unroll
                 for (int u = 0; u < KPT; ++u) {
-                    const float4 k4 = *reinterpret_cast<const float4*>(Ks + (tx + TX * u) * KS + c);
-                    s[u] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[u]))));
-                    t[u] = fmaf(r4.x, k4.x, fmaf(r4.y, k4.y, fmaf(r4.z, k4.z, fmaf(r4.w, k4.w, t[u]))));
+                    s[u] = key0 + tx + TX * u < limit ? s[u] * a.scale : -INFINITY;
+                    bm = fmaxf(bm, s[u]);
                 }
-            }
-            float bm = -INFINITY;
 #pragma unroll
-            for (int u = 0; u < KPT; ++u) {
-                s[u] = key0 + tx + TX * u < limit ? s[u] * a.scale : -INFINITY;
-                bm = fmaxf(bm, s[u]);
-            }
+                for (int o = TX / 2; o; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
+                const float mn = fmaxf(m, bm);
+                const float base = mn == -INFINITY ? 0.f : mn;
+                const float corr = exp2f(m - base);      // m = -inf: 0
+                float ps = 0.f, pt = 0.f;
 #pragma unroll
-            for (int o = TX / 2; o; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
-            const float mn = fmaxf(m, bm);
-            const float base = mn == -INFINITY ? 0.f : mn;
-            const float corr = exp2f(m - base);          // m = -inf: 0
-            float ps = 0.f, pt = 0.f;
+                for (int u = 0; u < KPT; ++u) {
+                    s[u] = exp2f(s[u] - base);
+                    ps += s[u];
+                    pt = fmaf(s[u], t[u], pt);
+                }
 #pragma unroll
-            for (int u = 0; u < KPT; ++u) {
-                s[u] = exp2f(s[u] - base);
-                ps += s[u];
-                pt = fmaf(s[u], t[u], pt);
-            }
+                for (int o = TX / 2; o; o >>= 1) {
+                    ps += __shfl_xor_sync(0xffffffffu, ps, o);
+                    pt += __shfl_xor_sync(0xffffffffu, pt, o);
+                }
+                if (om == 0.f && ps > 0.f) s0 = pt / ps; // the row's first block with keys
+                m = mn;
+                om = om * corr + ps;
+                A = A * corr + (pt - s0 * ps);
 #pragma unroll
-            for (int o = TX / 2; o; o >>= 1) {
-                ps += __shfl_xor_sync(0xffffffffu, ps, o);
-                pt += __shfl_xor_sync(0xffffffffu, pt, o);
-            }
-            if (om == 0.f && ps > 0.f) s0 = pt / ps;     // the row's first block with keys
-            m = mn;
-            om = om * corr + ps;
-            A = A * corr + (pt - s0 * ps);
-#pragma unroll
-            for (int u = 0; u < KPT; ++u) {
-                P1[row * BN + tx + TX * u] = s[u];
-                P2[row * BN + tx + TX * u] = s[u] * (t[u] - s0);
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < CPT; ++i) {
-                o1[i] *= corr;
-                o2[i] *= corr;
-            }
-#pragma unroll 4
-            for (int kk = 0; kk < BN; ++kk) {
-                const float a1 = P1[row * BN + kk], a2 = P2[row * BN + kk];
+                for (int u = 0; u < KPT; ++u) {
+                    P1[row * PS + tx + TX * u] = s[u];
+                    P2[row * PS + tx + TX * u] = s[u] * (t[u] - s0);
+                }
+                __syncwarp();
 #pragma unroll
                 for (int i = 0; i < CPT; ++i) {
-                    const int c = tx + TX * i;
-                    if (D % TX == 0 || c < D) {
-                        const float x = Vs[kk * D + c];
-                        o1[i] = fmaf(a1, x, o1[i]);
-                        o2[i] = fmaf(a2, x, o2[i]);
-                    }
+                    o1[i] *= corr;
+                    o2[i] *= corr;
+                }
+#pragma unroll 2
+                for (int kk = 0; kk < BN; kk += 4) {
+                    const float4 w1 = *reinterpret_cast<const float4*>(P1 + row * PS + kk);
+                    const float4 w2 = *reinterpret_cast<const float4*>(P2 + row * PS + kk);
+                    const float a1[4] = {w1.x, w1.y, w1.z, w1.w}, a2[4] = {w2.x, w2.y, w2.z, w2.w};
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int g = 0; g < CPT / VW; ++g) {
+                            const int c = (tx + TX * g) * VW;
+                            float v[VW];
+                            if (D % TX == 0 || c < D) {
+                                if constexpr (VW == 4) {
+                                    const float4 y = *reinterpret_cast<const float4*>(Vs + (kk + x) * D + c);
+                                    v[0] = y.x; v[1] = y.y; v[2] = y.z; v[3] = y.w;
+                                } else if constexpr (VW == 2) {
+                                    const float2 y = *reinterpret_cast<const float2*>(Vs + (kk + x) * D + c);
+                                    v[0] = y.x; v[1] = y.y;
+                                } else {
+                                    v[0] = Vs[(kk + x) * D + c];
+                                }
+#pragma unroll
+                                for (int i = 0; i < VW; ++i) {
+                                    o1[g * VW + i] = fmaf(a1[x], v[i], o1[g * VW + i]);
+                                    o2[g * VW + i] = fmaf(a2[x], v[i], o2[g * VW + i]);
+                                }
+                            }
+                        }
                 }
             }
             __syncthreads();
@@ -211,17 +238,21 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
                 T* o = static_cast<T*>(a.out) + ((long long)token * a.Hq + head) * D;
                 const float inv = om != 0.f ? 1.f / om : 0.f, c1 = 1.f + A * inv;
 #pragma unroll
-                for (int i = 0; i < CPT; ++i)
-                    if (D % TX == 0 || tx + TX * i < D) put(o + tx + TX * i, (c1 * o1[i] - o2[i]) * inv);
+                for (int i = 0; i < CPT; ++i) {
+                    const int c = (tx + TX * (i / VW)) * VW + i % VW;
+                    if (D % TX == 0 || c < D) put(o + c, (c1 * o1[i] - o2[i]) * inv);
+                }
             } else {
                 if (tx == 0) part_stats(w, blockIdx.x, p.slot, D)[row] = make_float4(m, om, A, s0);
                 float4* ps = part_sums(w, blockIdx.x, p.slot, D);
 #pragma unroll
-                for (int i = 0; i < CPT; ++i)
-                    if (D % TX == 0 || tx + TX * i < D) {
-                        *part_element(ps, R, D, 0, row, tx + TX * i) = o1[i];
-                        *part_element(ps, R, D, 1, row, tx + TX * i) = o2[i];
+                for (int i = 0; i < CPT; ++i) {
+                    const int c = (tx + TX * (i / VW)) * VW + i % VW;
+                    if (D % TX == 0 || c < D) {
+                        *part_element(ps, R, D, 0, row, c) = o1[i];
+                        *part_element(ps, R, D, 1, row, c) = o2[i];
                     }
+                }
             }
         }
         __syncthreads();
@@ -384,7 +415,7 @@ cudaError_t merge_typed(const Work& w, void* out, int Hq, int d, cudaStream_t st
 PagedSplit paged_simt_split(const PagedProblem& p, int sms) {
     // rows: 8 where no sequence has more than eight query rows to a key head (a decode step), else 32
     const bool few = (long long)p.max_new * p.G <= 8;
-    return PagedSplit{few ? 8 : 32, few ? 64 : 32, 2 * sms, few ? 2 : 4};
+    return PagedSplit{few ? 8 : 32, few ? 64 : 32, 2 * sms, 2};
 }
 
 cudaError_t launch_paged_simt(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream) {
