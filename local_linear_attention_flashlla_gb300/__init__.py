@@ -537,6 +537,11 @@ def _ints(name, t, shape, dtype, device):
     return t.data_ptr()
 
 
+def _same(name, t, shape, dtype, device):
+    _ints(name, t, shape, dtype, device)
+    return t
+
+
 def _check_caches(k_cache, v_cache):
     """(num_pages, Hkv, page_size, d, page stride, lla dtype) of two caches laid out alike."""
     import torch
@@ -586,6 +591,26 @@ def _paged_workspace_bytes(device_index, dtype, path, Hq, Hkv, d, page_size, max
     return lla_paged_parallax_workspace_size(dtype, path, 1, 1, Hq, Hkv, d, page_size, 1, max_new)
 
 
+# Scratch of eager attention calls by (device, stream): calls on one stream follow one another, so they can share
+# it, and taking it from the allocator costs as much as all checks.  A call under graph capture takes its own
+# (the graph keeps it), so that graphs never share scratch with anything.  At most eight are kept.
+_SCRATCH = {}
+
+
+def _scratch(device, stream_ptr, nbytes):
+    import torch
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    key = (device.index, stream_ptr)
+    t = _SCRATCH.get(key)
+    if t is None or t.numel() < nbytes:
+        _SCRATCH.pop(key, None)
+        while len(_SCRATCH) >= 8:
+            _SCRATCH.pop(next(iter(_SCRATCH)), None)
+        t = _SCRATCH[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return t
+
+
 def paged_plan(ctx_lens, new_lens, block_table, free_pages, free_count, page_size, num_rows, *, kv_lens=None, cu_q=None,
                slots=None, positions=None, granted=None, free_left=None, stream=None):
     """Pages and slots for a step's new tokens, from the requests' lengths, on the GPU (include/lla.h,
@@ -611,17 +636,13 @@ def paged_plan(ctx_lens, new_lens, block_table, free_pages, free_count, page_siz
     ctx_ptr, new_ptr = _ints("ctx_lens", ctx_lens, (S,), i32, dev), _ints("new_lens", new_lens, (S,), i32, dev)
     table_ptr = _ints("block_table", block_table, (S, W), i32, dev)
     free_ptr, count_ptr = _ints("free_pages", free_pages, (F,), i32, dev), _ints("free_count", free_count, (1,), i32, dev)
-    given = (kv_lens, cu_q, granted, free_left, positions)
-    kv_lens, cu_q, granted, free_left, positions = (
-        torch.empty(n, dtype=i32, device=dev) if t is None else t for t, n in zip(given, (S, S + 1, S, 1, T)))
-    if any(t is not None for t in given):
-        for name, t, n in (("kv_lens", kv_lens, S), ("cu_q", cu_q, S + 1), ("granted", granted, S),
-                           ("free_left", free_left, 1), ("positions", positions, T)):
-            _ints(name, t, (n,), i32, dev)
-    if slots is None:
-        slots = torch.empty(T, dtype=i64, device=dev)
-    else:
-        _ints("slots", slots, (T,), i64, dev)
+    empty, like = torch.empty, torch.empty_like
+    kv_lens = like(ctx_lens) if kv_lens is None else _same("kv_lens", kv_lens, (S,), i32, dev)
+    granted = like(ctx_lens) if granted is None else _same("granted", granted, (S,), i32, dev)
+    free_left = like(free_count) if free_left is None else _same("free_left", free_left, (1,), i32, dev)
+    cu_q = empty(S + 1, dtype=i32, device=dev) if cu_q is None else _same("cu_q", cu_q, (S + 1,), i32, dev)
+    slots = empty(T, dtype=i64, device=dev) if slots is None else _same("slots", slots, (T,), i64, dev)
+    positions = empty(T, dtype=i32, device=dev) if positions is None else _same("positions", positions, (T,), i32, dev)
     status = load_library().lla_paged_plan(
         ctx_ptr, new_ptr, S, int(page_size), table_ptr, W, free_ptr, F, count_ptr, T, kv_lens.data_ptr(), cu_q.data_ptr(),
         slots.data_ptr(), positions.data_ptr(), granted.data_ptr(), free_left.data_ptr(),
@@ -661,8 +682,9 @@ def paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, 
     block_table [S, W], cu_q [S+1], kv_lens [S]: int32 CUDA tensors (paged_plan's); max_new: the most
     tokens of one sequence in this step.  causal=False: every row sees all of its sequence's keys.
     Returns out [T, Hq, d]; rows behind the last sequence are left as they were.  Asynchronous on the
-    current (or given) stream.  workspace: None (taken from torch's allocator), or a uint8 CUDA tensor of
-    lla_paged_parallax_workspace_size(...) bytes.
+    current (or given) stream.  workspace: None (scratch kept per stream; under graph capture the graph's
+    own), or a CUDA tensor of lla_paged_parallax_workspace_size(...) bytes that no other call uses at the
+    same time.
     """
     import torch
     P, Hkv, Z, d, page_stride, dtype = _check_caches(k_cache, v_cache)
@@ -688,9 +710,9 @@ def paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, 
         out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
     elif out.shape != q.shape or out.dtype is not q.dtype or out.device != dev or not out.is_contiguous():
         raise _bad(f"out must be a contiguous {q.dtype} tensor of shape {tuple(q.shape)} on {dev}")
+    stream_ptr = torch._C._cuda_getCurrentRawStream(dev.index)
     if workspace is None:
-        workspace = torch.empty(_paged_workspace_bytes(dev.index, dtype, path, Hq, Hkv, d, Z, max_new),
-                                dtype=torch.uint8, device=dev)
+        workspace = _scratch(dev, stream_ptr, _paged_workspace_bytes(dev.index, dtype, path, Hq, Hkv, d, Z, max_new))
         ws_bytes = workspace.numel()
     elif workspace.device != dev or not workspace.is_contiguous():
         raise _bad(f"workspace must be a contiguous tensor on {dev}")
@@ -699,7 +721,7 @@ def paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, 
     status = load_library().lla_paged_parallax(
         dtype, path, q.data_ptr(), probe.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table_ptr, cu_ptr, kv_ptr,
         out.data_ptr(), T, S, Hq, Hkv, d, Z, P, W, max_new, qs, rs, page_stride, float(tau), 1 if causal else 0,
-        workspace.data_ptr(), ws_bytes, torch._C._cuda_getCurrentRawStream(dev.index))
+        workspace.data_ptr(), ws_bytes, stream_ptr)
     if status != LLA_OK:
         _check(status)
     return out
