@@ -385,7 +385,7 @@ int lla_paged_plan(const int* ctx_lens, const int* new_lens, int S, int page_siz
  *               num_pages * page_size is skipped and reported by lla_sync_status.  Two rows must not
  *               have the same slot.
  * k_cache, v_cache  [num_pages, Hkv, page_size, d] in dtype, pages page_stride elements apart
- *               (>= Hkv*page_size*d, a multiple of 16 bytes).
+ *               (>= Hkv*page_size*d, a multiple of page_size*d).
  * Pointers 16-byte aligned; d in {16, 32, 64, 128}.  Asynchronous on `stream`, one launch, no scratch.
  */
 int lla_paged_append(int dtype, const void* k_new, const void* v_new, const long long* slots, void* k_cache,

@@ -338,8 +338,10 @@ int lla_paged_append(int dtype, const void* k_new, const void* v_new, const long
     const int es = dtype == LLA_DTYPE_BF16 ? 2 : 4, ve = 16 / es;
     if (k_stride < (long long)Hkv * d || v_stride < (long long)Hkv * d || k_stride % ve || v_stride % ve)
         return failf(LLA_ERR_INVALID_ARG, "token strides must be >= Hkv*d and multiples of 16 bytes");
-    if (page_stride < (long long)Hkv * page_size * d || page_stride % ve)
-        return failf(LLA_ERR_INVALID_ARG, "page_stride must be >= Hkv*page_size*d and a multiple of 16 bytes");
+    if (page_stride < (long long)Hkv * page_size * d || page_stride % ((long long)page_size * d))
+        return failf(LLA_ERR_INVALID_ARG, "page_stride must be >= Hkv*page_size*d and a multiple of page_size*d");
+    if (page_stride / ((long long)page_size * d) * num_pages > INT_MAX)
+        return failf(LLA_ERR_INVALID_ARG, "problem too large (head slices of the cache must number < 2^31)");
     unsigned* err = lla::device_error_word();
     if (!err) return failf(LLA_ERR_CUDA, "lla_paged_append: device error word not found");
     lla::AppendArgs a{static_cast<const char*>(k_new), static_cast<const char*>(v_new), slots,
@@ -384,8 +386,10 @@ int lla_paged_parallax(int dtype, int path, const void* q, const void* probe, co
     const int es = dtype == LLA_DTYPE_BF16 ? 2 : 4, ve = 16 / es;
     if (q_stride < (long long)Hq * d || probe_stride < (long long)Hq * d || q_stride % ve || probe_stride % ve)
         return failf(LLA_ERR_INVALID_ARG, "token strides must be >= Hq*d and multiples of 16 bytes");
-    if (page_stride < (long long)Hkv * page_size * d || page_stride % ve)
-        return failf(LLA_ERR_INVALID_ARG, "page_stride must be >= Hkv*page_size*d and a multiple of 16 bytes");
+    if (page_stride < (long long)Hkv * page_size * d || page_stride % ((long long)page_size * d))
+        return failf(LLA_ERR_INVALID_ARG, "page_stride must be >= Hkv*page_size*d and a multiple of page_size*d");
+    if (page_stride / ((long long)page_size * d) * num_pages > INT_MAX)
+        return failf(LLA_ERR_INVALID_ARG, "problem too large (head slices of the cache must number < 2^31)");
 
     lla::PagedProblem p{};
     p.q = q; p.probe = probe; p.k = k_cache; p.v = v_cache; p.table = block_table; p.cu_q = cu_q; p.kv_lens = kv_lens;

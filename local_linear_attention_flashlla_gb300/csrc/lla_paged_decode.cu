@@ -29,7 +29,7 @@ constexpr int kThreads = (kWarps + 1) * 32;
 template <int D>
 struct DecShape {
     static constexpr int kStages = D == 128 ? 3 : 6;
-    static constexpr int kTile = kKeys * D * 2;            // bytes of a K (or V) block: [D / 64][64 rows][128 B]
+    static constexpr int kTile = kKeys * D * 2;            // bytes of a K (or V) block
     static constexpr int kScratch = 8192;                  // joining the warps' sums
     static constexpr size_t smem = (size_t)kStages * 2 * kTile + kScratch + 1024;   // 1024: alignment of the ring
 };
@@ -39,7 +39,7 @@ struct DecArgs {
     const __nv_bfloat16* q;
     const __nv_bfloat16* probe;
     __nv_bfloat16* out;
-    int Hq;
+    int Hq, slices;                            // slices: head slices from page to page
     long long q_stride, r_stride;
     float scale;                               // tau log2(e)
 };
@@ -59,15 +59,10 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Byte offset of 16-byte piece c of row r in a block ([D / 64][64 rows][128 B], 128-byte swizzle).
-__device__ __forceinline__ uint32_t piece_off(int r, int c) {
-    return (uint32_t)((c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-}
-
 // The feeding warp: one block after another of this CTA's pieces, a box to a lane.
 template <int D>
-__device__ void feed(const Work& w, Walk wk, const CUtensorMap* mk, const CUtensorMap* mv, uint32_t ring, uint64_t* full,
-                     uint64_t* empty, volatile int* err) {
+__device__ void feed(const Work& w, Walk wk, const CUtensorMap* mk, const CUtensorMap* mv, int slices, uint32_t ring,
+                     uint64_t* full, uint64_t* empty, volatile int* err) {
     constexpr int kStages = DecShape<D>::kStages, kTile = DecShape<D>::kTile;
     const int lane = threadIdx.x & 31;
     const int box = min(1 << w.page_shift, kBoxRows);        // rows of a box
@@ -87,13 +82,10 @@ __device__ void feed(const Work& w, Walk wk, const CUtensorMap* mk, const CUtens
             if (lane == 0) tc::mbar_arrive_expect_tx(&full[stage], (uint32_t)(count * box * D * 4));
             __syncwarp();
             if (mine) {
-                const uint32_t dst = ring + (uint32_t)(stage * 2 * kTile + lane * box * 128);
-                const int y = key & ((1 << w.page_shift) - 1);
-#pragma unroll
-                for (int x = 0; x < D / 64; ++x) {
-                    tma_load_4d(dst + x * (kKeys * 128), mk, &full[stage], x * 64, y, p.h, page);
-                    tma_load_4d(dst + kTile + x * (kKeys * 128), mv, &full[stage], x * 64, y, p.h, page);
-                }
+                const uint32_t dst = ring + (uint32_t)(stage * 2 * kTile + lane * box * D * 2);
+                const int group = (key & ((1 << w.page_shift) - 1)) >> 3, slice = page * slices + p.h;
+                tma_load_rows(dst, mk, &full[stage], group, slice);
+                tma_load_rows(dst + kTile, mv, &full[stage], group, slice);
             }
             __syncwarp();
             ++issued;
@@ -145,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
 
     if (warp == kWarps) {
-        feed<D>(w, wk, &mk, &mv, ring, full, empty, &err);
+        feed<D>(w, wk, &mk, &mv, a.slices, ring, full, empty, &err);
     } else {
         const int g = lane >> 2, c2 = (lane & 3) * 2;
         int stage = 0, phase = 0;
@@ -214,7 +206,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         for (int e = lane; e < 16 * (D / 8); e += 32) {
                             const int r = e / (D / 8), c = e % (D / 8);
                             if (key0 + r >= p.keys)
-                                *reinterpret_cast<uint4*>(base + (vt - ring) + piece_off(row0 + r, c)) = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4*>(base + (vt - ring) + piece_off<D>(row0 + r, c)) = make_uint4(0, 0, 0, 0);
                         }
                         tc::fence_proxy_async_smem();        // the ring's next copy is the async proxy's
                         __syncwarp();
@@ -229,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                         for (int k = 0; k < KS; ++k) {
                             uint32_t b[4];
-                            ldsm4(kt + piece_off(r, k * 2 + half), b);
+                            ldsm4(kt + piece_off<D>(r, k * 2 + half), b);
 #pragma unroll
                             for (int mt = 0; mt < MT; ++mt) {
                                 uint32_t f[4];
@@ -306,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                         for (int n = 0; n < NT / 2; ++n) {
                             uint32_t b[4];
-                            ldsm4t(vt + piece_off(r, n * 2 + half), b);
+                            ldsm4t(vt + piece_off<D>(r, n * 2 + half), b);
 #pragma unroll
                             for (int mt = 0; mt < MT; ++mt) {
                                 mma16816(o[mt][n * 2], pf[mt], b[0], b[1]);
@@ -426,7 +418,7 @@ cudaError_t launch_paged_decode(const PagedProblem& p, const PagedSplit& sp, cud
         return cudaErrorInvalidValue;
     }
     paged::DecArgs a{paged::make_work(p, sp), static_cast<const __nv_bfloat16*>(p.q), static_cast<const __nv_bfloat16*>(p.probe),
-                     static_cast<__nv_bfloat16*>(p.out), p.Hq, p.q_stride, p.r_stride, p.tau * 1.4426950408889634f};
+                     static_cast<__nv_bfloat16*>(p.out), p.Hq, (int)paged::slices_of_page(p), p.q_stride, p.r_stride, p.tau * 1.4426950408889634f};
     if (p.d == 128)
         return sp.rows == 8 ? paged::launch_dec<128, 1>(a, mk, mv, stream) : paged::launch_dec<128, 2>(a, mk, mv, stream);
     return sp.rows == 8 ? paged::launch_dec<64, 1>(a, mk, mv, stream) : paged::launch_dec<64, 2>(a, mk, mv, stream);

@@ -36,8 +36,8 @@ struct TcShape {
     static constexpr int kStages = D == 128 ? 2 : 4;       // of K and of V
     static constexpr int kCols = kKeys / 2;                // columns of S (and T) that a thread holds
     static constexpr int kTmem = 512;                      // columns: S, T, O1, O2 (a power of two)
-    static constexpr int kRowTile = kRows * D * 2;         // bytes of Q or R: [D / 64][128 rows][128 B]
-    static constexpr int kTile = kKeys * D * 2;            // bytes of a K or V block: [D / 64][kKeys rows][128 B]
+    static constexpr int kRowTile = kRows * D * 2;         // bytes of Q or R
+    static constexpr int kTile = kKeys * D * 2;            // bytes of a K or V block
     static constexpr size_t smem = (size_t)2 * kRowTile + (size_t)2 * kStages * kTile + 1024;
 };
 
@@ -46,7 +46,7 @@ struct TcArgs {
     const __nv_bfloat16* q;
     const __nv_bfloat16* probe;
     __nv_bfloat16* out;
-    int Hq;
+    int Hq, slices;                            // slices: head slices from page to page
     long long q_stride, r_stride;
     float scale;                               // tau log2(e)
 };
@@ -62,14 +62,9 @@ struct TcBars {
     float2 tot[2][kRows];                      // by column half: omega and A of a tile
 };
 
-// Byte offset of 16-byte piece c of row r in a tile of `rows` rows ([D / 64][rows][128 B], 128-byte swizzle).
-__device__ __forceinline__ uint32_t piece_off(int rows, int r, int c) {
-    return (uint32_t)((c >> 3) * (rows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-}
-
 // One box to a lane; K and V of a block go to rings of their own (K is given back a product earlier).
 template <int D>
-__device__ void feed_kv(const Work& w, Walk wk, const CUtensorMap* mk, const CUtensorMap* mv, uint32_t kring,
+__device__ void feed_kv(const Work& w, Walk wk, const CUtensorMap* mk, const CUtensorMap* mv, int slices, uint32_t kring,
                         uint32_t vring, TcBars<D>& b) {
     constexpr int NS = TcShape<D>::kStages, kTile = TcShape<D>::kTile, kKeys = TcShape<D>::kKeys;
     const int lane = threadIdx.x & 31;
@@ -95,10 +90,8 @@ __device__ void feed_kv(const Work& w, Walk wk, const CUtensorMap* mk, const CUt
                 if (lane == 0) mbar_arrive_expect_tx(full, bytes);
                 __syncwarp();
                 if (mine) {
-                    const uint32_t dst = (kv ? vring : kring) + (uint32_t)(st * kTile + lane * box * 128);
-#pragma unroll
-                    for (int x = 0; x < D / 64; ++x)
-                        tma_load_4d(dst + x * (kKeys * 128), kv ? mv : mk, full, x * 64, y, p.h, page);
+                    const uint32_t dst = (kv ? vring : kring) + (uint32_t)(st * kTile + lane * box * D * 2);
+                    tma_load_rows(dst, kv ? mv : mk, full, y >> 3, page * slices + p.h);
                 }
                 __syncwarp();
             }
@@ -117,13 +110,12 @@ template <int D>
 __device__ __forceinline__ void gemm_ss(uint32_t d, uint32_t a_addr, uint32_t b_addr) {
     constexpr int kKeys = TcShape<D>::kKeys;
     constexpr uint32_t ID = idesc_bf16(kRows, kKeys, false, false);
-    const uint64_t a0 = sdesc_sw128(a_addr, 16, 1024), b0 = sdesc_sw128(b_addr, 16, 1024);
+    const uint64_t a0 = sdesc_sw128(a_addr, 16, D * 16), b0 = sdesc_sw128(b_addr, 16, D * 16);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-        const uint64_t ao = (uint64_t)(((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4);
-        const uint64_t bo = (uint64_t)(((ks >> 2) * (kKeys * 128) + (ks & 3) * 32) >> 4);
-        if (ks == 0) umma_ss_c<false>(d, a0 + ao, b0 + bo, ID);
-        else umma_ss_c<true>(d, a0 + ao, b0 + bo, ID);
+        const uint64_t off = (uint64_t)(((ks >> 2) * 1024 + (ks & 3) * 32) >> 4);
+        if (ks == 0) umma_ss_c<false>(d, a0 + off, b0 + off, ID);
+        else umma_ss_c<true>(d, a0 + off, b0 + off, ID);
     }
 }
 // D[tmem] (+)= P V, 128 x D x kKeys: P bf16 pairs in TMEM (each half of the keys in the first columns of the half
@@ -132,12 +124,12 @@ template <int D>
 __device__ __forceinline__ void gemm_ts(uint32_t d, uint32_t p, uint32_t v_addr, bool acc) {
     constexpr int kKeys = TcShape<D>::kKeys, kHalf = kKeys / 32;      // k steps of a half
     constexpr uint32_t ID = idesc_bf16(kRows, D, false, true);
-    const uint64_t b0 = sdesc_sw128(v_addr, kKeys * 128, 1024);
+    const uint64_t b0 = sdesc_sw128(v_addr, 1024, D * 16);
     if (acc) umma_ts_c<true>(d, p, b0, ID);
     else umma_ts_c<false>(d, p, b0, ID);
 #pragma unroll
     for (int ks = 1; ks < kKeys / 16; ++ks)
-        umma_ts_c<true>(d, p + (ks / kHalf) * (kKeys / 2) + (ks % kHalf) * 8, b0 + (uint64_t)((ks * 2048) >> 4), ID);
+        umma_ts_c<true>(d, p + (ks / kHalf) * (kKeys / 2) + (ks % kHalf) * 8, b0 + (uint64_t)((ks * D * 32) >> 4), ID);
 }
 
 // The issuing warp.  All lanes run the loop and one elected lane issues: with everything that the products'
@@ -302,8 +294,8 @@ __device__ __forceinline__ void load_rows(const TcArgs& a, const Piece& p, uint3
         const bool in = rr < p.rows;
         const int f = in ? p.row0 + rr : 0, tk = over_g(w, f);
         const long long token = p.q.token0 + tk, hc = (long long)(p.h * w.G + f - tk * w.G) * D + c * 8;
-        copy16(qa + piece_off(kRows, rr, c), a.q + token * a.q_stride + hc, in);
-        copy16(ra + piece_off(kRows, rr, c), a.probe + token * a.r_stride + hc, in);
+        copy16(qa + piece_off<D>(rr, c), a.q + token * a.q_stride + hc, in);
+        copy16(ra + piece_off<D>(rr, c), a.probe + token * a.r_stride + hc, in);
     }
 }
 
@@ -353,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= kSoft / 32) {
         setmaxnreg_dec72();
-        if (warp == kSoft / 32) feed_kv<D>(w, wk, &mk, &mv, kring, vring, b);
+        if (warp == kSoft / 32) feed_kv<D>(w, wk, &mk, &mv, a.slices, kring, vring, b);
         if (warp == kSoft / 32 + 1)
         issue<D>(w, wk, __shfl_sync(0xffffffffu, tm, 0), __shfl_sync(0xffffffffu, qa, 0),
                  __shfl_sync(0xffffffffu, ra, 0), __shfl_sync(0xffffffffu, kring, 0),
@@ -438,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int e = tid; e < kKeys * (D / 8); e += kSoft) {
                         const int rr = e / (D / 8), c = e % (D / 8);
                         if (key0 + rr >= p.keys)
-                            *reinterpret_cast<uint4*>(vs + (size_t)st * kTile + piece_off(kKeys, rr, c)) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4*>(vs + (size_t)st * kTile + piece_off<D>(rr, c)) = make_uint4(0, 0, 0, 0);
                     }
                     fence_proxy_async_smem();
                 }
@@ -601,7 +593,7 @@ cudaError_t launch_paged_tc(const PagedProblem& p, const PagedSplit& sp, cudaStr
         return cudaErrorInvalidValue;
     }
     paged::TcArgs a{paged::make_work(p, sp), static_cast<const __nv_bfloat16*>(p.q), static_cast<const __nv_bfloat16*>(p.probe),
-                    static_cast<__nv_bfloat16*>(p.out), p.Hq, p.q_stride, p.r_stride, p.tau * 1.4426950408889634f};
+                    static_cast<__nv_bfloat16*>(p.out), p.Hq, (int)paged::slices_of_page(p), p.q_stride, p.r_stride, p.tau * 1.4426950408889634f};
     return p.d == 128 ? paged::launch_tc<128>(a, mk, mv, stream) : paged::launch_tc<64>(a, mk, mv, stream);
 }
 
