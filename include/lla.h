@@ -414,7 +414,7 @@ int lla_paged_append(int dtype, const void* k_new, const void* v_new, const long
  * block_table [S, table_width], cu_q [S+1], kv_lens [S] int32.  max_new: the most tokens of a sequence
  *            (T serves; a small value lets a decode step take the decode kernel).
  * Hq a multiple of Hkv; d in {16, 32, 64, 128}; S <= 2^20; T*Hq <= 2^30; table_width*page_size <= 2^28
- * and, times Hq/Hkv, <= 2^31; Hq/Hkv <= 1024.
+ * and, times Hq/Hkv, <= 2^30; Hq/Hkv <= 1024.
  * Lengths or page ids on the device that lie outside the tensors (cu_q beyond T or falling, more than
  * max_new tokens, kv_lens beyond the table, a page id outside [0, num_pages)) are never followed: the
  * access is cut or reads zeros, and lla_sync_status reports LLA_ERR_INVALID_ARG.  What pages hold behind a

@@ -255,9 +255,9 @@ int check_paged_sizes(int dtype, int path, int T, int S, int Hq, int Hkv, int d,
     if (dtype != LLA_DTYPE_BF16 && dtype != LLA_DTYPE_FP32) return failf(LLA_ERR_INVALID_ARG, "unknown dtype %d", dtype);
     if (path < LLA_PATH_AUTO || path > LLA_PATH_FP32) return failf(LLA_ERR_INVALID_ARG, "unknown path %d", path);
     if (S > (1 << 20) || (long long)T * Hq > (1LL << 30) || (long long)table_width * page_size > (1LL << 28) ||
-        (long long)table_width * page_size * (Hq / Hkv) > (1LL << 31) || Hkv > 65535 || Hq / Hkv > 1024)
+        (long long)table_width * page_size * (Hq / Hkv) > (1LL << 30) || Hkv > 65535 || Hq / Hkv > 1024)
         return failf(LLA_ERR_INVALID_ARG, "problem too large (S <= 2^20, T*Hq <= 2^30, table_width*page_size <= 2^28 and "
-                                          "<= 2^31 Hkv/Hq, Hq/Hkv <= 1024)");
+                                          "<= 2^30 Hkv/Hq, Hq/Hkv <= 1024)");
     *rpath = lla_resolve_path(dtype, path, d);
     if (*rpath == LLA_PATH_TENSOR && (dtype != LLA_DTYPE_BF16 || (d != 64 && d != 128)))
         return failf(LLA_ERR_UNSUPPORTED, "tensor path needs bf16 inputs and d in {64, 128}");

@@ -50,7 +50,8 @@ inline size_t paged_workspace_bytes(int ctas, int rows, int d) {
     return (size_t)kPagedMaxCtas * sizeof(PartHeader) + (size_t)ctas * 2 * paged_part_floats(rows, d) * sizeof(float);
 }
 
-// How a path divides the work: rows of a tile, keys of a block, CTAs, least units worth a CTA.
+// How a path divides the work: rows of a tile, keys of a block (powers of two, rows <= keys), CTAs, least units
+// worth a CTA.
 struct PagedSplit {
     int rows, keys, ctas, min_units;
 };
@@ -86,6 +87,20 @@ inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, si
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// Division of x < 2^31 by a number known on the host: multiplication with the rounded-up reciprocal.
+struct Divisor {
+    unsigned mul, shift;
+};
+inline int log2_up(int x) {
+    int s = 0;
+    while ((1 << s) < x) ++s;
+    return s;
+}
+inline Divisor make_divisor(int d) {
+    const unsigned s = (unsigned)log2_up(d);
+    return Divisor{(unsigned)((((1ull << 32) * ((1ull << s) - (unsigned)d)) / (unsigned)d) + 1), s};
+}
+
 // What a kernel needs of the problem, by value.
 struct Work {
     const int* table;
@@ -93,8 +108,8 @@ struct Work {
     const int* kv_lens;
     int T, S, Hkv, G, width, page_shift, num_pages, max_new, causal;
     int rows, keys, ctas, min_units;
-    int keys_shift, both_shift;       // log2 of keys and of min(rows, keys)
-    unsigned g_mul, g_shift;          // division by G (over_g)
+    int keys_shift, rows_shift;       // their log2; rows <= keys
+    Divisor g, m;                     // G, and keys / rows * G
     PartHeader* hdr;
     float* part;
     unsigned* err;
@@ -106,21 +121,20 @@ inline Work make_work(const PagedProblem& p, const PagedSplit& sp) {
     w.T = p.T; w.S = p.S; w.Hkv = p.Hkv; w.G = p.G; w.width = p.width; w.page_shift = p.page_shift;
     w.num_pages = p.num_pages; w.max_new = p.max_new; w.causal = p.causal;
     w.rows = sp.rows; w.keys = sp.keys; w.ctas = sp.ctas; w.min_units = sp.min_units;
-    auto log2i = [](int x) { int s = 0; while ((1 << s) < x) ++s; return s; };
-    w.keys_shift = log2i(sp.keys);
-    w.both_shift = log2i(sp.rows < sp.keys ? sp.rows : sp.keys);
-    w.g_shift = (unsigned)log2i(p.G);
-    w.g_mul = (unsigned)((((1ull << 32) * ((1ull << w.g_shift) - (unsigned)p.G)) / (unsigned)p.G) + 1);
+    w.keys_shift = log2_up(sp.keys);
+    w.rows_shift = log2_up(sp.rows);
+    w.g = make_divisor(p.G);
+    w.m = make_divisor(sp.keys / sp.rows * p.G);
     w.hdr = static_cast<PartHeader*>(p.ws);
     w.part = reinterpret_cast<float*>(static_cast<char*>(p.ws) + (size_t)kPagedMaxCtas * sizeof(PartHeader));
     w.err = p.err;
     return w;
 }
 
-// x / G for 0 <= x < 2^31, by multiplication with the rounded-up reciprocal.
-__device__ __forceinline__ int over_g(const Work& w, int x) {
-    return (int)((__umulhi(w.g_mul, (unsigned)x) + (unsigned)x) >> w.g_shift);
+__device__ __forceinline__ unsigned over(const Divisor& d, unsigned x) {
+    return (__umulhi(d.mul, x) + x) >> d.shift;
 }
+__device__ __forceinline__ int over_g(const Work& w, int x) { return (int)over(w.g, (unsigned)x); }
 
 // a / b for 0 <= a, 0 < b; a 32-bit division where both fit (they nearly always do).
 __device__ __forceinline__ long long div_units(long long a, long long b) {
@@ -145,19 +159,10 @@ __device__ __forceinline__ Seq load_seq(const Work& w, int s) {
     return q;
 }
 
-// sum_{x < X} floor(x / m) = m q (q - 1) / 2 + q r, X = q m + r.
-__device__ inline long long quotient_sum(unsigned X, unsigned m) {
-    const unsigned q = X / m, r = X - q * m;
+// sum_{x < X} floor(x / m) = m q (q - 1) / 2 + q r, X = q m + r, for m = keys / rows * G.
+__device__ inline long long quotient_sum(const Work& w, unsigned X) {
+    const unsigned m = (unsigned)((w.keys >> w.rows_shift) * w.G), q = over(w.m, X), r = X - q * m;
     return (long long)((unsigned long long)q * (q - 1) / 2 * m + (unsigned long long)q * r);
-}
-// sum_{i < n} floor((a i + b) / m), a 1 or 2: the difference of two quotient sums; for a = 2 with
-// floor((2 i + b) / (2 m)) = floor((i + floor(b / 2)) / m) and, for odd m, floor(x / m) = floor(x / (2 m)) +
-// floor((x + m) / (2 m)).
-__device__ inline long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
-    if (a == 1) return quotient_sum(b + n, m) - quotient_sum(b, m);
-    if ((m & 1) == 0) return quotient_sum((b >> 1) + n, m >> 1) - quotient_sum(b >> 1, m >> 1);
-    const unsigned c = b + m;
-    return quotient_sum((b >> 1) + n, m) - quotient_sum(b >> 1, m) + quotient_sum((c >> 1) + n, m) - quotient_sum(c >> 1, m);
 }
 
 __device__ __forceinline__ int tiles_of(const Work& w, const Seq& q) { return (q.nq * w.G + w.rows - 1) / w.rows; }
@@ -189,10 +194,10 @@ __device__ inline long long units_before(const Work& w, const Seq& q, int n) {
         --full;
     }
     if (full > 0) {
-        // tile i: floor((c0 G + rows (i + 1) - 1) / (keys G)) + 1 units; rows and keys are powers of two, so
-        // their common factor leaves the quotient as it is
-        const unsigned c0 = (unsigned)max(q.L - q.nq, 0) * w.G + w.rows - 1;
-        u += full + floor_sum(full, (w.keys >> w.both_shift) * w.G, w.rows >> w.both_shift, c0 >> w.both_shift);
+        // tile i: floor((c0 G + rows (i + 1) - 1) / (keys G)) + 1 = floor((i + b) / (keys / rows G)) + 1 units, rows and
+        // keys being powers of two
+        const unsigned b = ((unsigned)max(q.L - q.nq, 0) * w.G + w.rows - 1) >> w.rows_shift;
+        u += full + quotient_sum(w, b + full) - quotient_sum(w, b);
     }
     return u;
 }

@@ -11,8 +11,9 @@
 // Eight warps hold the rows, a thread half of a row's columns.  The exponents are taken against the
 // reference point of the blocks before while the maximum is taken beside them, and only the vote of a
 // row's two warps on whether it grew stands between: the softmax of a block is one pass.  One warp feeds K
-// and V through TMA rings (a box per page), one issues the products.  The next tile's queries are loaded
-// while the last block of a tile is weighted, and its first products run under the epilogue.
+// and V through TMA rings (a box per page), one issues the products, two divide the work, publish the tiles
+// and load the next tile's queries as soon as the last product that reads the present ones is done: the next
+// tile's first products run under the epilogue.
 #include <math.h>
 
 #include "../../include/lla.h"
@@ -28,7 +29,8 @@ using namespace tc;
 
 constexpr int kRows = 128;
 constexpr int kSoft = 256;                     // threads that hold rows
-constexpr int kThreads = kSoft + 128;          // 168 registers each at launch: 384 x 168 = 256 x 216 + 128 x 72
+constexpr int kLoad = 64;                      // threads that load queries and probes
+constexpr int kThreads = kSoft + 64 + kLoad;   // 168 registers each at launch: 384 x 168 = 256 x 216 + 128 x 72
 
 template <int D>
 struct TcShape {
@@ -36,7 +38,7 @@ struct TcShape {
     static constexpr int kStages = D == 128 ? 2 : 4;       // of K and of V
     static constexpr int kCols = kKeys / 2;                // columns of S (and T) that a thread holds
     static constexpr int kTmem = 512;                      // columns: S, T, O1, O2 (a power of two)
-    static constexpr int kRowTile = kRows * D * 2;         // bytes of Q or R
+    static constexpr int kRowTile = kRows * D * 2;         // bytes of Q or R: [D / 64][128 rows][128 B]
     static constexpr int kTile = kKeys * D * 2;            // bytes of a K or V block
     static constexpr size_t smem = (size_t)2 * kRowTile + (size_t)2 * kStages * kTile + 1024;
 };
@@ -49,13 +51,18 @@ struct TcArgs {
     int Hq, slices;                            // slices: head slices from page to page
     long long q_stride, r_stride;
     float scale;                               // tau log2(e)
+    int row_boxes;                             // 128 is a multiple of G: a tile's rows are whole tokens
 };
+
+constexpr int kRing = 4;                       // pieces published ahead
 
 template <int D>
 struct TcBars {
     uint64_t kfull[TcShape<D>::kStages], kempty[TcShape<D>::kStages];
     uint64_t vfull[TcShape<D>::kStages], vempty[TcShape<D>::kStages];
-    uint64_t qfull, sfull, tfull, p1, p2, done, fin;
+    uint64_t qfull, qfree, sfull, tfull, p1, p2, done, fin;
+    uint64_t ready[kRing], free[kRing];        // of the published pieces
+    Piece piece[kRing];                        // rows 0: no more
     uint32_t tmem;
     int err;
     float mx[2][kRows], s0[kRows];             // by column half: row maxima; centres
@@ -110,12 +117,13 @@ template <int D>
 __device__ __forceinline__ void gemm_ss(uint32_t d, uint32_t a_addr, uint32_t b_addr) {
     constexpr int kKeys = TcShape<D>::kKeys;
     constexpr uint32_t ID = idesc_bf16(kRows, kKeys, false, false);
-    const uint64_t a0 = sdesc_sw128(a_addr, 16, D * 16), b0 = sdesc_sw128(b_addr, 16, D * 16);
+    const uint64_t a0 = sdesc_sw128(a_addr, 16, 1024), b0 = sdesc_sw128(b_addr, 16, D * 16);
 #pragma unroll
     for (int ks = 0; ks < D / 16; ++ks) {
-        const uint64_t off = (uint64_t)(((ks >> 2) * 1024 + (ks & 3) * 32) >> 4);
-        if (ks == 0) umma_ss_c<false>(d, a0 + off, b0 + off, ID);
-        else umma_ss_c<true>(d, a0 + off, b0 + off, ID);
+        const uint64_t ao = (uint64_t)(((ks >> 2) * (kRows * 128) + (ks & 3) * 32) >> 4);
+        const uint64_t bo = (uint64_t)(((ks >> 2) * 1024 + (ks & 3) * 32) >> 4);
+        if (ks == 0) umma_ss_c<false>(d, a0 + ao, b0 + bo, ID);
+        else umma_ss_c<true>(d, a0 + ao, b0 + bo, ID);
     }
 }
 // D[tmem] (+)= P V, 128 x D x kKeys: P bf16 pairs in TMEM (each half of the keys in the first columns of the half
@@ -157,6 +165,7 @@ __device__ void issue(const Work& w, Walk wk, uint32_t tm, uint32_t qa, uint32_t
             gemm_ss<D>(tT, ra, kring + (n % NS) * kTile);
             umma_commit(&b.tfull);
             umma_commit(&b.kempty[n % NS]);
+            if (nb == 1) umma_commit(&b.qfree);
         }
         __syncwarp();
         ok = __all_sync(0xffffffffu, mbar_wait(&b.vfull[n % NS], (n / NS) & 1, &b.err));
@@ -190,6 +199,7 @@ __device__ void issue(const Work& w, Walk wk, uint32_t tm, uint32_t qa, uint32_t
                     gemm_ss<D>(tT, ra, kring + sk * kTile);
                     umma_commit(&b.tfull);
                     umma_commit(&b.kempty[sk]);
+                    if (j + 2 == nb) umma_commit(&b.qfree);   // the last product that reads Q and R
                 } else {
                     umma_commit(&b.done);
                 }
@@ -234,6 +244,27 @@ __device__ __forceinline__ void store_cols(uint32_t t, const uint32_t (&x)[N]) {
 #pragma unroll
     for (int c = 0; c < N; c += 16) tmem_st16(t + c, *reinterpret_cast<const uint32_t (*)[16]>(&x[c]));
     tmem_st_wait();
+}
+
+// 16-byte pieces of four neighbouring lanes, transposed: piece k of lane i and piece i of lane k change places.
+__device__ __forceinline__ void transpose4(uint32_t (&y)[4][4]) {
+    const bool b0 = threadIdx.x & 1, b1 = threadIdx.x & 2;
+#pragma unroll
+    for (int i = 0; i < 4; i += 2)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, b0 ? y[i][e] : y[i + 1][e], 1);
+            y[i][e] = b0 ? got : y[i][e];
+            y[i + 1][e] = b0 ? y[i + 1][e] : got;
+        }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, b1 ? y[i][e] : y[i + 2][e], 2);
+            y[i][e] = b1 ? got : y[i][e];
+            y[i + 2][e] = b1 ? y[i + 2][e] : got;
+        }
 }
 
 // Or of x over the two warps of a row set (64 threads).
@@ -283,25 +314,75 @@ __device__ __forceinline__ float top_of(const float (&x)[N]) {
     return fmaxf(a, b);
 }
 
-// The tile's queries and probes into shared memory (not waited for); rows behind its last are zeros.
+// The two loading warps: publish the pieces, and bring each tile's queries and probes into shared memory once the
+// products of the tile before have read theirs.  Where 128 is a multiple of G a tile's rows are the G heads of
+// 128 / G tokens, a box of the token rows (rows behind the tile's last hold what follows, or zeros behind
+// the tensor); else each row is copied by itself.  (Copied rows take a tile 6500 cycles, boxes 1500.)
 template <int D>
-__device__ __forceinline__ void load_rows(const TcArgs& a, const Piece& p, uint32_t qa, uint32_t ra) {
+__device__ void load_tiles(const TcArgs& a, Walk wk, const CUtensorMap* mq, const CUtensorMap* mr, uint32_t qa, uint32_t ra,
+                           TcBars<D>& b) {
     const Work& w = a.w;
-    const int tid = threadIdx.x;
+    const int t = threadIdx.x - (kThreads - kLoad), lane = threadIdx.x & 31;
+    constexpr int kPieces = D / 8, kStep = kLoad / kPieces;      // 16-byte pieces of a row; rows at a time
+    const int c = t % kPieces;
+    bool ok = true, more = true;
+    int tiles = 0;
+    for (int k = 0; ok && more; ++k) {
+        Piece p;
+        more = next_piece(w, wk, p);
+        if (!more) p.rows = 0;
+        if (t < 32) {
+            if (k >= kRing) ok = __all_sync(0xffffffffu, mbar_wait(&b.free[k % kRing], (k / kRing - 1) & 1, &b.err));
+            if (!ok) break;
+            if (lane == 0) {
+                b.piece[k % kRing] = p;
+                mbar_arrive(&b.ready[k % kRing]);
+            }
+            __syncwarp();
+        }
+        if (!more || p.j1 == p.j0) continue;
+        if (tiles > 0) ok = __all_sync(0xffffffffu, mbar_wait(&b.qfree, (tiles - 1) & 1, &b.err));
+        if (!ok) break;
+        ++tiles;
+        if (a.row_boxes) {
+            if (lane == 0) {
+                if (t == 0) {
+                    mbar_arrive_expect_tx(&b.qfull, 2 * TcShape<D>::kRowTile);
+                    const int token = p.q.token0 + over_g(w, p.row0);
 #pragma unroll
-    for (int i = 0; i < kRows * (D / 8) / kSoft; ++i) {
-        const int e = i * kSoft + tid, rr = e / (D / 8), c = e % (D / 8);
-        const bool in = rr < p.rows;
-        const int f = in ? p.row0 + rr : 0, tk = over_g(w, f);
-        const long long token = p.q.token0 + tk, hc = (long long)(p.h * w.G + f - tk * w.G) * D + c * 8;
-        copy16(qa + piece_off<D>(rr, c), a.q + token * a.q_stride + hc, in);
-        copy16(ra + piece_off<D>(rr, c), a.probe + token * a.r_stride + hc, in);
+                    for (int x = 0; x < D / 64; ++x) {
+                        tma_load_4d(qa + x * (kRows * 128), mq, &b.qfull, x * 64, 0, p.h, token);
+                        tma_load_4d(ra + x * (kRows * 128), mr, &b.qfull, x * 64, 0, p.h, token);
+                    }
+                } else {
+                    mbar_arrive(&b.qfull);
+                }
+            }
+            __syncwarp();
+            continue;
+        }
+        const long long hc = (long long)p.h * w.G * D + c * 8;
+#pragma unroll 4
+        for (int rr = t / kPieces; rr < kRows; rr += kStep) {
+            const bool in = rr < p.rows;
+            const int f = in ? p.row0 + rr : 0, tk = over_g(w, f);
+            const long long token = p.q.token0 + tk, col = hc + (f - tk * w.G) * D;
+            const uint32_t to = (uint32_t)((c >> 3) * (kRows * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4));
+            copy16(qa + to, a.q + token * a.q_stride + col, in);
+            copy16(ra + to, a.probe + token * a.r_stride + col, in);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b.qfull);
     }
+    if (a.row_boxes && tiles > 0 && (!ok || *(volatile int*)&b.err)) drain(&b.qfull, (tiles - 1) & 1);
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-    paged_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    paged_tc_kernel(TcArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                    const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mr) {
     using Sh = TcShape<D>;
     constexpr int NS = Sh::kStages, kTile = Sh::kTile, kKeys = Sh::kKeys, kCols = Sh::kCols, HD = D / 2;
     extern __shared__ unsigned char raw[];
@@ -321,7 +402,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&b.vfull[i], 1);
             mbar_init(&b.vempty[i], 1);
         }
-        mbar_init(&b.qfull, kSoft / 32);
+        mbar_init(&b.qfull, kLoad / 32);
+        mbar_init(&b.qfree, 1);
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&b.ready[i], 1);
+            mbar_init(&b.free[i], kSoft / 32);
+        }
         mbar_init(&b.p1, kSoft / 32);
         mbar_init(&b.p2, kSoft / 32);
         mbar_init(&b.sfull, 1);
@@ -346,10 +432,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= kSoft / 32) {
         setmaxnreg_dec72();
         if (warp == kSoft / 32) feed_kv<D>(w, wk, &mk, &mv, a.slices, kring, vring, b);
-        if (warp == kSoft / 32 + 1)
-        issue<D>(w, wk, __shfl_sync(0xffffffffu, tm, 0), __shfl_sync(0xffffffffu, qa, 0),
-                 __shfl_sync(0xffffffffu, ra, 0), __shfl_sync(0xffffffffu, kring, 0),
-                 __shfl_sync(0xffffffffu, vring, 0), b);
+        else if (warp == kSoft / 32 + 1)
+            issue<D>(w, wk, __shfl_sync(0xffffffffu, tm, 0), __shfl_sync(0xffffffffu, qa, 0), __shfl_sync(0xffffffffu, ra, 0),
+                     __shfl_sync(0xffffffffu, kring, 0), __shfl_sync(0xffffffffu, vring, 0), b);
+        else
+            load_tiles<D>(a, wk, &mq, &mr, qa, ra, b);
     } else {
         setmaxnreg_inc216();
         const int half = warp >> 2, r = (warp & 3) * 32 + lane;      // column half, row
@@ -357,27 +444,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t tS = lanes + half * kCols, tT = tS + kKeys;
         const uint32_t tO1 = lanes + 2 * kKeys + half * HD, tO2 = tO1 + D;   // this half's output columns
-        int n = 0, pieces = 0;
-        bool shared = false, loaded = false;
-        Piece p, next;
-        p.parts = 0; p.row0 = p.rows = p.h = 0; p.q.token0 = 0;
-        bool have = next_piece(w, wk, next);
-        // after a wait that gave up, the others give up at once (they see the flag) and every barrier is still
-        // passed: the CTA ends, with results that the error word disowns
-        while (have) {
-            p = next;
-            shared = p.slot == 1;
+        int n = 0, pieces = 0, k = 0;
+        // The two warps of a row set agree on each piece before they use it, so that they pass the same barriers
+        // whatever a wait gave.  Within a piece, after a wait that gave up, the others give up at once (they see the
+        // flag) and every barrier is still passed: the CTA ends, with results that the error word disowns.
+        for (;; ++k) {
+            const bool got = mbar_wait(&b.ready[k % kRing], (k / kRing) & 1, &b.err);
+            if (pair_or(pair, !got)) break;
+            const Piece& p = b.piece[k % kRing];
+            if (p.rows == 0) break;
             const int nb = p.j1 - p.j0;
-            if (nb > 0 && !loaded) {
-                load_rows<D>(a, p, qa, ra);
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&b.qfull);
-            }
-            loaded = false;
-            have = next_piece(w, wk, next);
-            const int fr = min(p.row0 + r, p.row0 + p.rows - 1), tk = over_g(w, fr);
+            const int tk = over_g(w, min(p.row0 + r, p.row0 + p.rows - 1));
             float m = -INFINITY, om = 0.f, A = 0.f, s0 = 0.f;
             // rows behind the tile's last compute on zeros and are not written
             int limit = p.keys;
@@ -404,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 scores();
                 if (j > 0) {
                     weigh(x, a.scale, m == -INFINITY ? 0.f : m, pk, ps, over);
-                    grow = pair_or(pair, over);
+                    grow = pair_or(pair, over && r < p.rows);   // rows that are not the tile's do not decide
                     if (grow) scores();        // S is still there
                 }
                 if (grow) {
@@ -443,10 +520,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // ------------------------------------------------------------- T: the weights p (t - s0)
                 mbar_wait(&b.tfull, n & 1, &b.err);
                 tc_fence_after();
-                if (j + 1 == nb && have && next.j1 > next.j0) {   // Q and R have been read: the next tile's
-                    load_rows<D>(a, next, qa, ra);
-                    loaded = true;
-                }
                 if (j > 0 && grow) {           // O2 of the blocks before (complete: T of this one came after it)
 #pragma unroll 1
                     for (int c = 0; c < HD; c += 32) scale32(tO2 + c, f);
@@ -500,13 +573,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 A += y + z;
             }
 
+            // where this lane stores: four lanes write 64 bytes of a row, of four rows one after another
+            __nv_bfloat16* to[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int rr = (r & ~3) + i, f2 = p.row0 + rr, t2 = over_g(w, f2);
+                to[i] = rr < p.rows ? a.out + ((p.q.token0 + (long long)t2) * a.Hq + p.h * w.G + f2 - t2 * w.G) * D +
+                                          half * HD + (lane & 3) * 8
+                                    : nullptr;
+            }
             if (nb > 0) {
-                if (loaded) {
-                    asm volatile("cp.async.wait_all;" ::: "memory");
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&b.qfull);
-                }
                 b.tot[half][r] = make_float2(om, A);
                 named_bar_sync(pair, 64);
                 om = b.tot[0][r].x + b.tot[1][r].x;
@@ -515,8 +591,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 ++pieces;
             }
-            const long long token = p.q.token0 + tk;
-            const int head = p.h * w.G + fr - tk * w.G;
             const float inv = om != 0.f ? 1.f / om : 0.f, c1 = (1.f + A * inv) * inv;
 #pragma unroll
             for (int c = 0; c < HD; c += 32) {
@@ -529,36 +603,40 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o1[i] = o2[i] = 0.f;
                 }
-                if (r < p.rows) {
-                    const int col = half * HD + c;
-                    if (p.slot < 0) {
-                        uint4* o = reinterpret_cast<uint4*>(a.out + (token * a.Hq + head) * D + col);
+                if (p.slot < 0) {
+                    uint32_t y[4][4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t y[4];
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int k = i * 8 + e * 2;
-                                y[e] = pack_bf16(c1 * o1[k] - inv * o2[k], c1 * o1[k + 1] - inv * o2[k + 1]);
-                            }
-                            o[i] = make_uint4(y[0], y[1], y[2], y[3]);
+                        for (int e = 0; e < 4; ++e) {
+                            const int k = i * 8 + e * 2;
+                            y[i][e] = pack_bf16(c1 * o1[k] - inv * o2[k], c1 * o1[k + 1] - inv * o2[k + 1]);
                         }
-                    } else {
-                        float4* d1 = part_sums(w, blockIdx.x, p.slot, D) + (size_t)(col / 4) * kRows + r;
-                        float4* d2 = d1 + (size_t)(D / 4) * kRows;
+                    transpose4(y);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            d1[i * kRows] = make_float4(o1[4 * i], o1[4 * i + 1], o1[4 * i + 2], o1[4 * i + 3]);
-                            d2[i * kRows] = make_float4(o2[4 * i], o2[4 * i + 1], o2[4 * i + 2], o2[4 * i + 3]);
-                        }
+                    for (int k = 0; k < 4; ++k)
+                        if (to[k]) *reinterpret_cast<uint4*>(to[k] + c) = make_uint4(y[k][0], y[k][1], y[k][2], y[k][3]);
+                } else if (r < p.rows) {
+                    float4* d1 = part_sums(w, blockIdx.x, p.slot, D) + (size_t)((half * HD + c) / 4) * kRows + r;
+                    float4* d2 = d1 + (size_t)(D / 4) * kRows;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        d1[i * kRows] = make_float4(o1[4 * i], o1[4 * i + 1], o1[4 * i + 2], o1[4 * i + 3]);
+                        d2[i * kRows] = make_float4(o2[4 * i], o2[4 * i + 1], o2[4 * i + 2], o2[4 * i + 3]);
                     }
                 }
             }
             if (r < p.rows && half == 0 && p.slot >= 0)
                 part_stats(w, blockIdx.x, p.slot, D)[r] = make_float4(m, om, A, s0);
             tc_fence_before();                 // O is read: the next tile's products may write it (after p1)
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&b.free[k % kRing]);
         }
-        if (tid == 0) write_header(w, blockIdx.x, p, shared);
+        // the last piece (its place is not used again) is the one that others may finish
+        if (tid == 0) {
+            const Piece& last = b.piece[(k + kRing - 1) % kRing];
+            write_header(w, blockIdx.x, last, k > 0 && last.slot == 1 && !*(volatile int*)&b.err);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -570,12 +648,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (tid == 0 && b.err) atomicOr(w.err, (unsigned)kDevErrMbarTimeout);
 }
 
+// Token rows [T, Hq, d] as (column, head of a group, key head, token); box: 64 columns of the G heads of 128 / G tokens.
+bool make_rows_map(CUtensorMap* map, const void* rows, long long stride, const PagedProblem& p) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[4] = {(cuuint64_t)p.d, (cuuint64_t)p.G, (cuuint64_t)p.Hkv, (cuuint64_t)p.T};
+    cuuint64_t strides[3] = {(cuuint64_t)p.d * 2, (cuuint64_t)p.G * p.d * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[4] = {64, (cuuint32_t)p.G, 1, (cuuint32_t)(kRows / p.G)};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(rows), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D>
-cudaError_t launch_tc(const TcArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
+cudaError_t launch_tc(const TcArgs& a, const CUtensorMap (&m)[4], cudaStream_t stream) {
     constexpr size_t smem = TcShape<D>::smem;
     cudaError_t e = cudaFuncSetAttribute(paged_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_after(paged_tc_kernel<D>, dim3(a.w.ctas), kThreads, smem, stream, a, mk, mv);
+    return launch_after(paged_tc_kernel<D>, dim3(a.w.ctas), kThreads, smem, stream, a, m[0], m[1], m[2], m[3]);
 }
 
 }  // namespace
@@ -587,14 +678,17 @@ PagedSplit paged_tc_split(const PagedProblem& p, int sms) {
 }
 
 cudaError_t launch_paged_tc(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream, const char** why) {
-    CUtensorMap mk, mv;
-    if (!paged::make_cache_map(&mk, p.k, p) || !paged::make_cache_map(&mv, p.v, p)) {
-        *why = "tensor map of a paged cache";
+    CUtensorMap m[4] = {};
+    const bool boxes = paged::kRows % p.G == 0;
+    if (!paged::make_cache_map(&m[0], p.k, p) || !paged::make_cache_map(&m[1], p.v, p) ||
+        (boxes && (!paged::make_rows_map(&m[2], p.q, p.q_stride, p) || !paged::make_rows_map(&m[3], p.probe, p.r_stride, p)))) {
+        *why = "tensor map of a paged call";
         return cudaErrorInvalidValue;
     }
     paged::TcArgs a{paged::make_work(p, sp), static_cast<const __nv_bfloat16*>(p.q), static_cast<const __nv_bfloat16*>(p.probe),
-                    static_cast<__nv_bfloat16*>(p.out), p.Hq, (int)paged::slices_of_page(p), p.q_stride, p.r_stride, p.tau * 1.4426950408889634f};
-    return p.d == 128 ? paged::launch_tc<128>(a, mk, mv, stream) : paged::launch_tc<64>(a, mk, mv, stream);
+                    static_cast<__nv_bfloat16*>(p.out), p.Hq, (int)paged::slices_of_page(p), p.q_stride, p.r_stride,
+                    p.tau * 1.4426950408889634f, boxes};
+    return p.d == 128 ? paged::launch_tc<128>(a, m, stream) : paged::launch_tc<64>(a, m, stream);
 }
 
 }  // namespace lla
