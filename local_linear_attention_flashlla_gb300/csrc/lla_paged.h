@@ -54,6 +54,7 @@ inline size_t paged_workspace_bytes(int ctas, int rows, int d) {
 // worth a CTA.
 struct PagedSplit {
     int rows, keys, ctas, min_units;
+    int extra;      // units charged for a tile beside its blocks: what a tile costs before its first block and after its last
 };
 
 // bf16, d in {64, 128}, at most 16 query rows to a key head (max_new * G): lla_paged_decode.cu.
@@ -107,7 +108,7 @@ struct Work {
     const int* cu_q;
     const int* kv_lens;
     int T, S, Hkv, G, width, page_shift, num_pages, max_new, causal;
-    int rows, keys, ctas, min_units;
+    int rows, keys, ctas, min_units, extra;
     int keys_shift, rows_shift;       // their log2; rows <= keys
     Divisor g, m;                     // G, and keys / rows * G
     PartHeader* hdr;
@@ -121,6 +122,7 @@ inline Work make_work(const PagedProblem& p, const PagedSplit& sp) {
     w.T = p.T; w.S = p.S; w.Hkv = p.Hkv; w.G = p.G; w.width = p.width; w.page_shift = p.page_shift;
     w.num_pages = p.num_pages; w.max_new = p.max_new; w.causal = p.causal;
     w.rows = sp.rows; w.keys = sp.keys; w.ctas = sp.ctas; w.min_units = sp.min_units;
+    w.extra = sp.extra;
     w.keys_shift = log2_up(sp.keys);
     w.rows_shift = log2_up(sp.rows);
     w.g = make_divisor(p.G);
@@ -174,12 +176,13 @@ __device__ __forceinline__ int tile_keys(const Work& w, const Seq& q, int i) {
     return min(max(q.L - q.nq + last + 1, 0), q.L);
 }
 
-// Units charged for tile i (>= 1: a tile without keys still has its rows to write).  A causal sequence
+// Units charged for tile i: its blocks (>= 1: a tile without keys still has its rows to write) and the extra ones,
+// which come first.  A causal sequence
 // with fewer keys than tokens is charged as if it had as many.
 __device__ __forceinline__ int tile_units(const Work& w, const Seq& q, int i) {
-    if (!w.causal) return max(1, (q.L + w.keys - 1) >> w.keys_shift);
+    if (!w.causal) return max(1, (q.L + w.keys - 1) >> w.keys_shift) + w.extra;
     const int last = over_g(w, min((i + 1) * w.rows, q.nq * w.G) - 1);
-    return ((max(q.L - q.nq, 0) + last) >> w.keys_shift) + 1;
+    return ((max(q.L - q.nq, 0) + last) >> w.keys_shift) + 1 + w.extra;
 }
 
 // Units of the first n tiles of one key head (n <= tiles).
@@ -197,7 +200,7 @@ __device__ inline long long units_before(const Work& w, const Seq& q, int n) {
         // tile i: floor((c0 G + rows (i + 1) - 1) / (keys G)) + 1 = floor((i + b) / (keys / rows G)) + 1 units, rows and
         // keys being powers of two
         const unsigned b = ((unsigned)max(q.L - q.nq, 0) * w.G + w.rows - 1) >> w.rows_shift;
-        u += full + quotient_sum(w, b + full) - quotient_sum(w, b);
+        u += (long long)full * (1 + w.extra) + quotient_sum(w, b + full) - quotient_sum(w, b);
     }
     return u;
 }
@@ -215,6 +218,15 @@ struct Walk {
     int s, h, i, j;       // sequence, key head, tile, block
     Seq q;
 };
+
+// A range border within a tile's extra units counts as lying before the tile: who ends there leaves the tile, who
+// begins there takes all of it, so that no piece is without blocks for that reason.
+__device__ __forceinline__ void snap_start(const Work& w, Walk& k) {
+    if (k.j <= w.extra) {
+        k.u -= k.j;
+        k.j = 0;
+    }
+}
 
 // Inclusive sum of v over the block's threads in thread order; *all: the block's total.  sh: 32 long longs.
 __device__ __forceinline__ long long block_scan(long long v, long long* sh, long long* all) {
@@ -296,6 +308,7 @@ __device__ inline Walk begin_walk(const Work& w, int cta, long long* sh) {
         rem -= units_before(w, k.q, lo);
     }
     k.j = (int)rem;
+    snap_start(w, k);
     return k;
 }
 
@@ -315,13 +328,14 @@ __device__ __forceinline__ bool next_piece(const Work& w, Walk& k, Piece& p) {
     const int units = tile_units(w, k.q, k.i);
     const long long left = k.end - k.u;
     const int take = (int)(left < units - k.j ? left : units - k.j);
+    if (k.j == 0 && take <= w.extra) return false;       // the border lies in the tile's extra units
     p.s = k.s; p.h = k.h; p.i = k.i; p.q = k.q;
     p.row0 = k.i * w.rows;
     p.rows = min(w.rows, k.q.nq * w.G - p.row0);
     p.keys = tile_keys(w, k.q, k.i);
     const int nb = (p.keys + w.keys - 1) >> w.keys_shift;
-    p.j0 = min(k.j, nb);
-    p.j1 = min(k.j + take, nb);
+    p.j0 = min(max(k.j - w.extra, 0), nb);
+    p.j1 = min(max(k.j + take - w.extra, 0), nb);
     const bool first = k.j == 0, last = k.j + take == units;
     p.slot = first && last ? -1 : first ? 1 : 0;
     p.parts = 0;

@@ -415,7 +415,7 @@ cudaError_t merge_typed(const Work& w, void* out, int Hq, int d, cudaStream_t st
 PagedSplit paged_simt_split(const PagedProblem& p, int sms) {
     // rows: 8 where no sequence has more than eight query rows to a key head (a decode step), else 32
     const bool few = (long long)p.max_new * p.G <= 8;
-    return PagedSplit{few ? 8 : 32, few ? 64 : 32, 2 * sms, 2};
+    return PagedSplit{few ? 8 : 32, few ? 64 : 32, 2 * sms, 2, 0};
 }
 
 cudaError_t launch_paged_simt(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream) {
