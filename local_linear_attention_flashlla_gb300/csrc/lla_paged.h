@@ -50,8 +50,8 @@ inline size_t paged_workspace_bytes(int ctas, int rows, int d) {
     return (size_t)kPagedMaxCtas * sizeof(PartHeader) + (size_t)ctas * 2 * paged_part_floats(rows, d) * sizeof(float);
 }
 
-// How a path divides the work: rows of a tile, keys of a block (powers of two, rows <= keys), CTAs, least units
-// worth a CTA.
+// How a path divides the work: rows of a tile, keys of a block (rows <= keys), CTAs, least units worth a CTA (all
+// but the CTAs powers of two).
 struct PagedSplit {
     int rows, keys, ctas, min_units;
     int extra;      // units charged for a tile beside its blocks: what a tile costs before its first block and after its last
@@ -108,7 +108,7 @@ struct Work {
     const int* cu_q;
     const int* kv_lens;
     int T, S, Hkv, G, width, page_shift, num_pages, max_new, causal;
-    int rows, keys, ctas, min_units, extra;
+    int rows, keys, ctas, min_shift, extra;
     int keys_shift, rows_shift;       // their log2; rows <= keys
     Divisor g, m;                     // G, and keys / rows * G
     PartHeader* hdr;
@@ -121,7 +121,7 @@ inline Work make_work(const PagedProblem& p, const PagedSplit& sp) {
     w.table = p.table; w.cu_q = p.cu_q; w.kv_lens = p.kv_lens;
     w.T = p.T; w.S = p.S; w.Hkv = p.Hkv; w.G = p.G; w.width = p.width; w.page_shift = p.page_shift;
     w.num_pages = p.num_pages; w.max_new = p.max_new; w.causal = p.causal;
-    w.rows = sp.rows; w.keys = sp.keys; w.ctas = sp.ctas; w.min_units = sp.min_units;
+    w.rows = sp.rows; w.keys = sp.keys; w.ctas = sp.ctas; w.min_shift = log2_up(sp.min_units);
     w.extra = sp.extra;
     w.keys_shift = log2_up(sp.keys);
     w.rows_shift = log2_up(sp.rows);
@@ -167,7 +167,7 @@ __device__ inline long long quotient_sum(const Work& w, unsigned X) {
     return (long long)((unsigned long long)q * (q - 1) / 2 * m + (unsigned long long)q * r);
 }
 
-__device__ __forceinline__ int tiles_of(const Work& w, const Seq& q) { return (q.nq * w.G + w.rows - 1) / w.rows; }
+__device__ __forceinline__ int tiles_of(const Work& w, const Seq& q) { return (q.nq * w.G + w.rows - 1) >> w.rows_shift; }
 
 // Keys that the rows of tile i see, at most (the last row's); 0 if none.
 __device__ __forceinline__ int tile_keys(const Work& w, const Seq& q, int i) {
@@ -205,19 +205,27 @@ __device__ inline long long units_before(const Work& w, const Seq& q, int n) {
     return u;
 }
 
-__device__ __forceinline__ long long seq_units(const Work& w, const Seq& q) {
-    return q.nq > 0 ? units_before(w, q, tiles_of(w, q)) * w.Hkv : 0;
+// Units of one key head of a sequence.
+__device__ __forceinline__ long long head_units(const Work& w, const Seq& q) {
+    return q.nq > 0 ? units_before(w, q, tiles_of(w, q)) : 0;
 }
 
 // A position in the order of units.
 struct Walk {
     int cta;              // whose range it is (a CTA, or a pair of them)
     long long u, end;     // next unit of this CTA, end of its range
-    long long total;
-    int active;           // CTAs that have work
+    long long share;      // units of a CTA's range; the first `over` ranges have one more
+    int over, active;     // active: CTAs that have work
     int s, h, i, j;       // sequence, key head, tile, block
     Seq q;
 };
+
+// First unit of range c, and the range that holds unit u.
+__device__ __forceinline__ long long range_start(const Walk& k, int c) { return c * k.share + min(c, k.over); }
+__device__ __forceinline__ int range_of(const Walk& k, long long u) {
+    const long long big = k.over * (k.share + 1);        // units of the longer ranges
+    return u < big ? (int)div_units(u, k.share + 1) : k.over + (int)div_units(u - big, k.share);
+}
 
 // A range border within a tile's extra units counts as lying before the tile: who ends there leaves the tile, who
 // begins there takes all of it, so that no piece is without blocks for that reason.
@@ -227,6 +235,8 @@ __device__ __forceinline__ void snap_start(const Work& w, Walk& k) {
         k.j = 0;
     }
 }
+
+constexpr int kMostWarps = 12;       // of a block that divides work
 
 // Inclusive sum of v over the block's threads in thread order; *all: the block's total.  sh: 32 long longs.
 __device__ __forceinline__ long long block_scan(long long v, long long* sh, long long* all) {
@@ -238,9 +248,11 @@ __device__ __forceinline__ long long block_scan(long long v, long long* sh, long
     if (lane == 31) sh[warp] = v;
     __syncthreads();
     long long sum = 0;
-    for (int i = 0; i < nw; ++i) {
-        if (i == warp) v += sum;
-        sum += sh[i];
+#pragma unroll
+    for (int i = 0; i < kMostWarps; ++i) {
+        const long long t = i < nw ? sh[i] : 0;
+        if (i < warp) v += t;
+        sum += t;
     }
     *all = sum;
     __syncthreads();
@@ -258,29 +270,34 @@ __device__ inline Walk begin_walk(const Work& w, int cta, long long* sh) {
     k.s = k.h = k.i = k.j = 0;
     k.q.token0 = k.q.nq = k.q.L = 0;
     k.u = k.end = 0;
-    long long mine = 0;
+    long long mine = 0, unit = 0, total;           // unit: of a key head of the last sequence looked at
     for (int s = s0; s < s1; ++s) {
         k.q = load_seq(w, s);
-        mine += seq_units(w, k.q);
+        unit = head_units(w, k.q);
+        mine += unit * w.Hkv;
     }
-    long long pre = block_scan(mine, sh, &k.total) - mine;
-    const long long most = div_units(k.total + w.min_units - 1, w.min_units);
+    long long pre = block_scan(mine, sh, &total) - mine;
+    const long long most = (total + (1 << w.min_shift) - 1) >> w.min_shift;
     k.active = (int)(most < w.ctas ? most : w.ctas);
     if (cta >= k.active) return k;
-    k.u = div_units(k.total * cta, k.active);
-    k.end = div_units(k.total * (cta + 1), k.active);
+    k.share = div_units(total, k.active);
+    k.over = (int)(total - k.share * k.active);
+    k.u = range_start(k, cta);
+    k.end = range_start(k, cta + 1);
     int* at = reinterpret_cast<int*>(sh + 32);     // sequence, token0, nq, L
     if (k.u >= pre && k.u < pre + mine) {
         int s = s0;
         if (per > 1) {
             for (; s + 1 < s1; ++s) {
-                const long long u = seq_units(w, load_seq(w, s));
+                const long long u = head_units(w, load_seq(w, s)) * w.Hkv;
                 if (k.u < pre + u) break;
                 pre += u;
             }
             k.q = load_seq(w, s);
+            unit = head_units(w, k.q);
         }
         sh[36] = pre;
+        sh[37] = unit;
         at[0] = s;
         at[1] = k.q.token0;
         at[2] = k.q.nq;
@@ -292,8 +309,8 @@ __device__ inline Walk begin_walk(const Work& w, int cta, long long* sh) {
     k.q.nq = at[2];
     k.q.L = at[3];
     long long rem = k.u - sh[36];
+    unit = sh[37];
     const int tiles = tiles_of(w, k.q);
-    const long long unit = units_before(w, k.q, tiles);
     k.h = (int)div_units(rem, unit);
     rem -= k.h * unit;
     if (tiles > 1) {
@@ -341,8 +358,7 @@ __device__ __forceinline__ bool next_piece(const Work& w, Walk& k, Piece& p) {
     p.parts = 0;
     if (p.slot == 1) {
         const long long tile_end = k.u + units;      // first unit behind the tile (k.j is 0)
-        const long long c = div_units(tile_end * k.active - 1, k.total);
-        p.parts = (int)(c - k.cta) + 1;
+        p.parts = range_of(k, tile_end - 1) - k.cta + 1;
     }
     k.u += take;
     k.j += take;
