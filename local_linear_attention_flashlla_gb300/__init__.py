@@ -12,6 +12,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import threading
 from collections import namedtuple
 
 __all__ = [
@@ -591,9 +592,10 @@ def _paged_workspace_bytes(device_index, dtype, path, Hq, Hkv, d, page_size, max
     return lla_paged_parallax_workspace_size(dtype, path, 1, 1, Hq, Hkv, d, page_size, 1, max_new)
 
 
-# Scratch of eager attention calls by (device, stream): calls on one stream follow one another, so they can share
-# it, and taking it from the allocator costs as much as all checks.  A call under graph capture takes its own
-# (the graph keeps it), so that graphs never share scratch with anything.  At most eight are kept.
+# Scratch of eager attention calls by (device, stream, host thread): a thread's calls on one stream follow one
+# another, so they can share it, and taking it from the allocator costs as much as all checks.  A call under
+# graph capture takes its own (the graph keeps it), so that graphs never share scratch with anything.  At most
+# eight are kept.
 _SCRATCH = {}
 
 
@@ -601,7 +603,7 @@ def _scratch(device, stream_ptr, nbytes):
     import torch
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    key = (device.index, stream_ptr)
+    key = (device.index, stream_ptr, threading.get_ident())
     t = _SCRATCH.get(key)
     if t is None or t.numel() < nbytes:
         _SCRATCH.pop(key, None)
@@ -682,8 +684,8 @@ def paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, 
     block_table [S, W], cu_q [S+1], kv_lens [S]: int32 CUDA tensors (paged_plan's); max_new: the most
     tokens of one sequence in this step.  causal=False: every row sees all of its sequence's keys.
     Returns out [T, Hq, d]; rows behind the last sequence are left as they were.  Asynchronous on the
-    current (or given) stream.  workspace: None (scratch kept per stream; under graph capture the graph's
-    own), or a CUDA tensor of lla_paged_parallax_workspace_size(...) bytes that no other call uses at the
+    current (or given) stream.  workspace: None (scratch kept per stream and thread; under graph capture the
+    graph's own), or a CUDA tensor of lla_paged_parallax_workspace_size(...) bytes that no other call uses at the
     same time.
     """
     import torch

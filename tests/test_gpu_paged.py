@@ -402,6 +402,90 @@ def test_two_calls_at_once_and_on_a_given_stream(lla_gpu):
 
 
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("fp32", 32)])
+@pytest.mark.parametrize("most", [1, 3, 40])
+def test_more_sequences_than_threads(lla_gpu, dtype, d, most):
+    """1100 short sequences, empty ones among them: a thread of the work division sums several."""
+    rng = np.random.default_rng(most)
+    new = rng.integers(0, most + 1, 1100)
+    kv = new + rng.integers(0, 60, 1100) * (rng.random(1100) < 0.7)
+    c = Case(new.tolist(), kv.tolist(), 4, 2, d, 8, dtype, pad=1)
+    for path, tensor in paths(dtype, d):
+        c.check(run(c, path), tensor)
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("fp32", 32)])
+@pytest.mark.parametrize("new,kv,G", [([1, 1], [300, 70], 4), ([5, 20], [300, 200], 4), ([130, 40], [130, 400], 3)])
+def test_rows_of_others_and_padding_do_not_reach_a_sequence(lla_gpu, dtype, d, new, kv, G):
+    """NaN in padding rows, and other queries in the last sequence, leave the first one's bits as they were."""
+    c = Case(new, kv, 2 * G, 2, d, 16, dtype, pad=30)
+    for path, tensor in paths(dtype, d):
+        a = c.device()
+        first = run(c, path)
+        q, r = a["q"].clone(), a["probe"].clone()
+        q[c.cu[-1]:], r[c.cu[-1]:] = float("nan"), float("nan")
+        q[c.cu[1]:c.cu[-1]] *= 3
+        other = run(c, path, q=q, probe=r)
+        assert torch.equal(first[:c.cu[1]], other[:c.cu[1]])
+        assert torch.isfinite(other[:c.cu[-1]]).all()
+
+
+def test_max_new_may_be_larger(lla_gpu):
+    for d in (64, 128):
+        c = Case([1, 1, 2], [300, 70, 130], 4, 2, d, 16, pad=5)
+        c.check(run(c, max_new=len(c.q)), True)
+
+
+def test_scratch_of_one_stream_grows_and_is_used_again(lla_gpu):
+    small, large = Case([1] * 3, [700, 40, 90], 4, 2, 128, 16), Case([100] * 4, [900] * 4, 4, 2, 128, 16)
+    want = [run(small), run(large)]
+    for _ in range(3):
+        got = [lla.paged_parallax(**c.device()) for c in (small, large, small)]
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[0])
+    lla.lla_sync_status()
+
+
+def test_two_host_threads_on_one_stream(lla_gpu):
+    import threading
+    cs = [Case([1], [6000], 4, 2, 128, 16, seed=7), Case([150], [2000], 4, 2, 128, 16, seed=8)]
+    dev, want, bad = [c.device() for c in cs], [run(c) for c in cs], []
+
+    def work(i):
+        outs = [lla.paged_parallax(**dev[i]) for _ in range(60)]
+        torch.cuda.synchronize()
+        bad.extend(k for k, o in enumerate(outs) if not torch.equal(o, want[i]))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    lla.lla_sync_status()
+    assert not bad
+
+
+def test_two_graphs_and_eager_calls_share_nothing(lla_gpu):
+    cs = [Case([1] * 4, [2500, 90, 10, 700], 4, 2, 128, 16, seed=3), Case([120, 9], [700, 300], 4, 2, 128, 16, seed=4)]
+    dev, want = [c.device() for c in cs], [run(c) for c in cs]
+    outs, graphs = [torch.zeros_like(w) for w in want], []
+    for d, o in zip(dev, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            lla.paged_parallax(**d, out=o)
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = [lla.paged_parallax(**d) for d in dev]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(outs + eager, want + want))
+    lla.lla_sync_status()
+
+
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("fp32", 32)])
 @pytest.mark.parametrize("new", [[1, 1], [30, 80]])
 def test_bad_lengths_and_pages_are_cut_and_reported(lla_gpu, dtype, d, new):
     """What the device arrays hold is never followed outside the tensors: the kernels compare every

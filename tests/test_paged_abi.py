@@ -46,7 +46,7 @@ def _append(lib, **kw):
 @pytest.mark.parametrize("bad", [
     dict(k=None), dict(v=None), dict(slots=None), dict(kc=None), dict(vc=None), dict(k=24), dict(vc=8), dict(slots=52),
     dict(dtype=2), dict(d=48), dict(d=0), dict(page=12), dict(T=0), dict(Hkv=0), dict(P=0), dict(ks=120), dict(vs=130),
-    dict(ps=2047), dict(ps=2052), dict(ks=-128),
+    dict(ps=2047), dict(ps=2052), dict(ps=2056), dict(ks=-128), dict(P=1 << 30, ps=2048),
 ])
 def test_append_refusals(lib, bad):
     assert _append(lib, **bad) == lla.LLA_ERR_INVALID_ARG
@@ -67,7 +67,7 @@ def _attend(lib, **kw):
     dict(out=None), dict(q=24), dict(r=40), dict(kc=8), dict(out=132), dict(table=82), dict(cu=97), dict(kv=3),
     dict(T=0), dict(S=0), dict(S=(1 << 20) + 1), dict(Hq=0), dict(Hkv=0), dict(Hq=5), dict(Hq=4096, Hkv=2, qs=1 << 20),
     dict(d=48), dict(d=256), dict(page=7), dict(page=1024), dict(P=0), dict(W=0), dict(W=1 << 25), dict(max_new=0),
-    dict(qs=255), dict(rs=252), dict(qs=260), dict(ps=1024), dict(ps=2050), dict(tau=0.0), dict(tau=-1.0),
+    dict(qs=255), dict(rs=252), dict(qs=260), dict(ps=1024), dict(ps=2050), dict(ps=2056), dict(ps=2560), dict(tau=0.0), dict(tau=-1.0),
     dict(tau=float("nan")), dict(tau=float("inf")), dict(dtype=4), dict(path=3), dict(path=-1), dict(T=1 << 29),
 ])
 def test_attention_refusals(lib, bad):
