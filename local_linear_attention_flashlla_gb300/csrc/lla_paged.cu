@@ -169,20 +169,35 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
     const int total_rows = (int)(red[0] < a.T ? red[0] : a.T);
     taken = taken_sh;
 
-    for (int t = rank * kPlanThreads + tid; t < a.T; t += ranks * kPlanThreads) {
-        long long slot = -1;
-        int pos = 0;
-        if (t < total_rows) {
-            const int s = bisect(cu, a.S, t);
-            pos = ctx[s] + (t - cu[s]);
-            if (okay[s]) {
-                const int lp = pos >> a.page_shift, held = (ctx[s] + page - 1) >> a.page_shift;
-                const int id = lp < held ? a.table[(size_t)s * a.width + lp] : a.free_pages[have - 1 - (base[s] + lp - held)];
-                if (id >= 0) slot = ((long long)id << a.page_shift) + (pos & (page - 1));
+    // a warp takes runs of 32 kRun rows, a lane every 32nd of them: a bisection where the sequence changes, the table
+    // reads side by side
+    constexpr int kRun = 4;
+    const int lane = tid & 31, warps = ranks * (kPlanThreads / 32);
+    for (int t0 = (rank * (kPlanThreads / 32) + (tid >> 5)) * 32 * kRun; t0 < a.T; t0 += warps * 32 * kRun) {
+        int pos[kRun], id[kRun], s = bisect(cu, a.S, min(t0 + lane, max(total_rows - 1, 0)));
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            const int t = t0 + lane + 32 * i;
+            pos[i] = 0;
+            id[i] = -1;
+            if (t < total_rows) {
+                if (s + 1 < a.S && cu[s + 1] <= t) s += 1 + bisect(cu + s + 1, a.S - s - 1, t);   // another sequence
+                pos[i] = ctx[s] + (t - cu[s]);
+                if (okay[s]) {
+                    const int lp = pos[i] >> a.page_shift, held = (ctx[s] + page - 1) >> a.page_shift;
+                    id[i] = lp < held ? a.table[(size_t)s * a.width + lp]
+                                      : a.free_pages[have - 1 - (base[s] + lp - held)];
+                }
             }
         }
-        a.slots[t] = slot;
-        if (a.positions) a.positions[t] = pos;
+#pragma unroll
+        for (int i = 0; i < kRun; ++i) {
+            const int t = t0 + lane + 32 * i;
+            if (t < a.T) {
+                a.slots[t] = id[i] >= 0 ? ((long long)id[i] << a.page_shift) + (pos[i] & (page - 1)) : -1;
+                if (a.positions) a.positions[t] = pos[i];
+            }
+        }
     }
     for (int k = rank * kPlanThreads + tid; k < taken; k += ranks * kPlanThreads) {
         const int s = bisect(base, a.S, k);

@@ -13,6 +13,7 @@
 #include "../../include/lla.h"
 #include "lla_internal.h"
 #include "lla_paged.h"
+#include "tc_ptx.cuh"
 
 namespace lla {
 namespace paged {
@@ -32,11 +33,11 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, float4 x) {
 
 constexpr int kThreads = 256;
 
-// R rows of a tile, TX threads to a row (they lie in one warp), BN keys of a block.
-template <int D, int R>
-struct Shape {
-    static constexpr int TX = kThreads / R;
-    static constexpr int BN = R == 32 ? 32 : 64;
+// Few rows (a decode step): eight rows of a tile, a warp to a row, a lane two of the 64 keys of a block; warps without
+// a row only help to load, and reading the cache bounds it.
+template <int D>
+struct FewShape {
+    static constexpr int R = 8, BN = 64, TX = 32;
     static constexpr int KPT = BN / TX;                 // keys of a thread
     static constexpr int CPT = (D + TX - 1) / TX;       // output columns of a thread,
     static constexpr int VW = CPT < 4 ? CPT : 4;        // this many side by side
@@ -57,10 +58,59 @@ struct SimtArgs {
     float scale;     // tau log2(e)
 };
 
-template <typename T, int D, int R>
-__global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
-    using Sh = Shape<D, R>;
-    constexpr int TX = Sh::TX, BN = Sh::BN, KPT = Sh::KPT, CPT = Sh::CPT, VW = Sh::VW, KS = Sh::KS, PS = Sh::PS;
+// 16 bytes of T as floats.
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4& raw, float* dst) {
+    const T* e = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+    for (int i = 0; i < (int)(16 / sizeof(T)); i += 4)
+        *reinterpret_cast<float4*>(dst + i) = make_float4(to_f(e[i]), to_f(e[i + 1]), to_f(e[i + 2]), to_f(e[i + 3]));
+}
+
+// The e-th 16-byte piece of K and of V of the block of `keys` keys from key0 on; zeros behind the last key that the
+// tile sees, whatever the page holds there.
+template <typename T, int D>
+__device__ __forceinline__ void fetch_piece(const SimtArgs& a, const Piece& p, int key0, int keys, int e, uint4& k, uint4& v) {
+    constexpr int VE = 16 / sizeof(T);
+    const Work& w = a.w;
+    const int kk = e / (D / VE), c = (e % (D / VE)) * VE, key = key0 + kk;
+    k = v = make_uint4(0, 0, 0, 0);
+    if (kk < keys && key < p.keys) {
+        const int page = w.table[(size_t)p.s * w.width + (key >> w.page_shift)];
+        if (page < 0 || page >= w.num_pages) {
+            atomicOr(w.err, (unsigned)kDevErrPagedArg);
+        } else {
+            const long long off = page * a.page_stride +
+                (((long long)p.h << w.page_shift) + (key & ((1 << w.page_shift) - 1))) * D + c;
+            k = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.k) + off);
+            v = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.v) + off);
+        }
+    }
+}
+
+// A tile's queries and probes, in fp32; rows behind its last are zeros.
+template <typename T, int D>
+__device__ __forceinline__ void load_tile_rows(const SimtArgs& a, const Piece& p, int rows, int threads, float* Qs, float* Rs) {
+    constexpr int VE = 16 / sizeof(T);
+    const Work& w = a.w;
+    for (int e = threadIdx.x; e < rows * (D / VE); e += threads) {
+        const int r = e / (D / VE), c = (e % (D / VE)) * VE;
+        uint4 x = make_uint4(0, 0, 0, 0), y = x;
+        if (r < p.rows) {
+            const int fr = p.row0 + r, tk = over_g(w, fr);
+            const long long token = p.q.token0 + tk, hc = (long long)(p.h * w.G + fr - tk * w.G) * D + c;
+            x = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + token * a.q_stride + hc);
+            y = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.probe) + token * a.r_stride + hc);
+        }
+        unpack<T>(x, Qs + r * D + c);
+        unpack<T>(y, Rs + r * D + c);
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 2) paged_simt_few_kernel(SimtArgs a) {
+    using Sh = FewShape<D>;
+    constexpr int R = Sh::R, TX = Sh::TX, BN = Sh::BN, KPT = Sh::KPT, CPT = Sh::CPT, VW = Sh::VW, KS = Sh::KS, PS = Sh::PS;
     constexpr int VE = 16 / sizeof(T);                  // elements of a 16-byte piece
     constexpr int PPT = (BN * D / VE + kThreads - 1) / kThreads;   // pieces of K (and of V) that a thread loads
     extern __shared__ __align__(16) float sm[];
@@ -73,10 +123,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
     float* P2 = P1 + R * PS;
     const Work& w = a.w;
     const int tid = threadIdx.x, row = tid / TX, tx = tid % TX;
-    const T* gq = static_cast<const T*>(a.q);
-    const T* gr = static_cast<const T*>(a.probe);
-    const T* gk = static_cast<const T*>(a.k);
-    const T* gv = static_cast<const T*>(a.v);
 
     cudaGridDependencySynchronize();           // the lengths may be the previous kernel's
     Walk wk = begin_walk(w, blockIdx.x, scratch);
@@ -88,44 +134,13 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
     uint4 kraw[PPT], vraw[PPT];
     auto fetch = [&](int j) {
 #pragma unroll
-        for (int i = 0; i < PPT; ++i) {
-            const int e = tid + i * kThreads, kk = e / (D / VE), c = (e % (D / VE)) * VE, key = j * BN + kk;
-            kraw[i] = vraw[i] = make_uint4(0, 0, 0, 0);  // keys that no row sees: zeros, whatever the page holds
-            if (e < BN * (D / VE) && key < p.keys) {
-                const int page = w.table[(size_t)p.s * w.width + (key >> w.page_shift)];
-                if (page < 0 || page >= w.num_pages) {
-                    atomicOr(w.err, (unsigned)kDevErrPagedArg);
-                } else {
-                    const long long off = page * a.page_stride +
-                        (((long long)p.h << w.page_shift) + (key & ((1 << w.page_shift) - 1))) * D + c;
-                    kraw[i] = *reinterpret_cast<const uint4*>(gk + off);
-                    vraw[i] = *reinterpret_cast<const uint4*>(gv + off);
-                }
-            }
-        }
-    };
-    auto unpack = [&](const uint4& raw, float* dst) {
-        const T* e = reinterpret_cast<const T*>(&raw);
-#pragma unroll
-        for (int i = 0; i < VE; i += 4)
-            *reinterpret_cast<float4*>(dst + i) = make_float4(to_f(e[i]), to_f(e[i + 1]), to_f(e[i + 2]), to_f(e[i + 3]));
+        for (int i = 0; i < PPT; ++i) fetch_piece<T, D>(a, p, j * BN, BN, tid + i * kThreads, kraw[i], vraw[i]);
     };
 
     while (next_piece(w, wk, p)) {
         shared = p.slot == 1;
         if (p.j0 < p.j1) fetch(p.j0);
-        for (int e = tid; e < R * (D / VE); e += kThreads) {
-            const int r = e / (D / VE), c = (e % (D / VE)) * VE;
-            uint4 x = make_uint4(0, 0, 0, 0), y = x;
-            if (r < p.rows) {
-                const int fr = p.row0 + r, tk = over_g(w, fr);
-                const long long token = p.q.token0 + tk, hc = (long long)(p.h * w.G + fr - tk * w.G) * D + c;
-                x = *reinterpret_cast<const uint4*>(gq + token * a.q_stride + hc);
-                y = *reinterpret_cast<const uint4*>(gr + token * a.r_stride + hc);
-            }
-            unpack(x, Qs + r * D + c);
-            unpack(y, Rs + r * D + c);
-        }
+        load_tile_rows<T, D>(a, p, R, kThreads, Qs, Rs);
         int limit = 0;                                   // keys this row sees
         if (row < p.rows) limit = w.causal ? min(max(p.q.L - p.q.nq + over_g(w, p.row0 + row) + 1, 0), p.q.L) : p.q.L;
         const bool busy = __any_sync(0xffffffffu, row < p.rows);   // a warp without rows only helps to load
@@ -140,8 +155,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
             for (int i = 0; i < PPT; ++i) {
                 const int e = tid + i * kThreads, kk = e / (D / VE), c = (e % (D / VE)) * VE;
                 if (e < BN * (D / VE)) {
-                    unpack(kraw[i], Ks + kk * KS + c);
-                    unpack(vraw[i], Vs + kk * D + c);
+                    unpack<T>(kraw[i], Ks + kk * KS + c);
+                    unpack<T>(vraw[i], Vs + kk * D + c);
                 }
             }
             __syncthreads();
@@ -260,6 +275,240 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_kernel(SimtArgs a) {
     if (tid == 0) write_header(w, blockIdx.x, p, shared);
 }
 
+// ------------------------------------------------------------------------------------------ many rows
+//
+// 32 rows to a tile, a warp to eight of them.  Its lanes are four pairs of rows by eight key columns: in the first
+// product a lane has two rows and an eighth of the keys, in the second the same rows and an eighth of the output
+// columns.  So a 16-byte read of K or V serves two rows and one of q, the probe or the weights eight keys or columns:
+// twelve reads to 128 products (a row a thread and four keys: six to 32), and shared-memory reads bound this kernel.
+// Products and sums are pairs of fp32 (fma.rn.f32x2: each rounded as the scalar instruction).
+constexpr int kManyThreads = 128;
+
+template <int D>
+struct ManyShape {
+    static constexpr int R = 32, BN = 32;
+    static constexpr int kCtas = D == 128 ? 2 : D == 64 ? 3 : 4;   // to an SM (registers)
+    static constexpr int KPT = BN / 8;                  // keys of a lane
+    static constexpr int CPT = D / 8;                   // output columns of a lane, in runs of VW
+    static constexpr int VW = CPT < 4 ? CPT : 4;
+    static constexpr int KS = D + 4, PS = BN + 4;       // row strides of K and of the weights
+    static constexpr size_t smem = sizeof(float) * (2 * R * D + BN * KS + BN * D + 2 * R * PS);
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kManyThreads, ManyShape<D>::kCtas) paged_simt_many_kernel(SimtArgs a) {
+    using Sh = ManyShape<D>;
+    constexpr int R = Sh::R, BN = Sh::BN, KPT = Sh::KPT, CPT = Sh::CPT, VW = Sh::VW, KS = Sh::KS, PS = Sh::PS;
+    constexpr int VE = 16 / sizeof(T);
+    constexpr int PPT = (BN * D / VE + kManyThreads - 1) / kManyThreads;
+    extern __shared__ __align__(16) float sm[];
+    __shared__ long long scratch[40];
+    float* Qs = sm;
+    float* Rs = Qs + R * D;
+    float* Ks = Rs + R * D;
+    float* Vs = Ks + BN * KS;
+    float* P1 = Vs + BN * D;
+    float* P2 = P1 + R * PS;
+    const Work& w = a.w;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int row = warp * 8 + (lane >> 3) * 2, g8 = lane & 7;   // the lane's first row; its key and column group
+
+    cudaGridDependencySynchronize();           // the lengths may be the previous kernel's
+    Walk wk = begin_walk(w, blockIdx.x, scratch);
+    cudaTriggerProgrammaticLaunchCompletion();   // the merge waits for this grid's end all the same
+    Piece p;
+    p.parts = 0; p.row0 = p.rows = p.h = 0; p.q.token0 = 0;
+    bool shared = false;
+    uint4 kraw[PPT], vraw[PPT];                // a block of K and V on its way, while the one before is computed
+    auto fetch = [&](int j) {
+#pragma unroll
+        for (int i = 0; i < PPT; ++i) fetch_piece<T, D>(a, p, j * BN, BN, tid + i * kManyThreads, kraw[i], vraw[i]);
+    };
+
+    while (next_piece(w, wk, p)) {
+        shared = p.slot == 1;
+        if (p.j0 < p.j1) fetch(p.j0);
+        load_tile_rows<T, D>(a, p, R, kManyThreads, Qs, Rs);
+        const bool busy = warp * 8 < p.rows;             // a warp without rows only helps to load
+        int limit[2];                                    // keys a row sees
+        float m[2], om[2], A[2], s0[2];                  // om, A: this lane's keys
+        uint64_t o1[2][CPT / 2], o2[2][CPT / 2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            limit[i] = 0;
+            if (row + i < p.rows)
+                limit[i] = w.causal ? min(max(p.q.L - p.q.nq + over_g(w, p.row0 + row + i) + 1, 0), p.q.L) : p.q.L;
+            m[i] = -INFINITY;
+            om[i] = A[i] = s0[i] = 0.f;
+#pragma unroll
+            for (int c = 0; c < CPT / 2; ++c) o1[i][c] = o2[i][c] = tc::f2_pack(0.f, 0.f);
+        }
+
+        for (int j = p.j0; j < p.j1; ++j) {
+            const int key0 = j * BN;
+#pragma unroll
+            for (int i = 0; i < PPT; ++i) {
+                const int e = tid + i * kManyThreads, kk = e / (D / VE), c = (e % (D / VE)) * VE;
+                if (e < BN * (D / VE)) {
+                    unpack<T>(kraw[i], Ks + kk * KS + c);
+                    unpack<T>(vraw[i], Vs + kk * D + c);
+                }
+            }
+            __syncthreads();
+            if (j + 1 < p.j1) fetch(j + 1);
+            if (busy) {
+                float s[2][KPT], t[2][KPT];
+                {
+                    uint64_t s2[2][KPT], t2[2][KPT];     // even and odd columns apart
+#pragma unroll
+                    for (int u = 0; u < KPT; ++u) s2[0][u] = s2[1][u] = t2[0][u] = t2[1][u] = tc::f2_pack(0.f, 0.f);
+#pragma unroll 2
+                    for (int c = 0; c < D; c += 4) {
+                        ulonglong2 q4[2], r4[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            q4[i] = *reinterpret_cast<const ulonglong2*>(Qs + (row + i) * D + c);
+                            r4[i] = *reinterpret_cast<const ulonglong2*>(Rs + (row + i) * D + c);
+                        }
+#pragma unroll
+                        for (int u = 0; u < KPT; ++u) {
+                            const ulonglong2 k4 = *reinterpret_cast<const ulonglong2*>(Ks + (g8 + 8 * u) * KS + c);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                s2[i][u] = tc::f2_fma(q4[i].y, k4.y, tc::f2_fma(q4[i].x, k4.x, s2[i][u]));
+                                t2[i][u] = tc::f2_fma(r4[i].y, k4.y, tc::f2_fma(r4[i].x, k4.x, t2[i][u]));
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int u = 0; u < KPT; ++u) {
+                            float x, y;
+                            tc::f2_unpack(s2[i][u], x, y);
+                            s[i][u] = x + y;
+                            tc::f2_unpack(t2[i][u], x, y);
+                            t[i][u] = x + y;
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float bm = -INFINITY;
+#pragma unroll
+                    for (int u = 0; u < KPT; ++u) {
+                        s[i][u] = key0 + g8 + 8 * u < limit[i] ? s[i][u] * a.scale : -INFINITY;
+                        bm = fmaxf(bm, s[i][u]);
+                    }
+#pragma unroll
+                    for (int o = 4; o; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
+                    const float mn = fmaxf(m[i], bm), base = mn == -INFINITY ? 0.f : mn;
+                    const bool first = m[i] == -INFINITY;    // the row's first block with keys
+                    const float corr = exp2f(m[i] - base);   // m = -inf: 0
+                    const uint64_t c2 = tc::f2_pack(corr, corr);
+                    om[i] *= corr;
+                    A[i] *= corr;
+#pragma unroll
+                    for (int c = 0; c < CPT / 2; ++c) {
+                        o1[i][c] = tc::f2_mul(o1[i][c], c2);
+                        o2[i][c] = tc::f2_mul(o2[i][c], c2);
+                    }
+                    m[i] = mn;
+                    float ps = 0.f, pt = 0.f;
+#pragma unroll
+                    for (int u = 0; u < KPT; ++u) {
+                        s[i][u] = exp2f(s[i][u] - base);
+                        ps += s[i][u];
+                        pt = fmaf(s[i][u], t[i][u], pt);
+                    }
+                    float x = ps, y = pt;
+#pragma unroll
+                    for (int o = 4; o; o >>= 1) {
+                        x += __shfl_xor_sync(0xffffffffu, x, o);
+                        y += __shfl_xor_sync(0xffffffffu, y, o);
+                    }
+                    if (first) s0[i] = x > 0.f ? y / x : 0.f;
+                    om[i] += ps;
+#pragma unroll
+                    for (int u = 0; u < KPT; ++u) {
+                        const float z = s[i][u] * (t[i][u] - s0[i]);
+                        A[i] += z;
+                        P1[(row + i) * PS + g8 + 8 * u] = s[i][u];
+                        P2[(row + i) * PS + g8 + 8 * u] = z;
+                    }
+                }
+                __syncwarp();
+#pragma unroll 2
+                for (int kk = 0; kk < BN; kk += 4) {
+                    float w1[2][4], w2[2][4];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        *reinterpret_cast<float4*>(w1[i]) = *reinterpret_cast<const float4*>(P1 + (row + i) * PS + kk);
+                        *reinterpret_cast<float4*>(w2[i]) = *reinterpret_cast<const float4*>(P2 + (row + i) * PS + kk);
+                    }
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+#pragma unroll
+                        for (int g = 0; g < CPT / VW; ++g) {
+                            const float* src = Vs + (kk + x) * D + (g8 + 8 * g) * VW;
+                            uint64_t v[VW / 2];
+                            if constexpr (VW == 4) {
+                                const ulonglong2 y = *reinterpret_cast<const ulonglong2*>(src);
+                                v[0] = y.x;
+                                v[VW / 2 - 1] = y.y;
+                            } else {
+                                v[0] = *reinterpret_cast<const uint64_t*>(src);
+                            }
+#pragma unroll
+                            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                                for (int c = 0; c < VW / 2; ++c) {
+                                    const int n = g * (VW / 2) + c;
+                                    o1[i][n] = tc::f2_fma(tc::f2_pack(w1[i][x], w1[i][x]), v[c], o1[i][n]);
+                                    o2[i][n] = tc::f2_fma(tc::f2_pack(w2[i][x], w2[i][x]), v[c], o2[i][n]);
+                                }
+                        }
+                    }
+                }
+            }
+            __syncthreads();
+        }
+
+        if (busy) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int o = 4; o; o >>= 1) {
+                    om[i] += __shfl_xor_sync(0xffffffffu, om[i], o);
+                    A[i] += __shfl_xor_sync(0xffffffffu, A[i], o);
+                }
+                const int r = row + i;
+                if (r >= p.rows) continue;
+                const int fr = p.row0 + r, tk = over_g(w, fr);
+                T* o = static_cast<T*>(a.out) + ((long long)(p.q.token0 + tk) * a.Hq + p.h * w.G + fr - tk * w.G) * D;
+                float4* ps = p.slot >= 0 ? part_sums(w, blockIdx.x, p.slot, D) : nullptr;
+                if (p.slot >= 0 && g8 == 0) part_stats(w, blockIdx.x, p.slot, D)[r] = make_float4(m[i], om[i], A[i], s0[i]);
+                const float inv = om[i] != 0.f ? 1.f / om[i] : 0.f, c1 = 1.f + A[i] * inv;
+#pragma unroll
+                for (int n = 0; n < CPT / 2; ++n) {
+                    const int c = (g8 + 8 * (2 * n / VW)) * VW + 2 * n % VW;
+                    float x1, y1, x2, y2;
+                    tc::f2_unpack(o1[i][n], x1, y1);
+                    tc::f2_unpack(o2[i][n], x2, y2);
+                    if (p.slot < 0) {
+                        put(o + c, (c1 * x1 - x2) * inv);
+                        put(o + c + 1, (c1 * y1 - y2) * inv);
+                    } else {
+                        *reinterpret_cast<float2*>(part_element(ps, R, D, 0, r, c)) = make_float2(x1, y1);
+                        *reinterpret_cast<float2*>(part_element(ps, R, D, 1, r, c)) = make_float2(x2, y2);
+                    }
+                }
+            }
+        }
+        __syncthreads();
+    }
+    if (tid == 0) write_header(w, blockIdx.x, p, shared);
+}
+
 // Joins the parts of the tile that CTA blockIdx.x starts and others finish: part 0 is its slot 1, part
 // i > 0 slot 0 of CTA blockIdx.x + i.  With the common maximum and one centre,
 //   out = sum_i f_i ((1 + A/w - (s0_i - s0)) O1_i - O2_i) / w,   f_i = 2^(m_i - m).
@@ -362,23 +611,23 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(Work w, T* __restrict_
     }
 }
 
-template <typename T, int D, int R>
+template <typename T, int D>
 cudaError_t launch_one(const SimtArgs& a, cudaStream_t stream) {
-    constexpr size_t smem = Shape<D, R>::smem;
-    auto* kern = paged_simt_kernel<T, D, R>;
+    const bool few = a.w.rows == 8;
+    auto* kern = few ? paged_simt_few_kernel<T, D> : paged_simt_many_kernel<T, D>;
+    const size_t smem = few ? FewShape<D>::smem : ManyShape<D>::smem;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_after(kern, dim3(a.w.ctas), kThreads, smem, stream, a);
+    return launch_after(kern, dim3(a.w.ctas), few ? kThreads : kManyThreads, smem, stream, a);
 }
 
 template <typename T>
 cudaError_t launch_typed(const SimtArgs& a, int d, cudaStream_t stream) {
-    const bool few = a.w.rows == 8;
     switch (d) {
-        case 16: return few ? launch_one<T, 16, 8>(a, stream) : launch_one<T, 16, 32>(a, stream);
-        case 32: return few ? launch_one<T, 32, 8>(a, stream) : launch_one<T, 32, 32>(a, stream);
-        case 64: return few ? launch_one<T, 64, 8>(a, stream) : launch_one<T, 64, 32>(a, stream);
-        default: return few ? launch_one<T, 128, 8>(a, stream) : launch_one<T, 128, 32>(a, stream);
+        case 16: return launch_one<T, 16>(a, stream);
+        case 32: return launch_one<T, 32>(a, stream);
+        case 64: return launch_one<T, 64>(a, stream);
+        default: return launch_one<T, 128>(a, stream);
     }
 }
 
@@ -415,7 +664,8 @@ cudaError_t merge_typed(const Work& w, void* out, int Hq, int d, cudaStream_t st
 PagedSplit paged_simt_split(const PagedProblem& p, int sms) {
     // rows: 8 where no sequence has more than eight query rows to a key head (a decode step), else 32
     const bool few = (long long)p.max_new * p.G <= 8;
-    return PagedSplit{few ? 8 : 32, few ? 64 : 32, 2 * sms, 2, 0};
+    if (few) return PagedSplit{8, 64, 2 * sms, 2, 0};
+    return PagedSplit{32, paged::ManyShape<128>::BN, (p.d == 128 ? paged::ManyShape<128>::kCtas : p.d == 64 ? paged::ManyShape<64>::kCtas : paged::ManyShape<32>::kCtas) * sms, 2, 0};
 }
 
 cudaError_t launch_paged_simt(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream) {
