@@ -592,6 +592,27 @@ def _paged_workspace_bytes(device_index, dtype, path, Hq, Hkv, d, page_size, max
     return lla_paged_parallax_workspace_size(dtype, path, 1, 1, Hq, Hkv, d, page_size, 1, max_new)
 
 
+_BIND = None
+
+
+def _bind():
+    """The marshalling module (csrc/paged_bind.c), tied to the loaded library; False if it was not built."""
+    global _BIND
+    if _BIND is None:
+        import torch
+        lib = load_library()
+        try:
+            from . import _paged_bind as m
+        except ImportError:
+            _BIND = False
+        else:
+            m.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (lib.lla_paged_plan, lib.lla_paged_append,
+                                                                      lib.lla_paged_parallax)),
+                   torch.bfloat16, torch.float32, torch.int32, torch.int64)
+            _BIND = m
+    return _BIND
+
+
 # Scratch of eager attention calls by (device, stream, host thread): a thread's calls on one stream follow one
 # another, so they can share it, and taking it from the allocator costs as much as all checks.  A call under
 # graph capture takes its own (the graph keeps it), so that graphs never share scratch with anything.  At most
@@ -634,6 +655,14 @@ def paged_plan(ctx_lens, new_lens, block_table, free_pages, free_count, page_siz
                               cu_q=cu_q, slots=slots, positions=positions, granted=granted, free_left=free_left)
     if block_table.dim() != 2 or T < 1:
         raise _bad("block_table must be [S, W] and num_rows >= 1")
+    stream_ptr = torch._C._cuda_getCurrentRawStream(dev.index)
+    if kv_lens is cu_q is slots is positions is granted is free_left is None and _bind():
+        S, empty, like = ctx_lens.shape[0] if ctx_lens.dim() else 0, torch.empty, torch.empty_like
+        r = PagedPlan(like(ctx_lens), empty(S + 1, dtype=i32, device=dev), empty(T, dtype=i64, device=dev),
+                      empty(T, dtype=i32, device=dev), like(ctx_lens), like(free_count))
+        if _BIND.plan(dev.index, ctx_lens, new_lens, block_table, free_pages, free_count, page_size, T, r[0], r[1], r[2],
+                      r[3], r[4], r[5], stream_ptr) == LLA_OK:
+            return r
     S, W, F = ctx_lens.numel(), block_table.shape[1], free_pages.numel()
     ctx_ptr, new_ptr = _ints("ctx_lens", ctx_lens, (S,), i32, dev), _ints("new_lens", new_lens, (S,), i32, dev)
     table_ptr = _ints("block_table", block_table, (S, W), i32, dev)
@@ -647,8 +676,7 @@ def paged_plan(ctx_lens, new_lens, block_table, free_pages, free_count, page_siz
     positions = empty(T, dtype=i32, device=dev) if positions is None else _same("positions", positions, (T,), i32, dev)
     status = load_library().lla_paged_plan(
         ctx_ptr, new_ptr, S, int(page_size), table_ptr, W, free_ptr, F, count_ptr, T, kv_lens.data_ptr(), cu_q.data_ptr(),
-        slots.data_ptr(), positions.data_ptr(), granted.data_ptr(), free_left.data_ptr(),
-        torch._C._cuda_getCurrentRawStream(dev.index))
+        slots.data_ptr(), positions.data_ptr(), granted.data_ptr(), free_left.data_ptr(), stream_ptr)
     if status != LLA_OK:
         _check(status)
     return PagedPlan(kv_lens, cu_q, slots, positions, granted, free_left)
@@ -659,6 +687,10 @@ def paged_append(k_new, v_new, slots, k_cache, v_cache, *, stream=None):
     (int64, a plan's; rows with a negative slot are skipped).  In place, asynchronous on the current (or
     given) stream.  Rows may be slices of a fused projection (any 16-byte token stride)."""
     import torch
+    if stream is None and k_cache.is_cuda and _bind():
+        index = torch.cuda.current_device()
+        if _BIND.append(index, k_new, v_new, slots, k_cache, v_cache, torch._C._cuda_getCurrentRawStream(index)) == LLA_OK:
+            return
     P, Hkv, Z, d, page_stride, dtype = _check_caches(k_cache, v_cache)
     dev = k_cache.device
     if stream is not None or dev.index != torch.cuda.current_device():
@@ -689,6 +721,15 @@ def paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, 
     same time.
     """
     import torch
+    if stream is None and workspace is None and k_cache.is_cuda and _bind():
+        index = torch.cuda.current_device()
+        stream_ptr = torch._C._cuda_getCurrentRawStream(index)
+        t = _SCRATCH.get((index, stream_ptr, threading.get_ident()))
+        if t is not None and not torch.cuda.is_current_stream_capturing():
+            res = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
+            if _BIND.parallax(index, q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, res, tau, max_new, causal, path,
+                              t.data_ptr(), t.numel(), stream_ptr) == LLA_OK:
+                return res
     P, Hkv, Z, d, page_stride, dtype = _check_caches(k_cache, v_cache)
     dev = k_cache.device
     if stream is not None or dev.index != torch.cuda.current_device():

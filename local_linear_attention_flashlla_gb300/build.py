@@ -3,12 +3,16 @@
 Each CUDA translation unit under csrc/ is compiled in parallel to an object in
 _build/, then linked into liblla.so next to this file.  No CMake, no torch
 extension machinery: the library has a plain C ABI (include/lla.h).
+csrc/paged_bind.c, the paged calls' argument marshalling, becomes the extension
+module _paged_bind where the Python headers are there; without it the binding
+marshals in Python.
 """
 from __future__ import annotations
 
 import os
 import shutil
 import subprocess
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -16,6 +20,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "liblla.so")
+BIND = os.path.join(PKG, "_paged_bind.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -41,6 +46,18 @@ def _run(cmd):
     return r.stdout
 
 
+def build_binding():
+    """Compile _paged_bind.so; returns its path, or None without a C compiler or the Python headers."""
+    include = sysconfig.get_paths()["include"]
+    cc = shutil.which("gcc") or shutil.which("cc")
+    if not cc or not os.path.exists(os.path.join(include, "Python.h")):
+        return None
+    tmp = BIND + ".tmp"
+    _run([cc, "-O2", "-shared", "-fPIC", "-I" + include, os.path.join(CSRC, "paged_bind.c"), "-o", tmp])
+    os.replace(tmp, BIND)
+    return BIND
+
+
 def build(verbose=False, extra_flags=()):
     """Build liblla.so; returns its path."""
     nvcc = nvcc_path()
@@ -50,6 +67,7 @@ def build(verbose=False, extra_flags=()):
     for lib, srcs in groups.items():
         for s in srcs:
             jobs.append((lib, s, os.path.join(BUILD, os.path.basename(s)[:-3] + ".o")))
+    build_binding()
     cmds = [[nvcc, *ARCH, *NVFLAGS, *extra_flags, "-c", s, "-o", o] for _, s, o in jobs]
     with ThreadPoolExecutor(max_workers=max(1, min(len(cmds), os.cpu_count() or 1))) as ex:
         outs = list(ex.map(_run, cmds))

@@ -429,6 +429,26 @@ def test_rows_of_others_and_padding_do_not_reach_a_sequence(lla_gpu, dtype, d, n
         assert torch.isfinite(other[:c.cu[-1]]).all()
 
 
+def test_both_ways_of_marshalling_give_the_same_bits(lla_gpu, monkeypatch):
+    """The calls through csrc/paged_bind.c and through Python launch the same."""
+    c = Case([1, 4, 1], [300, 70, 130], 4, 2, 64, 16, pad=2)
+    ctx, new, table, free, count, T = _plan_case(3, 20, 16, 2, 60, 5, None, None)
+
+    def all_calls():
+        tb = _i32(table)
+        pl = lla.paged_plan(_i32(ctx), _i32(new), tb, _i32(free), _i32([count]), 16, T)
+        kc, vc = torch.zeros(5000, 2, 16, 64, device="cuda"), torch.zeros(5000, 2, 16, 64, device="cuda")
+        k = torch.arange(T * 128, dtype=torch.float32, device="cuda").view(T, 2, 64)
+        lla.paged_append(k, -k, pl.slots, kc, vc)
+        return [*pl, tb, kc, vc, run(c)[:6]]
+
+    assert lla._bind()
+    fast = all_calls()
+    monkeypatch.setattr(lla, "_BIND", False)
+    slow = all_calls()
+    assert all(torch.equal(a, b) for a, b in zip(fast, slow))
+
+
 def test_max_new_may_be_larger(lla_gpu):
     for d in (64, 128):
         c = Case([1, 1, 2], [300, 70, 130], 4, 2, d, 16, pad=5)

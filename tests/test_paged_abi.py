@@ -102,6 +102,27 @@ def test_binding_refuses_cpu_tensors():
         lla.paged_parallax(x, x, c, c, torch.zeros(1, 2, dtype=torch.int32), i[:2], i[:1], 0.1, 4)
 
 
+def test_marshalling_module_hands_back_what_it_does_not_know(lib):
+    """csrc/paged_bind.c never raises on an argument and launches nothing for one that is not as expected."""
+    torch = pytest.importorskip("torch")
+    from local_linear_attention_flashlla_gb300 import _bind
+    m = _bind()
+    if not m:
+        pytest.skip("built without a C compiler or the Python headers")
+    i = torch.zeros(4, dtype=torch.int32)
+    c, x, s = torch.zeros(2, 1, 16, 64), torch.zeros(4, 1, 64), torch.zeros(4, dtype=torch.int64)
+    tb = torch.zeros(1, 2, dtype=torch.int32)
+    for k in (c, None, 3, "cache", c[0], c.half(), c.transpose(1, 2)):            # CPU tensors: device -1, never 0
+        assert m.append(0, x, x, s, k, k, 0) == -1
+        assert m.parallax(0, x, x, k, k, tb, i[:2], i[:1], x, 0.1, 1, True, 0, 0, 0, 0) == -1
+    assert m.append(-1, x, x, s, c, c, 0) == -1
+    assert m.parallax(0, x, x, c, c, tb, i[:2], i[:1], x, "tau", 1, True, 0, 0, 0, 0) == -1
+    assert m.parallax(0, x, x, c, c, tb, i[:2], i[:1], x, 0.1, 1 << 80, True, 0, 0, 0, 0) == -1
+    assert m.plan(0, i, i, tb, i, i[:1], 16, 4, i, i, s, i, i, i, 0) == -1
+    assert m.plan(0, None, i, tb, i, i[:1], 16, 4, i, i, s, i, i, i, 0) == -1
+    assert m.plan(0, i) == -1 and m.append() == -1 and m.parallax(0) == -1
+
+
 def test_token_rows_are_taken_as_they_lie_or_copied():
     """The binding's row check, on CPU tensors: packed heads at any 16-byte token stride pass as they are."""
     torch = pytest.importorskip("torch")
