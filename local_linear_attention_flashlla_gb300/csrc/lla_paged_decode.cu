@@ -408,7 +408,7 @@ cudaError_t launch_dec(const DecArgs& a, const CUtensorMap& mk, const CUtensorMa
 bool paged_decode_fits(const PagedProblem& p) { return (long long)p.max_new * p.G <= 16; }
 
 PagedSplit paged_decode_split(const PagedProblem& p, int sms) {
-    return PagedSplit{(long long)p.max_new * p.G <= 8 ? 8 : 16, paged::kKeys, 2 * sms, 4, 1};
+    return PagedSplit{(long long)p.max_new * p.G <= 8 ? 8 : 16, paged::kKeys, 2 * sms, 4, 2};
 }
 
 cudaError_t launch_paged_decode(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream, const char** why) {
