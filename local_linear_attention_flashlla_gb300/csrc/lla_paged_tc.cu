@@ -7,6 +7,9 @@
 // that they came from.  The products are issued as
 //     S(j+1)  O2(j)  T(j+1)  O1(j+1)  S(j+2)  O2(j+1) ...
 // : the softmax of S(j+1) runs under O2(j) and T(j+1), the weighting of T(j+1) under O1(j+1) and S(j+2).
+// 512 tokens over 16,384 keys, 32 query / 4 key heads, d = 128: 177 us, 1.58 PFLOP/s (a block takes 2700 cycles,
+// its products 2048); prompts of 700 to 4096 tokens, 16 heads: 257 us, 1.17 PFLOP/s (a tile's first and last block
+// and its epilogue cost 4000 cycles).  At d = 64 the row warps bound it, 2300 cycles a block.
 //
 // Eight warps hold the rows, a thread half of a row's columns.  The exponents are taken against the
 // reference point of the blocks before while the maximum is taken beside them, and only the vote of a
@@ -456,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nb = p.j1 - p.j0;
             const int tk = over_g(w, min(p.row0 + r, p.row0 + p.rows - 1));
             float m = -INFINITY, om = 0.f, A = 0.f, s0 = 0.f;
-            // rows behind the tile's last compute on zeros and are not written
+            // rows behind the tile's last compute on whatever was loaded for them and are not written
             int limit = p.keys;
             if (r < p.rows && w.causal) limit = min(max(p.q.L - p.q.nq + tk + 1, 0), p.q.L);
             for (int j = 0; j < nb; ++j, ++n) {
