@@ -259,6 +259,39 @@ __device__ __forceinline__ long long block_scan(long long v, long long* sh, long
     return v;
 }
 
+// CTA cta's range of `total` units; false: it has none.
+__device__ __forceinline__ bool set_range(const Work& w, Walk& k, int cta, long long total) {
+    const long long most = (total + (1 << w.min_shift) - 1) >> w.min_shift;
+    k.active = (int)(most < w.ctas ? most : w.ctas);
+    if (cta >= k.active) return false;
+    k.share = div_units(total, k.active);
+    k.over = (int)(total - k.share * k.active);
+    k.u = range_start(k, cta);
+    k.end = range_start(k, cta + 1);
+    return true;
+}
+
+// The tile and block of a walk whose next unit is the rem-th of its sequence, `unit` units to a key head.
+__device__ __forceinline__ Walk find_tile(const Work& w, Walk k, long long rem, long long unit) {
+    const int lane = threadIdx.x & 31, tiles = tiles_of(w, k.q);
+    k.h = (int)div_units(rem, unit);
+    rem -= k.h * unit;
+    if (tiles > 1) {
+        int lo = 0;                                // the last tile with units_before <= rem: 32 probes at a time
+        for (int range = tiles; range > 1;) {
+            const int step = (range + 31) >> 5, probe = lo + lane * step;
+            const bool yes = lane * step < range && units_before(w, k.q, probe) <= rem;
+            lo += (__popc(__ballot_sync(0xffffffffu, yes)) - 1) * step;
+            range = min(step, tiles - lo);
+        }
+        k.i = lo;
+        rem -= units_before(w, k.q, lo);
+    }
+    k.j = (int)rem;
+    snap_start(w, k);
+    return k;
+}
+
 // Range of CTA `cta` and the tile it begins in.  Every thread of the block calls it; the shared scratch is
 // 40 long longs.  active = 0: no units at all.  blockDim.x is a multiple of 32.  A thread sums a run of
 // consecutive sequences, so that one scan finds the total and, with it, whose sequence the range begins in.
@@ -271,19 +304,38 @@ __device__ inline Walk begin_walk(const Work& w, int cta, long long* sh) {
     k.q.token0 = k.q.nq = k.q.L = 0;
     k.u = k.end = 0;
     long long mine = 0, unit = 0, total;           // unit: of a key head of the last sequence looked at
+    if (w.S <= 32) {
+        // a lane to a sequence, every warp for itself: no barrier
+        Seq q;
+        q.token0 = q.nq = q.L = 0;
+        if (lane < w.S) {
+            q = load_seq(w, lane);
+            unit = head_units(w, q);
+            mine = unit * w.Hkv;
+        }
+        long long inc = mine;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += t;
+        }
+        total = __shfl_sync(0xffffffffu, inc, 31);
+        if (!set_range(w, k, cta, total)) return k;
+        const unsigned here = __ballot_sync(0xffffffffu, k.u >= inc - mine && k.u < inc);
+        const int s = __ffs((int)here) - 1;
+        k.s = s;
+        k.q.token0 = __shfl_sync(0xffffffffu, q.token0, s);
+        k.q.nq = __shfl_sync(0xffffffffu, q.nq, s);
+        k.q.L = __shfl_sync(0xffffffffu, q.L, s);
+        unit = __shfl_sync(0xffffffffu, unit, s);
+        return find_tile(w, k, k.u - __shfl_sync(0xffffffffu, inc - mine, s), unit);
+    }
     for (int s = s0; s < s1; ++s) {
         k.q = load_seq(w, s);
         unit = head_units(w, k.q);
         mine += unit * w.Hkv;
     }
     long long pre = block_scan(mine, sh, &total) - mine;
-    const long long most = (total + (1 << w.min_shift) - 1) >> w.min_shift;
-    k.active = (int)(most < w.ctas ? most : w.ctas);
-    if (cta >= k.active) return k;
-    k.share = div_units(total, k.active);
-    k.over = (int)(total - k.share * k.active);
-    k.u = range_start(k, cta);
-    k.end = range_start(k, cta + 1);
+    if (!set_range(w, k, cta, total)) return k;
     int* at = reinterpret_cast<int*>(sh + 32);     // sequence, token0, nq, L
     if (k.u >= pre && k.u < pre + mine) {
         int s = s0;
@@ -308,25 +360,7 @@ __device__ inline Walk begin_walk(const Work& w, int cta, long long* sh) {
     k.q.token0 = at[1];
     k.q.nq = at[2];
     k.q.L = at[3];
-    long long rem = k.u - sh[36];
-    unit = sh[37];
-    const int tiles = tiles_of(w, k.q);
-    k.h = (int)div_units(rem, unit);
-    rem -= k.h * unit;
-    if (tiles > 1) {
-        int lo = 0;                                // the last tile with units_before <= rem: 32 probes at a time
-        for (int range = tiles; range > 1;) {
-            const int step = (range + 31) >> 5, probe = lo + lane * step;
-            const bool yes = lane * step < range && units_before(w, k.q, probe) <= rem;
-            lo += (__popc(__ballot_sync(0xffffffffu, yes)) - 1) * step;
-            range = min(step, tiles - lo);
-        }
-        k.i = lo;
-        rem -= units_before(w, k.q, lo);
-    }
-    k.j = (int)rem;
-    snap_start(w, k);
-    return k;
+    return find_tile(w, k, k.u - sh[36], sh[37]);
 }
 
 // The CTA's next piece of work: blocks [j0, j1) of a tile.

@@ -126,6 +126,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
+        tc::tma_prefetch_desc(&mk);
+        tc::tma_prefetch_desc(&mv);
         for (int i = 0; i < kStages; ++i) {
             tc::mbar_init(&full[i], 1);
             tc::mbar_init(&empty[i], kWarps);

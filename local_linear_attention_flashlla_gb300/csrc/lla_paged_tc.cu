@@ -399,6 +399,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (tid == 0) {
+        tma_prefetch_desc(&mk);
+        tma_prefetch_desc(&mv);
+        if (a.row_boxes) {
+            tma_prefetch_desc(&mq);
+            tma_prefetch_desc(&mr);
+        }
         for (int i = 0; i < NS; ++i) {
             mbar_init(&b.kfull[i], 1);
             mbar_init(&b.kempty[i], 1);
