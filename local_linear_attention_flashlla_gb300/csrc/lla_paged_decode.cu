@@ -8,11 +8,12 @@
 // hold O1 = sum p v and O2 = sum p (t - s0) v.  A 128-row tcgen05 tile would carry 8 to 16 useful
 // rows and wait for its row warps (2300 cycles per 128 keys at d = 64); here the tensor pipe is busy 17 % of the
 // time.  64 sequences x 16 heads at 4096 keys: 318 us, 6.75 TB/s; 96 ragged sequences (100 to 16,000 keys,
-// eight query heads to a key head, 16-row pages): 235 us, 6.4 TB/s.
+// eight query heads to a key head, 16-row pages): 230 us, 6.5 TB/s.
 //
 // A CTA has four computing warps, each with a quarter of every 64-key block and a running maximum of
 // its own, and one warp that feeds the blocks through a TMA ring (a box per page); two CTAs to an SM
-// keep 192 KB of the cache in flight.  The four warps' sums are joined once per tile.
+// keep 192 KB of the cache in flight.  The four warps' sums are joined once per tile, in the space of its
+// last block: slices of an own 8 KB cost two barriers each, 1 us of the 10.5 that a tile of one block takes.
 #include <math.h>
 
 #include "../../include/lla.h"
@@ -28,12 +29,13 @@ constexpr int kKeys = 64;                      // keys of a block
 constexpr int kWarps = 4;                      // computing warps
 constexpr int kThreads = (kWarps + 1) * 32;
 
-template <int D>
+template <int D, int MT>
 struct DecShape {
     static constexpr int kStages = D == 128 ? 3 : 6;
     static constexpr int kTile = kKeys * D * 2;            // bytes of a K (or V) block
-    static constexpr int kScratch = 8192;                  // joining the warps' sums
-    static constexpr size_t smem = (size_t)kStages * 2 * kTile + kScratch + 1024;   // 1024: alignment of the ring
+    static constexpr int kOperand = MT > 1 ? MT * (D / 16) * 512 : 0;   // the first operand, where registers do not hold it
+    static constexpr size_t smem = (size_t)kStages * 2 * kTile + kOperand + 1024;   // 1024: alignment of the ring
+    static_assert(kWarps * 2 * 8 * D * 4 <= 2 * kTile, "a block's space takes the warps' sums of eight rows");
 };
 
 struct DecArgs {
@@ -62,10 +64,10 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 // The feeding warp: one block after another of this CTA's pieces, a box to a lane.
-template <int D>
+template <int D, int MT>
 __device__ void feed(const Work& w, Walk wk, const CUtensorMap* mk, const CUtensorMap* mv, int slices, uint32_t ring,
                      uint64_t* full, uint64_t* empty, volatile int* err) {
-    constexpr int kStages = DecShape<D>::kStages, kTile = DecShape<D>::kTile;
+    constexpr int kStages = DecShape<D, MT>::kStages, kTile = DecShape<D, MT>::kTile;
     const int lane = threadIdx.x & 31;
     const int box = min(1 << w.page_shift, kBoxRows);        // rows of a box
     const int boxes = kKeys / box;                           // <= 8
@@ -105,12 +107,11 @@ __device__ void feed(const Work& w, Walk wk, const CUtensorMap* mk, const CUtens
 template <int D, int MT>
 __global__ void __launch_bounds__(kThreads, 2)
     paged_decode_kernel(DecArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-    using Sh = DecShape<D>;
+    using Sh = DecShape<D, MT>;
     constexpr int kStages = Sh::kStages, kTile = Sh::kTile;
     constexpr int KS = D / 16;                 // k steps of the first product
     constexpr int NT = D / 8;                  // column tiles of the second
     constexpr int R = 8 * MT;
-    constexpr int SW = Sh::kScratch / (kWarps * R * 2 * 4);   // columns joined at a time
     extern __shared__ unsigned char raw[];
     __shared__ long long scratch[40];
     __shared__ uint64_t full[kStages], empty[kStages];
@@ -118,10 +119,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __shared__ float4 stats[kWarps][R];
     unsigned char* base = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
     const uint32_t ring = tc::smem_u32(base);
-    float* join = reinterpret_cast<float*>(base + (size_t)kStages * 2 * kTile);
-    // MT > 1: the first operand, by lane; the space serves the join after the last block of a piece
-    uint32_t* qs = reinterpret_cast<uint32_t*>(join);
-    static_assert(MT == 1 || MT * KS * 4 * 32 * 4 <= Sh::kScratch, "operand space");
+    uint32_t* qs = reinterpret_cast<uint32_t*>(base + (size_t)kStages * 2 * kTile);   // MT > 1: first operand, by lane
     const Work& w = a.w;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
@@ -141,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
 
     if (warp == kWarps) {
-        feed<D>(w, wk, &mk, &mv, a.slices, ring, full, empty, &err);
+        feed<D, MT>(w, wk, &mk, &mv, a.slices, ring, full, empty, &err);
     } else {
         const int g = lane >> 2, c2 = (lane & 3) * 2;
         int stage = 0, phase = 0;
@@ -311,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                     }
                 }
+                if (j + 1 == p.j1) break;      // the last block's space serves the join before it is given back
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&empty[stage]);
                 if (++stage == kStages) {
@@ -345,50 +344,66 @@ __global__ void __launch_bounds__(kThreads, 2)
                     o[mt][n][1] *= f;
                 }
             }
+            // the sums of eight rows at a time, in the last block's space: [warp][O1, O2][row][column], columns swizzled by
+            // the row so that neither the writes nor the reads collide; then a thread has four columns of a row
+            float* sums = reinterpret_cast<float*>(base + (size_t)stage * 2 * kTile);
+            auto place = [&](int x, int half, int r, int c) { return ((x * 2 + half) * 8 + r) * D + (c ^ ((r & 3) << 3)); };
 #pragma unroll
-            for (int sl = 0; sl < D / SW; ++sl) {
+            for (int mt = 0; mt < MT; ++mt) {
+                if (mt > 0) tc::named_bar_sync(1, kWarps * 32);
+                if (p.j0 < p.j1) {
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int n = 0; n < SW / 8; ++n) {
-                        float* d1 = join + ((size_t)(warp * R + mt * 8 + g) * 2) * SW + n * 8 + c2;
-                        *reinterpret_cast<float2*>(d1) = make_float2(o[mt][sl * (SW / 8) + n][0], o[mt][sl * (SW / 8) + n][1]);
-                        *reinterpret_cast<float2*>(d1 + SW) = make_float2(o[mt][sl * (SW / 8) + n][2], o[mt][sl * (SW / 8) + n][3]);
+                    for (int n = 0; n < NT; ++n) {
+                        *reinterpret_cast<float2*>(sums + place(warp, 0, g, n * 8 + c2)) = make_float2(o[mt][n][0], o[mt][n][1]);
+                        *reinterpret_cast<float2*>(sums + place(warp, 1, g, n * 8 + c2)) = make_float2(o[mt][n][2], o[mt][n][3]);
                     }
-                tc::named_bar_sync(1, kWarps * 32);
-                for (int e = tid; e < R * SW; e += kWarps * 32) {
-                    const int r = e / SW, c = e % SW;
-                    if (r < p.rows) {
-                        float x1 = 0.f, x2 = 0.f, mm = -INFINITY, ow = 0.f, aw = 0.f;
-                        const float sref = stats[0][r].w;
+                    tc::named_bar_sync(1, kWarps * 32);
+                }
+#pragma unroll 1
+                for (int e = tid; e < 8 * (D / 4); e += kWarps * 32) {
+                    const int r8 = e / (D / 4), c = e % (D / 4) * 4, r = mt * 8 + r8;
+                    if (r >= p.rows) continue;
+                    float4 x1 = make_float4(0.f, 0.f, 0.f, 0.f), x2 = x1;
+                    float mm = -INFINITY, ow = 0.f, aw = 0.f;
+                    const float sref = stats[0][r].w;
 #pragma unroll
-                        for (int x = 0; x < kWarps; ++x) {
-                            x1 += join[((size_t)(x * R + r) * 2) * SW + c];
-                            x2 += join[((size_t)(x * R + r) * 2 + 1) * SW + c];
-                            mm = fmaxf(mm, stats[x][r].x);
-                        }
-                        const float mb = mm == -INFINITY ? 0.f : mm;
+                    for (int x = 0; x < kWarps; ++x) mm = fmaxf(mm, stats[x][r].x);
+                    const float mb = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
-                        for (int x = 0; x < kWarps; ++x) {
-                            const float4 st = stats[x][r];
-                            const float f = tc::ex2(st.x - mb);
-                            ow = fmaf(f, st.y, ow);
-                            aw = fmaf(f, fmaf(st.w - sref, st.y, st.z), aw);
+                    for (int x = 0; x < kWarps; ++x) {
+                        const float4 st = stats[x][r];
+                        const float f = tc::ex2(st.x - mb);
+                        ow = fmaf(f, st.y, ow);
+                        aw = fmaf(f, fmaf(st.w - sref, st.y, st.z), aw);
+                        if (p.j0 < p.j1) {
+                            const float4 y = *reinterpret_cast<const float4*>(sums + place(x, 0, r8, c));
+                            const float4 z = *reinterpret_cast<const float4*>(sums + place(x, 1, r8, c));
+                            x1.x += y.x; x1.y += y.y; x1.z += y.z; x1.w += y.w;
+                            x2.x += z.x; x2.y += z.y; x2.z += z.z; x2.w += z.w;
                         }
-                        if (p.slot < 0) {
-                            const int fr = p.row0 + r;
-                            const float inv = ow != 0.f ? 1.f / ow : 0.f;
-                            a.out[((long long)(p.q.token0 + over_g(w, fr)) * a.Hq + p.h * w.G + (fr - over_g(w, fr) * w.G)) * D + sl * SW + c] =
-                                __float2bfloat16_rn(((1.f + aw * inv) * x1 - x2) * inv);
-                        } else {
-                            float4* ps = part_sums(w, blockIdx.x, p.slot, D);
-                            *part_element(ps, R, D, 0, r, sl * SW + c) = x1;
-                            *part_element(ps, R, D, 1, r, sl * SW + c) = x2;
-                            if (sl == 0 && c == 0) part_stats(w, blockIdx.x, p.slot, D)[r] = make_float4(mm, ow, aw, sref);
-                        }
+                    }
+                    if (p.slot < 0) {
+                        const int fr = p.row0 + r, tk = over_g(w, fr);
+                        const float inv = ow != 0.f ? 1.f / ow : 0.f, c1 = (1.f + aw * inv) * inv;
+                        *reinterpret_cast<uint2*>(a.out + ((long long)(p.q.token0 + tk) * a.Hq + p.h * w.G + fr - tk * w.G) * D + c) =
+                            make_uint2(pack_bf16(c1 * x1.x - inv * x2.x, c1 * x1.y - inv * x2.y),
+                                       pack_bf16(c1 * x1.z - inv * x2.z, c1 * x1.w - inv * x2.w));
+                    } else {
+                        float4* ps = part_sums(w, blockIdx.x, p.slot, D) + (size_t)(c / 4) * R + r;
+                        ps[0] = x1;
+                        ps[(size_t)(D / 4) * R] = x2;
+                        if (c == 0) part_stats(w, blockIdx.x, p.slot, D)[r] = make_float4(mm, ow, aw, sref);
                     }
                 }
-                tc::named_bar_sync(1, kWarps * 32);
+            }
+            tc::fence_proxy_async_smem();      // the space's next copy is the async proxy's
+            tc::named_bar_sync(1, kWarps * 32);
+            if (ok && p.j0 < p.j1) {
+                if (lane == 0) tc::mbar_arrive(&empty[stage]);
+                if (++stage == kStages) {
+                    stage = 0;
+                    phase ^= 1;
+                }
             }
         }
         if (tid == 0) write_header(w, blockIdx.x, p, shared);
@@ -399,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 template <int D, int MT>
 cudaError_t launch_dec(const DecArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
-    constexpr size_t smem = DecShape<D>::smem;
+    constexpr size_t smem = DecShape<D, MT>::smem;
     auto* kern = paged_decode_kernel<D, MT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
