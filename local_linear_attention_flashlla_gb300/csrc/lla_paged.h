@@ -57,7 +57,7 @@ struct PagedSplit {
     int extra;      // units charged for a tile beside its blocks: what a tile costs before its first block and after its last
 };
 
-// bf16, d in {64, 128}, at most 16 query rows to a key head (max_new * G): lla_paged_decode.cu.
+// bf16, d in {64, 128}, at most 32 query rows to a key head (max_new * G): lla_paged_decode.cu.
 bool paged_decode_fits(const PagedProblem& p);
 PagedSplit paged_decode_split(const PagedProblem& p, int sms);
 cudaError_t launch_paged_decode(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream, const char** why);

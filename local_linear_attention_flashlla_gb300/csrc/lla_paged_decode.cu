@@ -1,19 +1,24 @@
 // Parallax attention over a paged bf16 cache for few query rows to a key head (a decode step, a few
 // drafted tokens): reading the cache bounds it, 2 d bytes of K and of V for 8 d flops per row.
 //
-// The query rows and their probes are stacked in one 16-row operand of mma.m16n8k16 (rows 0-7 the
+// Eight query rows and their probes are stacked in one 16-row operand of mma.m16n8k16 (rows 0-7 the
 // queries, 8-15 the probes of the same rows), so one product gives the logits and t = probe.k, and the
 // accumulator layout puts both of a (row, key) pair in one thread.  The weights p and p (t - s0) are
 // then, without any exchange, the two row halves of the second product's operand, whose accumulators
-// hold O1 = sum p v and O2 = sum p (t - s0) v.  A 128-row tcgen05 tile would carry 8 to 16 useful
+// hold O1 = sum p v and O2 = sum p (t - s0) v.  A 128-row tcgen05 tile would carry 8 to 32 useful
 // rows and wait for its row warps (2300 cycles per 128 keys at d = 64); here the tensor pipe is busy 17 % of the
-// time.  64 sequences x 16 heads at 4096 keys: 318 us, 6.75 TB/s; 96 ragged sequences (100 to 16,000 keys,
-// eight query heads to a key head, 16-row pages): 230 us, 6.5 TB/s.
+// time with eight rows.  64 sequences x 16 heads at 4096 keys: 317 us, 6.8 TB/s; 96 ragged sequences (100 to
+// 16,000 keys, eight query heads to a key head, 16-row pages): 230 us, 6.5 TB/s.
 //
-// A CTA has four computing warps, each with a quarter of every 64-key block and a running maximum of
-// its own, and one warp that feeds the blocks through a TMA ring (a box per page); two CTAs to an SM
-// keep 192 KB of the cache in flight.  The four warps' sums are joined once per tile, in the space of its
-// last block: slices of an own 8 KB cost two barriers each, 1 us of the 10.5 that a tile of one block takes.
+// A CTA has four computing warps and one that feeds 64-key blocks through a TMA ring (a box per page);
+// two CTAs to an SM keep 192 KB of the cache in flight.  The four warps are one, two or four sets of
+// eight rows by four, two or one parts of a block's keys, each with a running maximum of its own; the
+// parts are joined once per tile, in the space of its last block (slices of an own 8 KB cost two barriers
+// each, 1 us of the 10.5 that a tile of one block takes).  With two sets of rows in every warp instead the sums
+// do not fit the registers: 32 sequences of 300 to 6000 keys, four key heads, 16 rows, 82 us at d = 128 where this
+// takes 56, and 37 against 31 at d = 64.  20 rows, d = 64: 34 us here, 42 on tcgen05 tiles; a warp then waits for its
+// own chain of products and exponentials, and three or four CTAs to an SM (39 and 42 us) only add starts and parts.
+// 32 rows at d = 128: 60 us, 62 on tcgen05 tiles; 48 rows at d = 64 would be two tiles, 42 us there.
 #include <math.h>
 
 #include "../../include/lla.h"
@@ -29,13 +34,19 @@ constexpr int kKeys = 64;                      // keys of a block
 constexpr int kWarps = 4;                      // computing warps
 constexpr int kThreads = (kWarps + 1) * 32;
 
-template <int D, int MT>
+// RS sets of eight query rows in a tile: 1, 2 or 4.
+template <int D, int RS>
 struct DecShape {
+    static constexpr int kParts = kWarps / RS;             // warps that share a set's keys
+    static constexpr int kShare = kKeys / kParts;          // keys of a block that a warp has
+    // key tiles of a step and operand steps in registers: as many as the registers take (the others in shared memory)
+    static constexpr int kTiles = D == 128 && RS == 4 ? 4 : kShare / 8;
+    static constexpr int kRegSteps = D == 128 && RS > 1 ? 4 : D / 16;
     static constexpr int kStages = D == 128 ? 3 : 6;
     static constexpr int kTile = kKeys * D * 2;            // bytes of a K (or V) block
-    static constexpr int kOperand = MT > 1 ? MT * (D / 16) * 512 : 0;   // the first operand, where registers do not hold it
+    static constexpr int kOperand = kWarps * (D / 16 - kRegSteps) * 512;
     static constexpr size_t smem = (size_t)kStages * 2 * kTile + kOperand + 1024;   // 1024: alignment of the ring
-    static_assert(kWarps * 2 * 8 * D * 4 <= 2 * kTile, "a block's space takes the warps' sums of eight rows");
+    static_assert(kWarps * 2 * 8 * D * 4 <= 2 * kTile, "a block's space takes the warps' sums");
 };
 
 struct DecArgs {
@@ -64,10 +75,10 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 // The feeding warp: one block after another of this CTA's pieces, a box to a lane.
-template <int D, int MT>
+template <int D, int RS>
 __device__ void feed(const Work& w, Walk wk, const CUtensorMap* mk, const CUtensorMap* mv, int slices, uint32_t ring,
                      uint64_t* full, uint64_t* empty, volatile int* err) {
-    constexpr int kStages = DecShape<D, MT>::kStages, kTile = DecShape<D, MT>::kTile;
+    constexpr int kStages = DecShape<D, RS>::kStages, kTile = DecShape<D, RS>::kTile;
     const int lane = threadIdx.x & 31;
     const int box = min(1 << w.page_shift, kBoxRows);        // rows of a box
     const int boxes = kKeys / box;                           // <= 8
@@ -103,25 +114,26 @@ __device__ void feed(const Work& w, Walk wk, const CUtensorMap* mk, const CUtens
         for (int t = max(issued - kStages, 0); t < issued; ++t) drain(&full[t % kStages], (t / kStages) & 1);
 }
 
-// MT sets of eight query rows.
-template <int D, int MT>
+template <int D, int RS>
 __global__ void __launch_bounds__(kThreads, 2)
     paged_decode_kernel(DecArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-    using Sh = DecShape<D, MT>;
+    using Sh = DecShape<D, RS>;
     constexpr int kStages = Sh::kStages, kTile = Sh::kTile;
     constexpr int KS = D / 16;                 // k steps of the first product
     constexpr int NT = D / 8;                  // column tiles of the second
-    constexpr int R = 8 * MT;
+    constexpr int NK = Sh::kTiles, KR = Sh::kRegSteps;
+    constexpr int R = RS * 8;
     extern __shared__ unsigned char raw[];
     __shared__ long long scratch[40];
     __shared__ uint64_t full[kStages], empty[kStages];
     __shared__ int err;
-    __shared__ float4 stats[kWarps][R];
+    __shared__ float4 stats[kWarps][8];
     unsigned char* base = raw + ((1024u - (tc::smem_u32(raw) & 1023u)) & 1023u);
     const uint32_t ring = tc::smem_u32(base);
-    uint32_t* qs = reinterpret_cast<uint32_t*>(base + (size_t)kStages * 2 * kTile);   // MT > 1: first operand, by lane
     const Work& w = a.w;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    // this lane's operand steps that registers do not hold
+    uint4* qs = reinterpret_cast<uint4*>(base + (size_t)kStages * 2 * kTile) + warp * (KS - KR) * 32 + lane;
 
     if (tid == 0) {
         tc::tma_prefetch_desc(&mk);
@@ -139,9 +151,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
 
     if (warp == kWarps) {
-        feed<D, MT>(w, wk, &mk, &mv, a.slices, ring, full, empty, &err);
+        feed<D, RS>(w, wk, &mk, &mv, a.slices, ring, full, empty, &err);
     } else {
         const int g = lane >> 2, c2 = (lane & 3) * 2;
+        const int set = warp % RS, share0 = warp / RS * Sh::kShare;     // this warp's rows and keys of a block
         int stage = 0, phase = 0;
         bool shared = false, ok = true;
         Piece p;
@@ -149,167 +162,154 @@ __global__ void __launch_bounds__(kThreads, 2)
         // a warp whose wait gave up (ok false) computes nothing more, but passes every barrier of the join
         while (next_piece(w, wk, p)) {
             shared = p.slot == 1;
+            const int r = set * 8 + g, fr = p.row0 + r, token = p.q.token0 + over_g(w, fr);
+            const int head = p.h * w.G + (fr - over_g(w, fr) * w.G);
+            const bool in = r < p.rows;
             // first operand, rows g: queries in registers 0 and 2, probes in 1 and 3
-            uint32_t qf[MT == 1 ? KS : 1][4];
-            int limit[MT];
+            uint32_t qf[KR][4];
+            int limit = 0;
+            const __nv_bfloat16* gq = a.q;
+            const __nv_bfloat16* gr = a.probe;
+            if (in) {
+                limit = w.causal ? min(max(p.q.L - p.q.nq + over_g(w, fr) + 1, 0), p.q.L) : p.q.L;
+                gq += (long long)token * a.q_stride + (long long)head * D + c2;
+                gr += (long long)token * a.r_stride + (long long)head * D + c2;
+            }
+            // keys that all of this warp's rows see
+            const int all = __reduce_min_sync(0xffffffffu, in ? limit : 0x7fffffff);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                const int r = mt * 8 + g, fr = p.row0 + r;
-                const bool in = r < p.rows;
-                limit[mt] = 0;
-                const __nv_bfloat16* gq = a.q;
-                const __nv_bfloat16* gr = a.probe;
+            for (int k = 0; k < KS; ++k) {
+                uint32_t f[4] = {0u, 0u, 0u, 0u};
                 if (in) {
-                    limit[mt] = w.causal ? min(max(p.q.L - p.q.nq + over_g(w, fr) + 1, 0), p.q.L) : p.q.L;
-                    const long long token = p.q.token0 + over_g(w, fr);
-                    const int head = p.h * w.G + (fr - over_g(w, fr) * w.G);
-                    gq += token * a.q_stride + (long long)head * D + c2;
-                    gr += token * a.r_stride + (long long)head * D + c2;
+                    f[0] = *reinterpret_cast<const uint32_t*>(gq + k * 16);
+                    f[1] = *reinterpret_cast<const uint32_t*>(gr + k * 16);
+                    f[2] = *reinterpret_cast<const uint32_t*>(gq + k * 16 + 8);
+                    f[3] = *reinterpret_cast<const uint32_t*>(gr + k * 16 + 8);
                 }
+                if (k < KR) {
 #pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    if (MT > 1 && k % kWarps != warp) continue;      // MT > 1: a quarter of the steps each
-                    uint32_t f[4] = {0u, 0u, 0u, 0u};
-                    if (in) {
-                        f[0] = *reinterpret_cast<const uint32_t*>(gq + k * 16);
-                        f[1] = *reinterpret_cast<const uint32_t*>(gr + k * 16);
-                        f[2] = *reinterpret_cast<const uint32_t*>(gq + k * 16 + 8);
-                        f[3] = *reinterpret_cast<const uint32_t*>(gr + k * 16 + 8);
-                    }
-                    if (MT == 1) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) qf[k % (MT == 1 ? KS : 1)][i] = f[i];
-                    } else {
-                        *reinterpret_cast<uint4*>(&qs[((mt * KS + k) * 32 + lane) * 4]) = make_uint4(f[0], f[1], f[2], f[3]);
-                    }
+                    for (int i = 0; i < 4; ++i) qf[k % KR][i] = f[i];
+                } else {
+                    qs[(k - KR) * 32] = make_uint4(f[0], f[1], f[2], f[3]);
                 }
             }
-            if (MT > 1) tc::named_bar_sync(1, kWarps * 32);
-            float m[MT], om[MT], A[MT], s0[MT];
-            float o[MT][NT][4];                // per column pair: O1, O1, O2, O2
+            float m = -INFINITY, om = 0.f, A = 0.f, s0 = 0.f;
+            float o[NT][4];                    // per column pair: O1, O1, O2, O2
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                m[mt] = -INFINITY;
-                om[mt] = A[mt] = s0[mt] = 0.f;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) o[mt][n][0] = o[mt][n][1] = o[mt][n][2] = o[mt][n][3] = 0.f;
-            }
+            for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
             bool first = true;
             for (int j = p.j0; ok && j < p.j1; ++j) {
                 ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[stage], phase, &err));
                 if (!ok) break;
-                const int key0 = j * kKeys + warp * 16;
-                if (key0 < p.keys) {
-                    const uint32_t kt = ring + stage * 2 * kTile, vt = kt + kTile;
-                    const int row0 = warp * 16;
-                    if (key0 + 16 > p.keys) {
-                        // keys behind the last: their value rows hold a page's rest or an earlier block, and
-                        // a zero weight does not remove a NaN, so the rows are cleared
-                        for (int e = lane; e < 16 * (D / 8); e += 32) {
-                            const int r = e / (D / 8), c = e % (D / 8);
-                            if (key0 + r >= p.keys)
-                                *reinterpret_cast<uint4*>(base + (vt - ring) + piece_off<D>(row0 + r, c)) = make_uint4(0, 0, 0, 0);
-                        }
+                const uint32_t kt = ring + stage * 2 * kTile, vt = kt + kTile;
+                const int behind = p.keys - j * kKeys;       // rows of the block that hold keys
+                const int share1 = min(behind, share0 + Sh::kShare);
+                if (set * 8 < p.rows && share0 < share1) {
+                    if (share1 < share0 + Sh::kShare) {
+                        // value rows behind the last key hold a page's rest or an earlier block, and a zero weight does not
+                        // remove a NaN: they are cleared (by each of the warps that read them, to the same zeros)
+                        for (int e = share1 * (D / 8) + lane; e < (share0 + Sh::kShare) * (D / 8); e += 32)
+                            *reinterpret_cast<uint4*>(base + (vt - ring) + piece_off<D>(e / (D / 8), e % (D / 8))) = make_uint4(0, 0, 0, 0);
                         tc::fence_proxy_async_smem();        // the ring's next copy is the async proxy's
                         __syncwarp();
                     }
-                    float s[MT][2][4];
+#pragma unroll 1
+                    for (int row0 = share0; row0 < share1; row0 += NK * 8) {
+                        float s[NK][4];
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) s[mt][n][0] = s[mt][n][1] = s[mt][n][2] = s[mt][n][3] = 0.f;
-                    {
-                        const int r = row0 + (lane & 7) + ((lane >> 4) << 3), half = (lane >> 3) & 1;
+                        for (int n = 0; n < NK; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
 #pragma unroll
                         for (int k = 0; k < KS; ++k) {
-                            uint32_t b[4];
-                            ldsm4(kt + piece_off<D>(r, k * 2 + half), b);
+                            uint32_t f[4];
+                            if (k < KR) {
 #pragma unroll
-                            for (int mt = 0; mt < MT; ++mt) {
-                                uint32_t f[4];
-                                if (MT == 1) {
+                                for (int i = 0; i < 4; ++i) f[i] = qf[k % KR][i];
+                            } else {
+                                const uint4 x = qs[(k - KR) * 32];
+                                f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+                            }
 #pragma unroll
-                                    for (int i = 0; i < 4; ++i) f[i] = qf[k % (MT == 1 ? KS : 1)][i];
-                                } else {
-                                    const uint4 x = *reinterpret_cast<const uint4*>(&qs[((mt * KS + k) * 32 + lane) * 4]);
-                                    f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
-                                }
-                                mma16816(s[mt][0], f, b[0], b[1]);
-                                mma16816(s[mt][1], f, b[2], b[3]);
+                            for (int n = 0; n < NK; n += 2) {
+                                uint32_t b[4];
+                                ldsm4(kt + piece_off<D>(row0 + n * 8 + (lane & 7) + ((lane >> 4) << 3), k * 2 + ((lane >> 3) & 1)), b);
+                                mma16816(s[n], f, b[0], b[1]);
+                                mma16816(s[n + 1], f, b[2], b[3]);
                             }
                         }
-                    }
-                    uint32_t pf[MT][4];
+                        const int key0 = j * kKeys + row0;
+                        if (key0 + NK * 8 > all) {           // some row does not see all of the step's keys
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        float l[4], t[4];
+                            for (int n = 0; n < NK; ++n)
 #pragma unroll
-                        for (int n = 0; n < 2; ++n)
+                                for (int e = 0; e < 2; ++e)
+                                    if (key0 + n * 8 + c2 + e >= limit) {
+                                        s[n][e] = -INFINITY;
+                                        s[n][2 + e] = 0.f;
+                                    }
+                        }
+                        float bm = -INFINITY;
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const bool in = key0 + n * 8 + c2 + e < limit[mt];
-                                l[n * 2 + e] = in ? s[mt][n][e] * a.scale : -INFINITY;
-                                t[n * 2 + e] = in ? s[mt][n][2 + e] : 0.f;
-                            }
-                        float bm = fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3]));
+                        for (int n = 0; n < NK; ++n) bm = fmaxf(bm, fmaxf(s[n][0], s[n][1]));
                         bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 1));
-                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2));
-                        // the reference point of the exponents follows the maximum only when that has grown by
-                        // more than 8 (weights to 2^8): most blocks then rescale nothing
-                        if (__any_sync(0xffffffffu, bm > m[mt] + 8.f)) {
-                            const float mn = fmaxf(m[mt], bm);
-                            const float f = mn == -INFINITY ? 1.f : tc::ex2(m[mt] - mn);
-                            m[mt] = mn;
-                            om[mt] *= f;
-                            A[mt] *= f;
+                        bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, 2)) * a.scale;
+                        // the reference point of the exponents follows the maximum only when that has grown by more than 8
+                        // (weights to 2^8): most blocks then rescale nothing
+                        if (__any_sync(0xffffffffu, bm > m + 8.f)) {
+                            const float mn = fmaxf(m, bm);
+                            const float f = mn == -INFINITY ? 1.f : tc::ex2(m - mn);
+                            m = mn;
+                            om *= f;
+                            A *= f;
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
-                                o[mt][n][0] *= f;
-                                o[mt][n][1] *= f;
-                                o[mt][n][2] *= f;
-                                o[mt][n][3] *= f;
+                                o[n][0] *= f;
+                                o[n][1] *= f;
+                                o[n][2] *= f;
+                                o[n][3] *= f;
                             }
                         }
-                        const float mb = m[mt] == -INFINITY ? 0.f : m[mt];
+                        const float mb = m == -INFINITY ? 0.f : m;
                         float ps = 0.f, pt = 0.f;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            l[e] = tc::ex2(l[e] - mb);
-                            ps += l[e];
-                            pt = fmaf(l[e], t[e], pt);
-                        }
+                        for (int n = 0; n < NK; ++n)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                s[n][e] = tc::ex2(fmaf(s[n][e], a.scale, -mb));
+                                ps += s[n][e];
+                                pt = fmaf(s[n][e], s[n][2 + e], pt);
+                            }
                         if (first) {           // centre: the softmax mean of t over the first keys
                             float x = ps, y = pt;
                             x += __shfl_xor_sync(0xffffffffu, x, 1);
                             y += __shfl_xor_sync(0xffffffffu, y, 1);
                             x += __shfl_xor_sync(0xffffffffu, x, 2);
                             y += __shfl_xor_sync(0xffffffffu, y, 2);
-                            s0[mt] = x > 0.f ? y / x : 0.f;
+                            s0 = x > 0.f ? y / x : 0.f;
+                            first = false;
                         }
-                        om[mt] += ps;
-                        A[mt] += pt - s0[mt] * ps;
-                        // the value product takes the weights in bf16 (half a step is 2^-8 of each): its sums are fp32
-                        pf[mt][0] = pack_bf16(l[0], l[1]);
-                        pf[mt][1] = pack_bf16(l[0] * (t[0] - s0[mt]), l[1] * (t[1] - s0[mt]));
-                        pf[mt][2] = pack_bf16(l[2], l[3]);
-                        pf[mt][3] = pack_bf16(l[2] * (t[2] - s0[mt]), l[3] * (t[3] - s0[mt]));
-                    }
-                    first = false;
-                    {
-                        const int r = row0 + (lane & 15), half = lane >> 4;
+                        om += ps;
+                        A += pt - s0 * ps;
 #pragma unroll
-                        for (int n = 0; n < NT / 2; ++n) {
-                            uint32_t b[4];
-                            ldsm4t(vt + piece_off<D>(r, n * 2 + half), b);
+                        for (int kk = 0; kk < NK; kk += 2) {
+                            // the value product takes the weights in bf16 (half a step is 2^-8 of each): its sums are fp32
+                            uint32_t pf[4];
 #pragma unroll
-                            for (int mt = 0; mt < MT; ++mt) {
-                                mma16816(o[mt][n * 2], pf[mt], b[0], b[1]);
-                                mma16816(o[mt][n * 2 + 1], pf[mt], b[2], b[3]);
+                            for (int x = 0; x < 2; ++x) {
+                                const float* y = s[kk + x];
+                                pf[2 * x] = pack_bf16(y[0], y[1]);
+                                pf[2 * x + 1] = pack_bf16(y[0] * (y[2] - s0), y[1] * (y[3] - s0));
+                            }
+#pragma unroll
+                            for (int n = 0; n < NT / 2; ++n) {
+                                uint32_t b[4];
+                                ldsm4t(vt + piece_off<D>(row0 + kk * 8 + (lane & 15), n * 2 + (lane >> 4)), b);
+                                mma16816(o[n * 2], pf, b[0], b[1]);
+                                mma16816(o[n * 2 + 1], pf, b[2], b[3]);
                             }
                         }
                     }
                 }
-                if (j + 1 == p.j1) break;      // the last block's space serves the join before it is given back
+                if (RS < 4 && j + 1 == p.j1) break;      // the last block's space serves the join before it is given back
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(&empty[stage]);
                 if (++stage == kStages) {
@@ -317,83 +317,87 @@ __global__ void __launch_bounds__(kThreads, 2)
                     phase ^= 1;
                 }
             }
+#pragma unroll
+            for (int x = 1; x <= 2; x <<= 1) {
+                om += __shfl_xor_sync(0xffffffffu, om, x);
+                A += __shfl_xor_sync(0xffffffffu, A, x);
+            }
 
-            // join the four warps: common maximum, centre of warp 0 (it has the piece's first keys)
+            if constexpr (RS == 4) {
+                // a warp has all keys of its rows
+                if (!in) continue;
+                if (p.slot < 0) {
+                    const float inv = om != 0.f ? 1.f / om : 0.f, c1 = (1.f + A * inv) * inv;
+                    __nv_bfloat16* out = a.out + ((long long)token * a.Hq + head) * D + c2;
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-                for (int x = 1; x <= 2; x <<= 1) {
-                    om[mt] += __shfl_xor_sync(0xffffffffu, om[mt], x);
-                    A[mt] += __shfl_xor_sync(0xffffffffu, A[mt], x);
-                }
-                if ((lane & 3) == 0) stats[warp][mt * 8 + g] = make_float4(m[mt], om[mt], A[mt], s0[mt]);
-            }
-            tc::named_bar_sync(1, kWarps * 32);
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                float mm = -INFINITY;
-#pragma unroll
-                for (int x = 0; x < kWarps; ++x) mm = fmaxf(mm, stats[x][mt * 8 + g].x);
-                const float f = m[mt] == -INFINITY ? (om[mt] == 0.f ? 0.f : om[mt]) : tc::ex2(m[mt] - mm);
-                const float ds = s0[mt] - stats[0][mt * 8 + g].w;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    o[mt][n][2] = f * fmaf(ds, o[mt][n][0], o[mt][n][2]);
-                    o[mt][n][3] = f * fmaf(ds, o[mt][n][1], o[mt][n][3]);
-                    o[mt][n][0] *= f;
-                    o[mt][n][1] *= f;
-                }
-            }
-            // the sums of eight rows at a time, in the last block's space: [warp][O1, O2][row][column], columns swizzled by
-            // the row so that neither the writes nor the reads collide; then a thread has four columns of a row
-            float* sums = reinterpret_cast<float*>(base + (size_t)stage * 2 * kTile);
-            auto place = [&](int x, int half, int r, int c) { return ((x * 2 + half) * 8 + r) * D + (c ^ ((r & 3) << 3)); };
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                if (mt > 0) tc::named_bar_sync(1, kWarps * 32);
-                if (p.j0 < p.j1) {
+                    for (int n = 0; n < NT; ++n)
+                        *reinterpret_cast<uint32_t*>(out + n * 8) = pack_bf16(c1 * o[n][0] - inv * o[n][2], c1 * o[n][1] - inv * o[n][3]);
+                } else {
+                    float4* ps = part_sums(w, blockIdx.x, p.slot, D);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        *reinterpret_cast<float2*>(sums + place(warp, 0, g, n * 8 + c2)) = make_float2(o[mt][n][0], o[mt][n][1]);
-                        *reinterpret_cast<float2*>(sums + place(warp, 1, g, n * 8 + c2)) = make_float2(o[mt][n][2], o[mt][n][3]);
+                        *reinterpret_cast<float2*>(part_element(ps, R, D, 0, r, n * 8 + c2)) = make_float2(o[n][0], o[n][1]);
+                        *reinterpret_cast<float2*>(part_element(ps, R, D, 1, r, n * 8 + c2)) = make_float2(o[n][2], o[n][3]);
                     }
-                    tc::named_bar_sync(1, kWarps * 32);
+                    if (c2 == 0) part_stats(w, blockIdx.x, p.slot, D)[r] = make_float4(m, om, A, s0);
                 }
+                continue;
+            }
+
+            // join the warps of a set: common maximum, centre of the first of them (it has the piece's first keys)
+            if (c2 == 0) stats[warp][g] = make_float4(m, om, A, s0);
+            tc::named_bar_sync(1, kWarps * 32);
+            // the sums in the last block's space: [warp][O1, O2][row][column], columns swizzled by the row so that
+            // neither the writes nor the reads collide; then a thread has four columns of a row
+            float* sums = reinterpret_cast<float*>(base + (size_t)stage * 2 * kTile);
+            auto place = [&](int x, int half, int row, int c) { return ((x * 2 + half) * 8 + row) * D + (c ^ ((row & 3) << 3)); };
+            if (p.j0 < p.j1) {
+                float mm = -INFINITY;
+#pragma unroll
+                for (int x = 0; x < Sh::kParts; ++x) mm = fmaxf(mm, stats[x * RS + set][g].x);
+                const float f = m == -INFINITY ? (om == 0.f ? 0.f : om) : tc::ex2(m - mm);
+                const float ds = s0 - stats[set][g].w;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    *reinterpret_cast<float2*>(sums + place(warp, 0, g, n * 8 + c2)) = make_float2(f * o[n][0], f * o[n][1]);
+                    *reinterpret_cast<float2*>(sums + place(warp, 1, g, n * 8 + c2)) =
+                        make_float2(f * fmaf(ds, o[n][0], o[n][2]), f * fmaf(ds, o[n][1], o[n][3]));
+                }
+                tc::named_bar_sync(1, kWarps * 32);
+            }
 #pragma unroll 1
-                for (int e = tid; e < 8 * (D / 4); e += kWarps * 32) {
-                    const int r8 = e / (D / 4), c = e % (D / 4) * 4, r = mt * 8 + r8;
-                    if (r >= p.rows) continue;
-                    float4 x1 = make_float4(0.f, 0.f, 0.f, 0.f), x2 = x1;
-                    float mm = -INFINITY, ow = 0.f, aw = 0.f;
-                    const float sref = stats[0][r].w;
+            for (int e = tid; e < p.rows * (D / 4); e += kWarps * 32) {
+                const int row = e / (D / 4), c = e % (D / 4) * 4, st = row / 8;
+                float4 x1 = make_float4(0.f, 0.f, 0.f, 0.f), x2 = x1;
+                float mm = -INFINITY, ow = 0.f, aw = 0.f;
+                const float sref = stats[st][row % 8].w;
 #pragma unroll
-                    for (int x = 0; x < kWarps; ++x) mm = fmaxf(mm, stats[x][r].x);
-                    const float mb = mm == -INFINITY ? 0.f : mm;
+                for (int x = 0; x < Sh::kParts; ++x) mm = fmaxf(mm, stats[x * RS + st][row % 8].x);
+                const float mb = mm == -INFINITY ? 0.f : mm;
 #pragma unroll
-                    for (int x = 0; x < kWarps; ++x) {
-                        const float4 st = stats[x][r];
-                        const float f = tc::ex2(st.x - mb);
-                        ow = fmaf(f, st.y, ow);
-                        aw = fmaf(f, fmaf(st.w - sref, st.y, st.z), aw);
-                        if (p.j0 < p.j1) {
-                            const float4 y = *reinterpret_cast<const float4*>(sums + place(x, 0, r8, c));
-                            const float4 z = *reinterpret_cast<const float4*>(sums + place(x, 1, r8, c));
-                            x1.x += y.x; x1.y += y.y; x1.z += y.z; x1.w += y.w;
-                            x2.x += z.x; x2.y += z.y; x2.z += z.z; x2.w += z.w;
-                        }
+                for (int x = 0; x < Sh::kParts; ++x) {
+                    const float4 t = stats[x * RS + st][row % 8];
+                    const float f = tc::ex2(t.x - mb);
+                    ow = fmaf(f, t.y, ow);
+                    aw = fmaf(f, fmaf(t.w - sref, t.y, t.z), aw);
+                    if (p.j0 < p.j1) {
+                        const float4 y = *reinterpret_cast<const float4*>(sums + place(x * RS + st, 0, row % 8, c));
+                        const float4 z = *reinterpret_cast<const float4*>(sums + place(x * RS + st, 1, row % 8, c));
+                        x1.x += y.x; x1.y += y.y; x1.z += y.z; x1.w += y.w;
+                        x2.x += z.x; x2.y += z.y; x2.z += z.z; x2.w += z.w;
                     }
-                    if (p.slot < 0) {
-                        const int fr = p.row0 + r, tk = over_g(w, fr);
-                        const float inv = ow != 0.f ? 1.f / ow : 0.f, c1 = (1.f + aw * inv) * inv;
-                        *reinterpret_cast<uint2*>(a.out + ((long long)(p.q.token0 + tk) * a.Hq + p.h * w.G + fr - tk * w.G) * D + c) =
-                            make_uint2(pack_bf16(c1 * x1.x - inv * x2.x, c1 * x1.y - inv * x2.y),
-                                       pack_bf16(c1 * x1.z - inv * x2.z, c1 * x1.w - inv * x2.w));
-                    } else {
-                        float4* ps = part_sums(w, blockIdx.x, p.slot, D) + (size_t)(c / 4) * R + r;
-                        ps[0] = x1;
-                        ps[(size_t)(D / 4) * R] = x2;
-                        if (c == 0) part_stats(w, blockIdx.x, p.slot, D)[r] = make_float4(mm, ow, aw, sref);
-                    }
+                }
+                if (p.slot < 0) {
+                    const int er = p.row0 + row, tk = over_g(w, er);
+                    const float inv = ow != 0.f ? 1.f / ow : 0.f, c1 = (1.f + aw * inv) * inv;
+                    *reinterpret_cast<uint2*>(a.out + ((long long)(p.q.token0 + tk) * a.Hq + p.h * w.G + er - tk * w.G) * D + c) =
+                        make_uint2(pack_bf16(c1 * x1.x - inv * x2.x, c1 * x1.y - inv * x2.y),
+                                   pack_bf16(c1 * x1.z - inv * x2.z, c1 * x1.w - inv * x2.w));
+                } else {
+                    float4* ps = part_sums(w, blockIdx.x, p.slot, D) + (size_t)(c / 4) * R + row;
+                    ps[0] = x1;
+                    ps[(size_t)(D / 4) * R] = x2;
+                    if (c == 0) part_stats(w, blockIdx.x, p.slot, D)[row] = make_float4(mm, ow, aw, sref);
                 }
             }
             tc::fence_proxy_async_smem();      // the space's next copy is the async proxy's
@@ -412,10 +416,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (tid == 0 && err) atomicOr(w.err, (unsigned)kDevErrMbarTimeout);
 }
 
-template <int D, int MT>
+template <int D, int RS>
 cudaError_t launch_dec(const DecArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
-    constexpr size_t smem = DecShape<D, MT>::smem;
-    auto* kern = paged_decode_kernel<D, MT>;
+    constexpr size_t smem = DecShape<D, RS>::smem;
+    auto* kern = paged_decode_kernel<D, RS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_after(kern, dim3(a.w.ctas), kThreads, smem, stream, a, mk, mv);
@@ -424,10 +428,11 @@ cudaError_t launch_dec(const DecArgs& a, const CUtensorMap& mk, const CUtensorMa
 }  // namespace
 }  // namespace paged
 
-bool paged_decode_fits(const PagedProblem& p) { return (long long)p.max_new * p.G <= 16; }
+bool paged_decode_fits(const PagedProblem& p) { return (long long)p.max_new * p.G <= 32; }
 
 PagedSplit paged_decode_split(const PagedProblem& p, int sms) {
-    return PagedSplit{(long long)p.max_new * p.G <= 8 ? 8 : 16, paged::kKeys, 2 * sms, 4, 2};
+    const long long rows = (long long)p.max_new * p.G;
+    return PagedSplit{rows <= 8 ? 8 : rows <= 16 ? 16 : 32, paged::kKeys, 2 * sms, 4, 2};
 }
 
 cudaError_t launch_paged_decode(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream, const char** why) {
@@ -439,8 +444,12 @@ cudaError_t launch_paged_decode(const PagedProblem& p, const PagedSplit& sp, cud
     paged::DecArgs a{paged::make_work(p, sp), static_cast<const __nv_bfloat16*>(p.q), static_cast<const __nv_bfloat16*>(p.probe),
                      static_cast<__nv_bfloat16*>(p.out), p.Hq, (int)paged::slices_of_page(p), p.q_stride, p.r_stride, p.tau * 1.4426950408889634f};
     if (p.d == 128)
-        return sp.rows == 8 ? paged::launch_dec<128, 1>(a, mk, mv, stream) : paged::launch_dec<128, 2>(a, mk, mv, stream);
-    return sp.rows == 8 ? paged::launch_dec<64, 1>(a, mk, mv, stream) : paged::launch_dec<64, 2>(a, mk, mv, stream);
+        return sp.rows == 8    ? paged::launch_dec<128, 1>(a, mk, mv, stream)
+               : sp.rows == 16 ? paged::launch_dec<128, 2>(a, mk, mv, stream)
+                               : paged::launch_dec<128, 4>(a, mk, mv, stream);
+    return sp.rows == 8    ? paged::launch_dec<64, 1>(a, mk, mv, stream)
+           : sp.rows == 16 ? paged::launch_dec<64, 2>(a, mk, mv, stream)
+                           : paged::launch_dec<64, 4>(a, mk, mv, stream);
 }
 
 }  // namespace lla

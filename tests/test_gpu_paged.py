@@ -259,6 +259,25 @@ def test_attention(lla_gpu, dtype, d, kind, G, Hkv, page):
         c.check(run(c, path), tensor)
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("G,most", [(1, 9), (3, 5), (16, 1), (4, 5), (5, 6), (1, 32)])
+def test_up_to_32_rows_to_a_key_head(lla_gpu, d, causal, G, most):
+    """Sets of eight rows, full and ragged; lengths about a warp's share of a block, a block and a range border;
+    logits that grow with the position, sequences without keys or with fewer keys than tokens."""
+    new = [most, 1, most, most, 0, most, max(most - 1, 1), most]
+    kv = [most, 15, 47, 64 + 17, 30, max(most - 3, 0), 700, 5001]
+    c = Case(new, kv, 2 * G, 2, d, 16, "bf16", causal=causal, pad=2, scale=1.5)
+    for s, n in enumerate(c.kv):
+        for x in range(0, n, 7):
+            c.kc[c.table[s, x // 16], :, x % 16] *= 0.2 + 1.3 * x / n
+    c.knorm = 1.5
+    out = torch.full((len(c.q), 2 * G, d), 123.0, dtype=torch.bfloat16, device="cuda")
+    got = c.check(run(c, lla.LLA_PATH_TENSOR, out=out), True)
+    assert (got[c.cu[-1]:] == 123.0).all()
+    assert torch.equal(out, run(c, lla.LLA_PATH_TENSOR, out=out.clone()))
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("fp32", 32)])
 @pytest.mark.parametrize("new,kv", [([5, 40, 1], [77, 1, 130]), ([1, 1], [500, 33]), ([300], [129])])
 def test_cross_attention(lla_gpu, dtype, d, new, kv):
