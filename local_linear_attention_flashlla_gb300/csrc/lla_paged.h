@@ -51,7 +51,7 @@ inline size_t paged_workspace_bytes(int ctas, int rows, int d) {
 }
 
 // How a path divides the work: rows of a tile, keys of a block (rows <= keys), CTAs, least units worth a CTA (all
-// but the CTAs powers of two).
+// but the CTAs powers of two; 0: by the longest tile, see least_shift).
 struct PagedSplit {
     int rows, keys, ctas, min_units;
     int extra;      // units charged for a tile beside its blocks: what a tile costs before its first block and after its last
@@ -121,7 +121,7 @@ inline Work make_work(const PagedProblem& p, const PagedSplit& sp) {
     w.table = p.table; w.cu_q = p.cu_q; w.kv_lens = p.kv_lens;
     w.T = p.T; w.S = p.S; w.Hkv = p.Hkv; w.G = p.G; w.width = p.width; w.page_shift = p.page_shift;
     w.num_pages = p.num_pages; w.max_new = p.max_new; w.causal = p.causal;
-    w.rows = sp.rows; w.keys = sp.keys; w.ctas = sp.ctas; w.min_shift = log2_up(sp.min_units);
+    w.rows = sp.rows; w.keys = sp.keys; w.ctas = sp.ctas; w.min_shift = sp.min_units ? log2_up(sp.min_units) : -1;
     w.extra = sp.extra;
     w.keys_shift = log2_up(sp.keys);
     w.rows_shift = log2_up(sp.rows);
@@ -259,9 +259,23 @@ __device__ __forceinline__ long long block_scan(long long v, long long* sh, long
     return v;
 }
 
+// Units of the longest tile of a sequence.
+__device__ __forceinline__ int longest_tile(const Work& w, const Seq& q) {
+    return q.nq > 0 ? tile_units(w, q, tiles_of(w, q) - 1) : 0;
+}
+
+// log2 of the least units worth a CTA: a tile of B units cut into parts of m takes m blocks one after another (0.7 us
+// each for decode tiles) and the join of B / m parts (0.08 us each), least at m = sqrt(B / 9); the power of two
+// at or above half of it.  One sequence, two key heads: 200 to 1000 keys 8.3 us where m = 4 takes 10 and m = 8
+// takes 9 to 13; 8000 keys 11.0 where m = 1 takes 15; 32,768 keys 16.3 where m = 4 takes 18.
+__device__ __forceinline__ int least_shift(const Work& w, int longest) {
+    return w.min_shift >= 0 ? w.min_shift : (32 - __clz(longest / 9 | 1)) / 2;
+}
+
 // CTA cta's range of `total` units; false: it has none.
-__device__ __forceinline__ bool set_range(const Work& w, Walk& k, int cta, long long total) {
-    const long long most = (total + (1 << w.min_shift) - 1) >> w.min_shift;
+__device__ __forceinline__ bool set_range(const Work& w, Walk& k, int cta, long long total, int longest) {
+    const int shift = least_shift(w, longest);
+    const long long most = (total + (1 << shift) - 1) >> shift;
     k.active = (int)(most < w.ctas ? most : w.ctas);
     if (cta >= k.active) return false;
     k.share = div_units(total, k.active);
@@ -303,6 +317,7 @@ __device__ inline Walk begin_walk(const Work& w, int cta, long long* sh) {
     k.s = k.h = k.i = k.j = 0;
     k.q.token0 = k.q.nq = k.q.L = 0;
     k.u = k.end = 0;
+    int longest = 0;
     long long mine = 0, unit = 0, total;           // unit: of a key head of the last sequence looked at
     if (w.S <= 32) {
         // a lane to a sequence, every warp for itself: no barrier
@@ -312,6 +327,7 @@ __device__ inline Walk begin_walk(const Work& w, int cta, long long* sh) {
             q = load_seq(w, lane);
             unit = head_units(w, q);
             mine = unit * w.Hkv;
+            longest = longest_tile(w, q);
         }
         long long inc = mine;
         for (int o = 1; o < 32; o <<= 1) {
@@ -319,7 +335,7 @@ __device__ inline Walk begin_walk(const Work& w, int cta, long long* sh) {
             if (lane >= o) inc += t;
         }
         total = __shfl_sync(0xffffffffu, inc, 31);
-        if (!set_range(w, k, cta, total)) return k;
+        if (!set_range(w, k, cta, total, (int)__reduce_max_sync(0xffffffffu, (unsigned)longest))) return k;
         const unsigned here = __ballot_sync(0xffffffffu, k.u >= inc - mine && k.u < inc);
         const int s = __ffs((int)here) - 1;
         k.s = s;
@@ -333,9 +349,14 @@ __device__ inline Walk begin_walk(const Work& w, int cta, long long* sh) {
         k.q = load_seq(w, s);
         unit = head_units(w, k.q);
         mine += unit * w.Hkv;
+        longest = max(longest, longest_tile(w, k.q));
     }
+    unsigned* most = reinterpret_cast<unsigned*>(sh + kMostWarps);        // a warp's longest tile, behind the scan's sums
+    longest = (int)__reduce_max_sync(0xffffffffu, (unsigned)longest);
+    if (lane == 0) most[tid >> 5] = (unsigned)longest;
     long long pre = block_scan(mine, sh, &total) - mine;
-    if (!set_range(w, k, cta, total)) return k;
+    for (int i = 0; i < (nt + 31) >> 5; ++i) longest = max(longest, (int)most[i]);
+    if (!set_range(w, k, cta, total, longest)) return k;
     int* at = reinterpret_cast<int*>(sh + 32);     // sequence, token0, nq, L
     if (k.u >= pre && k.u < pre + mine) {
         int s = s0;
