@@ -50,10 +50,9 @@ inline size_t paged_workspace_bytes(int ctas, int rows, int d) {
     return (size_t)kPagedMaxCtas * sizeof(PartHeader) + (size_t)ctas * 2 * paged_part_floats(rows, d) * sizeof(float);
 }
 
-// How a path divides the work: rows of a tile, keys of a block (rows <= keys), CTAs, least units worth a CTA (all
-// but the CTAs powers of two; 0: by the longest tile, see least_shift).
+// How a path divides the work: rows of a tile, keys of a block (powers of two, rows <= keys), CTAs.
 struct PagedSplit {
-    int rows, keys, ctas, min_units;
+    int rows, keys, ctas;
     int extra;      // units charged for a tile beside its blocks: what a tile costs before its first block and after its last
 };
 
@@ -108,7 +107,7 @@ struct Work {
     const int* cu_q;
     const int* kv_lens;
     int T, S, Hkv, G, width, page_shift, num_pages, max_new, causal;
-    int rows, keys, ctas, min_shift, extra;
+    int rows, keys, ctas, extra;
     int keys_shift, rows_shift;       // their log2; rows <= keys
     Divisor g, m;                     // G, and keys / rows * G
     PartHeader* hdr;
@@ -121,7 +120,7 @@ inline Work make_work(const PagedProblem& p, const PagedSplit& sp) {
     w.table = p.table; w.cu_q = p.cu_q; w.kv_lens = p.kv_lens;
     w.T = p.T; w.S = p.S; w.Hkv = p.Hkv; w.G = p.G; w.width = p.width; w.page_shift = p.page_shift;
     w.num_pages = p.num_pages; w.max_new = p.max_new; w.causal = p.causal;
-    w.rows = sp.rows; w.keys = sp.keys; w.ctas = sp.ctas; w.min_shift = sp.min_units ? log2_up(sp.min_units) : -1;
+    w.rows = sp.rows; w.keys = sp.keys; w.ctas = sp.ctas;
     w.extra = sp.extra;
     w.keys_shift = log2_up(sp.keys);
     w.rows_shift = log2_up(sp.rows);
@@ -265,16 +264,16 @@ __device__ __forceinline__ int longest_tile(const Work& w, const Seq& q) {
 }
 
 // log2 of the least units worth a CTA: a tile of B units cut into parts of m takes m blocks one after another (0.7 us
-// each for decode tiles) and the join of B / m parts (0.08 us each), least at m = sqrt(B / 9); the power of two
-// at or above half of it.  One sequence, two key heads: 200 to 1000 keys 8.3 us where m = 4 takes 10 and m = 8
-// takes 9 to 13; 8000 keys 11.0 where m = 1 takes 15; 32,768 keys 16.3 where m = 4 takes 18.
-__device__ __forceinline__ int least_shift(const Work& w, int longest) {
-    return w.min_shift >= 0 ? w.min_shift : (32 - __clz(longest / 9 | 1)) / 2;
-}
+// each for decode tiles) and the join of B / m parts (0.08 us each), least at m = sqrt(B / 9); a power of two
+// beside it.  One sequence, two key heads, one token: 200 to 1000 keys 8.3 us where m = 4 takes 10 and m = 8
+// takes 9 to 13; 8000 keys 11.0 where m = 1 takes 15; 32,768 keys 16.3 where m = 4 takes 18.  The other kernels' blocks
+// and joins both cost more: 64 tokens over 500 keys (128-row tiles) 16.6 us where m = 4 takes 19, a prompt of 300 tokens
+// 15.8 and 14.7, 32 rows over 500 keys on CUDA cores 10.3 where m = 2 takes 13.6, over 4000 keys 20.5 and 18.5.
+__device__ __forceinline__ int least_shift(int longest) { return (32 - __clz(longest / 9 | 1)) / 2; }
 
 // CTA cta's range of `total` units; false: it has none.
 __device__ __forceinline__ bool set_range(const Work& w, Walk& k, int cta, long long total, int longest) {
-    const int shift = least_shift(w, longest);
+    const int shift = least_shift(longest);
     const long long most = (total + (1 << shift) - 1) >> shift;
     k.active = (int)(most < w.ctas ? most : w.ctas);
     if (cta >= k.active) return false;

@@ -432,7 +432,7 @@ bool paged_decode_fits(const PagedProblem& p) { return (long long)p.max_new * p.
 
 PagedSplit paged_decode_split(const PagedProblem& p, int sms) {
     const long long rows = (long long)p.max_new * p.G;
-    return PagedSplit{rows <= 8 ? 8 : rows <= 16 ? 16 : 32, paged::kKeys, 2 * sms, 0, 2};
+    return PagedSplit{rows <= 8 ? 8 : rows <= 16 ? 16 : 32, paged::kKeys, 2 * sms, 2};
 }
 
 cudaError_t launch_paged_decode(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream, const char** why) {

@@ -683,8 +683,8 @@ cudaError_t merge_typed(const Work& w, void* out, int Hq, int d, cudaStream_t st
 PagedSplit paged_simt_split(const PagedProblem& p, int sms) {
     // rows: 8 where no sequence has more than eight query rows to a key head (a decode step), else 32
     const bool few = (long long)p.max_new * p.G <= 8;
-    if (few) return PagedSplit{8, 64, 2 * sms, 2, 0};
-    return PagedSplit{32, paged::ManyShape<128>::BN, (p.d == 128 ? paged::ManyShape<128>::kCtas : p.d == 64 ? paged::ManyShape<64>::kCtas : paged::ManyShape<32>::kCtas) * sms, 2, 0};
+    if (few) return PagedSplit{8, 64, 2 * sms, 0};
+    return PagedSplit{32, paged::ManyShape<128>::BN, (p.d == 128 ? paged::ManyShape<128>::kCtas : p.d == 64 ? paged::ManyShape<64>::kCtas : paged::ManyShape<32>::kCtas) * sms, 0};
 }
 
 cudaError_t launch_paged_simt(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream) {

@@ -683,7 +683,7 @@ cudaError_t launch_tc(const TcArgs& a, const CUtensorMap (&m)[4], cudaStream_t s
 
 PagedSplit paged_tc_split(const PagedProblem& p, int sms) {
     (void)p;
-    return PagedSplit{paged::kRows, paged::TcShape<128>::kKeys, sms, 4, 2};
+    return PagedSplit{paged::kRows, paged::TcShape<128>::kKeys, sms, 2};
 }
 
 cudaError_t launch_paged_tc(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream, const char** why) {
