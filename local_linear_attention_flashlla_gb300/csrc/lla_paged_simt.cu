@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(kManyThreads, ManyShape<D>::kCtas) paged_simt_
         if (p.j0 < p.j1) fetch(p.j0);
         load_tile_rows<T, D>(a, p, R, kManyThreads, Qs, Rs);
         const bool busy = warp * 8 < p.rows;             // a warp without rows only helps to load
-        int limit[2];                                    // keys a row sees
+        int limit[2], all = INT_MAX;                     // keys a row sees, keys that all of the warp's rows see
         float m[2], om[2], A[2], s0[2];                  // om, A: this lane's keys
         uint64_t o1[2][CPT / 2], o2[2][CPT / 2];
 #pragma unroll
@@ -341,11 +341,14 @@ __global__ void __launch_bounds__(kManyThreads, ManyShape<D>::kCtas) paged_simt_
             limit[i] = 0;
             if (row + i < p.rows)
                 limit[i] = w.causal ? min(max(p.q.L - p.q.nq + over_g(w, p.row0 + row + i) + 1, 0), p.q.L) : p.q.L;
+            all = min(all, row + i < p.rows ? limit[i] : INT_MAX);
             m[i] = -INFINITY;
             om[i] = A[i] = s0[i] = 0.f;
 #pragma unroll
             for (int c = 0; c < CPT / 2; ++c) o1[i][c] = o2[i][c] = tc::f2_pack(0.f, 0.f);
         }
+
+        all = __reduce_min_sync(0xffffffffu, all);
 
         for (int j = p.j0; j < p.j1; ++j) {
             const int key0 = j * BN;
@@ -394,42 +397,62 @@ __global__ void __launch_bounds__(kManyThreads, ManyShape<D>::kCtas) paged_simt_
                             t[i][u] = x + y;
                         }
                 }
+                if (key0 + BN > all) {
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int u = 0; u < KPT; ++u)
+                            if (key0 + g8 + 8 * u >= limit[i]) s[i][u] = -INFINITY;
+                }
+                float mn[2];
+                bool grown = false, first[2];                // first: the row's first block with keys
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float bm = -INFINITY;
+                    float bm = s[i][0];
 #pragma unroll
-                    for (int u = 0; u < KPT; ++u) {
-                        s[i][u] = key0 + g8 + 8 * u < limit[i] ? s[i][u] * a.scale : -INFINITY;
-                        bm = fmaxf(bm, s[i][u]);
-                    }
+                    for (int u = 1; u < KPT; ++u) bm = fmaxf(bm, s[i][u]);
 #pragma unroll
                     for (int o = 4; o; o >>= 1) bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
-                    const float mn = fmaxf(m[i], bm), base = mn == -INFINITY ? 0.f : mn;
-                    const bool first = m[i] == -INFINITY;    // the row's first block with keys
-                    const float corr = exp2f(m[i] - base);   // m = -inf: 0
-                    const uint64_t c2 = tc::f2_pack(corr, corr);
-                    om[i] *= corr;
-                    A[i] *= corr;
+                    mn[i] = fmaxf(m[i], bm * a.scale);
+                    grown |= mn[i] > m[i];
+                    first[i] = m[i] == -INFINITY && mn[i] != -INFINITY;
+                }
+                grown = __any_sync(0xffffffffu, grown);
+                if (grown) {
 #pragma unroll
-                    for (int c = 0; c < CPT / 2; ++c) {
-                        o1[i][c] = tc::f2_mul(o1[i][c], c2);
-                        o2[i][c] = tc::f2_mul(o2[i][c], c2);
+                    for (int i = 0; i < 2; ++i) {
+                        const float corr = tc::ex2(m[i] - (mn[i] == -INFINITY ? 0.f : mn[i]));   // m = -inf: 0
+                        const uint64_t c2 = tc::f2_pack(corr, corr);
+                        om[i] *= corr;
+                        A[i] *= corr;
+#pragma unroll
+                        for (int c = 0; c < CPT / 2; ++c) {
+                            o1[i][c] = tc::f2_mul(o1[i][c], c2);
+                            o2[i][c] = tc::f2_mul(o2[i][c], c2);
+                        }
+                        m[i] = mn[i];
                     }
-                    m[i] = mn;
-                    float ps = 0.f, pt = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float base = m[i] == -INFINITY ? 0.f : m[i];
+                    float ps = 0.f;
 #pragma unroll
                     for (int u = 0; u < KPT; ++u) {
-                        s[i][u] = exp2f(s[i][u] - base);
+                        s[i][u] = tc::ex2(fmaf(s[i][u], a.scale, -base));
                         ps += s[i][u];
-                        pt = fmaf(s[i][u], t[i][u], pt);
                     }
-                    float x = ps, y = pt;
+                    if (grown) {                             // so it is in a row's first block with keys
+                        float x = ps, y = 0.f;
 #pragma unroll
-                    for (int o = 4; o; o >>= 1) {
-                        x += __shfl_xor_sync(0xffffffffu, x, o);
-                        y += __shfl_xor_sync(0xffffffffu, y, o);
+                        for (int u = 0; u < KPT; ++u) y = fmaf(s[i][u], t[i][u], y);
+#pragma unroll
+                        for (int o = 4; o; o >>= 1) {
+                            x += __shfl_xor_sync(0xffffffffu, x, o);
+                            y += __shfl_xor_sync(0xffffffffu, y, o);
+                        }
+                        if (first[i]) s0[i] = x > 0.f ? y / x : 0.f;
                     }
-                    if (first) s0[i] = x > 0.f ? y / x : 0.f;
                     om[i] += ps;
 #pragma unroll
                     for (int u = 0; u < KPT; ++u) {
