@@ -407,8 +407,10 @@ int lla_paged_append(int dtype, const void* k_new, const void* v_new, const long
  *
  * dtype      of q, probe, out and the caches.  The probe is taken in dtype (lla_parallax_forward
  *            takes fp32), as a serving projection gives it.
- * path       LLA_PATH_AUTO: bf16 with d in {64, 128} takes the tensor cores, all else LLA_PATH_FP32
- *            (CUDA cores, every product in fp32).
+ * path       LLA_PATH_AUTO: bf16 with d in {64, 128} takes LLA_PATH_TENSOR, all else LLA_PATH_FP32.  There
+ *            fp32 tensors with d in {32, 64} are multiplied as three tensor-core products of their upper and lower
+ *            11 bits (each product within 3 2^-22 of itself; magnitudes from 2^127 on count as infinite), all
+ *            else in fp32 on CUDA cores; weights, sums and states are fp32 in both.
  * q, probe   [T, Hq, d], token strides q_stride / probe_stride elements (>= Hq*d, multiples of 16 bytes).
  * out        [T, Hq, d] contiguous; rows behind the last sequence are not written.
  * block_table [S, table_width], cu_q [S+1], kv_lens [S] int32.  max_new: the most tokens of a sequence

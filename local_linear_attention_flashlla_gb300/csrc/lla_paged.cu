@@ -280,8 +280,8 @@ int check_paged_sizes(int dtype, int path, int T, int S, int Hq, int Hkv, int d,
 }
 
 PagedSplit split_of(const PagedProblem& p, int rpath, int sms) {
-    if (rpath == LLA_PATH_TENSOR) return paged_decode_fits(p) ? paged_decode_split(p, sms) : paged_tc_split(p, sms);
-    return paged_simt_split(p, sms);
+    if (paged_decode_fits(p, rpath)) return paged_decode_split(p, sms);
+    return rpath == LLA_PATH_TENSOR ? paged_tc_split(p, sms) : paged_simt_split(p, sms);
 }
 
 }  // namespace
@@ -430,7 +430,7 @@ int lla_paged_parallax(int dtype, int path, const void* q, const void* probe, co
     if (!workspace && (e = cudaMallocAsync(&p.ws, need, stream)) != cudaSuccess)
         return cuda_failf(e, "cudaMallocAsync(workspace)");
     const char* why = nullptr;
-    if (rpath == LLA_PATH_TENSOR && lla::paged_decode_fits(p)) e = lla::launch_paged_decode(p, sp, stream, &why);
+    if (lla::paged_decode_fits(p, rpath)) e = lla::launch_paged_decode(p, sp, stream, &why);
     else if (rpath == LLA_PATH_TENSOR) e = lla::launch_paged_tc(p, sp, stream, &why);
     else e = lla::launch_paged_simt(p, sp, stream);
     if (e == cudaSuccess) e = lla::launch_paged_merge(p, sp, stream);

@@ -56,8 +56,8 @@ struct PagedSplit {
     int extra;      // units charged for a tile beside its blocks: what a tile costs before its first block and after its last
 };
 
-// bf16, d in {64, 128}, at most 32 query rows to a key head (max_new * G): lla_paged_decode.cu.
-bool paged_decode_fits(const PagedProblem& p);
+// bf16, d in {64, 128}, at most 32 query rows to a key head (max_new * G); fp32, d in {32, 64}: lla_paged_decode.cu.
+bool paged_decode_fits(const PagedProblem& p, int path);
 PagedSplit paged_decode_split(const PagedProblem& p, int sms);
 cudaError_t launch_paged_decode(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream, const char** why);
 // bf16, d in {64, 128}, any number of rows: lla_paged_tc.cu.

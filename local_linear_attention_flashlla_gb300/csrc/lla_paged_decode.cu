@@ -1,5 +1,6 @@
 // Parallax attention over a paged bf16 cache for few query rows to a key head (a decode step, a few
-// drafted tokens): reading the cache bounds it, 2 d bytes of K and of V for 8 d flops per row.
+// drafted tokens): reading the cache bounds it, 2 d bytes of K and of V for 8 d flops per row.  And over a paged
+// fp32 cache (d = 32 or 64) for any number of rows.
 //
 // Eight query rows and their probes are stacked in one 16-row operand of mma.m16n8k16 (rows 0-7 the
 // queries, 8-15 the probes of the same rows), so one product gives the logits and t = probe.k, and the
@@ -19,6 +20,17 @@
 // takes 56, and 37 against 31 at d = 64.  20 rows, d = 64: 34 us here, 42 on tcgen05 tiles; a warp then waits for its
 // own chain of products and exponentials, and three or four CTAs to an SM (39 and 42 us) only add starts and parts.
 // 32 rows at d = 128: 60 us, 62 on tcgen05 tiles; 48 rows at d = 64 would be two tiles, 42 us there.
+//
+// fp32: a cache row lies in the ring as a bf16 row of twice the columns would, and ldmatrix hands out its 32-bit
+// words as it does pairs of bf16, so the first product only has other instructions: x y = xh yh + xh yl + xl yh,
+// h and l the upper and lower 11 bits (three of m16n8k8 in tf32, fp32 sums).  What is left out and rounded is
+// 3 2^-22 of a product, where an fp32 product has 2^-24 and the sums of d and of the keys more than either; outputs are
+// as far from float64 as with fp32 products (2.8e-7 on the first case below).  The second product takes a step's keys
+// in an order in which the accumulators are already its operand.  16 sequences of 1 to 97 tokens over 200 to 1024 keys,
+// 4 heads, d = 32: 27 us (fp32 products on CUDA cores, which wait for shared memory, 35); 64 such sequences 78 (104),
+// d = 64 153 (192); decode of 32 x 16 heads at 4096 keys, d = 32 and 64: 117 and 215 us (174 and 254), 4.6 and 5 TB/s;
+// one row over 1000 keys, d = 64: 10.2 (7.5).  At d = 128 the ring leaves room for one CTA: 411 us where CUDA cores take
+// 369, so they keep it.
 #include <math.h>
 
 #include "../../include/lla.h"
@@ -35,25 +47,27 @@ constexpr int kWarps = 4;                      // computing warps
 constexpr int kThreads = (kWarps + 1) * 32;
 
 // RS sets of eight query rows in a tile: 1, 2 or 4.
-template <int D, int RS>
+template <typename T, int D, int RS>
 struct DecShape {
+    static constexpr int kWide = D * (int)sizeof(T) / 2;   // a row's bytes as bf16 columns
     static constexpr int kParts = kWarps / RS;             // warps that share a set's keys
     static constexpr int kShare = kKeys / kParts;          // keys of a block that a warp has
     // key tiles of a step and operand steps in registers: as many as the registers take (the others in shared memory)
-    static constexpr int kTiles = D == 128 && RS == 4 ? 4 : kShare / 8;
-    static constexpr int kRegSteps = D == 128 && RS > 1 ? 4 : D / 16;
-    static constexpr int kStages = D == 128 ? 3 : 6;
-    static constexpr int kTile = kKeys * D * 2;            // bytes of a K (or V) block
-    static constexpr int kOperand = kWarps * (D / 16 - kRegSteps) * 512;
+    static constexpr int kTiles = (kWide >= 128 || sizeof(T) == 4) && RS == 4 ? 4 : kShare / 8;
+    // (fp32 steps are split where they are used: in registers the compiler would keep the halves of all of them)
+    static constexpr int kRegSteps = kWide == 128 && (RS > 1 || sizeof(T) == 4) ? 4 : sizeof(T) == 4 ? 0 : kWide / 16;
+    static constexpr int kStages = kWide == 128 ? 3 : 6;
+    static constexpr int kTile = kKeys * kWide * 2;        // bytes of a K (or V) block
+    static constexpr int kOperand = kWarps * (kWide / 16 - kRegSteps) * 512;
     static constexpr size_t smem = (size_t)kStages * 2 * kTile + kOperand + 1024;   // 1024: alignment of the ring
     static_assert(kWarps * 2 * 8 * D * 4 <= 2 * kTile, "a block's space takes the warps' sums");
 };
 
 struct DecArgs {
     Work w;
-    const __nv_bfloat16* q;
-    const __nv_bfloat16* probe;
-    __nv_bfloat16* out;
+    const void* q;
+    const void* probe;
+    void* out;
     int Hq, slices;                            // slices: head slices from page to page
     long long q_stride, r_stride;
     float scale;                               // tau log2(e)
@@ -74,11 +88,45 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// x = hi + lo but for 2^-22 of it: 11 bits each (tf32), rounded half away from zero.
+__device__ __forceinline__ void split(uint32_t x, uint32_t& hi, uint32_t& lo) {
+    hi = (x + 0x1000u) & 0xffffe000u;
+    lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi)) + 0x1000u;      // the product reads its upper 19 bits
+}
+__device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// c + x += a b over eight fp32 columns, as three products of halves.  The tensor core cuts its sums off instead of
+// rounding them, so the two small products have a sum of their own, x, and the sums are short: a step's value product
+// begins at zero (all in one sum, outputs over 1000 keys are off by 2.4e-6; like this by 3e-7).
+__device__ __forceinline__ void product(float (&c)[4], float (&x)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    uint32_t ah[4], al[4], h0, l0, h1, l1;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split(a[i], ah[i], al[i]);
+    split(b0, h0, l0);
+    split(b1, h1, l1);
+    mma1688(x, al, h0, h1);
+    mma1688(x, ah, l0, l1);
+    mma1688(c, ah, h0, h1);
+}
+
+__device__ __forceinline__ void put2(__nv_bfloat16* p, float x, float y) { *reinterpret_cast<uint32_t*>(p) = pack_bf16(x, y); }
+__device__ __forceinline__ void put2(float* p, float x, float y) { *reinterpret_cast<float2*>(p) = make_float2(x, y); }
+__device__ __forceinline__ void put4(__nv_bfloat16* p, float x, float y, float z, float w) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16(x, y), pack_bf16(z, w));
+}
+__device__ __forceinline__ void put4(float* p, float x, float y, float z, float w) {
+    *reinterpret_cast<float4*>(p) = make_float4(x, y, z, w);
+}
+
 // The feeding warp: one block after another of this CTA's pieces, a box to a lane.
-template <int D, int RS>
+template <typename Sh>
 __device__ void feed(const Work& w, Walk wk, const CUtensorMap* mk, const CUtensorMap* mv, int slices, uint32_t ring,
                      uint64_t* full, uint64_t* empty, volatile int* err) {
-    constexpr int kStages = DecShape<D, RS>::kStages, kTile = DecShape<D, RS>::kTile;
+    constexpr int kStages = Sh::kStages, kTile = Sh::kTile, kRow = Sh::kWide * 2;
     const int lane = threadIdx.x & 31;
     const int box = min(1 << w.page_shift, kBoxRows);        // rows of a box
     const int boxes = kKeys / box;                           // <= 8
@@ -94,10 +142,10 @@ __device__ void feed(const Work& w, Walk wk, const CUtensorMap* mk, const CUtens
             const int count = __popc(__ballot_sync(0xffffffffu, mine));
             ok = __all_sync(0xffffffffu, tc::mbar_wait(&empty[stage], phase ^ 1, err));
             if (!ok) break;
-            if (lane == 0) tc::mbar_arrive_expect_tx(&full[stage], (uint32_t)(count * box * D * 4));
+            if (lane == 0) tc::mbar_arrive_expect_tx(&full[stage], (uint32_t)(count * box * kRow * 2));
             __syncwarp();
             if (mine) {
-                const uint32_t dst = ring + (uint32_t)(stage * 2 * kTile + lane * box * D * 2);
+                const uint32_t dst = ring + (uint32_t)(stage * 2 * kTile + lane * box * kRow);
                 const int group = (key & ((1 << w.page_shift) - 1)) >> 3, slice = page * slices + p.h;
                 tma_load_rows(dst, mk, &full[stage], group, slice);
                 tma_load_rows(dst + kTile, mv, &full[stage], group, slice);
@@ -114,12 +162,12 @@ __device__ void feed(const Work& w, Walk wk, const CUtensorMap* mk, const CUtens
         for (int t = max(issued - kStages, 0); t < issued; ++t) drain(&full[t % kStages], (t / kStages) & 1);
 }
 
-template <int D, int RS>
+template <typename T, int D, int RS>
 __global__ void __launch_bounds__(kThreads, 2)
     paged_decode_kernel(DecArgs a, const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-    using Sh = DecShape<D, RS>;
+    using Sh = DecShape<T, D, RS>;
     constexpr int kStages = Sh::kStages, kTile = Sh::kTile;
-    constexpr int KS = D / 16;                 // k steps of the first product
+    constexpr int DB = Sh::kWide, KS = DB / 16;   // k steps of the first product
     constexpr int NT = D / 8;                  // column tiles of the second
     constexpr int NK = Sh::kTiles, KR = Sh::kRegSteps;
     constexpr int R = RS * 8;
@@ -151,7 +199,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     __syncthreads();
 
     if (warp == kWarps) {
-        feed<D, RS>(w, wk, &mk, &mv, a.slices, ring, full, empty, &err);
+        feed<Sh>(w, wk, &mk, &mv, a.slices, ring, full, empty, &err);
     } else {
         const int g = lane >> 2, c2 = (lane & 3) * 2;
         const int set = warp % RS, share0 = warp / RS * Sh::kShare;     // this warp's rows and keys of a block
@@ -166,14 +214,14 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int head = p.h * w.G + (fr - over_g(w, fr) * w.G);
             const bool in = r < p.rows;
             // first operand, rows g: queries in registers 0 and 2, probes in 1 and 3
-            uint32_t qf[KR][4];
+            uint32_t qf[KR > 0 ? KR : 1][4];
             int limit = 0;
-            const __nv_bfloat16* gq = a.q;
-            const __nv_bfloat16* gr = a.probe;
+            const uint32_t* gq = static_cast<const uint32_t*>(a.q);        // in words of 32 bits
+            const uint32_t* gr = static_cast<const uint32_t*>(a.probe);
             if (in) {
                 limit = w.causal ? min(max(p.q.L - p.q.nq + over_g(w, fr) + 1, 0), p.q.L) : p.q.L;
-                gq += (long long)token * a.q_stride + (long long)head * D + c2;
-                gr += (long long)token * a.r_stride + (long long)head * D + c2;
+                gq += ((long long)token * a.q_stride + (long long)head * D) * (int)sizeof(T) / 4 + (lane & 3);
+                gr += ((long long)token * a.r_stride + (long long)head * D) * (int)sizeof(T) / 4 + (lane & 3);
             }
             // keys that all of this warp's rows see
             const int all = __reduce_min_sync(0xffffffffu, in ? limit : 0x7fffffff);
@@ -181,14 +229,14 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int k = 0; k < KS; ++k) {
                 uint32_t f[4] = {0u, 0u, 0u, 0u};
                 if (in) {
-                    f[0] = *reinterpret_cast<const uint32_t*>(gq + k * 16);
-                    f[1] = *reinterpret_cast<const uint32_t*>(gr + k * 16);
-                    f[2] = *reinterpret_cast<const uint32_t*>(gq + k * 16 + 8);
-                    f[3] = *reinterpret_cast<const uint32_t*>(gr + k * 16 + 8);
+                    f[0] = gq[k * 8];
+                    f[1] = gr[k * 8];
+                    f[2] = gq[k * 8 + 4];
+                    f[3] = gr[k * 8 + 4];
                 }
                 if (k < KR) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) qf[k % KR][i] = f[i];
+                    for (int i = 0; i < 4; ++i) qf[KR > 0 ? k % KR : 0][i] = f[i];
                 } else {
                     qs[(k - KR) * 32] = make_uint4(f[0], f[1], f[2], f[3]);
                 }
@@ -208,22 +256,24 @@ __global__ void __launch_bounds__(kThreads, 2)
                     if (share1 < share0 + Sh::kShare) {
                         // value rows behind the last key hold a page's rest or an earlier block, and a zero weight does not
                         // remove a NaN: they are cleared (by each of the warps that read them, to the same zeros)
-                        for (int e = share1 * (D / 8) + lane; e < (share0 + Sh::kShare) * (D / 8); e += 32)
-                            *reinterpret_cast<uint4*>(base + (vt - ring) + piece_off<D>(e / (D / 8), e % (D / 8))) = make_uint4(0, 0, 0, 0);
+                        for (int e = share1 * (DB / 8) + lane; e < (share0 + Sh::kShare) * (DB / 8); e += 32)
+                            *reinterpret_cast<uint4*>(base + (vt - ring) + piece_off<DB>(e / (DB / 8), e % (DB / 8))) = make_uint4(0, 0, 0, 0);
                         tc::fence_proxy_async_smem();        // the ring's next copy is the async proxy's
                         __syncwarp();
                     }
 #pragma unroll 1
                     for (int row0 = share0; row0 < share1; row0 += NK * 8) {
-                        float s[NK][4];
+                        float s[NK][4], small[sizeof(T) == 4 ? NK : 1][4];
 #pragma unroll
                         for (int n = 0; n < NK; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+#pragma unroll
+                        for (int n = 0; n < (sizeof(T) == 4 ? NK : 0); ++n) small[n][0] = small[n][1] = small[n][2] = small[n][3] = 0.f;
 #pragma unroll
                         for (int k = 0; k < KS; ++k) {
                             uint32_t f[4];
                             if (k < KR) {
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) f[i] = qf[k % KR][i];
+                                for (int i = 0; i < 4; ++i) f[i] = qf[KR > 0 ? k % KR : 0][i];
                             } else {
                                 const uint4 x = qs[(k - KR) * 32];
                                 f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
@@ -231,10 +281,21 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                             for (int n = 0; n < NK; n += 2) {
                                 uint32_t b[4];
-                                ldsm4(kt + piece_off<D>(row0 + n * 8 + (lane & 7) + ((lane >> 4) << 3), k * 2 + ((lane >> 3) & 1)), b);
-                                mma16816(s[n], f, b[0], b[1]);
-                                mma16816(s[n + 1], f, b[2], b[3]);
+                                ldsm4(kt + piece_off<DB>(row0 + n * 8 + (lane & 7) + ((lane >> 4) << 3), k * 2 + ((lane >> 3) & 1)), b);
+                                if constexpr (sizeof(T) == 2) {
+                                    mma16816(s[n], f, b[0], b[1]);
+                                    mma16816(s[n + 1], f, b[2], b[3]);
+                                } else {
+                                    product(s[n], small[n], f, b[0], b[1]);
+                                    product(s[n + 1], small[n + 1], f, b[2], b[3]);
+                                }
                             }
+                        }
+                        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+                            for (int n = 0; n < NK; ++n)
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) s[n][i] += small[n][i];
                         }
                         const int key0 = j * kKeys + row0;
                         if (key0 + NK * 8 > all) {           // some row does not see all of the step's keys
@@ -289,22 +350,49 @@ __global__ void __launch_bounds__(kThreads, 2)
                         }
                         om += ps;
                         A += pt - s0 * ps;
+                        if constexpr (sizeof(T) == 2) {
 #pragma unroll
-                        for (int kk = 0; kk < NK; kk += 2) {
-                            // the value product takes the weights in bf16 (half a step is 2^-8 of each): its sums are fp32
-                            uint32_t pf[4];
+                            for (int kk = 0; kk < NK; kk += 2) {
+                                // the value product takes the weights in bf16 (half a step is 2^-8 of each): its sums are fp32
+                                uint32_t pf[4];
 #pragma unroll
-                            for (int x = 0; x < 2; ++x) {
-                                const float* y = s[kk + x];
-                                pf[2 * x] = pack_bf16(y[0], y[1]);
-                                pf[2 * x + 1] = pack_bf16(y[0] * (y[2] - s0), y[1] * (y[3] - s0));
+                                for (int x = 0; x < 2; ++x) {
+                                    const float* y = s[kk + x];
+                                    pf[2 * x] = pack_bf16(y[0], y[1]);
+                                    pf[2 * x + 1] = pack_bf16(y[0] * (y[2] - s0), y[1] * (y[3] - s0));
+                                }
+#pragma unroll
+                                for (int n = 0; n < NT / 2; ++n) {
+                                    uint32_t b[4];
+                                    ldsm4t(vt + piece_off<DB>(row0 + kk * 8 + (lane & 15), n * 2 + (lane >> 4)), b);
+                                    mma16816(o[n * 2], pf, b[0], b[1]);
+                                    mma16816(o[n * 2 + 1], pf, b[2], b[3]);
+                                }
+                            }
+                        } else {
+                            // eight keys in the order 0 2 4 6 1 3 5 7, in which a lane has its two weights
+                            uint32_t pf[NK][4];
+#pragma unroll
+                            for (int kk = 0; kk < NK; ++kk) {
+                                const float* y = s[kk];
+                                pf[kk][0] = __float_as_uint(y[0]);
+                                pf[kk][1] = __float_as_uint(y[0] * (y[2] - s0));
+                                pf[kk][2] = __float_as_uint(y[1]);
+                                pf[kk][3] = __float_as_uint(y[1] * (y[3] - s0));
                             }
 #pragma unroll
-                            for (int n = 0; n < NT / 2; ++n) {
-                                uint32_t b[4];
-                                ldsm4t(vt + piece_off<D>(row0 + kk * 8 + (lane & 15), n * 2 + (lane >> 4)), b);
-                                mma16816(o[n * 2], pf, b[0], b[1]);
-                                mma16816(o[n * 2 + 1], pf, b[2], b[3]);
+                            for (int n = 0; n < NT; ++n) {
+                                float t[4] = {0.f, 0.f, 0.f, 0.f}, x[4] = {0.f, 0.f, 0.f, 0.f};
+                                const int c = n * 8 + g;
+                                const unsigned char* v = base + (vt - ring) + (c & 3) * 4;
+#pragma unroll
+                                for (int kk = 0; kk < NK; ++kk) {
+                                    const int vr = row0 + kk * 8 + c2;
+                                    product(t, x, pf[kk], *reinterpret_cast<const uint32_t*>(v + piece_off<DB>(vr, c >> 2)),
+                                            *reinterpret_cast<const uint32_t*>(v + piece_off<DB>(vr + 1, c >> 2)));
+                                }
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) o[n][i] += t[i] + x[i];
                             }
                         }
                     }
@@ -328,10 +416,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (!in) continue;
                 if (p.slot < 0) {
                     const float inv = om != 0.f ? 1.f / om : 0.f, c1 = (1.f + A * inv) * inv;
-                    __nv_bfloat16* out = a.out + ((long long)token * a.Hq + head) * D + c2;
+                    T* out = static_cast<T*>(a.out) + ((long long)token * a.Hq + head) * D + c2;
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        *reinterpret_cast<uint32_t*>(out + n * 8) = pack_bf16(c1 * o[n][0] - inv * o[n][2], c1 * o[n][1] - inv * o[n][3]);
+                    for (int n = 0; n < NT; ++n) put2(out + n * 8, c1 * o[n][0] - inv * o[n][2], c1 * o[n][1] - inv * o[n][3]);
                 } else {
                     float4* ps = part_sums(w, blockIdx.x, p.slot, D);
 #pragma unroll
@@ -390,9 +477,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (p.slot < 0) {
                     const int er = p.row0 + row, tk = over_g(w, er);
                     const float inv = ow != 0.f ? 1.f / ow : 0.f, c1 = (1.f + aw * inv) * inv;
-                    *reinterpret_cast<uint2*>(a.out + ((long long)(p.q.token0 + tk) * a.Hq + p.h * w.G + er - tk * w.G) * D + c) =
-                        make_uint2(pack_bf16(c1 * x1.x - inv * x2.x, c1 * x1.y - inv * x2.y),
-                                   pack_bf16(c1 * x1.z - inv * x2.z, c1 * x1.w - inv * x2.w));
+                    put4(static_cast<T*>(a.out) + ((long long)(p.q.token0 + tk) * a.Hq + p.h * w.G + er - tk * w.G) * D + c,
+                         c1 * x1.x - inv * x2.x, c1 * x1.y - inv * x2.y, c1 * x1.z - inv * x2.z, c1 * x1.w - inv * x2.w);
                 } else {
                     float4* ps = part_sums(w, blockIdx.x, p.slot, D) + (size_t)(c / 4) * R + row;
                     ps[0] = x1;
@@ -416,19 +502,31 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (tid == 0 && err) atomicOr(w.err, (unsigned)kDevErrMbarTimeout);
 }
 
-template <int D, int RS>
-cudaError_t launch_dec(const DecArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
-    constexpr size_t smem = DecShape<D, RS>::smem;
-    auto* kern = paged_decode_kernel<D, RS>;
+template <typename T, int D, int RS>
+cudaError_t launch_one(const DecArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
+    constexpr size_t smem = DecShape<T, D, RS>::smem;
+    auto* kern = paged_decode_kernel<T, D, RS>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_after(kern, dim3(a.w.ctas), kThreads, smem, stream, a, mk, mv);
 }
 
+template <typename T, int D>
+cudaError_t launch_dec(const DecArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t stream) {
+    switch (a.w.rows) {
+        case 8: return launch_one<T, D, 1>(a, mk, mv, stream);
+        case 16: return launch_one<T, D, 2>(a, mk, mv, stream);
+        default: return launch_one<T, D, 4>(a, mk, mv, stream);
+    }
+}
+
 }  // namespace
 }  // namespace paged
 
-bool paged_decode_fits(const PagedProblem& p) { return (long long)p.max_new * p.G <= 32; }
+bool paged_decode_fits(const PagedProblem& p, int path) {
+    if (path == LLA_PATH_TENSOR) return (long long)p.max_new * p.G <= 32;
+    return p.dtype == LLA_DTYPE_FP32 && (p.d == 32 || p.d == 64);
+}
 
 PagedSplit paged_decode_split(const PagedProblem& p, int sms) {
     const long long rows = (long long)p.max_new * p.G;
@@ -437,19 +535,21 @@ PagedSplit paged_decode_split(const PagedProblem& p, int sms) {
 
 cudaError_t launch_paged_decode(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream, const char** why) {
     CUtensorMap mk, mv;
-    if (!paged::make_cache_map(&mk, p.k, p) || !paged::make_cache_map(&mv, p.v, p)) {
+    PagedProblem bytes = p;                    // as a bf16 cache of the same bytes
+    if (p.dtype == LLA_DTYPE_FP32) {
+        bytes.d *= 2;
+        bytes.page_stride *= 2;
+    }
+    if (!paged::make_cache_map(&mk, p.k, bytes) || !paged::make_cache_map(&mv, p.v, bytes)) {
         *why = "tensor map of a paged cache";
         return cudaErrorInvalidValue;
     }
-    paged::DecArgs a{paged::make_work(p, sp), static_cast<const __nv_bfloat16*>(p.q), static_cast<const __nv_bfloat16*>(p.probe),
-                     static_cast<__nv_bfloat16*>(p.out), p.Hq, (int)paged::slices_of_page(p), p.q_stride, p.r_stride, p.tau * 1.4426950408889634f};
-    if (p.d == 128)
-        return sp.rows == 8    ? paged::launch_dec<128, 1>(a, mk, mv, stream)
-               : sp.rows == 16 ? paged::launch_dec<128, 2>(a, mk, mv, stream)
-                               : paged::launch_dec<128, 4>(a, mk, mv, stream);
-    return sp.rows == 8    ? paged::launch_dec<64, 1>(a, mk, mv, stream)
-           : sp.rows == 16 ? paged::launch_dec<64, 2>(a, mk, mv, stream)
-                           : paged::launch_dec<64, 4>(a, mk, mv, stream);
+    paged::DecArgs a{paged::make_work(p, sp), p.q, p.probe, p.out, p.Hq, (int)paged::slices_of_page(p), p.q_stride, p.r_stride,
+                     p.tau * 1.4426950408889634f};
+    if (p.dtype == LLA_DTYPE_FP32)
+        return p.d == 64 ? paged::launch_dec<float, 64>(a, mk, mv, stream) : paged::launch_dec<float, 32>(a, mk, mv, stream);
+    return p.d == 128 ? paged::launch_dec<__nv_bfloat16, 128>(a, mk, mv, stream)
+                      : paged::launch_dec<__nv_bfloat16, 64>(a, mk, mv, stream);
 }
 
 }  // namespace lla

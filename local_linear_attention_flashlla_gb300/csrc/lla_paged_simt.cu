@@ -1,5 +1,5 @@
-// Parallax attention over a paged cache on CUDA cores (every product in fp32; any head dim, bf16 or
-// fp32), and the merge of row tiles that several CTAs share (all paths).
+// Parallax attention over a paged cache on CUDA cores (every product in fp32: bf16 of any head dim, fp32 with
+// d = 16 or 128), and the merge of row tiles that several CTAs share (all paths).
 //
 // Per query row, over its keys in blocks, one pass (base-2 logits l = tau log2(e) q.k, t = probe.k):
 //   m <- max(m, max l),  p = 2^(l - m),  w += p,  A += p (t - s0),  O1 += p v,  O2 += p (t - s0) v,
@@ -34,7 +34,7 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, float4 x) {
 constexpr int kThreads = 256;
 
 // Few rows (a decode step): eight rows of a tile, a warp to a row, a lane two of the 64 keys of a block; warps without
-// a row only help to load.  fp32, 32 sequences x 16 heads at 4096 keys, d = 128: 510 us, 4.2 TB/s, bound by the
+// a row only help to load.  fp32, 32 sequences x 16 heads at 4096 keys, d = 128: 532 us, 4.0 TB/s, bound by the
 // shared-memory reads of K beside the loads.
 template <int D>
 struct FewShape {
@@ -282,8 +282,8 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_few_kernel(SimtArgs a)
 // product a lane has two rows and an eighth of the keys, in the second the same rows and an eighth of the output
 // columns.  So a 16-byte read of K or V serves two rows and one of q, the probe or the weights eight keys or columns:
 // eight reads to 64 products (a row a thread and four keys: six to 32), and shared-memory reads bound this kernel:
-// 16 sequences of 1 to 97 new tokens over 200 to 1024 keys, 4 heads, d = 32, 35 us (44 with a row a thread); 30
-// TFLOP/s on longer chunks.
+// 64 sequences of 1 to 97 new tokens over 200 to 1024 keys, 4 heads, fp32, d = 128: 369 us, 24 TFLOP/s (d = 32, which
+// the tensor cores have now, 16 sequences: 35 us, 44 with a row a thread).
 // Products and sums are pairs of fp32 (fma.rn.f32x2: each rounded as the scalar instruction).
 constexpr int kManyThreads = 128;
 
@@ -663,8 +663,12 @@ cudaError_t launch_one(const SimtArgs& a, cudaStream_t stream) {
     return launch_after(kern, dim3(a.w.ctas), few ? kThreads : kManyThreads, smem, stream, a);
 }
 
-template <typename T>
-cudaError_t launch_typed(const SimtArgs& a, int d, cudaStream_t stream) {
+cudaError_t launch_fp32(const SimtArgs& a, int d, cudaStream_t stream) {
+    return d == 16 ? launch_one<float, 16>(a, stream) : launch_one<float, 128>(a, stream);
+}
+
+cudaError_t launch_bf16(const SimtArgs& a, int d, cudaStream_t stream) {
+    using T = __nv_bfloat16;
     switch (d) {
         case 16: return launch_one<T, 16>(a, stream);
         case 32: return launch_one<T, 32>(a, stream);
@@ -713,8 +717,7 @@ PagedSplit paged_simt_split(const PagedProblem& p, int sms) {
 cudaError_t launch_paged_simt(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream) {
     paged::SimtArgs a{paged::make_work(p, sp), p.q, p.probe, p.k, p.v, p.out, p.Hq, p.q_stride, p.r_stride,
                       p.page_stride, p.tau * 1.4426950408889634f};
-    return p.dtype == LLA_DTYPE_BF16 ? paged::launch_typed<__nv_bfloat16>(a, p.d, stream)
-                                     : paged::launch_typed<float>(a, p.d, stream);
+    return p.dtype == LLA_DTYPE_BF16 ? paged::launch_bf16(a, p.d, stream) : paged::launch_fp32(a, p.d, stream);
 }
 
 cudaError_t launch_paged_merge(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream) {

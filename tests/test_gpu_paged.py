@@ -278,6 +278,36 @@ def test_up_to_32_rows_to_a_key_head(lla_gpu, d, causal, G, most):
     assert torch.equal(out, run(c, lla.LLA_PATH_TENSOR, out=out.clone()))
 
 
+@pytest.mark.parametrize("d", [16, 32, 64, 128])
+@pytest.mark.parametrize("G,most", [(1, 1), (3, 5), (4, 8), (1, 70)])
+def test_fp32_sets_of_rows(lla_gpu, d, G, most):
+    """Sets of eight fp32 rows.  Products of halves (d = 32, 64) are off by at most 3 2^-22 = 12 2^-24 of themselves: in
+    the logit, in t and in the value product 36 2^-24 of the terms together, within the 32 + 2 d of the bound."""
+    new, kv = [most, 1, most, 0, most], [most, 300, 65 + most, 10, 2500]
+    c = Case(new, kv, 2 * G, 2, d, 16, "fp32", pad=2, scale=1.5)
+    out = torch.full((len(c.q), 2 * G, d), 123.0, device="cuda")
+    got = c.check(run(c, out=out), False)
+    assert (got[c.cu[-1]:] == 123.0).all()
+
+
+def test_fp32_products_hold_more_than_two_terms_of_11_bits(lla_gpu):
+    """One key: out is its value, to fp32's last bits although each half has 11 (one or two products would leave 2^-11
+    or 2^-12 of it)."""
+    for d in (32, 64, 128):
+        c = Case([1] * 40, [1] * 40, 4, 2, d, 8, "fp32")
+        got = run(c).double().cpu().numpy()
+        assert np.abs(got / c.ref()[0] - 1).max() <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** 100])
+def test_fp32_values_of_any_size(lla_gpu, size):
+    """The scale of the values is that of the result: a power of two leaves the same bits."""
+    c = Case([1, 5], [50, 200], 4, 2, 64, 16, "fp32")
+    a = c.device()
+    plain = run(c)
+    assert torch.equal(plain * size, run(c, v_cache=a["v_cache"] * size))
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("fp32", 32)])
 @pytest.mark.parametrize("new,kv", [([5, 40, 1], [77, 1, 130]), ([1, 1], [500, 33]), ([300], [129])])
 def test_cross_attention(lla_gpu, dtype, d, new, kv):
