@@ -330,7 +330,7 @@ int lla_paged_plan(const int* ctx_lens, const int* new_lens, int S, int page_siz
     at[0].val.clusterDim.x = ctas;
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = ctas > 1;                   // a CTA alone is a cluster of one
     e = cudaLaunchKernelEx(&cfg, lla::paged_plan_kernel, a);
     if (e != cudaSuccess) return cuda_failf(e, "lla_paged_plan launch");
     return LLA_OK;
