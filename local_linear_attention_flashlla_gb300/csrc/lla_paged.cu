@@ -49,11 +49,10 @@ int sm_count() {
 // are taken by every CTA for itself, in shared memory; the token rows and new pages are then dealt to
 // the CTAs of one cluster, each finding its sequence by bisection of the sums.  What it moves is a few
 // bytes a sequence and 12 a row: latency bounds it (two dependent reads and the scans), so it is one
-// launch (5.7 us for 64 decoding sequences, 12 us for 512 sequences with 64,000 new rows; a CTA alone took 13).  The cluster barrier lets kv_lens take ctx_lens' place and free_left free_count's: they are
+// launch (3.6 us for 64 decoding sequences, where 256 threads do: 1024 took 5.5; 10.3 us for 512 sequences with
+// 64,000 new rows, where a thread has one sequence: 11.8 with room for eight, more in one CTA).  The cluster barrier lets kv_lens take ctx_lens' place and free_left free_count's: they are
 // written after every CTA has read.
-constexpr int kPlanThreads = 1024;
 constexpr int kPlanMaxSeqs = 8192;
-constexpr int kPlanPer = kPlanMaxSeqs / kPlanThreads;
 
 struct PlanArgs {
     const int* ctx;
@@ -70,7 +69,8 @@ struct PlanArgs {
     int S, width, page_shift, free_cap, T;
 };
 
-// Inclusive sum over the block's threads in thread order.
+// Inclusive sum over the block's TH threads in thread order.
+template <int TH>
 __device__ long long scan_block(long long v, long long* red) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int o = 1; o < 32; o <<= 1) {
@@ -80,7 +80,7 @@ __device__ long long scan_block(long long v, long long* red) {
     if (lane == 31) red[warp] = v;
     __syncthreads();
     if (warp == 0) {
-        long long x = red[lane];
+        long long x = lane < TH / 32 ? red[lane] : 0;
         for (int o = 1; o < 32; o <<= 1) {
             const long long t = __shfl_up_sync(0xffffffffu, x, o);
             if (lane >= o) x += t;
@@ -104,7 +104,8 @@ __device__ __forceinline__ int bisect(const int* a, int n, int x) {
     return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
+template <int TH, int PER>           // at most TH PER sequences
+__global__ void __launch_bounds__(TH) paged_plan_kernel(PlanArgs a) {
     namespace cg = cooperative_groups;
     extern __shared__ int psm[];
     __shared__ long long red[32];
@@ -116,14 +117,14 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
     const int tid = threadIdx.x, page = 1 << a.page_shift;
-    const int per = (a.S + kPlanThreads - 1) / kPlanThreads, s0 = tid * per;
+    const int per = (a.S + TH - 1) / TH, s0 = tid * per;
     const int have = min(max(*a.free_count, 0), a.free_cap);
 
     if (tid == 0) taken_sh = 0;
-    int c[kPlanPer], n[kPlanPer];
+    int c[PER], n[PER];
     long long rows = 0;
 #pragma unroll
-    for (int i = 0; i < kPlanPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
         c[i] = n[i] = 0;
         if (i < per && s0 + i < a.S) {
             c[i] = max(a.ctx[s0 + i], 0);
@@ -131,13 +132,13 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
             rows += n[i];
         }
     }
-    const long long rows_end = scan_block(rows, red);
+    const long long rows_end = scan_block<TH>(rows, red);
     long long row = rows_end - rows, asks = 0;
     const long long room = (long long)a.width << a.page_shift;
-    int need[kPlanPer];
-    bool fits[kPlanPer];
+    int need[PER];
+    bool fits[PER];
 #pragma unroll
-    for (int i = 0; i < kPlanPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
         need[i] = 0;
         fits[i] = false;
         if (i < per && s0 + i < a.S) {
@@ -150,11 +151,11 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
             asks += need[i];
         }
     }
-    const long long asks_end = scan_block(asks, red);
+    const long long asks_end = scan_block<TH>(asks, red);
     long long ask = asks_end - asks;
     int taken = 0;
 #pragma unroll
-    for (int i = 0; i < kPlanPer; ++i)
+    for (int i = 0; i < PER; ++i)
         if (i < per && s0 + i < a.S) {
             base[s0 + i] = (int)(ask < have ? ask : have);
             ask += need[i];
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
         }
     if (taken) atomicMax(&taken_sh, taken);
     // rows_end of the last thread is the number of token rows
-    if (tid == kPlanThreads - 1) red[0] = rows_end;
+    if (tid == TH - 1) red[0] = rows_end;
     __syncthreads();
     const int total_rows = (int)(red[0] < a.T ? red[0] : a.T);
     taken = taken_sh;
@@ -172,8 +173,8 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
     // a warp takes runs of 32 kRun rows, a lane every 32nd of them: a bisection where the sequence changes, the table
     // reads side by side
     constexpr int kRun = 4;
-    const int lane = tid & 31, warps = ranks * (kPlanThreads / 32);
-    for (int t0 = (rank * (kPlanThreads / 32) + (tid >> 5)) * 32 * kRun; t0 < a.T; t0 += warps * 32 * kRun) {
+    const int lane = tid & 31, warps = ranks * (TH / 32);
+    for (int t0 = (rank * (TH / 32) + (tid >> 5)) * 32 * kRun; t0 < a.T; t0 += warps * 32 * kRun) {
         int pos[kRun], id[kRun], s = bisect(cu, a.S, min(t0 + lane, max(total_rows - 1, 0)));
 #pragma unroll
         for (int i = 0; i < kRun; ++i) {
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
             }
         }
     }
-    for (int k = rank * kPlanThreads + tid; k < taken; k += ranks * kPlanThreads) {
+    for (int k = rank * TH + tid; k < taken; k += ranks * TH) {
         const int s = bisect(base, a.S, k);
         const int held = (ctx[s] + page - 1) >> a.page_shift;
         a.table[(size_t)s * a.width + held + (k - base[s])] = a.free_pages[have - 1 - k];
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(kPlanThreads) paged_plan_kernel(PlanArgs a) {
     cluster.sync();
     if (rank == 0) {
 #pragma unroll
-        for (int i = 0; i < kPlanPer; ++i)
+        for (int i = 0; i < PER; ++i)
             if (i < per && s0 + i < a.S) {
                 a.kv_lens[s0 + i] = c[i] + (okay[s0 + i] ? n[i] : 0);
                 a.granted[s0 + i] = okay[s0 + i];
@@ -316,13 +317,15 @@ int lla_paged_plan(const int* ctx_lens, const int* new_lens, int S, int page_siz
                     granted, free_left, S, table_width, shift, free_capacity, T};
     const size_t smem = (size_t)S * 4 * sizeof(int);
     cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024)
-        e = cudaFuncSetAttribute(lla::paged_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    auto* kern = S <= 256 && T <= 1024 ? lla::paged_plan_kernel<256, 1>
+                 : S <= 1024           ? lla::paged_plan_kernel<1024, 1>
+                                       : lla::paged_plan_kernel<1024, lla::kPlanMaxSeqs / 1024>;
+    if (smem > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return cuda_failf(e, "lla_paged_plan");
     const int ctas = T > 4096 ? 8 : T > 1024 ? 4 : 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
-    cfg.blockDim = dim3(lla::kPlanThreads);
+    cfg.blockDim = dim3(S <= 256 && T <= 1024 ? 256 : 1024);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream_);
     cudaLaunchAttribute at[1];
@@ -331,7 +334,7 @@ int lla_paged_plan(const int* ctx_lens, const int* new_lens, int S, int page_siz
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = ctas > 1;                   // a CTA alone is a cluster of one
-    e = cudaLaunchKernelEx(&cfg, lla::paged_plan_kernel, a);
+    e = cudaLaunchKernelEx(&cfg, kern, a);
     if (e != cudaSuccess) return cuda_failf(e, "lla_paged_plan launch");
     return LLA_OK;
 }

@@ -108,6 +108,19 @@ def test_plan_in_place_decode_loop_in_a_graph(lla_gpu):
 
 
 # ----------------------------------------------------------------------------------------- append
+@pytest.mark.parametrize("S,new_hi,count", [(255, 1, None), (256, 3, None), (257, 3, None), (256, 3, 40), (256, 9, None),
+                                            (30, 64, None), (31, 70, 20), (1024, 2, None), (1024, 5, 300)])
+def test_plan_where_the_block_size_changes(lla_gpu, S, new_hi, count):
+    """Up to 256 sequences and 1024 rows a small block plans, beyond either a large one; from 1025 sequences on a thread
+    has several."""
+    ctx, new, table, free, count, T = _plan_case(S + new_hi, S, 8, 2, 100, new_hi, None, count)
+    for rows in {T, max(1024, T), max(1025, T)}:          # more rows than the step's tokens: a padded batch
+        tb = _i32(table)
+        got = lla.paged_plan(_i32(ctx), _i32(new), tb, _i32(free), _i32([count]), 8, rows)
+        torch.cuda.synchronize()
+        _check_plan(ctx, new, table, free, count, 8, rows, got, tb)
+
+
 @pytest.mark.parametrize("dtype,d,Hkv,page,T", [("bf16", 128, 8, 16, 1), ("bf16", 16, 1, 8, 77), ("fp32", 32, 3, 64, 300),
                                                 ("bf16", 64, 5, 256, 1000), ("fp32", 128, 2, 32, 4097)])
 def test_append(lla_gpu, dtype, d, Hkv, page, T):
