@@ -312,6 +312,48 @@ def test_fp32_products_hold_more_than_two_terms_of_11_bits(lla_gpu):
         assert np.abs(got / c.ref()[0] - 1).max() <= 2.0 ** -20
 
 
+def test_fp32_attention_past_32_bit_offsets(lla_gpu):
+    """A page whose elements lie past 2^32 (an fp32 cache of 17 GB each): one key, so out is its value to 3 2^-22."""
+    page, Hkv, d = 64, 8, 64
+    P = (1 << 32) // (page * Hkv * d) + 2
+    kc = torch.zeros(P, Hkv, page, d, device="cuda")
+    vc = torch.zeros_like(kc)
+    k = torch.randn(1, Hkv, d, device="cuda")
+    lla.paged_append(k, -k, torch.tensor([(P - 1) * page], device="cuda"), kc, vc)
+    out = lla.paged_parallax(torch.randn_like(k), torch.zeros_like(k), kc, vc, _i32([[P - 1]]), _i32([0, 1]), _i32([1]), 0.1, 1)
+    torch.cuda.synchronize()
+    lla.lla_sync_status()
+    assert (out / -k - 1).abs().max() <= 2.0 ** -20
+
+
+@pytest.mark.parametrize("d", [32, 64])
+def test_fp32_captured_step_replays_with_other_lengths(lla_gpu, d):
+    c = Case([1, 5, 1], [200, 70, 900], 4, 2, d, 16, "fp32")
+    a = c.device()
+    shorter = [150, 66, 3]
+    want = [run(c), None]
+    short = Case([1, 5, 1], shorter, 4, 2, d, 16, "fp32")
+    short.kc, short.vc, short.table = c.kc, c.vc, c.table
+    short.q, short.probe, short.P = c.q, c.probe, c.P
+    want[1] = run(short)
+    out, lens = torch.empty_like(a["q"]), a["kv_lens"].clone()
+    a["kv_lens"] = lens
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        lla.paged_parallax(**a, out=out)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lla.paged_parallax(**a, out=out)
+    for kv, ref in ((c.kv, want[0]), (shorter, want[1]), (c.kv, want[0])):
+        lens.copy_(_i32(kv))
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+    lla.lla_sync_status()
+
+
 @pytest.mark.parametrize("size", [2.0 ** -100, 2.0 ** 100])
 def test_fp32_values_of_any_size(lla_gpu, size):
     """The scale of the values is that of the result: a power of two leaves the same bits."""
