@@ -139,7 +139,8 @@ size_t lla_forward_host_buffer_size(int dtype, int path, int B, int H, int n, in
  * word: set when a bounded wait inside a kernel gave up (LLA_ERR_DEVICE_TIMEOUT), when the
  * tensor kernel found its dynamic shared memory not 1024-byte aligned and did no work
  * (LLA_ERR_CUDA), or when a paged call found a length, slot or page id on the device that its
- * tensors do not hold (LLA_ERR_INVALID_ARG).
+ * tensors do not hold (LLA_ERR_INVALID_ARG).  Where several were set, work that was not done or not
+ * finished is what it returns, and the message names the paged call's argument as well.
  */
 int lla_sync_status(void* stream);
 

@@ -150,7 +150,8 @@ def lla_profile_read():
 
 
 def lla_sync_status(stream=None):
-    """Synchronise the stream and raise if a kernel recorded a device-side wait timeout."""
+    """Synchronise the stream and raise if a kernel recorded an error: a device-side wait timeout, no work done, or a
+    paged call's length, slot or page id that its tensors do not hold (include/lla.h)."""
     _check(load_library().lla_sync_status(_stream_ptr(stream)))
 
 

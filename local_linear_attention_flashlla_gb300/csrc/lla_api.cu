@@ -676,14 +676,17 @@ int lla_sync_status(void* stream) {
     unsigned word = 0;
     cudaError_t e = lla::read_and_clear_device_error(&word, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return lla::cuda_fail(e, "lla_sync_status");
+    // results that no kernel finished come before an argument whose access was cut; the message names both
+    const bool arg = word & lla::kDevErrPagedArg;
+    const char* also = arg ? ", and a paged call met a length, slot or page id that its tensors do not hold" : "";
     if (word & lla::kDevErrSmemAlign)
-        return fail(LLA_ERR_CUDA, "tensor kernel: dynamic shared memory not 1024-byte aligned, no work done (error word 0x%x)",
-                    word);
-    if (word & lla::kDevErrPagedArg)
+        return fail(LLA_ERR_CUDA, "tensor kernel: dynamic shared memory not 1024-byte aligned, no work done%s (error word 0x%x)",
+                    also, word);
+    if (word & lla::kDevErrMbarTimeout)
+        return fail(LLA_ERR_DEVICE_TIMEOUT, "a bounded device-side wait gave up%s (error word 0x%x)", also, word);
+    if (arg)
         return fail(LLA_ERR_INVALID_ARG,
                     "a paged call met a length, slot or page id that its tensors do not hold (error word 0x%x)", word);
-    if (word & lla::kDevErrMbarTimeout)
-        return fail(LLA_ERR_DEVICE_TIMEOUT, "a bounded device-side wait gave up (error word 0x%x)", word);
     return LLA_OK;
 }
 
