@@ -22,6 +22,7 @@
 #include "../../include/lla.h"
 #include "lla_internal.h"
 #include "lla_paged.h"
+#include "paged_feed.h"
 #include "paged_tc.cuh"
 
 namespace lla {
@@ -72,47 +73,57 @@ struct TcBars {
     float2 tot[2][kRows];                      // by column half: omega and A of a tile
 };
 
-// One box to a lane; K and V of a block go to rings of their own (K is given back a product earlier).
+// What feed_kv's two rings of copies are filled and drained through (paged_feed.h): one box to a lane.
+template <int D>
+struct KvRings {
+    const CUtensorMap* map[2];                 // of K, of V
+    uint32_t ring[2];
+    TcBars<D>& b;
+    int box, lane;
+    // the block at hand: this lane's box, if it has one, and the boxes' bytes
+    bool mine;
+    int group, slice;
+    uint32_t bytes;
+
+    __device__ __forceinline__ uint64_t* full(int kv, int stage) { return kv ? &b.vfull[stage] : &b.kfull[stage]; }
+    __device__ __forceinline__ bool wait_empty(int kv, int stage, int parity) {
+        return __all_sync(0xffffffffu, mbar_wait(kv ? &b.vempty[stage] : &b.kempty[stage], parity, &b.err));
+    }
+    __device__ __forceinline__ void copy(int kv, int stage) {
+        if (lane == 0) mbar_arrive_expect_tx(full(kv, stage), bytes);
+        __syncwarp();
+        if (mine) {
+            const uint32_t dst = ring[kv] + (uint32_t)(stage * TcShape<D>::kTile + lane * box * D * 2);
+            tma_load_rows(dst, map[kv], full(kv, stage), group, slice);
+        }
+        __syncwarp();
+    }
+    __device__ __forceinline__ void wait_full(int kv, int stage, int parity) { drain(full(kv, stage), parity); }
+};
+
+// K and V of a block go to rings of their own (K is given back a product earlier).
 template <int D>
 __device__ void feed_kv(const Work& w, Walk wk, const CUtensorMap* mk, const CUtensorMap* mv, int slices, uint32_t kring,
                         uint32_t vring, TcBars<D>& b) {
-    constexpr int NS = TcShape<D>::kStages, kTile = TcShape<D>::kTile, kKeys = TcShape<D>::kKeys;
+    constexpr int NS = TcShape<D>::kStages, kKeys = TcShape<D>::kKeys;
     const int lane = threadIdx.x & 31;
     const int box = min(1 << w.page_shift, kBoxRows), boxes = kKeys / box;     // <= 16
-    int n = 0;                                 // blocks issued
+    KvRings<D> rings{{mk, mv}, {kring, vring}, b, box, lane, false, 0, 0, 0};
+    RingCount<NS> n;
     bool ok = true;
     Piece p;
     while (ok && next_piece(w, wk, p)) {
         const int* row = w.table + (size_t)p.s * w.width;
-        for (int j = p.j0; j < p.j1; ++j, ++n) {
+        for (int j = p.j0; ok && j < p.j1; ++j) {
             const int key = j * kKeys + lane * box;
-            const bool mine = lane < boxes && key < p.keys;
-            const int page = mine ? checked_page(w, row, key) : 0;
-            const int y = key & ((1 << w.page_shift) - 1);
-            const uint32_t bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, mine)) * box * D * 2);
-            const int st = n % NS;
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-                uint64_t* full = kv ? &b.vfull[st] : &b.kfull[st];
-                uint64_t* empty = kv ? &b.vempty[st] : &b.kempty[st];
-                ok = __all_sync(0xffffffffu, mbar_wait(empty, ((n / NS) & 1) ^ 1, &b.err));
-                if (!ok) break;
-                if (lane == 0) mbar_arrive_expect_tx(full, bytes);
-                __syncwarp();
-                if (mine) {
-                    const uint32_t dst = (kv ? vring : kring) + (uint32_t)(st * kTile + lane * box * D * 2);
-                    tma_load_rows(dst, kv ? mv : mk, full, y >> 3, page * slices + p.h);
-                }
-                __syncwarp();
-            }
-            if (!ok) break;
+            rings.mine = lane < boxes && key < p.keys;
+            rings.slice = (rings.mine ? checked_page(w, row, key) : 0) * slices + p.h;
+            rings.group = (key & ((1 << w.page_shift) - 1)) >> 3;
+            rings.bytes = (uint32_t)(__popc(__ballot_sync(0xffffffffu, rings.mine)) * box * D * 2);
+            ok = n.feed_block(rings);
         }
     }
-    if (!ok || *(volatile int*)&b.err)         // copies in flight land before the CTA gives its memory back
-        for (int t = max(n - NS, 0); t < n; ++t) {
-            drain(&b.kfull[t % NS], (t / NS) & 1);
-            drain(&b.vfull[t % NS], (t / NS) & 1);
-        }
+    if (!ok || *(volatile int*)&b.err) n.drain(rings);    // copies in flight land before the CTA gives its memory back
 }
 
 // D[tmem] = A B^T, 128 x kKeys x D, both operands K-major in shared memory.
