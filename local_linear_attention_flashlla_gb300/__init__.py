@@ -615,23 +615,42 @@ def _bind():
 
 
 # Scratch of eager attention calls by (device, stream, host thread): a thread's calls on one stream follow one
-# another, so they can share it, and taking it from the allocator costs as much as all checks.  A call under
-# graph capture takes its own (the graph keeps it), so that graphs never share scratch with anything.  At most
-# eight are kept.
+# another, so they can share it, and taking it from the allocator costs as much as all checks.  A thread keeps at
+# most eight, and they go back to the allocator when it ends.
 _SCRATCH = {}
+
+
+class _ThreadKeys(list):
+    """Keys of _SCRATCH that are one thread's, the oldest first."""
+
+    def __del__(self, pop=_SCRATCH.pop):
+        for key in self:
+            pop(key, None)
+
+
+class _Thread(threading.local):
+    def __init__(self):
+        self.keys = _ThreadKeys()
+
+
+_THREAD = _Thread()
 
 
 def _scratch(device, stream_ptr, nbytes):
     import torch
+    # a call under graph capture takes its own (the graph keeps it), so that graphs never share scratch with anything
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    key = (device.index, stream_ptr, threading.get_ident())
+    keys, key = _THREAD.keys, (device.index, stream_ptr, threading.get_ident())
     t = _SCRATCH.get(key)
     if t is None or t.numel() < nbytes:
-        _SCRATCH.pop(key, None)
-        while len(_SCRATCH) >= 8:
-            _SCRATCH.pop(next(iter(_SCRATCH)), None)
-        t = _SCRATCH[key] = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        if _SCRATCH.pop(key, None) is not None:
+            keys.remove(key)
+        while len(keys) >= 8:
+            _SCRATCH.pop(keys.pop(0), None)
+        t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        keys.append(key)
+        _SCRATCH[key] = t
     return t
 
 
@@ -717,7 +736,7 @@ def paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, 
     block_table [S, W], cu_q [S+1], kv_lens [S]: int32 CUDA tensors (paged_plan's); max_new: the most
     tokens of one sequence in this step.  causal=False: every row sees all of its sequence's keys.
     Returns out [T, Hq, d]; rows behind the last sequence are left as they were.  Asynchronous on the
-    current (or given) stream.  workspace: None (scratch kept per stream and thread; under graph capture the
+    current (or given) stream.  workspace: None (scratch kept per stream while the thread lives; under graph capture the
     graph's own), or a CUDA tensor of lla_paged_parallax_workspace_size(...) bytes that no other call uses at the
     same time.
     """
