@@ -4,8 +4,9 @@ Each CUDA translation unit under csrc/ is compiled in parallel to an object in
 _build/, then linked into liblla.so next to this file.  No CMake, no torch
 extension machinery: the library has a plain C ABI (include/lla.h).
 csrc/paged_bind.c, the paged calls' argument marshalling, becomes the extension
-module _paged_bind where the Python headers are there; without it the binding
-marshals in Python.
+module _paged_bind where a C compiler and the Python headers are there; without
+it, or where it does not compile (a warning says so), the binding marshals in
+Python.  A module of an earlier build is never left beside a newer library.
 """
 from __future__ import annotations
 
@@ -13,6 +14,7 @@ import os
 import shutil
 import subprocess
 import sysconfig
+import warnings
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -46,14 +48,25 @@ def _run(cmd):
     return r.stdout
 
 
+def _drop_binding():
+    if os.path.exists(BIND):
+        os.remove(BIND)
+
+
 def build_binding():
-    """Compile _paged_bind.so; returns its path, or None without a C compiler or the Python headers."""
+    """Compile _paged_bind.so; returns its path, or None (and no module) without a C compiler or the Python headers, or
+    with a warning where it does not compile."""
+    _drop_binding()
     include = sysconfig.get_paths()["include"]
     cc = shutil.which("gcc") or shutil.which("cc")
     if not cc or not os.path.exists(os.path.join(include, "Python.h")):
         return None
     tmp = BIND + ".tmp"
-    _run([cc, "-O2", "-shared", "-fPIC", "-I" + include, os.path.join(CSRC, "paged_bind.c"), "-o", tmp])
+    try:
+        _run([cc, "-O2", "-shared", "-fPIC", "-I" + include, os.path.join(CSRC, "paged_bind.c"), "-o", tmp])
+    except RuntimeError as e:
+        warnings.warn(f"the paged calls will be marshalled in Python: {e}")
+        return None
     os.replace(tmp, BIND)
     return BIND
 
@@ -67,7 +80,6 @@ def build(verbose=False, extra_flags=()):
     for lib, srcs in groups.items():
         for s in srcs:
             jobs.append((lib, s, os.path.join(BUILD, os.path.basename(s)[:-3] + ".o")))
-    build_binding()
     cmds = [[nvcc, *ARCH, *NVFLAGS, *extra_flags, "-c", s, "-o", o] for _, s, o in jobs]
     with ThreadPoolExecutor(max_workers=max(1, min(len(cmds), os.cpu_count() or 1))) as ex:
         outs = list(ex.map(_run, cmds))
@@ -80,7 +92,9 @@ def build(verbose=False, extra_flags=()):
         objs = [o for l, _, o in jobs if l == lib]
         tmp = lib + ".tmp"
         _run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"])
+        _drop_binding()                # has the signatures of the library before
         os.replace(tmp, lib)
+    build_binding()
     return LIB
 
 
