@@ -358,6 +358,9 @@ size_t lla_backward_host_buffer_size(int dtype, int path, int B, int H, int n, i
  * tokens or none: it is refused when ctx + new exceeds table_width * page_size, when its rows do not
  * lie within T, or when it needs pages and the free list does not hold its pages and those of the
  * sequences before it; a refused sequence keeps its length and its table row, and its rows' slots are -1.
+ * It keeps its token rows too, and lla_paged_parallax does not know of the refusal: it computes them as the
+ * tokens of the last n of the ctx positions (rows before the first: zeros).  Those are numbers, but
+ * no answer for these tokens: the caller drops the rows by `granted` and brings the tokens again.
  *
  * ctx_lens, new_lens  [S] int32.
  * block_table  [S, table_width] int32, updated: the ceil(ctx/page_size) entries held are read, entries

@@ -663,6 +663,8 @@ def paged_plan(ctx_lens, new_lens, block_table, free_pages, free_count, page_siz
     stack of free page ids; num_rows: token rows of the step's tensors.  All int32 CUDA tensors.
     Returns PagedPlan(kv_lens [S], cu_q [S+1], slots [num_rows] int64, positions [num_rows], granted [S],
     free_left [1]).  kv_lens=ctx_lens and free_left=free_count update a decode loop's state in place.
+    A sequence is granted all of its tokens or none; what paged_parallax gives for the rows of a refused one
+    (granted 0) is no answer for its tokens and has to be dropped.
     Asynchronous on the current (or given) stream.
     """
     import torch
