@@ -347,7 +347,8 @@ size_t lla_backward_host_buffer_size(int dtype, int path, int B, int H, int n, i
  * sequence s has rows cu_q[s] .. cu_q[s+1]-1, and rows from cu_q[S] on are padding.  A step is
  * lla_paged_plan, then per layer lla_paged_append and lla_paged_parallax.  Every length lives on the
  * device and no call synchronises, so a step can be captured into a CUDA graph and replayed with other
- * lengths.
+ * lengths.  T, S and the free list's capacity are at least 1 (LLA_ERR_INVALID_ARG otherwise): a step without
+ * tokens makes no calls.
  *
  * lla_paged_plan -- block tables and slot maps from request lengths, on the GPU.
  *
@@ -411,21 +412,29 @@ int lla_paged_append(int dtype, const void* k_new, const void* v_new, const long
  *
  * dtype      of q, probe, out and the caches.  The probe is taken in dtype (lla_parallax_forward
  *            takes fp32), as a serving projection gives it.
- * path       LLA_PATH_AUTO: bf16 with d in {64, 128} takes LLA_PATH_TENSOR, all else LLA_PATH_FP32.  There
- *            fp32 tensors with d in {32, 64} are multiplied as three tensor-core products of their upper and lower
- *            11 bits (each product within 3 2^-22 of itself; magnitudes from 2^127 on count as infinite), all
- *            else in fp32 on CUDA cores; weights, sums and states are fp32 in both.
+ * path       LLA_PATH_AUTO: bf16 with d in {64, 128} takes LLA_PATH_TENSOR, all else LLA_PATH_FP32.  Logits, sums
+ *            and states are fp32 in both.
+ *            LLA_PATH_TENSOR trades precision for speed: the weights p and p (t - c0) are rounded to bf16 before the
+ *            value products, 2^-8 of each term at most (outputs are off from float64 by 2.4e-3 of their norm, where
+ *            the rounding of the output alone gives 1.7e-3).  bf16 tensors take fp32 weights and products on
+ *            CUDA cores with LLA_PATH_FP32, by name.
+ *            LLA_PATH_FP32 multiplies fp32 tensors with d in {32, 64} as three tensor-core products of their upper
+ *            and lower 11 bits: each product within 3 2^-22 of itself for magnitudes from 2^-114 on (below, an
+ *            operand is off by up to 2^-136) to 2^127 (from there on they count as infinite, and an infinity gives
+ *            NaN); all else in fp32 on CUDA cores.
  * q, probe   [T, Hq, d], token strides q_stride / probe_stride elements (>= Hq*d, multiples of 16 bytes).
  * out        [T, Hq, d] contiguous; rows behind the last sequence are not written.
  * block_table [S, table_width], cu_q [S+1], kv_lens [S] int32.  max_new: the most tokens of a sequence
- *            (T serves; a small value lets a decode step take the decode kernel).
+ *            (T serves).  It chooses the kernel and the height of the row tiles for the whole batch: bf16 with
+ *            max_new * Hq/Hkv <= 32 takes the decode kernel, more 128-row tiles; a batch of single tokens called
+ *            with a large max_new is slower (by a fifth at d = 128, by half at d = 64, twofold in fp32).
  * Hq a multiple of Hkv; d in {16, 32, 64, 128}; S <= 2^20; T*Hq <= 2^30; table_width*page_size <= 2^28
  * and, times Hq/Hkv, <= 2^30; Hq/Hkv <= 1024.
  * Lengths or page ids on the device that lie outside the tensors (cu_q beyond T or falling, more than
  * max_new tokens, kv_lens beyond the table, a page id outside [0, num_pages)) are never followed: the
  * access is cut or reads zeros, and lla_sync_status reports LLA_ERR_INVALID_ARG.  What pages hold behind a
  * sequence's length never reaches a result; values at positions that are part of it should be finite (a
- * NaN or infinity at one position can reach rows of the same step that do not see it).
+ * NaN or infinity at one position can reach rows of the same step that do not see it; a row that reads a NaN is NaN).
  * workspace  NULL (stream-ordered pool) or lla_paged_parallax_workspace_size(...) bytes, 256-byte aligned,
  *            used by no other call at the same time; its contents need not be kept or cleared.
  * Results do not depend on the run: the order of every sum is fixed by the lengths.

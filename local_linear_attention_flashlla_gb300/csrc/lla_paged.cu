@@ -49,9 +49,9 @@ int sm_count() {
 // are taken by every CTA for itself, in shared memory; the token rows and new pages are then dealt to
 // the CTAs of one cluster, each finding its sequence by bisection of the sums.  What it moves is a few
 // bytes a sequence and 12 a row: latency bounds it (two dependent reads and the scans), so it is one
-// launch (3.6 us for 64 decoding sequences, where 256 threads do: 1024 took 5.5; 10.3 us for 512 sequences with
-// 64,000 new rows, where a thread has one sequence: 11.8 with room for eight, more in one CTA).  The cluster barrier lets kv_lens take ctx_lens' place and free_left free_count's: they are
-// written after every CTA has read.
+// launch (on the device 3.6 us for 64 decoding sequences, where 256 threads do: 1024 took 5.5; 10.4 us for 512 sequences
+// with 64,000 new rows, where a thread has one sequence: 11.8 with room for eight, more in one CTA).  The cluster barrier
+// lets kv_lens take ctx_lens' place and free_left free_count's: they are written after every CTA has read.
 constexpr int kPlanMaxSeqs = 8192;
 
 struct PlanArgs {
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(TH) paged_plan_kernel(PlanArgs a) {
 //
 // A thread moves 16 bytes of a key row and the 16 bytes of the value row at the same place: both
 // directions are whole rows of d elements, so every warp reads and writes full lines.  Bound by the
-// copied bytes: 145 MB of prompt rows (8 heads, d = 128) in 24.5 us, 5.9 TB/s.
+// copied bytes: 145 MB of prompt rows (8 heads, d = 128) in 26.6 us, 5.4 TB/s (24.7 replayed from a graph).
 struct AppendArgs {
     const char* k_new;
     const char* v_new;

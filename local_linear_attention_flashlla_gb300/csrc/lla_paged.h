@@ -87,7 +87,8 @@ inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, si
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// Division of x < 2^31 by a number known on the host: multiplication with the rounded-up reciprocal.
+// Division of x < 2^31 by a number known on the host: multiplication with the rounded-up reciprocal (T. Granlund and
+// P. Montgomery, Division by Invariant Integers using Multiplication, 1994).
 struct Divisor {
     unsigned mul, shift;
 };

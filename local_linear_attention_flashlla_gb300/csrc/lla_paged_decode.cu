@@ -9,7 +9,13 @@
 // hold O1 = sum p v and O2 = sum p (t - s0) v.  A 128-row tcgen05 tile would carry 8 to 32 useful
 // rows and wait for its row warps (2300 cycles per 128 keys at d = 64); here the tensor pipe is busy 17 % of the
 // time with eight rows.  64 sequences x 16 heads at 4096 keys: 317 us, 6.8 TB/s; 96 ragged sequences (100 to
-// 16,000 keys, eight query heads to a key head, 16-row pages): 230 us, 6.5 TB/s.
+// 16,000 keys, eight query heads to a key head, 16-row pages): 234 us, 6.4 TB/s (d = 64: 170 us, 6.3 TB/s, and 136).
+//
+// The weights are bf16 in the value product: with the output's rounding (1.7e-3) outputs are off from float64 by 2.4e-3 of
+// their norm.  As two bf16 halves each (a second value product) they leave the 1.7e-3 alone, for 321 us instead of 317 and 232.5
+// instead of 231.5 on these two, but 17.5 instead of 16.2 on one sequence of 32,768 keys, 42.5 instead of 33.9 on 20 rows at d = 64
+// and 77 instead of 61 on 32 rows at d = 128; the tcgen05 tiles, which are bound by their products, would have half as
+// many again.  So no kernel does, and one sequence's prompt and its later tokens round alike.
 //
 // A CTA has four computing warps and one that feeds 64-key blocks through a TMA ring (a box per page);
 // two CTAs to an SM keep 192 KB of the cache in flight.  The four warps are one, two or four sets of
@@ -27,9 +33,9 @@
 // 3 2^-22 of a product, where an fp32 product has 2^-24 and the sums of d and of the keys more than either; outputs are
 // as far from float64 as with fp32 products (2.8e-7 on the first case below).  The second product takes a step's keys
 // in an order in which the accumulators are already its operand.  16 sequences of 1 to 97 tokens over 200 to 1024 keys,
-// 4 heads, d = 32: 27 us (fp32 products on CUDA cores, which wait for shared memory, 35); 64 such sequences 78 (104),
-// d = 64 153 (192); decode of 32 x 16 heads at 4096 keys, d = 32 and 64: 117 and 215 us (174 and 254), 4.6 and 5 TB/s;
-// one row over 1000 keys, d = 64: 10.2 (7.5).  At d = 128 the ring leaves room for one CTA: 411 us where CUDA cores take
+// 4 heads, d = 32: 26.5 us (fp32 products on CUDA cores, which wait for shared memory, 35); 64 such sequences 76 (104),
+// d = 64 148 (196); decode of 32 x 16 heads at 4096 keys, d = 32 and 64: 109 and 202 us (151 and 231), 4.9 and 5.3 TB/s;
+// one row over 1000 keys, d = 64: 9.5 (7.5).  At d = 128 the ring leaves room for one CTA: 411 us where CUDA cores take
 // 369, so they keep it.
 #include <math.h>
 

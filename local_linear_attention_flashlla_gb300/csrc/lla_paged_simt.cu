@@ -34,8 +34,9 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, float4 x) {
 constexpr int kThreads = 256;
 
 // Few rows (a decode step): eight rows of a tile, a warp to a row, a lane two of the 64 keys of a block; warps without
-// a row only help to load.  fp32, 32 sequences x 16 heads at 4096 keys, d = 128: 532 us, 4.0 TB/s, bound by the
-// shared-memory reads of K beside the loads.
+// a row only help to load.  fp32, 32 sequences x 16 heads at 4096 keys, d = 128: 496, 506 or 520 us from process to process
+// (the same program and inputs), 4.1 to 4.3 TB/s, bound by the shared-memory reads of K beside the loads.  bf16, 64
+// sequences, d = 32 and 16: 274 and 428 us.
 template <int D>
 struct FewShape {
     static constexpr int R = 8, BN = 64, TX = 32;

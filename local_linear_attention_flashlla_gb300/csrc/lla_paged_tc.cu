@@ -7,9 +7,10 @@
 // that they came from.  The products are issued as
 //     S(j+1)  O2(j)  T(j+1)  O1(j+1)  S(j+2)  O2(j+1) ...
 // : the softmax of S(j+1) runs under O2(j) and T(j+1), the weighting of T(j+1) under O1(j+1) and S(j+2).
-// 512 tokens over 16,384 keys, 32 query / 4 key heads, d = 128: 177 us, 1.58 PFLOP/s (a block takes 2700 cycles,
-// its products 2048); prompts of 700 to 4096 tokens, 16 heads: 257 us, 1.17 PFLOP/s (a tile's first and last block
-// and its epilogue cost 4000 cycles).  At d = 64 the row warps bound it, 2300 cycles a block.
+// 512 tokens over 16,384 keys, 32 query / 4 key heads, d = 128: 189 us, 1.47 PFLOP/s (175 replayed from a graph on the same
+// inputs; a block takes 2700 cycles, its products 2048); prompts of 700 to 4096 tokens, 16 heads: 269 us, 1.11 PFLOP/s
+// (258 replayed; a tile's first and last block and its epilogue cost 4000 cycles).  At d = 64 the row warps bound it, 2300
+// cycles a block: 144 and 195 us replayed.
 //
 // Eight warps hold the rows, a thread half of a row's columns.  The exponents are taken against the
 // reference point of the blocks before while the maximum is taken beside them, and only the vote of a
