@@ -434,7 +434,8 @@ int lla_paged_append(int dtype, const void* k_new, const void* v_new, const long
  * max_new tokens, kv_lens beyond the table, a page id outside [0, num_pages)) are never followed: the
  * access is cut or reads zeros, and lla_sync_status reports LLA_ERR_INVALID_ARG.  What pages hold behind a
  * sequence's length never reaches a result; values at positions that are part of it should be finite (a
- * NaN or infinity at one position can reach rows of the same step that do not see it; a row that reads a NaN is NaN).
+ * NaN or infinity at one position can reach rows of the same step that do not see it; a NaN that a row reads
+ * reaches it).
  * workspace  NULL (stream-ordered pool) or lla_paged_parallax_workspace_size(...) bytes, 256-byte aligned,
  *            used by no other call at the same time; its contents need not be kept or cleared.
  * Results do not depend on the run: the order of every sum is fixed by the lengths.
