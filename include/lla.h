@@ -414,10 +414,11 @@ int lla_paged_append(int dtype, const void* k_new, const void* v_new, const long
  *            takes fp32), as a serving projection gives it.
  * path       LLA_PATH_AUTO: bf16 with d in {64, 128} takes LLA_PATH_TENSOR, all else LLA_PATH_FP32.  Logits, sums
  *            and states are fp32 in both.
- *            LLA_PATH_TENSOR trades precision for speed: the weights p and p (t - c0) are rounded to bf16 before the
- *            value products, 2^-8 of each term at most (outputs are off from float64 by 2.4e-3 of their norm, where
- *            the rounding of the output alone gives 1.7e-3).  bf16 tensors take fp32 weights and products on
- *            CUDA cores with LLA_PATH_FP32, by name.
+ *            LLA_PATH_TENSOR trades precision for speed where a sequence has more than 16 rows to a key head
+ *            (max_new * Hq/Hkv > 16): the weights p and p (t - c0) are rounded to bf16 before the value products, 2^-8 of
+ *            each term at most (outputs are off from float64 by 2.4e-3 of their norm, where the rounding of the output
+ *            alone gives 1.7e-3).  Up to 16 rows the weights are within 2^-16.  bf16 tensors take fp32 weights and
+ *            products on CUDA cores with LLA_PATH_FP32, by name.
  *            LLA_PATH_FP32 multiplies fp32 tensors with d in {32, 64} as three tensor-core products of their upper
  *            and lower 11 bits: each product within 3 2^-22 of itself for magnitudes from 2^-114 on (below, an
  *            operand is off by up to 2^-136) to 2^127 (from there on they count as infinite, and an infinity gives

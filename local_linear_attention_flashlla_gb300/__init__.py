@@ -738,7 +738,8 @@ def paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, 
     block_table [S, W], cu_q [S+1], kv_lens [S]: int32 CUDA tensors (paged_plan's); max_new: the most
     tokens of one sequence in this step (it chooses the kernel for the whole batch: pass what the step needs, not what
     it could need).  causal=False: every row sees all of its sequence's keys.  path: LLA_PATH_AUTO takes bf16 with d 64
-    or 128 to the tensor cores, where the weights are rounded to bf16; LLA_PATH_FP32 keeps them in fp32.
+    or 128 to the tensor cores, where the weights are rounded to bf16 from 17 rows to a key head on; LLA_PATH_FP32 keeps
+    them in fp32.
     Returns out [T, Hq, d]; rows behind the last sequence are left as they were.  Asynchronous on the
     current (or given) stream.  workspace: None (scratch kept per stream while the thread lives; under graph capture the
     graph's own), or a CUDA tensor of lla_paged_parallax_workspace_size(...) bytes that no other call uses at the

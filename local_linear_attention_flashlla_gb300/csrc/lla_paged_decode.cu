@@ -8,14 +8,15 @@
 // then, without any exchange, the two row halves of the second product's operand, whose accumulators
 // hold O1 = sum p v and O2 = sum p (t - s0) v.  A 128-row tcgen05 tile would carry 8 to 32 useful
 // rows and wait for its row warps (2300 cycles per 128 keys at d = 64); here the tensor pipe is busy 17 % of the
-// time with eight rows.  64 sequences x 16 heads at 4096 keys: 317 us, 6.8 TB/s; 96 ragged sequences (100 to
-// 16,000 keys, eight query heads to a key head, 16-row pages): 234 us, 6.4 TB/s (d = 64: 170 us, 6.3 TB/s, and 136).
+// time with eight rows.  64 sequences x 16 heads at 4096 keys: 321 us, 6.7 TB/s; 96 ragged sequences (100 to
+// 16,000 keys, eight query heads to a key head, 16-row pages): 234 us, 6.4 TB/s (d = 64: 172 us, 6.2 TB/s, and 137).
 //
-// The weights are bf16 in the value product: with the output's rounding (1.7e-3) outputs are off from float64 by 2.4e-3 of
-// their norm.  As two bf16 halves each (a second value product) they leave the 1.7e-3 alone, for 321 us instead of 317 and 232.5
-// instead of 231.5 on these two, but 17.5 instead of 16.2 on one sequence of 32,768 keys, 42.5 instead of 33.9 on 20 rows at d = 64
-// and 77 instead of 61 on 32 rows at d = 128; the tcgen05 tiles, which are bound by their products, would have half as
-// many again.  So no kernel does, and one sequence's prompt and its later tokens round alike.
+// Up to 16 rows the value product takes each weight as two bf16 halves, in two products: outputs are then off from float64 by
+// their own rounding alone (1.66e-3 of the norm), with bf16 weights by 2.4e-3.  That costs 320 us instead of 318 and 231 instead
+// of 230 on these two, 16.6 instead of 16.0 on one sequence of 32,768 keys and 33.5 instead of 31.6 on 16 rows at d = 64 (the
+// rest right after its half, in the same sums, 17.5 and 33.8).  With 17 to 32 rows the chain of products is what a warp waits
+// for, 42.5 instead of 33.9 on 20 rows at d = 64 and 77 instead of 61 on 32 rows at d = 128: there, as on tcgen05 tiles (which would
+// have six products to a block instead of four), the weights are bf16.
 //
 // A CTA has four computing warps and one that feeds 64-key blocks through a TMA ring (a box per page);
 // two CTAs to an SM keep 192 KB of the cache in flight.  The four warps are one, two or four sets of
@@ -23,7 +24,7 @@
 // parts are joined once per tile, in the space of its last block (slices of an own 8 KB cost two barriers
 // each, 1 us of the 10.5 that a tile of one block takes).  With two sets of rows in every warp instead the sums
 // do not fit the registers: 32 sequences of 300 to 6000 keys, four key heads, 16 rows, 82 us at d = 128 where this
-// takes 56, and 37 against 31 at d = 64.  20 rows, d = 64: 34 us here, 42 on tcgen05 tiles; a warp then waits for its
+// took 56 with bf16 weights, and 37 against 31 at d = 64.  20 rows, d = 64: 34 us here, 42 on tcgen05 tiles; a warp then waits for its
 // own chain of products and exponentials, and three or four CTAs to an SM (39 and 42 us) only add starts and parts.
 // 32 rows at d = 128: 60 us, 62 on tcgen05 tiles; 48 rows at d = 64 would be two tiles, 42 us there.
 //
@@ -62,6 +63,9 @@ struct DecShape {
     static constexpr int kTiles = (kWide >= 128 || sizeof(T) == 4) && RS == 4 ? 4 : kShare / 8;
     // (fp32 steps are split where they are used: in registers the compiler would keep the halves of all of them)
     static constexpr int kRegSteps = kWide == 128 && (RS > 1 || sizeof(T) == 4) ? 4 : sizeof(T) == 4 ? 0 : kWide / 16;
+    // the value product takes the weights as two bf16 halves (2^-16 of each is left out); with four sets in bf16 alone (half a
+    // step is 2^-8 of each): see above.  Its sums are fp32 in both.
+    static constexpr bool kHalves = sizeof(T) == 2 && RS < 4;
     static constexpr int kStages = kWide == 128 ? 3 : 6;
     static constexpr int kTile = kKeys * kWide * 2;        // bytes of a K (or V) block
     static constexpr int kOperand = kWarps * (kWide / 16 - kRegSteps) * 512;
@@ -107,6 +111,11 @@ __device__ __forceinline__ void mma1688(float (&c)[4], const uint32_t (&a)[4], u
     asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// What two values packed as bf16 lost by it, packed as bf16.
+__device__ __forceinline__ uint32_t rest_bf16(uint32_t packed, float lo, float hi) {
+    return pack_bf16(lo - __uint_as_float(packed << 16), hi - __uint_as_float(packed & 0xffff0000u));
 }
 
 // c + x += a b over eight fp32 columns, as three products of halves.  The tensor core cuts its sums off instead of
@@ -363,20 +372,32 @@ __global__ void __launch_bounds__(kThreads, 2)
                         if constexpr (sizeof(T) == 2) {
 #pragma unroll
                             for (int kk = 0; kk < NK; kk += 2) {
-                                // the value product takes the weights in bf16 (half a step is 2^-8 of each): its sums are fp32
-                                uint32_t pf[4];
+                                uint32_t pf[4], rest[4];
 #pragma unroll
                                 for (int x = 0; x < 2; ++x) {
                                     const float* y = s[kk + x];
+                                    const float z0 = y[0] * (y[2] - s0), z1 = y[1] * (y[3] - s0);
                                     pf[2 * x] = pack_bf16(y[0], y[1]);
-                                    pf[2 * x + 1] = pack_bf16(y[0] * (y[2] - s0), y[1] * (y[3] - s0));
+                                    pf[2 * x + 1] = pack_bf16(z0, z1);
+                                    rest[2 * x] = rest_bf16(pf[2 * x], y[0], y[1]);
+                                    rest[2 * x + 1] = rest_bf16(pf[2 * x + 1], z0, z1);
                                 }
+                                // four pairs of column tiles together: a product of the rests does not wait for the one
+                                // before it in the same sums
+                                constexpr int kPairs = 4;
 #pragma unroll
-                                for (int n = 0; n < NT / 2; ++n) {
-                                    uint32_t b[4];
-                                    ldsm4t(vt + piece_off<DB>(row0 + kk * 8 + (lane & 15), n * 2 + (lane >> 4)), b);
-                                    mma16816(o[n * 2], pf, b[0], b[1]);
-                                    mma16816(o[n * 2 + 1], pf, b[2], b[3]);
+                                for (int n0 = 0; n0 < NT / 2; n0 += kPairs) {
+                                    uint32_t b[kPairs][4];
+#pragma unroll
+                                    for (int n = 0; n < kPairs; ++n)
+                                        ldsm4t(vt + piece_off<DB>(row0 + kk * 8 + (lane & 15), (n0 + n) * 2 + (lane >> 4)), b[n]);
+#pragma unroll
+                                    for (int h = 0; h < (Sh::kHalves ? 2 : 1); ++h)
+#pragma unroll
+                                        for (int n = 0; n < kPairs; ++n) {
+                                            mma16816(o[(n0 + n) * 2], h ? rest : pf, b[n][0], b[n][1]);
+                                            mma16816(o[(n0 + n) * 2 + 1], h ? rest : pf, b[n][2], b[n][3]);
+                                        }
                                 }
                             }
                         } else {
