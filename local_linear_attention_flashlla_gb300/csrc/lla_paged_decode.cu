@@ -7,7 +7,7 @@
 // accumulator layout puts both of a (row, key) pair in one thread.  The weights p and p (t - s0) are
 // then, without any exchange, the two row halves of the second product's operand, whose accumulators
 // hold O1 = sum p v and O2 = sum p (t - s0) v.  A 128-row tcgen05 tile would carry 8 to 32 useful
-// rows and wait for its row warps (2300 cycles per 128 keys at d = 64); here the tensor pipe is busy 17 % of the
+// rows and wait for its row warps (2300 cycles per 128 keys at d = 64); here the tensor pipe is busy 26 % of the
 // time with eight rows.  64 sequences x 16 heads at 4096 keys: 321 us, 6.7 TB/s; 96 ragged sequences (100 to
 // 16,000 keys, eight query heads to a key head, 16-row pages): 234 us, 6.4 TB/s (d = 64: 172 us, 6.2 TB/s, and 137).
 //
