@@ -448,6 +448,20 @@ int lla_paged_parallax(int dtype, int path, const void* q, const void* probe, co
                        long long probe_stride, long long page_stride, float tau, int causal, void* workspace,
                        size_t workspace_bytes, void* stream);
 
+/*
+ * lla_paged_parallax_ex -- lla_paged_parallax that also writes, for every row and query head, the logarithm of the
+ * softmax's denominator: lse = log sum_j exp(tau q.k_j) over the keys the row sees (a row that sees no key: -inf), so
+ * that exp(tau q.k_j - lse) is the row's weight on key j.
+ *
+ * lse   NULL, or [T, Hq] fp32, 4-byte aligned; rows behind the last sequence are not written.  Within a few fp32
+ *       roundings of the weights' sum and of |lse|.  out has the bits it has without lse.
+ */
+int lla_paged_parallax_ex(int dtype, int path, const void* q, const void* probe, const void* k_cache, const void* v_cache,
+                          const int* block_table, const int* cu_q, const int* kv_lens, void* out, float* lse, int T, int S,
+                          int Hq, int Hkv, int d, int page_size, int num_pages, int table_width, int max_new,
+                          long long q_stride, long long probe_stride, long long page_stride, float tau, int causal,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
 /* Bytes of scratch lla_paged_parallax needs for these sizes (0 for invalid ones). */
 size_t lla_paged_parallax_workspace_size(int dtype, int path, int T, int S, int Hq, int Hkv, int d, int page_size,
                                          int table_width, int max_new);

@@ -23,7 +23,7 @@ __all__ = [
     "lla_profile_enable", "lla_profile_read", "lla_forward_noalloc", "lla_parallax_forward", "parallax_forward",
     "lla_decode", "lla_decode_ex", "lla_decode_max_n", "decode", "lla_backward", "lla_backward_workspace_size", "backward",
     "lla_backward_host", "lla_backward_host_buffer_size", "backward_host",
-    "lla_paged_plan", "lla_paged_append", "lla_paged_parallax", "lla_paged_parallax_workspace_size",
+    "lla_paged_plan", "lla_paged_append", "lla_paged_parallax", "lla_paged_parallax_ex", "lla_paged_parallax_workspace_size",
     "PagedPlan", "paged_plan", "paged_append", "paged_parallax",
     "LLA_OK", "LLA_ERR_INVALID_ARG", "LLA_ERR_UNSUPPORTED", "LLA_ERR_CUDA", "LLA_ERR_DEVICE_TIMEOUT",
     "LLA_DTYPE_BF16", "LLA_DTYPE_FP32", "LLA_PATH_AUTO", "LLA_PATH_TENSOR", "LLA_PATH_FP32",
@@ -78,6 +78,9 @@ _SIGNATURES = {
     "lla_paged_parallax": (_c_int, [_c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int,
                                     _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_ll, _c_ll, _c_ll, _c_float,
                                     _c_int, _vp, _c_size, _vp]),
+    "lla_paged_parallax_ex": (_c_int, [_c_int, _c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int,
+                                       _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_ll, _c_ll, _c_ll, _c_float,
+                                       _c_int, _vp, _c_size, _vp]),
     "lla_paged_parallax_workspace_size": (_c_size, [_c_int] * 10),
     "lla_profile_enable": (_c_int, [_c_int]),
     "lla_profile_read": (_c_int, [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_float)]),
@@ -500,6 +503,16 @@ def lla_paged_parallax(dtype, path, q_ptr, probe_ptr, k_cache_ptr, v_cache_ptr, 
                                              stream_ptr))
 
 
+def lla_paged_parallax_ex(dtype, path, q_ptr, probe_ptr, k_cache_ptr, v_cache_ptr, table_ptr, cu_ptr, kv_ptr, out_ptr, lse_ptr,
+                          T, S, Hq, Hkv, d, page_size, num_pages, table_width, max_new, q_stride, probe_stride, page_stride,
+                          tau, causal, ws_ptr, ws_bytes, stream_ptr):
+    """Raw paged Parallax entry point that also writes the rows' logsumexp; raises LLAError on failure."""
+    _check(load_library().lla_paged_parallax_ex(dtype, path, q_ptr, probe_ptr, k_cache_ptr, v_cache_ptr, table_ptr, cu_ptr,
+                                                kv_ptr, out_ptr, lse_ptr, T, S, Hq, Hkv, d, page_size, num_pages, table_width,
+                                                max_new, q_stride, probe_stride, page_stride, tau, causal, ws_ptr, ws_bytes,
+                                                stream_ptr))
+
+
 def lla_paged_parallax_workspace_size(dtype, path, T, S, Hq, Hkv, d, page_size, table_width, max_new):
     return load_library().lla_paged_parallax_workspace_size(dtype, path, T, S, Hq, Hkv, d, page_size, table_width, max_new)
 
@@ -608,7 +621,7 @@ def _bind():
             _BIND = False
         else:
             m.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (lib.lla_paged_plan, lib.lla_paged_append,
-                                                                      lib.lla_paged_parallax)),
+                                                                      lib.lla_paged_parallax_ex)),
                    torch.bfloat16, torch.float32, torch.int32, torch.int64)
             _BIND = m
     return _BIND
@@ -731,7 +744,7 @@ def paged_append(k_new, v_new, slots, k_cache, v_cache, *, stream=None):
 
 
 def paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, max_new, *, causal=True,
-                   path=LLA_PATH_AUTO, out=None, workspace=None, stream=None):
+                   path=LLA_PATH_AUTO, out=None, lse=None, workspace=None, stream=None):
     """Parallax-form attention of a step's token rows q, probe [T, Hq, d] over paged caches
     [num_pages, Hkv, page_size, d] (include/lla.h, lla_paged_parallax).
 
@@ -744,6 +757,8 @@ def paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, 
     current (or given) stream.  workspace: None (scratch kept per stream while the thread lives; under graph capture the
     graph's own), or a CUDA tensor of lla_paged_parallax_workspace_size(...) bytes that no other call uses at the
     same time.
+    lse: None, or an fp32 [T, Hq] tensor to be given the logsumexp of every row's scaled logits, which paged_weigh takes
+    (include/lla.h, lla_paged_parallax_ex).
     """
     import torch
     if stream is None and workspace is None and k_cache.is_cuda and _bind():
@@ -753,14 +768,14 @@ def paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, 
         if t is not None and not torch.cuda.is_current_stream_capturing():
             res = torch.empty(q.shape, dtype=q.dtype, device=q.device) if out is None else out
             if _BIND.parallax(index, q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, res, tau, max_new, causal, path,
-                              t.data_ptr(), t.numel(), stream_ptr) == LLA_OK:
+                              t.data_ptr(), t.numel(), stream_ptr, lse) == LLA_OK:
                 return res
     P, Hkv, Z, d, page_stride, dtype = _check_caches(k_cache, v_cache)
     dev = k_cache.device
     if stream is not None or dev.index != torch.cuda.current_device():
         with _on_stream(dev, stream):
             return paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, max_new, causal=causal,
-                                  path=path, out=out, workspace=workspace)
+                                  path=path, out=out, lse=lse, workspace=workspace)
     if q.dim() != 3:
         raise _bad(f"q must be [T, Hq, d], got {tuple(q.shape)}")
     if probe.shape != q.shape:
@@ -786,9 +801,10 @@ def paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, 
         raise _bad(f"workspace must be a contiguous tensor on {dev}")
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
-    status = load_library().lla_paged_parallax(
+    lse_ptr = None if lse is None else _ints("lse", lse, (T, Hq), torch.float32, dev)
+    status = load_library().lla_paged_parallax_ex(
         dtype, path, q.data_ptr(), probe.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), table_ptr, cu_ptr, kv_ptr,
-        out.data_ptr(), T, S, Hq, Hkv, d, Z, P, W, max_new, qs, rs, page_stride, float(tau), 1 if causal else 0,
+        out.data_ptr(), lse_ptr, T, S, Hq, Hkv, d, Z, P, W, max_new, qs, rs, page_stride, float(tau), 1 if causal else 0,
         workspace.data_ptr(), ws_bytes, stream_ptr)
     if status != LLA_OK:
         _check(status)

@@ -389,14 +389,24 @@ int lla_paged_parallax(int dtype, int path, const void* q, const void* probe, co
                        const int* block_table, const int* cu_q, const int* kv_lens, void* out, int T, int S, int Hq,
                        int Hkv, int d, int page_size, int num_pages, int table_width, int max_new, long long q_stride,
                        long long probe_stride, long long page_stride, float tau, int causal, void* workspace,
-                       size_t workspace_bytes, void* stream_) {
+                       size_t workspace_bytes, void* stream) {
+    return lla_paged_parallax_ex(dtype, path, q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, out, nullptr, T, S, Hq,
+                                 Hkv, d, page_size, num_pages, table_width, max_new, q_stride, probe_stride, page_stride, tau,
+                                 causal, workspace, workspace_bytes, stream);
+}
+
+int lla_paged_parallax_ex(int dtype, int path, const void* q, const void* probe, const void* k_cache, const void* v_cache,
+                          const int* block_table, const int* cu_q, const int* kv_lens, void* out, float* lse, int T, int S,
+                          int Hq, int Hkv, int d, int page_size, int num_pages, int table_width, int max_new,
+                          long long q_stride, long long probe_stride, long long page_stride, float tau, int causal,
+                          void* workspace, size_t workspace_bytes, void* stream_) {
     lla::set_error(LLA_OK, "");
     if (!q || !probe || !k_cache || !v_cache || !block_table || !cu_q || !kv_lens || !out)
         return failf(LLA_ERR_INVALID_ARG, "null tensor pointer");
     if (!aligned(q, 16) || !aligned(probe, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
         return failf(LLA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
-    if (!aligned(block_table, 4) || !aligned(cu_q, 4) || !aligned(kv_lens, 4))
-        return failf(LLA_ERR_INVALID_ARG, "int32 pointers must be 4-byte aligned");
+    if (!aligned(block_table, 4) || !aligned(cu_q, 4) || !aligned(kv_lens, 4) || !aligned(lse, 4))
+        return failf(LLA_ERR_INVALID_ARG, "int32 and lse pointers must be 4-byte aligned");
     int rpath = 0;
     const int st = lla::check_paged_sizes(dtype, path, T, S, Hq, Hkv, d, page_size, num_pages, table_width, max_new, &rpath);
     if (st != LLA_OK) return st;
@@ -411,7 +421,7 @@ int lla_paged_parallax(int dtype, int path, const void* q, const void* probe, co
 
     lla::PagedProblem p{};
     p.q = q; p.probe = probe; p.k = k_cache; p.v = v_cache; p.table = block_table; p.cu_q = cu_q; p.kv_lens = kv_lens;
-    p.out = out; p.T = T; p.S = S; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.d = d;
+    p.out = out; p.lse = lse; p.T = T; p.S = S; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.d = d;
     p.page_shift = lla::page_shift_of(page_size); p.num_pages = num_pages; p.width = table_width; p.max_new = max_new;
     p.q_stride = q_stride; p.r_stride = probe_stride; p.page_stride = page_stride;
     p.tau = tau; p.causal = causal != 0; p.dtype = dtype;

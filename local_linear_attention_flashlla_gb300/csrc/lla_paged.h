@@ -19,6 +19,7 @@ struct PagedProblem {
     const int* cu_q;          // [S + 1]
     const int* kv_lens;       // [S]
     void* out;                // [T, Hq, d] contiguous
+    float* lse;               // [T, Hq], or null
     int T, S, Hq, Hkv, G, d, page_shift, num_pages, width, max_new;
     long long q_stride, r_stride, page_stride;   // elements
     float tau;
@@ -114,6 +115,7 @@ struct Work {
     PartHeader* hdr;
     float* part;
     unsigned* err;
+    float* lse;                       // [T, Hq], or null
 };
 
 inline Work make_work(const PagedProblem& p, const PagedSplit& sp) {
@@ -130,6 +132,7 @@ inline Work make_work(const PagedProblem& p, const PagedSplit& sp) {
     w.hdr = static_cast<PartHeader*>(p.ws);
     w.part = reinterpret_cast<float*>(static_cast<char*>(p.ws) + (size_t)kPagedMaxCtas * sizeof(PartHeader));
     w.err = p.err;
+    w.lse = p.lse;
     return w;
 }
 
@@ -449,6 +452,12 @@ __device__ __forceinline__ float4* part_sums(const Work& w, int cta, int slot, i
 // Element of the sums (half 0: O1, 1: O2) of a row's column.
 __device__ __forceinline__ float* part_element(float4* sums, int rows, int d, int half, int row, int col) {
     return reinterpret_cast<float*>(sums + (size_t)(half * (d / 4) + col / 4) * rows + row) + col % 4;
+}
+
+// A row's logsumexp of its scaled logits, from its exponents' reference point (log2) and its weights' sum; a row that
+// sees no key has m = -inf and om = 0, and gets -inf.
+__device__ __forceinline__ void put_lse(const Work& w, long long token, int head, float m, float om) {
+    if (w.lse) w.lse[token * (w.Hkv * w.G) + head] = (m + log2f(om)) * 0.6931471805599453f;
 }
 
 // This CTA's header: written once by every CTA, with the tile that it starts and others finish (its

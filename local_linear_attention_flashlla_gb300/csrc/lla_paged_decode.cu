@@ -450,6 +450,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     T* out = static_cast<T*>(a.out) + ((long long)token * a.Hq + head) * D + c2;
 #pragma unroll
                     for (int n = 0; n < NT; ++n) put2(out + n * 8, c1 * o[n][0] - inv * o[n][2], c1 * o[n][1] - inv * o[n][3]);
+                    if (c2 == 0) put_lse(w, token, head, m, om);
                 } else {
                     float4* ps = part_sums(w, blockIdx.x, p.slot, D);
 #pragma unroll
@@ -510,6 +511,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const float inv = ow != 0.f ? 1.f / ow : 0.f, c1 = (1.f + aw * inv) * inv;
                     put4(static_cast<T*>(a.out) + ((long long)(p.q.token0 + tk) * a.Hq + p.h * w.G + er - tk * w.G) * D + c,
                          c1 * x1.x - inv * x2.x, c1 * x1.y - inv * x2.y, c1 * x1.z - inv * x2.z, c1 * x1.w - inv * x2.w);
+                    if (c == 0) put_lse(w, p.q.token0 + tk, p.h * w.G + er - tk * w.G, mm, ow);
                 } else {
                     float4* ps = part_sums(w, blockIdx.x, p.slot, D) + (size_t)(c / 4) * R + row;
                     ps[0] = x1;

@@ -259,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_few_kernel(SimtArgs a)
                     const int c = (tx + TX * (i / VW)) * VW + i % VW;
                     if (D % TX == 0 || c < D) put(o + c, (c1 * o1[i] - o2[i]) * inv);
                 }
+                if (tx == 0) put_lse(w, token, head, m, om);
             } else {
                 if (tx == 0) part_stats(w, blockIdx.x, p.slot, D)[row] = make_float4(m, om, A, s0);
                 float4* ps = part_sums(w, blockIdx.x, p.slot, D);
@@ -514,6 +515,7 @@ __global__ void __launch_bounds__(kManyThreads, ManyShape<D>::kCtas) paged_simt_
                 T* o = static_cast<T*>(a.out) + ((long long)(p.q.token0 + tk) * a.Hq + p.h * w.G + fr - tk * w.G) * D;
                 float4* ps = p.slot >= 0 ? part_sums(w, blockIdx.x, p.slot, D) : nullptr;
                 if (p.slot >= 0 && g8 == 0) part_stats(w, blockIdx.x, p.slot, D)[r] = make_float4(m[i], om[i], A[i], s0[i]);
+                if (p.slot < 0 && g8 == 0) put_lse(w, p.q.token0 + tk, p.h * w.G + fr - tk * w.G, m[i], om[i]);
                 const float inv = om[i] != 0.f ? 1.f / om[i] : 0.f, c1 = 1.f + A[i] * inv;
 #pragma unroll
                 for (int n = 0; n < CPT / 2; ++n) {
@@ -603,6 +605,10 @@ __global__ void __launch_bounds__(256, 5) paged_merge_kernel(Work w, T* __restri
         A += __shfl_xor_sync(0xffffffffu, A, o);
     }
     const float inv = om != 0.f ? 1.f / om : 0.f, c1 = 1.f + A * inv;   // om 0: no key in any part; NaN stays NaN
+    if (live && ln == 0 && c0 == 0) {
+        const int fr = h.row0 + row, tk = over_g(w, fr);
+        put_lse(w, h.token0 + tk, h.head * w.G + fr - tk * w.G, m, om);
+    }
 
     const int r = tid % kMergeRows, c4 = c0 + tid / kMergeRows % Sh::kC, lane = tid / kItems;
     const bool mine = row0 + r < h.rows;

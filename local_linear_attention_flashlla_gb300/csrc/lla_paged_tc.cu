@@ -647,8 +647,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (r < p.rows && half == 0 && p.slot >= 0)
-                part_stats(w, blockIdx.x, p.slot, D)[r] = make_float4(m, om, A, s0);
+            if (r < p.rows && half == 0) {
+                if (p.slot >= 0) part_stats(w, blockIdx.x, p.slot, D)[r] = make_float4(m, om, A, s0);
+                else put_lse(w, p.q.token0 + tk, p.h * w.G + p.row0 + r - tk * w.G, m, om);
+            }
             tc_fence_before();                 // O is read: the next tile's products may write it (after p1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&b.free[k % kRing]);

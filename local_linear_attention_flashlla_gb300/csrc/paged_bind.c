@@ -14,7 +14,7 @@ typedef int (*plan_fn)(const void*, const void*, int, int, void*, int, const voi
 typedef int (*append_fn)(int, const void*, const void*, const void*, void*, void*, int, int, int, int, int, long long,
                          long long, long long, void*);
 typedef int (*attend_fn)(int, int, const void*, const void*, const void*, const void*, const void*, const void*,
-                         const void*, void*, int, int, int, int, int, int, int, int, int, long long, long long, long long,
+                         const void*, void*, void*, int, int, int, int, int, int, int, int, int, long long, long long, long long,
                          float, int, void*, size_t, void*);
 
 static plan_fn f_plan;
@@ -166,13 +166,13 @@ static PyObject* append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 }
 
 /* parallax(device, q, probe, k_cache, v_cache, table, cu_q, kv_lens, out, tau, max_new, causal, path, workspace,
- * workspace bytes, stream) */
+ * workspace bytes, stream[, lse or None]) */
 static PyObject* parallax(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-    Tensor q, r, kc, vc, table, cu, kv, out;
+    Tensor q, r, kc, vc, table, cu, kv, out, lse;
     long long qs, rs, os, ps;
     int status = -1;
     (void)self;
-    if (n != 16) return PyLong_FromLong(-1);
+    if (n != 16 && n != 17) return PyLong_FromLong(-1);
     const long device = PyLong_AsLong(a[0]);
     const double tau = PyFloat_AsDouble(a[9]);
     const long long max_new = PyLong_AsLongLong(a[10]);
@@ -190,12 +190,17 @@ static PyObject* parallax(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         out.shape[0] != q.shape[0] || os != q.shape[1] * q.shape[2] || !read_tensor(a[7], &kv) || kv.dim != 1)
         return PyLong_FromLong(-1);
     const long long S = kv.shape[0];
+    lse.ptr = 0;
+    if (n == 17 && a[16] != Py_None &&
+        (!read_tensor(a[16], &lse) || lse.dtype != t_fp32 || lse.device != device || lse.dim != 2 || lse.shape[0] != q.shape[0] ||
+         lse.shape[1] != q.shape[1] || lse.stride[1] != 1 || lse.stride[0] != q.shape[1]))
+        return PyLong_FromLong(-1);
     if (vector(a[7], t_i32, device, S, &kv) && vector(a[6], t_i32, device, S + 1, &cu) && matrix(a[5], t_i32, device, S, &table) &&
         fits(q.shape[0]) && fits(q.shape[1]) && fits(S) && fits(table.shape[1]) && fits(kc.shape[0]) && fits(kc.shape[1]) &&
         fits(kc.shape[2]) && fits(max_new)) {
         Py_BEGIN_ALLOW_THREADS
         status = f_attend(kc.dtype == t_bf16 ? 0 : 1, (int)path, P(q.ptr), P(r.ptr), P(kc.ptr), P(vc.ptr), P(table.ptr),
-                          P(cu.ptr), P(kv.ptr), P(out.ptr), (int)q.shape[0], (int)S, (int)q.shape[1], (int)kc.shape[1],
+                          P(cu.ptr), P(kv.ptr), P(out.ptr), P(lse.ptr), (int)q.shape[0], (int)S, (int)q.shape[1], (int)kc.shape[1],
                           (int)kc.shape[3], (int)kc.shape[2], (int)kc.shape[0], (int)table.shape[1], (int)max_new, qs, rs, ps,
                           (float)tau, causal, P(ws), ws_bytes, P(stream));
         Py_END_ALLOW_THREADS
