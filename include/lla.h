@@ -340,6 +340,55 @@ int lla_backward_host(int dtype, int path, const void* q, const void* k, const v
 size_t lla_backward_host_buffer_size(int dtype, int path, int B, int H, int n, int d, int chunk_slices);
 
 /*
+ * lla_rotary -- rotary positions of the heads' rows of up to LLA_ROTARY_MOST tensors (queries, keys, probes), with RMS
+ * normalisation and a gain before them (the Parallax page's probe is RMSNorm(W_R x) with rotary positions):
+ *
+ *     u = gain x / sqrt(mean(x^2) + eps)            (eps >= 0; with eps < 0: u = x)
+ *     y = m Rot(p) u on the first rot columns, u on the others,
+ *
+ * Rot(p) turning pair i of columns by p turns[i] 2^-64 of a full turn: columns (i, i + rot/2), or with interleaved != 0
+ * (2 i, 2 i + 1), become (a cos - b sin, b cos + a sin).
+ *
+ * dtype      LLA_DTYPE_BF16 or LLA_DTYPE_FP32: x and out.  All arithmetic is fp32, with one rounding to out's type; angles
+ *            are fixed-point products modulo a turn, as exact at position 2^31 - 1 as at 1.
+ * rows       [count], a host array: tensors [B, heads, n, d], row (b, h, t) b stride[0] + h stride[1] + t stride[2]
+ *            elements from the pointer.  Strides are multiples of 16 bytes, a row's d elements are contiguous; out may be
+ *            x (strides alike), other overlaps of inputs and outputs may not be.  gain: NULL or [d] fp32.
+ * positions  [n] (position_stride 0) or [B, n] (position_stride n) int32; negative ones turn back.
+ * turns      [rot / 2]: a frequency f in radians per position is f / (2 pi) 2^64, modulo 2^64.
+ * rot        even, in [2, d].  magnitude (m): finite, not 0 (1 but for tables scaled for long contexts).
+ * cu_q, shift  NULL, or (B = 1) [S + 1] and [S] int32: shift[s] is added to the positions cu_q[s] <= t < cu_q[s + 1], as
+ *            slot positions of a sequence that tokens were evicted from need it (lla_paged_trim's dropped).
+ * d in {16, 32, 64, 128}; B * n <= 2^30; pointers 16-byte aligned.  Asynchronous on `stream`, one launch, no scratch.
+ *
+ * lla_rotary_backward -- its gradient: with L = sum dy.y, out = dL/dx in dtype (out may be x or, of one dtype, dy) and
+ * dgain = dL/dgain (NULL, or [d] fp32, written), the sum over all rows of the tensor.  dy: dy_dtype is dtype or fp32 (as
+ * lla_backward's dq and dk are).  x is not read with eps < 0.  workspace: NULL (stream-ordered pool) or
+ * lla_rotary_backward_workspace_size(...) bytes, 256-byte aligned, used by no other call at the same time; needed for
+ * dgain only.  Results do not depend on the run.  One launch, and a small one where a gain's gradient is asked for.
+ */
+#define LLA_ROTARY_MOST 4
+typedef struct {
+    const void* x;
+    const void* dy;              /* backward only */
+    void* out;                   /* forward: y; backward: dx */
+    const float* gain;
+    float* dgain;                /* backward only */
+    long long x_stride[3], dy_stride[3], out_stride[3];
+    int heads;
+} lla_rotary_rows;
+int lla_rotary(int dtype, const lla_rotary_rows* rows, int count, int B, int n, int d, const int* positions,
+               long long position_stride, const long long* turns, int rot, int interleaved, float magnitude, float eps,
+               const int* cu_q, const int* shift, int S, void* stream);
+int lla_rotary_backward(int dtype, int dy_dtype, const lla_rotary_rows* rows, int count, int B, int n, int d,
+                        const int* positions, long long position_stride, const long long* turns, int rot, int interleaved,
+                        float magnitude, float eps, const int* cu_q, const int* shift, int S, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* Bytes of scratch lla_rotary_backward needs for these sizes (0 for invalid ones). */
+size_t lla_rotary_backward_workspace_size(int count, int d);
+
+/*
  * Paged caches: the keys and values of many sequences of different lengths in pages of page_size
  * positions, [num_pages, Hkv, page_size, d] in dtype, page_size a power of two in 8 .. 256.  Position
  * x of sequence s lies in page block_table[s][x / page_size] at row x % page_size; its slot is

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 import threading
 from collections import namedtuple
@@ -24,6 +25,8 @@ __all__ = [
     "lla_decode", "lla_decode_ex", "lla_decode_max_n", "decode", "lla_backward", "lla_backward_workspace_size", "backward",
     "lla_backward_host", "lla_backward_host_buffer_size", "backward_host",
     "lla_paged_plan", "lla_paged_append", "lla_paged_parallax", "lla_paged_parallax_ex", "lla_paged_parallax_workspace_size",
+    "lla_rotary", "lla_rotary_backward", "lla_rotary_backward_workspace_size", "RotaryTable", "rotary_table", "rotary",
+    "rotary_backward",
     "PagedPlan", "paged_plan", "paged_append", "paged_parallax",
     "LLA_OK", "LLA_ERR_INVALID_ARG", "LLA_ERR_UNSUPPORTED", "LLA_ERR_CUDA", "LLA_ERR_DEVICE_TIMEOUT",
     "LLA_DTYPE_BF16", "LLA_DTYPE_FP32", "LLA_PATH_AUTO", "LLA_PATH_TENSOR", "LLA_PATH_FP32",
@@ -41,6 +44,14 @@ _LIB = None
 
 _c_int, _c_float, _c_size, _vp = ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p
 _c_ll = ctypes.c_longlong
+
+LLA_ROTARY_MOST = 4
+
+
+class lla_rotary_rows(ctypes.Structure):
+    _fields_ = [("x", _vp), ("dy", _vp), ("out", _vp), ("gain", _vp), ("dgain", _vp), ("x_stride", _c_ll * 3),
+                ("dy_stride", _c_ll * 3), ("out_stride", _c_ll * 3), ("heads", _c_int)]
+
 
 # name -> (restype, argtypes); mirrors include/lla.h
 _SIGNATURES = {
@@ -82,6 +93,11 @@ _SIGNATURES = {
                                        _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_ll, _c_ll, _c_ll, _c_float,
                                        _c_int, _vp, _c_size, _vp]),
     "lla_paged_parallax_workspace_size": (_c_size, [_c_int] * 10),
+    "lla_rotary": (_c_int, [_c_int, ctypes.POINTER(lla_rotary_rows), _c_int, _c_int, _c_int, _c_int, _vp, _c_ll, _vp, _c_int,
+                            _c_int, _c_float, _c_float, _vp, _vp, _c_int, _vp]),
+    "lla_rotary_backward": (_c_int, [_c_int, _c_int, ctypes.POINTER(lla_rotary_rows), _c_int, _c_int, _c_int, _c_int, _vp, _c_ll,
+                                     _vp, _c_int, _c_int, _c_float, _c_float, _vp, _vp, _c_int, _vp, _c_size, _vp]),
+    "lla_rotary_backward_workspace_size": (_c_size, [_c_int, _c_int]),
     "lla_profile_enable": (_c_int, [_c_int]),
     "lla_profile_read": (_c_int, [ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_float)]),
     "lla_version": (_c_int, []),
@@ -809,3 +825,236 @@ def paged_parallax(q, probe, k_cache, v_cache, block_table, cu_q, kv_lens, tau, 
     if status != LLA_OK:
         _check(status)
     return out
+
+
+# ------------------------------------------------------------------------------------------------ rotary positions
+RotaryTable = namedtuple("RotaryTable", "turns dim magnitude")
+
+
+def rotary_table(dim, base=10000.0, *, scaling=None, factor=1.0, original=4096, low=1.0, high=32.0, magnitude=None, device=None):
+    """Frequencies f_i = base^(-2 i / dim) of rotary positions over the first `dim` columns of a head, as the GPU takes
+    them: turns per position in 64-bit fixed point (include/lla.h, lla_rotary).  Made once, kept by the caller.
+
+    scaling, for contexts longer than those trained on, by `factor`: None; "linear", every frequency divided by it;
+    "ntk", the base raised by factor^(dim / (dim - 2)), which leaves the fastest pair and divides the slowest by the
+    factor; "parts" (NTK-by-parts, B. Peng et al., YaRN, 2023), frequencies of fewer than `low` turns over the `original`
+    length divided, those of more than `high` kept, a linear ramp between, and a magnitude of 0.1 ln(factor) + 1.
+    magnitude: what rotated columns are multiplied by, unless the scaling's own (1, but for "parts").
+    """
+    import decimal
+
+    import torch
+    dim, base, factor = int(dim), float(base), float(factor)
+    if dim < 2 or dim % 2:
+        raise _bad(f"dim must be even and >= 2 (got {dim})")
+    if not 0.0 < base < math.inf or not 0.0 < factor < math.inf:
+        raise _bad("base and factor must be positive and finite")
+    if scaling not in (None, "linear", "ntk", "parts"):
+        raise _bad(f"scaling must be None, 'linear', 'ntk' or 'parts' (got {scaling!r})")
+    if scaling == "parts" and not (0 < original and low < high):
+        raise _bad("'parts' needs original > 0 and low < high")
+    turns = []
+    with decimal.localcontext() as ctx:            # a float64 frequency would be off by 2^-22 of a radian at position 2^31
+        ctx.prec = 50
+        D = decimal.Decimal
+        b, k, two_pi = D(base), D(factor), 2 * D("3.14159265358979323846264338327950288419716939937510582")
+        if scaling == "ntk":
+            b *= k ** (D(dim) / max(dim - 2, 1))
+        for i in range(0, dim, 2):
+            f = b ** (D(-i) / dim)
+            if scaling == "linear":
+                f /= k
+            elif scaling == "parts":
+                keep = min(max((D(original) * f / two_pi - D(low)) / (D(high) - D(low)), D(0)), D(1))
+                f = f * keep + f / k * (1 - keep)
+            t = int((f / two_pi * 2 ** 64).to_integral_value()) % 2 ** 64
+            turns.append(t - 2 ** 64 if t >= 2 ** 63 else t)
+    if magnitude is None:
+        magnitude = 0.1 * math.log(factor) + 1.0 if scaling == "parts" else 1.0
+    return RotaryTable(torch.tensor(turns, dtype=torch.int64, device="cuda" if device is None else device), dim, float(magnitude))
+
+
+def lla_rotary(dtype, rows, count, B, n, d, positions_ptr, position_stride, turns_ptr, rot, interleaved, magnitude, eps, cu_ptr,
+               shift_ptr, S, stream_ptr):
+    """Raw rotary entry point; rows: a ctypes array of lla_rotary_rows.  Raises LLAError on failure."""
+    _check(load_library().lla_rotary(dtype, rows, count, B, n, d, positions_ptr, position_stride, turns_ptr, rot, interleaved,
+                                     magnitude, eps, cu_ptr, shift_ptr, S, stream_ptr))
+
+
+def lla_rotary_backward(dtype, dy_dtype, rows, count, B, n, d, positions_ptr, position_stride, turns_ptr, rot, interleaved,
+                        magnitude, eps, cu_ptr, shift_ptr, S, ws_ptr, ws_bytes, stream_ptr):
+    """Raw entry point of the rotary gradient; raises LLAError on failure."""
+    _check(load_library().lla_rotary_backward(dtype, dy_dtype, rows, count, B, n, d, positions_ptr, position_stride, turns_ptr,
+                                              rot, interleaved, magnitude, eps, cu_ptr, shift_ptr, S, ws_ptr, ws_bytes,
+                                              stream_ptr))
+
+
+def lla_rotary_backward_workspace_size(count, d):
+    return load_library().lla_rotary_backward_workspace_size(count, d)
+
+
+def _listed(t, count=None, name=None):
+    """A tensor, None or a sequence of them as a list (of `count`)."""
+    if count is None:
+        return list(t) if isinstance(t, (tuple, list)) else [t]
+    if t is None:
+        return [None] * count
+    got = list(t) if isinstance(t, (tuple, list)) else [t]
+    if len(got) != count:
+        raise _bad(f"{name} must be one for each of the {count} tensors")
+    return got
+
+
+def _head_rows(t, name, dtype, like, copy):
+    """(tensor, strides of batch, head and position) of [T, heads, d] or [B, heads, n, d] rows as the kernels take them:
+    contiguous rows, 16-byte strides; anything else is copied, or refused where it is written."""
+    if t.shape != like.shape or t.dtype is not dtype or t.device != like.device:
+        raise _bad(f"{name} must be {tuple(like.shape)} {dtype} on {like.device}, got {tuple(t.shape)} {t.dtype} on {t.device}")
+    ve = 16 // t.element_size()
+    s = t.stride()
+    if s[-1] != 1 or t.data_ptr() % 16 or any(x % ve for x in s[:-1]):
+        if not copy:
+            raise _bad(f"{name} must have contiguous rows and 16-byte strides")
+        import torch
+        t = t.contiguous() if t.data_ptr() % 16 == 0 and not t.is_contiguous() else t.clone(memory_format=torch.contiguous_format)
+        s = t.stride()
+    return t, ((0, s[1], s[0]) if t.dim() == 3 else s[:3])
+
+
+def _rotary_call(x, dy, positions, table, gain, eps, cu_q, shift, out, backward):
+    """Checks and marshalling of rotary and rotary_backward; returns what the C calls take."""
+    import torch
+    like = _listed(x if x is not None else dy)
+    count, first = len(like), like[0]
+    if not 1 <= count <= LLA_ROTARY_MOST:
+        raise _bad(f"1 to {LLA_ROTARY_MOST} tensors expected, got {count}")
+    if not isinstance(table, RotaryTable):
+        raise _bad("table must be a RotaryTable (rotary_table)")
+    xs, dys = _listed(x, count, "x"), _listed(dy, count, "dy") if backward else [None] * count
+    gains, outs = _listed(gain, count, "gain"), _listed(out, count, "out")
+    dev = first.device
+    if not first.is_cuda:
+        raise _bad("rotary takes CUDA tensors (there is no CPU path)")
+    if first.dim() not in (3, 4):
+        raise _bad(f"rows must be [T, heads, d] or [B, heads, n, d], got {tuple(first.shape)}")
+    dt = first.dtype
+    if dt is torch.bfloat16:
+        dtype = LLA_DTYPE_BF16
+    elif dt is torch.float32:
+        dtype = LLA_DTYPE_FP32
+    else:
+        raise _bad("rows must be bf16 or fp32")
+    rows3 = first.dim() == 3
+    B, n, d = (1, first.shape[0], first.shape[2]) if rows3 else (first.shape[0], first.shape[2], first.shape[3])
+    if positions.shape == (n,):
+        position_stride = 0
+    elif not rows3 and positions.shape == (B, n):
+        position_stride = n
+    else:
+        raise _bad(f"positions must be [{n}]" + ("" if rows3 else f" or [{B}, {n}]") + f", got {tuple(positions.shape)}")
+    i32, f32 = torch.int32, torch.float32
+    pos_ptr = _ints("positions", positions, tuple(positions.shape), i32, dev)
+    turns_ptr = _ints("table.turns", table.turns, (table.dim // 2,), torch.int64, dev)
+    if (cu_q is None) != (shift is None):
+        raise _bad("cu_q and shift go together")
+    cu_ptr = shift_ptr = None
+    S = 0
+    if shift is not None:
+        if not rows3:
+            raise _bad("shift goes with [T, heads, d] rows")
+        S = shift.numel()
+        cu_ptr, shift_ptr = _ints("cu_q", cu_q, (S + 1,), i32, dev), _ints("shift", shift, (S,), i32, dev)
+    rows, keep, dy_dt = (lla_rotary_rows * count)(), [], None
+    for i in range(count):
+        r, t = rows[i], like[i]
+        if t.dim() != first.dim() or t.dtype is not dt or t.device != dev or t.shape[-1] != d or \
+                (t.shape[0] != n if rows3 else t.shape[0] != B or t.shape[2] != n):
+            raise _bad(f"the tensors must share dtype, device and all sizes but the heads, got {tuple(t.shape)} {t.dtype} on {t.device}")
+        r.heads = t.shape[1]
+        if xs[i] is not None:
+            xi, s = _head_rows(xs[i], "x", dt, t, True)
+            keep.append(xi)
+            r.x, r.x_stride[:] = xi.data_ptr(), s
+        if backward:
+            g = dys[i]
+            if dy_dt is None:
+                dy_dt = g.dtype
+                if dy_dt is not dt and dy_dt is not f32:
+                    raise _bad(f"dy must be {dt} or fp32")
+            g, s = _head_rows(g, "dy", dy_dt, t, True)
+            keep.append(g)
+            r.dy, r.dy_stride[:] = g.data_ptr(), s
+        if outs[i] is None:
+            outs[i] = torch.empty(t.shape, dtype=dt, device=dev)
+        o, s = _head_rows(outs[i], "dx" if backward else "out", dt, t, False)
+        r.out, r.out_stride[:] = o.data_ptr(), s
+        if gains[i] is not None:
+            if eps is None:
+                raise _bad("a gain goes with the normalisation: give eps")
+            r.gain = _ints("gain", gains[i], (d,), f32, dev)
+    eps = -1.0 if eps is None else float(eps)
+    if eps < 0.0 and any(g is not None for g in gains):
+        raise _bad("eps must be >= 0")
+    return (dtype, LLA_DTYPE_BF16 if dy_dt is torch.bfloat16 else LLA_DTYPE_FP32, rows, count, B, n, d, pos_ptr, position_stride,
+            turns_ptr, table.dim, float(table.magnitude), eps, cu_ptr, shift_ptr, S, outs, gains, keep)
+
+
+def rotary(x, positions, table, *, gain=None, eps=None, interleaved=False, cu_q=None, shift=None, out=None, stream=None):
+    """Rotary positions of the heads' rows of x, with RMS normalisation and a gain before them (include/lla.h, lla_rotary).
+
+    x: [T, heads, d] token rows or [B, heads, n, d], bf16 or fp32, any 16-byte strides (slices of a fused projection), or
+    up to four such tensors of different heads (queries, keys, probes) that share one launch.  positions: int32 [T] (a
+    plan's) or [n] or [B, n].  table: rotary_table(...).  eps: None, or the rows are divided by sqrt(mean(x^2) + eps) and
+    multiplied by gain (fp32 [d], one per tensor, or None) first.  interleaved: columns 2 i and 2 i + 1 turn together, else
+    i and i + dim / 2.  cu_q [S + 1], shift [S]: int32, shift[s] is added to the positions of sequence s (tokens
+    that eviction dropped: paged_trim).  out: where to write (x itself serves).
+    Returns the rotated tensor, or a tuple where x is a sequence.  Asynchronous on the current (or given) stream.
+    """
+    import torch
+    first = _listed(x)[0]
+    if first.is_cuda and (stream is not None or first.device.index != torch.cuda.current_device()):
+        with _on_stream(first.device, stream):
+            return rotary(x, positions, table, gain=gain, eps=eps, interleaved=interleaved, cu_q=cu_q, shift=shift, out=out)
+    dtype, _, rows, count, B, n, d, pos, ps, turns, rot, m, e, cu, sh, S, outs, _, _ = \
+        _rotary_call(x, None, positions, table, gain, eps, cu_q, shift, out, False)
+    lla_rotary(dtype, rows, count, B, n, d, pos, ps, turns, rot, 1 if interleaved else 0, m, e, cu, sh, S,
+               torch._C._cuda_getCurrentRawStream(first.device.index))
+    return tuple(outs) if isinstance(x, (tuple, list)) else outs[0]
+
+
+def rotary_backward(dy, x, positions, table, *, gain=None, eps=None, interleaved=False, cu_q=None, shift=None, dx=None,
+                    workspace=None, stream=None):
+    """Gradients of rotary: (dx, dgain) for L = sum(dy * rotary(x)), with rotary's arguments (include/lla.h,
+    lla_rotary_backward).  dy: x's dtype or fp32 (as backward()'s dq and dk are); dx has x's dtype; dgain is fp32 [d], or
+    None where no gain was given; tuples where x is a sequence.  x may be None where eps is (then it is not read, and dx
+    has dy's dtype).  workspace: None or a CUDA tensor of lla_rotary_backward_workspace_size(...) bytes that no other call uses
+    at the same time.  Results have the same bits every run.  Asynchronous on the current (or given) stream.
+    """
+    import torch
+    if x is None and eps is not None:
+        raise _bad("x is needed where the rows were normalised (eps)")
+    first = _listed(dy)[0]
+    if first.is_cuda and (stream is not None or first.device.index != torch.cuda.current_device()):
+        with _on_stream(first.device, stream):
+            return rotary_backward(dy, x, positions, table, gain=gain, eps=eps, interleaved=interleaved, cu_q=cu_q, shift=shift,
+                                   dx=dx, workspace=workspace)
+    dtype, dy_dtype, rows, count, B, n, d, pos, ps, turns, rot, m, e, cu, sh, S, outs, gains, _ = \
+        _rotary_call(x, dy, positions, table, gain, eps, cu_q, shift, dx, True)
+    dgains = [None if g is None else torch.empty_like(g) for g in gains]
+    for r, g in zip(rows, dgains):
+        if g is not None:
+            r.dgain = g.data_ptr()
+    stream_ptr = torch._C._cuda_getCurrentRawStream(first.device.index)
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        if workspace.device != first.device or not workspace.is_contiguous():
+            raise _bad(f"workspace must be a contiguous tensor on {first.device}")
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif any(g is not None for g in dgains):
+        workspace = _scratch(first.device, stream_ptr, lla_rotary_backward_workspace_size(count, d))
+        ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
+    lla_rotary_backward(dtype, dy_dtype, rows, count, B, n, d, pos, ps, turns, rot, 1 if interleaved else 0, m, e, cu, sh, S,
+                        ws_ptr, ws_bytes, stream_ptr)
+    many = isinstance(dy, (tuple, list))
+    dgain = None if all(g is None for g in dgains) else tuple(dgains) if many else dgains[0]
+    return (tuple(outs) if many else outs[0]), dgain
