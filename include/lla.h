@@ -515,6 +515,81 @@ int lla_paged_parallax_ex(int dtype, int path, const void* q, const void* probe,
 size_t lla_paged_parallax_workspace_size(int dtype, int path, int T, int S, int Hq, int Hkv, int d, int page_size,
                                          int table_width, int max_new);
 
+/*
+ * Bounded caches: positions of small attention weight leave a paged cache.  Beside its caches a layer has scores
+ * [num_pages, Hkv, page_size] fp32 and positions [num_pages, Hkv, page_size] int32 (both contiguous), laid out and indexed
+ * as the pages are: the attention each cached position has received, and the position in its sequence that a slot holds.
+ * A step is lla_paged_plan, then per layer lla_rotary, lla_paged_append, lla_paged_parallax_ex (with lse) and
+ * lla_paged_weigh.  Where caches are to shrink, after the step: lla_paged_evict for every layer, then lla_paged_trim once.
+ * Keys are cached rotated, so a key keeps its position when it moves to another slot; the next step's token rows get theirs
+ * from lla_rotary with shift = dropped.  As in the other paged calls every length is read on the device, and no
+ * call synchronises.
+ *
+ * lla_paged_weigh -- for every sequence s that brings tokens (n = cu_q[s+1]-cu_q[s] >= 1 rows, L = kv_lens[s]), every key
+ * head h and slot j < L, over the rows of the last `last` tokens (0: of all) and the query heads of h that see the key:
+ *
+ *     w_j = sum exp(tau q.k_j - lse),
+ *     scores_out_j = w_j                        for j >= L - n in causal attention (the step's own tokens),
+ *                    decay scores_j + w_j       for the others (decay 0: scores is not read).
+ *
+ * dtype      of q and the cache.
+ * q          [T, Hq, d], token stride q_stride, as in lla_paged_parallax.
+ * lse        [T, Hq] fp32: what lla_paged_parallax_ex wrote for these rows.  A row of -inf adds nothing.
+ * k_cache    [num_pages, Hkv, page_size, d], pages page_stride elements apart, as there.
+ * scores, scores_out  may be one array.  Only slots j < L of sequences that bring tokens are written.
+ * positions  NULL, or written at the step's own tokens in causal attention: j + dropped[s] (dropped NULL: j).
+ * causal     as in lla_paged_parallax; with 0 the keys hold none of the step's tokens.
+ * last >= 0, decay >= 0 and finite; all other arguments, limits and errors are those of lla_paged_parallax (no path: bf16
+ * products are exact, fp32 ones as its LLA_PATH_FP32 says for d in {32, 64}, sums and weights are fp32).
+ * workspace  NULL (stream-ordered pool) or lla_paged_weigh_workspace_size(...) bytes, 256-byte aligned, used by no other
+ *            call at the same time.  Results do not depend on the run.
+ */
+int lla_paged_weigh(int dtype, const void* q, const float* lse, const void* k_cache, const float* scores, float* scores_out,
+                    int* positions, const int* dropped, const int* block_table, const int* cu_q, const int* kv_lens, int T, int S,
+                    int Hq, int Hkv, int d, int page_size, int num_pages, int table_width, int max_new, long long q_stride,
+                    long long page_stride, float tau, float decay, int last, int causal, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/* Bytes of scratch lla_paged_weigh needs for these sizes (0 for invalid ones). */
+size_t lla_paged_weigh_workspace_size(int dtype, int T, int S, int Hq, int Hkv, int d, int page_size, int table_width, int max_new);
+
+/*
+ * lla_paged_evict -- keeps, of every sequence (L = kv_lens[s]) and key head, the b = min(L, keep[s]) positions that rank
+ * highest: positions below `sinks` and the last `recent` ones (positions >= L + dropped[s] - recent) first, then the
+ * others by falling score; among equals the lower slot first.  NaN ranks as -inf.  Kept rows of slots below b stay; those
+ * of slots from b on go, in ascending order, to the slots below b that are not kept, in ascending order.  So the kept
+ * positions are in slots 0 .. b-1, in no particular order; attention does not depend on it.  Slots from b on are left as they
+ * were.  Lengths and block table are not changed (they are shared by the layers): lla_paged_trim does that.
+ *
+ * scores     [num_pages, Hkv, page_size] fp32, read.  scores_out: given the kept positions' scores at their new slots; may be
+ *            scores (then only moved ones are written), else no overlap.
+ * positions, positions_out  NULL (then sinks and recent are 0), or int32 alike: lla_paged_weigh's.
+ * k_cache, v_cache  in dtype, as in lla_paged_append; rows are moved in place.
+ * keep       [S] int32 (below 0 counts as 0).  dropped: NULL or [S] int32.
+ * sinks, recent >= 0; S <= 2^20; d in {16, 32, 64, 128}.  A slot below L whose page is not in the cache ranks below all, is
+ * not moved, and is reported by lla_sync_status.  Asynchronous on `stream`, one launch, no scratch.
+ */
+int lla_paged_evict(int dtype, const float* scores, float* scores_out, const int* positions, int* positions_out, void* k_cache,
+                    void* v_cache, const int* block_table, const int* kv_lens, const int* keep, const int* dropped, int S,
+                    int Hkv, int d, int page_size, int num_pages, int table_width, long long page_stride, int sinks, int recent,
+                    void* stream);
+
+/*
+ * lla_paged_trim -- lengths after an eviction, and the pages behind them back to the free list (a stack, as lla_paged_plan
+ * takes them).  For every sequence, b = min(L, keep[s]): new_lens[s] = b, new_dropped[s] = dropped[s] + L - b, and the
+ * table's entries ceil(b / page_size) .. ceil(L / page_size) - 1 that are not negative are pushed, sequences and entries in
+ * order.  The table is not written: those entries are free from then on.  keep 0 ends a sequence.
+ *
+ * kv_lens, keep  [S] int32, S in [1, 8192].  dropped, new_dropped: NULL, or [S] int32 (dropped alone may be NULL: 0).
+ * free_pages [free_capacity] int32, written from *free_count on; free_left [1]: the new length.  A page for which there is
+ *            no room is lost, and reported by lla_sync_status.
+ * new_lens may be kv_lens, new_dropped dropped and free_left free_count; no other two arrays may overlap.
+ * Asynchronous on `stream`, one launch, no scratch.
+ */
+int lla_paged_trim(const int* kv_lens, const int* keep, int S, int page_size, const int* block_table, int table_width,
+                   int* free_pages, int free_capacity, const int* free_count, const int* dropped, int* new_lens, int* new_dropped,
+                   int* free_left, void* stream);
+
 /* Message for the calling thread's most recent failure ("" if none). Owned by the library. */
 const char* lla_last_error(void);
 

@@ -27,6 +27,8 @@ __all__ = [
     "lla_paged_plan", "lla_paged_append", "lla_paged_parallax", "lla_paged_parallax_ex", "lla_paged_parallax_workspace_size",
     "lla_rotary", "lla_rotary_backward", "lla_rotary_backward_workspace_size", "RotaryTable", "rotary_table", "rotary",
     "rotary_backward",
+    "lla_paged_weigh", "lla_paged_weigh_workspace_size", "lla_paged_evict", "lla_paged_trim",
+    "paged_weigh", "paged_evict", "PagedTrim", "paged_trim",
     "PagedPlan", "paged_plan", "paged_append", "paged_parallax",
     "LLA_OK", "LLA_ERR_INVALID_ARG", "LLA_ERR_UNSUPPORTED", "LLA_ERR_CUDA", "LLA_ERR_DEVICE_TIMEOUT",
     "LLA_DTYPE_BF16", "LLA_DTYPE_FP32", "LLA_PATH_AUTO", "LLA_PATH_TENSOR", "LLA_PATH_FP32",
@@ -93,6 +95,11 @@ _SIGNATURES = {
                                        _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_ll, _c_ll, _c_ll, _c_float,
                                        _c_int, _vp, _c_size, _vp]),
     "lla_paged_parallax_workspace_size": (_c_size, [_c_int] * 10),
+    "lla_paged_weigh": (_c_int, [_c_int] + [_vp] * 10 + [_c_int] * 9 + [_c_ll, _c_ll, _c_float, _c_float, _c_int, _c_int, _vp,
+                                 _c_size, _vp]),
+    "lla_paged_weigh_workspace_size": (_c_size, [_c_int] * 9),
+    "lla_paged_evict": (_c_int, [_c_int] + [_vp] * 10 + [_c_int] * 6 + [_c_ll, _c_int, _c_int, _vp]),
+    "lla_paged_trim": (_c_int, [_vp, _vp, _c_int, _c_int, _vp, _c_int, _vp, _c_int, _vp, _vp, _vp, _vp, _vp, _vp]),
     "lla_rotary": (_c_int, [_c_int, ctypes.POINTER(lla_rotary_rows), _c_int, _c_int, _c_int, _c_int, _vp, _c_ll, _vp, _c_int,
                             _c_int, _c_float, _c_float, _vp, _vp, _c_int, _vp]),
     "lla_rotary_backward": (_c_int, [_c_int, _c_int, ctypes.POINTER(lla_rotary_rows), _c_int, _c_int, _c_int, _c_int, _vp, _c_ll,
@@ -1058,3 +1065,156 @@ def rotary_backward(dy, x, positions, table, *, gain=None, eps=None, interleaved
     many = isinstance(dy, (tuple, list))
     dgain = None if all(g is None for g in dgains) else tuple(dgains) if many else dgains[0]
     return (tuple(outs) if many else outs[0]), dgain
+
+
+# -------------------------------------------------------------------------------------------------- bounded caches
+def lla_paged_weigh(dtype, q_ptr, lse_ptr, k_cache_ptr, scores_ptr, scores_out_ptr, positions_ptr, dropped_ptr, table_ptr, cu_ptr,
+                    kv_ptr, T, S, Hq, Hkv, d, page_size, num_pages, table_width, max_new, q_stride, page_stride, tau, decay, last,
+                    causal, ws_ptr, ws_bytes, stream_ptr):
+    """Raw entry point on device pointers (ints); raises LLAError on failure."""
+    _check(load_library().lla_paged_weigh(dtype, q_ptr, lse_ptr, k_cache_ptr, scores_ptr, scores_out_ptr, positions_ptr, dropped_ptr,
+                                          table_ptr, cu_ptr, kv_ptr, T, S, Hq, Hkv, d, page_size, num_pages, table_width, max_new,
+                                          q_stride, page_stride, tau, decay, last, causal, ws_ptr, ws_bytes, stream_ptr))
+
+
+def lla_paged_weigh_workspace_size(dtype, T, S, Hq, Hkv, d, page_size, table_width, max_new):
+    return load_library().lla_paged_weigh_workspace_size(dtype, T, S, Hq, Hkv, d, page_size, table_width, max_new)
+
+
+def lla_paged_evict(dtype, scores_ptr, scores_out_ptr, positions_ptr, positions_out_ptr, k_cache_ptr, v_cache_ptr, table_ptr, kv_ptr,
+                    keep_ptr, dropped_ptr, S, Hkv, d, page_size, num_pages, table_width, page_stride, sinks, recent, stream_ptr):
+    """Raw entry point on device pointers (ints); raises LLAError on failure."""
+    _check(load_library().lla_paged_evict(dtype, scores_ptr, scores_out_ptr, positions_ptr, positions_out_ptr, k_cache_ptr,
+                                          v_cache_ptr, table_ptr, kv_ptr, keep_ptr, dropped_ptr, S, Hkv, d, page_size, num_pages,
+                                          table_width, page_stride, sinks, recent, stream_ptr))
+
+
+def lla_paged_trim(kv_ptr, keep_ptr, S, page_size, table_ptr, table_width, free_ptr, free_capacity, free_count_ptr, dropped_ptr,
+                   new_lens_ptr, new_dropped_ptr, free_left_ptr, stream_ptr):
+    """Raw entry point on device pointers (ints); raises LLAError on failure."""
+    _check(load_library().lla_paged_trim(kv_ptr, keep_ptr, S, page_size, table_ptr, table_width, free_ptr, free_capacity,
+                                         free_count_ptr, dropped_ptr, new_lens_ptr, new_dropped_ptr, free_left_ptr, stream_ptr))
+
+
+@functools.lru_cache(maxsize=256)
+def _weigh_workspace_bytes(device_index, dtype, Hq, Hkv, d, page_size, max_new):
+    """Scratch of a paged_weigh call: a function of these sizes alone (0: the call will be refused)."""
+    return lla_paged_weigh_workspace_size(dtype, 1, 1, Hq, Hkv, d, page_size, 1, max_new)
+
+
+def _check_cache(cache):
+    """(num_pages, Hkv, page_size, d, page stride, lla dtype) of one cache."""
+    return _check_caches(cache, cache)
+
+
+def paged_weigh(q, lse, k_cache, scores, block_table, cu_q, kv_lens, tau, max_new, *, positions=None, dropped=None, decay=1.0,
+                last=0, causal=True, out=None, workspace=None, stream=None):
+    """Adds the attention that a step's rows gave every cached position to its score (include/lla.h, lla_paged_weigh):
+    scores = decay * scores (0 for the step's own tokens) + the sum over rows of exp(tau q.k - lse).
+
+    q [T, Hq, d], k_cache, block_table, cu_q, kv_lens, tau, max_new, causal: paged_parallax's, and lse [T, Hq] what it wrote.
+    scores [num_pages, Hkv, page_size] fp32, updated in place or, with out, written there.  positions: None, or int32 like
+    scores, given each new token's position in its sequence (slot + dropped[s]; dropped [S] int32, paged_trim's).
+    last: only rows of the last `last` tokens of a sequence count (0: all).
+    Returns the new scores.  Sequences without tokens in the step are left alone.  Results have the same bits every run.
+    Asynchronous on the current (or given) stream.  workspace: as for paged_parallax.
+    """
+    import torch
+    P, Hkv, Z, d, page_stride, dtype = _check_cache(k_cache)
+    dev = k_cache.device
+    if stream is not None or dev.index != torch.cuda.current_device():
+        with _on_stream(dev, stream):
+            return paged_weigh(q, lse, k_cache, scores, block_table, cu_q, kv_lens, tau, max_new, positions=positions,
+                               dropped=dropped, decay=decay, last=last, causal=causal, out=out, workspace=workspace)
+    if q.dim() != 3 or block_table.dim() != 2:
+        raise _bad(f"q must be [T, Hq, d] and block_table [S, W], got {tuple(q.shape)}, {tuple(block_table.shape)}")
+    T, Hq, _ = q.shape
+    S, W = block_table.shape
+    i32, f32, max_new = torch.int32, torch.float32, int(max_new)
+    q, qs = _token_rows(q, "q", k_cache, Hq, d)
+    lse_ptr, scores_ptr = _ints("lse", lse, (T, Hq), f32, dev), _ints("scores", scores, (P, Hkv, Z), f32, dev)
+    out = scores if out is None else _same("out", out, (P, Hkv, Z), f32, dev)
+    pos_ptr = None if positions is None else _ints("positions", positions, (P, Hkv, Z), i32, dev)
+    drop_ptr = None if dropped is None else _ints("dropped", dropped, (S,), i32, dev)
+    table_ptr = _ints("block_table", block_table, (S, W), i32, dev)
+    cu_ptr, kv_ptr = _ints("cu_q", cu_q, (S + 1,), i32, dev), _ints("kv_lens", kv_lens, (S,), i32, dev)
+    stream_ptr = torch._C._cuda_getCurrentRawStream(dev.index)
+    if workspace is None:
+        workspace = _scratch(dev, stream_ptr, _weigh_workspace_bytes(dev.index, dtype, Hq, Hkv, d, Z, max_new))
+        ws_bytes = workspace.numel()
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise _bad(f"workspace must be a contiguous tensor on {dev}")
+    else:
+        ws_bytes = workspace.numel() * workspace.element_size()
+    lla_paged_weigh(dtype, q.data_ptr(), lse_ptr, k_cache.data_ptr(), scores_ptr, out.data_ptr(), pos_ptr, drop_ptr, table_ptr,
+                    cu_ptr, kv_ptr, T, S, Hq, Hkv, d, Z, P, W, max_new, qs, page_stride, float(tau), float(decay), int(last),
+                    1 if causal else 0, workspace.data_ptr(), ws_bytes, stream_ptr)
+    return out
+
+
+def paged_evict(scores, k_cache, v_cache, block_table, kv_lens, keep, *, positions=None, dropped=None, sinks=0, recent=0,
+                scores_out=None, positions_out=None, stream=None):
+    """Keeps the keep[s] positions of largest score of every sequence and key head, in slots 0 .. keep[s]-1 (include/lla.h,
+    lla_paged_evict): kept rows of keys and values, scores and positions move in place into the slots that others leave.
+
+    scores, positions: paged_weigh's, [num_pages, Hkv, page_size]; block_table [S, W], kv_lens, keep [S]: int32 CUDA tensors.
+    sinks, recent: the first and the last so many positions of a sequence rank before all others (they need positions, and
+    dropped where paged_trim has counted any).  scores_out, positions_out: where the results go, in place by default.
+    Lengths and pages stay as they are until paged_trim, which is called once after every layer's eviction.
+    Asynchronous on the current (or given) stream.
+    """
+    import torch
+    P, Hkv, Z, d, page_stride, dtype = _check_caches(k_cache, v_cache)
+    dev = k_cache.device
+    if stream is not None or dev.index != torch.cuda.current_device():
+        with _on_stream(dev, stream):
+            return paged_evict(scores, k_cache, v_cache, block_table, kv_lens, keep, positions=positions, dropped=dropped,
+                               sinks=sinks, recent=recent, scores_out=scores_out, positions_out=positions_out)
+    if block_table.dim() != 2:
+        raise _bad("block_table must be [S, W]")
+    S, W = block_table.shape
+    i32, f32, like = torch.int32, torch.float32, (P, Hkv, Z)
+    scores_ptr = _ints("scores", scores, like, f32, dev)
+    scores_out_ptr = scores_ptr if scores_out is None else _ints("scores_out", scores_out, like, f32, dev)
+    pos_ptr = None if positions is None else _ints("positions", positions, like, i32, dev)
+    pos_out_ptr = pos_ptr if positions_out is None else _ints("positions_out", positions_out, like, i32, dev)
+    lla_paged_evict(dtype, scores_ptr, scores_out_ptr, pos_ptr, pos_out_ptr, k_cache.data_ptr(), v_cache.data_ptr(),
+                    _ints("block_table", block_table, (S, W), i32, dev), _ints("kv_lens", kv_lens, (S,), i32, dev),
+                    _ints("keep", keep, (S,), i32, dev), None if dropped is None else _ints("dropped", dropped, (S,), i32, dev),
+                    S, Hkv, d, Z, P, W, page_stride, int(sinks), int(recent), torch._C._cuda_getCurrentRawStream(dev.index))
+
+
+PagedTrim = namedtuple("PagedTrim", "kv_lens dropped free_left")
+
+
+def paged_trim(kv_lens, keep, block_table, free_pages, free_count, page_size, *, dropped=None, new_lens=None, new_dropped=None,
+               free_left=None, stream=None):
+    """Lengths after an eviction, and the pages behind them back to the free stack (include/lla.h, lla_paged_trim).
+
+    kv_lens, keep [S], block_table [S, W], free_pages [F] (pushed to in place), free_count [1]: int32 CUDA tensors, paged_plan's.
+    dropped: None (zeros) or [S], the tokens that left each sequence before.  Returns PagedTrim(kv_lens, dropped, free_left);
+    new_lens=kv_lens, new_dropped=dropped and free_left=free_count update a serving loop's state in place.  keep[s] = 0 ends a
+    sequence.  Asynchronous on the current (or given) stream.
+    """
+    import torch
+    if not kv_lens.is_cuda:
+        raise _bad("paged_trim takes CUDA tensors (there is no CPU path)")
+    dev, i32 = kv_lens.device, torch.int32
+    if stream is not None or dev.index != torch.cuda.current_device():
+        with _on_stream(dev, stream):
+            return paged_trim(kv_lens, keep, block_table, free_pages, free_count, page_size, dropped=dropped, new_lens=new_lens,
+                              new_dropped=new_dropped, free_left=free_left)
+    if block_table.dim() != 2:
+        raise _bad("block_table must be [S, W]")
+    S, W = block_table.shape
+    F, like = free_pages.numel(), torch.empty_like
+    kv_ptr, keep_ptr = _ints("kv_lens", kv_lens, (S,), i32, dev), _ints("keep", keep, (S,), i32, dev)
+    table_ptr, free_ptr = _ints("block_table", block_table, (S, W), i32, dev), _ints("free_pages", free_pages, (F,), i32, dev)
+    count_ptr = _ints("free_count", free_count, (1,), i32, dev)
+    drop_ptr = None if dropped is None else _ints("dropped", dropped, (S,), i32, dev)
+    new_lens = like(kv_lens) if new_lens is None else _same("new_lens", new_lens, (S,), i32, dev)
+    new_dropped = like(kv_lens) if new_dropped is None else _same("new_dropped", new_dropped, (S,), i32, dev)
+    free_left = like(free_count) if free_left is None else _same("free_left", free_left, (1,), i32, dev)
+    lla_paged_trim(kv_ptr, keep_ptr, S, int(page_size), table_ptr, W, free_ptr, F, count_ptr, drop_ptr, new_lens.data_ptr(),
+                   new_dropped.data_ptr(), free_left.data_ptr(), torch._C._cuda_getCurrentRawStream(dev.index))
+    return PagedTrim(new_lens, new_dropped, free_left)

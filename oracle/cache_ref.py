@@ -131,8 +131,8 @@ def paged_evict_ref(scores, table, kv_lens, keep, page, Hkv, positions=None, dro
                 must = [int(positions[a]) < sinks or int(positions[a]) >= newest - recent for a in at]
             order = sorted(range(L), key=lambda j: (not must[j], 0.0 if must[j] else -value[j], j))
             stay = sorted(order[:b])
-            source = list(range(b))
-            holes = [j for j in range(b) if j not in set(stay)]
+            source, kept = list(range(b)), set(stay)
+            holes = [j for j in range(b) if j not in kept]
             for hole, j in zip(holes, [j for j in stay if j >= b]):
                 source[hole] = j
             out[s, h] = source
