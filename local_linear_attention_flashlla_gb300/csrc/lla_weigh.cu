@@ -27,14 +27,14 @@ constexpr int kTile = 64, kBlock = 32;       // keys of a tile, rows of a block
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kKeys = kTile / kWarps;        // a warp's
 
+// RS sets of eight query rows at a time.
 template <typename T, int D>
 struct Shape {
     static constexpr int kRow = D * (int)sizeof(T);              // bytes of a key
     static constexpr int kPieces = kRow / 16;                    // 16-byte pieces of it
-    static constexpr int kStage = kKeys * kRow;                  // a warp's 16 keys
+    static constexpr int kStage = kKeys * (kRow + 8);            // a warp's 16 keys, their pages and old scores
     static constexpr int kStages = kRow >= 512 ? 3 : kRow >= 256 ? 4 : 6;
     static constexpr int kSteps = kRow / 32;                     // mma steps over d: 32 bytes of a row each
-    static constexpr int kSets = kRow >= 512 ? 1 : 2;            // sets of eight rows at a time
     static constexpr size_t smem = (size_t)kWarps * kStages * kStage;
 };
 
@@ -75,41 +75,86 @@ __device__ __forceinline__ void split(uint32_t x, uint32_t& hi, uint32_t& lo) {
     lo = __float_as_uint(__uint_as_float(x) - __uint_as_float(hi));
 }
 
-template <typename T, int D>
+// Where a tile is one unit (rows of one block, no extra units), the next piece is the next tile: no divisions.
+__device__ __forceinline__ bool next_tile(const Work& w, Walk& k, Piece& p, int& tiles) {
+    if (k.u >= k.end) return false;
+    p.s = k.s; p.h = k.h; p.t = k.t; p.q = k.q;
+    p.b0 = 0; p.b1 = 1;
+    p.slot = -1; p.parts = 0;
+    ++k.u;
+    if (++k.t == tiles) {
+        k.t = 0;
+        if (++k.h == w.Hkv) {
+            k.h = 0;
+            if (k.u < k.end) {
+                do {
+                    if (++k.s >= w.S) {                  // lengths that changed during the call
+                        k.end = k.u;
+                        break;
+                    }
+                    k.q = load_seq(w, k.s);
+                } while (tiles_of(w, k.q) == 0);
+                tiles = tiles_of(w, k.q);
+            }
+        }
+    }
+    return true;
+}
+
+// ONE: no sequence has more than 8 RS rows to a key head, so a tile is one unit and its rows stay in registers from tile to
+// tile.  Else blocks of kBlock rows, RS sets of them at a time.
+template <typename T, int D, int RS, bool ONE>
 __global__ void __launch_bounds__(kThreads) weigh_mma_kernel(Args a) {
     using Sh = Shape<T, D>;
-    constexpr int NS = Sh::kStages, SETS = Sh::kSets, STEPS = Sh::kSteps, P = Sh::kPieces;
+    constexpr int NS = Sh::kStages, STEPS = Sh::kSteps, P = Sh::kPieces, SW = P < 8 ? P - 1 : 7;
     extern __shared__ __align__(128) unsigned char ring[];
     __shared__ long long scratch[40];
     const Work& w = a.w;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
-    const uint32_t base = tc::smem_u32(ring) + warp * NS * Sh::kStage;
+    unsigned char* mine = ring + warp * NS * Sh::kStage;         // stages: keys, pages [16], old scores [16]
+    const uint32_t base = tc::smem_u32(mine);
     cudaGridDependencySynchronize();
     Walk ahead = begin_walk(w, scratch), wk = ahead;
+    int tiles_a = tiles_of(w, ahead.q), tiles_w = tiles_a;
+    auto next = [&](Walk& k, Piece& p, int& tiles) { return ONE ? next_tile(w, k, p, tiles) : next_piece(w, k, p); };
 
-    // copies of this warp's keys of a piece into a stage
-    auto fetch = [&](int stage, bool& more) {
-        Piece p;
-        more = more && next_piece(w, ahead, p);
+    // The piece to be copied next, and the page of its key `lane & 15` (loaded a piece ahead of its use).
+    Piece n;
+    int page = -1;
+    bool more;
+    auto look = [&] {
+        more = next(ahead, n, tiles_a);
+        page = -1;
+        const int key = (n.t << w.keys_shift) + warp * kKeys + (lane & 15);
+        if (more && key < n.q.L) page = w.table[(size_t)n.s * w.width + (key >> w.page_shift)];
+    };
+    look();
+    auto fetch = [&](int stage) {
         if (more) {
-            const int key0 = (p.t << w.keys_shift) + warp * kKeys;
-            const int* row = w.table + (size_t)p.s * w.width;
+            const int key0 = (n.t << w.keys_shift) + warp * kKeys, in = (1 << w.page_shift) - 1;
+            const int id = page >= 0 && page < w.num_pages ? page : -1;      // (reported where its score would be written)
 #pragma unroll
             for (int i = 0; i < (kKeys * P + 31) / 32; ++i) {
-                const int e = i * 32 + lane, r = e / P, x = e % P, key = key0 + r;
-                if (e >= kKeys * P || key >= p.q.L) continue;        // keys behind the last are never weighed
-                const int page = row[key >> w.page_shift];
-                if (page < 0 || page >= w.num_pages) continue;       // (reported where its score would be written)
-                const int in = key & ((1 << w.page_shift) - 1);
-                copy16(base + stage * Sh::kStage + r * Sh::kRow + ((x ^ (r & (P < 8 ? P - 1 : 7))) << 4),
-                       a.k + page * a.page_bytes + ((long long)((p.h << w.page_shift) + in) * P + x) * 16);
+                const int e = i * 32 + lane, r = e / P, x = e % P;
+                const int pg = __shfl_sync(0xffffffffu, id, r & 15);         // keys behind the last have none: never weighed
+                if (pg >= 0 && e < kKeys * P)
+                    copy16(base + stage * Sh::kStage + r * Sh::kRow + ((x ^ (r & SW)) << 4),
+                           a.k + pg * a.page_bytes + ((long long)((n.h << w.page_shift) + ((key0 + r) & in)) * P + x) * 16);
             }
+            if (lane < kKeys) {
+                const int key = key0 + lane;
+                reinterpret_cast<int*>(mine + stage * Sh::kStage + kKeys * Sh::kRow)[lane] = page;
+                if (id >= 0 && n.slot < 0 && w.decay != 0.f && !(w.causal && key >= n.q.L - n.q.n))
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;"
+                                 ::"r"(base + stage * Sh::kStage + kKeys * (Sh::kRow + 4) + lane * 4),
+                                 "l"(w.scores + ((((long long)id * w.Hkv + n.h) << w.page_shift) + (key & in)) ) : "memory");
+            }
+            look();
         }
         copies_end();
     };
-    bool more = true;
 #pragma unroll
-    for (int i = 0; i < NS - 1; ++i) fetch(i, more);
+    for (int i = 0; i < NS - 1; ++i) fetch(i);
 
     const uint32_t* q32 = static_cast<const uint32_t*>(a.q);
     int stage = 0;
@@ -117,107 +162,113 @@ __global__ void __launch_bounds__(kThreads) weigh_mma_kernel(Args a) {
     p.parts = p.s = p.h = p.t = 0;
     p.slot = -1;
     int at_s = -1, at_h = -1;                // whose rows the operand holds, where they are all of them
-    uint32_t b[SETS][STEPS][2];
-    float lse[SETS][2];
-    int limit[SETS][2];
-    while (next_piece(w, wk, p)) {
+    uint32_t b[RS][STEPS][2];
+    float lse[RS][2];
+    int limit[RS][2];
+    while (next(wk, p, tiles_w)) {
         copies_wait<NS - 2>();
         __syncwarp();
         const int key0 = (p.t << w.keys_shift) + warp * kKeys, rows = rows_of(w, p.q);
-        const bool all = rows <= SETS * 8;   // the operand can stay from tile to tile
         float sum[2] = {0.f, 0.f};           // of keys g and g + 8
         const uint32_t at = base + stage * Sh::kStage;
         if (key0 < p.q.L) {
+            const int r1 = ONE ? 1 : min(p.b1 * kBlock, rows);
 #pragma unroll 1
-            for (int r0 = p.b0 * kBlock; r0 < min(p.b1 * kBlock, rows); r0 += SETS * 8) {
-                if (!all || at_s != p.s || at_h != p.h) {
-                    at_s = all ? p.s : -1;
+            for (int r0 = ONE ? 0 : p.b0 * kBlock; r0 < r1; r0 += RS * 8) {
+                if (!ONE || at_s != p.s || at_h != p.h) {
+                    at_s = p.s;
                     at_h = p.h;
 #pragma unroll
-                    for (int n = 0; n < SETS; ++n) {
-                        const int r = r0 + n * 8 + g;               // the lane's row of the operand
+                    for (int m = 0; m < RS; ++m) {
+                        const int r = r0 + m * 8 + g;               // the lane's row of the operand
                         const int i = over_g(w, min(r, rows - 1)), head = p.h * w.G + min(r, rows - 1) - i * w.G;
                         const uint32_t* src = q32 + ((p.q.token0 + p.q.first + i) * a.q_stride + (long long)head * D) * (int)sizeof(T) / 4;
 #pragma unroll
                         for (int k = 0; k < STEPS; ++k) {
-                            b[n][k][0] = r < rows ? src[k * 8 + c] : 0u;
-                            b[n][k][1] = r < rows ? src[k * 8 + c + 4] : 0u;
+                            b[m][k][0] = r < rows ? src[k * 8 + c] : 0u;
+                            b[m][k][1] = r < rows ? src[k * 8 + c + 4] : 0u;
                         }
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {               // the lane's columns of the products
-                            const int x = r0 + n * 8 + 2 * c + e;
-                            limit[n][e] = 0;
-                            lse[n][e] = 0.f;
+                            const int x = r0 + m * 8 + 2 * c + e;
+                            limit[m][e] = 0;
+                            lse[m][e] = 0.f;
                             if (x < rows) {
                                 const int ix = over_g(w, x);
                                 const float y = a.lse[(long long)(p.q.token0 + p.q.first + ix) * a.Hq + p.h * w.G + x - ix * w.G];
-                                lse[n][e] = y * 1.4426950408889634f;
-                                limit[n][e] = y == -INFINITY ? 0 : keys_seen(w, p.q, ix);     // -inf: a row without weights
+                                lse[m][e] = y * 1.4426950408889634f;
+                                limit[m][e] = y == -INFINITY ? 0 : keys_seen(w, p.q, ix);     // -inf: a row without weights
                             }
                         }
                     }
                 }
-                float s[SETS][4], small[sizeof(T) == 4 ? SETS : 1][4];
+                // even and odd steps of bf16, large and small products of fp32, have sums of their own
+                float s[RS][4], other[RS][4];
 #pragma unroll
-                for (int n = 0; n < SETS; ++n)
+                for (int m = 0; m < RS; ++m)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        s[n][i] = 0.f;
-                        if (sizeof(T) == 4) small[sizeof(T) == 4 ? n : 0][i] = 0.f;
-                    }
+                    for (int i = 0; i < 4; ++i) s[m][i] = other[m][i] = 0.f;
 #pragma unroll
                 for (int k = 0; k < STEPS; ++k) {
                     uint32_t f[4];
                     const int r = lane & 15, x = k * 2 + (lane >> 4);
-                    ldsm4(at + r * Sh::kRow + ((x ^ (r & (P < 8 ? P - 1 : 7))) << 4), f);
+                    ldsm4(at + r * Sh::kRow + ((x ^ (r & SW)) << 4), f);
                     if constexpr (sizeof(T) == 2) {
 #pragma unroll
-                        for (int n = 0; n < SETS; ++n) mma(s[n], f, b[n][k][0], b[n][k][1]);
+                        for (int m = 0; m < RS; ++m) mma(k & 1 ? other[m] : s[m], f, b[m][k][0], b[m][k][1]);
                     } else {
                         uint32_t fh[4], fl[4];
 #pragma unroll
                         for (int i = 0; i < 4; ++i) split(f[i], fh[i], fl[i]);
 #pragma unroll
-                        for (int n = 0; n < SETS; ++n) {
+                        for (int m = 0; m < RS; ++m) {
                             uint32_t h0, l0, h1, l1;
-                            split(b[n][k][0], h0, l0);
-                            split(b[n][k][1], h1, l1);
-                            mma_tf32(small[n], fl, h0, h1);
-                            mma_tf32(small[n], fh, l0, l1);
-                            mma_tf32(s[n], fh, h0, h1);
+                            split(b[m][k][0], h0, l0);
+                            split(b[m][k][1], h1, l1);
+                            mma_tf32(other[m], fl, h0, h1);
+                            mma_tf32(other[m], fh, l0, l1);
+                            mma_tf32(s[m], fh, h0, h1);
                         }
                     }
                 }
 #pragma unroll
-                for (int n = 0; n < SETS; ++n)
+                for (int m = 0; m < RS; ++m)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = key0 + g + (i >> 1) * 8;
-                        float x = s[n][i];
-                        if constexpr (sizeof(T) == 4) x += small[n][i];
-                        if (key < limit[n][i & 1]) sum[i >> 1] += tc::ex2(fmaf(x, a.scale, -lse[n][i & 1]));
-                    }
+                    for (int i = 0; i < 4; ++i)
+                        if (key0 + g + (i >> 1) * 8 < limit[m][i & 1])
+                            sum[i >> 1] += tc::ex2(fmaf(s[m][i] + other[m][i], a.scale, -lse[m][i & 1]));
             }
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
                 sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
             }
-            const float mine = c == 0 ? sum[0] : sum[1];
-            const int k = warp * kKeys + g + c * 8;
-            if (c < 2) {
-                if (p.slot < 0) put_score(w, p.q, p.s, p.h, (p.t << w.keys_shift) + k, mine);
-                else part_of(w, blockIdx.x, p.slot)[k] = mine;
+        }
+        if (c < 2) {
+            const int k = g + c * 8, key = key0 + k;
+            float x = c == 0 ? sum[0] : sum[1];
+            if (p.slot >= 0) {
+                part_of(w, blockIdx.x, p.slot)[warp * kKeys + k] = x;
+            } else if (key < p.q.L) {
+                const unsigned char* st = mine + stage * Sh::kStage + kKeys * Sh::kRow;
+                const int pg = reinterpret_cast<const int*>(st)[k];
+                if (pg < 0 || pg >= w.num_pages) {
+                    atomicOr(w.err, (unsigned)kDevErrPagedArg);
+                } else {
+                    const long long e = (((long long)pg * w.Hkv + p.h) << w.page_shift) + (key & ((1 << w.page_shift) - 1));
+                    const bool fresh = w.causal && key >= p.q.L - p.q.n;
+                    if (!fresh && w.decay != 0.f) x = fmaf(w.decay, reinterpret_cast<const float*>(st)[kKeys + k], x);
+                    w.out[e] = x;
+                    if (fresh && w.positions) w.positions[e] = key + (w.dropped ? w.dropped[p.s] : 0);
+                }
             }
-        } else if (p.slot >= 0 && c < 2) {
-            part_of(w, blockIdx.x, p.slot)[warp * kKeys + g + c * 8] = 0.f;
         }
         __syncwarp();                        // the stage before this one is read: it may be filled again
-        fetch((stage + NS - 1) % NS, more);
+        fetch((stage + NS - 1) % NS);
         if (++stage == NS) stage = 0;
     }
     copies_wait<0>();
-    if (tid == 0) w.hdr[blockIdx.x] = WeighHeader{p.slot == 1 ? p.parts : 0, p.s, p.h, p.t};
+    if (!ONE && tid == 0) w.hdr[blockIdx.x] = WeighHeader{p.slot == 1 ? p.parts : 0, p.s, p.h, p.t};
 }
 
 // Adds the parts of the tile that CTA blockIdx.x starts and others finish: its slot 1, then slots 0 of those behind it.
@@ -233,20 +284,31 @@ __global__ void __launch_bounds__(256) weigh_join_kernel(Work w) {
     }
 }
 
-template <typename T, int D>
-cudaError_t launch_one(const Args& a, cudaStream_t stream) {
+template <typename T, int D, int RS, bool ONE>
+cudaError_t launch_rows(const Args& a, cudaStream_t stream) {
     constexpr size_t smem = Shape<T, D>::smem;
-    cudaError_t e = cudaFuncSetAttribute(weigh_mma_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    auto* kern = weigh_mma_kernel<T, D, RS, ONE>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return paged::launch_after(weigh_mma_kernel<T, D>, dim3(a.w.ctas), kThreads, smem, stream, a);
+    return paged::launch_after(kern, dim3(a.w.ctas), kThreads, smem, stream, a);
+}
+// rows: the most that a sequence has to a key head.  Sets that stay in registers, as many as there is room for.
+template <typename T, int D>
+cudaError_t launch_one(const Args& a, long long rows, cudaStream_t stream) {
+    if (rows <= 8) return launch_rows<T, D, 1, true>(a, stream);
+    if (rows <= 16) return launch_rows<T, D, 2, true>(a, stream);
+    if constexpr (D * sizeof(T) <= 256) {
+        if (rows <= 32) return launch_rows<T, D, 4, true>(a, stream);
+    }
+    return launch_rows<T, D, 2, false>(a, stream);
 }
 template <typename T>
-cudaError_t launch_typed(const Args& a, int d, cudaStream_t stream) {
+cudaError_t launch_typed(const Args& a, int d, long long rows, cudaStream_t stream) {
     switch (d) {
-        case 16: return launch_one<T, 16>(a, stream);
-        case 32: return launch_one<T, 32>(a, stream);
-        case 64: return launch_one<T, 64>(a, stream);
-        default: return launch_one<T, 128>(a, stream);
+        case 16: return launch_one<T, 16>(a, rows, stream);
+        case 32: return launch_one<T, 32>(a, rows, stream);
+        case 64: return launch_one<T, 64>(a, rows, stream);
+        default: return launch_one<T, 128>(a, rows, stream);
     }
 }
 
@@ -304,7 +366,9 @@ cudaError_t launch_weigh_mma(const WeighProblem& p, const WeighSplit& sp, cudaSt
     const int es = p.dtype == LLA_DTYPE_BF16 ? 2 : 4;
     weigh::Args a{weigh::make_work(p, sp), p.q, p.lse, static_cast<const char*>(p.k), p.Hq, p.q_stride, p.page_stride * es,
                   p.tau * 1.4426950408889634f};
-    return p.dtype == LLA_DTYPE_BF16 ? weigh::launch_typed<__nv_bfloat16>(a, p.d, stream) : weigh::launch_typed<float>(a, p.d, stream);
+    const long long rows = most_rows(p);
+    return p.dtype == LLA_DTYPE_BF16 ? weigh::launch_typed<__nv_bfloat16>(a, p.d, rows, stream)
+                                     : weigh::launch_typed<float>(a, p.d, rows, stream);
 }
 
 cudaError_t launch_weigh_join(const WeighProblem& p, const WeighSplit& sp, cudaStream_t stream) {
@@ -373,8 +437,7 @@ int lla_paged_weigh(int dtype, const void* q, const float* lse, const void* k_ca
     if (!workspace && (e = cudaMallocAsync(&p.ws, need, stream)) != cudaSuccess) return lw::cuda_failf(e, "cudaMallocAsync(workspace)");
     e = lla::launch_weigh_mma(p, sp, stream);
     // a tile of one block is never cut
-    const long long most = (long long)(last > 0 && last < max_new ? last : max_new) * p.G;
-    if (e == cudaSuccess && most > sp.rows) e = lla::launch_weigh_join(p, sp, stream);
+    if (e == cudaSuccess && lla::most_rows(p) > sp.rows) e = lla::launch_weigh_join(p, sp, stream);
     if (!workspace) {
         const cudaError_t e2 = cudaFreeAsync(p.ws, stream);
         if (e == cudaSuccess && e2 != cudaSuccess) return lw::cuda_failf(e2, "cudaFreeAsync(workspace)");

@@ -32,6 +32,9 @@ struct WeighProblem {
     void* ws;
 };
 
+// The most rows that count which a sequence has to a key head.
+inline long long most_rows(const WeighProblem& p) { return (long long)(p.last > 0 && p.last < p.max_new ? p.last : p.max_new) * p.G; }
+
 struct WeighHeader {
     int parts;      // 0: this CTA starts no tile that others finish; else CTAs that share it
     int s, h, tile;
