@@ -32,7 +32,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kRows = 128;
+constexpr int kRows = kTileRows;
 constexpr int kSoft = 256;                     // threads that hold rows
 constexpr int kLoad = 64;                      // threads that load queries and probes
 constexpr int kThreads = kSoft + 64 + kLoad;   // 168 registers each at launch: 384 x 168 = 256 x 216 + 128 x 72
@@ -669,19 +669,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_dealloc(tm, Sh::kTmem);
     }
     if (tid == 0 && b.err) atomicOr(w.err, (unsigned)kDevErrMbarTimeout);
-}
-
-// Token rows [T, Hq, d] as (column, head of a group, key head, token); box: 64 columns of the G heads of 128 / G tokens.
-bool make_rows_map(CUtensorMap* map, const void* rows, long long stride, const PagedProblem& p) {
-    auto enc = tensor_map_encoder();
-    if (!enc) return false;
-    cuuint64_t dims[4] = {(cuuint64_t)p.d, (cuuint64_t)p.G, (cuuint64_t)p.Hkv, (cuuint64_t)p.T};
-    cuuint64_t strides[3] = {(cuuint64_t)p.d * 2, (cuuint64_t)p.G * p.d * 2, (cuuint64_t)stride * 2};
-    cuuint32_t box[4] = {64, (cuuint32_t)p.G, 1, (cuuint32_t)(kRows / p.G)};
-    cuuint32_t estr[4] = {1, 1, 1, 1};
-    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(rows), dims, strides, box, estr,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D>

@@ -352,7 +352,7 @@ int check_sizes(int dtype, int T, int S, int Hq, int Hkv, int d, int page_size, 
     return LLA_OK;
 }
 
-WeighSplit split_of(const WeighProblem& p, int sms) { return weigh_mma_split(p, sms); }
+WeighSplit split_of(const WeighProblem& p, int sms) { return weigh_tc_fits(p) ? weigh_tc_split(p, sms) : weigh_mma_split(p, sms); }
 
 }  // namespace
 }  // namespace weigh
@@ -435,14 +435,15 @@ int lla_paged_weigh(int dtype, const void* q, const float* lse, const void* k_ca
     p.ws = workspace;
     cudaError_t e = cudaSuccess;
     if (!workspace && (e = cudaMallocAsync(&p.ws, need, stream)) != cudaSuccess) return lw::cuda_failf(e, "cudaMallocAsync(workspace)");
-    e = lla::launch_weigh_mma(p, sp, stream);
+    const char* why = "lla_paged_weigh launch";
+    e = lla::weigh_tc_fits(p) ? lla::launch_weigh_tc(p, sp, stream, &why) : lla::launch_weigh_mma(p, sp, stream);
     // a tile of one block is never cut
     if (e == cudaSuccess && lla::most_rows(p) > sp.rows) e = lla::launch_weigh_join(p, sp, stream);
     if (!workspace) {
         const cudaError_t e2 = cudaFreeAsync(p.ws, stream);
         if (e == cudaSuccess && e2 != cudaSuccess) return lw::cuda_failf(e2, "cudaFreeAsync(workspace)");
     }
-    if (e != cudaSuccess) return lw::cuda_failf(e, "lla_paged_weigh launch");
+    if (e != cudaSuccess) return lw::cuda_failf(e, why);
     return LLA_OK;
 }
 

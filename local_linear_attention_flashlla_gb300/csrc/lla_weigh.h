@@ -48,6 +48,9 @@ inline size_t weigh_workspace_bytes(const WeighSplit& sp) {
 }
 
 // bf16, d in {64, 128}, many rows: lla_weigh_tc.cu.  Everything else: lla_weigh.cu.
+bool weigh_tc_fits(const WeighProblem& p);
+WeighSplit weigh_tc_split(const WeighProblem& p, int sms);
+cudaError_t launch_weigh_tc(const WeighProblem& p, const WeighSplit& sp, cudaStream_t stream, const char** why);
 WeighSplit weigh_mma_split(const WeighProblem& p, int sms);
 cudaError_t launch_weigh_mma(const WeighProblem& p, const WeighSplit& sp, cudaStream_t stream);
 cudaError_t launch_weigh_join(const WeighProblem& p, const WeighSplit& sp, cudaStream_t stream);
