@@ -241,7 +241,8 @@ __device__ __forceinline__ void snap_start(const Work& w, Walk& k) {
 
 constexpr int kMostWarps = 12;       // of a block that divides work
 
-// Inclusive sum of v over the block's threads in thread order; *all: the block's total.  sh: 32 long longs.
+// Inclusive sum of v over the block's threads in thread order; *all: the block's total.  sh: 32 long longs.  NW: the most warps.
+template <int NW = kMostWarps>
 __device__ __forceinline__ long long block_scan(long long v, long long* sh, long long* all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = (blockDim.x + 31) >> 5;
     for (int o = 1; o < 32; o <<= 1) {
@@ -252,7 +253,7 @@ __device__ __forceinline__ long long block_scan(long long v, long long* sh, long
     __syncthreads();
     long long sum = 0;
 #pragma unroll
-    for (int i = 0; i < kMostWarps; ++i) {
+    for (int i = 0; i < NW; ++i) {
         const long long t = i < nw ? sh[i] : 0;
         if (i < warp) v += t;
         sum += t;

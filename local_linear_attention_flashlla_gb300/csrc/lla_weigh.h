@@ -155,8 +155,10 @@ struct Walk {
     Seq q;
 };
 
+constexpr int kMostWarps = 20;
+
 // Range of CTA blockIdx.x and the tile it begins in.  Every thread of the block calls it; sh: 40 long longs; blockDim.x is
-// a multiple of 32 and at most 32 paged::kMostWarps.
+// a multiple of 32 and at most 32 kMostWarps.
 __device__ inline Walk begin_walk(const Work& w, long long* sh) {
     const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, cta = blockIdx.x;
     const int per = (w.S + nt - 1) / nt, s0 = min(tid * per, w.S), s1 = min(s0 + per, w.S);
@@ -169,7 +171,7 @@ __device__ inline Walk begin_walk(const Work& w, long long* sh) {
         k.q = load_seq(w, s);
         mine += head_units(w, k.q) * w.Hkv;
     }
-    long long pre = paged::block_scan(mine, sh, &total) - mine;
+    long long pre = paged::block_scan<kMostWarps>(mine, sh, &total) - mine;
     const int active = (int)(total < w.ctas ? total : w.ctas);
     if (cta >= active) return k;
     k.share = paged::div_units(total, active);

@@ -6,9 +6,10 @@
 // tensor pipe 512 cycles and its exponentials (16 a cycle) 1024: the exponentials bound it.  Two halves of the keys share each
 // block of queries, which halves what comes from L2.
 //
-// Warps 0-3 and 4-7 weigh the halves, warp 8 copies keys and queries (TMA: a box per page, and per 64 columns of a block's rows),
-// warp 9 issues the products, warps 10 and 11 lay out each block's logsumexps and the keys that its rows see (and copy its
-// rows where 128 is not a multiple of G).  The four accumulators, two for each half, fill TMEM.
+// Sixteen warps weigh (a thread a key and half of a block's columns: eight with whole rows wait for TMEM and for their own
+// chains), one copies keys and queries (TMA: a box per page, and per 64 columns of a block's rows), one issues the products, two lay
+// out each block's logsumexps and the keys that its rows see (and copy its rows where 128 is not a multiple of G).  The
+// four accumulators, two for each half, fill TMEM.
 #include <math.h>
 
 #include "../../include/lla.h"
@@ -27,7 +28,7 @@ using paged::kBoxRows;
 using paged::kTileRows;
 
 constexpr int kHalf = 128, kTile = 2 * kHalf;      // keys
-constexpr int kSum = 256, kLoad = 64;              // threads that weigh, that lay out rows
+constexpr int kSum = 512, kLoad = 64;              // threads that weigh, that lay out rows
 constexpr int kThreads = kSum + 64 + kLoad;
 constexpr int kK = 2, kQ = 2, kR = 4;              // stages of keys, of queries, of the rows' numbers
 
@@ -50,12 +51,14 @@ struct Args {
 struct Shared {
     uint64_t kfull[kK], kempty[kK], qfull[kQ], qempty[kQ], rfull[kR], rempty[kR];
     uint64_t sfull[2][2], sempty[2][2];            // by half and buffer
+    uint64_t pfull[8], pempty[8];                  // of the sums that a second warp leaves
     uint64_t fin;
     uint32_t tmem;
     int err;
     int all[kR][2];                                // keys that all rows of the block see (by loading warp)
     float nlse[kR][kTileRows];                     // -lse log2(e)
     int limit[kR][kTileRows];                      // keys a row sees
+    float other[kTile];
 };
 
 __device__ __forceinline__ int columns_of(int rows) { return (rows + 15) & ~15; }      // N of a product
@@ -229,25 +232,20 @@ __device__ __forceinline__ void weigh32(const float (&x)[32], const float* nlse,
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(nlse + 4 * i);
-        int4 lim = make_int4(0, 0, 0, 0);
-        if (MASK) lim = *reinterpret_cast<const int4*>(limit + 4 * i);
-        float u, v;
-        f2_unpack(f2_fma(f2_pack(x[4 * i], x[4 * i + 1]), sc2, nl.x), u, v);
-        u = ex2(u);
-        v = ex2(v);
+        float y[4];
+        f2_unpack(f2_fma(f2_pack(x[4 * i], x[4 * i + 1]), sc2, nl.x), y[0], y[1]);
+        f2_unpack(f2_fma(f2_pack(x[4 * i + 2], x[4 * i + 3]), sc2, nl.y), y[2], y[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = ex2(y[k]);
         if (MASK) {
-            u = key < lim.x ? u : 0.f;
-            v = key < lim.y ? v : 0.f;
+            const int4 lim = *reinterpret_cast<const int4*>(limit + 4 * i);
+            y[0] = key < lim.x ? y[0] : 0.f;
+            y[1] = key < lim.y ? y[1] : 0.f;
+            y[2] = key < lim.z ? y[2] : 0.f;
+            y[3] = key < lim.w ? y[3] : 0.f;
         }
-        sum[0] = f2_add(sum[0], f2_pack(u, v));
-        f2_unpack(f2_fma(f2_pack(x[4 * i + 2], x[4 * i + 3]), sc2, nl.y), u, v);
-        u = ex2(u);
-        v = ex2(v);
-        if (MASK) {
-            u = key < lim.z ? u : 0.f;
-            v = key < lim.w ? v : 0.f;
-        }
-        sum[1] = f2_add(sum[1], f2_pack(u, v));
+        sum[0] = f2_add(sum[0], f2_pack(y[0], y[1]));
+        sum[1] = f2_add(sum[1], f2_pack(y[2], y[3]));
     }
 }
 
@@ -278,7 +276,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&b.sfull[i >> 1][i & 1], 1);
-            mbar_init(&b.sempty[i >> 1][i & 1], kSum / 64);
+            mbar_init(&b.sempty[i >> 1][i & 1], kSum / 64);            // warps of a half
+        }
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(&b.pfull[i], 1);
+            mbar_init(&b.pempty[i], 1);
         }
         mbar_init(&b.fin, 1);
         b.err = 0;
@@ -301,18 +303,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp > kSum / 32 + 1) {
         lay_out<D>(a, wk, qring, b);
     } else {
-        const int half = warp >> 2;
-        const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16) + half * 2 * kTileRows;
+        // warps w and w + 8 have the same keys, 64 columns of a block each; the first takes the sums of the second
+        const int pair = warp & 7, half = pair >> 2, part = warp >> 3;
+        const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16) + half * 2 * kTileRows + part * (kTileRows / 2);
         const uint64_t sc2 = f2_pack(a.scale, a.scale);
-        int n = 0;
+        int n = 0, pieces = 0;
         bool ok = true;
         Piece p;
         p.parts = p.s = p.h = p.t = 0;
         p.slot = -1;
         while (ok && next_piece(w, wk, p)) {
-            const int in_tile = half * kHalf + (warp & 3) * 32 + lane, key = p.t * kTile + in_tile;
+            const int in_tile = pair * 32 + lane, key = p.t * kTile + in_tile;
             const int last = min(p.t * kTile + half * kHalf + kHalf, p.q.L);      // behind the half's last key
-            const bool live = has_half(p, half), whole = p.slot < 0 && key < p.q.L;
+            const bool live = has_half(p, half), whole = part == 0 && p.slot < 0 && key < p.q.L;
             const bool fresh = w.causal && key >= p.q.L - p.q.n;
             // page and old score, on their way while the rows are summed
             int page = -1;
@@ -332,9 +335,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_fence_after();
                 if (live) {
                     const bool open = last <= min(b.all[sr][0], b.all[sr][1]);    // every row sees all of the half's keys
-                    for (int c = 0; c < cols; c += 32) {
+#pragma unroll
+                    for (int i = 0; i < kTileRows / 2; i += 32) {
+                        const int c = part * (kTileRows / 2) + i;
+                        if (c >= cols) break;
                         float x[32];
-                        tmem_ld32(lanes + buf * kTileRows + c, x);
+                        tmem_ld32(lanes + buf * kTileRows + i, x);
                         tmem_ld_wait();
                         // (columns behind the block's, where it has an odd number of sixteens, are old ones: masked)
                         if (open && c + 32 <= cols) weigh32<false>(x, &b.nlse[sr][c], &b.limit[sr][c], key, sc2, sum);
@@ -352,13 +358,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             float x, y, z;
             f2_unpack(f2_add(sum[0], sum[1]), x, y);
             z = x + y;
-            if (p.slot >= 0) part_of(w, blockIdx.x, p.slot)[in_tile] = z;
-            else if (there) {
-                w.out[e] = !fresh && w.decay != 0.f ? fmaf(w.decay, old, z) : z;
-                if (fresh && w.positions) w.positions[e] = key + (w.dropped ? w.dropped[p.s] : 0);
-            } else if (whole) {
-                atomicOr(w.err, (unsigned)kDevErrPagedArg);
+            if (part == 1) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&b.pempty[pair], (pieces & 1) ^ 1, &b.err));
+                if (!ok) break;
+                b.other[in_tile] = z;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.pfull[pair]);
+            } else {
+                ok = __all_sync(0xffffffffu, mbar_wait(&b.pfull[pair], pieces & 1, &b.err));
+                if (!ok) break;
+                z += b.other[in_tile];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.pempty[pair]);
+                if (p.slot >= 0) part_of(w, blockIdx.x, p.slot)[in_tile] = z;
+                else if (there) {
+                    w.out[e] = !fresh && w.decay != 0.f ? fmaf(w.decay, old, z) : z;
+                    if (fresh && w.positions) w.positions[e] = key + (w.dropped ? w.dropped[p.s] : 0);
+                } else if (whole) {
+                    atomicOr(w.err, (unsigned)kDevErrPagedArg);
+                }
             }
+            ++pieces;
         }
         if (tid == 0) w.hdr[blockIdx.x] = WeighHeader{ok && p.slot == 1 ? p.parts : 0, p.s, p.h, p.t};
     }
