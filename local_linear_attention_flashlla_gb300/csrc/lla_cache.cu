@@ -49,11 +49,14 @@ int sm_count() {
 // what changes is touched: after a step of 64 new positions 64 rows move, where closing the gaps in order would move
 // half the cache.
 //
-// The threshold is found bit by bit from the top, two bits a pass over the scores (in shared memory as integers of the
-// same order), the counts of the four digits in one 64-bit word a thread.
+// Scores become integers of the same order, held in shared memory (those behind kHeld are read again).  The threshold is
+// found by histograms of 2048 equal ranges between the lowest and the highest of them, each pass within the range that holds the
+// threshold: two passes for most scores, three at most.  (Two bits a pass took sixteen, and most of 177 us on 64 x 16 heads
+// of 4145 positions.)  Then windows of kWindow slots are marked, with one scan for all of a window's ballots.
 constexpr int kEvictThreads = 512, kEvictWarps = kEvictThreads / 32;
-constexpr int kHeld = 12288;             // scores of a sequence that shared memory holds; those behind are read again
-constexpr int kBuffer = 2 * kEvictThreads;
+constexpr int kHeld = 10240;             // scores of a sequence that shared memory holds
+constexpr int kBins = 4 * kEvictThreads;
+constexpr int kChunks = 8, kWindow = kChunks * kEvictThreads;
 
 struct EvictArgs {
     const float* scores;
@@ -67,7 +70,7 @@ struct EvictArgs {
     const int* keep;
     const int* dropped;                  // or null
     long long page_bytes;                // from page to page of a cache
-    int S, Hkv, width, page_shift, num_pages, row_bytes, sinks, recent;
+    int S, Hkv, width, page_shift, num_pages, vec_shift, sinks, recent;   // vec_shift: log2 of 16-byte pieces of a row
     unsigned* err;
 };
 
@@ -107,32 +110,72 @@ __device__ __forceinline__ uint32_t rank_of(const EvictArgs& a, const Pair& p, i
     return order_of(a.scores[e]);
 }
 
-// Inclusive prefix over the block of two 16-bit counts a thread (in one word), and the block's total.
-__device__ __forceinline__ uint2 scan_pairs(uint32_t x, uint32_t* sh) {
+// Inclusive sum of x over the block's threads, and the block's total.
+__device__ __forceinline__ int2 scan_block(int x, int* sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t t = __shfl_up_sync(0xffffffffu, x, o);
+        const int t = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += t;
     }
     if (lane == 31) sh[warp] = x;
     __syncthreads();
-    uint32_t before = 0, all = 0;
+    int before = 0, all = 0;
 #pragma unroll
     for (int i = 0; i < kEvictWarps; ++i) {
-        const uint32_t t = sh[i];
+        const int t = sh[i];
         if (i < warp) before += t;
         all += t;
     }
     __syncthreads();
-    return make_uint2(x + before, all);
+    return make_int2(x + before, all);
 }
 
-__global__ void __launch_bounds__(kEvictThreads) paged_evict_kernel(EvictArgs a) {
+struct EvictShared {
+    int red[kEvictWarps];
+    uint32_t low[kEvictWarps], high[kEvictWarps];
+    int count[kChunks * kEvictWarps];        // of a window's ballots, then the sums before them
+    union {
+        unsigned bins[kBins];
+        uint16_t list[2][kWindow];           // holes and movers, from their windows' first slots on
+    };
+    int found[3];                            // bin, what it has, what is still needed of it
+};
+
+// Marks of a window's slots: flag(slot), asked of every slot in [first, end), and for those that have it put(slot, rank), the rank counted
+// from `base` on.  Returns how many there are.
+template <typename Flag, typename Put>
+__device__ __forceinline__ int mark_window(EvictShared& sh, int first, int end, int base, Flag flag, Put put) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    unsigned mine = 0;
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        const int j = first + c * kEvictThreads + tid;
+        const bool yes = j < end && flag(j);
+        const unsigned some = __ballot_sync(0xffffffffu, yes);
+        if (lane == 0) sh.count[c * kEvictWarps + warp] = __popc(some);
+        mine |= (unsigned)yes << c;
+    }
+    __syncthreads();
+    constexpr int kEntries = kChunks * kEvictWarps;
+    static_assert(kEntries <= kEvictThreads, "an entry to a thread");
+    const int n = tid < kEntries ? sh.count[tid] : 0;
+    const int2 t = scan_block(n, sh.red);
+    if (tid < kEntries) sh.count[tid] = base + t.x - n;
+    __syncthreads();
+#pragma unroll
+    for (int c = 0; c < kChunks; ++c) {
+        const bool yes = mine >> c & 1;
+        const unsigned some = __ballot_sync(0xffffffffu, yes);
+        if (yes) put(first + c * kEvictThreads + tid, sh.count[c * kEvictWarps + warp] + __popc(some & ((1u << lane) - 1)));
+    }
+    __syncthreads();
+    return t.y;
+}
+
+__global__ void __launch_bounds__(kEvictThreads, 3) paged_evict_kernel(EvictArgs a) {
     extern __shared__ uint32_t held[];               // kHeld ranks
-    __shared__ unsigned long long counts[kEvictWarps][2];
-    __shared__ uint32_t red[kEvictWarps];
-    __shared__ int holes[kBuffer], movers[kBuffer];
+    __shared__ EvictShared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = (int)cluster.num_blocks(), me = (int)cluster.block_rank();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -148,86 +191,6 @@ __global__ void __launch_bounds__(kEvictThreads) paged_evict_kernel(EvictArgs a)
     p.b = min(p.L, max(a.keep[p.s], 0));
     p.newest = p.L + (a.dropped ? a.dropped[p.s] : 0);
     const bool out = a.scores_out != a.scores, pos_out = a.positions && a.positions_out != a.positions;
-
-    uint32_t threshold = 0;
-    int ties = INT_MAX;                              // slots at the threshold that are kept, the lowest ones
-    const bool cut = p.b < p.L;
-    auto rank = [&](int j) { return j < kHeld ? held[j] : rank_of(a, p, j); };
-    if (cut && p.b > 0) {
-        for (int j = tid; j < min(p.L, kHeld); j += kEvictThreads) held[j] = rank_of(a, p, j);
-        __syncthreads();
-        int need = p.b;                              // of those that agree with the threshold so far
-        uint32_t mask = 0;
-        for (int shift = 30; shift >= 0; shift -= 2) {
-            uint32_t c01 = 0, c23 = 0;               // counts of digits 0, 1 and 2, 3: 16 bits each
-            unsigned long long w01 = 0, w23 = 0;
-            int n = 0;
-            for (int j = tid; j < p.L; j += kEvictThreads) {
-                const uint32_t x = rank(j);
-                if ((x & mask) == threshold) {
-                    const uint32_t digit = (x >> shift) & 3u, one = 1u << ((digit & 1u) * 16);
-                    if (digit & 2u) c23 += one;
-                    else c01 += one;
-                }
-                if (++n == 65535) {                  // before a 16-bit count can overflow
-                    w01 += (c01 & 0xffffu) | ((unsigned long long)(c01 >> 16) << 32);
-                    w23 += (c23 & 0xffffu) | ((unsigned long long)(c23 >> 16) << 32);
-                    c01 = c23 = 0;
-                    n = 0;
-                }
-            }
-            w01 += (c01 & 0xffffu) | ((unsigned long long)(c01 >> 16) << 32);
-            w23 += (c23 & 0xffffu) | ((unsigned long long)(c23 >> 16) << 32);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) {
-                w01 += __shfl_xor_sync(0xffffffffu, w01, o);
-                w23 += __shfl_xor_sync(0xffffffffu, w23, o);
-            }
-            if (lane == 0) {
-                counts[warp][0] = w01;
-                counts[warp][1] = w23;
-            }
-            __syncthreads();
-            w01 = w23 = 0;
-#pragma unroll
-            for (int i = 0; i < kEvictWarps; ++i) {
-                w01 += counts[i][0];
-                w23 += counts[i][1];
-            }
-            __syncthreads();
-            const int c[4] = {(int)(uint32_t)w01, (int)(w01 >> 32), (int)(uint32_t)w23, (int)(w23 >> 32)};
-            int digit = 3;
-            while (digit > 0 && need > c[digit]) need -= c[digit--];
-            threshold |= (uint32_t)digit << shift;
-            mask |= 3u << shift;
-            if (need == c[digit]) {                  // all that agree are kept: the bits below need not be known
-                ties = INT_MAX;
-                break;
-            }
-            ties = need;
-        }
-    }
-    // kept: rank above the threshold, or at it (its unknown bits are zeros) while ties last
-
-    const int vecs = a.row_bytes / 16;
-    auto move_rows = [&](int n) {                    // rows movers[i] -> holes[i], i < n, those of this CTA
-        for (int e = tid; e < ((n + ranks - 1 - me) / ranks) * vecs; e += kEvictThreads) {
-            const int i = e / vecs * ranks + me, c = e % vecs;
-            const int sp = page_of(a, p, movers[i]), dp = page_of(a, p, holes[i]);
-            if (sp < 0 || dp < 0) continue;
-            const int in = (1 << a.page_shift) - 1;
-            const long long from = sp * a.page_bytes + ((long long)((p.h << a.page_shift) + (movers[i] & in)) * vecs + c) * 16;
-            const long long to = dp * a.page_bytes + ((long long)((p.h << a.page_shift) + (holes[i] & in)) * vecs + c) * 16;
-            const uint4 x = *reinterpret_cast<const uint4*>(a.k + from), y = *reinterpret_cast<const uint4*>(a.v + from);
-            *reinterpret_cast<uint4*>(a.k + to) = x;
-            *reinterpret_cast<uint4*>(a.v + to) = y;
-            if (c == 0) {
-                const long long se = element_of(a, p, sp, movers[i]), de = element_of(a, p, dp, holes[i]);
-                a.scores_out[de] = a.scores[se];
-                if (a.positions) a.positions_out[de] = a.positions[se];
-            }
-        }
-    };
     auto carry = [&](int j) {                        // a kept slot that stays, where the results go elsewhere
         if ((!out && !pos_out) || j % ranks != me) return;
         const int page = page_of(a, p, j);
@@ -236,82 +199,190 @@ __global__ void __launch_bounds__(kEvictThreads) paged_evict_kernel(EvictArgs a)
         if (out) a.scores_out[e] = a.scores[e];
         if (pos_out) a.positions_out[e] = a.positions[e];
     };
-    if (!cut) {
+    if (p.b == p.L) {
         for (int j = tid; j < p.L; j += kEvictThreads) carry(j);
         return;
     }
     if (p.b == 0) return;
-    // Slots in order, holes and movers into two buffers; as many as both have are moved whenever one is full.
-    int hole_at = 0, mover_at = p.b;                 // next slots to look at
-    int nh = 0, nm = 0;                              // in the buffers
-    int tied = 0;                                    // slots at the threshold before hole_at and before mover_at
-    int tied_m = 0;
-    // ties below b come before those behind it
-    if (ties != INT_MAX) {
+
+    // ranks, the lowest and highest of those that are not mandatory, and how many are
+    constexpr uint32_t kMust = 0xffffffffu;          // above every score's rank
+    uint32_t lo = kMust, hi = 0;
+    int need = 0;
+#pragma unroll 4
+    for (int j = tid; j < p.L; j += kEvictThreads) {
+        const uint32_t x = rank_of(a, p, j);
+        if (j < kHeld) held[j] = x;
+        if (x == kMust) ++need;
+        else {
+            lo = min(lo, x);
+            hi = max(hi, x);
+        }
+    }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    need = __reduce_add_sync(0xffffffffu, need);
+    if (lane == 0) {
+        sh.low[warp] = lo;
+        sh.high[warp] = hi;
+        sh.red[warp] = need;
+    }
+    __syncthreads();
+    need = p.b;
+#pragma unroll
+    for (int i = 0; i < kEvictWarps; ++i) {
+        lo = min(lo, sh.low[i]);
+        hi = max(hi, sh.high[i]);
+        need -= sh.red[i];
+    }
+    auto rank = [&](int j) { return j < kHeld ? held[j] : rank_of(a, p, j); };
+    // kept: every rank above `threshold`, and of those at it the first `ties`
+    uint32_t threshold = kMust;
+    int ties = p.b;                                  // more mandatory ones than are kept
+    if (need == 0) {
+        threshold = kMust - 1;                       // (no score has it)
+        ties = 0;
+    }
+    while (need > 0) {
+        if (lo == hi) {
+            threshold = lo;
+            ties = need;
+            break;
+        }
+        const int shift = max(32 - __clz(hi - lo) - 11, 0);      // (hi - lo) >> shift < 2048
+#pragma unroll
+        for (int i = 0; i < kBins / kEvictThreads; ++i) sh.bins[i * kEvictThreads + tid] = 0;
+        __syncthreads();
+#pragma unroll 4
+        for (int j = tid; j < p.L; j += kEvictThreads) {
+            const uint32_t x = rank(j);
+            if (x >= lo && x <= hi) atomicAdd(&sh.bins[(x - lo) >> shift], 1u);
+        }
+        __syncthreads();
+        // bins from the highest down, four to a thread
+        constexpr int kOf = kBins / kEvictThreads;
+        int n[kOf], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kOf; ++i) {
+            n[i] = (int)sh.bins[kBins - 1 - (tid * kOf + i)];
+            sum += n[i];
+        }
+        const int2 t = scan_block(sum, sh.red);
+        int before = t.x - sum;
+        if (before < need && need <= t.x) {
+#pragma unroll
+            for (int i = 0; i < kOf; ++i) {
+                if (before < need && need <= before + n[i]) {
+                    sh.found[0] = kBins - 1 - (tid * kOf + i);
+                    sh.found[1] = n[i];
+                    sh.found[2] = need - before;
+                }
+                before += n[i];
+            }
+        }
+        __syncthreads();
+        lo += (uint32_t)sh.found[0] << shift;
+        hi = min(hi, lo + ((1u << shift) - 1));
+        const bool all = sh.found[1] == sh.found[2];
+        need = sh.found[2];
+        __syncthreads();
+        if (all) {                                   // all of the bin are kept: what lies in it need not be told apart
+            threshold = lo - 1;                      // (lo > 0: with it the lowest would be kept, and with that all)
+            ties = 0;
+            break;
+        }
+    }
+
+    auto page_element = [&](int page, int j, int c) {          // byte offset of piece c of slot j in a cache
+        const int in = (1 << a.page_shift) - 1;
+        return page * a.page_bytes + ((((long long)((p.h << a.page_shift) + (j & in))) << a.vec_shift) + c) * 16;
+    };
+    // windows of holes from slot 0 on, of movers from b on; as many as both have are moved, then the empty one's next window is marked
+    int next[2] = {0, p.b}, base[2] = {0, 0}, have[2] = {0, 0}, used[2] = {0, 0}, tied = 0, tied_behind = 0;
+    const int end[2] = {p.b, p.L};
+    if (ties > 0) {                                  // ties below b come before those behind it
         int mine = 0;
         for (int j = tid; j < p.b; j += kEvictThreads) mine += rank(j) == threshold;
         mine = __reduce_add_sync(0xffffffffu, mine);
-        if (lane == 0) red[warp] = (uint32_t)mine;
+        if (lane == 0) sh.red[warp] = mine;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kEvictWarps; ++i) tied_m += (int)red[i];
+        for (int i = 0; i < kEvictWarps; ++i) tied_behind += sh.red[i];
         __syncthreads();
     }
-    auto keeps = [&](uint32_t x, int before) { return x > threshold || (x == threshold && (ties == INT_MAX || before < ties)); };
     for (;;) {
-        while (nh + kEvictThreads <= kBuffer && hole_at < p.b) {
-            const int j = hole_at + tid;
-            const bool in = j < p.b;
-            const uint32_t x = in ? rank(j) : 0u;
-            const uint32_t tie = in && x == threshold && ties != INT_MAX ? 1u : 0u;
-            uint2 t = scan_pairs(tie, red);
-            const bool kept = in && keeps(x, tied + (int)(t.x - tie));
-            tied += (int)t.y;
-            if (kept) carry(j);
-            const uint32_t hole = in && !kept ? 1u : 0u;
-            t = scan_pairs(hole, red);
-            if (hole) holes[nh + t.x - 1] = j;
-            nh += (int)t.y;
-            hole_at += kEvictThreads;
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+            while (used[side] == have[side] && next[side] < end[side]) {
+                const int first = next[side], last = min(first + kWindow, end[side]);
+                int& before = side == 0 ? tied : tied_behind;
+                // ties are kept while they last: those that are not leave their mark in the list's place
+                if (ties > 0 && before < ties) {
+                    const int n = mark_window(sh, first, last, before, [&](int j) { return rank(j) == threshold; },
+                                              [&](int j, int k) { sh.list[side][j - first] = k < ties; });
+                    have[side] = 0;
+                    unsigned keep = 0;               // bit c: the thread's slot of chunk c is a tie that is kept
+#pragma unroll
+                    for (int c = 0; c < kChunks; ++c) {
+                        const int j = first + c * kEvictThreads + tid;
+                        if (j < last && rank(j) == threshold && sh.list[side][j - first]) keep |= 1u << c;
+                    }
+                    __syncthreads();
+                    have[side] = mark_window(sh, first, last, 0, [&](int j) {
+                        const bool kept = rank(j) > threshold || (keep >> ((j - first) / kEvictThreads) & 1);
+                        if (side == 0 && kept) carry(j);
+                        return kept == (side == 1);
+                    }, [&](int j, int k) { sh.list[side][k] = (uint16_t)(j - first); });
+                    before += n;
+                } else {
+                    have[side] = mark_window(sh, first, last, 0, [&](int j) {
+                        const bool kept = rank(j) > threshold;
+                        if (side == 0 && kept) carry(j);
+                        return kept == (side == 1);
+                    }, [&](int j, int k) { sh.list[side][k] = (uint16_t)(j - first); });
+                }
+                base[side] = first;
+                next[side] = last;
+                used[side] = 0;
+            }
         }
-        while (nm + kEvictThreads <= kBuffer && mover_at < p.L) {
-            const int j = mover_at + tid;
-            const bool in = j < p.L;
-            const uint32_t x = in ? rank(j) : 0u;
-            const uint32_t tie = in && x == threshold && ties != INT_MAX ? 1u : 0u;
-            uint2 t = scan_pairs(tie, red);
-            const uint32_t move = in && keeps(x, tied_m + (int)(t.x - tie)) ? 1u : 0u;
-            tied_m += (int)t.y;
-            t = scan_pairs(move, red);
-            if (move) movers[nm + t.x - 1] = j;
-            nm += (int)t.y;
-            mover_at += kEvictThreads;
-        }
-        // every CTA has looked at the slots before hole_at and mover_at (all look at the same ones): they may be written
+        // every CTA has looked at the slots before next[0] and next[1] (all look at the same ones): they may be written
         if (ranks > 1) cluster.sync();
         else __syncthreads();
-        const int n = min(nh, nm);
-        move_rows(n);
-        __syncthreads();
-        if (hole_at >= p.b && mover_at >= p.L) break;
-        // the rest to the front
-        const int left_h = nh - n, left_m = nm - n;
-        int keep_h[2], keep_m[2];
+        const int n = min(have[0] - used[0], have[1] - used[1]);
+        if (n == 0) break;                           // (holes and movers end together)
+        const int vecs = 1 << a.vec_shift, mine = ((n - me + ranks - 1) / ranks) << a.vec_shift;
+        for (int e0 = tid; e0 < mine; e0 += 4 * kEvictThreads) {
+            uint4 x[4], y[4];
+            long long to[4];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int at = tid + i * kEvictThreads;
-            keep_h[i] = at < left_h ? holes[n + at] : 0;
-            keep_m[i] = at < left_m ? movers[n + at] : 0;
-        }
-        __syncthreads();
+            for (int u = 0; u < 4; ++u) {
+                const int e = e0 + u * kEvictThreads;
+                to[u] = -1;
+                if (e >= mine) continue;
+                const int i = (e >> a.vec_shift) * ranks + me, c = e & (vecs - 1);
+                const int from_j = base[1] + sh.list[1][used[1] + i], to_j = base[0] + sh.list[0][used[0] + i];
+                const int sp = page_of(a, p, from_j), dp = page_of(a, p, to_j);
+                if (sp < 0 || dp < 0) continue;
+                const long long from = page_element(sp, from_j, c);
+                x[u] = *reinterpret_cast<const uint4*>(a.k + from);
+                y[u] = *reinterpret_cast<const uint4*>(a.v + from);
+                to[u] = page_element(dp, to_j, c);
+                if (c == 0) {
+                    const long long se = element_of(a, p, sp, from_j), de = element_of(a, p, dp, to_j);
+                    a.scores_out[de] = a.scores[se];
+                    if (a.positions) a.positions_out[de] = a.positions[se];
+                }
+            }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int at = tid + i * kEvictThreads;
-            if (at < left_h) holes[at] = keep_h[i];
-            if (at < left_m) movers[at] = keep_m[i];
+            for (int u = 0; u < 4; ++u)
+                if (to[u] >= 0) {
+                    *reinterpret_cast<uint4*>(a.k + to[u]) = x[u];
+                    *reinterpret_cast<uint4*>(a.v + to[u]) = y[u];
+                }
         }
-        nh = left_h;
-        nm = left_m;
+        used[0] += n;
+        used[1] += n;
         __syncthreads();
     }
 }
@@ -459,7 +530,7 @@ int lla_paged_evict(int dtype, const float* scores, float* scores_out, const int
     unsigned* err = lla::device_error_word();
     if (!err) return lc::failf(LLA_ERR_CUDA, "lla_paged_evict: device error word not found");
     lc::EvictArgs a{scores, scores_out, positions, positions_out, static_cast<char*>(k_cache), static_cast<char*>(v_cache),
-                    block_table, kv_lens, keep, dropped, page_stride * es, S, Hkv, table_width, shift, num_pages, d * es, sinks,
+                    block_table, kv_lens, keep, dropped, page_stride * es, S, Hkv, table_width, shift, num_pages, lla::paged::log2_up(d * es / 16), sinks,
                     recent, err};
     constexpr size_t smem = lc::kHeld * sizeof(uint32_t);
     cudaError_t e = cudaFuncSetAttribute(lc::paged_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);

@@ -2,14 +2,23 @@
 //
 // A tile is 256 keys: two products of 128 keys x N query rows x d, S = K Q^T, for every block of up to 128 rows, the keys being
 // the rows of the accumulator.  So a thread has a key, sums exp(scale s - lse) over its columns in registers, and the sum
-// over query rows needs no exchange; the keys stay in shared memory while query blocks pass.  128 x 128 x 128 takes the
-// tensor pipe 512 cycles and its exponentials (16 a cycle) 1024: the exponentials bound it.  Two halves of the keys share each
-// block of queries, which halves what comes from L2.
+// over query rows needs hardly any exchange; the keys stay in shared memory while query blocks pass.  128 x 128 x 128 takes
+// the tensor pipe 512 cycles and its exponentials (32 a cycle) as many.  Two halves of the keys share each block of queries,
+// which halves what comes from L2.
 //
-// Sixteen warps weigh (a thread a key and half of a block's columns: eight with whole rows wait for TMEM and for their own
-// chains), one copies keys and queries (TMA: a box per page, and per 64 columns of a block's rows), one issues the products, two lay
-// out each block's logsumexps and the keys that its rows see (and copy its rows where 128 is not a multiple of G).  The
-// four accumulators, two for each half, fill TMEM.
+// A last step of 16 columns takes the logsumexp off inside the product: the keys have ones there, a query -lse / tau as three
+// bf16 terms, together exact to 2^-25 of it (added last, so the sum rounds once at that size).  Read from shared memory by the
+// weighing threads instead, 16 bytes for four columns beside the products' operands: 72 us for 71.
+//
+// Sixteen warps weigh (a thread a key and half of a block's columns), one copies keys and queries (TMA: a box per page, and per 64
+// columns of a block's rows), one issues the products, two lay out each block's logsumexps and the keys that its rows see (and
+// copy its rows where 128 is not a multiple of G).  The four accumulators, two for each half, fill TMEM.
+//
+// 512 tokens over 16,384 keys, 32/4 heads, d = 128: 70.7 us, 0.99 PFLOP/s, of which 10 are the start and the join of cut tiles.  The
+// products alone take 64 (what the issuing warp does between two of them delays the next), copies and numbers alone 42, and
+// weights beside the products slow their issue.  Tried there: eight weighing warps 76; exponentials partly on the FMA pipe 81 to
+// 102; three stages of queries 75; N = 256 with one accumulator to a half 89 (products alone 57); 512 keys to a tile 88,
+// with two or four issuing warps 81; an issuing warp to a half 80 (products alone 60).
 #include <math.h>
 
 #include "../../include/lla.h"
@@ -31,11 +40,12 @@ constexpr int kHalf = 128, kTile = 2 * kHalf;      // keys
 constexpr int kSum = 512, kLoad = 64;              // threads that weigh, that lay out rows
 constexpr int kThreads = kSum + 64 + kLoad;
 constexpr int kK = 2, kQ = 2, kR = 4;              // stages of keys, of queries, of the rows' numbers
+constexpr int kTail = 128 * 32;                    // bytes of an operand's last step: 16 columns, no swizzle
 
 template <int D>
 struct Shape {
     static constexpr int kKeyTile = kTile * D * 2, kRowTile = kTileRows * D * 2;
-    static constexpr size_t smem = (size_t)kK * kKeyTile + (size_t)kQ * kRowTile + 1024;
+    static constexpr size_t smem = (size_t)kK * kKeyTile + (size_t)kQ * kRowTile + (kR + 1) * kTail + 1024;
 };
 
 struct Args {
@@ -56,11 +66,16 @@ struct Shared {
     uint32_t tmem;
     int err;
     int all[kR][2];                                // keys that all rows of the block see (by loading warp)
-    float nlse[kR][kTileRows];                     // -lse log2(e)
-    int limit[kR][kTileRows];                      // keys a row sees
+    alignas(16) int limit[kR][kTileRows];                      // keys a row sees
     float other[kTile];
 };
 
+// Offset of 16-byte piece c of row r in a last step: eight rows of a piece are one 128-byte block.
+__device__ __forceinline__ uint32_t tail_off(int r, int c) { return (uint32_t)((r >> 3) * 256 + c * 128 + (r & 7) * 16); }
+// Descriptor of such an operand: no swizzle; 128 bytes from piece to piece, 256 from eight rows to the next.
+__device__ __forceinline__ uint64_t tail_desc(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)(256 >> 4) << 32) | (1ull << 46);
+}
 __device__ __forceinline__ int columns_of(int rows) { return (rows + 15) & ~15; }      // N of a product
 __device__ __forceinline__ bool has_half(const Piece& p, int half) { return p.t * kTile + half * kHalf < p.q.L; }
 
@@ -114,7 +129,7 @@ __device__ void feed(const Args& a, Walk wk, const CUtensorMap* mk, const CUtens
 
 // All lanes run the loop and one issues: what the descriptors are made of is uniform (lla_paged_tc.cu).
 template <int D>
-__device__ void issue(const Work& w, Walk wk, uint32_t tm, uint32_t kring, uint32_t qring, Shared& b) {
+__device__ void issue(const Work& w, Walk wk, uint32_t tm, uint32_t kring, uint32_t qring, uint32_t tails, Shared& b) {
     using Sh = Shape<D>;
     int nk = 0, n = 0;
     bool ok = true;
@@ -127,8 +142,8 @@ __device__ void issue(const Work& w, Walk wk, uint32_t tm, uint32_t kring, uint3
         const int rows = __shfl_sync(0xffffffffu, rows_of(w, p.q), 0);
         const bool second = __shfl_sync(0xffffffffu, (int)has_half(p, 1), 0);
         for (int j = b0; j < b1; ++j, ++n) {
-            const int sq = n % kQ, buf = n & 1;
-            ok = __all_sync(0xffffffffu, mbar_wait(&b.qfull[sq], (n / kQ) & 1, &b.err));
+            const int sq = n % kQ, sr = n % kR, buf = n & 1;
+            ok = __all_sync(0xffffffffu, mbar_wait(&b.qfull[sq], (n / kQ) & 1, &b.err) && mbar_wait(&b.rfull[sr], (n / kR) & 1, &b.err));
             if (!ok) break;
             const uint32_t id = idesc_bf16(kHalf, 16, false, false) - ((16u >> 3) << 17) +
                                 ((uint32_t)(columns_of(min(rows - j * kTileRows, kTileRows)) >> 3) << 17);
@@ -148,6 +163,7 @@ __device__ void issue(const Work& w, Walk wk, uint32_t tm, uint32_t kring, uint3
                             if (ks == 0) umma_ss_c<false>(d, k0 + ko, q0 + qo, id);
                             else umma_ss_c<true>(d, k0 + ko, q0 + qo, id);
                         }
+                        umma_ss_c<true>(tm + (half * 2 + buf) * kTileRows, tail_desc(tails + kR * kTail), tail_desc(tails + sr * kTail), id);
                     }
                     umma_commit(&b.sfull[half][buf]);
                 }
@@ -156,6 +172,7 @@ __device__ void issue(const Work& w, Walk wk, uint32_t tm, uint32_t kring, uint3
             if (!ok) break;
             if (elect_one()) {
                 umma_commit(&b.qempty[sq]);
+                umma_commit(&b.rempty[sr]);
                 if (j + 1 == b1) umma_commit(&b.kempty[st]);
             }
             __syncwarp();
@@ -173,7 +190,7 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
 
 // Each block's numbers, and its rows where boxes cannot bring them.
 template <int D>
-__device__ void lay_out(const Args& a, Walk wk, uint32_t qring, Shared& b) {
+__device__ void lay_out(const Args& a, Walk wk, uint32_t qring, unsigned char* tails, Shared& b) {
     const Work& w = a.w;
     const int t = threadIdx.x - (kThreads - kLoad), lane = threadIdx.x & 31, warp = t >> 5;
     bool ok = true;
@@ -189,20 +206,26 @@ __device__ void lay_out(const Args& a, Walk wk, uint32_t qring, Shared& b) {
 #pragma unroll
             for (int i = 0; i < kTileRows / kLoad; ++i) {
                 const int r = i * kLoad + t, row = row0 + r;
-                float nl = 0.f;
+                float v = 0.f;
                 int limit = 0;
                 if (row < rows) {
                     const int tk = over_g(w, row);
                     const float y = a.lse[(long long)(p.q.token0 + p.q.first + tk) * a.Hq + p.h * w.G + row - tk * w.G];
-                    nl = -1.4426950408889634f * y;
-                    limit = y == -INFINITY ? 0 : keys_seen(w, p.q, tk);      // -inf: a row without weights
+                    if (y != -INFINITY) {                                    // -inf: a row without weights
+                        v = __fdiv_rn(-1.4426950408889634f * y, a.scale);
+                        limit = keys_seen(w, p.q, tk);
+                    }
                 }
-                b.nlse[sr][r] = nl;
+                const float hi = __bfloat162float(__float2bfloat16_rn(v)), left = fabsf(hi) < INFINITY ? v - hi : 0.f;
+                const float mid = __bfloat162float(__float2bfloat16_rn(left));
+                *reinterpret_cast<uint4*>(tails + sr * kTail + tail_off(r, 0)) =
+                    make_uint4(paged::pack_bf16(hi, mid), paged::pack_bf16(left - mid, 0.f), 0u, 0u);
                 b.limit[sr][r] = limit;
                 if (r < cols) all = min(all, limit);
             }
             all = __reduce_min_sync(0xffffffffu, all);
             if (lane == 0) b.all[sr][warp] = all;
+            fence_proxy_async_smem();            // the products read the last step
             __syncwarp();
             if (lane == 0) mbar_arrive(&b.rfull[sr]);
             if (!a.row_boxes) {
@@ -226,15 +249,14 @@ __device__ void lay_out(const Args& a, Walk wk, uint32_t qring, Shared& b) {
     }
 }
 
-// Sum of 2^(scale x + nl) over 32 columns, those with key < limit where MASK.
+// Sum of 2^(scale x) over 32 columns, those with key < limit where MASK.
 template <bool MASK>
-__device__ __forceinline__ void weigh32(const float (&x)[32], const float* nlse, const int* limit, int key, uint64_t sc2, uint64_t (&sum)[2]) {
+__device__ __forceinline__ void weigh32(const float (&x)[32], const int* limit, int key, uint64_t sc2, uint64_t (&sum)[2]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const ulonglong2 nl = *reinterpret_cast<const ulonglong2*>(nlse + 4 * i);
         float y[4];
-        f2_unpack(f2_fma(f2_pack(x[4 * i], x[4 * i + 1]), sc2, nl.x), y[0], y[1]);
-        f2_unpack(f2_fma(f2_pack(x[4 * i + 2], x[4 * i + 3]), sc2, nl.y), y[2], y[3]);
+        f2_unpack(f2_mul(f2_pack(x[4 * i], x[4 * i + 1]), sc2), y[0], y[1]);
+        f2_unpack(f2_mul(f2_pack(x[4 * i + 2], x[4 * i + 3]), sc2), y[2], y[3]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) y[k] = ex2(y[k]);
         if (MASK) {
@@ -257,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ long long scratch[40];
     __shared__ __align__(16) Shared b;
     const uint32_t kring = smem_u32(raw) + ((1024u - (smem_u32(raw) & 1023u)) & 1023u), qring = kring + kK * Sh::kKeyTile;
+    const uint32_t tails = qring + kQ * Sh::kRowTile;        // of the query stages, and of the keys behind them
     const Work& w = a.w;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
@@ -272,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < kR; ++i) {
             mbar_init(&b.rfull[i], kLoad / 32);
-            mbar_init(&b.rempty[i], kSum / 32);
+            mbar_init(&b.rempty[i], kSum / 32 + 1);
         }
         for (int i = 0; i < 4; ++i) {
             mbar_init(&b.sfull[i >> 1][i & 1], 1);
@@ -285,6 +308,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&b.fin, 1);
         b.err = 0;
         mbar_fence_init();
+    }
+    {   // the last steps: ones for the keys, zeros in the second pieces of the queries
+        unsigned char* t = raw + (tails - smem_u32(raw));
+        for (int r = tid; r < 128; r += kThreads) {
+            const uint32_t one = 0x3f80u;
+            *reinterpret_cast<uint4*>(t + kR * kTail + tail_off(r, 0)) = make_uint4(one | one << 16, one, 0u, 0u);
+            for (int i = 0; i <= kR; ++i) *reinterpret_cast<uint4*>(t + i * kTail + tail_off(r, 1)) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        fence_proxy_async_smem();
     }
     if (warp == kSum / 32) {
         tmem_alloc(&b.tmem, 512);
@@ -299,9 +331,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kSum / 32) {
         feed<D>(a, wk, &mk, &mq, kring, qring, b);
     } else if (warp == kSum / 32 + 1) {
-        issue<D>(w, wk, __shfl_sync(0xffffffffu, tm, 0), __shfl_sync(0xffffffffu, kring, 0), __shfl_sync(0xffffffffu, qring, 0), b);
+        issue<D>(w, wk, __shfl_sync(0xffffffffu, tm, 0), __shfl_sync(0xffffffffu, kring, 0), __shfl_sync(0xffffffffu, qring, 0),
+                 __shfl_sync(0xffffffffu, tails, 0), b);
     } else if (warp > kSum / 32 + 1) {
-        lay_out<D>(a, wk, qring, b);
+        lay_out<D>(a, wk, qring, raw + (tails - smem_u32(raw)), b);
     } else {
         // warps w and w + 8 have the same keys, 64 columns of a block each; the first takes the sums of the second
         const int pair = warp & 7, half = pair >> 2, part = warp >> 3;
@@ -343,8 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld32(lanes + buf * kTileRows + i, x);
                         tmem_ld_wait();
                         // (columns behind the block's, where it has an odd number of sixteens, are old ones: masked)
-                        if (open && c + 32 <= cols) weigh32<false>(x, &b.nlse[sr][c], &b.limit[sr][c], key, sc2, sum);
-                        else weigh32<true>(x, &b.nlse[sr][c], &b.limit[sr][c], key, sc2, sum);
+                        if (open && c + 32 <= cols) weigh32<false>(x, &b.limit[sr][c], key, sc2, sum);
+                        else weigh32<true>(x, &b.limit[sr][c], key, sc2, sum);
                     }
                 }
                 tc_fence_before();
@@ -404,7 +437,9 @@ cudaError_t launch_one(const Args& a, const CUtensorMap& mk, const CUtensorMap& 
 }  // namespace weigh
 
 bool weigh_tc_fits(const WeighProblem& p) {
-    return p.dtype == LLA_DTYPE_BF16 && (p.d == 64 || p.d == 128) && most_rows(p) > 32;
+    // 32 sequences of 300 to 6000 keys, four key heads (us, this kernel and lla_weigh.cu's): 12 rows d = 128 33 and 31, 20 rows 33 and
+    // 49; at d = 64 16 rows 29 and 23, 20 rows 29 and 27; 64 x 8 key heads at 3000 to 4096 keys, 32 rows, d = 128 104 and 157
+    return p.dtype == LLA_DTYPE_BF16 && ((p.d == 128 && most_rows(p) > 16) || (p.d == 64 && most_rows(p) > 32));
 }
 
 WeighSplit weigh_tc_split(const WeighProblem& p, int sms) {
