@@ -517,8 +517,8 @@ size_t lla_paged_parallax_workspace_size(int dtype, int path, int T, int S, int 
 
 /*
  * Bounded caches: positions of small attention weight leave a paged cache.  Beside its caches a layer has scores
- * [num_pages, Hkv, page_size] fp32 and positions [num_pages, Hkv, page_size] int32 (both contiguous), laid out and indexed
- * as the pages are: the attention each cached position has received, and the position in its sequence that a slot holds.
+ * [num_pages, Hkv, page_size] fp32 and positions [num_pages, Hkv, page_size] int32 (both contiguous, 16-byte aligned), laid out
+ * and indexed as the pages are: the attention each cached position has received, and the position in its sequence that a slot holds.
  * A step is lla_paged_plan, then per layer lla_rotary, lla_paged_append, lla_paged_parallax_ex (with lse) and
  * lla_paged_weigh.  Where caches are to shrink, after the step: lla_paged_evict for every layer, then lla_paged_trim once.
  * Keys are cached rotated, so a key keeps its position when it moves to another slot; the next step's token rows get theirs

@@ -49,14 +49,13 @@ int sm_count() {
 // what changes is touched: after a step of 64 new positions 64 rows move, where closing the gaps in order would move
 // half the cache.
 //
-// Scores become integers of the same order, held in shared memory (those behind kHeld are read again).  The threshold is
-// found by histograms of 2048 equal ranges between the lowest and the highest of them, each pass within the range that holds the
-// threshold: two passes for most scores, three at most.  (Two bits a pass took sixteen, and most of 177 us on 64 x 16 heads
-// of 4145 positions.)  Then windows of kWindow slots are marked, with one scan for all of a window's ballots.
-constexpr int kEvictThreads = 512, kEvictWarps = kEvictThreads / 32;
-constexpr int kHeld = 10240;             // scores of a sequence that shared memory holds
-constexpr int kBins = 4 * kEvictThreads;
-constexpr int kChunks = 8, kWindow = kChunks * kEvictThreads;
+// Scores become integers of the same order, held in shared memory (those behind kHeld are read again), four neighbouring
+// slots to a thread: they lie on one page.  The threshold is found by histograms of 2048 equal ranges between the lowest and
+// the highest of them, each pass within the range that holds the threshold: two passes for most scores, three at most.  (Two
+// bits a pass took sixteen, and most of 177 us on 64 x 16 heads of 4145 positions.)  Then windows of kWindow slots are
+// marked with one scan each.
+constexpr int kHeld = 10240;             // scores of a sequence that shared memory holds at most
+constexpr int kBins = 2048, kWindow = 2048;
 
 struct EvictArgs {
     const float* scores;
@@ -70,7 +69,7 @@ struct EvictArgs {
     const int* keep;
     const int* dropped;                  // or null
     long long page_bytes;                // from page to page of a cache
-    int S, Hkv, width, page_shift, num_pages, vec_shift, sinks, recent;   // vec_shift: log2 of 16-byte pieces of a row
+    int S, Hkv, width, page_shift, num_pages, vec_shift, sinks, recent, held;   // vec_shift: log2 of 16-byte pieces of a row; held: scores in shared memory
     unsigned* err;
 };
 
@@ -95,128 +94,140 @@ __device__ __forceinline__ int page_of(const EvictArgs& a, const Pair& p, int j)
 __device__ __forceinline__ long long element_of(const EvictArgs& a, const Pair& p, int page, int j) {
     return (((long long)page * a.Hkv + p.h) << a.page_shift) + (j & ((1 << a.page_shift) - 1));
 }
-// Rank of slot j: mandatory positions above all scores, slots without a page below all.
-__device__ __forceinline__ uint32_t rank_of(const EvictArgs& a, const Pair& p, int j) {
-    const int page = page_of(a, p, j);
-    if (page < 0) {
-        atomicOr(a.err, (unsigned)kDevErrPagedArg);
-        return 0u;
-    }
-    const long long e = element_of(a, p, page, j);
-    if (a.positions) {
-        const int x = a.positions[e];
-        if (x < a.sinks || x >= p.newest - a.recent) return 0xffffffffu;
-    }
-    return order_of(a.scores[e]);
+// Ranks of slots 4 q .. 4 q + 3: mandatory positions (kMust) above all scores, a slot without a page (1) below all, and behind the
+// last slot 0, which no range begins with.
+constexpr uint32_t kMust = 0xffffffffu;
+__device__ __forceinline__ uint4 ranks_of(const EvictArgs& a, const Pair& p, int q) {
+    uint32_t r[4] = {0, 0, 0, 0};
+    const int j = 4 * q, page = page_of(a, p, j);
+    if (page < 0) atomicOr(a.err, (unsigned)kDevErrPagedArg);
+    const long long e = element_of(a, p, max(page, 0), j);
+    const float4 x = *reinterpret_cast<const float4*>(a.scores + e);
+    const float s[4] = {x.x, x.y, x.z, x.w};
+    int4 at = make_int4(0, 0, 0, 0);
+    if (a.positions) at = *reinterpret_cast<const int4*>(a.positions + e);
+    const int w[4] = {at.x, at.y, at.z, at.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (j + i < p.L) r[i] = page < 0 ? 1u : a.positions && (w[i] < a.sinks || w[i] >= p.newest - a.recent) ? kMust : order_of(s[i]);
+    return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// Inclusive sum of x over the block's threads, and the block's total.
-__device__ __forceinline__ int2 scan_block(int x, int* sh) {
+// Sums of x[0 .. N-1] over the block, in the order x[0] of all its threads, x[1] of all, ...: what lies before each of the thread's
+// own goes to x, the sum of all is returned.  sh: N integers a warp.
+template <int T, int N>
+__device__ __forceinline__ int scan_block(int (&x)[N], int* sh) {
+    constexpr int W = T / 32;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int own[N];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int t = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += t;
-    }
-    if (lane == 31) sh[warp] = x;
-    __syncthreads();
-    int before = 0, all = 0;
+    for (int i = 0; i < N; ++i) own[i] = x[i];
 #pragma unroll
-    for (int i = 0; i < kEvictWarps; ++i) {
-        const int t = sh[i];
-        if (i < warp) before += t;
-        all += t;
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int t = __shfl_up_sync(0xffffffffu, x[i], o);
+            if (lane >= o) x[i] += t;
+        }
+    if (lane == 31) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) sh[i * W + warp] = x[i];
     }
     __syncthreads();
-    return make_int2(x + before, all);
+    int all = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        x[i] -= own[i];
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            if (k == warp) x[i] += all;
+            all += sh[i * W + k];
+        }
+    }
+    __syncthreads();
+    return all;
 }
 
 struct EvictShared {
-    int red[kEvictWarps];
-    uint32_t low[kEvictWarps], high[kEvictWarps];
-    int count[kChunks * kEvictWarps];        // of a window's ballots, then the sums before them
+    int red[16];
+    uint32_t low[16], high[16];
     union {
         unsigned bins[kBins];
         uint16_t list[2][kWindow];           // holes and movers, from their windows' first slots on
     };
+    int red2[64];
     int found[3];                            // bin, what it has, what is still needed of it
 };
 
-// Marks of a window's slots: flag(slot), asked of every slot in [first, end), and for those that have it put(slot, rank), the rank counted
-// from `base` on.  Returns how many there are.
-template <typename Flag, typename Put>
-__device__ __forceinline__ int mark_window(EvictShared& sh, int first, int end, int base, Flag flag, Put put) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    unsigned mine = 0;
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-        const int j = first + c * kEvictThreads + tid;
-        const bool yes = j < end && flag(j);
-        const unsigned some = __ballot_sync(0xffffffffu, yes);
-        if (lane == 0) sh.count[c * kEvictWarps + warp] = __popc(some);
-        mine |= (unsigned)yes << c;
-    }
-    __syncthreads();
-    constexpr int kEntries = kChunks * kEvictWarps;
-    static_assert(kEntries <= kEvictThreads, "an entry to a thread");
-    const int n = tid < kEntries ? sh.count[tid] : 0;
-    const int2 t = scan_block(n, sh.red);
-    if (tid < kEntries) sh.count[tid] = base + t.x - n;
-    __syncthreads();
-#pragma unroll
-    for (int c = 0; c < kChunks; ++c) {
-        const bool yes = mine >> c & 1;
-        const unsigned some = __ballot_sync(0xffffffffu, yes);
-        if (yes) put(first + c * kEvictThreads + tid, sh.count[c * kEvictWarps + warp] + __popc(some & ((1u << lane) - 1)));
-    }
-    __syncthreads();
-    return t.y;
-}
-
-__global__ void __launch_bounds__(kEvictThreads, 3) paged_evict_kernel(EvictArgs a) {
-    extern __shared__ uint32_t held[];               // kHeld ranks
+// T threads: 512, or 128 where there are pairs enough to fill the device with such blocks.  Each step waits for the one
+// before, so many small blocks side by side hide what few large ones cannot.
+template <int T>
+__global__ void __launch_bounds__(T, T == 128 ? 8 : 2) paged_evict_kernel(EvictArgs a) {
+    constexpr int W = T / 32, N = kWindow / 4 / T;             // warps; quads of a window that a thread has
+    extern __shared__ uint4 held[];                  // a.held / 4 of ranks_of
     __shared__ EvictShared sh;
     cg::cluster_group cluster = cg::this_cluster();
-    const int ranks = (int)cluster.num_blocks(), me = (int)cluster.block_rank();
+    const int ranks = (int)cluster.num_blocks(), me = (int)cluster.block_rank();         // a power of two of CTAs
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int pair = blockIdx.x / ranks;
     cudaGridDependencySynchronize();
     Pair p;
     p.s = pair / a.Hkv;
-    p.h = pair % a.Hkv;
+    p.h = pair - p.s * a.Hkv;
     p.row = a.table + (size_t)p.s * a.width;
     const int kv = a.kv_lens[p.s], room = a.width << a.page_shift;
     p.L = min(max(kv, 0), room);
     if (p.L != kv && tid == 0) atomicOr(a.err, (unsigned)kDevErrPagedArg);
     p.b = min(p.L, max(a.keep[p.s], 0));
     p.newest = p.L + (a.dropped ? a.dropped[p.s] : 0);
+    const int quads = (p.L + 3) >> 2, held4 = a.held >> 2;
     const bool out = a.scores_out != a.scores, pos_out = a.positions && a.positions_out != a.positions;
-    auto carry = [&](int j) {                        // a kept slot that stays, where the results go elsewhere
-        if ((!out && !pos_out) || j % ranks != me) return;
-        const int page = page_of(a, p, j);
+    // kept slots (bits of `kept`) of quad q that stay, where the results go elsewhere
+    auto carry = [&](int q, unsigned kept) {
+        if ((!out && !pos_out) || !kept || (q & (ranks - 1)) != me) return;
+        const int page = page_of(a, p, 4 * q);
         if (page < 0) return;
-        const long long e = element_of(a, p, page, j);
-        if (out) a.scores_out[e] = a.scores[e];
-        if (pos_out) a.positions_out[e] = a.positions[e];
+        const long long e = element_of(a, p, page, 4 * q);
+        if (out) {
+            const float4 x = *reinterpret_cast<const float4*>(a.scores + e);
+            if (kept == 15u) *reinterpret_cast<float4*>(a.scores_out + e) = x;
+            else {
+                if (kept & 1) a.scores_out[e] = x.x;
+                if (kept & 2) a.scores_out[e + 1] = x.y;
+                if (kept & 4) a.scores_out[e + 2] = x.z;
+                if (kept & 8) a.scores_out[e + 3] = x.w;
+            }
+        }
+        if (pos_out) {
+            const int4 x = *reinterpret_cast<const int4*>(a.positions + e);
+            if (kept == 15u) *reinterpret_cast<int4*>(a.positions_out + e) = x;
+            else {
+                if (kept & 1) a.positions_out[e] = x.x;
+                if (kept & 2) a.positions_out[e + 1] = x.y;
+                if (kept & 4) a.positions_out[e + 2] = x.z;
+                if (kept & 8) a.positions_out[e + 3] = x.w;
+            }
+        }
     };
     if (p.b == p.L) {
-        for (int j = tid; j < p.L; j += kEvictThreads) carry(j);
+        for (int q = tid; q < quads; q += T) carry(q, p.L - 4 * q >= 4 ? 15u : (1u << (p.L - 4 * q)) - 1);
         return;
     }
     if (p.b == 0) return;
 
     // ranks, the lowest and highest of those that are not mandatory, and how many are
-    constexpr uint32_t kMust = 0xffffffffu;          // above every score's rank
     uint32_t lo = kMust, hi = 0;
     int need = 0;
-#pragma unroll 4
-    for (int j = tid; j < p.L; j += kEvictThreads) {
-        const uint32_t x = rank_of(a, p, j);
-        if (j < kHeld) held[j] = x;
-        if (x == kMust) ++need;
-        else {
-            lo = min(lo, x);
-            hi = max(hi, x);
+#pragma unroll 2
+    for (int q = tid; q < quads; q += T) {
+        const uint4 r = ranks_of(a, p, q);
+        if (q < held4) held[q] = r;
+        const uint32_t x[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            need += x[i] == kMust;
+            hi = max(hi, x[i] == kMust ? 0u : x[i]);
+            lo = min(lo, x[i] == 0u ? kMust : x[i]);
         }
     }
     lo = __reduce_min_sync(0xffffffffu, lo);
@@ -230,12 +241,12 @@ __global__ void __launch_bounds__(kEvictThreads, 3) paged_evict_kernel(EvictArgs
     __syncthreads();
     need = p.b;
 #pragma unroll
-    for (int i = 0; i < kEvictWarps; ++i) {
+    for (int i = 0; i < W; ++i) {
         lo = min(lo, sh.low[i]);
         hi = max(hi, sh.high[i]);
         need -= sh.red[i];
     }
-    auto rank = [&](int j) { return j < kHeld ? held[j] : rank_of(a, p, j); };
+    auto rank = [&](int q) { return q < held4 ? held[q] : ranks_of(a, p, q); };
     // kept: every rank above `threshold`, and of those at it the first `ties`
     uint32_t threshold = kMust;
     int ties = p.b;                                  // more mandatory ones than are kept
@@ -251,123 +262,147 @@ __global__ void __launch_bounds__(kEvictThreads, 3) paged_evict_kernel(EvictArgs
         }
         const int shift = max(32 - __clz(hi - lo) - 11, 0);      // (hi - lo) >> shift < 2048
 #pragma unroll
-        for (int i = 0; i < kBins / kEvictThreads; ++i) sh.bins[i * kEvictThreads + tid] = 0;
+        for (int i = 0; i < kBins / T; ++i) sh.bins[i * T + tid] = 0;
         __syncthreads();
-#pragma unroll 4
-        for (int j = tid; j < p.L; j += kEvictThreads) {
-            const uint32_t x = rank(j);
-            if (x >= lo && x <= hi) atomicAdd(&sh.bins[(x - lo) >> shift], 1u);
+#pragma unroll 2
+        for (int q = tid; q < quads; q += T) {
+            const uint4 r = rank(q);
+            if (r.x >= lo && r.x <= hi) atomicAdd(&sh.bins[(r.x - lo) >> shift], 1u);
+            if (r.y >= lo && r.y <= hi) atomicAdd(&sh.bins[(r.y - lo) >> shift], 1u);
+            if (r.z >= lo && r.z <= hi) atomicAdd(&sh.bins[(r.z - lo) >> shift], 1u);
+            if (r.w >= lo && r.w <= hi) atomicAdd(&sh.bins[(r.w - lo) >> shift], 1u);
         }
         __syncthreads();
-        // bins from the highest down, four to a thread
-        constexpr int kOf = kBins / kEvictThreads;
-        int n[kOf], sum = 0;
+        // bins from the highest down, a run of them to a thread
+        constexpr int R = kBins / T;
+        int sum[1] = {0};
 #pragma unroll
-        for (int i = 0; i < kOf; ++i) {
-            n[i] = (int)sh.bins[kBins - 1 - (tid * kOf + i)];
-            sum += n[i];
-        }
-        const int2 t = scan_block(sum, sh.red);
-        int before = t.x - sum;
-        if (before < need && need <= t.x) {
-#pragma unroll
-            for (int i = 0; i < kOf; ++i) {
-                if (before < need && need <= before + n[i]) {
-                    sh.found[0] = kBins - 1 - (tid * kOf + i);
-                    sh.found[1] = n[i];
+        for (int i = 0; i < R; ++i) sum[0] += (int)sh.bins[kBins - 1 - (tid * R + i)];
+        const int mine = sum[0];
+        scan_block<T>(sum, sh.red);
+        int before = sum[0];
+        if (before < need && need <= before + mine) {
+            for (int i = 0; i < R; ++i) {
+                const int n = (int)sh.bins[kBins - 1 - (tid * R + i)];
+                if (before < need && need <= before + n) {
+                    sh.found[0] = kBins - 1 - (tid * R + i);
+                    sh.found[1] = n;
                     sh.found[2] = need - before;
                 }
-                before += n[i];
+                before += n;
             }
         }
         __syncthreads();
         lo += (uint32_t)sh.found[0] << shift;
         hi = min(hi, lo + ((1u << shift) - 1));
-        const bool all = sh.found[1] == sh.found[2];
         need = sh.found[2];
+        const bool all = sh.found[1] == need;
         __syncthreads();
         if (all) {                                   // all of the bin are kept: what lies in it need not be told apart
-            threshold = lo - 1;                      // (lo > 0: with it the lowest would be kept, and with that all)
+            threshold = lo - 1;
             ties = 0;
             break;
         }
     }
 
-    auto page_element = [&](int page, int j, int c) {          // byte offset of piece c of slot j in a cache
-        const int in = (1 << a.page_shift) - 1;
-        return page * a.page_bytes + ((((long long)((p.h << a.page_shift) + (j & in))) << a.vec_shift) + c) * 16;
+    // slots of quad q whose rank is above the threshold, and at it
+    auto above = [&](const uint4& r) {
+        return (unsigned)(r.x > threshold) | (unsigned)(r.y > threshold) << 1 | (unsigned)(r.z > threshold) << 2 | (unsigned)(r.w > threshold) << 3;
+    };
+    auto equal = [&](const uint4& r) {
+        return (unsigned)(r.x == threshold) | (unsigned)(r.y == threshold) << 1 | (unsigned)(r.z == threshold) << 2 |
+               (unsigned)(r.w == threshold) << 3;
+    };
+    // bits of quad q that lie in [from, to)
+    auto within = [&](int q, int from, int to) {
+        const int f = from - 4 * q, t = to - 4 * q;
+        return (f <= 0 ? 15u : f >= 4 ? 0u : 15u << f & 15u) & (t >= 4 ? 15u : t <= 0 ? 0u : (1u << t) - 1);
     };
     // windows of holes from slot 0 on, of movers from b on; as many as both have are moved, then the empty one's next window is marked
-    int next[2] = {0, p.b}, base[2] = {0, 0}, have[2] = {0, 0}, used[2] = {0, 0}, tied = 0, tied_behind = 0;
-    const int end[2] = {p.b, p.L};
+    struct Side {
+        int next, base, have, used, tied;            // next window; the present one's first slot, its marks, those used; ties before `next`
+    } hole = {0, 0, 0, 0, 0}, mover = {p.b & ~3, 0, 0, 0, 0};
     if (ties > 0) {                                  // ties below b come before those behind it
         int mine = 0;
-        for (int j = tid; j < p.b; j += kEvictThreads) mine += rank(j) == threshold;
+        for (int q = tid; 4 * q < p.b; q += T) mine += __popc(equal(rank(q)) & within(q, 0, p.b));
         mine = __reduce_add_sync(0xffffffffu, mine);
         if (lane == 0) sh.red[warp] = mine;
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kEvictWarps; ++i) tied_behind += sh.red[i];
+        for (int i = 0; i < W; ++i) mover.tied += sh.red[i];
         __syncthreads();
     }
-    for (;;) {
+    auto refill = [&](Side& d, bool holes, int begin, int end) {
+        while (d.used == d.have && d.next < end) {
+            const int q0 = d.next >> 2;
+            unsigned in = 0, kept = 0, tie = 0;      // four bits to a quad of the thread's N
 #pragma unroll
-        for (int side = 0; side < 2; ++side) {
-            while (used[side] == have[side] && next[side] < end[side]) {
-                const int first = next[side], last = min(first + kWindow, end[side]);
-                int& before = side == 0 ? tied : tied_behind;
-                // ties are kept while they last: those that are not leave their mark in the list's place
-                if (ties > 0 && before < ties) {
-                    const int n = mark_window(sh, first, last, before, [&](int j) { return rank(j) == threshold; },
-                                              [&](int j, int k) { sh.list[side][j - first] = k < ties; });
-                    have[side] = 0;
-                    unsigned keep = 0;               // bit c: the thread's slot of chunk c is a tie that is kept
-#pragma unroll
-                    for (int c = 0; c < kChunks; ++c) {
-                        const int j = first + c * kEvictThreads + tid;
-                        if (j < last && rank(j) == threshold && sh.list[side][j - first]) keep |= 1u << c;
-                    }
-                    __syncthreads();
-                    have[side] = mark_window(sh, first, last, 0, [&](int j) {
-                        const bool kept = rank(j) > threshold || (keep >> ((j - first) / kEvictThreads) & 1);
-                        if (side == 0 && kept) carry(j);
-                        return kept == (side == 1);
-                    }, [&](int j, int k) { sh.list[side][k] = (uint16_t)(j - first); });
-                    before += n;
-                } else {
-                    have[side] = mark_window(sh, first, last, 0, [&](int j) {
-                        const bool kept = rank(j) > threshold;
-                        if (side == 0 && kept) carry(j);
-                        return kept == (side == 1);
-                    }, [&](int j, int k) { sh.list[side][k] = (uint16_t)(j - first); });
+            for (int i = 0; i < N; ++i) {
+                const int q = q0 + i * T + tid;
+                const unsigned here = within(q, begin, end);
+                if (here) {
+                    const uint4 r = rank(q);
+                    in |= here << 4 * i;
+                    kept |= (above(r) & here) << 4 * i;
+                    tie |= (equal(r) & here) << 4 * i;
                 }
-                base[side] = first;
-                next[side] = last;
-                used[side] = 0;
             }
+            int n[N];
+            if (ties > d.tied) {                     // ties are kept while they last, the lowest slots first
+#pragma unroll
+                for (int i = 0; i < N; ++i) n[i] = __popc(tie >> 4 * i & 15u);
+                const int all = scan_block<T>(n, sh.red2);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    int before = d.tied + n[i];
+#pragma unroll
+                    for (int k = 4 * i; k < 4 * i + 4; ++k)
+                        if (tie >> k & 1) kept |= (unsigned)(before++ < ties) << k;
+                }
+                d.tied += all;
+            }
+            const unsigned mark = holes ? in & ~kept : kept;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (holes) carry(q0 + i * T + tid, kept >> 4 * i & 15u);
+                n[i] = __popc(mark >> 4 * i & 15u);
+            }
+            d.have = scan_block<T>(n, sh.red2);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                for (unsigned m = mark >> 4 * i & 15u, k = n[i]; m; m &= m - 1, ++k)
+                    sh.list[!holes][k] = (uint16_t)(4 * (i * T + tid) + __ffs((int)m) - 1);
+            d.base = d.next;
+            d.used = 0;
+            d.next += kWindow;
         }
-        // every CTA has looked at the slots before next[0] and next[1] (all look at the same ones): they may be written
+    };
+    for (;;) {
+        refill(hole, true, 0, p.b);
+        refill(mover, false, p.b, p.L);
+        // every CTA has looked at the slots before the next windows (all look at the same ones): they may be written
         if (ranks > 1) cluster.sync();
         else __syncthreads();
-        const int n = min(have[0] - used[0], have[1] - used[1]);
+        const int n = min(hole.have - hole.used, mover.have - mover.used);
         if (n == 0) break;                           // (holes and movers end together)
-        const int vecs = 1 << a.vec_shift, mine = ((n - me + ranks - 1) / ranks) << a.vec_shift;
-        for (int e0 = tid; e0 < mine; e0 += 4 * kEvictThreads) {
-            uint4 x[4], y[4];
-            long long to[4];
+        const int in = (1 << a.page_shift) - 1, vecs = 1 << a.vec_shift, mine = ((n - me + ranks - 1) / ranks) << a.vec_shift;
+        constexpr int U = 4;
+        for (int e0 = tid; e0 < mine; e0 += U * T) {
+            uint4 x[U], y[U];
+            long long to[U];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int e = e0 + u * kEvictThreads;
+            for (int u = 0; u < U; ++u) {
+                const int e = e0 + u * T;
                 to[u] = -1;
                 if (e >= mine) continue;
                 const int i = (e >> a.vec_shift) * ranks + me, c = e & (vecs - 1);
-                const int from_j = base[1] + sh.list[1][used[1] + i], to_j = base[0] + sh.list[0][used[0] + i];
+                const int from_j = mover.base + sh.list[1][mover.used + i], to_j = hole.base + sh.list[0][hole.used + i];
                 const int sp = page_of(a, p, from_j), dp = page_of(a, p, to_j);
                 if (sp < 0 || dp < 0) continue;
-                const long long from = page_element(sp, from_j, c);
+                const long long from = sp * a.page_bytes + (((p.h << a.page_shift) + (from_j & in)) * (long long)vecs + c) * 16;
                 x[u] = *reinterpret_cast<const uint4*>(a.k + from);
                 y[u] = *reinterpret_cast<const uint4*>(a.v + from);
-                to[u] = page_element(dp, to_j, c);
+                to[u] = dp * a.page_bytes + (((p.h << a.page_shift) + (to_j & in)) * (long long)vecs + c) * 16;
                 if (c == 0) {
                     const long long se = element_of(a, p, sp, from_j), de = element_of(a, p, dp, to_j);
                     a.scores_out[de] = a.scores[se];
@@ -375,14 +410,14 @@ __global__ void __launch_bounds__(kEvictThreads, 3) paged_evict_kernel(EvictArgs
                 }
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < U; ++u)
                 if (to[u] >= 0) {
                     *reinterpret_cast<uint4*>(a.k + to[u]) = x[u];
                     *reinterpret_cast<uint4*>(a.v + to[u]) = y[u];
                 }
         }
-        used[0] += n;
-        used[1] += n;
+        hole.used += n;
+        mover.used += n;
         __syncthreads();
     }
 }
@@ -509,10 +544,11 @@ int lla_paged_evict(int dtype, const float* scores, float* scores_out, const int
     if ((positions != nullptr) != (positions_out != nullptr))
         return lc::failf(LLA_ERR_INVALID_ARG, "positions and positions_out go together");
     if (!positions && (sinks > 0 || recent > 0)) return lc::failf(LLA_ERR_INVALID_ARG, "sinks and recent need the slots' positions");
-    const void* words[] = {scores, scores_out, positions, positions_out, block_table, kv_lens, keep, dropped};
+    const void* words[] = {block_table, kv_lens, keep, dropped}, *wide[] = {scores, scores_out, positions, positions_out, k_cache, v_cache};
     for (const void* x : words)
-        if (!lc::aligned(x, 4)) return lc::failf(LLA_ERR_INVALID_ARG, "int32 and fp32 pointers must be 4-byte aligned");
-    if (!lc::aligned(k_cache, 16) || !lc::aligned(v_cache, 16)) return lc::failf(LLA_ERR_INVALID_ARG, "caches must be 16-byte aligned");
+        if (!lc::aligned(x, 4)) return lc::failf(LLA_ERR_INVALID_ARG, "lengths and tables must be 4-byte aligned");
+    for (const void* x : wide)
+        if (!lc::aligned(x, 16)) return lc::failf(LLA_ERR_INVALID_ARG, "caches, scores and positions must be 16-byte aligned");
     if (dtype != LLA_DTYPE_BF16 && dtype != LLA_DTYPE_FP32) return lc::failf(LLA_ERR_INVALID_ARG, "unknown dtype %d", dtype);
     if (d != 16 && d != 32 && d != 64 && d != 128)
         return lc::failf(LLA_ERR_INVALID_ARG, "head dim d must be 16, 32, 64 or 128 (got %d)", d);
@@ -529,18 +565,22 @@ int lla_paged_evict(int dtype, const float* scores, float* scores_out, const int
     if (sms < 1) return lc::failf(LLA_ERR_CUDA, "lla_paged_evict: no device");
     unsigned* err = lla::device_error_word();
     if (!err) return lc::failf(LLA_ERR_CUDA, "lla_paged_evict: device error word not found");
+    const long long room = (long long)table_width * page_size;
+    const int held = room < lc::kHeld ? (int)room : lc::kHeld;
     lc::EvictArgs a{scores, scores_out, positions, positions_out, static_cast<char*>(k_cache), static_cast<char*>(v_cache),
                     block_table, kv_lens, keep, dropped, page_stride * es, S, Hkv, table_width, shift, num_pages, lla::paged::log2_up(d * es / 16), sinks,
-                    recent, err};
-    constexpr size_t smem = lc::kHeld * sizeof(uint32_t);
-    cudaError_t e = cudaFuncSetAttribute(lc::paged_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return lc::cuda_failf(e, "lla_paged_evict");
+                    recent, held, err};
+    const size_t smem = (size_t)held * sizeof(uint32_t);
     const long long pairs = (long long)S * Hkv;
+    const bool small = pairs >= 4LL * sms;
+    auto* kern = small ? lc::paged_evict_kernel<128> : lc::paged_evict_kernel<512>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(lc::kHeld * sizeof(uint32_t)));
+    if (e != cudaSuccess) return lc::cuda_failf(e, "lla_paged_evict");
     int ranks = 1;
     while (ranks < 8 && pairs * ranks * 2 <= 2LL * sms) ranks *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(pairs * ranks));
-    cfg.blockDim = dim3(lc::kEvictThreads);
+    cfg.blockDim = dim3(small ? 128 : 512);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream_);
     cudaLaunchAttribute at[2];
@@ -551,7 +591,7 @@ int lla_paged_evict(int dtype, const float* scores, float* scores_out, const int
     at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = ranks > 1 ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, lc::paged_evict_kernel, a);
+    e = cudaLaunchKernelEx(&cfg, kern, a);
     if (e != cudaSuccess) return lc::cuda_failf(e, "lla_paged_evict launch");
     return LLA_OK;
 }

@@ -550,3 +550,14 @@ def test_serving_with_bounded_caches(lla_gpu, dtype, d, Hq, Hkv):
                     assert set(range(min(2, lens[s]))) <= set(mine) and set(range(max(total[s] - 10, 0), total[s])) <= set(mine)
                     for (p, i), x in zip(at, mine):
                         assert torch.equal(kc[p, h, i], seen[l][s][0][x][h]) and torch.equal(vc[p, h, i], seen[l][s][1][x][h])
+
+
+@pytest.mark.parametrize("kind", ["random", "ties", "equal", "odd", "close"])
+def test_evict_of_many_heads(lla_gpu, kind):
+    """Enough (sequence, key head) pairs for the kernel with small blocks: lengths around its windows' borders, and one beyond
+    what it holds in shared memory."""
+    rng = np.random.default_rng(5)
+    kv = [0, 1, 3, 511, 512, 513, 2047, 2048, 2049, 2560, 4097, 10240, 10241, 12000] + list(rng.integers(1, 300, 66))
+    keep = [5, 1, 1, 200, 511, 512, 2046, 1000, 2048, 2049, 4096, 9000, 10240, 11000] + list(rng.integers(0, 200, 66))
+    Evict(kv, keep, 8, 16, 16, "bf16", kind, sinks=2, recent=9).run()
+    Evict(kv[:8] + kv[14:], keep[:8] + keep[14:], 9, 32, 8, "fp32", kind, seed=3).run(positions=False)
