@@ -52,10 +52,10 @@ int sm_count() {
 // Scores become integers of the same order, held in shared memory (those behind kHeld are read again), four neighbouring
 // slots to a thread: they lie on one page.  The threshold is found by histograms of 2048 equal ranges between the lowest and
 // the highest of them, each pass within the range that holds the threshold: two passes for most scores, three at most.  (Two
-// bits a pass took sixteen, and most of 177 us on 64 x 16 heads of 4145 positions.)  Then windows of kWindow slots are
+// bits a pass took sixteen, and most of 177 us on 64 x 16 heads of 4145 positions.)  Then windows of slots are
 // marked with one scan each.
-constexpr int kHeld = 10240;             // scores of a sequence that shared memory holds at most
-constexpr int kBins = 2048, kWindow = 2048;
+constexpr int kHeld = 16384;             // scores of a sequence that shared memory holds at most
+constexpr int kBins = 2048;
 
 struct EvictArgs {
     const float* scores;
@@ -97,7 +97,9 @@ __device__ __forceinline__ long long element_of(const EvictArgs& a, const Pair& 
 // Ranks of slots 4 q .. 4 q + 3: mandatory positions (kMust) above all scores, a slot without a page (1) below all, and behind the
 // last slot 0, which no range begins with.
 constexpr uint32_t kMust = 0xffffffffu;
-__device__ __forceinline__ uint4 ranks_of(const EvictArgs& a, const Pair& p, int q) {
+// Where `copy`, and the results go elsewhere, the scores and positions of slots below b go there on the way: holes' too,
+// which their movers' replace later.
+__device__ __forceinline__ uint4 ranks_of(const EvictArgs& a, const Pair& p, int q, bool copy = false) {
     uint32_t r[4] = {0, 0, 0, 0};
     const int j = 4 * q, page = page_of(a, p, j);
     if (page < 0) atomicOr(a.err, (unsigned)kDevErrPagedArg);
@@ -107,6 +109,20 @@ __device__ __forceinline__ uint4 ranks_of(const EvictArgs& a, const Pair& p, int
     int4 at = make_int4(0, 0, 0, 0);
     if (a.positions) at = *reinterpret_cast<const int4*>(a.positions + e);
     const int w[4] = {at.x, at.y, at.z, at.w};
+    if (copy && page >= 0 && j < p.b) {
+        const bool out = a.scores_out != a.scores, pos_out = a.positions && a.positions_out != a.positions;
+        if (j + 4 <= p.b) {
+            if (out) *reinterpret_cast<float4*>(a.scores_out + e) = x;
+            if (pos_out) *reinterpret_cast<int4*>(a.positions_out + e) = at;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 3; ++i)
+                if (j + i < p.b) {
+                    if (out) a.scores_out[e + i] = s[i];
+                    if (pos_out) a.positions_out[e + i] = w[i];
+                }
+        }
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (j + i < p.L) r[i] = page < 0 ? 1u : a.positions && (w[i] < a.sinks || w[i] >= p.newest - a.recent) ? kMust : order_of(s[i]);
@@ -148,24 +164,27 @@ __device__ __forceinline__ int scan_block(int (&x)[N], int* sh) {
     return all;
 }
 
+template <int WINDOW>
 struct EvictShared {
     int red[16];
     uint32_t low[16], high[16];
     union {
         unsigned bins[kBins];
-        uint16_t list[2][kWindow];           // holes and movers, from their windows' first slots on
+        uint16_t list[2][WINDOW];           // holes and movers, from their windows' first slots on
     };
-    int red2[64];
+    int red2[4 * 16];
     int found[3];                            // bin, what it has, what is still needed of it
 };
 
-// T threads: 512, or 128 where there are pairs enough to fill the device with such blocks.  Each step waits for the one
-// before, so many small blocks side by side hide what few large ones cannot.
+// T threads: 512, or 256 where there are pairs enough to fill the device with such blocks: each step waits for the one before,
+// and more blocks side by side hide that (us; 96 x 8 heads of 4145 positions 47 and 36, of 1000 to 4000 cut to 1000, where rows
+// that move count most, 114 and 123; 128 threads 40 and 152; 16 x 8 heads of 4145 14 and 18).
 template <int T>
-__global__ void __launch_bounds__(T, T == 128 ? 8 : 2) paged_evict_kernel(EvictArgs a) {
+__global__ void __launch_bounds__(T, 1024 / T) paged_evict_kernel(EvictArgs a) {
+    constexpr int kWindow = T == 512 ? 8192 : 2048;
     constexpr int W = T / 32, N = kWindow / 4 / T;             // warps; quads of a window that a thread has
     extern __shared__ uint4 held[];                  // a.held / 4 of ranks_of
-    __shared__ EvictShared sh;
+    __shared__ EvictShared<kWindow> sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int ranks = (int)cluster.num_blocks(), me = (int)cluster.block_rank();         // a power of two of CTAs
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -181,36 +200,9 @@ __global__ void __launch_bounds__(T, T == 128 ? 8 : 2) paged_evict_kernel(EvictA
     p.b = min(p.L, max(a.keep[p.s], 0));
     p.newest = p.L + (a.dropped ? a.dropped[p.s] : 0);
     const int quads = (p.L + 3) >> 2, held4 = a.held >> 2;
-    const bool out = a.scores_out != a.scores, pos_out = a.positions && a.positions_out != a.positions;
-    // kept slots (bits of `kept`) of quad q that stay, where the results go elsewhere
-    auto carry = [&](int q, unsigned kept) {
-        if ((!out && !pos_out) || !kept || (q & (ranks - 1)) != me) return;
-        const int page = page_of(a, p, 4 * q);
-        if (page < 0) return;
-        const long long e = element_of(a, p, page, 4 * q);
-        if (out) {
-            const float4 x = *reinterpret_cast<const float4*>(a.scores + e);
-            if (kept == 15u) *reinterpret_cast<float4*>(a.scores_out + e) = x;
-            else {
-                if (kept & 1) a.scores_out[e] = x.x;
-                if (kept & 2) a.scores_out[e + 1] = x.y;
-                if (kept & 4) a.scores_out[e + 2] = x.z;
-                if (kept & 8) a.scores_out[e + 3] = x.w;
-            }
-        }
-        if (pos_out) {
-            const int4 x = *reinterpret_cast<const int4*>(a.positions + e);
-            if (kept == 15u) *reinterpret_cast<int4*>(a.positions_out + e) = x;
-            else {
-                if (kept & 1) a.positions_out[e] = x.x;
-                if (kept & 2) a.positions_out[e + 1] = x.y;
-                if (kept & 4) a.positions_out[e + 2] = x.z;
-                if (kept & 8) a.positions_out[e + 3] = x.w;
-            }
-        }
-    };
-    if (p.b == p.L) {
-        for (int q = tid; q < quads; q += T) carry(q, p.L - 4 * q >= 4 ? 15u : (1u << (p.L - 4 * q)) - 1);
+    if (p.b == p.L) {                                // nothing leaves
+        if (a.scores_out != a.scores || a.positions_out != a.positions)
+            for (int q = tid; q < quads; q += T) ranks_of(a, p, q, (q & (ranks - 1)) == me);
         return;
     }
     if (p.b == 0) return;
@@ -218,9 +210,9 @@ __global__ void __launch_bounds__(T, T == 128 ? 8 : 2) paged_evict_kernel(EvictA
     // ranks, the lowest and highest of those that are not mandatory, and how many are
     uint32_t lo = kMust, hi = 0;
     int need = 0;
-#pragma unroll 2
+#pragma unroll 4
     for (int q = tid; q < quads; q += T) {
-        const uint4 r = ranks_of(a, p, q);
+        const uint4 r = ranks_of(a, p, q, (q & (ranks - 1)) == me);
         if (q < held4) held[q] = r;
         const uint32_t x[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -364,7 +356,6 @@ __global__ void __launch_bounds__(T, T == 128 ? 8 : 2) paged_evict_kernel(EvictA
             const unsigned mark = holes ? in & ~kept : kept;
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                if (holes) carry(q0 + i * T + tid, kept >> 4 * i & 15u);
                 n[i] = __popc(mark >> 4 * i & 15u);
             }
             d.have = scan_block<T>(n, sh.red2);
@@ -573,14 +564,14 @@ int lla_paged_evict(int dtype, const float* scores, float* scores_out, const int
     const size_t smem = (size_t)held * sizeof(uint32_t);
     const long long pairs = (long long)S * Hkv;
     const bool small = pairs >= 4LL * sms;
-    auto* kern = small ? lc::paged_evict_kernel<128> : lc::paged_evict_kernel<512>;
+    auto* kern = small ? lc::paged_evict_kernel<256> : lc::paged_evict_kernel<512>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(lc::kHeld * sizeof(uint32_t)));
     if (e != cudaSuccess) return lc::cuda_failf(e, "lla_paged_evict");
     int ranks = 1;
     while (ranks < 8 && pairs * ranks * 2 <= 2LL * sms) ranks *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(pairs * ranks));
-    cfg.blockDim = dim3(small ? 128 : 512);
+    cfg.blockDim = dim3(small ? 256 : 512);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = static_cast<cudaStream_t>(stream_);
     cudaLaunchAttribute at[2];
