@@ -646,6 +646,9 @@ def _bind():
             m.init(*(ctypes.cast(f, ctypes.c_void_p).value for f in (lib.lla_paged_plan, lib.lla_paged_append,
                                                                       lib.lla_paged_parallax_ex)),
                    torch.bfloat16, torch.float32, torch.int32, torch.int64)
+            m.init_bounded(*(ctypes.cast(f, ctypes.c_void_p).value for f in (lib.lla_rotary, lib.lla_rotary_backward,
+                                                                              lib.lla_paged_weigh, lib.lla_paged_evict,
+                                                                              lib.lla_paged_trim)))
             _BIND = m
     return _BIND
 
@@ -1018,6 +1021,13 @@ def rotary(x, positions, table, *, gain=None, eps=None, interleaved=False, cu_q=
     Returns the rotated tensor, or a tuple where x is a sequence.  Asynchronous on the current (or given) stream.
     """
     import torch
+    many = isinstance(x, (tuple, list))
+    if stream is None and out is None and isinstance(table, RotaryTable) and table.turns.is_cuda and _bind():
+        index, empty = torch.cuda.current_device(), torch.empty
+        res = tuple([empty(t.shape, dtype=t.dtype, device=t.device) for t in x]) if many else empty(x.shape, dtype=x.dtype, device=x.device)
+        if _BIND.rotary(index, x, positions, table.turns, table.dim, table.magnitude, gain, eps, interleaved, cu_q, shift, res,
+                        torch._C._cuda_getCurrentRawStream(index)) == LLA_OK:
+            return res
     first = _listed(x)[0]
     if first.is_cuda and (stream is not None or first.device.index != torch.cuda.current_device()):
         with _on_stream(first.device, stream):
@@ -1026,7 +1036,7 @@ def rotary(x, positions, table, *, gain=None, eps=None, interleaved=False, cu_q=
         _rotary_call(x, None, positions, table, gain, eps, cu_q, shift, out, False)
     lla_rotary(dtype, rows, count, B, n, d, pos, ps, turns, rot, 1 if interleaved else 0, m, e, cu, sh, S,
                torch._C._cuda_getCurrentRawStream(first.device.index))
-    return tuple(outs) if isinstance(x, (tuple, list)) else outs[0]
+    return tuple(outs) if many else outs[0]
 
 
 def rotary_backward(dy, x, positions, table, *, gain=None, eps=None, interleaved=False, cu_q=None, shift=None, dx=None,
@@ -1040,6 +1050,27 @@ def rotary_backward(dy, x, positions, table, *, gain=None, eps=None, interleaved
     import torch
     if x is None and eps is not None:
         raise _bad("x is needed where the rows were normalised (eps)")
+    many = isinstance(dy, (tuple, list))
+    if stream is None and dx is None and workspace is None and isinstance(table, RotaryTable) and table.turns.is_cuda and _bind():
+        index, empty = torch.cuda.current_device(), torch.empty
+        stream_ptr = torch._C._cuda_getCurrentRawStream(index)
+        t = _SCRATCH.get((index, stream_ptr, threading.get_ident()))
+        if gain is None or (t is not None and not torch.cuda.is_current_stream_capturing()):
+            like = dy if x is None else x
+            res = tuple([empty(r.shape, dtype=r.dtype, device=r.device) for r in like]) if many else \
+                empty(like.shape, dtype=like.dtype, device=like.device)
+            grads = None if gain is None else torch.empty_like(gain) if torch.is_tensor(gain) else \
+                tuple([None if g is None else torch.empty_like(g) for g in gain])
+            if _BIND.rotary_backward(index, dy, x, positions, table.turns, table.dim, table.magnitude, gain, eps, interleaved, cu_q,
+                                     shift, res, grads, 0 if t is None else t.data_ptr(), 0 if t is None else t.numel(),
+                                     stream_ptr) == LLA_OK:
+                if grads is not None and not many:
+                    grads = grads[0] if isinstance(grads, tuple) else grads
+                elif grads is not None and not isinstance(grads, tuple):
+                    grads = (grads,)
+                if isinstance(grads, tuple) and all(g is None for g in grads):
+                    grads = None
+                return res, grads
     first = _listed(dy)[0]
     if first.is_cuda and (stream is not None or first.device.index != torch.cuda.current_device()):
         with _on_stream(first.device, stream):
@@ -1062,7 +1093,6 @@ def rotary_backward(dy, x, positions, table, *, gain=None, eps=None, interleaved
         ws_ptr, ws_bytes = workspace.data_ptr(), workspace.numel()
     lla_rotary_backward(dtype, dy_dtype, rows, count, B, n, d, pos, ps, turns, rot, 1 if interleaved else 0, m, e, cu, sh, S,
                         ws_ptr, ws_bytes, stream_ptr)
-    many = isinstance(dy, (tuple, list))
     dgain = None if all(g is None for g in dgains) else tuple(dgains) if many else dgains[0]
     return (tuple(outs) if many else outs[0]), dgain
 
@@ -1120,6 +1150,15 @@ def paged_weigh(q, lse, k_cache, scores, block_table, cu_q, kv_lens, tau, max_ne
     Asynchronous on the current (or given) stream.  workspace: as for paged_parallax.
     """
     import torch
+    if stream is None and workspace is None and k_cache.is_cuda and _bind():
+        index = torch.cuda.current_device()
+        stream_ptr = torch._C._cuda_getCurrentRawStream(index)
+        t = _SCRATCH.get((index, stream_ptr, threading.get_ident()))
+        if t is not None and not torch.cuda.is_current_stream_capturing():
+            res = scores if out is None else out
+            if _BIND.weigh(index, q, lse, k_cache, scores, res, positions, dropped, block_table, cu_q, kv_lens, tau, max_new, decay,
+                           last, causal, t.data_ptr(), t.numel(), stream_ptr) == LLA_OK:
+                return res
     P, Hkv, Z, d, page_stride, dtype = _check_cache(k_cache)
     dev = k_cache.device
     if stream is not None or dev.index != torch.cuda.current_device():
@@ -1164,6 +1203,12 @@ def paged_evict(scores, k_cache, v_cache, block_table, kv_lens, keep, *, positio
     Asynchronous on the current (or given) stream.
     """
     import torch
+    if stream is None and k_cache.is_cuda and _bind():
+        index = torch.cuda.current_device()
+        if _BIND.evict(index, scores, scores if scores_out is None else scores_out, positions,
+                       positions if positions_out is None else positions_out, k_cache, v_cache, block_table, kv_lens, keep, dropped,
+                       sinks, recent, torch._C._cuda_getCurrentRawStream(index)) == LLA_OK:
+            return
     P, Hkv, Z, d, page_stride, dtype = _check_caches(k_cache, v_cache)
     dev = k_cache.device
     if stream is not None or dev.index != torch.cuda.current_device():
@@ -1204,6 +1249,13 @@ def paged_trim(kv_lens, keep, block_table, free_pages, free_count, page_size, *,
         with _on_stream(dev, stream):
             return paged_trim(kv_lens, keep, block_table, free_pages, free_count, page_size, dropped=dropped, new_lens=new_lens,
                               new_dropped=new_dropped, free_left=free_left)
+    if _bind():
+        like = torch.empty_like
+        r = PagedTrim(like(kv_lens) if new_lens is None else new_lens, like(kv_lens) if new_dropped is None else new_dropped,
+                      like(free_count) if free_left is None else free_left)
+        if _BIND.trim(dev.index, kv_lens, keep, block_table, free_pages, free_count, page_size, dropped, r[0], r[1], r[2],
+                      torch._C._cuda_getCurrentRawStream(dev.index)) == LLA_OK:
+            return r
     if block_table.dim() != 2:
         raise _bad("block_table must be [S, W]")
     S, W = block_table.shape

@@ -8,6 +8,7 @@
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <stdint.h>
+#include <string.h>
 
 typedef int (*plan_fn)(const void*, const void*, int, int, void*, int, const void*, int, const void*, int, void*, void*,
                        void*, void*, void*, void*, void*);
@@ -226,7 +227,317 @@ static PyObject* init(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     Py_RETURN_NONE;
 }
 
+/* ------------------------------------------------- rotary positions and bounded caches (include/lla.h)
+ * The entry points' arguments are written out once more here, as above. */
+typedef struct {
+    const void* x;
+    const void* dy;
+    void* out;
+    const void* gain;
+    void* dgain;
+    long long x_stride[3], dy_stride[3], out_stride[3];
+    int heads;
+} rotary_rows;
+enum { kRotaryMost = 4 };
+typedef int (*rotary_fn)(int, const rotary_rows*, int, int, int, int, const void*, long long, const void*, int, int, float, float,
+                         const void*, const void*, int, void*);
+typedef int (*rotary_backward_fn)(int, int, const rotary_rows*, int, int, int, int, const void*, long long, const void*, int, int,
+                                  float, float, const void*, const void*, int, void*, size_t, void*);
+typedef int (*weigh_fn)(int, const void*, const void*, const void*, const void*, void*, void*, const void*, const void*, const void*,
+                        const void*, int, int, int, int, int, int, int, int, int, long long, long long, float, float, int, int, void*,
+                        size_t, void*);
+typedef int (*evict_fn)(int, const void*, void*, const void*, void*, void*, void*, const void*, const void*, const void*, const void*,
+                        int, int, int, int, int, int, long long, int, int, void*);
+typedef int (*trim_fn)(const void*, const void*, int, int, const void*, int, void*, int, const void*, const void*, void*, void*, void*,
+                       void*);
+static rotary_fn f_rotary;
+static rotary_backward_fn f_rotary_backward;
+static weigh_fn f_weigh;
+static evict_fn f_evict;
+static trim_fn f_trim;
+
+/* Item i of a tuple or list of `count`, or the object itself where it stands for one; NULL where there is none. */
+static PyObject* item(PyObject* obj, Py_ssize_t i, Py_ssize_t count) {
+    if (PyTuple_Check(obj)) return PyTuple_GET_SIZE(obj) == count ? PyTuple_GET_ITEM(obj, i) : NULL;
+    if (PyList_Check(obj)) return PyList_GET_SIZE(obj) == count ? PyList_GET_ITEM(obj, i) : NULL;
+    return count == 1 ? obj : NULL;
+}
+/* A contiguous tensor of n elements in `dim` dimensions. */
+static int packed(PyObject* obj, PyObject* dtype, long device, const long long* shape, long dim, Tensor* t) {
+    long long step = 1;
+    if (!read_tensor(obj, t) || t->dtype != dtype || t->device != device || t->dim != dim) return 0;
+    for (long i = dim - 1; i >= 0; --i) {
+        if (t->shape[i] != shape[i] || (t->stride[i] != step && t->shape[i] > 1)) return 0;
+        step *= t->shape[i];
+    }
+    return 1;
+}
+/* [T, heads, d] or [B, heads, n, d] rows, 16-byte aligned and strided; their strides of batch, head and position. */
+static int head_rows(PyObject* obj, PyObject* dtype, long device, const Tensor* like, Tensor* t, long long* stride) {
+    const int ve = dtype == t_bf16 ? 8 : 4;
+    if (!read_tensor(obj, t) || t->dtype != dtype || t->device != device || t->dim != like->dim || t->ptr % 16) return 0;
+    for (long i = 0; i < t->dim; ++i)
+        if (t->shape[i] != like->shape[i] || (i + 1 < t->dim ? t->stride[i] % ve != 0 : t->stride[i] != 1)) return 0;
+    stride[0] = t->dim == 4 ? t->stride[0] : 0;
+    stride[1] = t->stride[1];
+    stride[2] = t->dim == 4 ? t->stride[2] : t->stride[0];
+    return 1;
+}
+
+typedef struct {
+    rotary_rows rows[kRotaryMost];
+    int dtype, dy_dtype, count, B, n, d, S;
+    long long position_stride;
+    uintptr_t positions, turns, cu, shift;
+} Rotary;
+
+/* What both directions take: x (or None), dy (or None in the forward pass), positions, turns, rot, gains, eps given, cu_q, shift, out. */
+static int rotary_args(Rotary* r, long device, PyObject* x, PyObject* dy, PyObject* positions, PyObject* turns, long rot, PyObject* gains,
+                       int normalise, PyObject* cu, PyObject* shift, PyObject* out) {
+    Tensor first, t, p;
+    PyObject* like = x != Py_None ? x : dy;
+    const Py_ssize_t count = PyTuple_Check(like) ? PyTuple_GET_SIZE(like) : PyList_Check(like) ? PyList_GET_SIZE(like) : 1;
+    if (count < 1 || count > kRotaryMost || !item(like, 0, count) || !read_tensor(item(like, 0, count), &first) || first.device != device ||
+        first.device < 0 || (first.dim != 3 && first.dim != 4))
+        return 0;
+    PyObject* dtype = first.dtype;
+    PyObject* dy_dtype = dtype;
+    if (dtype != t_bf16 && dtype != t_fp32) return 0;
+    if (dy != Py_None) {
+        if (!item(dy, 0, count) || !read_tensor(item(dy, 0, count), &t)) return 0;
+        dy_dtype = t.dtype;
+        if (dy_dtype != dtype && dy_dtype != t_fp32) return 0;
+    }
+    const int flat = first.dim == 3;
+    const long long B = flat ? 1 : first.shape[0], n = flat ? first.shape[0] : first.shape[2], d = first.shape[first.dim - 1];
+    if (!fits(B) || !fits(n) || !fits(d)) return 0;
+    memset(r, 0, sizeof *r);
+    for (Py_ssize_t i = 0; i < count; ++i) {
+        rotary_rows* o = &r->rows[i];
+        Tensor l;
+        PyObject* obj = item(like, i, count);
+        if (!obj || !read_tensor(obj, &l) || l.dim != first.dim || l.dtype != dtype || l.shape[l.dim - 1] != d ||
+            (flat ? l.shape[0] != n : l.shape[0] != B || l.shape[2] != n) || !fits(l.shape[1]))
+            return 0;
+        o->heads = (int)l.shape[1];
+        if (x != Py_None) {
+            if (!head_rows(obj, dtype, device, &l, &t, o->x_stride)) return 0;
+            o->x = P(t.ptr);
+        }
+        if (dy != Py_None) {
+            if (!item(dy, i, count) || !head_rows(item(dy, i, count), dy_dtype, device, &l, &t, o->dy_stride)) return 0;
+            o->dy = P(t.ptr);
+        }
+        if (!item(out, i, count) || !head_rows(item(out, i, count), dtype, device, &l, &t, o->out_stride)) return 0;
+        o->out = P(t.ptr);
+        if (gains != Py_None) {
+            PyObject* g = item(gains, i, count);
+            if (!g) return 0;
+            if (g != Py_None) {
+                if (!normalise || !vector(g, t_fp32, device, d, &t)) return 0;
+                o->gain = P(t.ptr);
+            }
+        }
+    }
+    const long long both[2] = {B, n};
+    if (vector(positions, t_i32, device, n, &p)) r->position_stride = 0;
+    else if (!flat && packed(positions, t_i32, device, both, 2, &p)) r->position_stride = n;
+    else return 0;
+    r->positions = p.ptr;
+    if (!vector(turns, t_i64, device, rot / 2, &t)) return 0;
+    r->turns = t.ptr;
+    if ((cu == Py_None) != (shift == Py_None)) return 0;
+    if (cu != Py_None) {
+        if (!flat || !vector(shift, t_i32, device, -1, &t) || !fits(t.shape[0])) return 0;
+        r->shift = t.ptr;
+        r->S = (int)t.shape[0];
+        if (!vector(cu, t_i32, device, r->S + 1, &t)) return 0;
+        r->cu = t.ptr;
+    }
+    r->dtype = dtype == t_bf16 ? 0 : 1;
+    r->dy_dtype = dy_dtype == t_bf16 ? 0 : 1;
+    r->count = (int)count;
+    r->B = (int)B;
+    r->n = (int)n;
+    r->d = (int)d;
+    return 1;
+}
+
+/* rotary(device, x, positions, turns, rot, magnitude, gains, eps, interleaved, cu_q, shift, out, stream); eps None: no normalisation */
+static PyObject* rotary(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    Rotary r;
+    int status = -1;
+    (void)self;
+    if (n != 13) return PyLong_FromLong(-1);
+    const long device = PyLong_AsLong(a[0]), rot = PyLong_AsLong(a[4]);
+    const double magnitude = PyFloat_AsDouble(a[5]), eps = a[7] == Py_None ? -1.0 : PyFloat_AsDouble(a[7]);
+    const int interleaved = PyObject_IsTrue(a[8]);
+    const uintptr_t stream = (uintptr_t)PyLong_AsUnsignedLongLong(a[12]);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        return PyLong_FromLong(-1);
+    }
+    if (rotary_args(&r, device, a[1], Py_None, a[2], a[3], rot, a[6], eps >= 0.0, a[9], a[10], a[11]) && (a[7] == Py_None || eps >= 0.0)) {
+        Py_BEGIN_ALLOW_THREADS
+        status = f_rotary(r.dtype, r.rows, r.count, r.B, r.n, r.d, P(r.positions), r.position_stride, P(r.turns), (int)rot, interleaved,
+                          (float)magnitude, (float)eps, P(r.cu), P(r.shift), r.S, P(stream));
+        Py_END_ALLOW_THREADS
+    }
+    return PyLong_FromLong(status);
+}
+
+/* rotary_backward(device, dy, x, positions, turns, rot, magnitude, gains, eps, interleaved, cu_q, shift, dx, dgains, workspace,
+ * workspace bytes, stream) */
+static PyObject* rotary_backward(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    Rotary r;
+    int status = -1;
+    (void)self;
+    if (n != 17) return PyLong_FromLong(-1);
+    const long device = PyLong_AsLong(a[0]), rot = PyLong_AsLong(a[5]);
+    const double magnitude = PyFloat_AsDouble(a[6]), eps = a[8] == Py_None ? -1.0 : PyFloat_AsDouble(a[8]);
+    const int interleaved = PyObject_IsTrue(a[9]);
+    const uintptr_t ws = (uintptr_t)PyLong_AsUnsignedLongLong(a[14]), stream = (uintptr_t)PyLong_AsUnsignedLongLong(a[16]);
+    const size_t ws_bytes = PyLong_AsSize_t(a[15]);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        return PyLong_FromLong(-1);
+    }
+    if (!rotary_args(&r, device, a[2], a[1], a[3], a[4], rot, a[7], eps >= 0.0, a[10], a[11], a[12]) || (a[8] != Py_None && eps < 0.0))
+        return PyLong_FromLong(-1);
+    for (int i = 0; i < r.count; ++i) {
+        if (!r.rows[i].gain) continue;
+        Tensor t;
+        PyObject* g = item(a[13], i, r.count);
+        if (!g || !vector(g, t_fp32, device, r.d, &t)) return PyLong_FromLong(-1);
+        r.rows[i].dgain = P(t.ptr);
+    }
+    Py_BEGIN_ALLOW_THREADS
+    status = f_rotary_backward(r.dtype, r.dy_dtype, r.rows, r.count, r.B, r.n, r.d, P(r.positions), r.position_stride, P(r.turns), (int)rot,
+                               interleaved, (float)magnitude, (float)eps, P(r.cu), P(r.shift), r.S, P(ws), ws_bytes, P(stream));
+    Py_END_ALLOW_THREADS
+    return PyLong_FromLong(status);
+}
+
+/* weigh(device, q, lse, k_cache, scores, out, positions or None, dropped or None, table, cu_q, kv_lens, tau, max_new, decay, last,
+ * causal, workspace, workspace bytes, stream) */
+static PyObject* weigh(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    Tensor q, lse, kc, vc, sc, so, pos, drop, table, cu, kv;
+    long long qs, ps;
+    int status = -1;
+    (void)self;
+    if (n != 19) return PyLong_FromLong(-1);
+    const long device = PyLong_AsLong(a[0]);
+    const double tau = PyFloat_AsDouble(a[11]), decay = PyFloat_AsDouble(a[13]);
+    const long long max_new = PyLong_AsLongLong(a[12]), last = PyLong_AsLongLong(a[14]);
+    const int causal = PyObject_IsTrue(a[15]);
+    const uintptr_t ws = (uintptr_t)PyLong_AsUnsignedLongLong(a[16]), stream = (uintptr_t)PyLong_AsUnsignedLongLong(a[18]);
+    const size_t ws_bytes = PyLong_AsSize_t(a[17]);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        return PyLong_FromLong(-1);
+    }
+    if (!caches(a[3], a[3], &kc, &vc, &ps) || kc.device != device || !read_tensor(a[1], &q) || q.dim != 3 || !rows(a[1], &kc, q.shape[1], &q, &qs) ||
+        !packed(a[2], t_fp32, device, q.shape, 2, &lse) || !packed(a[4], t_fp32, device, kc.shape, 3, &sc) ||
+        !packed(a[5], t_fp32, device, kc.shape, 3, &so) || !vector(a[10], t_i32, device, -1, &kv))
+        return PyLong_FromLong(-1);
+    const long long S = kv.shape[0];
+    pos.ptr = drop.ptr = 0;
+    if ((a[6] == Py_None || packed(a[6], t_i32, device, kc.shape, 3, &pos)) && (a[7] == Py_None || vector(a[7], t_i32, device, S, &drop)) &&
+        vector(a[9], t_i32, device, S + 1, &cu) && matrix(a[8], t_i32, device, S, &table) && fits(q.shape[0]) && fits(q.shape[1]) && fits(S) &&
+        fits(table.shape[1]) && fits(kc.shape[0]) && fits(kc.shape[1]) && fits(kc.shape[2]) && fits(max_new) && fits(last)) {
+        Py_BEGIN_ALLOW_THREADS
+        status = f_weigh(kc.dtype == t_bf16 ? 0 : 1, P(q.ptr), P(lse.ptr), P(kc.ptr), P(sc.ptr), P(so.ptr), P(pos.ptr), P(drop.ptr), P(table.ptr),
+                         P(cu.ptr), P(kv.ptr), (int)q.shape[0], (int)S, (int)q.shape[1], (int)kc.shape[1], (int)kc.shape[3], (int)kc.shape[2],
+                         (int)kc.shape[0], (int)table.shape[1], (int)max_new, qs, ps, (float)tau, (float)decay, (int)last, causal, P(ws),
+                         ws_bytes, P(stream));
+        Py_END_ALLOW_THREADS
+    }
+    return PyLong_FromLong(status);
+}
+
+/* evict(device, scores, scores_out, positions or None, positions_out or None, k_cache, v_cache, table, kv_lens, keep, dropped or None,
+ * sinks, recent, stream) */
+static PyObject* evict(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    Tensor sc, so, pos, po, kc, vc, table, kv, keep, drop;
+    long long ps;
+    int status = -1;
+    (void)self;
+    if (n != 14) return PyLong_FromLong(-1);
+    const long device = PyLong_AsLong(a[0]);
+    const long long sinks = PyLong_AsLongLong(a[11]), recent = PyLong_AsLongLong(a[12]);
+    const uintptr_t stream = (uintptr_t)PyLong_AsUnsignedLongLong(a[13]);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        return PyLong_FromLong(-1);
+    }
+    if (!caches(a[5], a[6], &kc, &vc, &ps) || kc.device != device || !vector(a[8], t_i32, device, -1, &kv)) return PyLong_FromLong(-1);
+    const long long S = kv.shape[0];
+    pos.ptr = po.ptr = drop.ptr = 0;
+    if (packed(a[1], t_fp32, device, kc.shape, 3, &sc) && packed(a[2], t_fp32, device, kc.shape, 3, &so) &&
+        (a[3] == Py_None || packed(a[3], t_i32, device, kc.shape, 3, &pos)) && (a[4] == Py_None || packed(a[4], t_i32, device, kc.shape, 3, &po)) &&
+        matrix(a[7], t_i32, device, S, &table) && vector(a[9], t_i32, device, S, &keep) &&
+        (a[10] == Py_None || vector(a[10], t_i32, device, S, &drop)) && fits(S) && fits(table.shape[1]) && fits(kc.shape[0]) &&
+        fits(kc.shape[1]) && fits(kc.shape[2]) && fits(sinks) && fits(recent)) {
+        Py_BEGIN_ALLOW_THREADS
+        status = f_evict(kc.dtype == t_bf16 ? 0 : 1, P(sc.ptr), P(so.ptr), P(pos.ptr), P(po.ptr), P(kc.ptr), P(vc.ptr), P(table.ptr), P(kv.ptr),
+                         P(keep.ptr), P(drop.ptr), (int)S, (int)kc.shape[1], (int)kc.shape[3], (int)kc.shape[2], (int)kc.shape[0],
+                         (int)table.shape[1], ps, (int)sinks, (int)recent, P(stream));
+        Py_END_ALLOW_THREADS
+    }
+    return PyLong_FromLong(status);
+}
+
+/* trim(device, kv_lens, keep, table, free, count, page, dropped or None, new_lens, new_dropped, left, stream) */
+static PyObject* trim(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    Tensor kv, keep, table, pages, count, drop, nl, nd, left;
+    int status = -1;
+    (void)self;
+    if (n != 12) return PyLong_FromLong(-1);
+    const long device = PyLong_AsLong(a[0]);
+    const long long page = PyLong_AsLongLong(a[6]);
+    const uintptr_t stream = (uintptr_t)PyLong_AsUnsignedLongLong(a[11]);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        return PyLong_FromLong(-1);
+    }
+    if (device < 0 || !vector(a[1], t_i32, device, -1, &kv)) return PyLong_FromLong(-1);
+    const long long S = kv.shape[0];
+    drop.ptr = 0;
+    if (vector(a[2], t_i32, device, S, &keep) && matrix(a[3], t_i32, device, S, &table) && vector(a[4], t_i32, device, -1, &pages) &&
+        vector(a[5], t_i32, device, 1, &count) && (a[7] == Py_None || vector(a[7], t_i32, device, S, &drop)) &&
+        vector(a[8], t_i32, device, S, &nl) && vector(a[9], t_i32, device, S, &nd) && vector(a[10], t_i32, device, 1, &left) && fits(S) &&
+        fits(table.shape[1]) && fits(pages.shape[0]) && fits(page)) {
+        Py_BEGIN_ALLOW_THREADS
+        status = f_trim(P(kv.ptr), P(keep.ptr), (int)S, (int)page, P(table.ptr), (int)table.shape[1], P(pages.ptr), (int)pages.shape[0],
+                        P(count.ptr), P(drop.ptr), P(nl.ptr), P(nd.ptr), P(left.ptr), P(stream));
+        Py_END_ALLOW_THREADS
+    }
+    return PyLong_FromLong(status);
+}
+
+/* init_bounded(rotary, rotary_backward, weigh, evict, trim addresses), after init */
+static PyObject* init_bounded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    if (n != 5) {
+        PyErr_SetString(PyExc_TypeError, "init_bounded takes five addresses");
+        return NULL;
+    }
+    f_rotary = (rotary_fn)(uintptr_t)PyLong_AsUnsignedLongLong(a[0]);
+    f_rotary_backward = (rotary_backward_fn)(uintptr_t)PyLong_AsUnsignedLongLong(a[1]);
+    f_weigh = (weigh_fn)(uintptr_t)PyLong_AsUnsignedLongLong(a[2]);
+    f_evict = (evict_fn)(uintptr_t)PyLong_AsUnsignedLongLong(a[3]);
+    f_trim = (trim_fn)(uintptr_t)PyLong_AsUnsignedLongLong(a[4]);
+    if (PyErr_Occurred()) return NULL;
+    Py_RETURN_NONE;
+}
+
 static PyMethodDef methods[] = {
+    {"rotary", (PyCFunction)(void (*)(void))rotary, METH_FASTCALL, NULL},
+    {"rotary_backward", (PyCFunction)(void (*)(void))rotary_backward, METH_FASTCALL, NULL},
+    {"weigh", (PyCFunction)(void (*)(void))weigh, METH_FASTCALL, NULL},
+    {"evict", (PyCFunction)(void (*)(void))evict, METH_FASTCALL, NULL},
+    {"trim", (PyCFunction)(void (*)(void))trim, METH_FASTCALL, NULL},
+    {"init_bounded", (PyCFunction)(void (*)(void))init_bounded, METH_FASTCALL, NULL},
     {"init", (PyCFunction)(void (*)(void))init, METH_FASTCALL, NULL},
     {"plan", (PyCFunction)(void (*)(void))plan, METH_FASTCALL, NULL},
     {"append", (PyCFunction)(void (*)(void))append, METH_FASTCALL, NULL},

@@ -561,3 +561,22 @@ def test_evict_of_many_heads(lla_gpu, kind):
     keep = [5, 1, 1, 200, 511, 512, 2046, 1000, 2048, 2049, 4096, 9000, 10240, 11000] + list(rng.integers(0, 200, 66))
     Evict(kv, keep, 8, 16, 16, "bf16", kind, sinks=2, recent=9).run()
     Evict(kv[:8] + kv[14:], keep[:8] + keep[14:], 9, 32, 8, "fp32", kind, seed=3).run(positions=False)
+
+
+def test_both_ways_of_marshalling_give_the_same_bits(lla_gpu, monkeypatch):
+    def calls():
+        w = Weigh(Case([3, 40], [90, 300], 4, 2, 64, 16))
+        w.run()
+        a = w.run(decay=0.5, last=2)
+        e = Evict([300, 40], [100, 9], 2, 64, 16, "bf16", "ties", 2, 9)
+        e.run(interleaved=True)
+        e.sinks = e.recent = 0
+        e.run(positions=False)
+        f = _i32([0] * 20)
+        t = lla.paged_trim(_i32([40, 90]), _i32([10, 0]), _i32([[1, 2, 3, 4, 5, 6]] * 2), f, _i32([3]), 16)
+        return a, f, *t
+
+    fast = calls()
+    monkeypatch.setattr(lla, "_BIND", False)
+    for a, b in zip(fast, calls()):
+        assert torch.equal(a, b)

@@ -255,3 +255,34 @@ def test_binding_refusals(lla_gpu):
             pytest.fail(f"call {i} was not refused")
     torch.cuda.synchronize()
     lla.lla_sync_status()
+
+
+def test_both_ways_of_marshalling_give_the_same_bits(lla_gpu, monkeypatch):
+    T, d = 33, 64
+    fused = make((T, 9 * d), "bf16")
+    xs = [t.reshape(T, -1, d) for t in fused.split([4 * d, 2 * d, 3 * d], 1)]
+    pos, table = torch.arange(T, dtype=torch.int32, device="cuda"), lla.rotary_table(d)
+    gains = [1 + 0.3 * make((d,), "fp32", i) for i in range(3)]
+    cu, shift = torch.tensor([0, 10, 30], dtype=torch.int32, device="cuda"), torch.tensor([5, 9], dtype=torch.int32, device="cuda")
+    dys = [make(x.shape, "fp32", 7) for x in xs]
+    four, dy4, pos4 = make((2, 3, T, d), "fp32"), make((2, 3, T, d), "fp32", 1), pos[None].repeat(2, 1)
+
+    def calls():
+        lla.rotary_backward(dys[0], xs[0], pos, table, gain=gains[0], eps=0.1)        # (the thread's scratch is there from now on)
+        return [lla.rotary(xs, pos, table, gain=gains, eps=1e-6, cu_q=cu, shift=shift), (lla.rotary(xs[1], pos, table, interleaved=True),),
+                lla.rotary((xs[0], xs[2]), pos, table, gain=(None, gains[0]), eps=0.1), (lla.rotary(four, pos4, table, eps=0.0),),
+                (lla.rotary(four, pos, table),), *[(*r[0], *[g for g in r[1] or () if g is not None]) for r in
+                                                   (lla.rotary_backward(dys, xs, pos, table, gain=gains, eps=1e-6, cu_q=cu, shift=shift),
+                                                    lla.rotary_backward(dys[:2], xs[:2], pos, table, gain=(None, gains[1]), eps=1e-6),
+                                                    lla.rotary_backward(dys, xs, pos, table, eps=1e-6), lla.rotary_backward(dys, None, pos, table))],
+                (lla.rotary_backward(dy4, four, pos4, table, gain=gains[0], eps=0.0)[1],)]
+
+    fast = calls()
+    one = lla.rotary_backward([dys[0]], [xs[0]], pos, table, gain=gains[0], eps=1e-6)
+    assert isinstance(one[0], tuple) and isinstance(one[1], tuple)
+    assert lla.rotary_backward(dys[:1], xs[:1], pos, table, gain=[None], eps=1e-6)[1] is None
+    monkeypatch.setattr(lla, "_BIND", False)
+    for a, b in zip(fast, calls()):
+        assert len(a) == len(b) and all(x.dtype is y.dtype and torch.equal(x, y) for x, y in zip(a, b))
+    two = lla.rotary_backward([dys[0]], [xs[0]], pos, table, gain=gains[0], eps=1e-6)
+    assert torch.equal(one[0][0], two[0][0]) and torch.equal(one[1][0], two[1][0])
