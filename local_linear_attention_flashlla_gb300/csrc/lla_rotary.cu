@@ -96,6 +96,26 @@ __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
     return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
 }
 
+// Sine and cosine of t 2^-32 turns.  The nearest quarter turn is taken off in integers, exactly; what is left, at most an eighth of
+// a turn, has polynomials in x^2 of least largest absolute error (Remez): degree 7 for the sine (2^-29), 8 for the cosine
+// (2^-34), with their fp32 roundings 2^-23.3 each (sincospif with its own reduction took 2.5 times the rows' copy for each
+// token: at one head to a warp 325 us on the train shape).
+__device__ __forceinline__ void sincos_turn(int t, float& s, float& c) {
+    const unsigned q = ((unsigned)t + 0x20000000u) >> 30;                       // quarter turns, modulo 4
+    const float x = (float)(int)((unsigned)t - (q << 30)) * 0x1.921fb6p-30f;    // 2 pi 2^-32
+    const float z = x * x;
+    float ps = fmaf(z, -0x1.98da66p-13f, 0x1.1105b4p-7f);
+    ps = fmaf(z, ps, -0x1.555540p-3f);
+    ps = fmaf(x * z, ps, x);
+    float pc = fmaf(z, 0x1.993430p-16f, -0x1.6c087ep-10f);
+    pc = fmaf(z, pc, 0x1.55553ep-5f);
+    pc = fmaf(z, pc, -0.5f);
+    pc = fmaf(z, pc, 1.f);
+    const float ss = q & 1 ? pc : ps, cc = q & 1 ? ps : pc;
+    s = q & 2 ? -ss : ss;
+    c = (q + 1) & 2 ? -cc : cc;
+}
+
 // How a row's pieces lie in its lanes, and how its columns pair up.
 //   kHalves  columns c and c + rot / 2 turn together, and half a rotary dimension is a whole number of pieces: a lane
 //            holds two such pieces (or two neighbouring ones behind the rotary columns)
@@ -137,7 +157,7 @@ struct Lane {
             s[i] = 0.f;
             if (2 * f < a.rot) {
                 const long long t = position * a.turns[f];          // modulo a turn
-                sincospif((float)(int)(t >> 32) * 0x1p-31f, &s[i], &c[i]);
+                sincos_turn((int)(t >> 32), s[i], c[i]);
                 c[i] *= a.magnitude;
                 s[i] *= a.magnitude;
             }
@@ -207,21 +227,25 @@ __device__ __forceinline__ float sum_lanes(float x) {
     return x;
 }
 
-// A warp's tokens and heads: work item w is token group w / splits and heads [split (w % splits), ...).
+// A warp's tokens and heads.  The kWarps items of a block are neighbouring groups of tokens and the same `split` heads: what a
+// block reads at a time is one run of a head's rows where these lie position after position.
 struct Item {
     int b, t, h0, h1;
     bool in;
 };
+__device__ __forceinline__ int splits_of(const Args& a) { return (a.heads + a.split - 1) / a.split; }
 template <int G>
 __device__ __forceinline__ Item item_of(const Args& a, long long w, int group) {
-    const int splits = (a.heads + a.split - 1) / a.split;
-    const long long token = w / splits * G + group, tokens = (long long)a.B * a.n;
+    const int splits = splits_of(a);
+    const long long run = w / (kWarps * splits);             // of kWarps groups
+    const int split = (int)(w / kWarps - run * splits);
+    const long long token = (run * kWarps + w % kWarps) * G + group, tokens = (long long)a.B * a.n;
     Item it;
     it.in = token < tokens;
     const long long k = it.in ? token : tokens - 1;          // lanes without a token take part in the shuffles only
     it.b = (int)(k / a.n);
     it.t = (int)(k - (long long)it.b * a.n);
-    it.h0 = (int)(w % splits) * a.split;
+    it.h0 = split * a.split;
     it.h1 = min(it.h0 + a.split, a.heads);
     return it;
 }
@@ -235,12 +259,11 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_kernel(const __grid_consta
     const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31;
     float* stage = staged + (F == kStaged ? (warp * G + ln / L) * D : 0);
     const long long w = (long long)blockIdx.x * kWarps + warp;
-    const int splits = (a.heads + a.split - 1) / a.split;
     Ln l;
     l.place(ln % L, a.rot);
     cudaGridDependencySynchronize();
-    if (w / splits * G >= (long long)a.B * a.n) return;
     const Item it = item_of<G>(a, w, ln / L);
+    if (!__any_sync(0xffffffffu, it.in)) return;
     l.angles(a, position_of(a, it.b, it.t));
     const bool norm = a.eps >= 0.f;
     int first = 0;                           // the tensor's first head
@@ -295,39 +318,97 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_kernel(const __grid_consta
     }
 }
 
-// 2 N values of dy at the lane's two pieces; dy has x's type or is fp32.
-template <typename Y, int N>
-__device__ __forceinline__ void load_dy(const char* dy, const int (&piece)[2], float (&g)[2][N]) {
-    constexpr int M = Vec<Y>::N;
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-#pragma unroll
-        for (int k = 0; k < N / M; ++k) {
-            float y[M];
-            unpack(*reinterpret_cast<const uint4*>(dy + (piece[p] * (N / M) + k) * 16), y);
-#pragma unroll
-            for (int e = 0; e < M; ++e) g[p][k * M + e] = y[e];
-        }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// A warp goes through work items, its sums for the gains' gradients in shared memory; a block's sums leave in the
-// order of its warps, and rotary_gain_kernel adds the blocks' in theirs: no atomics, the same bits every run.
+// A warp's rows one after another: work items, in them the tensors, in them the heads.
+template <int G>
+struct Cursor {
+    long long w;
+    int i, first, h, h1;                     // tensor, its first head; head in the tensor, and behind its last of the item
+    Item it;
+    bool more;
+    const char *dy, *x;                      // this lane's row; x only where it is normalised
+    __device__ __forceinline__ void enter(const Args& a) {       // the first tensor from i on that has heads of the item
+        for (; i < a.count; first += a.rows[i++].heads) {
+            const Rows& r = a.rows[i];
+            h = max(it.h0 - first, 0);
+            h1 = min(it.h1 - first, r.heads);
+            if (h < h1) {
+                dy = r.dy + it.b * r.dys[0] + it.t * r.dys[2] + h * r.dys[1];
+                x = r.x + it.b * r.xs[0] + it.t * r.xs[2] + h * r.xs[1];
+                return;
+            }
+        }
+        more = false;
+    }
+    __device__ __forceinline__ void begin(const Args& a, long long item, long long items, int group) {
+        w = item;
+        more = w < items;
+        if (!more) return;
+        it = item_of<G>(a, w, group);
+        i = first = 0;
+        enter(a);
+    }
+    __device__ __forceinline__ void step(const Args& a, long long stride, long long items, int group) {
+        if (++h < h1) {
+            dy += a.rows[i].dys[1];
+            x += a.rows[i].xs[1];
+            return;
+        }
+        first += a.rows[i++].heads;
+        enter(a);
+        if (!more) begin(a, w + stride, items, group);
+    }
+};
+
+// The rows come through shared memory, kStages of them to a warp, each lane copying and reading its own pieces: no barrier, and
+// loads stay in flight under the arithmetic (through registers the rows behind waited for the stores before: 226 us for the
+// train shape, 4.7 TB/s).  A warp goes through work items, its sums for the gains' gradients in shared memory; a block's sums
+// leave in the order of its warps, and rotary_gain_kernel adds the blocks' in theirs: no atomics, the same bits every run.
+constexpr int kStages = 4;
+template <typename T, typename Y>
+constexpr int stage_bytes() { return 32 * 16 * (2 * Vec<T>::N / Vec<Y>::N + 2); }
+
 template <typename T, typename Y, int D, int F>
 __global__ void __launch_bounds__(kThreads, 2) rotary_backward_kernel(const __grid_constant__ Args a, long long items) {
     using Ln = Lane<T, D, F>;
-    constexpr int N = Ln::N, L = Ln::L, G = Ln::G;
+    constexpr int N = Ln::N, L = Ln::L, G = Ln::G, M = Vec<Y>::N, K = N / M, kStage = stage_bytes<T, Y>();
+    extern __shared__ __align__(16) unsigned char ring[];
     __shared__ float staged[F == kStaged ? kWarps * G * D : 1];
-    __shared__ float sums[kWarps][kMost][D];
-    const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31;
-    float* stage = staged + (F == kStaged ? (warp * G + ln / L) * D : 0);
+    __shared__ __align__(16) float sums[kWarps][kMost][D], gains[kMost][D];
+    const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31, group = ln / L;
+    float* stage = staged + (F == kStaged ? (warp * G + group) * D : 0);
+    const unsigned char* mine = ring + warp * kStages * kStage + ln * 16;          // piece p of a stage: 512 p bytes on
+    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
     const bool norm = a.eps >= 0.f;
+    const long long stride = (long long)gridDim.x * kWarps, w0 = (long long)blockIdx.x * kWarps + warp;
     for (int e = ln; e < kMost * D; e += 32) sums[warp][e / D][e % D] = 0.f;
-    __syncwarp();
     Ln l;
     l.place(ln % L, a.rot);
     cudaGridDependencySynchronize();
-    for (long long w = (long long)blockIdx.x * kWarps + warp; w < items; w += (long long)gridDim.x * kWarps) {
-        const Item it = item_of<G>(a, w, ln / L);
+    for (int e = threadIdx.x; e < a.count * D; e += kThreads) gains[e / D][e % D] = a.rows[e / D].gain ? a.rows[e / D].gain[e % D] : 1.f;
+    __syncthreads();
+    Cursor<G> ahead;
+    ahead.begin(a, w0, items, group);
+    auto fetch = [&](int st) {
+        if (ahead.more) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+#pragma unroll
+                for (int k = 0; k < K; ++k) copy16(base + st * kStage + (p * K + k) * 512, ahead.dy + (l.piece[p] * K + k) * 16);
+                if (norm) copy16(base + st * kStage + (2 * K + p) * 512, ahead.x + l.piece[p] * 16);
+            }
+            ahead.step(a, stride, items, group);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(i);
+    int st = 0;
+    for (long long w = w0; w < items; w += stride) {
+        const Item it = item_of<G>(a, w, group);
         l.angles(a, position_of(a, it.b, it.t));
         int first = 0;
 #pragma unroll 1
@@ -335,25 +416,30 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_backward_kernel(const __gr
             const Rows& r = a.rows[i];
             const int h0 = max(it.h0 - first, 0), h1 = min(it.h1 - first, r.heads);
             if (h0 >= h1) continue;
-            float gain[2][N], dgain[2][N];
+            float dgain[2][N];
 #pragma unroll
             for (int p = 0; p < 2; ++p)
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    gain[p][e] = r.gain ? r.gain[l.piece[p] * N + e] : 1.f;
-                    dgain[p][e] = 0.f;
-                }
-            const char* x = r.x + it.b * r.xs[0] + it.t * r.xs[2];
-            const char* dy = r.dy + it.b * r.dys[0] + it.t * r.dys[2];
-            char* out = r.out + it.b * r.os[0] + it.t * r.os[2];
-#pragma unroll 2
-            for (int h = h0; h < h1; ++h) {
+                for (int e = 0; e < N; ++e) dgain[p][e] = 0.f;
+            char* out = r.out + it.b * r.os[0] + it.t * r.os[2] + h0 * r.os[1];
+#pragma unroll 1
+            for (int h = h0; h < h1; ++h, out += r.os[1]) {
+                asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+                const uint4* row = reinterpret_cast<const uint4*>(mine + st * kStage);
                 float g[2][N], v[2][N];
-                load_dy<Y, N>(dy + h * r.dys[1], l.piece, g);
-                if (norm) {
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) unpack(*reinterpret_cast<const uint4*>(x + h * r.xs[1] + l.piece[p] * 16), v[p]);
+                for (int p = 0; p < 2; ++p) {
+#pragma unroll
+                    for (int k = 0; k < K; ++k) {
+                        float y[M];
+                        unpack(row[(p * K + k) * 32], y);
+#pragma unroll
+                        for (int e = 0; e < M; ++e) g[p][k * M + e] = y[e];
+                    }
+                    if (norm) unpack(row[(2 * K + p) * 32], v[p]);
                 }
+                fetch(st == 0 ? kStages - 1 : st - 1);           // the stage of the row before
+                st = st + 1 == kStages ? 0 : st + 1;
                 l.turn(g, -1.f, a.rot, stage);
                 if (norm) {
                     float q = 0.f, m = 0.f;
@@ -368,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_backward_kernel(const __gr
                         for (int e = 0; e < N; ++e) {
                             v[p][e] *= rs;                              // the unit row
                             if (it.in) dgain[p][e] = fmaf(g[p][e], v[p][e], dgain[p][e]);
-                            g[p][e] *= gain[p][e];
+                            g[p][e] *= gains[i][l.piece[p] * N + e];
                             m = fmaf(g[p][e], v[p][e], m);
                         }
                     m = sum_lanes<L>(m) * (1.f / D);
@@ -379,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_backward_kernel(const __gr
                 }
                 if (it.in) {
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) *reinterpret_cast<uint4*>(out + h * r.os[1] + l.piece[p] * 16) = pack(g[p]);
+                    for (int p = 0; p < 2; ++p) *reinterpret_cast<uint4*>(out + l.piece[p] * 16) = pack(g[p]);
                 }
             }
             if (r.dgain) {
@@ -395,6 +481,7 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_backward_kernel(const __gr
             }
         }
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (!a.part) return;
     __syncthreads();
     for (int e = threadIdx.x; e < a.count * D; e += kThreads) {
@@ -449,12 +536,19 @@ cudaError_t launch_forward(const Args& a, int form, unsigned blocks, cudaStream_
         default: return paged::launch_after(rotary_kernel<T, D, kStaged>, dim3(blocks), kThreads, 0, s, a);
     }
 }
+template <typename T, typename Y, int D, int F>
+cudaError_t launch_backward_form(const Args& a, unsigned blocks, long long items, cudaStream_t s) {
+    constexpr size_t smem = (size_t)kWarps * kStages * stage_bytes<T, Y>();
+    cudaError_t e = cudaFuncSetAttribute(rotary_backward_kernel<T, Y, D, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return paged::launch_after(rotary_backward_kernel<T, Y, D, F>, dim3(blocks), kThreads, smem, s, a, items);
+}
 template <typename T, typename Y, int D>
 cudaError_t launch_backward(const Args& a, int form, unsigned blocks, long long items, cudaStream_t s) {
     switch (form) {
-        case kHalves: return paged::launch_after(rotary_backward_kernel<T, Y, D, kHalves>, dim3(blocks), kThreads, 0, s, a, items);
-        case kPairs: return paged::launch_after(rotary_backward_kernel<T, Y, D, kPairs>, dim3(blocks), kThreads, 0, s, a, items);
-        default: return paged::launch_after(rotary_backward_kernel<T, Y, D, kStaged>, dim3(blocks), kThreads, 0, s, a, items);
+        case kHalves: return launch_backward_form<T, Y, D, kHalves>(a, blocks, items, s);
+        case kPairs: return launch_backward_form<T, Y, D, kPairs>(a, blocks, items, s);
+        default: return launch_backward_form<T, Y, D, kStaged>(a, blocks, items, s);
     }
 }
 template <typename T>
@@ -550,8 +644,7 @@ int lla_rotary(int dtype, const lla_rotary_rows* rows, int count, int B, int n, 
     if (sms < 1) return lr::failf(LLA_ERR_CUDA, "lla_rotary: no device");
     lr::divide(a, es, d, sms);
     const int G = lr::rows_of_warp(es, d);
-    const long long items = ((long long)B * n + G - 1) / G * ((a.heads + a.split - 1) / a.split);
-    const long long blocks = (items + lr::kWarps - 1) / lr::kWarps;
+    const long long blocks = ((long long)B * n + G * lr::kWarps - 1) / (G * lr::kWarps) * ((a.heads + a.split - 1) / a.split);
     if (blocks > INT_MAX) return lr::failf(LLA_ERR_INVALID_ARG, "problem too large");
     const int form = lr::form_of(rot, interleaved, es);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -588,8 +681,8 @@ int lla_rotary_backward(int dtype, int dy_dtype, const lla_rotary_rows* rows, in
     if (sms < 1) return lr::failf(LLA_ERR_CUDA, "lla_rotary_backward: no device");
     lr::divide(a, es, d, sms);
     const int G = lr::rows_of_warp(es, d);
-    const long long items = ((long long)B * n + G - 1) / G * ((a.heads + a.split - 1) / a.split);
-    long long blocks = (items + lr::kWarps - 1) / lr::kWarps;
+    long long blocks = ((long long)B * n + G * lr::kWarps - 1) / (G * lr::kWarps) * ((a.heads + a.split - 1) / a.split);
+    const long long items = blocks * lr::kWarps;
     const long long most = lr::kBackwardBlocksPerSm * sms < lr::kMostBlocks ? lr::kBackwardBlocksPerSm * sms : lr::kMostBlocks;
     if (blocks > most) blocks = most;
     const int form = lr::form_of(rot, interleaved, es);

@@ -300,7 +300,7 @@ cudaError_t launch_one(const Args& a, long long rows, cudaStream_t stream) {
     if constexpr (D * sizeof(T) <= 256) {
         if (rows <= 32) return launch_rows<T, D, 4, true>(a, stream);
     }
-    return launch_rows<T, D, D * sizeof(T) <= 128 ? 4 : 2, false>(a, stream);
+    return launch_rows<T, D, 2, false>(a, stream);
 }
 template <typename T>
 cudaError_t launch_typed(const Args& a, int d, long long rows, cudaStream_t stream) {
