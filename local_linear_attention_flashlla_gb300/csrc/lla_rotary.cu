@@ -98,8 +98,7 @@ __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
 
 // Sine and cosine of t 2^-32 turns.  The nearest quarter turn is taken off in integers, exactly; what is left, at most an eighth of
 // a turn, has polynomials in x^2 of least largest absolute error (Remez): degree 7 for the sine (2^-29), 8 for the cosine
-// (2^-34), with their fp32 roundings 2^-23.3 each (sincospif with its own reduction took 2.5 times the rows' copy for each
-// token: at one head to a warp 325 us on the train shape).
+// (2^-34), with their fp32 roundings 2^-23.3 each.
 __device__ __forceinline__ void sincos_turn(int t, float& s, float& c) {
     const unsigned q = ((unsigned)t + 0x20000000u) >> 30;                       // quarter turns, modulo 4
     const float x = (float)(int)((unsigned)t - (q << 30)) * 0x1.921fb6p-30f;    // 2 pi 2^-32
@@ -132,16 +131,14 @@ struct Lane {
     int lane, piece[2];
     float c[A], s[A];
 
+    static __device__ __forceinline__ int piece_of(int l, int p, int rot) {
+        const int h = rot / 2 / N;
+        return F != kHalves || l >= h ? 2 * l + p : l + p * h;       // behind the rotary columns: 2 h + 2 (l - h) + p
+    }
     __device__ __forceinline__ void place(int l, int rot) {
         lane = l;
-        if (F == kHalves) {
-            const int h = rot / 2 / N;
-            piece[0] = l < h ? l : 2 * l;             // behind the rotary columns: 2 h + 2 (l - h)
-            piece[1] = l < h ? l + h : 2 * l + 1;
-        } else {
-            piece[0] = 2 * l;
-            piece[1] = 2 * l + 1;
-        }
+        piece[0] = piece_of(l, 0, rot);
+        piece[1] = piece_of(l, 1, rot);
     }
     // sines and cosines of the lane's angles, times the magnitude; columns that do not turn have 1 and 0
     __device__ __forceinline__ void angles(const Args& a, long long position) {
@@ -363,10 +360,14 @@ struct Cursor {
     }
 };
 
-// The rows come through shared memory, kStages of them to a warp, each lane copying and reading its own pieces: no barrier, and
-// loads stay in flight under the arithmetic (through registers the rows behind waited for the stores before: 226 us for the
-// train shape, 4.7 TB/s).  A warp goes through work items, its sums for the gains' gradients in shared memory; a block's sums
-// leave in the order of its warps, and rotary_gain_kernel adds the blocks' in theirs: no atomics, the same bits every run.
+// The rows come through shared memory, kStages of them to a warp: no barrier of the block, and loads stay in flight under the
+// arithmetic.  Where dy has K = 2 pieces of 16 bytes to one of x, a lane reads two neighbouring ones; the copies are shared out so
+// that neighbouring lanes copy neighbouring pieces (whole 32-byte sectors), and piece C of the warp's rows lies in slot
+// C ^ (C >> 3 & 1), which keeps eight lanes' writes and eight lanes' reads of every second piece in eight different slots.  Train
+// shape, fp32 dy: 168 us, 6.4 TB/s, 0.96 of a plain copy's bandwidth; each lane copying its own pieces 217, the copies shared out
+// without the swap of slots 229, rows through registers 226.  A warp goes through work items, its sums for the gains' gradients
+// in shared memory; a block's sums leave in the order of its warps, and rotary_gain_kernel adds the blocks' in theirs: no
+// atomics, the same bits every run.
 constexpr int kStages = 4;
 template <typename T, typename Y>
 constexpr int stage_bytes() { return 32 * 16 * (2 * Vec<T>::N / Vec<Y>::N + 2); }
@@ -377,14 +378,16 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_backward_kernel(const __gr
     constexpr int N = Ln::N, L = Ln::L, G = Ln::G, M = Vec<Y>::N, K = N / M, kStage = stage_bytes<T, Y>();
     extern __shared__ __align__(16) unsigned char ring[];
     __shared__ float staged[F == kStaged ? kWarps * G * D : 1];
-    __shared__ __align__(16) float sums[kWarps][kMost][D], gains[kMost][D];
+    __shared__ __align__(16) float gains[kMost][D];
     const int warp = threadIdx.x >> 5, ln = threadIdx.x & 31, group = ln / L;
     float* stage = staged + (F == kStaged ? (warp * G + group) * D : 0);
-    const unsigned char* mine = ring + warp * kStages * kStage + ln * 16;          // piece p of a stage: 512 p bytes on
+    const unsigned char* mine = ring + warp * kStages * kStage;          // 512 bytes to a piece of every lane: 2 K of dy, 2 of x
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(mine));
+    float* sums = reinterpret_cast<float*>(ring + kWarps * kStages * kStage);     // [warp][tensor][D], behind the stages
+    float* own = sums + warp * a.count * D;
     const bool norm = a.eps >= 0.f;
     const long long stride = (long long)gridDim.x * kWarps, w0 = (long long)blockIdx.x * kWarps + warp;
-    for (int e = ln; e < kMost * D; e += 32) sums[warp][e / D][e % D] = 0.f;
+    for (int e = ln; e < a.count * D; e += 32) own[e] = 0.f;
     Ln l;
     l.place(ln % L, a.rot);
     cudaGridDependencySynchronize();
@@ -392,13 +395,23 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_backward_kernel(const __gr
     __syncthreads();
     Cursor<G> ahead;
     ahead.begin(a, w0, items, group);
+    // what this lane copies of dy: of the L K pieces that the row's lanes read in turn, number k L + lane
+    auto slot = [](int c) { return (K == 2 ? c ^ (c >> 3 & 1) : c) * 16; };
+    int from[2][K], to[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        const int c = k * L + ln % L;
+        to[k] = slot(group * L * K + c);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) from[p][k] = (Ln::piece_of(c / K, p, a.rot) * K + c % K) * 16;
+    }
     auto fetch = [&](int st) {
         if (ahead.more) {
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
 #pragma unroll
-                for (int k = 0; k < K; ++k) copy16(base + st * kStage + (p * K + k) * 512, ahead.dy + (l.piece[p] * K + k) * 16);
-                if (norm) copy16(base + st * kStage + (2 * K + p) * 512, ahead.x + l.piece[p] * 16);
+                for (int k = 0; k < K; ++k) copy16(base + st * kStage + p * K * 512 + to[k], ahead.dy + from[p][k]);
+                if (norm) copy16(base + st * kStage + (2 * K + p) * 512 + ln * 16, ahead.x + l.piece[p] * 16);
             }
             ahead.step(a, stride, items, group);
         }
@@ -407,9 +420,15 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_backward_kernel(const __gr
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch(i);
     int st = 0;
+    Item next = item_of<G>(a, w0, group);
+    long long position = w0 < items ? position_of(a, next.b, next.t) : 0;
     for (long long w = w0; w < items; w += stride) {
-        const Item it = item_of<G>(a, w, group);
-        l.angles(a, position_of(a, it.b, it.t));
+        const Item it = next;
+        l.angles(a, position);
+        if (w + stride < items) {            // the next item's position is on its way under this one's rows
+            next = item_of<G>(a, w + stride, group);
+            position = position_of(a, next.b, next.t);
+        }
         int first = 0;
 #pragma unroll 1
         for (int i = 0; i < a.count; first += a.rows[i].heads, ++i) {
@@ -425,18 +444,19 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_backward_kernel(const __gr
 #pragma unroll 1
             for (int h = h0; h < h1; ++h, out += r.os[1]) {
                 asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-                const uint4* row = reinterpret_cast<const uint4*>(mine + st * kStage);
+                __syncwarp();                                    // other lanes' copies; and the row before is read
+                const unsigned char* row = mine + st * kStage;
                 float g[2][N], v[2][N];
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
 #pragma unroll
                     for (int k = 0; k < K; ++k) {
                         float y[M];
-                        unpack(row[(p * K + k) * 32], y);
+                        unpack(*reinterpret_cast<const uint4*>(row + p * K * 512 + slot(ln * K + k)), y);
 #pragma unroll
                         for (int e = 0; e < M; ++e) g[p][k * M + e] = y[e];
                     }
-                    if (norm) unpack(row[(2 * K + p) * 32], v[p]);
+                    if (norm) unpack(*reinterpret_cast<const uint4*>(row + (2 * K + p) * 512 + ln * 16), v[p]);
                 }
                 fetch(st == 0 ? kStages - 1 : st - 1);           // the stage of the row before
                 st = st + 1 == kStages ? 0 : st + 1;
@@ -476,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_backward_kernel(const __gr
                         float d = dgain[p][e];
 #pragma unroll
                         for (int o = L; o < 32; o <<= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-                        if (ln < L) sums[warp][i][l.piece[p] * N + e] += d;
+                        if (ln < L) own[i * D + l.piece[p] * N + e] += d;
                     }
             }
         }
@@ -487,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 2) rotary_backward_kernel(const __gr
     for (int e = threadIdx.x; e < a.count * D; e += kThreads) {
         float t = 0.f;
 #pragma unroll
-        for (int k = 0; k < kWarps; ++k) t += sums[k][e / D][e % D];
+        for (int k = 0; k < kWarps; ++k) t += sums[k * a.count * D + e];
         a.part[(long long)blockIdx.x * a.count * D + e] = t;
     }
 }
@@ -520,7 +540,8 @@ size_t part_bytes(int count, int d) { return (size_t)kMostBlocks * count * d * s
 
 int rows_of_warp(int es, int d) { return 32 / (d * es / 32); }
 
-// Heads to a warp: as many as leave the device 32 warps an SM, so that a token's sines serve several rows.
+// Heads to a warp: as many as leave the device 32 warps an SM, so that a token's sines serve several rows, and 16 at most (train
+// shape: 8 97 us, 16 90, 32 91; gradient 241, 217, 227 then; 1 to a warp, whose start nothing hides, 303 and 611).
 void divide(Args& a, int es, int d, int sms) {
     const long long groups = ((long long)a.B * a.n + rows_of_warp(es, d) - 1) / rows_of_warp(es, d);
     const long long each = groups * a.heads / ((long long)sms * 32);
@@ -538,8 +559,9 @@ cudaError_t launch_forward(const Args& a, int form, unsigned blocks, cudaStream_
 }
 template <typename T, typename Y, int D, int F>
 cudaError_t launch_backward_form(const Args& a, unsigned blocks, long long items, cudaStream_t s) {
-    constexpr size_t smem = (size_t)kWarps * kStages * stage_bytes<T, Y>();
-    cudaError_t e = cudaFuncSetAttribute(rotary_backward_kernel<T, Y, D, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    constexpr size_t rows = (size_t)kWarps * kStages * stage_bytes<T, Y>(), sums = (size_t)kWarps * D * sizeof(float);   // of a tensor
+    const size_t smem = rows + a.count * sums;
+    cudaError_t e = cudaFuncSetAttribute(rotary_backward_kernel<T, Y, D, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(rows + kMost * sums));
     if (e != cudaSuccess) return e;
     return paged::launch_after(rotary_backward_kernel<T, Y, D, F>, dim3(blocks), kThreads, smem, s, a, items);
 }
