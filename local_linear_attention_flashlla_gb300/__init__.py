@@ -870,8 +870,10 @@ def rotary_table(dim, base=10000.0, *, scaling=None, factor=1.0, original=4096, 
         b, k, two_pi = D(base), D(factor), 2 * D("3.14159265358979323846264338327950288419716939937510582")
         if scaling == "ntk":
             b *= k ** (D(dim) / max(dim - 2, 1))
-        for i in range(0, dim, 2):
-            f = b ** (D(-i) / dim)
+        power, step = D(1), b ** (D(-2) / dim)     # dim / 2 products, each off by 10^-50: no frequency's rounding sees that
+        for _ in range(0, dim, 2):
+            f = power
+            power *= step
             if scaling == "linear":
                 f /= k
             elif scaling == "parts":
@@ -1023,8 +1025,8 @@ def rotary(x, positions, table, *, gain=None, eps=None, interleaved=False, cu_q=
     import torch
     many = isinstance(x, (tuple, list))
     if stream is None and out is None and isinstance(table, RotaryTable) and table.turns.is_cuda and _bind():
-        index, empty = torch.cuda.current_device(), torch.empty
-        res = tuple([empty(t.shape, dtype=t.dtype, device=t.device) for t in x]) if many else empty(x.shape, dtype=x.dtype, device=x.device)
+        index = torch.cuda.current_device()
+        res = tuple([t.new_empty(t.shape) for t in x]) if many else x.new_empty(x.shape)
         if _BIND.rotary(index, x, positions, table.turns, table.dim, table.magnitude, gain, eps, interleaved, cu_q, shift, res,
                         torch._C._cuda_getCurrentRawStream(index)) == LLA_OK:
             return res
@@ -1052,15 +1054,14 @@ def rotary_backward(dy, x, positions, table, *, gain=None, eps=None, interleaved
         raise _bad("x is needed where the rows were normalised (eps)")
     many = isinstance(dy, (tuple, list))
     if stream is None and dx is None and workspace is None and isinstance(table, RotaryTable) and table.turns.is_cuda and _bind():
-        index, empty = torch.cuda.current_device(), torch.empty
+        index = torch.cuda.current_device()
         stream_ptr = torch._C._cuda_getCurrentRawStream(index)
         t = _SCRATCH.get((index, stream_ptr, threading.get_ident()))
         if gain is None or (t is not None and not torch.cuda.is_current_stream_capturing()):
             like = dy if x is None else x
-            res = tuple([empty(r.shape, dtype=r.dtype, device=r.device) for r in like]) if many else \
-                empty(like.shape, dtype=like.dtype, device=like.device)
-            grads = None if gain is None else torch.empty_like(gain) if torch.is_tensor(gain) else \
-                tuple([None if g is None else torch.empty_like(g) for g in gain])
+            res = tuple([r.new_empty(r.shape) for r in like]) if many else like.new_empty(like.shape)
+            grads = None if gain is None else gain.new_empty(gain.shape) if torch.is_tensor(gain) else \
+                tuple([None if g is None else g.new_empty(g.shape) for g in gain])
             if _BIND.rotary_backward(index, dy, x, positions, table.turns, table.dim, table.magnitude, gain, eps, interleaved, cu_q,
                                      shift, res, grads, 0 if t is None else t.data_ptr(), 0 if t is None else t.numel(),
                                      stream_ptr) == LLA_OK:

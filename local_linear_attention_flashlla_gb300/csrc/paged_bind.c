@@ -273,9 +273,9 @@ static int packed(PyObject* obj, PyObject* dtype, long device, const long long* 
     return 1;
 }
 /* [T, heads, d] or [B, heads, n, d] rows, 16-byte aligned and strided; their strides of batch, head and position. */
-static int head_rows(PyObject* obj, PyObject* dtype, long device, const Tensor* like, Tensor* t, long long* stride) {
+static int head_rows(const Tensor* t, PyObject* dtype, long device, const Tensor* like, long long* stride) {
     const int ve = dtype == t_bf16 ? 8 : 4;
-    if (!read_tensor(obj, t) || t->dtype != dtype || t->device != device || t->dim != like->dim || t->ptr % 16) return 0;
+    if (t->dtype != dtype || t->device != device || t->dim != like->dim || t->ptr % 16) return 0;
     for (long i = 0; i < t->dim; ++i)
         if (t->shape[i] != like->shape[i] || (i + 1 < t->dim ? t->stride[i] % ve != 0 : t->stride[i] != 1)) return 0;
     stride[0] = t->dim == 4 ? t->stride[0] : 0;
@@ -291,7 +291,8 @@ typedef struct {
     uintptr_t positions, turns, cu, shift;
 } Rotary;
 
-/* What both directions take: x (or None), dy (or None in the forward pass), positions, turns, rot, gains, eps given, cu_q, shift, out. */
+/* What both directions take: x (or None), dy (or None in the forward pass), positions, turns, rot, gains, eps given, cu_q, shift, and
+ * out: contiguous tensors that the caller made like x. */
 static int rotary_args(Rotary* r, long device, PyObject* x, PyObject* dy, PyObject* positions, PyObject* turns, long rot, PyObject* gains,
                        int normalise, PyObject* cu, PyObject* shift, PyObject* out) {
     Tensor first, t, p;
@@ -304,7 +305,8 @@ static int rotary_args(Rotary* r, long device, PyObject* x, PyObject* dy, PyObje
     PyObject* dy_dtype = dtype;
     if (dtype != t_bf16 && dtype != t_fp32) return 0;
     if (dy != Py_None) {
-        if (!item(dy, 0, count) || !read_tensor(item(dy, 0, count), &t)) return 0;
+        if (x == Py_None) t = first;
+        else if (!item(dy, 0, count) || !read_tensor(item(dy, 0, count), &t)) return 0;
         dy_dtype = t.dtype;
         if (dy_dtype != dtype && dy_dtype != t_fp32) return 0;
     }
@@ -314,22 +316,28 @@ static int rotary_args(Rotary* r, long device, PyObject* x, PyObject* dy, PyObje
     memset(r, 0, sizeof *r);
     for (Py_ssize_t i = 0; i < count; ++i) {
         rotary_rows* o = &r->rows[i];
-        Tensor l;
-        PyObject* obj = item(like, i, count);
-        if (!obj || !read_tensor(obj, &l) || l.dim != first.dim || l.dtype != dtype || l.shape[l.dim - 1] != d ||
+        Tensor l = first;
+        if (i > 0 && (!item(like, i, count) || !read_tensor(item(like, i, count), &l))) return 0;
+        if (l.dim != first.dim || l.dtype != dtype || l.shape[l.dim - 1] != d ||
             (flat ? l.shape[0] != n : l.shape[0] != B || l.shape[2] != n) || !fits(l.shape[1]))
             return 0;
         o->heads = (int)l.shape[1];
         if (x != Py_None) {
-            if (!head_rows(obj, dtype, device, &l, &t, o->x_stride)) return 0;
-            o->x = P(t.ptr);
+            if (!head_rows(&l, dtype, device, &l, o->x_stride)) return 0;
+            o->x = P(l.ptr);
         }
         if (dy != Py_None) {
-            if (!item(dy, i, count) || !head_rows(item(dy, i, count), dy_dtype, device, &l, &t, o->dy_stride)) return 0;
+            if (x == Py_None) t = l;
+            else if (!item(dy, i, count) || !read_tensor(item(dy, i, count), &t)) return 0;
+            if (!head_rows(&t, dy_dtype, device, &l, o->dy_stride)) return 0;
             o->dy = P(t.ptr);
         }
-        if (!item(out, i, count) || !head_rows(item(out, i, count), dtype, device, &l, &t, o->out_stride)) return 0;
-        o->out = P(t.ptr);
+        const uintptr_t to = item(out, i, count) ? pointer_of(item(out, i, count)) : 0;
+        if (!to) return 0;
+        o->out = P(to);
+        o->out_stride[0] = flat ? 0 : l.shape[1] * n * d;
+        o->out_stride[1] = flat ? d : n * d;
+        o->out_stride[2] = flat ? l.shape[1] * d : d;
         if (gains != Py_None) {
             PyObject* g = item(gains, i, count);
             if (!g) return 0;
@@ -406,10 +414,10 @@ static PyObject* rotary_backward(PyObject* self, PyObject* const* a, Py_ssize_t 
         return PyLong_FromLong(-1);
     for (int i = 0; i < r.count; ++i) {
         if (!r.rows[i].gain) continue;
-        Tensor t;
-        PyObject* g = item(a[13], i, r.count);
-        if (!g || !vector(g, t_fp32, device, r.d, &t)) return PyLong_FromLong(-1);
-        r.rows[i].dgain = P(t.ptr);
+        PyObject* g = item(a[13], i, r.count);               /* the caller's own, like the gain */
+        const uintptr_t to = g ? pointer_of(g) : 0;
+        if (!to) return PyLong_FromLong(-1);
+        r.rows[i].dgain = P(to);
     }
     Py_BEGIN_ALLOW_THREADS
     status = f_rotary_backward(r.dtype, r.dy_dtype, r.rows, r.count, r.B, r.n, r.d, P(r.positions), r.position_stride, P(r.turns), (int)rot,
