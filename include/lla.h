@@ -523,7 +523,8 @@ size_t lla_paged_parallax_workspace_size(int dtype, int path, int T, int S, int 
  * lla_paged_weigh.  Where caches are to shrink, after the step: lla_paged_evict for every layer, then lla_paged_trim once.
  * Keys are cached rotated, so a key keeps its position when it moves to another slot; the next step's token rows get theirs
  * from lla_rotary with shift = dropped.  As in the other paged calls every length is read on the device, and no
- * call synchronises.
+ * call synchronises.  A page is one sequence's: where two rows of the table name the same page, its scores are written by both,
+ * eviction moves its rows twice and trimming frees it twice, in no defined order.
  *
  * lla_paged_weigh -- for every sequence s that brings tokens (n = cu_q[s+1]-cu_q[s] >= 1 rows, L = kv_lens[s]), every key
  * head h and slot j < L, over the rows of the last `last` tokens (0: of all) and the query heads of h that see the key:
@@ -539,7 +540,7 @@ size_t lla_paged_parallax_workspace_size(int dtype, int path, int T, int S, int 
  * scores, scores_out  may be one array.  Only slots j < L of sequences that bring tokens are written.
  * positions  NULL, or written at the step's own tokens in causal attention: j + dropped[s] (dropped NULL: j).
  * causal     as in lla_paged_parallax; with 0 the keys hold none of the step's tokens.
- * last >= 0, decay >= 0 and finite; all other arguments, limits and errors are those of lla_paged_parallax (no path: bf16
+ * last >= 0, decay >= 0 and finite, tau in [1e-30, 1e30); all other arguments, limits and errors are those of lla_paged_parallax (no path: bf16
  * products are exact, fp32 ones as its LLA_PATH_FP32 says for d in {32, 64}, sums and weights are fp32).
  * workspace  NULL (stream-ordered pool) or lla_paged_weigh_workspace_size(...) bytes, 256-byte aligned, used by no other
  *            call at the same time.  Results do not depend on the run.

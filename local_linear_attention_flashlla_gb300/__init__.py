@@ -1148,6 +1148,7 @@ def paged_weigh(q, lse, k_cache, scores, block_table, cu_q, kv_lens, tau, max_ne
     scores, given each new token's position in its sequence (slot + dropped[s]; dropped [S] int32, paged_trim's).
     last: only rows of the last `last` tokens of a sequence count (0: all).
     Returns the new scores.  Sequences without tokens in the step are left alone.  Results have the same bits every run.
+    A page belongs to one sequence (of this call and of paged_evict and paged_trim).
     Asynchronous on the current (or given) stream.  workspace: as for paged_parallax.
     """
     import torch

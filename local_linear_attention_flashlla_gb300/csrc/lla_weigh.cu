@@ -403,7 +403,8 @@ int lla_paged_weigh(int dtype, const void* q, const float* lse, const void* k_ca
         if (!lw::aligned(x, 4)) return lw::failf(LLA_ERR_INVALID_ARG, "int32 and fp32 pointers must be 4-byte aligned");
     const int st = lw::check_sizes(dtype, T, S, Hq, Hkv, d, page_size, num_pages, table_width, max_new);
     if (st != LLA_OK) return st;
-    if (!(tau > 0.f) || !(tau < 1e30f)) return lw::failf(LLA_ERR_INVALID_ARG, "tau must be finite and > 0");
+    // (the tensor cores' logsumexp is -lse / tau: it stays finite)
+    if (!(tau >= 1e-30f) || !(tau < 1e30f)) return lw::failf(LLA_ERR_INVALID_ARG, "tau must be in [1e-30, 1e30)");
     if (!(decay >= 0.f) || !(decay < INFINITY)) return lw::failf(LLA_ERR_INVALID_ARG, "decay must be finite and >= 0");
     if (last < 0) return lw::failf(LLA_ERR_INVALID_ARG, "last must be >= 0 (0: every row)");
     const int es = dtype == LLA_DTYPE_BF16 ? 2 : 4, ve = 16 / es;

@@ -29,7 +29,7 @@ def _weigh(lib, **kw):
     dict(q=None), dict(lse=None), dict(kc=None), dict(sc=None), dict(so=None), dict(table=None), dict(cu=None), dict(kv=None),
     dict(q=24), dict(kc=40), dict(lse=34), dict(sc=65), dict(so=66), dict(pos=81), dict(drop=98), dict(table=113), dict(T=0),
     dict(S=0), dict(S=(1 << 20) + 1), dict(Hq=0), dict(Hkv=0), dict(Hq=5), dict(d=48), dict(page=7), dict(page=512), dict(P=0),
-    dict(W=0), dict(W=1 << 25), dict(max_new=0), dict(qs=255), dict(qs=252), dict(ps=1024), dict(ps=2050), dict(tau=0.0),
+    dict(W=0), dict(W=1 << 25), dict(max_new=0), dict(qs=255), dict(qs=252), dict(ps=1024), dict(ps=2050), dict(tau=0.0), dict(tau=1e-31),
     dict(tau=float("nan")), dict(tau=float("inf")), dict(decay=-0.5), dict(decay=float("nan")), dict(decay=float("inf")), dict(last=-1),
     dict(dtype=2), dict(T=1 << 29), dict(Hq=4096, qs=1 << 20), dict(P=1 << 30),
 ])

@@ -130,6 +130,31 @@ def test_weigh_large_logits_and_rows_of_nothing(lla_gpu):
     w.run()
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("fp32", 32)])
+@pytest.mark.parametrize("new,kv", [([30, 45], [200, 70]), ([200], [300]), ([3, 1], [90, 5])])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_weigh_nan_and_infinity_in_masked_places(lla_gpu, dtype, d, new, kv, bad):
+    """A key that only the last token sees, and a row without weights (lse -inf), hold NaN or infinity; slots behind the lengths hold
+    NaN already.  Every other score is as if they did not."""
+    w = Weigh(Case(new, kv, 2, 1, d, 16, dtype))
+    c = w.c
+    w.lse[0] = -float("inf")
+    clean = lla.paged_weigh(**w.device(), scores=w.scores.cuda())
+    args = w.device()
+    args["q"][0] = bad
+    page, at = int(c.table[0, (kv[0] - 1) // 16]), (kv[0] - 1) % 16
+    args["k_cache"][page, :, at] = bad
+    pos = w.positions.cuda()
+    got = lla.paged_weigh(**args, scores=w.scores.cuda(), positions=pos)
+    torch.cuda.synchronize()
+    lla.lla_sync_status()
+    alone = torch.isnan(got) | torch.isinf(got)
+    alone[page, :, at] = False
+    assert not alone.any() and not torch.equal(got[page, :, at], clean[page, :, at])
+    got[page, :, at] = clean[page, :, at]
+    w.check(got, pos)
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp32", 32)])
 @pytest.mark.parametrize("new,kv", [([1, 1, 1], [5, 70, 300]), ([40, 90], [60, 150])])
 def test_weigh_strided_rows_and_interleaved_caches(lla_gpu, dtype, d, new, kv):

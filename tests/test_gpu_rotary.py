@@ -15,6 +15,7 @@ import torch
 
 import local_linear_attention_flashlla_gb300 as lla
 from oracle.cache_ref import rotary_backward_ref, rotary_ref, turn_angles
+from oracle.lla_ref import lla_grad_ref
 
 pytestmark = pytest.mark.gpu
 DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
@@ -286,3 +287,42 @@ def test_both_ways_of_marshalling_give_the_same_bits(lla_gpu, monkeypatch):
         assert len(a) == len(b) and all(x.dtype is y.dtype and torch.equal(x, y) for x, y in zip(a, b))
     two = lla.rotary_backward([dys[0]], [xs[0]], pos, table, gain=gains[0], eps=1e-6)
     assert torch.equal(one[0][0], two[0][0]) and torch.equal(one[1][0], two[1][0])
+
+
+@pytest.mark.parametrize("B,H,n,d,rot,interleaved", [(1, 2, 40, 32, 32, False), (2, 1, 33, 64, 24, True)])
+def test_training_step(lla_gpu, B, H, n, d, rot, interleaved):
+    """Rotated, normalised queries and keys through the attention and back: gradients of the unrotated rows and of the gains.
+
+    The oracle's attention gradients are taken at the rotated rows that the GPU made (checked by themselves).  dq and dk are
+    within 1e-3 of their RMS, floored at 1e-2 RMS(dout), the bound of a forward and a backward call in series; the way back through
+    rotation and norm is linear in them.
+    """
+    tau, lam, caps = d ** -0.5, 0.1, (4 * d + 64, 1e-6)
+    xs = [make((B, H, n, d), "fp32", i) for i in range(2)]
+    v, dout = make((B, H, n, d), "fp32", 2), make((B, H, n, d), "fp32", 3)
+    gains = [1 + 0.3 * make((d,), "fp32", 4 + i) for i in range(2)]
+    pos, table = torch.arange(n, dtype=torch.int32, device="cuda"), lla.rotary_table(rot)
+    kw = dict(gain=gains, eps=1e-6, interleaved=interleaved)
+    q, k = lla.rotary(xs, pos, table, **kw)
+    _, rho, denom = lla.forward(q, k, v, tau, lam, *caps, path=lla.LLA_PATH_FP32)
+    dq, dk, _ = lla.backward(q, k, v, rho, denom, dout, tau, lam, *caps, path=lla.LLA_PATH_FP32)
+    dxs, dgains = lla.rotary_backward([dq, dk], xs, pos, table, **kw)
+    torch.cuda.synchronize()
+    lla.lla_sync_status()
+    ang = angles_of(pos, table, False)
+    for x, y, gain in zip(xs, (q, k), gains):
+        check_forward(y, x, ang, table, "fp32", gain, 1e-6, interleaved)
+    grads = lla_grad_ref(f64(q), f64(k), f64(v), f64(dout), tau, lam)[:2]
+    floor = 1e-2 * np.sqrt((f64(dout) ** 2).mean())
+    for x, g, gain, dx, dgain, own in zip(xs, grads, gains, dxs, dgains, (dq, dk)):
+        check_backward(dx, dgain, own, x, ang, table, "fp32", gain, 1e-6, interleaved)
+        ref, rg = rotary_backward_ref(g, f64(x), ang, f64(gain), 1e-6, interleaved)
+        off = pair_sum(np.full(g.shape, 1e-3 * max(np.sqrt((g ** 2).mean()), floor)), rot, interleaved)
+        size = pair_sum(g, rot, interleaved)
+        s = 1 / np.sqrt((f64(x) ** 2).mean(-1, keepdims=True) + 1e-6)
+        m = np.abs(f64(x) * s)
+        h = (off + (2 * d + 64) * U * size) * np.abs(f64(gain))
+        worst = (np.abs(f64(dx) - ref) / (s * (h + m * (m * h).mean(-1, keepdims=True)) + U * np.abs(ref))).max()
+        assert worst <= 1.0, worst
+        worst = (np.abs(f64(dgain) - rg) / ((off + (B * H * n + 64 + 2 * d) * U * size) * m).reshape(-1, d).sum(0)).max()
+        assert worst <= 1.0, worst

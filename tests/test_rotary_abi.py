@@ -10,6 +10,7 @@ import torch
 import local_linear_attention_flashlla_gb300 as lla
 from local_linear_attention_flashlla_gb300 import build as lla_build
 from oracle.cache_ref import frequencies, rotary_backward_ref, rotary_ref, turn_angles
+from oracle.lla_ref import lla_grad_ref, lla_ref
 
 
 @pytest.fixture(scope="module")
@@ -151,3 +152,26 @@ def test_marshalling_module_refuses_what_does_not_fit():
     assert m.rotary(0) == m.rotary_backward() == m.weigh(1, 2) == m.evict() == m.trim(0) == -1
     with pytest.raises(TypeError):
         m.init_bounded(1)
+
+
+def test_gradient_of_rotated_attention_by_differences():
+    """The formulas of a training step (norm, rotation, attention and their gradients) against central differences in 64 bits:
+    step 1e-5, so the third derivative's term is about 1e-10 and the rounding 1e-16 / 1e-5 of the loss; 1e-6 of it is asked for."""
+    rng = np.random.default_rng(5)
+    H, n, d, rot, tau, lam = 2, 9, 8, 6, 0.4, 0.1
+    x, v, w = rng.standard_normal((2, 1, H, n, d)), rng.standard_normal((1, H, n, d)), rng.standard_normal((1, H, n, d))
+    gain = 1 + 0.2 * rng.standard_normal((2, d))
+    ang = np.arange(n)[:, None] * np.array([1.0, 0.3, 0.07])
+
+    def loss(x, gain):
+        q, k = (rotary_ref(x[i], ang, gain[i], 1e-6) for i in range(2))
+        return (lla_ref(q, k, v, tau, lam)[0].reshape(w.shape) * w).sum()
+
+    q, k = (rotary_ref(x[i], ang, gain[i], 1e-6) for i in range(2))
+    back = [rotary_backward_ref(g, x[i], ang, gain[i], 1e-6) for i, g in enumerate(lla_grad_ref(q, k, v, w, tau, lam)[:2])]
+    for _ in range(6):
+        u, g = rng.standard_normal(x.shape), rng.standard_normal(gain.shape)
+        step = 1e-5
+        diff = (loss(x + step * u, gain + step * g) - loss(x - step * u, gain - step * g)) / (2 * step)
+        own = sum((back[i][0] * u[i]).sum() + (back[i][1] * g[i]).sum() for i in range(2))
+        assert abs(diff - own) <= 1e-6 * max(1.0, sum(np.abs(back[i][0] * u[i]).sum() for i in range(2)))
