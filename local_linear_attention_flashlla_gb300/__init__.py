@@ -1004,9 +1004,9 @@ def _rotary_call(x, dy, positions, table, gain, eps, cu_q, shift, out, backward)
             if eps is None:
                 raise _bad("a gain goes with the normalisation: give eps")
             r.gain = _ints("gain", gains[i], (d,), f32, dev)
-    eps = -1.0 if eps is None else float(eps)
-    if eps < 0.0 and any(g is not None for g in gains):
+    if eps is not None and not float(eps) >= 0.0:
         raise _bad("eps must be >= 0")
+    eps = -1.0 if eps is None else float(eps)
     return (dtype, LLA_DTYPE_BF16 if dy_dt is torch.bfloat16 else LLA_DTYPE_FP32, rows, count, B, n, d, pos_ptr, position_stride,
             turns_ptr, table.dim, float(table.magnitude), eps, cu_ptr, shift_ptr, S, outs, gains, keep)
 
@@ -1133,6 +1133,14 @@ def _weigh_workspace_bytes(device_index, dtype, Hq, Hkv, d, page_size, max_new):
     return lla_paged_weigh_workspace_size(dtype, 1, 1, Hq, Hkv, d, page_size, 1, max_new)
 
 
+def _int_arg(name, x):
+    """x as a C int: a larger one would lose its upper bits on the way."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise _bad(f"{name} must fit 32 bits (got {x})")
+    return x
+
+
 def _check_cache(cache):
     """(num_pages, Hkv, page_size, d, page stride, lla dtype) of one cache."""
     return _check_caches(cache, cache)
@@ -1171,7 +1179,7 @@ def paged_weigh(q, lse, k_cache, scores, block_table, cu_q, kv_lens, tau, max_ne
         raise _bad(f"q must be [T, Hq, d] and block_table [S, W], got {tuple(q.shape)}, {tuple(block_table.shape)}")
     T, Hq, _ = q.shape
     S, W = block_table.shape
-    i32, f32, max_new = torch.int32, torch.float32, int(max_new)
+    i32, f32, max_new = torch.int32, torch.float32, _int_arg("max_new", max_new)
     q, qs = _token_rows(q, "q", k_cache, Hq, d)
     lse_ptr, scores_ptr = _ints("lse", lse, (T, Hq), f32, dev), _ints("scores", scores, (P, Hkv, Z), f32, dev)
     out = scores if out is None else _same("out", out, (P, Hkv, Z), f32, dev)
@@ -1188,7 +1196,7 @@ def paged_weigh(q, lse, k_cache, scores, block_table, cu_q, kv_lens, tau, max_ne
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
     lla_paged_weigh(dtype, q.data_ptr(), lse_ptr, k_cache.data_ptr(), scores_ptr, out.data_ptr(), pos_ptr, drop_ptr, table_ptr,
-                    cu_ptr, kv_ptr, T, S, Hq, Hkv, d, Z, P, W, max_new, qs, page_stride, float(tau), float(decay), int(last),
+                    cu_ptr, kv_ptr, T, S, Hq, Hkv, d, Z, P, W, max_new, qs, page_stride, float(tau), float(decay), _int_arg("last", last),
                     1 if causal else 0, workspace.data_ptr(), ws_bytes, stream_ptr)
     return out
 
@@ -1228,7 +1236,8 @@ def paged_evict(scores, k_cache, v_cache, block_table, kv_lens, keep, *, positio
     lla_paged_evict(dtype, scores_ptr, scores_out_ptr, pos_ptr, pos_out_ptr, k_cache.data_ptr(), v_cache.data_ptr(),
                     _ints("block_table", block_table, (S, W), i32, dev), _ints("kv_lens", kv_lens, (S,), i32, dev),
                     _ints("keep", keep, (S,), i32, dev), None if dropped is None else _ints("dropped", dropped, (S,), i32, dev),
-                    S, Hkv, d, Z, P, W, page_stride, int(sinks), int(recent), torch._C._cuda_getCurrentRawStream(dev.index))
+                    S, Hkv, d, Z, P, W, page_stride, _int_arg("sinks", sinks), _int_arg("recent", recent),
+                    torch._C._cuda_getCurrentRawStream(dev.index))
 
 
 PagedTrim = namedtuple("PagedTrim", "kv_lens dropped free_left")
@@ -1269,6 +1278,6 @@ def paged_trim(kv_lens, keep, block_table, free_pages, free_count, page_size, *,
     new_lens = like(kv_lens) if new_lens is None else _same("new_lens", new_lens, (S,), i32, dev)
     new_dropped = like(kv_lens) if new_dropped is None else _same("new_dropped", new_dropped, (S,), i32, dev)
     free_left = like(free_count) if free_left is None else _same("free_left", free_left, (1,), i32, dev)
-    lla_paged_trim(kv_ptr, keep_ptr, S, int(page_size), table_ptr, W, free_ptr, F, count_ptr, drop_ptr, new_lens.data_ptr(),
-                   new_dropped.data_ptr(), free_left.data_ptr(), torch._C._cuda_getCurrentRawStream(dev.index))
+    lla_paged_trim(kv_ptr, keep_ptr, S, _int_arg("page_size", page_size), table_ptr, W, free_ptr, F, count_ptr, drop_ptr,
+                   new_lens.data_ptr(), new_dropped.data_ptr(), free_left.data_ptr(), torch._C._cuda_getCurrentRawStream(dev.index))
     return PagedTrim(new_lens, new_dropped, free_left)

@@ -280,7 +280,7 @@ def test_weigh_binding_refusals(lla_gpu):
     for bad in (dict(q=f["q"].float()), dict(q=f["q"][:, :3]), dict(q=f["q"][0]), dict(lse=f["lse"][:, :2]), dict(lse=f["lse"].double()),
                 dict(scores=f["scores"][:2]), dict(scores=f["scores"].half()), dict(out=f["scores"][:, :1]), dict(positions=f["scores"]),
                 dict(dropped=f["dropped"].long()), dict(block_table=f["block_table"][0]), dict(cu_q=f["cu_q"][:2]), dict(kv_lens=f["kv_lens"].cpu()),
-                dict(tau=0.0), dict(decay=-1.0), dict(last=-2), dict(max_new=0), dict(k_cache=f["k_cache"].cpu()), dict(k_cache=f["k_cache"].half()),
+                dict(tau=0.0), dict(decay=-1.0), dict(last=-2), dict(last=2 ** 32), dict(max_new=0), dict(max_new=2 ** 32 + 5), dict(k_cache=f["k_cache"].cpu()), dict(k_cache=f["k_cache"].half()),
                 dict(workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(lla.LLAError):
             lla.paged_weigh(**{**f, **bad})
@@ -440,7 +440,7 @@ def test_evict_binding_refusals(lla_gpu):
     f = dict(scores=e.scores.cuda(), k_cache=e.kc.cuda(), v_cache=e.vc.cuda(), block_table=_i32(e.table), kv_lens=_i32([30]), keep=_i32([9]))
     for bad in (dict(scores=f["scores"].double()), dict(scores=f["scores"][:1]), dict(scores_out=f["scores"].cpu()), dict(positions=f["scores"]),
                 dict(v_cache=f["v_cache"].float()), dict(v_cache=f["v_cache"][:, :1]), dict(block_table=f["block_table"][0]), dict(keep=f["keep"].long()),
-                dict(keep=_i32([9, 9])), dict(kv_lens=f["kv_lens"].cpu()), dict(sinks=1), dict(recent=1), dict(recent=-1), dict(dropped=f["scores"]),
+                dict(keep=_i32([9, 9])), dict(kv_lens=f["kv_lens"].cpu()), dict(sinks=1), dict(recent=1), dict(recent=-1), dict(sinks=2 ** 32), dict(recent=-2 ** 32), dict(dropped=f["scores"]),
                 dict(positions_out=torch.zeros_like(f["scores"], dtype=torch.int32))):
         with pytest.raises(lla.LLAError):
             lla.paged_evict(**{**f, **bad})
@@ -501,7 +501,7 @@ def test_trim_lengths_beyond_the_table_and_refusals(lla_gpu):
         lla.lla_sync_status()
     assert r.kv_lens.tolist() == [5, 0] and r.dropped.tolist() == [27, 0] and f["free_pages"].tolist()[:1] == [2] and r.free_left.tolist() == [1]
     for bad in (dict(keep=_i32([5])), dict(kv_lens=f["kv_lens"].long()), dict(block_table=_i32([1, 2])), dict(block_table=_i32([[1, 2]])),
-                dict(free_pages=f["free_pages"].cpu()), dict(free_count=_i32([0, 0])), dict(page_size=12), dict(dropped=_i32([1])),
+                dict(free_pages=f["free_pages"].cpu()), dict(free_count=_i32([0, 0])), dict(page_size=12), dict(page_size=2 ** 32 + 16), dict(dropped=_i32([1])),
                 dict(new_lens=_i32([1])), dict(new_dropped=f["kv_lens"].float()), dict(free_left=_i32([]))):
         with pytest.raises(lla.LLAError):
             lla.paged_trim(**{**f, **bad})

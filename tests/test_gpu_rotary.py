@@ -242,6 +242,7 @@ def test_binding_refusals(lla_gpu):
     bad = [lambda: lla.rotary(x, pos.long(), t), lambda: lla.rotary(x, pos[:3], t), lambda: lla.rotary(x, pos.cpu(), t),
            lambda: lla.rotary(x.half(), pos, t), lambda: lla.rotary(x[0], pos, t), lambda: lla.rotary([x, x.float()], pos, t),
            lambda: lla.rotary([x, x[:3]], pos, t), lambda: lla.rotary(x, pos, t, gain=gain), lambda: lla.rotary(x, pos, t, eps=-1.0, gain=gain),
+           lambda: lla.rotary(x, pos, t, eps=-1.0), lambda: lla.rotary(x, pos, t, eps=float("nan")), lambda: lla.rotary_backward(x, x, pos, t, eps=-1.0),
            lambda: lla.rotary(x, pos, t, eps=0.0, gain=gain[:32]), lambda: lla.rotary(x, pos, t, eps=0.0, gain=gain.bfloat16()),
            lambda: lla.rotary([x, x], pos, t, eps=0.0, gain=[gain]), lambda: lla.rotary(x, pos, t, out=torch.empty_like(x).float()),
            lambda: lla.rotary(x, pos, t, out=torch.empty(4, 2, 65, device="cuda", dtype=torch.bfloat16)[..., 1:]),
