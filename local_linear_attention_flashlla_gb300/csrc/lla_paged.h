@@ -115,7 +115,6 @@ struct Work {
     PartHeader* hdr;
     float* part;
     unsigned* err;
-    float* lse;                       // [T, Hq], or null
 };
 
 inline Work make_work(const PagedProblem& p, const PagedSplit& sp) {
@@ -132,7 +131,6 @@ inline Work make_work(const PagedProblem& p, const PagedSplit& sp) {
     w.hdr = static_cast<PartHeader*>(p.ws);
     w.part = reinterpret_cast<float*>(static_cast<char*>(p.ws) + (size_t)kPagedMaxCtas * sizeof(PartHeader));
     w.err = p.err;
-    w.lse = p.lse;
     return w;
 }
 
@@ -457,8 +455,8 @@ __device__ __forceinline__ float* part_element(float4* sums, int rows, int d, in
 
 // A row's logsumexp of its scaled logits, from its exponents' reference point (log2) and its weights' sum; a row that
 // sees no key has m = -inf and om = 0, and gets -inf.
-__device__ __forceinline__ void put_lse(const Work& w, long long token, int head, float m, float om) {
-    if (w.lse) w.lse[token * (w.Hkv * w.G) + head] = (m + log2f(om)) * 0.6931471805599453f;
+__device__ __forceinline__ void put_lse(const Work& w, float* lse, long long token, int head, float m, float om) {
+    if (lse) lse[token * (w.Hkv * w.G) + head] = (m + log2f(om)) * 0.6931471805599453f;
 }
 
 // This CTA's header: written once by every CTA, with the tile that it starts and others finish (its

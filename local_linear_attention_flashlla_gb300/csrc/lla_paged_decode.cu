@@ -81,6 +81,7 @@ struct DecArgs {
     int Hq, slices;                            // slices: head slices from page to page
     long long q_stride, r_stride;
     float scale;                               // tau log2(e)
+    float* lse;                                // [T, Hq], or null
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     T* out = static_cast<T*>(a.out) + ((long long)token * a.Hq + head) * D + c2;
 #pragma unroll
                     for (int n = 0; n < NT; ++n) put2(out + n * 8, c1 * o[n][0] - inv * o[n][2], c1 * o[n][1] - inv * o[n][3]);
-                    if (c2 == 0) put_lse(w, token, head, m, om);
+                    if (c2 == 0) put_lse(w, a.lse, token, head, m, om);
                 } else {
                     float4* ps = part_sums(w, blockIdx.x, p.slot, D);
 #pragma unroll
@@ -511,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     const float inv = ow != 0.f ? 1.f / ow : 0.f, c1 = (1.f + aw * inv) * inv;
                     put4(static_cast<T*>(a.out) + ((long long)(p.q.token0 + tk) * a.Hq + p.h * w.G + er - tk * w.G) * D + c,
                          c1 * x1.x - inv * x2.x, c1 * x1.y - inv * x2.y, c1 * x1.z - inv * x2.z, c1 * x1.w - inv * x2.w);
-                    if (c == 0) put_lse(w, p.q.token0 + tk, p.h * w.G + er - tk * w.G, mm, ow);
+                    if (c == 0) put_lse(w, a.lse, p.q.token0 + tk, p.h * w.G + er - tk * w.G, mm, ow);
                 } else {
                     float4* ps = part_sums(w, blockIdx.x, p.slot, D) + (size_t)(c / 4) * R + row;
                     ps[0] = x1;
@@ -578,7 +579,7 @@ cudaError_t launch_paged_decode(const PagedProblem& p, const PagedSplit& sp, cud
         return cudaErrorInvalidValue;
     }
     paged::DecArgs a{paged::make_work(p, sp), p.q, p.probe, p.out, p.Hq, (int)paged::slices_of_page(p), p.q_stride, p.r_stride,
-                     p.tau * 1.4426950408889634f};
+                     p.tau * 1.4426950408889634f, p.lse};
     if (p.dtype == LLA_DTYPE_FP32)
         return p.d == 64 ? paged::launch_dec<float, 64>(a, mk, mv, stream) : paged::launch_dec<float, 32>(a, mk, mv, stream);
     return p.d == 128 ? paged::launch_dec<__nv_bfloat16, 128>(a, mk, mv, stream)

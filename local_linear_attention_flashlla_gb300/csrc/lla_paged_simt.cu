@@ -58,6 +58,7 @@ struct SimtArgs {
     int Hq;
     long long q_stride, r_stride, page_stride;
     float scale;     // tau log2(e)
+    float* lse;      // [T, Hq], or null
 };
 
 // 16 bytes of T as floats.
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_simt_few_kernel(SimtArgs a)
                     const int c = (tx + TX * (i / VW)) * VW + i % VW;
                     if (D % TX == 0 || c < D) put(o + c, (c1 * o1[i] - o2[i]) * inv);
                 }
-                if (tx == 0) put_lse(w, token, head, m, om);
+                if (tx == 0) put_lse(w, a.lse, token, head, m, om);
             } else {
                 if (tx == 0) part_stats(w, blockIdx.x, p.slot, D)[row] = make_float4(m, om, A, s0);
                 float4* ps = part_sums(w, blockIdx.x, p.slot, D);
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(kManyThreads, ManyShape<D>::kCtas) paged_simt_
                 T* o = static_cast<T*>(a.out) + ((long long)(p.q.token0 + tk) * a.Hq + p.h * w.G + fr - tk * w.G) * D;
                 float4* ps = p.slot >= 0 ? part_sums(w, blockIdx.x, p.slot, D) : nullptr;
                 if (p.slot >= 0 && g8 == 0) part_stats(w, blockIdx.x, p.slot, D)[r] = make_float4(m[i], om[i], A[i], s0[i]);
-                if (p.slot < 0 && g8 == 0) put_lse(w, p.q.token0 + tk, p.h * w.G + fr - tk * w.G, m[i], om[i]);
+                if (p.slot < 0 && g8 == 0) put_lse(w, a.lse, p.q.token0 + tk, p.h * w.G + fr - tk * w.G, m[i], om[i]);
                 const float inv = om[i] != 0.f ? 1.f / om[i] : 0.f, c1 = 1.f + A[i] * inv;
 #pragma unroll
                 for (int n = 0; n < CPT / 2; ++n) {
@@ -562,7 +563,7 @@ struct MergeShape {
 };
 
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(256, 5) paged_merge_kernel(Work w, T* __restrict__ out, int Hq) {
+__global__ void __launch_bounds__(256, 5) paged_merge_kernel(Work w, T* __restrict__ out, int Hq, float* __restrict__ lse) {
     using Sh = MergeShape<D, R>;
     constexpr int kItems = Sh::kItems, kLanes = Sh::kLanes, kHeld = Sh::kHeld, kChunk = Sh::kChunk;
     __shared__ float2 fac[kChunk][kMergeRows];
@@ -605,9 +606,9 @@ __global__ void __launch_bounds__(256, 5) paged_merge_kernel(Work w, T* __restri
         A += __shfl_xor_sync(0xffffffffu, A, o);
     }
     const float inv = om != 0.f ? 1.f / om : 0.f, c1 = 1.f + A * inv;   // om 0: no key in any part; NaN stays NaN
-    if (live && ln == 0 && c0 == 0) {
+    if (lse && live && ln == 0 && c0 == 0) {                 // (base: 0 where om is 0)
         const int fr = h.row0 + row, tk = over_g(w, fr);
-        put_lse(w, h.token0 + tk, h.head * w.G + fr - tk * w.G, m, om);
+        put_lse(w, lse, h.token0 + tk, h.head * w.G + fr - tk * w.G, base, om);
     }
 
     const int r = tid % kMergeRows, c4 = c0 + tid / kMergeRows % Sh::kC, lane = tid / kItems;
@@ -685,29 +686,29 @@ cudaError_t launch_bf16(const SimtArgs& a, int d, cudaStream_t stream) {
 }
 
 template <typename T, int D, int R>
-cudaError_t merge_one(const Work& w, void* out, int Hq, cudaStream_t stream) {
+cudaError_t merge_one(const Work& w, void* out, int Hq, float* lse, cudaStream_t stream) {
     return launch_after(paged_merge_kernel<T, D, R>, dim3(w.ctas, MergeShape<D, R>::kBlocks), 256, 0, stream, w,
-                        static_cast<T*>(out), Hq);
+                        static_cast<T*>(out), Hq, lse);
 }
 
 template <typename T, int D>
-cudaError_t merge_rows(const Work& w, void* out, int Hq, cudaStream_t stream) {
+cudaError_t merge_rows(const Work& w, void* out, int Hq, float* lse, cudaStream_t stream) {
     switch (w.rows) {
-        case 8: return merge_one<T, D, 8>(w, out, Hq, stream);
-        case 16: return merge_one<T, D, 16>(w, out, Hq, stream);
-        case 32: return merge_one<T, D, 32>(w, out, Hq, stream);
-        case 128: return merge_one<T, D, 128>(w, out, Hq, stream);
+        case 8: return merge_one<T, D, 8>(w, out, Hq, lse, stream);
+        case 16: return merge_one<T, D, 16>(w, out, Hq, lse, stream);
+        case 32: return merge_one<T, D, 32>(w, out, Hq, lse, stream);
+        case 128: return merge_one<T, D, 128>(w, out, Hq, lse, stream);
     }
     return cudaErrorInvalidValue;
 }
 
 template <typename T>
-cudaError_t merge_typed(const Work& w, void* out, int Hq, int d, cudaStream_t stream) {
+cudaError_t merge_typed(const Work& w, void* out, int Hq, float* lse, int d, cudaStream_t stream) {
     switch (d) {
-        case 16: return merge_rows<T, 16>(w, out, Hq, stream);
-        case 32: return merge_rows<T, 32>(w, out, Hq, stream);
-        case 64: return merge_rows<T, 64>(w, out, Hq, stream);
-        default: return merge_rows<T, 128>(w, out, Hq, stream);
+        case 16: return merge_rows<T, 16>(w, out, Hq, lse, stream);
+        case 32: return merge_rows<T, 32>(w, out, Hq, lse, stream);
+        case 64: return merge_rows<T, 64>(w, out, Hq, lse, stream);
+        default: return merge_rows<T, 128>(w, out, Hq, lse, stream);
     }
 }
 
@@ -723,14 +724,14 @@ PagedSplit paged_simt_split(const PagedProblem& p, int sms) {
 
 cudaError_t launch_paged_simt(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream) {
     paged::SimtArgs a{paged::make_work(p, sp), p.q, p.probe, p.k, p.v, p.out, p.Hq, p.q_stride, p.r_stride,
-                      p.page_stride, p.tau * 1.4426950408889634f};
+                      p.page_stride, p.tau * 1.4426950408889634f, p.lse};
     return p.dtype == LLA_DTYPE_BF16 ? paged::launch_bf16(a, p.d, stream) : paged::launch_fp32(a, p.d, stream);
 }
 
 cudaError_t launch_paged_merge(const PagedProblem& p, const PagedSplit& sp, cudaStream_t stream) {
     const paged::Work w = paged::make_work(p, sp);
-    return p.dtype == LLA_DTYPE_BF16 ? paged::merge_typed<__nv_bfloat16>(w, p.out, p.Hq, p.d, stream)
-                                     : paged::merge_typed<float>(w, p.out, p.Hq, p.d, stream);
+    return p.dtype == LLA_DTYPE_BF16 ? paged::merge_typed<__nv_bfloat16>(w, p.out, p.Hq, p.lse, p.d, stream)
+                                     : paged::merge_typed<float>(w, p.out, p.Hq, p.lse, p.d, stream);
 }
 
 }  // namespace lla

@@ -57,6 +57,7 @@ struct TcArgs {
     long long q_stride, r_stride;
     float scale;                               // tau log2(e)
     int row_boxes;                             // 128 is a multiple of G: a tile's rows are whole tokens
+    float* lse;                                // [T, Hq], or null
 };
 
 constexpr int kRing = 4;                       // pieces published ahead
@@ -649,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (r < p.rows && half == 0) {
                 if (p.slot >= 0) part_stats(w, blockIdx.x, p.slot, D)[r] = make_float4(m, om, A, s0);
-                else put_lse(w, p.q.token0 + tk, p.h * w.G + p.row0 + r - tk * w.G, m, om);
+                else put_lse(w, a.lse, p.q.token0 + tk, p.h * w.G + p.row0 + r - tk * w.G, m, om);
             }
             tc_fence_before();                 // O is read: the next tile's products may write it (after p1)
             __syncwarp();
@@ -697,7 +698,7 @@ cudaError_t launch_paged_tc(const PagedProblem& p, const PagedSplit& sp, cudaStr
     }
     paged::TcArgs a{paged::make_work(p, sp), static_cast<const __nv_bfloat16*>(p.q), static_cast<const __nv_bfloat16*>(p.probe),
                     static_cast<__nv_bfloat16*>(p.out), p.Hq, (int)paged::slices_of_page(p), p.q_stride, p.r_stride,
-                    p.tau * 1.4426950408889634f, boxes};
+                    p.tau * 1.4426950408889634f, boxes, p.lse};
     return p.d == 128 ? paged::launch_tc<128>(a, m, stream) : paged::launch_tc<64>(a, m, stream);
 }
 
