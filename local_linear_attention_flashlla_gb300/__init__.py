@@ -1025,8 +1025,8 @@ def rotary(x, positions, table, *, gain=None, eps=None, interleaved=False, cu_q=
     import torch
     many = isinstance(x, (tuple, list))
     if stream is None and out is None and isinstance(table, RotaryTable) and table.turns.is_cuda and _bind():
-        index = torch.cuda.current_device()
-        res = tuple([t.new_empty(t.shape) for t in x]) if many else x.new_empty(x.shape)
+        index, fresh, packed = torch.cuda.current_device(), torch.empty_like, torch.contiguous_format
+        res = tuple([fresh(t, memory_format=packed) for t in x]) if many else fresh(x, memory_format=packed)
         if _BIND.rotary(index, x, positions, table.turns, table.dim, table.magnitude, gain, eps, interleaved, cu_q, shift, res,
                         torch._C._cuda_getCurrentRawStream(index)) == LLA_OK:
             return res
@@ -1059,9 +1059,10 @@ def rotary_backward(dy, x, positions, table, *, gain=None, eps=None, interleaved
         t = _SCRATCH.get((index, stream_ptr, threading.get_ident()))
         if gain is None or (t is not None and not torch.cuda.is_current_stream_capturing()):
             like = dy if x is None else x
-            res = tuple([r.new_empty(r.shape) for r in like]) if many else like.new_empty(like.shape)
-            grads = None if gain is None else gain.new_empty(gain.shape) if torch.is_tensor(gain) else \
-                tuple([None if g is None else g.new_empty(g.shape) for g in gain])
+            fresh, packed = torch.empty_like, torch.contiguous_format
+            res = tuple([fresh(r, memory_format=packed) for r in like]) if many else fresh(like, memory_format=packed)
+            grads = None if gain is None else fresh(gain, memory_format=packed) if torch.is_tensor(gain) else \
+                tuple([None if g is None else fresh(g, memory_format=packed) for g in gain])
             if _BIND.rotary_backward(index, dy, x, positions, table.turns, table.dim, table.magnitude, gain, eps, interleaved, cu_q,
                                      shift, res, grads, 0 if t is None else t.data_ptr(), 0 if t is None else t.numel(),
                                      stream_ptr) == LLA_OK:
