@@ -55,7 +55,7 @@ struct Args {
     int Hq, slices;                                // slices: head slices from page to page
     long long q_stride;
     float scale;                                   // tau log2(e)
-    int row_boxes;                                 // 128 is a multiple of G: a block's rows are whole tokens
+    int row_boxes;                                 // rows of a box where 128 is a multiple of G (a block's rows are whole tokens), else 0
 };
 
 struct Shared {
@@ -112,7 +112,7 @@ __device__ void feed(const Args& a, Walk wk, const CUtensorMap* mk, const CUtens
             ok = __all_sync(0xffffffffu, mbar_wait(&b.qempty[sq], ((nq / kQ) & 1) ^ 1, &b.err));
             if (!ok) break;
             if (lane == 0) {
-                mbar_arrive_expect_tx(&b.qfull[sq], Sh::kRowTile);
+                mbar_arrive_expect_tx(&b.qfull[sq], (uint32_t)(a.row_boxes * D * 2));
                 const int token = p.q.token0 + p.q.first + over_g(w, j * kTileRows);
 #pragma unroll
                 for (int x = 0; x < D / 64; ++x)
@@ -188,63 +188,81 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
 
-// Each block's numbers, and its rows where boxes cannot bring them.
+// Each block's numbers, and its rows where boxes cannot bring them.  The logsumexps come a block ahead: where a tile
+// has one block their latency bounded it (64 x 8 key heads at 3000 to 4096 keys, 32 rows: 104 us, so 93).
 template <int D>
 __device__ void lay_out(const Args& a, Walk wk, uint32_t qring, unsigned char* tails, Shared& b) {
     const Work& w = a.w;
     const int t = threadIdx.x - (kThreads - kLoad), lane = threadIdx.x & 31, warp = t >> 5;
-    bool ok = true;
-    int n = 0;
-    Piece p;
-    while (ok && next_piece(w, wk, p)) {
-        const int rows = rows_of(w, p.q);
-        for (int j = p.b0; j < p.b1; ++j, ++n) {
-            const int sr = n % kR, sq = n % kQ, row0 = j * kTileRows, cols = columns_of(min(rows - row0, kTileRows));
-            ok = __all_sync(0xffffffffu, mbar_wait(&b.rempty[sr], ((n / kR) & 1) ^ 1, &b.err));
-            if (!ok) break;
-            int all = 0x7fffffff;
+    constexpr int E = kTileRows / kLoad;
+    Piece next;
+    bool ok = true, more = next_piece(w, wk, next);
+    int jn = next.b0;
+    float yn[E];
+    auto load = [&] {
+        const int rows = rows_of(w, next.q);
 #pragma unroll
-            for (int i = 0; i < kTileRows / kLoad; ++i) {
-                const int r = i * kLoad + t, row = row0 + r;
-                float v = 0.f;
-                int limit = 0;
-                if (row < rows) {
-                    const int tk = over_g(w, row);
-                    const float y = a.lse[(long long)(p.q.token0 + p.q.first + tk) * a.Hq + p.h * w.G + row - tk * w.G];
-                    if (y != -INFINITY) {                                    // -inf: a row without weights
-                        v = __fdiv_rn(-1.4426950408889634f * y, a.scale);
-                        limit = keys_seen(w, p.q, tk);
-                    }
-                }
-                const float hi = __bfloat162float(__float2bfloat16_rn(v)), left = fabsf(hi) < INFINITY ? v - hi : 0.f;
-                const float mid = __bfloat162float(__float2bfloat16_rn(left));
-                *reinterpret_cast<uint4*>(tails + sr * kTail + tail_off(r, 0)) =
-                    make_uint4(paged::pack_bf16(hi, mid), paged::pack_bf16(left - mid, 0.f), 0u, 0u);
-                b.limit[sr][r] = limit;
-                if (r < cols) all = min(all, limit);
+        for (int i = 0; i < E; ++i) {
+            const int row = jn * kTileRows + i * kLoad + t;
+            yn[i] = -INFINITY;
+            if (more && row < rows) {
+                const int tk = over_g(w, row);
+                yn[i] = a.lse[(long long)(next.q.token0 + next.q.first + tk) * a.Hq + next.h * w.G + row - tk * w.G];
             }
-            all = __reduce_min_sync(0xffffffffu, all);
-            if (lane == 0) b.all[sr][warp] = all;
-            fence_proxy_async_smem();            // the products read the last step
+        }
+    };
+    load();
+    for (int n = 0; ok && more; ++n) {
+        const Piece p = next;
+        const int sr = n % kR, sq = n % kQ, row0 = jn * kTileRows, rows = rows_of(w, p.q), cols = columns_of(min(rows - row0, kTileRows));
+        float y[E];
+#pragma unroll
+        for (int i = 0; i < E; ++i) y[i] = yn[i];
+        if (++jn == next.b1) {
+            more = next_piece(w, wk, next);
+            jn = next.b0;
+        }
+        load();
+        ok = __all_sync(0xffffffffu, mbar_wait(&b.rempty[sr], ((n / kR) & 1) ^ 1, &b.err));
+        if (!ok) break;
+        int all = 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const int r = i * kLoad + t;
+            float v = 0.f;
+            int limit = 0;
+            if (y[i] != -INFINITY) {                                     // -inf: a row without weights, or none
+                v = __fdiv_rn(-1.4426950408889634f * y[i], a.scale);
+                limit = keys_seen(w, p.q, over_g(w, row0 + r));
+            }
+            const float hi = __bfloat162float(__float2bfloat16_rn(v)), left = fabsf(hi) < INFINITY ? v - hi : 0.f;
+            const float mid = __bfloat162float(__float2bfloat16_rn(left));
+            *reinterpret_cast<uint4*>(tails + sr * kTail + tail_off(r, 0)) =
+                make_uint4(paged::pack_bf16(hi, mid), paged::pack_bf16(left - mid, 0.f), 0u, 0u);
+            b.limit[sr][r] = limit;
+            if (r < cols) all = min(all, limit);
+        }
+        all = __reduce_min_sync(0xffffffffu, all);
+        if (lane == 0) b.all[sr][warp] = all;
+        fence_proxy_async_smem();                // the products read the last step
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b.rfull[sr]);
+        if (!a.row_boxes) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&b.qempty[sq], ((n / kQ) & 1) ^ 1, &b.err));
+            if (!ok) break;
+            constexpr int kPieces = D / 8, kStep = kLoad / kPieces;
+            const int c = t % kPieces;
+            for (int r = t / kPieces; r < cols; r += kStep) {
+                const int row = min(row0 + r, rows - 1), tk = over_g(w, row);
+                const __nv_bfloat16* src = a.q + (p.q.token0 + p.q.first + tk) * a.q_stride +
+                                           (long long)(p.h * w.G + row - tk * w.G) * D + c * 8;
+                copy16(qring + sq * Shape<D>::kRowTile + (uint32_t)((c >> 3) * (kTileRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                       src, row0 + r < rows);
+            }
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&b.rfull[sr]);
-            if (!a.row_boxes) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&b.qempty[sq], ((n / kQ) & 1) ^ 1, &b.err));
-                if (!ok) break;
-                constexpr int kPieces = D / 8, kStep = kLoad / kPieces;
-                const int c = t % kPieces;
-                for (int r = t / kPieces; r < cols; r += kStep) {
-                    const int row = min(row0 + r, rows - 1), tk = over_g(w, row);
-                    const __nv_bfloat16* src = a.q + (p.q.token0 + p.q.first + tk) * a.q_stride +
-                                               (long long)(p.h * w.G + row - tk * w.G) * D + c * 8;
-                    copy16(qring + sq * Shape<D>::kRowTile + (uint32_t)((c >> 3) * (kTileRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
-                           src, row0 + r < rows);
-                }
-                asm volatile("cp.async.wait_all;" ::: "memory");
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&b.qfull[sq]);
-            }
+            if (lane == 0) mbar_arrive(&b.qfull[sq]);
         }
     }
 }
@@ -438,7 +456,7 @@ cudaError_t launch_one(const Args& a, const CUtensorMap& mk, const CUtensorMap& 
 
 bool weigh_tc_fits(const WeighProblem& p) {
     // 32 sequences of 300 to 6000 keys, four key heads (us, this kernel and lla_weigh.cu's): 12 rows d = 128 33 and 31, 20 rows 33 and
-    // 49; at d = 64 16 rows 29 and 23, 20 rows 29 and 27; 64 x 8 key heads at 3000 to 4096 keys, 32 rows, d = 128 104 and 157
+    // 49; at d = 64 16 rows 29 and 23, 20 rows 29 and 27; 64 x 8 key heads at 3000 to 4096 keys, 32 rows, d = 128 92 and 157
     return p.dtype == LLA_DTYPE_BF16 && ((p.d == 128 && most_rows(p) > 16) || (p.d == 64 && most_rows(p) > 32));
 }
 
@@ -452,8 +470,10 @@ cudaError_t launch_weigh_tc(const WeighProblem& p, const WeighSplit& sp, cudaStr
     c.T = p.T; c.Hq = p.Hq; c.Hkv = p.Hkv; c.G = p.G; c.d = p.d; c.page_shift = p.page_shift; c.num_pages = p.num_pages;
     c.page_stride = p.page_stride;
     CUtensorMap mk = {}, mq = {};
-    const bool boxes = paged::kTileRows % p.G == 0;
-    if (!paged::make_cache_map(&mk, p.k, c) || (boxes && !paged::make_rows_map(&mq, p.q, p.q_stride, c))) {
+    // a box: no more rows than any sequence has (32 rows beside 256 keys: 21.2 us with 128, 20.9)
+    int boxes = paged::kTileRows % p.G ? 0 : paged::kTileRows;
+    while (boxes / 2 >= most_rows(p) && boxes / 2 >= 16 && boxes / 2 >= p.G) boxes /= 2;
+    if (!paged::make_cache_map(&mk, p.k, c) || (boxes && !paged::make_rows_map(&mq, p.q, p.q_stride, c, boxes))) {
         *why = "tensor map of a paged call";
         return cudaErrorInvalidValue;
     }

@@ -46,13 +46,13 @@ inline bool make_cache_map(CUtensorMap* map, const void* cache, const PagedProbl
 }
 
 constexpr int kTileRows = 128;     // query rows of a tcgen05 tile
-// Token rows [T, Hq, d] as (column, head of a group, key head, token); box: 64 columns of the G heads of 128 / G tokens.
-inline bool make_rows_map(CUtensorMap* map, const void* rows, long long stride, const PagedProblem& p) {
+// Token rows [T, Hq, d] as (column, head of a group, key head, token); box: 64 columns of the G heads of box_rows / G tokens.
+inline bool make_rows_map(CUtensorMap* map, const void* rows, long long stride, const PagedProblem& p, int box_rows = kTileRows) {
     auto enc = tensor_map_encoder();
     if (!enc) return false;
     cuuint64_t dims[4] = {(cuuint64_t)p.d, (cuuint64_t)p.G, (cuuint64_t)p.Hkv, (cuuint64_t)p.T};
     cuuint64_t strides[3] = {(cuuint64_t)p.d * 2, (cuuint64_t)p.G * p.d * 2, (cuuint64_t)stride * 2};
-    cuuint32_t box[4] = {64, (cuuint32_t)p.G, 1, (cuuint32_t)(kTileRows / p.G)};
+    cuuint32_t box[4] = {64, (cuuint32_t)p.G, 1, (cuuint32_t)(box_rows / p.G)};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(rows), dims, strides, box, estr,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
