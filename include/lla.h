@@ -539,6 +539,8 @@ size_t lla_paged_parallax_workspace_size(int dtype, int path, int T, int S, int 
  * k_cache    [num_pages, Hkv, page_size, d], pages page_stride elements apart, as there.
  * scores, scores_out  may be one array.  Only slots j < L of sequences that bring tokens are written.
  * positions  NULL, or written at the step's own tokens in causal attention: j + dropped[s] (dropped NULL: j).
+ * granted    NULL, or [S] int32: sequences of 0 are left alone.  A step whose plan may refuse sequences passes the plan's, since
+ *            their rows are not among the cached positions, whose scores and positions they would overwrite.
  * causal     as in lla_paged_parallax; with 0 the keys hold none of the step's tokens.
  * last >= 0, decay >= 0 and finite, tau in [1e-30, 1e30); all other arguments, limits and errors are those of lla_paged_parallax (no path: bf16
  * products are exact, fp32 ones as its LLA_PATH_FP32 says for d in {32, 64}, sums and weights are fp32).
@@ -546,8 +548,8 @@ size_t lla_paged_parallax_workspace_size(int dtype, int path, int T, int S, int 
  *            call at the same time.  Results do not depend on the run.
  */
 int lla_paged_weigh(int dtype, const void* q, const float* lse, const void* k_cache, const float* scores, float* scores_out,
-                    int* positions, const int* dropped, const int* block_table, const int* cu_q, const int* kv_lens, int T, int S,
-                    int Hq, int Hkv, int d, int page_size, int num_pages, int table_width, int max_new, long long q_stride,
+                    int* positions, const int* dropped, const int* block_table, const int* cu_q, const int* kv_lens,
+                    const int* granted, int T, int S, int Hq, int Hkv, int d, int page_size, int num_pages, int table_width, int max_new, long long q_stride,
                     long long page_stride, float tau, float decay, int last, int causal, void* workspace, size_t workspace_bytes,
                     void* stream);
 

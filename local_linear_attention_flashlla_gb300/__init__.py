@@ -95,7 +95,7 @@ _SIGNATURES = {
                                        _c_int, _c_int, _c_int, _c_int, _c_int, _c_int, _c_ll, _c_ll, _c_ll, _c_float,
                                        _c_int, _vp, _c_size, _vp]),
     "lla_paged_parallax_workspace_size": (_c_size, [_c_int] * 10),
-    "lla_paged_weigh": (_c_int, [_c_int] + [_vp] * 10 + [_c_int] * 9 + [_c_ll, _c_ll, _c_float, _c_float, _c_int, _c_int, _vp,
+    "lla_paged_weigh": (_c_int, [_c_int] + [_vp] * 11 + [_c_int] * 9 + [_c_ll, _c_ll, _c_float, _c_float, _c_int, _c_int, _vp,
                                  _c_size, _vp]),
     "lla_paged_weigh_workspace_size": (_c_size, [_c_int] * 9),
     "lla_paged_evict": (_c_int, [_c_int] + [_vp] * 10 + [_c_int] * 6 + [_c_ll, _c_int, _c_int, _vp]),
@@ -1101,12 +1101,12 @@ def rotary_backward(dy, x, positions, table, *, gain=None, eps=None, interleaved
 
 # -------------------------------------------------------------------------------------------------- bounded caches
 def lla_paged_weigh(dtype, q_ptr, lse_ptr, k_cache_ptr, scores_ptr, scores_out_ptr, positions_ptr, dropped_ptr, table_ptr, cu_ptr,
-                    kv_ptr, T, S, Hq, Hkv, d, page_size, num_pages, table_width, max_new, q_stride, page_stride, tau, decay, last,
+                    kv_ptr, granted_ptr, T, S, Hq, Hkv, d, page_size, num_pages, table_width, max_new, q_stride, page_stride, tau, decay, last,
                     causal, ws_ptr, ws_bytes, stream_ptr):
     """Raw entry point on device pointers (ints); raises LLAError on failure."""
     _check(load_library().lla_paged_weigh(dtype, q_ptr, lse_ptr, k_cache_ptr, scores_ptr, scores_out_ptr, positions_ptr, dropped_ptr,
-                                          table_ptr, cu_ptr, kv_ptr, T, S, Hq, Hkv, d, page_size, num_pages, table_width, max_new,
-                                          q_stride, page_stride, tau, decay, last, causal, ws_ptr, ws_bytes, stream_ptr))
+                                          table_ptr, cu_ptr, kv_ptr, granted_ptr, T, S, Hq, Hkv, d, page_size, num_pages, table_width,
+                                          max_new, q_stride, page_stride, tau, decay, last, causal, ws_ptr, ws_bytes, stream_ptr))
 
 
 def lla_paged_weigh_workspace_size(dtype, T, S, Hq, Hkv, d, page_size, table_width, max_new):
@@ -1148,14 +1148,15 @@ def _check_cache(cache):
 
 
 def paged_weigh(q, lse, k_cache, scores, block_table, cu_q, kv_lens, tau, max_new, *, positions=None, dropped=None, decay=1.0,
-                last=0, causal=True, out=None, workspace=None, stream=None):
+                last=0, causal=True, granted=None, out=None, workspace=None, stream=None):
     """Adds the attention that a step's rows gave every cached position to its score (include/lla.h, lla_paged_weigh):
     scores = decay * scores (0 for the step's own tokens) + the sum over rows of exp(tau q.k - lse).
 
     q [T, Hq, d], k_cache, block_table, cu_q, kv_lens, tau, max_new, causal: paged_parallax's, and lse [T, Hq] what it wrote.
     scores [num_pages, Hkv, page_size] fp32, updated in place or, with out, written there.  positions: None, or int32 like
     scores, given each new token's position in its sequence (slot + dropped[s]; dropped [S] int32, paged_trim's).
-    last: only rows of the last `last` tokens of a sequence count (0: all).
+    last: only rows of the last `last` tokens of a sequence count (0: all).  granted: None, or the plan's, [S] int32: sequences of 0
+    are left alone (pass it wherever the plan may refuse one: its rows would overwrite what its cached positions have).
     Returns the new scores.  Sequences without tokens in the step are left alone.  Results have the same bits every run.
     A page belongs to one sequence (of this call and of paged_evict and paged_trim).
     Asynchronous on the current (or given) stream.  workspace: as for paged_parallax.
@@ -1168,14 +1169,15 @@ def paged_weigh(q, lse, k_cache, scores, block_table, cu_q, kv_lens, tau, max_ne
         if t is not None and not torch.cuda.is_current_stream_capturing():
             res = scores if out is None else out
             if _BIND.weigh(index, q, lse, k_cache, scores, res, positions, dropped, block_table, cu_q, kv_lens, tau, max_new, decay,
-                           last, causal, t.data_ptr(), t.numel(), stream_ptr) == LLA_OK:
+                           last, causal, t.data_ptr(), t.numel(), stream_ptr, granted) == LLA_OK:
                 return res
     P, Hkv, Z, d, page_stride, dtype = _check_cache(k_cache)
     dev = k_cache.device
     if stream is not None or dev.index != torch.cuda.current_device():
         with _on_stream(dev, stream):
             return paged_weigh(q, lse, k_cache, scores, block_table, cu_q, kv_lens, tau, max_new, positions=positions,
-                               dropped=dropped, decay=decay, last=last, causal=causal, out=out, workspace=workspace)
+                               dropped=dropped, decay=decay, last=last, causal=causal, granted=granted, out=out,
+                               workspace=workspace)
     if q.dim() != 3 or block_table.dim() != 2:
         raise _bad(f"q must be [T, Hq, d] and block_table [S, W], got {tuple(q.shape)}, {tuple(block_table.shape)}")
     T, Hq, _ = q.shape
@@ -1197,7 +1199,8 @@ def paged_weigh(q, lse, k_cache, scores, block_table, cu_q, kv_lens, tau, max_ne
     else:
         ws_bytes = workspace.numel() * workspace.element_size()
     lla_paged_weigh(dtype, q.data_ptr(), lse_ptr, k_cache.data_ptr(), scores_ptr, out.data_ptr(), pos_ptr, drop_ptr, table_ptr,
-                    cu_ptr, kv_ptr, T, S, Hq, Hkv, d, Z, P, W, max_new, qs, page_stride, float(tau), float(decay), _int_arg("last", last),
+                    cu_ptr, kv_ptr, None if granted is None else _ints("granted", granted, (S,), i32, dev), T, S, Hq, Hkv, d, Z, P, W,
+                    max_new, qs, page_stride, float(tau), float(decay), _int_arg("last", last),
                     1 if causal else 0, workspace.data_ptr(), ws_bytes, stream_ptr)
     return out
 

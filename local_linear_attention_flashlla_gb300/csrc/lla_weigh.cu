@@ -390,15 +390,15 @@ size_t lla_paged_weigh_workspace_size(int dtype, int T, int S, int Hq, int Hkv, 
 }
 
 int lla_paged_weigh(int dtype, const void* q, const float* lse, const void* k_cache, const float* scores, float* scores_out,
-                    int* positions, const int* dropped, const int* block_table, const int* cu_q, const int* kv_lens, int T, int S,
-                    int Hq, int Hkv, int d, int page_size, int num_pages, int table_width, int max_new, long long q_stride,
+                    int* positions, const int* dropped, const int* block_table, const int* cu_q, const int* kv_lens,
+                    const int* granted, int T, int S, int Hq, int Hkv, int d, int page_size, int num_pages, int table_width, int max_new, long long q_stride,
                     long long page_stride, float tau, float decay, int last, int causal, void* workspace, size_t workspace_bytes,
                     void* stream_) {
     lla::set_error(LLA_OK, "");
     if (!q || !lse || !k_cache || !scores || !scores_out || !block_table || !cu_q || !kv_lens)
         return lw::failf(LLA_ERR_INVALID_ARG, "null tensor pointer");
     if (!lw::aligned(q, 16) || !lw::aligned(k_cache, 16)) return lw::failf(LLA_ERR_INVALID_ARG, "tensor pointers must be 16-byte aligned");
-    const void* words[] = {lse, scores, scores_out, positions, dropped, block_table, cu_q, kv_lens};
+    const void* words[] = {lse, scores, scores_out, positions, dropped, block_table, cu_q, kv_lens, granted};
     for (const void* x : words)
         if (!lw::aligned(x, 4)) return lw::failf(LLA_ERR_INVALID_ARG, "int32 and fp32 pointers must be 4-byte aligned");
     const int st = lw::check_sizes(dtype, T, S, Hq, Hkv, d, page_size, num_pages, table_width, max_new);
@@ -417,7 +417,7 @@ int lla_paged_weigh(int dtype, const void* q, const float* lse, const void* k_ca
 
     lla::WeighProblem p{};
     p.q = q; p.lse = lse; p.k = k_cache; p.scores = scores; p.out = scores_out; p.positions = positions; p.dropped = dropped;
-    p.table = block_table; p.cu_q = cu_q; p.kv_lens = kv_lens; p.T = T; p.S = S; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.d = d;
+    p.table = block_table; p.cu_q = cu_q; p.kv_lens = kv_lens; p.granted = granted; p.T = T; p.S = S; p.Hq = Hq; p.Hkv = Hkv; p.G = Hq / Hkv; p.d = d;
     p.page_shift = lw::page_shift_of(page_size); p.num_pages = num_pages; p.width = table_width; p.max_new = max_new;
     p.last = last; p.causal = causal != 0; p.dtype = dtype; p.q_stride = q_stride; p.page_stride = page_stride; p.tau = tau;
     p.decay = decay;

@@ -25,6 +25,7 @@ struct WeighProblem {
     const int* table;
     const int* cu_q;
     const int* kv_lens;
+    const int* granted;       // or null
     int T, S, Hq, Hkv, G, d, page_shift, num_pages, width, max_new, last, causal, dtype;
     long long q_stride, page_stride;
     float tau, decay;
@@ -67,37 +68,38 @@ struct Work {
     int* positions;
     const int* dropped;
     int T, S, Hkv, G, width, page_shift, num_pages, max_new, last, causal;
-    int ctas, extra, keys_shift, rows_shift;
+    int ctas;
+    signed char extra, keys_shift, rows_shift;
     float decay;
     paged::Divisor g;
-    WeighHeader* hdr;
-    float* part;              // [ctas][2][KT]: slot 0 a tile that an earlier CTA starts, 1 one that others finish
+    const int* granted;       // or null
+    WeighHeader* hdr;         // [kPagedMaxCtas], then parts [ctas][2][KT]: slot 0 a tile that an earlier CTA starts, 1 one that others finish
     unsigned* err;
 };
 
 inline Work make_work(const WeighProblem& p, const WeighSplit& sp) {
     Work w;
-    w.table = p.table; w.cu_q = p.cu_q; w.kv_lens = p.kv_lens; w.scores = p.scores; w.out = p.out; w.positions = p.positions;
+    w.table = p.table; w.cu_q = p.cu_q; w.kv_lens = p.kv_lens; w.granted = p.granted; w.scores = p.scores; w.out = p.out; w.positions = p.positions;
     w.dropped = p.dropped; w.T = p.T; w.S = p.S; w.Hkv = p.Hkv; w.G = p.G; w.width = p.width; w.page_shift = p.page_shift;
     w.num_pages = p.num_pages; w.max_new = p.max_new; w.last = p.last; w.causal = p.causal;
-    w.ctas = sp.ctas; w.extra = sp.extra; w.keys_shift = paged::log2_up(sp.keys); w.rows_shift = paged::log2_up(sp.rows);
+    w.ctas = sp.ctas; w.extra = (signed char)sp.extra; w.keys_shift = (signed char)paged::log2_up(sp.keys); w.rows_shift = (signed char)paged::log2_up(sp.rows);
     w.decay = p.decay;
     w.g = paged::make_divisor(p.G);
     w.hdr = static_cast<WeighHeader*>(p.ws);
-    w.part = reinterpret_cast<float*>(static_cast<char*>(p.ws) + (size_t)kPagedMaxCtas * sizeof(WeighHeader));
     w.err = p.err;
     return w;
 }
 
 __device__ __forceinline__ int over_g(const Work& w, int x) { return (int)paged::over(w.g, (unsigned)x); }
 
-// A sequence, cut to what the tensors hold (and reported where it had to be): its tokens from token0 on, those that count from
+// A sequence, cut to what the tensors hold (and reported where it had to be), one that was refused without rows: its tokens from token0 on, those that count from
 // token0 + first on (the last `last` of them), rows = (n - first) G of them to a key head.
 struct Seq {
     int token0, n, first, L;
 };
 __device__ __forceinline__ Seq load_seq(const Work& w, int s) {
     const int c0 = w.cu_q[s], c1 = w.cu_q[s + 1], kv = w.kv_lens[s];
+    const bool refused = w.granted && w.granted[s] == 0;
     Seq q;
     q.token0 = min(max(c0, 0), w.T);
     const int end = min(max(c1, q.token0), w.T);
@@ -105,6 +107,7 @@ __device__ __forceinline__ Seq load_seq(const Work& w, int s) {
     q.L = min(max(kv, 0), w.width << w.page_shift);
     q.first = w.last > 0 ? max(q.n - w.last, 0) : 0;
     if (q.token0 != c0 || q.token0 + q.n != c1 || q.L != kv) atomicOr(w.err, (unsigned)kDevErrPagedArg);
+    if (refused) q.n = 0;                            // no rows: no tiles
     return q;
 }
 __device__ __forceinline__ int rows_of(const Work& w, const Seq& q) { return (q.n - q.first) * w.G; }
@@ -276,7 +279,7 @@ __device__ __forceinline__ void put_score(const Work& w, const Seq& q, int s, in
 }
 
 __device__ __forceinline__ float* part_of(const Work& w, int cta, int slot) {
-    return w.part + (((size_t)cta * 2 + slot) << w.keys_shift);
+    return reinterpret_cast<float*>(w.hdr + kPagedMaxCtas) + (((size_t)cta * 2 + slot) << w.keys_shift);
 }
 
 }  // namespace weigh

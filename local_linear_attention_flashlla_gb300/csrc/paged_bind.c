@@ -244,8 +244,8 @@ typedef int (*rotary_fn)(int, const rotary_rows*, int, int, int, int, const void
 typedef int (*rotary_backward_fn)(int, int, const rotary_rows*, int, int, int, int, const void*, long long, const void*, int, int,
                                   float, float, const void*, const void*, int, void*, size_t, void*);
 typedef int (*weigh_fn)(int, const void*, const void*, const void*, const void*, void*, void*, const void*, const void*, const void*,
-                        const void*, int, int, int, int, int, int, int, int, int, long long, long long, float, float, int, int, void*,
-                        size_t, void*);
+                        const void*, const void*, int, int, int, int, int, int, int, int, int, long long, long long, float, float, int,
+                        int, void*, size_t, void*);
 typedef int (*evict_fn)(int, const void*, void*, const void*, void*, void*, void*, const void*, const void*, const void*, const void*,
                         int, int, int, int, int, int, long long, int, int, void*);
 typedef int (*trim_fn)(const void*, const void*, int, int, const void*, int, void*, int, const void*, const void*, void*, void*, void*,
@@ -427,13 +427,13 @@ static PyObject* rotary_backward(PyObject* self, PyObject* const* a, Py_ssize_t 
 }
 
 /* weigh(device, q, lse, k_cache, scores, out, positions or None, dropped or None, table, cu_q, kv_lens, tau, max_new, decay, last,
- * causal, workspace, workspace bytes, stream) */
+ * causal, workspace, workspace bytes, stream, granted or None) */
 static PyObject* weigh(PyObject* self, PyObject* const* a, Py_ssize_t n) {
-    Tensor q, lse, kc, vc, sc, so, pos, drop, table, cu, kv;
+    Tensor q, lse, kc, vc, sc, so, pos, drop, table, cu, kv, ok;
     long long qs, ps;
     int status = -1;
     (void)self;
-    if (n != 19) return PyLong_FromLong(-1);
+    if (n != 20) return PyLong_FromLong(-1);
     const long device = PyLong_AsLong(a[0]);
     const double tau = PyFloat_AsDouble(a[11]), decay = PyFloat_AsDouble(a[13]);
     const long long max_new = PyLong_AsLongLong(a[12]), last = PyLong_AsLongLong(a[14]);
@@ -449,13 +449,13 @@ static PyObject* weigh(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         !packed(a[5], t_fp32, device, kc.shape, 3, &so) || !vector(a[10], t_i32, device, -1, &kv))
         return PyLong_FromLong(-1);
     const long long S = kv.shape[0];
-    pos.ptr = drop.ptr = 0;
-    if ((a[6] == Py_None || packed(a[6], t_i32, device, kc.shape, 3, &pos)) && (a[7] == Py_None || vector(a[7], t_i32, device, S, &drop)) &&
+    pos.ptr = drop.ptr = ok.ptr = 0;
+    if ((a[19] == Py_None || vector(a[19], t_i32, device, S, &ok)) && (a[6] == Py_None || packed(a[6], t_i32, device, kc.shape, 3, &pos)) && (a[7] == Py_None || vector(a[7], t_i32, device, S, &drop)) &&
         vector(a[9], t_i32, device, S + 1, &cu) && matrix(a[8], t_i32, device, S, &table) && fits(q.shape[0]) && fits(q.shape[1]) && fits(S) &&
         fits(table.shape[1]) && fits(kc.shape[0]) && fits(kc.shape[1]) && fits(kc.shape[2]) && fits(max_new) && fits(last)) {
         Py_BEGIN_ALLOW_THREADS
         status = f_weigh(kc.dtype == t_bf16 ? 0 : 1, P(q.ptr), P(lse.ptr), P(kc.ptr), P(sc.ptr), P(so.ptr), P(pos.ptr), P(drop.ptr), P(table.ptr),
-                         P(cu.ptr), P(kv.ptr), (int)q.shape[0], (int)S, (int)q.shape[1], (int)kc.shape[1], (int)kc.shape[3], (int)kc.shape[2],
+                         P(cu.ptr), P(kv.ptr), P(ok.ptr), (int)q.shape[0], (int)S, (int)q.shape[1], (int)kc.shape[1], (int)kc.shape[3], (int)kc.shape[2],
                          (int)kc.shape[0], (int)table.shape[1], (int)max_new, qs, ps, (float)tau, (float)decay, (int)last, causal, P(ws),
                          ws_bytes, P(stream));
         Py_END_ALLOW_THREADS

@@ -17,17 +17,17 @@ def lib():
 
 
 def _weigh(lib, **kw):
-    a = dict(dtype=0, q=16, lse=32, kc=48, sc=64, so=64, pos=80, drop=96, table=112, cu=128, kv=144, T=4, S=2, Hq=4, Hkv=2, d=64,
+    a = dict(dtype=0, q=16, lse=32, kc=48, sc=64, so=64, pos=80, drop=96, table=112, cu=128, kv=144, ok=None, T=4, S=2, Hq=4, Hkv=2, d=64,
              page=16, P=3, W=4, max_new=2, qs=256, ps=2048, tau=0.1, decay=1.0, last=0, causal=1, ws=None, wsb=0)
     a.update(kw)
     return lib.lla_paged_weigh(a["dtype"], a["q"], a["lse"], a["kc"], a["sc"], a["so"], a["pos"], a["drop"], a["table"], a["cu"],
-                               a["kv"], a["T"], a["S"], a["Hq"], a["Hkv"], a["d"], a["page"], a["P"], a["W"], a["max_new"], a["qs"],
+                               a["kv"], a["ok"], a["T"], a["S"], a["Hq"], a["Hkv"], a["d"], a["page"], a["P"], a["W"], a["max_new"], a["qs"],
                                a["ps"], a["tau"], a["decay"], a["last"], a["causal"], a["ws"], a["wsb"], None)
 
 
 @pytest.mark.parametrize("bad", [
     dict(q=None), dict(lse=None), dict(kc=None), dict(sc=None), dict(so=None), dict(table=None), dict(cu=None), dict(kv=None),
-    dict(q=24), dict(kc=40), dict(lse=34), dict(sc=65), dict(so=66), dict(pos=81), dict(drop=98), dict(table=113), dict(T=0),
+    dict(q=24), dict(kc=40), dict(lse=34), dict(sc=65), dict(so=66), dict(pos=81), dict(drop=98), dict(ok=177), dict(table=113), dict(T=0),
     dict(S=0), dict(S=(1 << 20) + 1), dict(Hq=0), dict(Hkv=0), dict(Hq=5), dict(d=48), dict(page=7), dict(page=512), dict(P=0),
     dict(W=0), dict(W=1 << 25), dict(max_new=0), dict(qs=255), dict(qs=252), dict(ps=1024), dict(ps=2050), dict(tau=0.0), dict(tau=1e-31),
     dict(tau=float("nan")), dict(tau=float("inf")), dict(decay=-0.5), dict(decay=float("nan")), dict(decay=float("inf")), dict(last=-1),

@@ -155,6 +155,51 @@ def test_weigh_nan_and_infinity_in_masked_places(lla_gpu, dtype, d, new, kv, bad
     w.check(got, pos)
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("bf16", 64), ("fp32", 32)])
+@pytest.mark.parametrize("new,ctx,free", [([1, 1, 1, 1], [31, 16, 40, 32], 1), ([20, 90, 3, 30], [10, 50, 13, 200], 4), ([50, 1], [64, 64], 0)])
+def test_weigh_leaves_refused_sequences_alone(lla_gpu, monkeypatch, dtype, d, new, ctx, free):
+    """A plan that runs out of pages: refused sequences keep the scores and positions of what they have cached; the others' are as
+    in a call without them."""
+    page, Hq, Hkv, S = 16, 4, 2, len(new)
+    held = [-(-n // page) for n in ctx]
+    ids = np.random.default_rng(d).permutation(sum(held) + max(free, 1))
+    table, at = np.full((S, 20), -1), 0
+    for s in range(S):
+        table[s, :held[s]] = ids[at:at + held[s]]
+        at += held[s]
+    tb = _i32(table)
+    pl = lla.paged_plan(_i32(ctx), _i32(new), tb, _i32(ids[at:at + max(free, 1)]), _i32([free]), page, sum(new))
+    granted = pl.granted.tolist()
+    assert 0 in granted
+    gen = torch.Generator().manual_seed(d)
+    P, T = len(ids), sum(new)
+    kc, q = (torch.randn(sh, generator=gen).to(DT[dtype]).cuda() for sh in ((P, Hkv, page, d), (T, Hq, d)))
+    lse, old = torch.rand((T, Hq), generator=gen).cuda() + 5, torch.rand((P, Hkv, page), generator=gen).cuda()
+    args = dict(block_table=tb, cu_q=pl.cu_q, kv_lens=pl.kv_lens, tau=d ** -0.5, max_new=max(new), decay=0.5)
+    keep = [s for s in range(S) if granted[s]]
+    want, want_pos = old.clone(), torch.full((P, Hkv, page), -7, dtype=torch.int32, device="cuda")
+    if keep:
+        cu = pl.cu_q.tolist()
+        rows = torch.cat([torch.arange(cu[s], cu[s + 1]) for s in keep]).cuda()
+        lla.paged_weigh(q[rows], lse[rows], kc, want, tb[keep], _i32(np.concatenate([[0], np.cumsum([new[s] for s in keep])])),
+                        pl.kv_lens[keep], d ** -0.5, max(new), positions=want_pos, decay=0.5)
+    for way in (None, False):
+        if way is False:
+            monkeypatch.setattr(lla, "_BIND", False)
+        scores, pos = old.clone(), torch.full_like(want_pos, -7)
+        lla.paged_weigh(q, lse, kc, scores, positions=pos, granted=pl.granted, **args)
+        torch.cuda.synchronize()
+        lla.lla_sync_status()
+        for s in range(S):
+            for c in range(held[s]):
+                if not granted[s]:
+                    assert torch.equal(scores[table[s, c]], old[table[s, c]]) and (pos[table[s, c]] == -7).all()
+        # a weight's sum may be cut elsewhere: 200 rows' fp32 sums
+        assert torch.equal(pos, want_pos) and ((scores - want).abs() <= 256 * U * want.abs()).all()
+    with pytest.raises(lla.LLAError):
+        lla.paged_weigh(q, lse, kc, scores, granted=pl.granted[:1], **args)
+
+
 @pytest.mark.parametrize("dtype,d", [("bf16", 128), ("fp32", 32)])
 @pytest.mark.parametrize("new,kv", [([1, 1, 1], [5, 70, 300]), ([40, 90], [60, 150])])
 def test_weigh_strided_rows_and_interleaved_caches(lla_gpu, dtype, d, new, kv):

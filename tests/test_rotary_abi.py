@@ -143,12 +143,12 @@ def test_marshalling_module_refuses_what_does_not_fit():
         assert m.rotary(dev, (x, x), p, t, 16, 1.0, None, None, False, None, None, (x,), 0) == -1
         assert m.rotary(dev, (), p, t, 16, 1.0, None, None, False, None, None, (), 0) == -1
         assert m.rotary_backward(dev, x, x, p, t, 16, 1.0, g, 1e-6, False, None, None, x, g, 0, 0, 0) == -1
-        assert m.weigh(dev, x, x[:, :, 0], c, s, s, None, None, p[None], p, i, 1.0, 1, 1.0, 0, True, 0, 0, 0) == -1
+        assert m.weigh(dev, x, x[:, :, 0], c, s, s, None, None, p[None], p, i, 1.0, 1, 1.0, 0, True, 0, 0, 0, None) == -1
         assert m.evict(dev, s, s, None, None, c, c, p[None], i, i, None, 0, 0, 0) == -1
         assert m.trim(dev, i, i, p[None], p, i, 16, None, i, i, i, 0) == -1
     assert m.rotary(0, None, p, t, 16, 1.0, None, None, False, None, None, x, 0) == -1
     assert m.rotary(0, x, p, t, 16, "one", None, None, False, None, None, x, 0) == -1
-    assert m.weigh(0, x, x, c, s, s, None, None, p[None], p, i, "tau", 1, 1.0, 0, True, 0, 0, 0) == -1
+    assert m.weigh(0, x, x, c, s, s, None, None, p[None], p, i, "tau", 1, 1.0, 0, True, 0, 0, 0, None) == -1
     assert m.rotary(0) == m.rotary_backward() == m.weigh(1, 2) == m.evict() == m.trim(0) == -1
     with pytest.raises(TypeError):
         m.init_bounded(1)
