@@ -549,9 +549,9 @@ size_t lla_paged_parallax_workspace_size(int dtype, int path, int T, int S, int 
  */
 int lla_paged_weigh(int dtype, const void* q, const float* lse, const void* k_cache, const float* scores, float* scores_out,
                     int* positions, const int* dropped, const int* block_table, const int* cu_q, const int* kv_lens,
-                    const int* granted, int T, int S, int Hq, int Hkv, int d, int page_size, int num_pages, int table_width, int max_new, long long q_stride,
-                    long long page_stride, float tau, float decay, int last, int causal, void* workspace, size_t workspace_bytes,
-                    void* stream);
+                    const int* granted, int T, int S, int Hq, int Hkv, int d, int page_size, int num_pages, int table_width,
+                    int max_new, long long q_stride, long long page_stride, float tau, float decay, int last, int causal,
+                    void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of scratch lla_paged_weigh needs for these sizes (0 for invalid ones). */
 size_t lla_paged_weigh_workspace_size(int dtype, int T, int S, int Hq, int Hkv, int d, int page_size, int table_width, int max_new);

@@ -36,6 +36,8 @@ struct Shape {
     static constexpr int kStages = kRow >= 512 ? 3 : kRow >= 256 ? 4 : 6;
     static constexpr int kSteps = kRow / 32;                     // mma steps over d: 32 bytes of a row each
     static constexpr size_t smem = (size_t)kWarps * kStages * kStage;
+    // on an SM; named to the compiler, which else kept to 128 registers or took too many for three (64 x 16 heads at 4096: 171 us for 168)
+    static constexpr int kCtas = kRow >= 512 ? 2 : 3;
 };
 
 struct Args {
@@ -104,7 +106,7 @@ __device__ __forceinline__ bool next_tile(const Work& w, Walk& k, Piece& p, int&
 // ONE: no sequence has more than 8 RS rows to a key head, so a tile is one unit and its rows stay in registers from tile to
 // tile.  Else blocks of kBlock rows, RS sets of them at a time.
 template <typename T, int D, int RS, bool ONE>
-__global__ void __launch_bounds__(kThreads) weigh_mma_kernel(Args a) {
+__global__ void __launch_bounds__(kThreads, (Shape<T, D>::kCtas)) weigh_mma_kernel(Args a) {
     using Sh = Shape<T, D>;
     constexpr int NS = Sh::kStages, STEPS = Sh::kSteps, P = Sh::kPieces, SW = P < 8 ? P - 1 : 7;
     extern __shared__ __align__(128) unsigned char ring[];
@@ -292,15 +294,18 @@ cudaError_t launch_rows(const Args& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     return paged::launch_after(kern, dim3(a.w.ctas), kThreads, smem, stream, a);
 }
-// rows: the most that a sequence has to a key head.  Sets that stay in registers, as many as there is room for.
+// rows: the most that a sequence has to a key head.  Sets that stay in registers, as many as there is room for.  bf16 with d = 128
+// comes here with 16 rows at most, with d = 64 32 (weigh_tc_fits).
 template <typename T, int D>
 cudaError_t launch_one(const Args& a, long long rows, cudaStream_t stream) {
+    constexpr bool kTc = sizeof(T) == 2 && D >= 64;
     if (rows <= 8) return launch_rows<T, D, 1, true>(a, stream);
-    if (rows <= 16) return launch_rows<T, D, 2, true>(a, stream);
-    if constexpr (D * sizeof(T) <= 256) {
-        if (rows <= 32) return launch_rows<T, D, 4, true>(a, stream);
+    if (rows <= 16 || (kTc && D == 128)) return launch_rows<T, D, 2, true>(a, stream);
+    if constexpr (D * sizeof(T) <= 256 && !(kTc && D == 128)) {
+        if (rows <= 32 || kTc) return launch_rows<T, D, 4, true>(a, stream);
     }
-    return launch_rows<T, D, 2, false>(a, stream);
+    if constexpr (!kTc) return launch_rows<T, D, 2, false>(a, stream);
+    return cudaErrorInvalidValue;
 }
 template <typename T>
 cudaError_t launch_typed(const Args& a, int d, long long rows, cudaStream_t stream) {
@@ -359,7 +364,7 @@ WeighSplit split_of(const WeighProblem& p, int sms) { return weigh_tc_fits(p) ? 
 
 WeighSplit weigh_mma_split(const WeighProblem& p, int sms) {
     const int row = p.d * (p.dtype == LLA_DTYPE_BF16 ? 2 : 4);
-    return WeighSplit{weigh::kTile, weigh::kBlock, (row >= 512 ? 2 : 3) * sms, 0};
+    return WeighSplit{weigh::kTile, weigh::kBlock, (row >= 512 ? 2 : 3) * sms, 0};      // Shape::kCtas
 }
 
 cudaError_t launch_weigh_mma(const WeighProblem& p, const WeighSplit& sp, cudaStream_t stream) {

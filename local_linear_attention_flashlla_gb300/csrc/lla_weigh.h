@@ -79,7 +79,8 @@ struct Work {
 
 inline Work make_work(const WeighProblem& p, const WeighSplit& sp) {
     Work w;
-    w.table = p.table; w.cu_q = p.cu_q; w.kv_lens = p.kv_lens; w.granted = p.granted; w.scores = p.scores; w.out = p.out; w.positions = p.positions;
+    w.table = p.table; w.cu_q = p.cu_q; w.kv_lens = p.kv_lens; w.granted = p.granted;
+    w.scores = p.scores; w.out = p.out; w.positions = p.positions;
     w.dropped = p.dropped; w.T = p.T; w.S = p.S; w.Hkv = p.Hkv; w.G = p.G; w.width = p.width; w.page_shift = p.page_shift;
     w.num_pages = p.num_pages; w.max_new = p.max_new; w.last = p.last; w.causal = p.causal;
     w.ctas = sp.ctas; w.extra = (signed char)sp.extra; w.keys_shift = (signed char)paged::log2_up(sp.keys); w.rows_shift = (signed char)paged::log2_up(sp.rows);
@@ -92,8 +93,8 @@ inline Work make_work(const WeighProblem& p, const WeighSplit& sp) {
 
 __device__ __forceinline__ int over_g(const Work& w, int x) { return (int)paged::over(w.g, (unsigned)x); }
 
-// A sequence, cut to what the tensors hold (and reported where it had to be), one that was refused without rows: its tokens from token0 on, those that count from
-// token0 + first on (the last `last` of them), rows = (n - first) G of them to a key head.
+// A sequence, cut to what the tensors hold (and reported where it had to be), without rows where it was refused: its tokens from
+// token0 on, those that count from token0 + first on (the last `last` of them), rows = (n - first) G of them to a key head.
 struct Seq {
     int token0, n, first, L;
 };

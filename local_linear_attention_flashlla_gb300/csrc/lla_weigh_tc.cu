@@ -14,7 +14,7 @@
 // columns of a block's rows), one issues the products, two lay out each block's logsumexps and the keys that its rows see (and
 // copy its rows where 128 is not a multiple of G).  The four accumulators, two for each half, fill TMEM.
 //
-// 512 tokens over 16,384 keys, 32/4 heads, d = 128: 70.7 us, 0.99 PFLOP/s, of which 10 are the start and the join of cut tiles.  The
+// 512 tokens over 16,384 keys, 32/4 heads, d = 128: 71 us, 0.98 PFLOP/s, of which 10 are the start and the join of cut tiles.  The
 // products alone take 64 (what the issuing warp does between two of them delays the next), copies and numbers alone 42, and
 // weights beside the products slow their issue.  Tried there: eight weighing warps 76; exponentials partly on the FMA pipe 81 to
 // 102; three stages of queries 75; N = 256 with one accumulator to a half 89 (products alone 57); 512 keys to a tile 88,
@@ -455,8 +455,8 @@ cudaError_t launch_one(const Args& a, const CUtensorMap& mk, const CUtensorMap& 
 }  // namespace weigh
 
 bool weigh_tc_fits(const WeighProblem& p) {
-    // 32 sequences of 300 to 6000 keys, four key heads (us, this kernel and lla_weigh.cu's): 12 rows d = 128 33 and 31, 20 rows 33 and
-    // 49; at d = 64 16 rows 29 and 23, 20 rows 29 and 27; 64 x 8 key heads at 3000 to 4096 keys, 32 rows, d = 128 92 and 157
+    // 32 sequences of 300 to 6000 keys, four key heads (us, this kernel and lla_weigh.cu's): 12 rows d = 128 33 and 28, 20 rows 32 and
+    // 49; at d = 64 16 rows 29 and 22, 20 rows 29 and 27; 64 x 8 key heads at 3000 to 4096 keys, 32 rows, d = 128 87 and 157
     return p.dtype == LLA_DTYPE_BF16 && ((p.d == 128 && most_rows(p) > 16) || (p.d == 64 && most_rows(p) > 32));
 }
 
