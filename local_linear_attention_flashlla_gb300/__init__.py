@@ -917,6 +917,14 @@ def _listed(t, count=None, name=None):
     return got
 
 
+def _tensors(x):
+    """x as a list of as many tensors as a rotary call takes."""
+    got = _listed(x)
+    if not 1 <= len(got) <= LLA_ROTARY_MOST:
+        raise _bad(f"1 to {LLA_ROTARY_MOST} tensors expected, got {len(got)}")
+    return got
+
+
 def _head_rows(t, name, dtype, like, copy):
     """(tensor, strides of batch, head and position) of [T, heads, d] or [B, heads, n, d] rows as the kernels take them:
     contiguous rows, 16-byte strides; anything else is copied, or refused where it is written."""
@@ -924,6 +932,8 @@ def _head_rows(t, name, dtype, like, copy):
         raise _bad(f"{name} must be {tuple(like.shape)} {dtype} on {like.device}, got {tuple(t.shape)} {t.dtype} on {t.device}")
     ve = 16 // t.element_size()
     s = t.stride()
+    if not copy and any(x == 0 and n > 1 for x, n in zip(s, t.shape)):
+        raise _bad(f"{name} has rows that lie on one another")
     if s[-1] != 1 or t.data_ptr() % 16 or any(x % ve for x in s[:-1]):
         if not copy:
             raise _bad(f"{name} must have contiguous rows and 16-byte strides")
@@ -936,10 +946,8 @@ def _head_rows(t, name, dtype, like, copy):
 def _rotary_call(x, dy, positions, table, gain, eps, cu_q, shift, out, backward):
     """Checks and marshalling of rotary and rotary_backward; returns what the C calls take."""
     import torch
-    like = _listed(x if x is not None else dy)
+    like = _tensors(x if x is not None else dy)
     count, first = len(like), like[0]
-    if not 1 <= count <= LLA_ROTARY_MOST:
-        raise _bad(f"1 to {LLA_ROTARY_MOST} tensors expected, got {count}")
     if not isinstance(table, RotaryTable):
         raise _bad("table must be a RotaryTable (rotary_table)")
     xs, dys = _listed(x, count, "x"), _listed(dy, count, "dy") if backward else [None] * count
@@ -1030,7 +1038,7 @@ def rotary(x, positions, table, *, gain=None, eps=None, interleaved=False, cu_q=
         if _BIND.rotary(index, x, positions, table.turns, table.dim, table.magnitude, gain, eps, interleaved, cu_q, shift, res,
                         torch._C._cuda_getCurrentRawStream(index)) == LLA_OK:
             return res
-    first = _listed(x)[0]
+    first = _tensors(x)[0]
     if first.is_cuda and (stream is not None or first.device.index != torch.cuda.current_device()):
         with _on_stream(first.device, stream):
             return rotary(x, positions, table, gain=gain, eps=eps, interleaved=interleaved, cu_q=cu_q, shift=shift, out=out)
@@ -1073,7 +1081,7 @@ def rotary_backward(dy, x, positions, table, *, gain=None, eps=None, interleaved
                 if isinstance(grads, tuple) and all(g is None for g in grads):
                     grads = None
                 return res, grads
-    first = _listed(dy)[0]
+    first = _tensors(dy)[0]
     if first.is_cuda and (stream is not None or first.device.index != torch.cuda.current_device()):
         with _on_stream(first.device, stream):
             return rotary_backward(dy, x, positions, table, gain=gain, eps=eps, interleaved=interleaved, cu_q=cu_q, shift=shift,

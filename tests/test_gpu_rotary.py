@@ -246,7 +246,8 @@ def test_binding_refusals(lla_gpu):
            lambda: lla.rotary(x, pos, t, eps=0.0, gain=gain[:32]), lambda: lla.rotary(x, pos, t, eps=0.0, gain=gain.bfloat16()),
            lambda: lla.rotary([x, x], pos, t, eps=0.0, gain=[gain]), lambda: lla.rotary(x, pos, t, out=torch.empty_like(x).float()),
            lambda: lla.rotary(x, pos, t, out=torch.empty(4, 2, 65, device="cuda", dtype=torch.bfloat16)[..., 1:]),
-           lambda: lla.rotary(x, pos, t, shift=pos), lambda: lla.rotary(x, pos, t, shift=pos, cu_q=pos),
+           lambda: lla.rotary([], pos, t), lambda: lla.rotary_backward([], None, pos, t), lambda: lla.rotary([x] * 5, pos, t),
+           lambda: lla.rotary(x, pos, t, out=torch.empty_like(x)[:1].expand(4, 2, 64)), lambda: lla.rotary(x, pos, t, shift=pos), lambda: lla.rotary(x, pos, t, shift=pos, cu_q=pos),
            lambda: lla.rotary(x, pos, lla.rotary_table(128)), lambda: lla.rotary(make((4, 2, 48), "bf16"), pos, lla.rotary_table(48)),
            lambda: lla.rotary(x[:0], pos[:0], t), lambda: lla.rotary_backward(x, x, pos[:2], t),
            lambda: lla.rotary_backward(x.half(), x, pos, t), lambda: lla.rotary_backward(x[:, :1], x, pos, t),
@@ -327,3 +328,18 @@ def test_training_step(lla_gpu, B, H, n, d, rot, interleaved):
         assert worst <= 1.0, worst
         worst = (np.abs(f64(dgain) - rg) / ((off + (B * H * n + 64 + 2 * d) * U * size) * m).reshape(-1, d).sum(0)).max()
         assert worst <= 1.0, worst
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_broadcast_inputs(lla_gpu, dtype):
+    """Rows that are one row repeated: a gradient of ones expanded, and x the same for all heads or positions."""
+    B, H, n, d = 2, 3, 21, 64
+    pos, table = torch.arange(n, dtype=torch.int32, device="cuda"), lla.rotary_table(d)
+    gain = 1 + 0.3 * make((d,), "fp32", 3)
+    ones = torch.ones((), dtype=DT[dtype], device="cuda").expand(B, H, n, d)
+    ang = angles_of(pos, table, False)
+    for x in (make((B, 1, n, d), dtype).expand(B, H, n, d), make((B, H, 1, d), dtype, 1).expand(B, H, n, d), make((1, H, n, d), dtype, 2).expand(B, H, n, d)):
+        check_forward(lla.rotary(x, pos, table, gain=gain, eps=1e-6), x, ang, table, dtype, gain, 1e-6, False)
+        for dy in (ones, ones.float(), make((B, 1, 1, d), dtype, 5).expand(B, H, n, d)):
+            dx, dgain = lla.rotary_backward(dy, x, pos, table, gain=gain, eps=1e-6)
+            check_backward(dx, dgain, dy, x, ang, table, dtype, gain, 1e-6, False)
