@@ -69,7 +69,7 @@ struct Work {
     const int* dropped;
     int T, S, Hkv, G, width, page_shift, num_pages, max_new, last, causal;
     int ctas;
-    signed char extra, keys_shift, rows_shift;
+    signed char extra, keys_shift, rows_shift;      // (three ints: 64 x 8 key heads with 32 rows 92 us for 87)
     float decay;
     paged::Divisor g;
     const int* granted;       // or null
