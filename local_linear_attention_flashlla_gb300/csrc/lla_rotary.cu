@@ -248,8 +248,8 @@ __device__ __forceinline__ Item item_of(const Args& a, long long w, int group) {
 }
 
 // A warp has one item; the rows of U heads are loaded to registers together.  Train shape (16 + 16 heads of 128, 8 x 4096): 90 us, 6.0
-// TB/s, 0.89 of a plain copy's bandwidth.  Tried there: one head at a time 109, three blocks to an SM 108 to 139, a persistent
-// kernel with the rows through shared memory, as the gradient's, 96 (more rows in flight, more mixing of reads and writes).
+// TB/s, 0.89 of a plain copy's bandwidth.  Tried there: three blocks to an SM 108 to 139, a persistent kernel with
+// the rows through shared memory, as the gradient's, 96, and 117 to 123 with three blocks.
 template <typename T, int D, int F>
 __global__ void __launch_bounds__(kThreads, 2) rotary_kernel(const __grid_constant__ Args a) {
     using Ln = Lane<T, D, F>;
