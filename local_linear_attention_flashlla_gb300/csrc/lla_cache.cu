@@ -318,10 +318,10 @@ __global__ void __launch_bounds__(T, 1024 / T) paged_evict_kernel(EvictArgs a) {
         int mine = 0;
         for (int q = tid; 4 * q < p.b; q += T) mine += __popc(equal(rank(q)) & within(q, 0, p.b));
         mine = __reduce_add_sync(0xffffffffu, mine);
-        if (lane == 0) sh.red[warp] = mine;
+        if (lane == 0) sh.red2[warp] = mine;         // (not to sh.red: without a histogram another warp may still read its counts)
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < W; ++i) mover.tied += sh.red[i];
+        for (int i = 0; i < W; ++i) mover.tied += sh.red2[i];
         __syncthreads();
     }
     auto refill = [&](Side& d, bool holes, int begin, int end) {
