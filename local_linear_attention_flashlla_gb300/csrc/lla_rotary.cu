@@ -21,6 +21,7 @@
 #include "../../include/lla.h"
 #include "lla_internal.h"
 #include "lla_paged.h"
+#include "rotary_angle.h"
 
 namespace lla {
 namespace rotary {
@@ -153,8 +154,7 @@ struct Lane {
             c[i] = 1.f;
             s[i] = 0.f;
             if (2 * f < a.rot) {
-                const long long t = position * a.turns[f];          // modulo a turn
-                sincos_turn((int)(t >> 32), s[i], c[i]);
+                sincos_turn(turn_of(position, a.turns[f]), s[i], c[i]);
                 c[i] *= a.magnitude;
                 s[i] *= a.magnitude;
             }
