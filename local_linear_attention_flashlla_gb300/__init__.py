@@ -1054,13 +1054,13 @@ def rotary_backward(dy, x, positions, table, *, gain=None, eps=None, interleaved
     """Gradients of rotary: (dx, dgain) for L = sum(dy * rotary(x)), with rotary's arguments (include/lla.h,
     lla_rotary_backward).  dy: x's dtype or fp32 (as backward()'s dq and dk are); dx has x's dtype; dgain is fp32 [d], or
     None where no gain was given; tuples where x is a sequence.  x may be None where eps is (then it is not read, and dx
-    has dy's dtype).  workspace: None or a CUDA tensor of lla_rotary_backward_workspace_size(...) bytes that no other call uses
+    has dy's dtype and is a tuple where dy is a sequence).  workspace: None or a CUDA tensor of lla_rotary_backward_workspace_size(...) bytes that no other call uses
     at the same time.  Results have the same bits every run.  Asynchronous on the current (or given) stream.
     """
     import torch
     if x is None and eps is not None:
         raise _bad("x is needed where the rows were normalised (eps)")
-    many = isinstance(dy, (tuple, list))
+    many = isinstance(dy if x is None else x, (tuple, list))
     if stream is None and dx is None and workspace is None and isinstance(table, RotaryTable) and table.turns.is_cuda and _bind():
         index = torch.cuda.current_device()
         stream_ptr = torch._C._cuda_getCurrentRawStream(index)
