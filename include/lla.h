@@ -569,8 +569,9 @@ size_t lla_paged_weigh_workspace_size(int dtype, int T, int S, int Hq, int Hkv, 
  * positions, positions_out  NULL (then sinks and recent are 0), or int32 alike: lla_paged_weigh's.
  * k_cache, v_cache  in dtype, as in lla_paged_append; rows are moved in place.
  * keep       [S] int32 (below 0 counts as 0).  dropped: NULL or [S] int32.
- * sinks, recent >= 0; S <= 2^20; d in {16, 32, 64, 128}.  A slot below L whose page is not in the cache ranks below all, is
- * not moved, and is reported by lla_sync_status.  Asynchronous on `stream`, one launch, no scratch.
+ * sinks, recent >= 0; S <= 2^20; d in {16, 32, 64, 128}.  A slot below L whose page is not in the cache is reported by
+ * lla_sync_status: it ranks below all, no row moves to or from it, and each such slot below b leaves room for one position less,
+ * so that those of lowest rank are not kept.  Asynchronous on `stream`, one launch, no scratch.
  */
 int lla_paged_evict(int dtype, const float* scores, float* scores_out, const int* positions, int* positions_out, void* k_cache,
                     void* v_cache, const int* block_table, const int* kv_lens, const int* keep, const int* dropped, int S,

@@ -95,7 +95,9 @@ __device__ __forceinline__ long long element_of(const EvictArgs& a, const Pair& 
     return (((long long)page * a.Hkv + p.h) << a.page_shift) + (j & ((1 << a.page_shift) - 1));
 }
 // Ranks of slots 4 q .. 4 q + 3: mandatory positions (kMust) above all scores, a slot without a page (1) below all, and behind the
-// last slot 0, which no range begins with.
+// last slot 0, which no range begins with.  A slot below b without a page counts as mandatory: it stays, so no row is moved to where
+// it would be lost, and one position less of the lowest rank is kept.  (Of more mandatory ones than b the first b slots' stay, and these
+// are below b: it is always among them.)
 constexpr uint32_t kMust = 0xffffffffu;
 // Where `copy`, and the results go elsewhere, the scores and positions of slots below b go there on the way: holes' too,
 // which their movers' replace later.
@@ -125,7 +127,7 @@ __device__ __forceinline__ uint4 ranks_of(const EvictArgs& a, const Pair& p, int
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (j + i < p.L) r[i] = page < 0 ? 1u : a.positions && (w[i] < a.sinks || w[i] >= p.newest - a.recent) ? kMust : order_of(s[i]);
+        if (j + i < p.L) r[i] = page < 0 ? (j + i < p.b ? kMust : 1u) : a.positions && (w[i] < a.sinks || w[i] >= p.newest - a.recent) ? kMust : order_of(s[i]);
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 

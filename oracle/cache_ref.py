@@ -117,22 +117,25 @@ def paged_weigh_ref(q, lse, k_cache, scores, table, cu_q, kv_lens, tau, decay=1.
 
 
 def paged_evict_ref(scores, table, kv_lens, keep, page, Hkv, positions=None, dropped=None, sinks=0, recent=0):
-    """For every (sequence, key head): the slot whose row each of its first min(L, keep) slots holds afterwards."""
-    out = {}
+    """For every (sequence, key head): the slot whose row each of its first min(L, keep) slots holds afterwards.  A slot whose
+    page is not in the cache holds no row and takes none: that many fewer positions are kept."""
+    out, pages = {}, len(scores)
     for s, L in enumerate(int(x) for x in kv_lens):
         b = min(L, max(int(keep[s]), 0))
         for h in range(Hkv):
             at = [(int(table[s][j // page]), h, j % page) for j in range(L)]
-            value = [float(scores[a]) for a in at]
-            value = [-np.inf if np.isnan(v) else v for v in value]
-            must = [False] * L
+            there = [j for j in range(L) if 0 <= at[j][0] < pages]
+            value = {j: float(scores[at[j]]) for j in there}
+            value = {j: -np.inf if np.isnan(v) else v for j, v in value.items()}
+            must = dict.fromkeys(there, False)
             if positions is not None:
                 newest = L + (0 if dropped is None else int(dropped[s]))
-                must = [int(positions[a]) < sinks or int(positions[a]) >= newest - recent for a in at]
-            order = sorted(range(L), key=lambda j: (not must[j], 0.0 if must[j] else -value[j], j))
-            stay = sorted(order[:b])
+                must = {j: int(positions[at[j]]) < sinks or int(positions[at[j]]) >= newest - recent for j in there}
+            order = sorted(there, key=lambda j: (not must[j], 0.0 if must[j] else -value[j], j))
+            places = sum(j < b for j in there)
+            stay = sorted(order[:places])
             source, kept = list(range(b)), set(stay)
-            holes = [j for j in range(b) if j not in kept]
+            holes = [j for j in there if j < b and j not in kept]
             for hole, j in zip(holes, [j for j in stay if j >= b]):
                 source[hole] = j
             out[s, h] = source
