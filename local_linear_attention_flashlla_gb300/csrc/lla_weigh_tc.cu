@@ -6,9 +6,12 @@
 // the tensor pipe 512 cycles and its exponentials (32 a cycle) as many.  Two halves of the keys share each block of queries,
 // which halves what comes from L2.
 //
-// A last step of 16 columns takes the logsumexp off inside the product: the keys have ones there, a query -lse / tau as three
-// bf16 terms, together exact to 2^-25 of it (added last, so the sum rounds once at that size).  Read from shared memory by the
-// weighing threads instead, 16 bytes for four columns beside the products' operands: 72 us for 71.
+// A last step of 16 columns takes the logsumexp off inside the product: the keys have ones there, a query -lse / tau as four
+// bf16 terms, together exact to 2^-32 of it.  They are made from a quotient in two parts (a rounded one was off by two units of
+// 2^-24 in the worst case) and added last, so the sum is cut once, at the size of q.k: single weights of logits in the hundreds are within
+// 1.0 unit of the logit's last place, 2.0 with the rounded quotient in three terms; the logsumexp read from shared memory by the
+// weighing threads, 16 bytes for four columns beside the products' operands, is off by as much as the rounded quotient and takes 74 us
+// for 70.7.
 //
 // Sixteen warps weigh (a thread a key and half of a block's columns), one copies keys and queries (TMA: a box per page, and per 64
 // columns of a block's rows), one issues the products, two lay out each block's logsumexps and the keys that its rows see (and
@@ -55,6 +58,7 @@ struct Args {
     int Hq, slices;                                // slices: head slices from page to page
     long long q_stride;
     float scale;                                   // tau log2(e)
+    float inv, inv_low;                            // log2(e) / scale, in two parts
     int row_boxes;                                 // rows of a box where 128 is a multiple of G (a block's rows are whole tokens), else 0
 };
 
@@ -229,16 +233,18 @@ __device__ void lay_out(const Args& a, Walk wk, uint32_t qring, unsigned char* t
 #pragma unroll
         for (int i = 0; i < E; ++i) {
             const int r = i * kLoad + t;
-            float v = 0.f;
+            float v = 0.f, low = 0.f;                                    // -lse log2(e) / scale, and what v's rounding leaves
             int limit = 0;
             if (y[i] != -INFINITY) {                                     // -inf: a row without weights, or none
-                v = __fdiv_rn(-1.4426950408889634f * y[i], a.scale);
+                v = -y[i] * a.inv;
+                low = fmaf(-y[i], a.inv, -v) - y[i] * a.inv_low;
                 limit = keys_seen(w, p.q, over_g(w, row0 + r));
             }
             const float hi = __bfloat162float(__float2bfloat16_rn(v)), left = fabsf(hi) < INFINITY ? v - hi : 0.f;
-            const float mid = __bfloat162float(__float2bfloat16_rn(left));
+            const float mid = __bfloat162float(__float2bfloat16_rn(left)), rest = fabsf(hi) < INFINITY ? left - mid + low : 0.f;
+            const float third = __bfloat162float(__float2bfloat16_rn(rest));
             *reinterpret_cast<uint4*>(tails + sr * kTail + tail_off(r, 0)) =
-                make_uint4(paged::pack_bf16(hi, mid), paged::pack_bf16(left - mid, 0.f), 0u, 0u);
+                make_uint4(paged::pack_bf16(hi, mid), paged::pack_bf16(third, rest - third), 0u, 0u);
             b.limit[sr][r] = limit;
             if (r < cols) all = min(all, limit);
         }
@@ -331,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         unsigned char* t = raw + (tails - smem_u32(raw));
         for (int r = tid; r < 128; r += kThreads) {
             const uint32_t one = 0x3f80u;
-            *reinterpret_cast<uint4*>(t + kR * kTail + tail_off(r, 0)) = make_uint4(one | one << 16, one, 0u, 0u);
+            *reinterpret_cast<uint4*>(t + kR * kTail + tail_off(r, 0)) = make_uint4(one | one << 16, one | one << 16, 0u, 0u);
             for (int i = 0; i <= kR; ++i) *reinterpret_cast<uint4*>(t + i * kTail + tail_off(r, 1)) = make_uint4(0u, 0u, 0u, 0u);
         }
         fence_proxy_async_smem();
@@ -477,8 +483,10 @@ cudaError_t launch_weigh_tc(const WeighProblem& p, const WeighSplit& sp, cudaStr
         *why = "tensor map of a paged call";
         return cudaErrorInvalidValue;
     }
+    const float scale = p.tau * 1.4426950408889634f;
+    const double inv = 1.4426950408889634074 / scale;
     weigh::Args a{weigh::make_work(p, sp), static_cast<const __nv_bfloat16*>(p.q), p.lse, p.Hq, (int)paged::slices_of_page(c),
-                  p.q_stride, p.tau * 1.4426950408889634f, boxes};
+                  p.q_stride, scale, (float)inv, (float)(inv - (double)(float)inv), boxes};
     return p.d == 128 ? weigh::launch_one<128>(a, mk, mq, stream) : weigh::launch_one<64>(a, mk, mq, stream);
 }
 
