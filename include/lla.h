@@ -533,6 +533,9 @@ size_t lla_paged_parallax_workspace_size(int dtype, int path, int T, int S, int 
  *     scores_out_j = w_j                        for j >= L - n in causal attention (the step's own tokens),
  *                    decay scores_j + w_j       for the others (decay 0: scores is not read).
  *
+ * The score sums the softmax's weights p_j alone: the factor 1 - (k_j - mean k).probe, which Parallax attention puts on p_j
+ * before the values are summed, may be of either sign and is left out.
+ *
  * dtype      of q and the cache.
  * q          [T, Hq, d], token stride q_stride, as in lla_paged_parallax.
  * lse        [T, Hq] fp32: what lla_paged_parallax_ex wrote for these rows.  A row of -inf adds nothing.

@@ -1158,7 +1158,8 @@ def _check_cache(cache):
 def paged_weigh(q, lse, k_cache, scores, block_table, cu_q, kv_lens, tau, max_new, *, positions=None, dropped=None, decay=1.0,
                 last=0, causal=True, granted=None, out=None, workspace=None, stream=None):
     """Adds the attention that a step's rows gave every cached position to its score (include/lla.h, lla_paged_weigh):
-    scores = decay * scores (0 for the step's own tokens) + the sum over rows of exp(tau q.k - lse).
+    scores = decay * scores (0 for the step's own tokens) + the sum over rows of exp(tau q.k - lse), the softmax's weights alone
+    (without the probe's factor).
 
     q [T, Hq, d], k_cache, block_table, cu_q, kv_lens, tau, max_new, causal: paged_parallax's, and lse [T, Hq] what it wrote.
     scores [num_pages, Hkv, page_size] fp32, updated in place or, with out, written there.  positions: None, or int32 like

@@ -54,6 +54,10 @@ int sm_count() {
 // the highest of them, each pass within the range that holds the threshold: two passes for most scores, three at most.  (Two
 // bits a pass took sixteen, and most of 177 us on 64 x 16 heads of 4145 positions.)  Then windows of slots are
 // marked with one scan each.
+//
+// Lengths are known on the device only, so the table's width says how much shared memory a block gets: 64 x 16 heads of 4145 positions
+// take 40 us with a table of 4288 (four blocks to an SM), and 53 with one of 16,384 or more (three, so a third wave of blocks).
+// In place or elsewhere makes no difference (39 and 40).
 constexpr int kHeld = 16384;             // scores of a sequence that shared memory holds at most
 constexpr int kBins = 2048;
 
@@ -418,7 +422,9 @@ __global__ void __launch_bounds__(T, 1024 / T) paged_evict_kernel(EvictArgs a) {
 // ------------------------------------------------------------------------------------------- trim
 //
 // Every CTA of one cluster counts the pages that its sequences give back, the counts are summed over the cluster, and
-// each writes its own: the free stack gets them sequence after sequence.  Latency bounds it (three dependent reads).
+// each writes its own: the free stack gets them sequence after sequence.  Latency bounds it: a warp takes its sequences one after
+// another, each in two passes of lengths and then 32 columns of the table at a time, and in the second pass a step's loads stand behind the
+// stores of the step before (512 sequences of up to 8000 positions in pages of 16: 14 us).
 constexpr int kTrimThreads = 1024, kTrimMaxSeqs = 8192, kTrimCtas = 8;
 
 struct TrimArgs {

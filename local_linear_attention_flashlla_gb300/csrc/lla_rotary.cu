@@ -98,8 +98,8 @@ __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
 }
 
 // Sine and cosine of t 2^-32 turns.  The nearest quarter turn is taken off in integers, exactly; what is left, at most an eighth of
-// a turn, has polynomials in x^2 of least largest absolute error (Remez): degree 7 for the sine (2^-29), 8 for the cosine
-// (2^-34), with their fp32 roundings 2^-23.3 each.
+// a turn, has polynomials in x^2 of least largest absolute error (Remez): degree 7 for the sine, 8 for the cosine
+// (2^-28.7 and 2^-29.1 with their coefficients in fp32), with the sums' fp32 roundings 2^-23.3 each.
 __device__ __forceinline__ void sincos_turn(int t, float& s, float& c) {
     const unsigned q = ((unsigned)t + 0x20000000u) >> 30;                       // quarter turns, modulo 4
     const float x = (float)(int)((unsigned)t - (q << 30)) * 0x1.921fb6p-30f;    // 2 pi 2^-32
@@ -249,7 +249,8 @@ __device__ __forceinline__ Item item_of(const Args& a, long long w, int group) {
 
 // A warp has one item; the rows of U heads are loaded to registers together.  Train shape (16 + 16 heads of 128, 8 x 4096): 90 us, 6.0
 // TB/s, 0.89 of a plain copy's bandwidth.  Tried there: three blocks to an SM 108 to 139, a persistent kernel with
-// the rows through shared memory, as the gradient's, 96, and 117 to 123 with three blocks.
+// the rows through shared memory, as the gradient's, 96, and 117 to 123 with three blocks.  The same in fp32: 163 us, 0.98; staged
+// (rot 100 of 128) 275.
 template <typename T, int D, int F>
 __global__ void __launch_bounds__(kThreads, 2) rotary_kernel(const __grid_constant__ Args a) {
     using Ln = Lane<T, D, F>;
@@ -367,7 +368,7 @@ struct Cursor {
 // arithmetic.  Where dy has K = 2 pieces of 16 bytes to one of x, a lane reads two neighbouring ones; the copies are shared out so
 // that neighbouring lanes copy neighbouring pieces (whole 32-byte sectors), and piece C of the warp's rows lies in slot
 // C ^ (C >> 3 & 1), which keeps eight lanes' writes and eight lanes' reads of every second piece in eight different slots.  Train
-// shape, fp32 dy: 168 us, 6.4 TB/s, 0.96 of a plain copy's bandwidth; each lane copying its own pieces 217, the copies shared out
+// shape, fp32 dy: 168 us, 6.4 TB/s, 0.96 of a plain copy's bandwidth (bf16 dy 129, 0.94; all in fp32 262, 0.92; staged, rot 100, 421); each lane copying its own pieces 217, the copies shared out
 // without the swap of slots 229, rows through registers 226.  A warp goes through work items, its sums for the gains' gradients
 // in shared memory; a block's sums leave in the order of its warps, and rotary_gain_kernel adds the blocks' in theirs: no
 // atomics, the same bits every run.
@@ -537,6 +538,8 @@ int sm_count() {
     return n;
 }
 
+// Two blocks' shared memory fits an SM, but for bf16 rows with fp32 dy where they are staged (one tensor of d = 16 still fits) or are four
+// tensors of d = 128: there the second half of the grid follows the first (train shape's rows as four tensors 192 us, as two 168).
 constexpr int kBackwardBlocksPerSm = 2;
 constexpr int kMostBlocks = 1024;
 size_t part_bytes(int count, int d) { return (size_t)kMostBlocks * count * d * sizeof(float); }

@@ -3,7 +3,7 @@
 // A tile is 256 keys: two products of 128 keys x N query rows x d, S = K Q^T, for every block of up to 128 rows, the keys being
 // the rows of the accumulator.  So a thread has a key, sums exp(scale s - lse) over its columns in registers, and the sum
 // over query rows needs hardly any exchange; the keys stay in shared memory while query blocks pass.  128 x 128 x 128 takes
-// the tensor pipe 512 cycles and its exponentials (32 a cycle) as many.  Two halves of the keys share each block of queries,
+// the tensor pipe 512 cycles (576 with the last step, below) and its exponentials (32 a cycle) 512.  Two halves of the keys share each block of queries,
 // which halves what comes from L2.
 //
 // A last step of 16 columns takes the logsumexp off inside the product: the keys have ones there, a query -lse / tau as four
@@ -17,9 +17,10 @@
 // columns of a block's rows), one issues the products, two lay out each block's logsumexps and the keys that its rows see (and
 // copy its rows where 128 is not a multiple of G).  The four accumulators, two for each half, fill TMEM.
 //
-// 512 tokens over 16,384 keys, 32/4 heads, d = 128: 71 us, 0.98 PFLOP/s, of which 10 are the start and the join of cut tiles.  The
-// products alone take 64 (what the issuing warp does between two of them delays the next), copies and numbers alone 42, and
-// weights beside the products slow their issue.  Tried there: eight weighing warps 76; exponentials partly on the FMA pipe 81 to
+// 512 tokens over 16,384 keys, 32/4 heads, d = 128: 70.6 us, 0.99 PFLOP/s, of which 10 are the start and the join of cut tiles.  The
+// products alone take 64, some 1100 cycles each; copies and numbers alone 42.  The likely cause: both operands come from shared
+// memory, 8 KB for every 64 cycles of the pipe, which is all that shared memory gives, beside the copies into it (N = 256, which reads a
+// quarter less for the same work, took 57); no counter tells that from the issuing warp's own pace.  Tried there: eight weighing warps 76; exponentials partly on the FMA pipe 81 to
 // 102; three stages of queries 75; N = 256 with one accumulator to a half 89 (products alone 57); 512 keys to a tile 88,
 // with two or four issuing warps 81; an issuing warp to a half 80 (products alone 60).
 #include <math.h>
